@@ -7,7 +7,8 @@ them, and raises FoxError on a non-OK status. There is no CPU fallback: if the
 library has not been built, every call fails with an error saying so.
 
 Names follow the C ABI: fox_fwd, fox_bwd, fox_fwd_workspace_bytes,
-fox_bwd_workspace_bytes, fox_check_error, fox_status_string.
+fox_bwd_workspace_bytes, fox_check_error, fox_status_string; fox_cache_append
+and fox_decode work on handles made by make_cache and make_batch.
 """
 from __future__ import annotations
 
@@ -56,6 +57,9 @@ EXPORTS = (
     "fox_gate_scan_workspace_bytes",
     "fox_gate_bwd",
     "fox_gate_bwd_workspace_bytes",
+    "fox_cache_workspace_bytes",
+    "fox_cache_append",
+    "fox_decode",
 )
 
 
@@ -77,6 +81,47 @@ class fox_params(ctypes.Structure):
         ("non_causal", ctypes.c_int),
         ("tile_skip", ctypes.c_int),
         ("gate_ready", ctypes.c_int),
+    ]
+
+
+class fox_cache(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("Hkv", ctypes.c_int),
+        ("d", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("gbase", ctypes.c_void_p),
+    ]
+
+
+class fox_batch(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int),
+        ("max_new", ctypes.c_int),
+        ("table_stride", ctypes.c_int),
+        ("prefix_len", ctypes.c_int),
+        ("cu_new", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("prefix_table", ctypes.c_void_p),
+    ]
+
+
+class fox_rotary(ctypes.Structure):
+    _fields_ = [
+        ("cos", ctypes.c_void_p),
+        ("sin", ctypes.c_void_p),
+        ("max_pos", ctypes.c_int),
+        ("dim", ctypes.c_int),
+        ("pairs", ctypes.c_int),
+        ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
     ]
 
 
@@ -141,6 +186,13 @@ def lib() -> ctypes.CDLL:
         L.fox_gate_bwd_workspace_bytes.restype = sz
         L.fox_gate_bwd.argtypes = [pp, vp, vp, vp, vp, vp, sz, vp]
         L.fox_gate_bwd.restype = i
+        pc, pb, i64 = ctypes.POINTER(fox_cache), ctypes.POINTER(fox_batch), ctypes.c_int64
+        L.fox_cache_workspace_bytes.argtypes = [pc, pb, i]
+        L.fox_cache_workspace_bytes.restype = sz
+        L.fox_cache_append.argtypes = [pc, pb, i, vp, i64, vp, i64, vp, i64, ctypes.POINTER(fox_rotary), vp, sz, vp]
+        L.fox_cache_append.restype = i
+        L.fox_decode.argtypes = [pc, pb, i, vp, i64, ctypes.c_float, i, vp, vp, vp, sz, vp]
+        L.fox_decode.restype = i
         L.fox_trace_begin.argtypes = []
         L.fox_trace_begin.restype = i
         L.fox_trace_end.argtypes = [ctypes.POINTER(fox_trace_record), i]
@@ -448,6 +500,218 @@ def fox_tile_span(q, k, z, *, scale: float = 0.0, bias_from_j: bool = False, ws=
     if st != 0:
         raise FoxError(st, "fox_tile_span")
     return jmin, imax
+
+
+# ------------------------------------------------------------------------------- paged cache
+
+
+class Cache:
+    """A paged cache over the caller's tensors (see fox_cache in include/fox.h). Made by make_cache or new_cache."""
+
+    __slots__ = ("k", "v", "g", "gbase", "params", "device", "dtype", "H", "Hkv", "d", "page_size")
+
+
+class Batch:
+    """One step's sequences over the caller's tensors (see fox_batch in include/fox.h). Made by make_batch.
+    The contents of its tensors may change between calls; their storage may not."""
+
+    __slots__ = ("lens", "table", "cu_new", "prefix_table", "params", "device", "B")
+
+
+def make_cache(k, v, g, gbase) -> Cache:
+    """A handle on a paged cache: k, v [pages, Hkv, page_size, d] (bf16 or fp32), g [pages, H, page_size] fp32,
+    gbase [pages, H, 2] fp32, all contiguous on one CUDA device."""
+    torch = _torch()
+    pages, Hkv, S, d = k.shape
+    H = g.shape[1]
+    if tuple(v.shape) != (pages, Hkv, S, d) or v.dtype != k.dtype:
+        raise ValueError("make_cache: v must have k's shape and type")
+    if tuple(g.shape) != (pages, H, S) or tuple(gbase.shape) != (pages, H, 2):
+        raise ValueError("make_cache: g must be [pages, H, page_size] and gbase [pages, H, 2]")
+    if g.dtype != torch.float32 or gbase.dtype != torch.float32:
+        raise TypeError("make_cache: g and gbase must be float32")
+    for t in (k, v, g, gbase):
+        if not t.is_contiguous():
+            raise ValueError("make_cache needs contiguous tensors")
+        if not t.is_cuda or t.device != k.device:
+            raise ValueError("make_cache needs tensors on one CUDA device")
+    c = Cache()
+    c.k, c.v, c.g, c.gbase, c.device, c.dtype = k, v, g, gbase, k.device, k.dtype
+    c.H, c.Hkv, c.d, c.page_size = H, Hkv, d, S
+    c.params = fox_cache(pages, S, H, Hkv, d, _dtype_code(k), _ptr(k), _ptr(v), _ptr(g), _ptr(gbase))
+    return c
+
+
+def new_cache(pages: int, page_size: int, H: int, Hkv: int, d: int, *, dtype=None, device="cuda") -> Cache:
+    """make_cache over newly allocated (uninitialised) tensors; dtype defaults to bfloat16."""
+    torch = _torch()
+    dtype = torch.bfloat16 if dtype is None else dtype
+    k, v = (torch.empty((pages, Hkv, page_size, d), dtype=dtype, device=device) for _ in range(2))
+    g = torch.empty((pages, H, page_size), dtype=torch.float32, device=device)
+    return make_cache(k, v, g, torch.empty((pages, H, 2), dtype=torch.float32, device=device))
+
+
+def make_batch(lens, table, *, cu_new=None, max_new: int = 1, prefix_table=None, prefix_len: int = 0) -> Batch:
+    """A handle on a batch: lens [B], table [B, entries], cu_new [B + 1] (None: the same number of rows each),
+    prefix_table [ceil(prefix_len / page_size)], int32 on one CUDA device. lens counts every token of a
+    sequence, the shared prefix and the new ones among them; 0 is an idle sequence."""
+    torch = _torch()
+    B = lens.shape[0]
+    if lens.dim() != 1 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("make_batch: lens must be [B] and table [B, entries]")
+    if cu_new is not None and tuple(cu_new.shape) != (B + 1,):
+        raise ValueError("make_batch: cu_new must be [B + 1]")
+    if (prefix_table is None) != (int(prefix_len) == 0):
+        raise ValueError("make_batch: prefix_table and prefix_len come together")
+    for t in (lens, table, cu_new, prefix_table):
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise TypeError("make_batch: lens, table, cu_new and prefix_table must be int32")
+        if not t.is_cuda or t.device != lens.device:
+            raise ValueError("make_batch needs tensors on one CUDA device")
+        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError("make_batch needs tensors whose last dimension is contiguous")
+    b = Batch()
+    b.lens, b.table, b.cu_new, b.prefix_table, b.device, b.B = lens, table, cu_new, prefix_table, lens.device, B
+    stride = table.stride(0) if B > 1 else table.shape[1]
+    if stride < table.shape[1]:
+        raise ValueError("make_batch: rows of table overlap")
+    # Entries between table's rows are the caller's too: the length check allows no token there.
+    if stride != table.shape[1]:
+        raise ValueError("make_batch: table must be contiguous")
+    if prefix_table is not None and prefix_table.dim() != 1:
+        raise ValueError("make_batch: prefix_table must be one-dimensional")
+    b.params = fox_batch(B, int(max_new), stride, int(prefix_len), _ptr(cu_new), _ptr(lens), _ptr(table),
+                         _ptr(prefix_table))
+    return b
+
+
+def fox_cache_workspace_bytes(cache: Cache, batch: Batch, rows: int) -> int:
+    return int(lib().fox_cache_workspace_bytes(ctypes.byref(cache.params), ctypes.byref(batch.params), int(rows)))
+
+
+def cache_workspace(cache: Cache, batch: Batch, rows: int):
+    """A workspace for fox_cache_append and fox_decode with up to `rows` rows of this batch, its error word zero."""
+    n = fox_cache_workspace_bytes(cache, batch, rows)
+    if n == 0:
+        raise FoxError(1, "cache_workspace")
+    ws = workspace(n, cache.device)
+    ws[:256].zero_()
+    return ws
+
+
+def _check_cache_call(where: str, cache: Cache, batch: Batch):
+    torch = _torch()
+    if batch.device != cache.device:
+        raise ValueError(f"{where}: cache and batch are on different devices")
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: the cache is not on the current CUDA device")
+    need = -(-batch.params.prefix_len // cache.page_size)
+    if need and batch.prefix_table.shape[0] < need:
+        raise ValueError(f"{where}: prefix_table has fewer than {need} pages")
+
+
+def _row_stride(where: str, name: str, t, cache: Cache, heads: int, rows: int) -> int:
+    """The stride of t's rows; t is [rows, heads, d] with contiguous rows, in the cache's type, on its device."""
+    if tuple(t.shape) != (rows, heads, cache.d):
+        raise ValueError(f"{where}: {name} must be [{rows}, {heads}, {cache.d}], got {tuple(t.shape)}")
+    if t.dtype != cache.dtype:
+        raise TypeError(f"{where}: {name} must be {cache.dtype}, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{where}: {name} is not on the cache's device")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (heads > 1 and s1 != cache.d)) and t.numel():
+        raise ValueError(f"{where}: {name} needs contiguous rows")
+    return s0
+
+
+def _on_stream(stream):
+    """The context in which this call's own allocations belong to the stream that uses them."""
+    torch = _torch()
+    import contextlib
+
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, sin=None, pairs: bool = False,
+                     q_out=None, ws=None, stream=None):
+    """Append the batch's new tokens: k, v [rows, Hkv, d] and gate logits z [rows, H] fp32 into the cache's pages.
+
+    cos, sin [positions, r / 2] fp32 rotate the first r channels of k by each token's position on the way
+    (channel i with i + r / 2; `pairs`: 2i with 2i + 1), and those of q [rows, H, d] into q_out, which is
+    returned (None without q). Rows may be strided views, as those of a joint projection's output."""
+    torch = _torch()
+    where = "fox_cache_append"
+    _check_cache_call(where, cache, batch)
+    rows = k.shape[0]
+    ks = _row_stride(where, "k", k, cache, cache.Hkv, rows)
+    vs = _row_stride(where, "v", v, cache, cache.Hkv, rows)
+    if tuple(z.shape) != (rows, cache.H) or z.dtype != torch.float32 or z.device != cache.device:
+        raise ValueError(f"{where}: z must be [{rows}, {cache.H}] float32 on the cache's device")
+    if cache.H > 1 and rows and z.stride(1) != 1:
+        raise ValueError(f"{where}: z needs contiguous rows")
+    rot = None
+    if (cos is None) != (sin is None) or (cos is None and (q is not None or q_out is not None)):
+        raise ValueError(f"{where}: cos and sin come together, and q only with them")
+    with _on_stream(stream):
+        if cos is not None:
+            if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32:
+                raise ValueError(f"{where}: cos and sin must be float32 [positions, r / 2]")
+            if not cos.is_contiguous() or not sin.is_contiguous() or cos.device != cache.device or sin.device != cache.device:
+                raise ValueError(f"{where}: cos and sin must be contiguous on the cache's device")
+            qs = 0
+            if q is not None:
+                qs = _row_stride(where, "q", q, cache, cache.H, rows)
+                if q_out is None:
+                    q_out = torch.empty((rows, cache.H, cache.d), dtype=q.dtype, device=q.device)
+                else:
+                    _row_stride(where, "q_out", q_out, cache, cache.H, rows)
+                    if not q_out.is_contiguous():
+                        raise ValueError(f"{where}: q_out must be contiguous")
+            elif q_out is not None:
+                raise ValueError(f"{where}: q_out without q")
+            rot = fox_rotary(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(pairs)), _ptr(q), qs, _ptr(q_out))
+        if ws is None:
+            ws = torch.zeros(256, dtype=torch.uint8, device=cache.device)
+        st = lib().fox_cache_append(
+            ctypes.byref(cache.params), ctypes.byref(batch.params), rows, _ptr(k), ks, _ptr(v), vs, _ptr(z), z.stride(0),
+            ctypes.byref(rot) if rot is not None else None, _ptr(ws), ws.numel(), _stream_handle(stream),
+        )
+    if st != 0:
+        raise FoxError(st, where)
+    return q_out
+
+
+def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
+               ws=None, stream=None) -> Tuple[object, object]:
+    """Attention of the batch's newest tokens, appended before, over the cache: q [rows, H, d] -> (O [rows, H, d],
+    LSE [rows, H] fp32). A shared prefix of the batch is read and multiplied once for all its sequences.
+    Rows of idle sequences get O = 0 and LSE = -inf; rows behind the last sequence are not written."""
+    torch = _torch()
+    where = "fox_decode"
+    _check_cache_call(where, cache, batch)
+    rows = q.shape[0]
+    qs = _row_stride(where, "q", q, cache, cache.H, rows)
+    with _on_stream(stream):
+        if o is None:
+            o = torch.empty((rows, cache.H, cache.d), dtype=cache.dtype, device=cache.device)
+        if lse is None:
+            lse = torch.empty((rows, cache.H), dtype=torch.float32, device=cache.device)
+        _row_stride(where, "o", o, cache, cache.H, rows)
+        if not o.is_contiguous() or not lse.is_contiguous():
+            raise ValueError(f"{where}: o and lse must be contiguous")
+        if tuple(lse.shape) != (rows, cache.H) or lse.dtype != torch.float32 or lse.device != cache.device:
+            raise ValueError(f"{where}: lse must be [{rows}, {cache.H}] float32 on the cache's device")
+        if ws is None:
+            ws = cache_workspace(cache, batch, rows)
+        st = lib().fox_decode(
+            ctypes.byref(cache.params), ctypes.byref(batch.params), rows, _ptr(q), qs, float(scale), int(bool(bias_from_j)),
+            _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream_handle(stream),
+        )
+    if st != 0:
+        raise FoxError(st, where)
+    return o, lse
 
 
 def fox_check_error(ws, stream=None) -> int:

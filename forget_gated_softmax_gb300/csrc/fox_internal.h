@@ -6,10 +6,13 @@
 #include <cuda_runtime.h>
 #include <cuda.h>
 
+#include "fox_paged.h"
+
 namespace fox {
 
 constexpr int kTile = 128;          // tokens per sequence tile (MMA M and KV tile)
 constexpr int kColRec = kTile + 4;  // floats per column record: 128 column terms + base hi, base lo, 2 pad
+constexpr int kSMs = 152;           // of one GB300: grids of resident workers are sized for it, any count works
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -239,6 +242,33 @@ cudaError_t launch_tile_span(const void* q, const void* k, int B, int N, int H, 
 // Epsilon-effective window per query row (fp64 prefix scan + binary search).
 cudaError_t launch_window(const float* z, int B, int N, int H, double eps, int* out, void* ws, cudaStream_t s);
 size_t window_workspace_bytes(int B, int N, int H);
+
+// Paged cache: new tokens into the cache (k, v rotated and gates), and attention over it.
+// Strides are elements from one token's row to the next.
+struct CacheAppendArgs {
+  PagedArgs a;
+  const void* k;
+  const void* v;
+  const float* z;
+  const void* q;  // rotated into q_out, or null
+  void* q_out;
+  long long k_stride, v_stride, z_stride, q_stride;
+  const float* cos;
+  const float* sin;
+  int max_pos, rot, pairs;
+};
+cudaError_t launch_cache_append(const CacheAppendArgs& x, bool f32, cudaStream_t s);
+struct DecodeArgs {
+  PagedArgs a;
+  const void* q;
+  long long q_stride;
+  float scale;
+  int bias_from_j;
+  void* o;
+  float* lse;
+};
+size_t decode_workspace_bytes(const PagedArgs& a, bool f32);
+cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t s);
 
 // Host helper: 4-D bf16 tensor map over [B, N, H, d] with a box of 64 channels x 1 head x
 // box_rows tokens x 1 batch and 128-byte swizzle. Returns false when the driver entry point is

@@ -1,0 +1,128 @@
+// Paged cache: argument block and index arithmetic shared by the append and decode kernels
+// and by the host. Plain C++ apart from the qualifiers, so that the arithmetic that decides
+// every read and write of the cache can be checked without a GPU.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define FOX_HD __host__ __device__ __forceinline__
+#else
+#define FOX_HD inline
+#endif
+
+namespace fox {
+
+constexpr int kMaxSeqs = 4096;  // sequences of one call: every CTA holds their work offsets in shared memory
+
+struct PagedArgs {
+  int num_pages, page_size, H, Hkv, d;
+  int B, rows, max_new;  // max_new: at least every sequence's count of new tokens
+  int table_stride, prefix_len;
+  const int32_t* cu;      // [B + 1] first row of each sequence, or null: rows / B rows each
+  const int32_t* lens;    // [B] tokens of each sequence, prefix and new ones included; 0: an idle sequence
+  const int32_t* table;   // [B][table_stride] pages of the tokens after the prefix
+  const int32_t* prefix;  // [ceil(prefix_len / page_size)] pages of the shared prefix
+  void* k;
+  void* v;
+  float* g;
+  float* gbase;
+  uint32_t* err;
+};
+
+// One sequence of the batch: its rows [row0, row0 + n) and its tokens after the prefix (the new
+// ones among them). An idle sequence (lens 0) keeps its rows and has own = -1: nothing is appended
+// for it and its rows attend to nothing. `bad` reports lengths that the batch cannot hold; the
+// sequence then has no rows.
+struct SeqInfo {
+  int row0, n, own;
+};
+
+FOX_HD SeqInfo seq_info(const PagedArgs& a, int b, bool* bad) {
+  SeqInfo s;
+  int r1;
+  if (a.cu) {
+    s.row0 = a.cu[b];
+    r1 = a.cu[b + 1];
+  } else {
+    const int each = a.rows / a.B;
+    s.row0 = b * each;
+    r1 = s.row0 + each;
+  }
+  const int len = a.lens[b];
+  const long long cap = (long long)a.prefix_len + (long long)a.table_stride * a.page_size;
+  const bool rows_ok = s.row0 >= 0 && r1 >= s.row0 && r1 <= a.rows && r1 - s.row0 <= a.max_new;
+  s.n = r1 - s.row0;
+  const bool ok = rows_ok && (len == 0 || (len > 0 && (long long)len >= (long long)a.prefix_len + s.n && len <= cap));
+  *bad = !ok;
+  if (!ok) {
+    s.row0 = 0;
+    s.n = 0;
+    s.own = -1;
+    return s;
+  }
+  s.own = len == 0 ? -1 : len - a.prefix_len;
+  return s;
+}
+
+// The sequence that row i belongs to, or -1: behind the last sequence. With cu not rising the
+// answer is some sequence in [0, B), whose seq_info then has to hold the row.
+FOX_HD int seq_of_row(const PagedArgs& a, int i) {
+  if (!a.cu) return i / (a.rows / a.B);
+  if (i >= a.cu[a.B] || i < a.cu[0]) return -1;
+  int lo = 0, hi = a.B;  // cu[lo] <= i < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= i)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The page of own token p of sequence b (0 <= p < table_stride * page_size), or -1 where the
+// table's entry is no page of the pool.
+FOX_HD int own_page(const PagedArgs& a, int b, int p) {
+  const int id = a.table[(size_t)b * a.table_stride + p / a.page_size];
+  return id >= 0 && id < a.num_pages ? id : -1;
+}
+FOX_HD int prefix_page(const PagedArgs& a, int p) {
+  const int id = a.prefix[p / a.page_size];
+  return id >= 0 && id < a.num_pages ? id : -1;
+}
+
+// Elements from the pool's start to (page, head, slot).
+FOX_HD size_t kv_offset(const PagedArgs& a, int page, int hkv, int slot) {
+  return (((size_t)page * a.Hkv + hkv) * a.page_size + slot) * a.d;
+}
+FOX_HD size_t g_offset(const PagedArgs& a, int page, int h, int slot) {
+  return ((size_t)page * a.H + h) * a.page_size + slot;
+}
+FOX_HD size_t gbase_offset(const PagedArgs& a, int page, int h) { return ((size_t)page * a.H + h) * 2; }
+
+// ---- work of the decode kernels ----
+// An item is (key head, sequence, row tile): `Rt` of the sequence's n * G query rows of that key
+// head (row r = token r / G, head hkv * G + r % G) against its keys. Its units are the key tiles of
+// kKeyTile tokens. The units of all items lie on one line, items in the order (key head, sequence,
+// row tile), and worker w takes units [w q, (w + 1) q): equal work whatever the lengths are.
+// An item that lies in one worker's range is finished there; the others leave one partial result a
+// worker, in slot worker + item: along the line each new (worker, item) pair raises one of the
+// two, so no two pairs meet, and there are fewer than workers + items slots.
+constexpr int kKeyTile = 32;
+
+FOX_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Keys that the item's own walk covers: the prefix too when nothing shares it out (`walk_prefix`).
+FOX_HD int walk_keys(const PagedArgs& a, const SeqInfo& s, bool walk_prefix) {
+  return s.own < 0 ? 0 : s.own + (walk_prefix ? a.prefix_len : 0);
+}
+FOX_HD long long seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, bool walk_prefix) {
+  return (long long)ceil_div(walk_keys(a, s, walk_prefix), kKeyTile) * ceil_div(s.n * (a.H / a.Hkv), Rt);
+}
+FOX_HD long long units_per_worker(long long total, int workers) {
+  const long long q = (total + workers - 1) / workers;
+  return q > 0 ? q : 1;
+}
+
+}  // namespace fox

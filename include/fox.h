@@ -239,6 +239,99 @@ fox_status fox_tile_span(const fox_params* p, const void* q, const void* k, cons
                          int32_t* imax, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---- Answering token by token: a paged cache, and attention over it ----
+ *
+ * The cache is a pool of pages of page_size tokens each, in device memory that the caller owns:
+ *   k, v  [num_pages, Hkv, page_size, d]  element type dtype
+ *   g     [num_pages, H, page_size] fp32  sum of log sigmoid(z) from the page's first token to this one
+ *   gbase [num_pages, H, 2] fp32          the sum over every earlier token of the sequence (high, low):
+ *                                         c of a token = gbase[0] + gbase[1] + g (natural log)
+ * H query heads share Hkv key heads: query head h reads key head h / (H / Hkv). The gate has one
+ * logit a query head, as everywhere in this library.
+ * Nothing has to be initialised: a page's slots are read only once tokens were appended to them.
+ */
+typedef struct fox_cache {
+  int num_pages; /* >= 1 */
+  int page_size; /* 16, 32, 64 or 128 */
+  int H;         /* query heads, a multiple of Hkv */
+  int Hkv;       /* key heads, >= 1 */
+  int d;         /* 64 or 128 */
+  int dtype;     /* FOX_DTYPE_BF16 or FOX_DTYPE_F32 */
+  void* k;       /* 16-byte aligned, as v, g and gbase */
+  void* v;
+  float* g;
+  float* gbase;
+} fox_cache;
+
+/*
+ * One step's sequences. Each brings its newest tokens: `rows` rows of q, k, v, z in all, the
+ * sequences' rows one after the other. All arrays are device memory and read when the work runs, so
+ * that a captured step can be replayed on new contents.
+ * With a shared prefix, every sequence begins with the same prefix_len tokens, held once in the
+ * pages of prefix_table; `table` then names the pages of each sequence's later tokens, the first of
+ * which starts a page of its own. The new tokens are never the prefix's (it is appended beforehand,
+ * as a sequence without a prefix).
+ * Two sequences of one append must not name the same page for their new tokens.
+ */
+typedef struct fox_batch {
+  int B;                       /* sequences, 0 .. 4096 */
+  int max_new;                 /* >= the new tokens of any sequence (ignored without cu_new), >= 1 */
+  int table_stride;            /* entries of a sequence's row of `table`, >= 1 */
+  int prefix_len;              /* tokens of the shared prefix; 0: none */
+  const int32_t* cu_new;       /* [B + 1] first row of each sequence, rising from 0; rows behind cu_new[B] are
+                                  neither read nor written. NULL: rows / B rows each (rows a multiple of B) */
+  const int32_t* lens;         /* [B] tokens of each sequence, the prefix and the new ones among them.
+                                  0: an idle sequence (padding); its rows are not appended, and attend to nothing */
+  const int32_t* table;        /* [B, table_stride] page ids */
+  const int32_t* prefix_table; /* [ceil(prefix_len / page_size)] page ids, or NULL with prefix_len 0 */
+} fox_batch;
+
+/*
+ * Workspace of fox_cache_append and fox_decode for these arguments (0 if they are invalid): the
+ * error word, and for fox_decode the partial results of keys split among the SMs. It depends on
+ * sizes only, never on the contents of lens. The first 4 bytes, the error word, must be zero before
+ * the first call; these calls only ever add bits to it (fox_check_error reads and clears it):
+ * a length, row range, page id or position outside what the arguments allow sets one, and nothing
+ * is read or written for it (the sequence, or the token, is skipped; its outputs are not meaningful).
+ */
+size_t fox_cache_workspace_bytes(const fox_cache* c, const fox_batch* s, int rows);
+
+/* Rotation of the first `dim` channels of k (and q) by the angles of the token's position in its sequence. */
+typedef struct fox_rotary {
+  const float* cos;  /* [max_pos, dim / 2] fp32, 16-byte aligned, as sin */
+  const float* sin;
+  int max_pos;       /* positions that the tables hold */
+  int dim;           /* 0 (none), or a multiple of 16 up to d */
+  int pairs;         /* 0: channel i with i + dim / 2;  1: channel 2i with 2i + 1 */
+  const void* q;     /* [rows, H, d] to rotate with the same angles, or NULL */
+  int64_t q_stride;  /* elements from one row of q to the next */
+  void* q_out;       /* [rows, H, d] contiguous */
+} fox_rotary;
+
+/*
+ * Appends the new tokens: K (rotated when rot is given; products and sums in fp32, rounded once), V and
+ * the gates' running sums go to the pages of positions lens[b] - n_b .. lens[b] - 1. Calling it again
+ * with the same arguments writes the same values. k, v: rows of [Hkv, d], row strides in elements
+ * (multiples of 16 bytes, 16-byte aligned); z: rows of [H] fp32, any stride >= H. rot may be NULL.
+ * Every value of the range that fox_fwd takes for z is allowed.
+ */
+fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of the new tokens over the cache (their own K, V and gates appended before): row i of
+ * sequence b at position pos attends to the sequence's keys 0 .. pos with the scores of fox_fwd,
+ *   x_ij = scale q_i . k_j + c_i - c_j   (c_{j-1} under bias_from_j = 1).
+ * q: rows of [H, d], q_stride elements apart (multiples of 16 bytes; 16-byte aligned).
+ * o: [rows, H, d] of the cache's type, lse: [rows, H] fp32, natural log. Rows of idle sequences get
+ * O = 0 and LSE = -inf. scale 0 selects d^-1/2.
+ * A K or V slot behind the sequence's end is never used, whatever it holds.
+ */
+fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
+                      int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Forward without a caller-provided workspace, for callers that cannot
  * allocate device memory where they run this code (a plugin in a host
  * application that owns all device memory, a latency-bound loop that cannot
