@@ -1,0 +1,515 @@
+// Attention of the newest tokens over the paged cache, bf16, on the tensor cores.
+//
+// Bound by memory: K and V of every key are read once, 2 bytes an element, for at most 16 query rows
+// of work each. So the kernel is built to keep copies in flight, and uses the small register MMAs
+// (16 x 8 x 16), of which it needs too few to matter: 128-row tensor-memory tiles would be 8 to
+// 128 times padding here.
+//
+// One warp is one worker of the work line (fox_paged.h), with a ring of key tiles of its own that TMA
+// fills: no barrier joins the warps, and each has the next tiles on their way while it computes.
+// A stage holds 32 keys: K, V (128-byte swizzled, 64 channels a block) and the gates' sums g of the
+// row tile's heads, from four slots before the first key, so that the exclusive sums of bias_from_j
+// are there too (0 before a page's first slot, which is what TMA fills in).
+//
+// Transposed products, so that the few query rows are the 8-wide side and K and V the 16-high one:
+//   S^T (keys x rows) = K Q^T     K as it lies (ldmatrix), Q in registers
+//   O^T (d x rows)   += V^T P^T   V transposed on the way (ldmatrix.trans), P^T turned in registers
+// x = scale2 S + log2e ((c_i - base of the page) - g_j), the difference of the cumulative sums in
+// two fp32 each. The running maximum moves only when a score passes it by 2^8, which one vote finds.
+// P is split into two bf16 terms (P = hi + lo, both multiplied): with one, its 8 significant bits
+// would add to O an error as large as O's own rounding; V keeps its full bf16 range.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "fox_decode.h"
+
+namespace fox {
+namespace {
+
+constexpr float kGrow = 8.0f;  // log2 units that a score may pass the running maximum by
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D, int NT>
+struct MmaLayout {
+  static constexpr int kWarps = D == 128 ? 4 : 8;
+  static constexpr int kMaxStages = 3;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTileBytes = kKeyTile * D * 2;  // K or V of a stage
+  static constexpr int kOutStride = D + 4;             // a result row in shared memory, in floats
+  static_assert(kRows * kOutStride * 4 <= 2 * kTileBytes, "results pass through a stage that was read");
+};
+
+// Shared memory: K and V of every (warp, stage), then its gates, then the sequences' work offsets.
+// Gates of a stage: per sub-page (32 slots, or two of 16) [heads][slots + 4] sums, then [heads] bases.
+struct MmaShape {
+  int stages, heads, gpitch;  // heads of a row tile; floats from one head's sums to the next's
+  int gsub, gstage;           // bytes of a sub-page's sums (a TMA destination: 128-byte steps); of a stage's gates
+};
+
+// A place on the work line: unit `tile` of item (hkv, b, rt).
+struct Cursor {
+  int hkv, b, rt, tile;       // tile of `tiles`
+  int tiles, rts, row0, n, own;
+};
+
+__device__ __forceinline__ void load_seq(const DecodeParams& p, Cursor& c) {
+  bool bad;
+  const SeqInfo s = seq_info(p.a, c.b, &bad);
+  c.row0 = s.row0;
+  c.n = s.n;
+  c.own = s.own;
+  c.tiles = s.own > 0 ? ceil_div(s.own, kKeyTile) : 0;
+  c.rts = ceil_div(s.n * p.Gp, p.Rt);
+}
+
+// The unit after this one; only called while one follows on the line.
+__device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
+  if (++c.tile < c.tiles) return;
+  c.tile = 0;
+  if (++c.rt < c.rts) return;
+  c.rt = 0;
+  do {
+    if (++c.b == p.a.B) {
+      c.b = 0;
+      ++c.hkv;
+    }
+    load_seq(p, c);
+  } while (c.tiles == 0 || c.rts == 0);
+}
+
+// Pages of a tile: one, or two where a page holds 16 tokens (-1: none; the second starts behind the
+// sequence's end). A table entry that is no page is reported and read as page 0.
+struct Pages {
+  int id[2];
+};
+__device__ __forceinline__ Pages tile_pages(const PagedArgs& a, const Cursor& c) {
+  Pages g;
+  const int j = c.tile * kKeyTile;
+  g.id[0] = own_page(a, c.b, j);
+  g.id[1] = a.page_size == 16 && j + 16 < c.own ? own_page(a, c.b, j + 16) : -2;
+  return g;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
+    decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                      const __grid_constant__ CUtensorMap tmap_g, const DecodeParams p, const MmaShape x) {
+  using L = MmaLayout<D, NT>;
+  constexpr int W = L::kWarps;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long scratch[W];
+  __shared__ __align__(8) uint64_t bars[W][L::kMaxStages];
+  __shared__ int abort_word;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &abort_word;
+  const PagedArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = x.stages;
+  uint8_t* ring = sm + warp * stages * (2 * L::kTileBytes);
+  uint8_t* gates = sm + W * stages * (2 * L::kTileBytes) + warp * stages * x.gstage;
+  long long* cum = reinterpret_cast<long long*>(sm + W * stages * (2 * L::kTileBytes + x.gstage));
+
+  grid_dep_trigger();
+  if (threadIdx.x == 0) abort_word = 0;
+  if (lane == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&bars[warp][s], 1);
+    fence_mbar_init();
+    if (warp == 0) {
+      tma_prefetch_desc(&tmap_k);
+      tma_prefetch_desc(&tmap_v);
+      tma_prefetch_desc(&tmap_g);
+    }
+  }
+  scan_units(p, cum, scratch);  // ends with a block barrier
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) p.cum[b] = cum[b];
+
+  const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size;
+  const int KS = S < kKeyTile ? S : kKeyTile;      // tokens of a sub-page
+  const int heads = x.heads, gpitch = x.gpitch;
+  const int base_off = (S == 16 ? 2 : 1) * x.gsub;
+  const long long per_head = cum[a.B], total = per_head * a.Hkv;
+  const long long each = units_per_worker(total, p.workers);
+  const long long w = (long long)blockIdx.x * W + warp;
+  const long long u0 = w * each, u1 = min(total, u0 + each);
+  // With a shared prefix this kernel is launched as a dependent of the prefix's, of which it needs
+  // nothing; the merge, its own dependent, needs both: so this grid does not end before that one.
+  if (u0 >= u1) {
+    if (blockIdx.x == 0) grid_dep_wait();
+    return;
+  }
+
+  // Consumer and producer cursors start at u0; the producer's runs up to `stages` units ahead.
+  Cursor cur;
+  {
+    cur.hkv = static_cast<int>(u0 / per_head);
+    const long long in_head = u0 - cur.hkv * per_head;
+    cur.b = find_seq(cum, a.B, in_head);
+    load_seq(p, cur);
+    const long long in_seq = in_head - cum[cur.b];
+    cur.rt = static_cast<int>(in_seq / cur.tiles);
+    cur.tile = static_cast<int>(in_seq % cur.tiles);
+  }
+  Cursor pro = cur;
+  const int count = static_cast<int>(u1 - u0);
+  Pages next = tile_pages(a, pro);  // pages of the producer's next tile, read one tile ahead of their use
+
+  // Issue the copies of the producer's tile into `stage` and move on.
+  auto issue = [&](int n, int stage) {
+    uint8_t* st = ring + stage * (2 * L::kTileBytes);
+    uint8_t* sg = gates + stage * x.gstage;
+    Pages g = next;
+    const Cursor c = pro;
+    if (n + 1 < count) {
+      advance(p, pro);
+      next = tile_pages(a, pro);
+    }
+    if (g.id[0] == -1 || g.id[1] == -1) {
+      if (lane == 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
+      if (g.id[0] == -1) g.id[0] = 0;
+      if (g.id[1] == -1) g.id[1] = 0;
+    }
+    const int h0 = c.hkv * G + (G > L::kRows ? c.rt * p.Rt % Gp : 0);
+    const int slot = S == 16 ? 0 : c.tile * kKeyTile % S;
+    const int subs = g.id[1] >= 0 ? 2 : 1;
+    if (lane == 0) {
+      uint64_t* bar = &bars[warp][stage];
+      mbar_arrive_expect_tx(bar, subs * (2 * KS * D * 2 + heads * gpitch * 4));
+      for (int i = 0; i < subs; ++i) {
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y) {
+          tma_load_4d(st + y * (kKeyTile * 128) + i * (16 * 128), &tmap_k, bar, y * 64, slot, c.hkv, g.id[i]);
+          tma_load_4d(st + L::kTileBytes + y * (kKeyTile * 128) + i * (16 * 128), &tmap_v, bar, y * 64, slot, c.hkv,
+                      g.id[i]);
+        }
+        tma_load_3d(sg + i * x.gsub, &tmap_g, bar, slot - 4, h0, g.id[i]);
+      }
+    }
+    for (int i = 0; i < subs; ++i)
+      if (lane < heads && h0 + lane < a.H)
+        cp_async8(smem_u32(sg + base_off) + (i * heads + lane) * 8, a.gbase + gbase_offset(a, g.id[i], h0 + lane));
+  };
+
+  for (int n = 0; n < stages; ++n) {
+    if (n < count) issue(n, n);
+    cp_async_commit();
+  }
+
+  const int g8 = lane >> 2, t4 = lane & 3;
+  // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
+  const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
+  const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
+
+  uint32_t qf[D / 16][NT][2];
+  float acc[D / 16][NT][4];
+  float m[NT][2], l[NT][2], ci_hi[NT][2], ci_lo[NT][2];
+  int pos[NT][2], gidx[NT][2];
+  bool opened = false, ok = true;
+  int stage = 0;
+  uint32_t phase = 0;
+
+  for (int n = 0; n < count; ++n) {
+    if (!opened) {
+      // The item's rows: Q fragments, places and cumulative gates of this thread's rows 2 t4, 2 t4 + 1.
+      opened = true;
+      const int r0 = cur.rt * p.Rt;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + nt * 8 + g8, t = r / Gp, g = r % Gp;
+        const bool in = t < cur.n && g < G;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                   (size_t)(cur.row0 + (in ? t : 0)) * p.q_stride + (size_t)(cur.hkv * G + (in ? g : 0)) * D;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          qf[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4) : 0u;
+          qf[ks][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4 + 8) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = r0 + nt * 8 + 2 * t4 + e, tt = rr / Gp, gg = rr % Gp;
+          const bool here = tt < cur.n && gg < G;
+          m[nt][e] = -INFINITY;
+          l[nt][e] = 0.f;
+          gidx[nt][e] = here ? (G > L::kRows ? gg - r0 % Gp : gg) : 0;
+          pos[nt][e] = cur.own - cur.n + tt;
+          ci_hi[nt][e] = -INFINITY;  // an empty row's scores are -inf
+          ci_lo[nt][e] = 0.f;
+          if (here) {
+            const double c = gate_at(a, cur.b, pos[nt][e], cur.hkv * G + gg);
+            ci_hi[nt][e] = static_cast<float>(c);
+            ci_lo[nt][e] = static_cast<float>(c - static_cast<double>(ci_hi[nt][e]));
+          }
+        }
+      }
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[dt][nt][e] = 0.f;
+    }
+    uint8_t* st = ring + stage * (2 * L::kTileBytes);
+    ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][stage], phase, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA));
+    if (!ok) break;
+    // the stage's bases: the groups committed after this stage's are `stages - 1`
+    if (stages == 3)
+      cp_async_wait<2>();
+    else
+      cp_async_wait<1>();
+    __syncwarp();
+
+    const int j0 = cur.tile * kKeyTile;
+    const uint32_t sk = smem_u32(st), sv = sk + L::kTileBytes;
+    float s[2][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t kf[4];
+        const int row = mt * 16 + krow, chunk = (ks & 3) * 2 + kchunk;
+        ldsm4(sk + (ks >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), kf);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], kf, qf[ks][nt][0], qf[ks][nt][1]);
+      }
+    }
+    // Scores of keys mt * 16 + g8 (+ 8) and rows 2 t4 (+ 1), in log2 units.
+    const uint8_t* sg = gates + stage * x.gstage;
+    const float2* bs = reinterpret_cast<const float2*>(sg + base_off);
+    const bool edge = j0 + kKeyTile > cur.own - cur.n;  // some key is behind some row
+    bool grow = false;
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[nt][e] = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const int sub = S == 16 ? mt : 0;
+          const float2 base = bs[sub * heads + gidx[nt][e]];
+          const float beta = (ci_hi[nt][e] - base.x) + (ci_lo[nt][e] - base.y);
+          const float* gr = reinterpret_cast<const float*>(sg + sub * x.gsub) + gidx[nt][e] * gpitch + 4 -
+                            p.bias_from_j + (S == 16 ? 0 : mt * 16);
+#pragma unroll
+          for (int k8 = 0; k8 < 2; ++k8) {
+            const int key = g8 + k8 * 8;
+            float x = fmaf(beta - gr[key], kLog2e, s[mt][nt][k8 * 2 + e] * p.scale2);
+            if (edge && j0 + mt * 16 + key > pos[nt][e]) x = -INFINITY;
+            s[mt][nt][k8 * 2 + e] = x;
+            top[nt][e] = fmaxf(top[nt][e], x);
+          }
+        }
+        grow |= top[nt][e] > m[nt][e] + kGrow;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = top[nt][e];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          const float mn = fmaxf(m[nt][e], x);
+          const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mn);
+          m[nt][e] = mn;
+          l[nt][e] *= alpha;
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt) {
+            acc[dt][nt][e] *= alpha;
+            acc[dt][nt][e + 2] *= alpha;
+          }
+        }
+    }
+    if (j0 + kKeyTile > cur.own) {
+      // Slots behind the sequence's end may hold anything: V there becomes 0 (its weights are 0).
+      for (int e = lane; e < (j0 + kKeyTile - cur.own) * (D / 8); e += 32) {
+        const int row = cur.own - j0 + e / (D / 8), c = e % (D / 8);
+        sts_v4(sv + (c >> 3) * (kKeyTile * 128) + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();  // before the next copy into this stage
+      __syncwarp();
+    }
+    // P^T fragments, hi and lo.
+    uint32_t ph[2][NT][2], pl[2][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float o0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], o1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int k8 = 0; k8 < 2; ++k8) {
+          const float p0 = ex2_approx(s[mt][nt][k8 * 2] - o0), p1 = ex2_approx(s[mt][nt][k8 * 2 + 1] - o1);
+          l[nt][0] += p0;
+          l[nt][1] += p1;
+          const uint32_t hi = pack_bf16x2(p0, p1);
+          ph[mt][nt][k8] = turn8x8(hi);
+          pl[mt][nt][k8] = turn8x8(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) {
+        uint32_t vf[4];
+        const int row = mt * 16 + vrow, chunk = (dt & 3) * 2 + vchunk;
+        ldsm4_t(sv + (dt >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), vf);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(acc[dt][nt], vf, ph[mt][nt][0], ph[mt][nt][1]);
+          mma16816(acc[dt][nt], vf, pl[mt][nt][0], pl[mt][nt][1]);
+        }
+      }
+    __syncwarp();  // every lane has read the stage
+
+    const bool last = cur.tile + 1 == cur.tiles || n + 1 == count;
+    if (last) {
+      // Results: O^T through the stage just read to rows, finished or the worker's part of them.
+      float* out = reinterpret_cast<float*>(st);
+      const long long i0 = cur.hkv * per_head + cum[cur.b] + (long long)cur.rt * cur.tiles, i1 = i0 + cur.tiles - 1;
+      const bool whole = p.pre.key_tiles == 0 && i0 / each == i1 / each;
+      const size_t slot = (size_t)(w + ((long long)cur.hkv * a.B + cur.b) * p.RTmax + cur.rt) * p.Rs;
+      const int r0 = cur.rt * p.Rt;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = l[nt][e];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          const float f = whole ? (x > 0.f ? 1.f / x : 0.f) : 1.f;
+          const int rl = nt * 8 + 2 * t4 + e;
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt) {
+            out[rl * L::kOutStride + dt * 16 + g8] = acc[dt][nt][e] * f;
+            out[rl * L::kOutStride + dt * 16 + g8 + 8] = acc[dt][nt][e + 2] * f;
+          }
+          const int r = r0 + rl, t = r / Gp, g = r % Gp;
+          if (g8 == 0 && t < cur.n && g < G) {
+            if (whole)
+              p.lse[(size_t)(cur.row0 + t) * a.H + cur.hkv * G + g] = x > 0.f ? (m[nt][e] + log2f(x)) * kLn2 : -INFINITY;
+            else
+              p.ml[slot + rl] = make_float2(m[nt][e], x);
+          }
+        }
+      __syncwarp();
+      constexpr int E = D / 32;
+      for (int rl = 0; rl < L::kRows; ++rl) {
+        const int r = r0 + rl, t = r / Gp, g = r % Gp;
+        if (t >= cur.n || g >= G) continue;
+        float f[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = out[rl * L::kOutStride + lane * E + e];
+        if (whole)
+          put_out<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(cur.row0 + t) * a.H + cur.hkv * G + g) * D + lane * E,
+                                 f, E);
+        else
+          put_out<float>(p.po + (slot + rl) * D + lane * E, f, E);
+      }
+      fence_proxy_async_smem();  // before the next copy into this stage
+      __syncwarp();
+      opened = false;
+    }
+    if (n + 1 < count) advance(p, cur);
+    if (n + stages < count) issue(n + stages, stage);
+    cp_async_commit();
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (!ok) {
+    // A wait gave up: every copy issued must still land before shared memory is released.
+    for (int s = 0; s < stages; ++s) mbar_wait_drain(&bars[warp][s], s < stage ? phase ^ 1 : phase);
+    cp_async_wait<0>();
+  }
+  if (blockIdx.x == 0) grid_dep_wait();
+}
+
+template <int D, int NT>
+cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t s) {
+  using L = MmaLayout<D, NT>;
+  auto kernel = decode_mma_kernel<D, NT>;
+  const int G = p.a.H / p.a.Hkv, subs = p.a.page_size == 16 ? 2 : 1;
+  MmaShape x;
+  x.heads = G < L::kRows ? G : L::kRows;
+  x.gpitch = (subs == 2 ? 16 : kKeyTile) + 4;
+  x.gsub = (x.heads * x.gpitch * 4 + 127) / 128 * 128;
+  x.gstage = subs * x.gsub + (subs * x.heads * 8 + 127) / 128 * 128;
+  constexpr int kMostGates = 2 * ((L::kRows * 20 * 4 + 127) / 128 * 128) + 256;
+  constexpr size_t kMost = 232448 - 1024;  // of an SM's shared memory, less the static part
+  const size_t fixed = 1024 + sizeof(long long) * ((size_t)p.a.B + 1);
+  const size_t one = (size_t)L::kWarps * (2 * L::kTileBytes + x.gstage);
+  // Three stages where they fit beside the gates and the sequences' offsets.
+  x.stages = fixed + 3 * one <= kMost ? 3 : 2;
+  const size_t smem = fixed + x.stages * one;
+  static_assert(1024 + 8 * (kMaxSeqs + 1) + 2 * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  TraceScope trace("decode", s);
+  if (p.pre.key_tiles == 0) {
+    kernel<<<kSMs, 32 * L::kWarps, smem, s>>>(maps[0], maps[1], maps[2], p, x);
+    return cudaGetLastError();
+  }
+  const cudaError_t f =
+      launch_dependent(kernel, dim3(kSMs), dim3(32 * L::kWarps), smem, s, maps[0], maps[1], maps[2], p, x);
+  return f != cudaSuccess ? f : cudaGetLastError();
+}
+
+}  // namespace
+
+int decode_mma_workers(int d) { return kSMs * (d == 128 ? MmaLayout<128, 1>::kWarps : MmaLayout<64, 1>::kWarps); }
+int decode_mma_rows(int rows) { return rows <= 8 ? 8 : 16; }
+
+cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t s) {
+  const PagedArgs& a = p.a;
+  const int KS = a.page_size < kKeyTile ? a.page_size : kKeyTile, G = a.H / a.Hkv;
+  CUtensorMap maps[3];
+  if (!make_page_map(&maps[0], a.k, a.d, a.page_size, a.Hkv, a.num_pages, KS) ||
+      !make_page_map(&maps[1], a.v, a.d, a.page_size, a.Hkv, a.num_pages, KS) ||
+      !make_f32_3d_map(&maps[2], a.g, a.page_size, a.H, a.num_pages, (uint64_t)a.page_size * 4,
+                       (uint64_t)a.page_size * a.H * 4, KS + 4, G < p.Rt ? G : p.Rt))
+    return cudaErrorInvalidValue;
+  if (a.d == 64) return p.Rt == 8 ? launch<64, 1>(p, maps, s) : launch<64, 2>(p, maps, s);
+  return p.Rt == 8 ? launch<128, 1>(p, maps, s) : launch<128, 2>(p, maps, s);
+}
+
+}  // namespace fox

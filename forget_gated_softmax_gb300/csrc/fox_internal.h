@@ -278,6 +278,11 @@ bool make_f32_3d_map(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d
                      uint64_t pitch2, uint32_t box0, uint32_t box1);
 bool make_bnhd_map(CUtensorMap* map, const void* base, int B, int N, int H, int d, int box_rows = kTile,
                    bool f16 = false);
+// 4-D bf16 tensor map over a paged pool [pages, Hkv, page_size, d], box 64 channels x box_rows tokens, 128-byte swizzle.
+bool make_page_map(CUtensorMap* map, const void* base, int d, int page_size, int Hkv, int pages, int box_rows);
+// 3-D bf16 tensor map over query rows [rows, H, d], `stride` elements a row, box 64 channels x box_heads x box_rows.
+bool make_q_rows_map(CUtensorMap* map, const void* base, int d, int H, int rows, long long stride, int box_heads,
+                     int box_rows);
 // Host helpers for the gate projection: x [B, N, hidden] with a box of 64 x 128 x 1, and
 // W_f [H, hidden] with a box of 64 x (H rounded up to 16); bf16, 128-byte swizzle.
 bool make_x_map(CUtensorMap* map, const void* base, int B, int N, int hidden);

@@ -102,9 +102,11 @@ FOX_HD size_t g_offset(const PagedArgs& a, int page, int h, int slot) {
 FOX_HD size_t gbase_offset(const PagedArgs& a, int page, int h) { return ((size_t)page * a.H + h) * 2; }
 
 // ---- work of the decode kernels ----
-// An item is (key head, sequence, row tile): `Rt` of the sequence's n * G query rows of that key
-// head (row r = token r / G, head hkv * G + r % G) against its keys. Its units are the key tiles of
-// kKeyTile tokens. The units of all items lie on one line, items in the order (key head, sequence,
+// An item is (key head, sequence, row tile): `Rt` of the sequence's n * Gp query rows of that key
+// head against its keys. Row r is token r / Gp and query head hkv * G + r % Gp of the group's G = H / Hkv;
+// Gp is G, or its next multiple of Rt where G is larger than a row tile, so that a tile never holds the
+// end of one token's group and the start of the next's (rows with r % Gp >= G are empty). An item's
+// units are the key tiles of kKeyTile tokens. The units of all items lie on one line, items in the order (key head, sequence,
 // row tile), and worker w takes units [w q, (w + 1) q): equal work whatever the lengths are.
 // An item that lies in one worker's range is finished there; the others leave one partial result a
 // worker, in slot worker + item: along the line each new (worker, item) pair raises one of the
@@ -117,8 +119,9 @@ FOX_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 FOX_HD int walk_keys(const PagedArgs& a, const SeqInfo& s, bool walk_prefix) {
   return s.own < 0 ? 0 : s.own + (walk_prefix ? a.prefix_len : 0);
 }
-FOX_HD long long seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, bool walk_prefix) {
-  return (long long)ceil_div(walk_keys(a, s, walk_prefix), kKeyTile) * ceil_div(s.n * (a.H / a.Hkv), Rt);
+FOX_HD int padded_group(int G, int Rt) { return G <= Rt ? G : ceil_div(G, Rt) * Rt; }
+FOX_HD long long seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, int Gp, bool walk_prefix) {
+  return (long long)ceil_div(walk_keys(a, s, walk_prefix), kKeyTile) * ceil_div(s.n * Gp, Rt);
 }
 FOX_HD long long units_per_worker(long long total, int workers) {
   const long long q = (total + workers - 1) / workers;

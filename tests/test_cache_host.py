@@ -152,7 +152,7 @@ long long t_g(const int* n, int page, int h, int s) { return (long long)g_offset
 long long t_units(const int* n, const int* cu, const int* lens, int b, int Rt, int walk) {
   const PagedArgs a = args(n, cu, lens, nullptr, nullptr);
   bool bad;
-  return seq_units(a, seq_info(a, b, &bad), Rt, walk);
+  return seq_units(a, seq_info(a, b, &bad), Rt, padded_group(a.H / a.Hkv, Rt), walk);
 }
 long long t_each(long long total, int workers) { return units_per_worker(total, workers); }
 }
@@ -246,7 +246,7 @@ def test_work_line_gives_every_pair_of_worker_and_item_its_own_slot(H, workers):
     its own, and fewer than workers + items are in use."""
     rng = random.Random(workers)
     for _ in range(30):
-        B, Hkv, G = rng.randint(1, 12), rng.choice([1, 2, 8]), rng.choice([1, 3, 4, 7])
+        B, Hkv, G = rng.randint(1, 12), rng.choice([1, 2, 8]), rng.choice([1, 3, 4, 7, 20])
         new = [rng.randint(0, 9) for _ in range(B)]
         cu = [0]
         for x in new:
@@ -255,12 +255,13 @@ def test_work_line_gives_every_pair_of_worker_and_item_its_own_slot(H, workers):
         Rt = rng.choice([8, 16, 32])
         n = _n(H=G * Hkv, Hkv=Hkv, B=B, rows=max(1, cu[-1]), max_new=max(new + [1]), stride=100)
         units = [H.t_units(n, _ints(cu), _ints(lens), b, Rt, 1) for b in range(B)]
-        rts = [-(-x * G // Rt) for x in new]
+        Gp = G if G <= Rt else -(-G // Rt) * Rt  # a token's rows fill whole row tiles, or lie in one
+        rts = [-(-x * Gp // Rt) for x in new]
         assert units == [(-(-y // 32)) * r for y, r in zip(lens, rts)]
         total = sum(units) * Hkv
         each = H.t_each(total, workers)
         assert each * workers >= total and each >= 1
-        RTmax, u, slots = -(-max(new + [1]) * G // Rt), 0, set()
+        RTmax, u, slots = -(-max(new + [1]) * Gp // Rt), 0, set()
         for h in range(Hkv):
             for b in range(B):
                 for rt in range(rts[b]):
