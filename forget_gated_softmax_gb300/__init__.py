@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_PKG, "libfox.so")
 
 FOX_DTYPE_BF16 = 0
 FOX_DTYPE_F32 = 1
+FOX_CACHE_ZERO_BYTES = 16384  # of a paged-cache workspace: zero before its first call
 
 STATUS_NAMES = {
     0: "FOX_OK",
@@ -508,14 +509,14 @@ def fox_tile_span(q, k, z, *, scale: float = 0.0, bias_from_j: bool = False, ws=
 class Cache:
     """A paged cache over the caller's tensors (see fox_cache in include/fox.h). Made by make_cache or new_cache."""
 
-    __slots__ = ("k", "v", "g", "gbase", "params", "device", "dtype", "H", "Hkv", "d", "page_size")
+    __slots__ = ("k", "v", "g", "gbase", "params", "ref", "device", "dtype", "H", "Hkv", "d", "page_size")
 
 
 class Batch:
     """One step's sequences over the caller's tensors (see fox_batch in include/fox.h). Made by make_batch.
     The contents of its tensors may change between calls; their storage may not."""
 
-    __slots__ = ("lens", "table", "cu_new", "prefix_table", "params", "device", "B")
+    __slots__ = ("lens", "table", "cu_new", "prefix_table", "params", "ref", "device", "B")
 
 
 def make_cache(k, v, g, gbase) -> Cache:
@@ -539,6 +540,7 @@ def make_cache(k, v, g, gbase) -> Cache:
     c.k, c.v, c.g, c.gbase, c.device, c.dtype = k, v, g, gbase, k.device, k.dtype
     c.H, c.Hkv, c.d, c.page_size = H, Hkv, d, S
     c.params = fox_cache(pages, S, H, Hkv, d, _dtype_code(k), _ptr(k), _ptr(v), _ptr(g), _ptr(gbase))
+    c.ref = ctypes.byref(c.params)
     return c
 
 
@@ -574,64 +576,72 @@ def make_batch(lens, table, *, cu_new=None, max_new: int = 1, prefix_table=None,
             raise ValueError("make_batch needs tensors whose last dimension is contiguous")
     b = Batch()
     b.lens, b.table, b.cu_new, b.prefix_table, b.device, b.B = lens, table, cu_new, prefix_table, lens.device, B
-    stride = table.stride(0) if B > 1 else table.shape[1]
-    if stride < table.shape[1]:
-        raise ValueError("make_batch: rows of table overlap")
-    # Entries between table's rows are the caller's too: the length check allows no token there.
-    if stride != table.shape[1]:
+    stride = table.shape[1]
+    if not table.is_contiguous():
         raise ValueError("make_batch: table must be contiguous")
     if prefix_table is not None and prefix_table.dim() != 1:
         raise ValueError("make_batch: prefix_table must be one-dimensional")
     b.params = fox_batch(B, int(max_new), stride, int(prefix_len), _ptr(cu_new), _ptr(lens), _ptr(table),
                          _ptr(prefix_table))
+    b.ref = ctypes.byref(b.params)
     return b
 
 
 def fox_cache_workspace_bytes(cache: Cache, batch: Batch, rows: int) -> int:
-    return int(lib().fox_cache_workspace_bytes(ctypes.byref(cache.params), ctypes.byref(batch.params), int(rows)))
+    return int(lib().fox_cache_workspace_bytes(cache.ref, batch.ref, int(rows)))
 
 
 def cache_workspace(cache: Cache, batch: Batch, rows: int):
-    """A workspace for fox_cache_append and fox_decode with up to `rows` rows of this batch, its error word zero."""
+    """A workspace for fox_cache_append and fox_decode with `rows` rows of this batch, its header zero."""
     n = fox_cache_workspace_bytes(cache, batch, rows)
     if n == 0:
         raise FoxError(1, "cache_workspace")
     ws = workspace(n, cache.device)
-    ws[:256].zero_()
+    ws[:FOX_CACHE_ZERO_BYTES].zero_()
     return ws
 
 
-def _check_cache_call(where: str, cache: Cache, batch: Batch):
+def _cache_call_device(where: str, cache: Cache, batch: Batch) -> int:
     torch = _torch()
+    index = cache.device.index
     if batch.device != cache.device:
         raise ValueError(f"{where}: cache and batch are on different devices")
-    if cache.device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise ValueError(f"{where}: the cache is not on the current CUDA device")
-    need = -(-batch.params.prefix_len // cache.page_size)
-    if need and batch.prefix_table.shape[0] < need:
-        raise ValueError(f"{where}: prefix_table has fewer than {need} pages")
+    if batch.prefix_table is not None and batch.prefix_table.shape[0] * cache.page_size < batch.params.prefix_len:
+        raise ValueError(f"{where}: prefix_table has too few pages")
+    return index
 
 
 def _row_stride(where: str, name: str, t, cache: Cache, heads: int, rows: int) -> int:
     """The stride of t's rows; t is [rows, heads, d] with contiguous rows, in the cache's type, on its device."""
-    if tuple(t.shape) != (rows, heads, cache.d):
+    if t.shape != (rows, heads, cache.d):
         raise ValueError(f"{where}: {name} must be [{rows}, {heads}, {cache.d}], got {tuple(t.shape)}")
     if t.dtype != cache.dtype:
         raise TypeError(f"{where}: {name} must be {cache.dtype}, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{where}: {name} is not on the cache's device")
     s0, s1, s2 = t.stride()
-    if (s2 != 1 or (heads > 1 and s1 != cache.d)) and t.numel():
+    if (s2 != 1 or (heads > 1 and s1 != cache.d)) and rows:
         raise ValueError(f"{where}: {name} needs contiguous rows")
     return s0
 
 
-def _on_stream(stream):
-    """The context in which this call's own allocations belong to the stream that uses them."""
-    torch = _torch()
-    import contextlib
+def _own_tensors(stream, *makers):
+    """What this call allocates itself, in the allocator's order of the stream that uses it."""
+    if stream is None:
+        return [m() for m in makers]
+    with _torch().cuda.stream(stream):
+        return [m() for m in makers]
 
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+def _launch_stream(stream, index: int) -> int:
+    """The handle to launch on; the current stream's without building a Stream object where torch offers it."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
 def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, sin=None, pairs: bool = False,
@@ -643,41 +653,44 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
     returned (None without q). Rows may be strided views, as those of a joint projection's output."""
     torch = _torch()
     where = "fox_cache_append"
-    _check_cache_call(where, cache, batch)
+    index = _cache_call_device(where, cache, batch)
     rows = k.shape[0]
     ks = _row_stride(where, "k", k, cache, cache.Hkv, rows)
     vs = _row_stride(where, "v", v, cache, cache.Hkv, rows)
-    if tuple(z.shape) != (rows, cache.H) or z.dtype != torch.float32 or z.device != cache.device:
+    if z.shape != (rows, cache.H) or z.dtype != torch.float32 or z.device != cache.device:
         raise ValueError(f"{where}: z must be [{rows}, {cache.H}] float32 on the cache's device")
-    if cache.H > 1 and rows and z.stride(1) != 1:
+    zs, z1 = z.stride()
+    if z1 != 1 and cache.H > 1 and rows:
         raise ValueError(f"{where}: z needs contiguous rows")
     rot = None
-    if (cos is None) != (sin is None) or (cos is None and (q is not None or q_out is not None)):
-        raise ValueError(f"{where}: cos and sin come together, and q only with them")
-    with _on_stream(stream):
-        if cos is not None:
-            if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32:
-                raise ValueError(f"{where}: cos and sin must be float32 [positions, r / 2]")
-            if not cos.is_contiguous() or not sin.is_contiguous() or cos.device != cache.device or sin.device != cache.device:
-                raise ValueError(f"{where}: cos and sin must be contiguous on the cache's device")
-            qs = 0
-            if q is not None:
-                qs = _row_stride(where, "q", q, cache, cache.H, rows)
-                if q_out is None:
-                    q_out = torch.empty((rows, cache.H, cache.d), dtype=q.dtype, device=q.device)
-                else:
-                    _row_stride(where, "q_out", q_out, cache, cache.H, rows)
-                    if not q_out.is_contiguous():
-                        raise ValueError(f"{where}: q_out must be contiguous")
-            elif q_out is not None:
-                raise ValueError(f"{where}: q_out without q")
-            rot = fox_rotary(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(pairs)), _ptr(q), qs, _ptr(q_out))
-        if ws is None:
-            ws = torch.zeros(256, dtype=torch.uint8, device=cache.device)
-        st = lib().fox_cache_append(
-            ctypes.byref(cache.params), ctypes.byref(batch.params), rows, _ptr(k), ks, _ptr(v), vs, _ptr(z), z.stride(0),
-            ctypes.byref(rot) if rot is not None else None, _ptr(ws), ws.numel(), _stream_handle(stream),
-        )
+    if cos is None or sin is None:
+        if cos is not None or sin is not None or q is not None or q_out is not None:
+            raise ValueError(f"{where}: cos and sin come together, and q only with them")
+    else:
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32:
+            raise ValueError(f"{where}: cos and sin must be float32 [positions, r / 2]")
+        if not cos.is_contiguous() or not sin.is_contiguous() or cos.device != cache.device or sin.device != cache.device:
+            raise ValueError(f"{where}: cos and sin must be contiguous on the cache's device")
+        qs = 0
+        if q is not None:
+            qs = _row_stride(where, "q", q, cache, cache.H, rows)
+            if q_out is None:
+                (q_out,) = _own_tensors(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+            else:
+                _row_stride(where, "q_out", q_out, cache, cache.H, rows)
+                if not q_out.is_contiguous():
+                    raise ValueError(f"{where}: q_out must be contiguous")
+        elif q_out is not None:
+            raise ValueError(f"{where}: q_out without q")
+        positions, half = cos.shape
+        rot = ctypes.byref(fox_rotary(cos.data_ptr(), sin.data_ptr(), positions, 2 * half, int(bool(pairs)),
+                                      _ptr(q), qs, _ptr(q_out)))
+    if ws is None:
+        (ws,) = _own_tensors(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
+    st = lib().fox_cache_append(
+        cache.ref, batch.ref, rows, k.data_ptr(), ks, v.data_ptr(), vs, z.data_ptr(), zs, rot, ws.data_ptr(), ws.numel(),
+        _launch_stream(stream, index),
+    )
     if st != 0:
         raise FoxError(st, where)
     return q_out
@@ -686,29 +699,29 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
 def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
                ws=None, stream=None) -> Tuple[object, object]:
     """Attention of the batch's newest tokens, appended before, over the cache: q [rows, H, d] -> (O [rows, H, d],
-    LSE [rows, H] fp32). A shared prefix of the batch is read and multiplied once for all its sequences.
+    LSE [rows, H] fp32). A shared prefix of the batch is read and multiplied once for all its sequences (bf16).
     Rows of idle sequences get O = 0 and LSE = -inf; rows behind the last sequence are not written."""
     torch = _torch()
     where = "fox_decode"
-    _check_cache_call(where, cache, batch)
+    index = _cache_call_device(where, cache, batch)
     rows = q.shape[0]
     qs = _row_stride(where, "q", q, cache, cache.H, rows)
-    with _on_stream(stream):
-        if o is None:
-            o = torch.empty((rows, cache.H, cache.d), dtype=cache.dtype, device=cache.device)
-        if lse is None:
-            lse = torch.empty((rows, cache.H), dtype=torch.float32, device=cache.device)
+    if o is None:
+        (o,) = _own_tensors(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+    else:
         _row_stride(where, "o", o, cache, cache.H, rows)
-        if not o.is_contiguous() or not lse.is_contiguous():
-            raise ValueError(f"{where}: o and lse must be contiguous")
-        if tuple(lse.shape) != (rows, cache.H) or lse.dtype != torch.float32 or lse.device != cache.device:
-            raise ValueError(f"{where}: lse must be [{rows}, {cache.H}] float32 on the cache's device")
-        if ws is None:
-            ws = cache_workspace(cache, batch, rows)
-        st = lib().fox_decode(
-            ctypes.byref(cache.params), ctypes.byref(batch.params), rows, _ptr(q), qs, float(scale), int(bool(bias_from_j)),
-            _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream_handle(stream),
-        )
+        if not o.is_contiguous():
+            raise ValueError(f"{where}: o must be contiguous")
+    if lse is None:
+        (lse,) = _own_tensors(stream, lambda: torch.empty((rows, cache.H), dtype=torch.float32, device=q.device))
+    elif lse.shape != (rows, cache.H) or lse.dtype != torch.float32 or lse.device != cache.device or not lse.is_contiguous():
+        raise ValueError(f"{where}: lse must be contiguous [{rows}, {cache.H}] float32 on the cache's device")
+    if ws is None:
+        (ws,) = _own_tensors(stream, lambda: cache_workspace(cache, batch, rows))
+    st = lib().fox_decode(
+        cache.ref, batch.ref, rows, q.data_ptr(), qs, scale, 1 if bias_from_j else 0, o.data_ptr(), lse.data_ptr(),
+        ws.data_ptr(), ws.numel(), _launch_stream(stream, index),
+    )
     if st != 0:
         raise FoxError(st, where)
     return o, lse

@@ -9,6 +9,8 @@
 
 using namespace fox;
 
+static_assert(FOX_CACHE_ZERO_BYTES == kCacheHeaderBytes, "the header that include/fox.h documents");
+
 namespace {
 
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -43,6 +45,7 @@ fox_status check_batch(const fox_cache* c, const fox_batch* s, int rows, PagedAr
     *a = PagedArgs{};
     a->num_pages = c->num_pages;
     a->page_size = c->page_size;
+    a->page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
     a->H = c->H;
     a->Hkv = c->Hkv;
     a->d = c->d;
@@ -91,7 +94,8 @@ extern "C" {
 size_t fox_cache_workspace_bytes(const fox_cache* c, const fox_batch* s, int rows) {
   PagedArgs a;
   if (check_cache(c) != FOX_OK || check_batch(c, s, rows, &a) != FOX_OK) return 0;
-  if (a.B == 0 || rows == 0) return kErrWordBytes;
+  if (a.B == 0 || rows == 0) return kCacheHeaderBytes;
+  if (!decode_fits(a, c->dtype == FOX_DTYPE_F32)) return 0;
   return decode_workspace_bytes(a, c->dtype == FOX_DTYPE_F32);
 }
 
@@ -155,6 +159,7 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
   if (!row_ok(q, q_stride, c->H, c, rows) || !o || !at16(o) || !lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return FOX_ERR_INVALID_ARG;
   const bool f32 = c->dtype == FOX_DTYPE_F32;
+  if (!decode_fits(x.a, f32)) return FOX_ERR_UNSUPPORTED;
   st = check_ws(workspace, workspace_bytes, decode_workspace_bytes(x.a, f32));
   if (st != FOX_OK) return st;
   x.a.err = static_cast<uint32_t*>(workspace);

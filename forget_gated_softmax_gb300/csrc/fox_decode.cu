@@ -1,5 +1,5 @@
 // Attention of the newest tokens of every sequence over the paged cache in fp32, on CUDA cores, and
-// the merge of partial results (of this kernel's and of the bf16 one's, fox_decode_mma.cu).
+// the launches of fox_decode.
 //
 // Math ("Forgetting Transformer (FoX) Attention" module source, ForgettingAttention.forward, for
 // the rows of the newest tokens): x_ij = scale q_i . k_j + c_i - c_j over the keys j <= pos_i of
@@ -28,35 +28,31 @@ __device__ __forceinline__ void load4(const float* p, float* f) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kSimtWarps) decode_simt_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int E = D / 32;
-  extern __shared__ long long cum[];  // [B + 1]
-  __shared__ long long scratch[kSimtWarps];
-  __shared__ float qs[kSimtWarps][kSimtRows][D];
-  __shared__ double ci[kSimtWarps][kSimtRows];
-  grid_dep_trigger();
+  extern __shared__ int cum[];  // [B + 1]
+  __shared__ int scratch[kSimtWarps];
+  __shared__ __align__(16) float qs[kSimtWarps][kSimtRows][D];  // scaled queries; at the end the kept rows
+  __shared__ Gate2 ci[kSimtWarps][kSimtRows];
+  __shared__ float wgt[kJoinMost * kSimtRows];
+  __shared__ float4 part[32 * kSimtWarps];
+  __shared__ Kept<kSimtRows, kSimtWarps> kept;
   const PagedArgs& a = p.a;
   scan_units(p, cum, scratch);
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) p.cum[b] = cum[b];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size;
-  const long long per_head = cum[a.B], total = per_head * a.Hkv;
-  const long long each = units_per_worker(total, p.workers);
-  const long long w = (long long)blockIdx.x * kSimtWarps + warp;
-  long long u = w * each;
-  const long long u_end = min(total, u + each);
-  while (u < u_end) {
-    const int hkv = static_cast<int>(u / per_head);
-    const long long in_head = u - hkv * per_head;
-    const int b = find_seq(cum, a.B, in_head);
-    bool bad;
-    const SeqInfo s = seq_info(a, b, &bad);
-    const int P = p.walk_prefix ? a.prefix_len : 0;
-    const int keys = walk_keys(a, s, p.walk_prefix), tiles = ceil_div(keys, kKeyTile);
-    const int rt = static_cast<int>((in_head - cum[b]) / tiles);
-    const int tile0 = static_cast<int>((in_head - cum[b]) % tiles);
-    const int tile1 = static_cast<int>(min(static_cast<long long>(tiles), tile0 + (u_end - u)));
+  const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size, P = a.prefix_len;
+  const int total = cum[a.B] * a.Hkv, each = units_per_worker(total, p.workers);
+  const int w = blockIdx.x * kSimtWarps + warp;
+  const int u0 = min(total, w * each);
+  int left = min(total, u0 + each) - u0;
+  Place at;
+  if (left > 0) at = place_of(p, cum, u0);
+  if (lane == 0) kept.i0[warp] = -1;
+  while (left > 0) {
+    // A segment: key tiles tile0 .. tile1 - 1 of one item.
+    const SeqInfo s = at.s;
+    const int b = at.b, hkv = at.hkv, rt = at.rt;
+    const int keys = walk_keys(a, s, true), tile0 = at.tile, tile1 = min(at.tiles, tile0 + left);
     const int R = min(p.Rt, s.n * Gp - rt * p.Rt);
 
     __syncwarp();
@@ -69,7 +65,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps) decode_simt_kernel(const Deco
 #pragma unroll
         for (int e = 0; e < 4; ++e) qs[warp][r][c + e] = f[e] * p.scale2;
       }
-      if (lane == 0) ci[warp][r] = gate_at(a, b, s.own - s.n + t, h);
+      if (lane == 0) {
+        const int i = s.own - s.n + t;
+        ci[warp][r] = gate_sum(a, own_page_or_0(a, b, i), i % S, h);
+      }
     }
     __syncwarp();
 
@@ -115,7 +114,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) decode_simt_kernel(const Deco
           const int rr = rt * p.Rt + r, t = rr / Gp, h = hkv * G + min(rr % Gp, G - 1);
           if (j <= P + s.own - s.n + t) {
             const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
-            const float beta = static_cast<float>(ci[warp][r] - base.x - base.y);
+            const float beta = (ci[warp][r].hi - base.x) + (ci[warp][r].lo - base.y);
             const int gs = p.bias_from_j ? slot - 1 : slot;
             const float gj = gs >= 0 ? a.g[g_offset(a, page, h, gs)] : 0.f;
             x = fmaf(beta - gj, kLog2e, sc[r]);
@@ -158,9 +157,15 @@ __global__ void __launch_bounds__(32 * kSimtWarps) decode_simt_kernel(const Deco
       }
     }
     // The item's first and last unit say whether this worker has all of it.
-    const long long i0 = hkv * per_head + cum[b] + (long long)rt * tiles, i1 = i0 + tiles - 1;
-    const bool whole = i0 / each == i1 / each;
-    const size_t slot0 = (size_t)(w + ((long long)hkv * a.B + b) * p.RTmax + rt) * p.Rs;
+    const int i0 = hkv * cum[a.B] + cum[b] + rt * at.tiles;
+    const bool whole = i0 / each == (i0 + at.tiles - 1) / each;
+    const bool keep = !whole && tile1 - tile0 == left;  // for the block to join with its neighbours'
+    const size_t slot0 = slot_of(p, w, hkv, b, rt);
+    if (keep && lane == 0) {
+      kept.i0[warp] = i0;
+      kept.at[warp] = at;
+    }
+    __syncwarp();
 #pragma unroll
     for (int r = 0; r < kSimtRows; ++r) {
       if (r >= R) continue;
@@ -176,111 +181,130 @@ __global__ void __launch_bounds__(32 * kSimtWarps) decode_simt_kernel(const Deco
         const size_t row = (size_t)(s.row0 + t) * a.H + h;
         put_out<float>(static_cast<float*>(p.o) + row * D + lane * E, acc[r], E);
         if (lane == 0) p.lse[row] = sum > 0.f ? (m[r] + log2f(sum)) * kLn2 : -INFINITY;
+      } else if (keep) {
+        if (lane == 0) {
+          kept.m[warp][r] = m[r];
+          kept.l[warp][r] = sum;
+        }
+        put_out<float>(&qs[warp][r][lane * E], acc[r], E);
       } else {
         if (lane == 0) p.ml[slot0 + r] = make_float2(m[r], sum);
         put_out<float>(p.po + (slot0 + r) * D + lane * E, acc[r], E);
       }
     }
-    u += tile1 - tile0;
+    left -= tile1 - tile0;
+    advance(p, at, tile1 - tile0, left > 0);
   }
+  clear_idle_rows<float, D>(p);
+  join_items<float, D, kSimtRows, kSimtWarps>(p, cum, total, each, kept, &qs[0][0][0], kSimtRows * D, D, wgt, part);
 }
 
-// One warp a (row, query head): the partial results of the row's item joined, in the workers' order.
-// Rows of idle sequences get O = 0 and LSE = -inf.
+// One output row by one warp: the partial results of its own item and of the shared prefix joined, in the
+// workers' order. One warp a (row, query head).
 constexpr int kMergeWarps = 4;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const DecodeParams p) {
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int E = D / 32;
-  grid_dep_wait();
   const PagedArgs& a = p.a;
-  const long long id = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int row = static_cast<int>(id / a.H), h = static_cast<int>(id % a.H);
+  const int id = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int row = id / a.H, h = id - row * a.H;
   if (row >= a.rows) return;
+  // What the call was given may be read before the kernels ahead are through.
   const int b = seq_of_row(a, row);
   if (b < 0) return;
   bool bad;
   const SeqInfo s = seq_info(a, b, &bad);
-  if (bad || row < s.row0 || row >= s.row0 + s.n) return;
-  T* o = static_cast<T*>(p.o) + ((size_t)row * a.H + h) * D + lane * E;
-  float* lse = p.lse + (size_t)row * a.H + h;
-  float acc[E] = {};
-  if (s.own < 0) {
-    put_out<T>(o, acc, E);
-    if (lane == 0) *lse = -INFINITY;
-    return;
-  }
-  const int G = a.H / a.Hkv, hkv = h / G, r = (row - s.row0) * p.Gp + h % G;
-  const int rt = r / p.Rt, tiles = ceil_div(walk_keys(a, s, p.walk_prefix), kKeyTile);
-  const long long per_head = p.cum[a.B], each = units_per_worker(per_head * a.Hkv, p.workers);
-  const long long i0 = hkv * per_head + p.cum[b] + (long long)rt * tiles, i1 = i0 + tiles - 1;
-  const long long w0 = i0 / each, w1 = i1 / each;
-  const bool shared = p.pre.key_tiles > 0;
-  if (w0 == w1 && !shared) return;  // finished by its one worker
-  // Partial results: the own item's, then the prefix's. Of result i, ml and po lie `step` rows further on.
-  const int n_own = static_cast<int>(w1 - w0) + 1;
-  const size_t own0 = (size_t)(w0 + ((long long)hkv * a.B + b) * p.RTmax + rt) * p.Rs + r % p.Rt;
-  int n = n_own, step = 0;
-  size_t pre0 = 0;
-  float shift = 0.f;  // log2 e (c_i - c_last): what the row's prefix scores lack
-  if (shared) {
-    const PrefixPlan& x = p.pre;
-    const int hl = h % G, tile = row / x.tpt * x.head_chunks + hl / x.hp;
-    const int item = hkv * x.items + (x.row_tiles == 1 ? 0 : tile / 2);
-    const long long pe = units_per_worker((long long)a.Hkv * x.items * x.key_tiles, x.workers);
-    const long long v0 = (long long)item * x.key_tiles / pe, v1 = ((long long)(item + 1) * x.key_tiles - 1) / pe;
-    const bool both = x.row_tiles == 1;  // the streams are two results, else this row is one stream's
-    n += static_cast<int>(v1 - v0 + 1) * (both ? 2 : 1);
-    step = both ? kTile : 2 * kTile;
-    pre0 = ((size_t)(v0 + item) * 2 + (both ? 0 : tile & 1)) * kTile + row % x.tpt * x.hp + hl % x.hp;
-    const int last = a.prefix_len - 1, page = max(prefix_page(a, last), 0);
-    shift = static_cast<float>(gate_at(a, b, s.own - s.n + (row - s.row0), h) - gate_sum(a, page, last % a.page_size, h)) *
-            kLog2e;
-  }
+  if (bad || row < s.row0 || row >= s.row0 + s.n || s.own < 0) return;  // idle rows are written already
+  const int G = a.H / a.Hkv, hkv = h / G, hl = h - hkv * G;
+  const int pos = s.own - s.n + (row - s.row0);
+  const int last = a.prefix_len - 1, lpage = max(prefix_page(a, last), 0);
+  const Gate2 ci = gate_sum(a, own_page_or_0(a, b, pos), pos % a.page_size, h);
+  const Gate2 cl = gate_sum(a, lpage, last % a.page_size, h);
+  const float shift = ((ci.hi - cl.hi) + (ci.lo - cl.lo)) * kLog2e;  // what the row's prefix scores lack
+  // The prefix's partial results: of result i, ml and po lie `step` rows further on.
+  const PrefixPlan& x = p.pre;
+  const int tile = row / x.tpt * x.head_chunks + hl / x.hp;
+  const bool both = x.row_tiles == 1;  // the streams are two results, else this row is one stream's
+  const int item = hkv * x.items + (both ? 0 : tile / 2);
+  const int peach = units_per_worker(a.Hkv * x.items * x.key_tiles, x.workers);
+  const int v0 = item * x.key_tiles / peach, v1 = ((item + 1) * x.key_tiles - 1) / peach;
+  const int n_pre = (v1 - v0 + 1) * (both ? 2 : 1), step = both ? kTile : 2 * kTile;
+  const size_t pre0 = ((size_t)(v0 + item) * 2 + (both ? 0 : tile & 1)) * kTile + row % x.tpt * x.hp + hl % x.hp;
+  grid_dep_wait();
+  const int tiles = ceil_div(s.own, kKeyTile), r = (row - s.row0) * p.Gp + hl, rt = r / p.Rt;
+  const int per_head = __ldcg(p.cum + a.B), each = units_per_worker(per_head * a.Hkv, p.workers);
+  const int i0 = hkv * per_head + __ldcg(p.cum + b) + rt * tiles;
+  // The own item's: one a block of workers, and its last worker's own where that is another (join_items).
+  const int i1 = i0 + tiles - 1, w0 = i0 / each, w1 = i1 / each, nb = w1 / p.warps - w0 / p.warps + 1;
+  const bool extra = w1 > w0 && w1 > w1 / p.warps * p.warps && min(per_head * a.Hkv, (w1 + 1) * each) > i1 + 1;
+  const int n_own = nb + extra, n = n_own + n_pre;
+  const size_t own0 = slot_of(p, 0, hkv, b, rt) + r - rt * p.Rt;
+  auto own_at = [&](int i) {
+    const int w = i == 0 ? w0 : i < nb ? (w0 / p.warps + i) * p.warps : w1;
+    return own0 + (size_t)w * p.Rs;
+  };
   auto ml_of = [&](int i) {
-    if (i < n_own) return p.ml[own0 + (size_t)i * p.Rs];
-    float2 x = p.pre.ml[pre0 + (size_t)(i - n_own) * step];
-    x.x += shift;
-    return x;
+    if (i < n_own) return __ldcg(p.ml + own_at(i));
+    float2 y = __ldcg(x.ml + pre0 + (size_t)(i - n_own) * step);
+    y.x += shift;
+    return y;
   };
-  auto po_of = [&](int i) {
-    return i < n_own ? p.po + (own0 + (size_t)i * p.Rs) * D : p.pre.po + (pre0 + (size_t)(i - n_own) * step) * D;
-  };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, ml_of(i).x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float safe = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+  float m = -INFINITY, l = 0.f, acc[E] = {};
   for (int first = 0; first < n; first += 32) {
-    float wgt = 0.f;
-    if (first + lane < n) {
-      const float2 ml = ml_of(first + lane);
-      wgt = ex2_approx(ml.x - safe);
-      l += ml.y * wgt;
-    }
-    const int c = min(32, n - first);
-#pragma unroll 8
-    for (int i = 0; i < c; ++i) {
-      const float f = __shfl_sync(0xffffffffu, wgt, i);
-      if (f == 0.f) continue;  // nothing of it counts (a stream without keys wrote no sums of V)
-      const float* src = po_of(first + i) + lane * E;
+    const float2 ml = first + lane < n ? ml_of(first + lane) : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src + e);
-        acc[e] = fmaf(f, x.x, acc[e]);
-        acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, m);
+    const float safe = top == -INFINITY ? 0.f : top;
+    const float alpha = ex2_approx(m - safe), wgt = ex2_approx(ml.x - safe);
+    m = top;
+    l = l * alpha + ml.y * wgt;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= alpha;
+    const int c = min(32, n - first);
+    constexpr int kBatch = 8;  // loads in flight
+    for (int i = 0; i < c; i += kBatch) {
+      float2 y[kBatch][E / 2];
+      float f[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        f[j] = __shfl_sync(0xffffffffu, wgt, (i + j) & 31);
+        // A weight of 0 counts for nothing (a stream without keys wrote no sums of V): result 0 is read instead.
+        if (i + j >= c) f[j] = 0.f;
+        const int k = f[j] != 0.f ? first + i + j : 0;
+        const float* src = (k < n_own ? p.po + own_at(k) * D
+                                      : x.po + (pre0 + (size_t)(k - n_own) * step) * D) +
+                           lane * E;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[j][e] = __ldcg(reinterpret_cast<const float2*>(src) + e);
       }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          acc[2 * e] = fmaf(f[j], y[j][e].x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(f[j], y[j][e].y, acc[2 * e + 1]);
+        }
     }
   }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] *= inv;
-  put_out<T>(o, acc, E);
-  if (lane == 0) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  const size_t at = (size_t)row * a.H + h;
+  put_out<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p.o) + at * D + lane * E, acc, E);
+  if (lane == 0) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+cudaError_t launch_merge(const DecodeParams& p, cudaStream_t s) {
+  TraceScope trace("decode_merge", s);
+  const cudaError_t e = launch_dependent(prefix_merge_kernel<D>, dim3(ceil_div(p.a.rows * p.a.H, kMergeWarps)),
+                                         dim3(32 * kMergeWarps), 0, s, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 struct DecodeLayout {
@@ -297,10 +321,10 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   const int most = a.max_new * L.Gp;
   L.Rs = most < L.Rt ? most : L.Rt;
   L.RTmax = ceil_div(most, L.Rt);
-  L.workers = f32 ? kSMs * kSimtCtas * kSimtWarps : decode_mma_workers(a.d);
+  L.workers = f32 ? kSMs * kSimtCtas * kSimtWarps : kSMs * decode_mma_warps(a.d);
   const size_t slots = (size_t)L.workers + (size_t)a.B * a.Hkv * L.RTmax;
-  L.cum = kErrWordBytes;
-  L.ml = align_up(L.cum + sizeof(long long) * ((size_t)a.B + 1), 256);
+  L.cum = kCacheHeaderBytes;
+  L.ml = align_up(L.cum + sizeof(int) * ((size_t)a.B + 1), 256);
   L.po = align_up(L.ml + sizeof(float2) * slots * L.Rs, 256);
   L.pml = align_up(L.po + sizeof(float) * slots * L.Rs * a.d, 256);
   L.ppo = L.end = L.pml;
@@ -318,21 +342,17 @@ template <int D>
 cudaError_t launch_simt(const DecodeParams& p, cudaStream_t s) {
   TraceScope trace("decode", s);
   decode_simt_kernel<D>
-      <<<kSMs * kSimtCtas, 32 * kSimtWarps, sizeof(long long) * (p.a.B + 1), s>>>(p);
+      <<<kSMs * kSimtCtas, 32 * kSimtWarps, sizeof(int) * (p.a.B + 1), s>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t launch_merge(const DecodeParams& p, cudaStream_t s) {
-  const long long blocks = ((long long)p.a.rows * p.a.H + kMergeWarps - 1) / kMergeWarps;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  TraceScope trace("decode_merge", s);
-  const cudaError_t e = launch_dependent(decode_merge_kernel<T, D>, dim3(static_cast<unsigned>(blocks)),
-                                         dim3(32 * kMergeWarps), 0, s, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 }  // namespace
+
+bool decode_fits(const PagedArgs& a, bool f32) {
+  const DecodeLayout L = decode_layout(a, f32);
+  return most_units(a, L.Rt, L.Gp) < 0x7fffffffLL - L.workers &&
+         (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.key_tiles < 0x7fffffffLL - L.pre.workers);
+}
 
 size_t decode_workspace_bytes(const PagedArgs& a, bool f32) { return decode_layout(a, f32).end; }
 
@@ -352,18 +372,21 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.RTmax = L.RTmax;
   p.Gp = L.Gp;
   p.workers = L.workers;
-  p.cum = reinterpret_cast<long long*>(ws + L.cum);
+  p.warps = f32 ? kSimtWarps : decode_mma_warps(x.a.d);
+  p.cum = reinterpret_cast<int*>(ws + L.cum);
+  p.count = reinterpret_cast<uint32_t*>(ws + kErrWordBytes);
   p.ml = reinterpret_cast<float2*>(ws + L.ml);
   p.po = reinterpret_cast<float*>(ws + L.po);
   p.pre = L.pre;
   p.pre.ml = reinterpret_cast<float2*>(ws + L.pml);
   p.pre.po = reinterpret_cast<float*>(ws + L.ppo);
-  cudaError_t e = p.pre.key_tiles > 0 ? launch_prefix(p, s) : cudaSuccess;
+  static_assert(kErrWordBytes + 4 * kSMs * kSimtCtas * kSimtWarps <= kCacheHeaderBytes, "counters of all workers");
+  const cudaError_t e = p.pre.key_tiles > 0 ? launch_prefix(p, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  e = !f32 ? launch_decode_mma(p, s) : x.a.d == 64 ? launch_simt<64>(p, s) : launch_simt<128>(p, s);
-  if (e != cudaSuccess) return e;
-  if (f32) return x.a.d == 64 ? launch_merge<float, 64>(p, s) : launch_merge<float, 128>(p, s);
-  return x.a.d == 64 ? launch_merge<__nv_bfloat16, 64>(p, s) : launch_merge<__nv_bfloat16, 128>(p, s);
+  if (f32) return x.a.d == 64 ? launch_simt<64>(p, s) : launch_simt<128>(p, s);
+  const cudaError_t f = launch_decode_mma(p, s);
+  if (f != cudaSuccess || p.pre.key_tiles == 0) return f;
+  return x.a.d == 64 ? launch_merge<64>(p, s) : launch_merge<128>(p, s);
 }
 
 }  // namespace fox

@@ -78,60 +78,25 @@ struct MmaShape {
   int gsub, gstage;           // bytes of a sub-page's sums (a TMA destination: 128-byte steps); of a stage's gates
 };
 
-// A place on the work line: unit `tile` of item (hkv, b, rt).
-struct Cursor {
-  int hkv, b, rt, tile;       // tile of `tiles`
-  int tiles, rts, row0, n, own;
+// Up to 32 successive key tiles of one item, and the page that lane i's tile lies in (with pages of 16
+// tokens, its two pages; -1: the second starts behind the sequence's end).
+struct Window {
+  int hkv, b, rt, tile, n;
+  int id0, id1;
 };
-
-__device__ __forceinline__ void load_seq(const DecodeParams& p, Cursor& c) {
-  bool bad;
-  const SeqInfo s = seq_info(p.a, c.b, &bad);
-  c.row0 = s.row0;
-  c.n = s.n;
-  c.own = s.own;
-  c.tiles = s.own > 0 ? ceil_div(s.own, kKeyTile) : 0;
-  c.rts = ceil_div(s.n * p.Gp, p.Rt);
-}
-
-// The unit after this one; only called while one follows on the line.
-__device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
-  if (++c.tile < c.tiles) return;
-  c.tile = 0;
-  if (++c.rt < c.rts) return;
-  c.rt = 0;
-  do {
-    if (++c.b == p.a.B) {
-      c.b = 0;
-      ++c.hkv;
-    }
-    load_seq(p, c);
-  } while (c.tiles == 0 || c.rts == 0);
-}
-
-// Pages of a tile: one, or two where a page holds 16 tokens (-1: none; the second starts behind the
-// sequence's end). A table entry that is no page is reported and read as page 0.
-struct Pages {
-  int id[2];
-};
-__device__ __forceinline__ Pages tile_pages(const PagedArgs& a, const Cursor& c) {
-  Pages g;
-  const int j = c.tile * kKeyTile;
-  g.id[0] = own_page(a, c.b, j);
-  g.id[1] = a.page_size == 16 && j + 16 < c.own ? own_page(a, c.b, j + 16) : -2;
-  return g;
-}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                      const __grid_constant__ CUtensorMap tmap_g, const DecodeParams p, const MmaShape x) {
+                      const __grid_constant__ CUtensorMap tmap_g, const __grid_constant__ DecodeParams p,
+                      const MmaShape x) {
   using L = MmaLayout<D, NT>;
   constexpr int W = L::kWarps;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long scratch[W];
+  __shared__ int scratch[W];
   __shared__ __align__(8) uint64_t bars[W][L::kMaxStages];
   __shared__ int abort_word;
+  __shared__ Kept<L::kRows, W> kept;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &abort_word;
   const PagedArgs& a = p.a;
@@ -139,146 +104,166 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   const int stages = x.stages;
   uint8_t* ring = sm + warp * stages * (2 * L::kTileBytes);
   uint8_t* gates = sm + W * stages * (2 * L::kTileBytes) + warp * stages * x.gstage;
-  long long* cum = reinterpret_cast<long long*>(sm + W * stages * (2 * L::kTileBytes + x.gstage));
+  int* cum = reinterpret_cast<int*>(sm + W * stages * (2 * L::kTileBytes + x.gstage));
 
   grid_dep_trigger();
   if (threadIdx.x == 0) abort_word = 0;
   if (lane == 0) {
+    kept.i0[warp] = -1;
     for (int s = 0; s < stages; ++s) mbar_init(&bars[warp][s], 1);
     fence_mbar_init();
-    if (warp == 0) {
-      tma_prefetch_desc(&tmap_k);
-      tma_prefetch_desc(&tmap_v);
-      tma_prefetch_desc(&tmap_g);
-    }
   }
   scan_units(p, cum, scratch);  // ends with a block barrier
-  if (blockIdx.x == 0)
+  const bool shared = p.pre.key_tiles > 0;
+  if (shared && blockIdx.x == 0)
     for (int b = threadIdx.x; b <= a.B; b += blockDim.x) p.cum[b] = cum[b];
 
   const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size;
   const int KS = S < kKeyTile ? S : kKeyTile;      // tokens of a sub-page
   const int heads = x.heads, gpitch = x.gpitch;
   const int base_off = (S == 16 ? 2 : 1) * x.gsub;
-  const long long per_head = cum[a.B], total = per_head * a.Hkv;
-  const long long each = units_per_worker(total, p.workers);
-  const long long w = (long long)blockIdx.x * W + warp;
-  const long long u0 = w * each, u1 = min(total, u0 + each);
-  // With a shared prefix this kernel is launched as a dependent of the prefix's, of which it needs
-  // nothing; the merge, its own dependent, needs both: so this grid does not end before that one.
-  if (u0 >= u1) {
-    if (blockIdx.x == 0) grid_dep_wait();
-    return;
-  }
+  const int total = cum[a.B] * a.Hkv, each = units_per_worker(total, p.workers);
+  const int w = blockIdx.x * W + warp;
+  const int u0 = min(total, w * each), count = min(total, u0 + each) - u0;
 
-  // Consumer and producer cursors start at u0; the producer's runs up to `stages` units ahead.
-  Cursor cur;
-  {
-    cur.hkv = static_cast<int>(u0 / per_head);
-    const long long in_head = u0 - cur.hkv * per_head;
-    cur.b = find_seq(cum, a.B, in_head);
-    load_seq(p, cur);
-    const long long in_seq = in_head - cum[cur.b];
-    cur.rt = static_cast<int>(in_seq / cur.tiles);
-    cur.tile = static_cast<int>(in_seq % cur.tiles);
-  }
-  Cursor pro = cur;
-  const int count = static_cast<int>(u1 - u0);
-  Pages next = tile_pages(a, pro);  // pages of the producer's next tile, read one tile ahead of their use
+  // The consumer's place, and the producer's, which runs ahead by a window or two.
+  Place cur = {}, pro = {};
+  int left = count;  // units that no window holds yet
+  auto load_window = [&]() {
+    Window v = {};
+    if (left == 0) return v;
+    v.hkv = pro.hkv;
+    v.b = pro.b;
+    v.rt = pro.rt;
+    v.tile = pro.tile;
+    v.n = min(min(32, pro.tiles - pro.tile), left);
+    v.id1 = -1;
+    if (lane < v.n) {
+      const int j = (v.tile + lane) * kKeyTile;
+      v.id0 = own_page_or_0(a, v.b, j);
+      if (S == 16 && j + 16 < pro.s.own) v.id1 = own_page_or_0(a, v.b, j + 16);
+    }
+    left -= v.n;
+    advance(p, pro, v.n, left > 0);
+    return v;
+  };
+  Window now = {}, next = {};
+  int at = 0;  // the producer's next tile of `now`
 
-  // Issue the copies of the producer's tile into `stage` and move on.
-  auto issue = [&](int n, int stage) {
+  // Copies of the producer's next tile into `stage`.
+  auto issue = [&](int stage) {
+    const int id0 = __shfl_sync(0xffffffffu, now.id0, at), id1 = __shfl_sync(0xffffffffu, now.id1, at);
     uint8_t* st = ring + stage * (2 * L::kTileBytes);
     uint8_t* sg = gates + stage * x.gstage;
-    Pages g = next;
-    const Cursor c = pro;
-    if (n + 1 < count) {
-      advance(p, pro);
-      next = tile_pages(a, pro);
-    }
-    if (g.id[0] == -1 || g.id[1] == -1) {
-      if (lane == 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
-      if (g.id[0] == -1) g.id[0] = 0;
-      if (g.id[1] == -1) g.id[1] = 0;
-    }
-    const int h0 = c.hkv * G + (G > L::kRows ? c.rt * p.Rt % Gp : 0);
-    const int slot = S == 16 ? 0 : c.tile * kKeyTile % S;
-    const int subs = g.id[1] >= 0 ? 2 : 1;
+    const int h0 = now.hkv * G + (G > L::kRows ? now.rt * p.Rt % Gp : 0);
+    const int slot = S == 16 ? 0 : (now.tile + at) * kKeyTile & (S - 1);
+    const int subs = id1 >= 0 ? 2 : 1;
     if (lane == 0) {
       uint64_t* bar = &bars[warp][stage];
       mbar_arrive_expect_tx(bar, subs * (2 * KS * D * 2 + heads * gpitch * 4));
       for (int i = 0; i < subs; ++i) {
+        const int id = i ? id1 : id0;
 #pragma unroll
         for (int y = 0; y < D / 64; ++y) {
-          tma_load_4d(st + y * (kKeyTile * 128) + i * (16 * 128), &tmap_k, bar, y * 64, slot, c.hkv, g.id[i]);
-          tma_load_4d(st + L::kTileBytes + y * (kKeyTile * 128) + i * (16 * 128), &tmap_v, bar, y * 64, slot, c.hkv,
-                      g.id[i]);
+          tma_load_4d(st + y * (kKeyTile * 128) + i * (16 * 128), &tmap_k, bar, y * 64, slot, now.hkv, id);
+          tma_load_4d(st + L::kTileBytes + y * (kKeyTile * 128) + i * (16 * 128), &tmap_v, bar, y * 64, slot, now.hkv,
+                      id);
         }
-        tma_load_3d(sg + i * x.gsub, &tmap_g, bar, slot - 4, h0, g.id[i]);
+        tma_load_3d(sg + i * x.gsub, &tmap_g, bar, slot - 4, h0, id);
       }
     }
     for (int i = 0; i < subs; ++i)
       if (lane < heads && h0 + lane < a.H)
-        cp_async8(smem_u32(sg + base_off) + (i * heads + lane) * 8, a.gbase + gbase_offset(a, g.id[i], h0 + lane));
+        cp_async8(smem_u32(sg + base_off) + (i * heads + lane) * 8, a.gbase + gbase_offset(a, i ? id1 : id0, h0 + lane));
+    if (++at == now.n) {
+      now = next.n > 0 ? next : load_window();
+      at = 0;
+      next = load_window();
+    }
   };
 
+  const int g8 = lane >> 2, t4 = lane & 3;
+  uint32_t qf[D / 16][NT][2];
+  float acc[D / 16][NT][4];
+  float m[NT][2], l[NT][2];
+  Gate2 ci[NT][2];
+  int pos[NT][2], gidx[NT][2];
+  // An item's rows: Q fragments (row g8 of each eight), and the pages of this thread's columns of S^T,
+  // rows 2 t4 and 2 t4 + 1.
+  int pg[NT][2];
+  auto open_rows = [&]() {
+    const int r0 = cur.rt * p.Rt;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + nt * 8 + 2 * t4 + e, t = r / Gp, g = r - t * Gp;
+        const bool here = t < cur.s.n && g < G;
+        pos[nt][e] = cur.s.own - cur.s.n + t;
+        gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : -1;
+        pg[nt][e] = here ? own_page_or_0(a, cur.b, pos[nt][e]) : 0;
+      }
+      const int r = r0 + nt * 8 + g8, t = r / Gp, g = r - t * Gp;
+      const bool in = t < cur.s.n && g < G;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(cur.s.row0 + (in ? t : 0)) * p.q_stride +
+                                 (size_t)(cur.hkv * G + (in ? g : 0)) * D + 2 * t4;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qf[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+        qf[ks][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+      }
+    }
+  };
+  // Their cumulative gates, and nothing summed yet.
+  auto open_sums = [&]() {
+    const int h0 = cur.hkv * G + (G > L::kRows ? cur.rt * p.Rt % Gp : 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ci[nt][e] = {-INFINITY, 0.f};  // an empty row's scores are -inf
+        if (gidx[nt][e] >= 0)
+          ci[nt][e] = gate_sum(a, pg[nt][e], pos[nt][e] & (S - 1), h0 + gidx[nt][e]);
+        else
+          gidx[nt][e] = 0;
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[dt][nt][e] = 0.f;
+  };
+
+  if (count > 0) {
+    // Loads that need nothing of each other first: the tiles' pages, then the rows'.
+    cur = pro = place_of(p, cum, u0);
+    now = load_window();
+    open_rows();
+  }
   for (int n = 0; n < stages; ++n) {
-    if (n < count) issue(n, n);
+    if (n < count) issue(n);
     cp_async_commit();
   }
+  if (count > 0) {
+    open_sums();
+    if (next.n == 0) next = load_window();
+  }
 
-  const int g8 = lane >> 2, t4 = lane & 3;
   // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
   const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
-
-  uint32_t qf[D / 16][NT][2];
-  float acc[D / 16][NT][4];
-  float m[NT][2], l[NT][2], ci_hi[NT][2], ci_lo[NT][2];
-  int pos[NT][2], gidx[NT][2];
-  bool opened = false, ok = true;
+  bool fresh = false, ok = true;
   int stage = 0;
   uint32_t phase = 0;
 
   for (int n = 0; n < count; ++n) {
-    if (!opened) {
-      // The item's rows: Q fragments, places and cumulative gates of this thread's rows 2 t4, 2 t4 + 1.
-      opened = true;
-      const int r0 = cur.rt * p.Rt;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + nt * 8 + g8, t = r / Gp, g = r % Gp;
-        const bool in = t < cur.n && g < G;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                   (size_t)(cur.row0 + (in ? t : 0)) * p.q_stride + (size_t)(cur.hkv * G + (in ? g : 0)) * D;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          qf[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4) : 0u;
-          qf[ks][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4 + 8) : 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rr = r0 + nt * 8 + 2 * t4 + e, tt = rr / Gp, gg = rr % Gp;
-          const bool here = tt < cur.n && gg < G;
-          m[nt][e] = -INFINITY;
-          l[nt][e] = 0.f;
-          gidx[nt][e] = here ? (G > L::kRows ? gg - r0 % Gp : gg) : 0;
-          pos[nt][e] = cur.own - cur.n + tt;
-          ci_hi[nt][e] = -INFINITY;  // an empty row's scores are -inf
-          ci_lo[nt][e] = 0.f;
-          if (here) {
-            const double c = gate_at(a, cur.b, pos[nt][e], cur.hkv * G + gg);
-            ci_hi[nt][e] = static_cast<float>(c);
-            ci_lo[nt][e] = static_cast<float>(c - static_cast<double>(ci_hi[nt][e]));
-          }
-        }
-      }
-#pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[dt][nt][e] = 0.f;
+    if (fresh) {
+      open_rows();
+      open_sums();
+      fresh = false;
     }
     uint8_t* st = ring + stage * (2 * L::kTileBytes);
     ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][stage], phase, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA));
@@ -313,7 +298,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     // Scores of keys mt * 16 + g8 (+ 8) and rows 2 t4 (+ 1), in log2 units.
     const uint8_t* sg = gates + stage * x.gstage;
     const float2* bs = reinterpret_cast<const float2*>(sg + base_off);
-    const bool edge = j0 + kKeyTile > cur.own - cur.n;  // some key is behind some row
+    const bool edge = j0 + kKeyTile > cur.s.own - cur.s.n;  // some key is behind some row
     bool grow = false;
     float top[NT][2];
 #pragma unroll
@@ -325,7 +310,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
         for (int mt = 0; mt < 2; ++mt) {
           const int sub = S == 16 ? mt : 0;
           const float2 base = bs[sub * heads + gidx[nt][e]];
-          const float beta = (ci_hi[nt][e] - base.x) + (ci_lo[nt][e] - base.y);
+          const float beta = (ci[nt][e].hi - base.x) + (ci[nt][e].lo - base.y);
           const float* gr = reinterpret_cast<const float*>(sg + sub * x.gsub) + gidx[nt][e] * gpitch + 4 -
                             p.bias_from_j + (S == 16 ? 0 : mt * 16);
 #pragma unroll
@@ -358,10 +343,10 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
           }
         }
     }
-    if (j0 + kKeyTile > cur.own) {
+    if (j0 + kKeyTile > cur.s.own) {
       // Slots behind the sequence's end may hold anything: V there becomes 0 (its weights are 0).
-      for (int e = lane; e < (j0 + kKeyTile - cur.own) * (D / 8); e += 32) {
-        const int row = cur.own - j0 + e / (D / 8), c = e % (D / 8);
+      for (int e = lane; e < (j0 + kKeyTile - cur.s.own) * (D / 8); e += 32) {
+        const int row = cur.s.own - j0 + e / (D / 8), c = e % (D / 8);
         sts_v4(sv + (c >> 3) * (kKeyTile * 128) + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
       }
       fence_proxy_async_smem();  // before the next copy into this stage
@@ -399,56 +384,67 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
       }
     __syncwarp();  // every lane has read the stage
 
-    const bool last = cur.tile + 1 == cur.tiles || n + 1 == count;
-    if (last) {
-      // Results: O^T through the stage just read to rows, finished or the worker's part of them.
-      float* out = reinterpret_cast<float*>(st);
-      const long long i0 = cur.hkv * per_head + cum[cur.b] + (long long)cur.rt * cur.tiles, i1 = i0 + cur.tiles - 1;
-      const bool whole = p.pre.key_tiles == 0 && i0 / each == i1 / each;
-      const size_t slot = (size_t)(w + ((long long)cur.hkv * a.B + cur.b) * p.RTmax + cur.rt) * p.Rs;
-      const int r0 = cur.rt * p.Rt;
+    if (cur.tile + 1 == cur.tiles || n + 1 == count) {
+      // Results: O^T through shared memory to rows, finished or the worker's part of them: by the stage just
+      // read, or, for the block to join with its neighbours', kept at the ring's start (all copies were read).
+      const int i0 = cur.hkv * cum[a.B] + cum[cur.b] + cur.rt * cur.tiles;
+      const bool alone = i0 / each == (i0 + cur.tiles - 1) / each, whole = alone && !shared;
+      const bool keep = !alone && n + 1 == count;
+      float* out = reinterpret_cast<float*>(keep ? ring : st);
+      const size_t slot = slot_of(p, w, cur.hkv, cur.b, cur.rt);
+      const int r0 = cur.rt * p.Rt, R = min(L::kRows, cur.s.n * Gp - r0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = l[nt][e];
+          float y = l[nt][e];
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          const float f = whole ? (x > 0.f ? 1.f / x : 0.f) : 1.f;
+          for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+          const float f = whole ? (y > 0.f ? 1.f / y : 0.f) : 1.f;
           const int rl = nt * 8 + 2 * t4 + e;
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
             out[rl * L::kOutStride + dt * 16 + g8] = acc[dt][nt][e] * f;
             out[rl * L::kOutStride + dt * 16 + g8 + 8] = acc[dt][nt][e + 2] * f;
           }
-          const int r = r0 + rl, t = r / Gp, g = r % Gp;
-          if (g8 == 0 && t < cur.n && g < G) {
-            if (whole)
-              p.lse[(size_t)(cur.row0 + t) * a.H + cur.hkv * G + g] = x > 0.f ? (m[nt][e] + log2f(x)) * kLn2 : -INFINITY;
-            else
-              p.ml[slot + rl] = make_float2(m[nt][e], x);
+          if (g8 == 0 && rl < R) {
+            const int r = r0 + rl, t = r / Gp, g = r - t * Gp;
+            if (keep) {
+              kept.m[warp][rl] = m[nt][e];
+              kept.l[warp][rl] = y;
+            } else if (!whole) {
+              p.ml[slot + rl] = make_float2(m[nt][e], y);
+            } else if (g < G)
+              p.lse[(size_t)(cur.s.row0 + t) * a.H + cur.hkv * G + g] =
+                  y > 0.f ? (m[nt][e] + log2f(y)) * kLn2 : -INFINITY;
           }
         }
       __syncwarp();
       constexpr int E = D / 32;
-      for (int rl = 0; rl < L::kRows; ++rl) {
-        const int r = r0 + rl, t = r / Gp, g = r % Gp;
-        if (t >= cur.n || g >= G) continue;
+      if (keep && lane == 0) {
+        kept.i0[warp] = i0;
+        kept.at[warp] = cur;
+      }
+#pragma unroll 1
+      for (int rl = 0; rl < R && !keep; ++rl) {
         float f[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) f[e] = out[rl * L::kOutStride + lane * E + e];
-        if (whole)
-          put_out<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(cur.row0 + t) * a.H + cur.hkv * G + g) * D + lane * E,
-                                 f, E);
-        else
+        if (whole) {
+          const int r = r0 + rl, t = r / Gp, g = r - t * Gp;
+          if (g < G)
+            put_out<__nv_bfloat16>(
+                static_cast<__nv_bfloat16*>(p.o) + ((size_t)(cur.s.row0 + t) * a.H + cur.hkv * G + g) * D + lane * E, f, E);
+        } else {
           put_out<float>(p.po + (slot + rl) * D + lane * E, f, E);
+        }
       }
       fence_proxy_async_smem();  // before the next copy into this stage
       __syncwarp();
-      opened = false;
+      fresh = true;
     }
-    if (n + 1 < count) advance(p, cur);
-    if (n + stages < count) issue(n + stages, stage);
+    advance(p, cur, 1, n + 1 < count);
+    if (n + stages < count) issue(stage);
     cp_async_commit();
     if (++stage == stages) {
       stage = 0;
@@ -456,11 +452,19 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     }
   }
   if (!ok) {
-    // A wait gave up: every copy issued must still land before shared memory is released.
+    // A wait gave up: every copy issued must still land before shared memory is used or released.
     for (int s = 0; s < stages; ++s) mbar_wait_drain(&bars[warp][s], s < stage ? phase ^ 1 : phase);
     cp_async_wait<0>();
   }
-  if (blockIdx.x == 0) grid_dep_wait();
+  clear_idle_rows<__nv_bfloat16, D>(p);
+  float* wgt = reinterpret_cast<float*>(sm + 2 * L::kTileBytes);  // the first warp's second stage
+  static_assert(L::kRows * kJoinMost * 4 + 32 * W * 16 <= 2 * L::kTileBytes, "weights and sums fit there");
+  join_items<__nv_bfloat16, D, L::kRows, W>(p, cum, total, each, kept, reinterpret_cast<const float*>(sm),
+                                            stages * (2 * L::kTileBytes) / 4, L::kOutStride, wgt,
+                                            reinterpret_cast<float4*>(wgt + L::kRows * kJoinMost));
+  // With a shared prefix a merge follows, launched as a dependent of this kernel as this one is of the
+  // prefix's; it needs both grids to be through, so this one ends after that one.
+  if (shared) grid_dep_wait();
 }
 
 template <int D, int NT>
@@ -474,13 +478,13 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
   x.gsub = (x.heads * x.gpitch * 4 + 127) / 128 * 128;
   x.gstage = subs * x.gsub + (subs * x.heads * 8 + 127) / 128 * 128;
   constexpr int kMostGates = 2 * ((L::kRows * 20 * 4 + 127) / 128 * 128) + 256;
-  constexpr size_t kMost = 232448 - 1024;  // of an SM's shared memory, less the static part
-  const size_t fixed = 1024 + sizeof(long long) * ((size_t)p.a.B + 1);
+  constexpr size_t kMost = 232448 - 3072;  // of an SM's shared memory, less the static part
+  const size_t fixed = 1024 + sizeof(int) * ((size_t)p.a.B + 1);
   const size_t one = (size_t)L::kWarps * (2 * L::kTileBytes + x.gstage);
   // Three stages where they fit beside the gates and the sequences' offsets.
   x.stages = fixed + 3 * one <= kMost ? 3 : 2;
   const size_t smem = fixed + x.stages * one;
-  static_assert(1024 + 8 * (kMaxSeqs + 1) + 2 * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
+  static_assert(1024 + 4 * (kMaxSeqs + 1) + 2 * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -496,7 +500,7 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
 
 }  // namespace
 
-int decode_mma_workers(int d) { return kSMs * (d == 128 ? MmaLayout<128, 1>::kWarps : MmaLayout<64, 1>::kWarps); }
+int decode_mma_warps(int d) { return d == 128 ? MmaLayout<128, 1>::kWarps : MmaLayout<64, 1>::kWarps; }
 int decode_mma_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
 cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t s) {

@@ -245,6 +245,7 @@ size_t window_workspace_bytes(int B, int N, int H);
 
 // Paged cache: new tokens into the cache (k, v rotated and gates), and attention over it.
 // Strides are elements from one token's row to the next.
+constexpr size_t kCacheHeaderBytes = 16384;  // error word, then a counter a decode worker: all zero between calls
 struct CacheAppendArgs {
   PagedArgs a;
   const void* k;
@@ -267,6 +268,7 @@ struct DecodeArgs {
   void* o;
   float* lse;
 };
+bool decode_fits(const PagedArgs& a, bool f32);  // its work is counted in ints
 size_t decode_workspace_bytes(const PagedArgs& a, bool f32);
 cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t s);
 

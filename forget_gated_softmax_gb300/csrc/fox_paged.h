@@ -16,7 +16,7 @@ namespace fox {
 constexpr int kMaxSeqs = 4096;  // sequences of one call: every CTA holds their work offsets in shared memory
 
 struct PagedArgs {
-  int num_pages, page_size, H, Hkv, d;
+  int num_pages, page_size, page_shift, H, Hkv, d;  // page_size = 1 << page_shift
   int B, rows, max_new;  // max_new: at least every sequence's count of new tokens
   int table_stride, prefix_len;
   const int32_t* cu;      // [B + 1] first row of each sequence, or null: rows / B rows each
@@ -84,11 +84,11 @@ FOX_HD int seq_of_row(const PagedArgs& a, int i) {
 // The page of own token p of sequence b (0 <= p < table_stride * page_size), or -1 where the
 // table's entry is no page of the pool.
 FOX_HD int own_page(const PagedArgs& a, int b, int p) {
-  const int id = a.table[(size_t)b * a.table_stride + p / a.page_size];
+  const int id = a.table[(size_t)b * a.table_stride + (p >> a.page_shift)];
   return id >= 0 && id < a.num_pages ? id : -1;
 }
 FOX_HD int prefix_page(const PagedArgs& a, int p) {
-  const int id = a.prefix[p / a.page_size];
+  const int id = a.prefix[p >> a.page_shift];
   return id >= 0 && id < a.num_pages ? id : -1;
 }
 
@@ -108,8 +108,8 @@ FOX_HD size_t gbase_offset(const PagedArgs& a, int page, int h) { return ((size_
 // end of one token's group and the start of the next's (rows with r % Gp >= G are empty). An item's
 // units are the key tiles of kKeyTile tokens. The units of all items lie on one line, items in the order (key head, sequence,
 // row tile), and worker w takes units [w q, (w + 1) q): equal work whatever the lengths are.
-// An item that lies in one worker's range is finished there; the others leave one partial result a
-// worker, in slot worker + item: along the line each new (worker, item) pair raises one of the
+// An item that lies in one worker's range is finished there; of the others a worker can leave a partial
+// result, in slot worker + item: along the line each new (worker, item) pair raises one of the
 // two, so no two pairs meet, and there are fewer than workers + items slots.
 constexpr int kKeyTile = 32;
 
@@ -120,11 +120,18 @@ FOX_HD int walk_keys(const PagedArgs& a, const SeqInfo& s, bool walk_prefix) {
   return s.own < 0 ? 0 : s.own + (walk_prefix ? a.prefix_len : 0);
 }
 FOX_HD int padded_group(int G, int Rt) { return G <= Rt ? G : ceil_div(G, Rt) * Rt; }
-FOX_HD long long seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, int Gp, bool walk_prefix) {
-  return (long long)ceil_div(walk_keys(a, s, walk_prefix), kKeyTile) * ceil_div(s.n * Gp, Rt);
+FOX_HD int seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, int Gp, bool walk_prefix) {
+  return ceil_div(walk_keys(a, s, walk_prefix), kKeyTile) * ceil_div(s.n * Gp, Rt);
 }
-FOX_HD long long units_per_worker(long long total, int workers) {
-  const long long q = (total + workers - 1) / workers;
+// The most units that the batch's tables and row counts allow: has to stay below 2^31 - workers, so
+// that places on the line are ints.
+FOX_HD long long most_units(const PagedArgs& a, int Rt, int Gp) {
+  const long long cap = (long long)a.prefix_len + (long long)a.table_stride * a.page_size;
+  const long long rows = (long long)a.max_new * Gp;
+  return (cap / kKeyTile + 1) * ((rows + Rt - 1) / Rt) * a.B * a.Hkv;
+}
+FOX_HD int units_per_worker(int total, int workers) {
+  const int q = (total + workers - 1) / workers;
   return q > 0 ? q : 1;
 }
 

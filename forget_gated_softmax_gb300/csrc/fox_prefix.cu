@@ -136,7 +136,7 @@ __device__ __forceinline__ float row_exp(uint32_t tS, const float* kap, float sc
 template <int D>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                  const __grid_constant__ CUtensorMap tmap_v, const DecodeParams p) {
+                  const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ DecodeParams p) {
   using L = PrefixLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[P_COUNT];
@@ -169,10 +169,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   tc_fence_after();
   const uint32_t tbase = tmem_word;
 
-  const long long total = (long long)a.Hkv * pp.items * pp.key_tiles;
-  const long long each = units_per_worker(total, pp.workers);
-  const long long u_end = min(total, (blockIdx.x + 1) * each);
-  long long u = blockIdx.x * each;
+  const int total = a.Hkv * pp.items * pp.key_tiles, each = units_per_worker(total, pp.workers);
+  const int u_end = min(total, static_cast<int>(blockIdx.x + 1) * each);
+  int u = blockIdx.x * each;
 
   bool ok = true;              // of this thread's role
   int c0 = 0;                  // key tiles before this segment (ring position)
@@ -181,10 +180,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   int seg = 0;
   while (u < u_end) {
     // A segment: key tiles t1 - 1 down to t0 of item (hkv, it).
-    const int item = static_cast<int>(u / pp.key_tiles);
-    const int hkv = item / pp.items, it = item % pp.items;
-    const int t0 = static_cast<int>(u % pp.key_tiles);
-    const int t1 = static_cast<int>(min(static_cast<long long>(pp.key_tiles), t0 + (u_end - u)));
+    const int item = u / pp.key_tiles, hkv = item / pp.items, it = item % pp.items;
+    const int t0 = u % pp.key_tiles, t1 = min(pp.key_tiles, t0 + (u_end - u));
     const int nT = t1 - t0;
     const int T0 = split_keys ? 0 : 2 * it;  // row tile of stream 0; stream 1 has the next, or the same
     const bool has1 = split_keys ? nT > 1 : T0 + 1 < pp.row_tiles;

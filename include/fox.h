@@ -288,12 +288,15 @@ typedef struct fox_batch {
 
 /*
  * Workspace of fox_cache_append and fox_decode for these arguments (0 if they are invalid): the
- * error word, and for fox_decode the partial results of keys split among the SMs. It depends on
- * sizes only, never on the contents of lens. The first 4 bytes, the error word, must be zero before
- * the first call; these calls only ever add bits to it (fox_check_error reads and clears it):
- * a length, row range, page id or position outside what the arguments allow sets one, and nothing
- * is read or written for it (the sequence, or the token, is skipped; its outputs are not meaningful).
+ * error word, and for fox_decode counters and the partial results of keys split among the SMs. It
+ * depends on sizes only, never on the contents of lens. Its first FOX_CACHE_ZERO_BYTES must be zero
+ * before its first call with these two functions (any other use in between, a call of fox_fwd for
+ * instance, makes it a new one); they leave the counters zero, and only ever add bits to the error word, the
+ * first 4 bytes, which fox_check_error reads and clears: a length, row range, page id or position
+ * outside what the arguments allow sets one. The sequence, or the token, is then skipped, or an
+ * unknown page read as page 0; its outputs are not meaningful, and no other sequence is touched.
  */
+#define FOX_CACHE_ZERO_BYTES 16384
 size_t fox_cache_workspace_bytes(const fox_cache* c, const fox_batch* s, int rows);
 
 /* Rotation of the first `dim` channels of k (and q) by the angles of the token's position in its sequence. */
@@ -326,7 +329,8 @@ fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, co
  * q: rows of [H, d], q_stride elements apart (multiples of 16 bytes; 16-byte aligned).
  * o: [rows, H, d] of the cache's type, lse: [rows, H] fp32, natural log. Rows of idle sequences get
  * O = 0 and LSE = -inf. scale 0 selects d^-1/2.
- * A K or V slot behind the sequence's end is never used, whatever it holds.
+ * A K or V slot behind the sequence's end is never used, whatever it holds. The same arguments and
+ * contents give the same bits; how a row's sums are ordered follows from the lengths of the whole batch.
  */
 fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
                       int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -83,6 +83,14 @@ def test_bad_rows_scales_and_workspaces_are_refused(L):
     assert L.fox_cache_append(ctypes.byref(_cache()), None, 1, FAKE, 8, FAKE, 8, FAKE, 8, None, FAKE, 256, None) == 1
 
 
+def test_more_work_than_ints_count_is_refused(L):
+    big = _batch(B=4096, table_stride=1 << 20)  # 67 million tokens a sequence
+    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(big), 4096) == 0
+    assert _decode(L, s=big, rows=4096) == 2
+    fits = _batch(B=4096, table_stride=1 << 11)
+    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(fits), 4096) > 0
+
+
 def test_bad_rotations_are_refused(L):
     def rot(**kw):
         f = dict(cos=FAKE, sin=FAKE, max_pos=100, dim=64, pairs=0, q=None, q_stride=0, q_out=None)
@@ -100,7 +108,7 @@ def test_nothing_to_do_is_ok(L):
     assert _decode(L, rows=0, q=None, ws=None, nbytes=0) == 0
     assert _append(L, s=_batch(B=0), rows=0, k=None, ws=None, nbytes=0) == 0
     assert L.fox_cache_workspace_bytes(ctypes.byref(_cache(d=96)), ctypes.byref(_batch()), 2) == 0
-    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(_batch(B=0)), 0) == 256
+    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(_batch(B=0)), 0) == fox.FOX_CACHE_ZERO_BYTES
 
 
 def test_binding_refuses_what_is_not_on_the_gpu():
@@ -134,7 +142,7 @@ using namespace fox;
 static PagedArgs args(const int* n, const int* cu, const int* lens, const int* table, const int* prefix) {
   PagedArgs a = {};
   a.num_pages = n[0]; a.page_size = n[1]; a.H = n[2]; a.Hkv = n[3]; a.d = n[4]; a.B = n[5]; a.rows = n[6];
-  a.max_new = n[7]; a.table_stride = n[8]; a.prefix_len = n[9];
+  a.max_new = n[7]; a.page_shift = __builtin_ctz(n[1]); a.table_stride = n[8]; a.prefix_len = n[9];
   a.cu = cu; a.lens = lens; a.table = table; a.prefix = prefix;
   return a;
 }
@@ -149,12 +157,12 @@ int t_own_page(const int* n, const int* table, int b, int p) { return own_page(a
 int t_prefix_page(const int* n, const int* prefix, int p) { return prefix_page(args(n, nullptr, nullptr, nullptr, prefix), p); }
 long long t_kv(const int* n, int page, int h, int s) { return (long long)kv_offset(args(n, nullptr, nullptr, nullptr, nullptr), page, h, s); }
 long long t_g(const int* n, int page, int h, int s) { return (long long)g_offset(args(n, nullptr, nullptr, nullptr, nullptr), page, h, s); }
-long long t_units(const int* n, const int* cu, const int* lens, int b, int Rt, int walk) {
+int t_units(const int* n, const int* cu, const int* lens, int b, int Rt, int walk) {
   const PagedArgs a = args(n, cu, lens, nullptr, nullptr);
   bool bad;
   return seq_units(a, seq_info(a, b, &bad), Rt, padded_group(a.H / a.Hkv, Rt), walk);
 }
-long long t_each(long long total, int workers) { return units_per_worker(total, workers); }
+int t_each(int total, int workers) { return units_per_worker(total, workers); }
 }
 """
 
@@ -166,9 +174,8 @@ def H(tmp_path_factory):
     src.write_text(HARNESS)
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", fbuild.CSRC, str(src), "-o", str(so)], check=True)
     lib = ctypes.CDLL(str(so))
-    for f in ("t_kv", "t_g", "t_units", "t_each"):
+    for f in ("t_kv", "t_g"):
         getattr(lib, f).restype = ctypes.c_longlong
-    lib.t_each.argtypes = [ctypes.c_longlong, ctypes.c_int]
     return lib
 
 

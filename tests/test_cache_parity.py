@@ -205,7 +205,7 @@ def test_decode(fox, n, dtype):
     c.put()
     cache, batch = c.cache(fox), c.batch(fox)
     ws = fox.cache_workspace(cache, batch, c.rows)
-    ws[256:] = 0xFF  # nothing is read that the call has not written
+    ws[fox.FOX_CACHE_ZERO_BYTES :] = 0xFF  # nothing is read that the call has not written
     o, lse = torch.full_like(c.q, float("nan")), torch.full((c.rows, H), float("nan"), device="cuda")
     fox.fox_decode(cache, batch, c.q, scale=scale or 0.0, bias_from_j=bj, o=o, lse=lse, ws=ws)
     assert fox.fox_check_error(ws) == 0
@@ -281,6 +281,7 @@ def test_what_the_batch_cannot_hold_is_reported_and_skipped(fox, dtype, prefix):
     k, v, z = good.new_rows()
     fox.fox_cache_append(good.cache(fox), good.batch(fox), k, v, z)
     o0, l0 = fox.fox_decode(good.cache(fox), good.batch(fox), good.q)
+    ro, rl = good.attend()
     for what in ("page", "negative page", "too long", "negative length", "in the prefix", "falling rows"):
         c = fresh()
         if what == "page":
@@ -303,7 +304,15 @@ def test_what_the_batch_cannot_hold_is_reported_and_skipped(fox, dtype, prefix):
         assert fox.fox_check_error(ws) == FOX_ERR_DEVICE, what
         assert fox.fox_check_error(ws) == 0
         rows = [0, 1] if what == "falling rows" else [0, 1, 4, 5]
-        assert torch.equal(bits(o[rows]), bits(o0[rows])) and torch.equal(bits(lse[rows]), bits(l0[rows])), what
+        if "page" in what:
+            assert torch.equal(bits(o[rows]), bits(o0[rows])) and torch.equal(bits(lse[rows]), bits(l0[rows])), what
+        else:
+            # A skipped sequence has no work, so the others' keys are split among the workers elsewhere and
+            # their fp32 sums of at most 200 terms round elsewhere (each side within 200 * 2^-24 of the exact
+            # sum, and LSE by as much): not the same bits, but within the bounds of the exact values.
+            assert_o(tensor_f64(o[rows]), tensor_f64(ro[rows]), dtype, f"decode beside {what} {dtype}")
+            assert (lse[rows].double() - rl[rows]).abs().max() <= (
+                foxtest.TOL_LSE_BF16 if dtype == "bf16" else foxtest.TOL_LSE_F32), what
         ids = torch.cat([good.table[0, :3], good.table[2, :3]]) if what != "falling rows" else good.table[0, :3]
         for a, b in ((c.k, good.k), (c.v, good.v), (c.g, good.g), (c.gbase, good.gbase)):
             assert torch.equal(bits(a[ids.long()]), bits(b[ids.long()])), what
