@@ -627,12 +627,10 @@ def _row_stride(where: str, name: str, t, cache: Cache, heads: int, rows: int) -
     return s0
 
 
-def _own_tensors(stream, *makers):
-    """What this call allocates itself, in the allocator's order of the stream that uses it."""
-    if stream is None:
-        return [m() for m in makers]
+def _alloc_on(stream, make):
+    """A tensor that the call allocates itself, made in the allocator's order of the stream that uses it."""
     with _torch().cuda.stream(stream):
-        return [m() for m in makers]
+        return make()
 
 
 def _launch_stream(stream, index: int) -> int:
@@ -675,7 +673,8 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
         if q is not None:
             qs = _row_stride(where, "q", q, cache, cache.H, rows)
             if q_out is None:
-                (q_out,) = _own_tensors(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else _alloc_on(
+                    stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
             else:
                 _row_stride(where, "q_out", q_out, cache, cache.H, rows)
                 if not q_out.is_contiguous():
@@ -686,7 +685,7 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
         rot = ctypes.byref(fox_rotary(cos.data_ptr(), sin.data_ptr(), positions, 2 * half, int(bool(pairs)),
                                       _ptr(q), qs, _ptr(q_out)))
     if ws is None:
-        (ws,) = _own_tensors(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
+        ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
     st = lib().fox_cache_append(
         cache.ref, batch.ref, rows, k.data_ptr(), ks, v.data_ptr(), vs, z.data_ptr(), zs, rot, ws.data_ptr(), ws.numel(),
         _launch_stream(stream, index),
@@ -707,17 +706,20 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
     rows = q.shape[0]
     qs = _row_stride(where, "q", q, cache, cache.H, rows)
     if o is None:
-        (o,) = _own_tensors(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+        fmt = torch.contiguous_format
+        o = torch.empty_like(q, memory_format=fmt) if stream is None else _alloc_on(
+            stream, lambda: torch.empty_like(q, memory_format=fmt))
     else:
         _row_stride(where, "o", o, cache, cache.H, rows)
         if not o.is_contiguous():
             raise ValueError(f"{where}: o must be contiguous")
     if lse is None:
-        (lse,) = _own_tensors(stream, lambda: torch.empty((rows, cache.H), dtype=torch.float32, device=q.device))
+        lse = torch.empty((rows, cache.H), dtype=torch.float32, device=cache.device) if stream is None else _alloc_on(
+            stream, lambda: torch.empty((rows, cache.H), dtype=torch.float32, device=cache.device))
     elif lse.shape != (rows, cache.H) or lse.dtype != torch.float32 or lse.device != cache.device or not lse.is_contiguous():
         raise ValueError(f"{where}: lse must be contiguous [{rows}, {cache.H}] float32 on the cache's device")
     if ws is None:
-        (ws,) = _own_tensors(stream, lambda: cache_workspace(cache, batch, rows))
+        ws = _alloc_on(stream, lambda: cache_workspace(cache, batch, rows))
     st = lib().fox_decode(
         cache.ref, batch.ref, rows, q.data_ptr(), qs, scale, 1 if bias_from_j else 0, o.data_ptr(), lse.data_ptr(),
         ws.data_ptr(), ws.numel(), _launch_stream(stream, index),

@@ -30,34 +30,36 @@ __device__ __forceinline__ void load4(const float* p, float* f) {
 template <int D>
 __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int E = D / 32;
-  extern __shared__ int cum[];  // [B + 1]
+  extern __shared__ Seq seqs[];  // [B + 1]
   __shared__ int scratch[kSimtWarps];
   __shared__ __align__(16) float qs[kSimtWarps][kSimtRows][D];  // scaled queries; at the end the kept rows
   __shared__ Gate2 ci[kSimtWarps][kSimtRows];
-  __shared__ float wgt[kJoinMost * kSimtRows];
-  __shared__ float4 part[32 * kSimtWarps];
+  __shared__ int offs[kSMs * kSimtCtas + 1];
+  __shared__ Column part[32 * kSimtWarps];
   __shared__ Kept<kSimtRows, kSimtWarps> kept;
   const PagedArgs& a = p.a;
-  scan_units(p, cum, scratch);
+  scan_sequences(p, seqs, scratch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size, P = a.prefix_len;
-  const int total = cum[a.B] * a.Hkv, each = units_per_worker(total, p.workers);
+  const int total = seqs[a.B].u0 * a.Hkv, each = units_per_worker(total, p.workers);
   const int w = blockIdx.x * kSimtWarps + warp;
   const int u0 = min(total, w * each);
-  int left = min(total, u0 + each) - u0;
+  const int u1 = min(total, u0 + each);
+  int left = u1 - u0;
   Place at;
-  if (left > 0) at = place_of(p, cum, u0);
+  if (left > 0) at = place_of(p, seqs, u0);
   if (lane == 0) kept.i0[warp] = -1;
   while (left > 0) {
     // A segment: key tiles tile0 .. tile1 - 1 of one item.
-    const SeqInfo s = at.s;
+    const Seq s = at.s;
     const int b = at.b, hkv = at.hkv, rt = at.rt;
-    const int keys = walk_keys(a, s, true), tile0 = at.tile, tile1 = min(at.tiles, tile0 + left);
-    const int R = min(p.Rt, s.n * Gp - rt * p.Rt);
+    const int keys = s.own + P, tile0 = at.tile, tile1 = min(at.tiles, tile0 + left);
+    const int R = rows_of(p, at);
 
     __syncwarp();
+#pragma unroll 1
     for (int r = 0; r < R; ++r) {
-      const int rr = rt * p.Rt + r, t = rr / Gp, h = hkv * G + min(rr % Gp, G - 1);
+      const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
       const float* src = static_cast<const float*>(p.q) + (size_t)(s.row0 + t) * p.q_stride + (size_t)h * D;
       for (int c = lane * 4; c < D; c += 128) {
         float f[4];
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
       }
       if (lane == 0) {
         const int i = s.own - s.n + t;
-        ci[warp][r] = gate_sum(a, own_page_or_0(a, b, i), i % S, h);
+        ci[warp][r] = gate_sum(a, own_page_or_0(a, b, i), i & (S - 1), h);
       }
     }
     __syncwarp();
@@ -85,9 +87,9 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
       const bool in = j < keys;
       int page = -1, slot = 0;
       if (in) {
-        const int at = j < P ? j : j - P;
-        page = j < P ? prefix_page(a, j) : own_page(a, b, at);
-        slot = at % S;
+        const int own = j - P;
+        page = j < P ? prefix_page(a, j) : own_page(a, b, own);
+        slot = (j < P ? j : own) & (S - 1);
         if (page < 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
       }
       const size_t kv = page >= 0 ? kv_offset(a, page, hkv, slot) : 0;
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
       for (int r = 0; r < kSimtRows; ++r) {
         float x = -INFINITY;
         if (r < R && page >= 0) {
-          const int rr = rt * p.Rt + r, t = rr / Gp, h = hkv * G + min(rr % Gp, G - 1);
+          const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
           if (j <= P + s.own - s.n + t) {
             const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
             const float beta = (ci[warp][r].hi - base.x) + (ci[warp][r].lo - base.y);
@@ -156,47 +158,34 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
         }
       }
     }
-    // The item's first and last unit say whether this worker has all of it.
-    const int i0 = hkv * cum[a.B] + cum[b] + rt * at.tiles;
-    const bool whole = i0 / each == (i0 + at.tiles - 1) / each;
-    const bool keep = !whole && tile1 - tile0 == left;  // for the block to join with its neighbours'
-    const size_t slot0 = slot_of(p, w, hkv, b, rt);
-    if (keep && lane == 0) {
-      kept.i0[warp] = i0;
-      kept.at[warp] = at;
-    }
+    // Results: rows in shared memory, where the queries were, for the block to join with its neighbours', or
+    // finished, or to the worker's slot.
+    const bool alone = at.i0 >= u0 && at.i0 + at.tiles <= u1, keep = !alone && tile1 - tile0 == left;
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < kSimtRows; ++r) {
-      if (r >= R) continue;
       float sum = l[r];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const int rr = rt * p.Rt + r, t = rr / Gp, h = hkv * G + min(rr % Gp, G - 1);
-      if (rr % Gp >= G) continue;  // an empty row
-      if (whole) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[r][e] *= inv;
-        const size_t row = (size_t)(s.row0 + t) * a.H + h;
-        put_out<float>(static_cast<float*>(p.o) + row * D + lane * E, acc[r], E);
-        if (lane == 0) p.lse[row] = sum > 0.f ? (m[r] + log2f(sum)) * kLn2 : -INFINITY;
-      } else if (keep) {
-        if (lane == 0) {
-          kept.m[warp][r] = m[r];
-          kept.l[warp][r] = sum;
-        }
-        put_out<float>(&qs[warp][r][lane * E], acc[r], E);
-      } else {
-        if (lane == 0) p.ml[slot0 + r] = make_float2(m[r], sum);
-        put_out<float>(p.po + (slot0 + r) * D + lane * E, acc[r], E);
+      if (lane == 0) {
+        kept.m[warp][r] = m[r];
+        kept.l[warp][r] = sum;
       }
+#pragma unroll
+      for (int e = 0; e < E; ++e) qs[warp][r][lane * E + e] = acc[r][e];
     }
+    if (keep && lane == 0) {
+      kept.i0[warp] = at.i0;
+      kept.at[warp] = at;
+    }
+    __syncwarp();
+    if (!keep) leave_rows<float, D>(p, at, w, alone, &qs[warp][0][0], D, kept.m[warp], kept.l[warp]);
     left -= tile1 - tile0;
-    advance(p, at, tile1 - tile0, left > 0);
+    at.tile = tile1;
+    if (tile1 == at.tiles && left > 0) next_item(p, seqs, at);
   }
-  clear_idle_rows<float, D>(p);
-  join_items<float, D, kSimtRows, kSimtWarps>(p, cum, total, each, kept, &qs[0][0][0], kSimtRows * D, D, wgt, part);
+  clear_idle_rows<float, D>(p, seqs);
+  join_items<float, D, kSimtRows, kSimtWarps>(p, seqs, total, each, kept, &qs[0][0][0], kSimtRows * D, D, offs, part);
 }
 
 // One output row by one warp: the partial results of its own item and of the shared prefix joined, in the
@@ -236,23 +225,26 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
   const int per_head = __ldcg(p.cum + a.B), each = units_per_worker(per_head * a.Hkv, p.workers);
   const int i0 = hkv * per_head + __ldcg(p.cum + b) + rt * tiles;
   // The own item's: one a block of workers, and its last worker's own where that is another (join_items).
-  const int i1 = i0 + tiles - 1, w0 = i0 / each, w1 = i1 / each, nb = w1 / p.warps - w0 / p.warps + 1;
-  const bool extra = w1 > w0 && w1 > w1 / p.warps * p.warps && min(per_head * a.Hkv, (w1 + 1) * each) > i1 + 1;
-  const int n_own = nb + extra, n = n_own + n_pre;
-  const size_t own0 = slot_of(p, 0, hkv, b, rt) + r - rt * p.Rt;
-  auto own_at = [&](int i) {
-    const int w = i == 0 ? w0 : i < nb ? (w0 / p.warps + i) * p.warps : w1;
-    return own0 + (size_t)w * p.Rs;
-  };
-  auto ml_of = [&](int i) {
-    if (i < n_own) return __ldcg(p.ml + own_at(i));
-    float2 y = __ldcg(x.ml + pre0 + (size_t)(i - n_own) * step);
-    y.x += shift;
-    return y;
-  };
+  const int i1 = i0 + tiles - 1, w0 = i0 / each, w1 = i1 / each, c0 = w0 / p.warps, c1 = w1 / p.warps, nb = c1 - c0 + 1;
+  const int n_own = nb + (w1 > w0 && w1 > c1 * p.warps && min(per_head * a.Hkv, (w1 + 1) * each) > i1 + 1);
+  const int n = n_own + n_pre, own0 = ((hkv * a.B + b) * p.RTmax + rt) * p.Rs + r - rt * p.Rt;
   float m = -INFINITY, l = 0.f, acc[E] = {};
+#pragma unroll 1
   for (int first = 0; first < n; first += 32) {
-    const float2 ml = first + lane < n ? ml_of(first + lane) : make_float2(-INFINITY, 0.f);
+    // lane i: where result first + i lies, its maximum and sum
+    const int i = first + lane;
+    const float* src = p.po;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (i < n_own) {
+      const int at = own0 + (i == 0 ? w0 : i < nb ? (c0 + i) * p.warps : w1) * p.Rs;
+      ml = __ldcg(p.ml + at);
+      src = p.po + (size_t)at * D;
+    } else if (i < n) {
+      const size_t at = pre0 + (size_t)(i - n_own) * step;
+      ml = __ldcg(x.ml + at);
+      ml.x += shift;
+      src = x.po + at * D;
+    }
     float top = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -263,30 +255,24 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     l = l * alpha + ml.y * wgt;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= alpha;
+    // Of a result without weight (a stream without keys wrote no sums of V) a written one is read instead.
+    const unsigned has = __ballot_sync(0xffffffffu, wgt != 0.f);
+    if (has == 0) continue;
+    unsigned long long addr = reinterpret_cast<unsigned long long>(src);
+    addr = wgt != 0.f ? addr : 0ull;
+    const unsigned long long some = __shfl_sync(0xffffffffu, addr, __ffs(has) - 1);
+    if (addr == 0ull) addr = some;
     const int c = min(32, n - first);
-    constexpr int kBatch = 8;  // loads in flight
-    for (int i = 0; i < c; i += kBatch) {
-      float2 y[kBatch][E / 2];
-      float f[kBatch];
+#pragma unroll 8
+    for (int j = 0; j < c; ++j) {
+      const float f = __shfl_sync(0xffffffffu, wgt, j);
+      const float2* y = reinterpret_cast<const float2*>(__shfl_sync(0xffffffffu, addr, j)) + lane * (E / 2);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        f[j] = __shfl_sync(0xffffffffu, wgt, (i + j) & 31);
-        // A weight of 0 counts for nothing (a stream without keys wrote no sums of V): result 0 is read instead.
-        if (i + j >= c) f[j] = 0.f;
-        const int k = f[j] != 0.f ? first + i + j : 0;
-        const float* src = (k < n_own ? p.po + own_at(k) * D
-                                      : x.po + (pre0 + (size_t)(k - n_own) * step) * D) +
-                           lane * E;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[j][e] = __ldcg(reinterpret_cast<const float2*>(src) + e);
+      for (int e = 0; e < E / 2; ++e) {
+        const float2 z = __ldcg(y + e);
+        acc[2 * e] = fmaf(f, z.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(f, z.y, acc[2 * e + 1]);
       }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          acc[2 * e] = fmaf(f[j], y[j][e].x, acc[2 * e]);
-          acc[2 * e + 1] = fmaf(f[j], y[j][e].y, acc[2 * e + 1]);
-        }
     }
   }
 #pragma unroll
@@ -295,7 +281,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] *= inv;
   const size_t at = (size_t)row * a.H + h;
-  put_out<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p.o) + at * D + lane * E, acc, E);
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + at * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(acc[e], acc[e + 1]);
   if (lane == 0) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
@@ -311,6 +299,7 @@ struct DecodeLayout {
   int Rt, Gp, Rs, RTmax, workers;
   size_t cum, ml, po, pml, ppo, end;
   PrefixPlan pre;
+  long long po_rows;
 };
 
 DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
@@ -324,6 +313,7 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   L.workers = f32 ? kSMs * kSimtCtas * kSimtWarps : kSMs * decode_mma_warps(a.d);
   const size_t slots = (size_t)L.workers + (size_t)a.B * a.Hkv * L.RTmax;
   L.cum = kCacheHeaderBytes;
+  L.po_rows = (long long)slots * L.Rs;
   L.ml = align_up(L.cum + sizeof(int) * ((size_t)a.B + 1), 256);
   L.po = align_up(L.ml + sizeof(float2) * slots * L.Rs, 256);
   L.pml = align_up(L.po + sizeof(float) * slots * L.Rs * a.d, 256);
@@ -340,9 +330,12 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
 
 template <int D>
 cudaError_t launch_simt(const DecodeParams& p, cudaStream_t s) {
+  const size_t smem = sizeof(Seq) * ((size_t)p.a.B + 1);
+  const cudaError_t e =
+      cudaFuncSetAttribute(decode_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
   TraceScope trace("decode", s);
-  decode_simt_kernel<D>
-      <<<kSMs * kSimtCtas, 32 * kSimtWarps, sizeof(int) * (p.a.B + 1), s>>>(p);
+  decode_simt_kernel<D><<<kSMs * kSimtCtas, 32 * kSimtWarps, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -351,6 +344,7 @@ cudaError_t launch_simt(const DecodeParams& p, cudaStream_t s) {
 bool decode_fits(const PagedArgs& a, bool f32) {
   const DecodeLayout L = decode_layout(a, f32);
   return most_units(a, L.Rt, L.Gp) < 0x7fffffffLL - L.workers &&
+         (unsigned long long)a.max_new * L.Gp * L.Gp < (1ull << 32) && L.po_rows < 0x7fffffffLL &&
          (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.key_tiles < 0x7fffffffLL - L.pre.workers);
 }
 
@@ -371,6 +365,7 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.Rs = L.Rs;
   p.RTmax = L.RTmax;
   p.Gp = L.Gp;
+  p.gp_inv = L.Gp > 1 ? static_cast<uint32_t>(((1ull << 32) + L.Gp - 1) / L.Gp) : 0u;
   p.workers = L.workers;
   p.warps = f32 ? kSimtWarps : decode_mma_warps(x.a.d);
   p.cum = reinterpret_cast<int*>(ws + L.cum);

@@ -35,6 +35,7 @@ struct DecodeParams {
   // Own items
   int Rt, Rs, RTmax;   // rows of a row tile; rows kept of a slot; most row tiles of a sequence
   int Gp;              // rows of a token (padded_group)
+  uint32_t gp_inv;     // ceil(2^32 / Gp), for token_of; 0: Gp is 1
   int workers, warps;  // workers, and of one CTA
   int* cum;            // [B + 1] units of one key head before each sequence, for the merge of a shared prefix
   uint32_t* count;     // [CTAs] arrivals at the item that reaches past this CTA's end; 0 between calls
@@ -43,21 +44,32 @@ struct DecodeParams {
   PrefixPlan pre;
 };
 
-// Unit offsets of the sequences into cum[0 .. B] (shared memory), by the whole block.
-// `scratch` holds one value a warp. Ends with a block barrier.
-__device__ __forceinline__ void scan_units(const DecodeParams& p, int* cum, int* scratch) {
+// Row r's token: r / Gp by a multiplication (exact while max_new * Gp^2 < 2^32, which decode_fits checks).
+__device__ __forceinline__ int token_of(const DecodeParams& p, int r) {
+  return p.gp_inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.gp_inv)) : r;
+}
+
+// The sequences as every CTA holds them in shared memory, [B + 1]: units of one key head before the
+// sequence, its rows, its tokens after the prefix (SeqInfo). The kernels run most of their code once a
+// launch, and then wait for instructions as much as for data: what they look up is made compact here once.
+struct Seq {
+  int u0, row0, n, own;
+};
+
+// Fills seqs[0 .. B] by the whole block; `scratch` holds one value a warp. Ends with a block barrier.
+__device__ __forceinline__ void scan_sequences(const DecodeParams& p, Seq* seqs, int* scratch) {
   const PagedArgs& a = p.a;
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = ceil_div(a.B, nt), b0 = tid * each, b1 = min(a.B, b0 + each);
   int mine = 0;
   bool any_bad = false;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     bool bad;
     const SeqInfo s = seq_info(a, b, &bad);
     any_bad |= bad;
-    const int u = seq_units(a, s, p.Rt, p.Gp, p.walk_prefix);
-    cum[b] = u;
-    mine += u;
+    seqs[b] = {mine, s.row0, s.n, s.own};
+    mine += seq_units(a, s, p.Rt, p.Gp, p.walk_prefix);
   }
   if (any_bad && blockIdx.x == 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
   int x = mine;
@@ -69,71 +81,65 @@ __device__ __forceinline__ void scan_units(const DecodeParams& p, int* cum, int*
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
   int before = x - mine;
+#pragma unroll 1
   for (int w = 0; w < warp; ++w) before += scratch[w];
-  for (int b = b0; b < b1; ++b) {
-    const int u = cum[b];
-    cum[b] = before;
-    before += u;
-  }
-  if (b0 < a.B && b1 == a.B) cum[a.B] = before;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) seqs[b].u0 += before;
+  if (b0 < a.B && b1 == a.B) seqs[a.B].u0 = before + mine;
   __syncthreads();
-}
-
-// The sequence whose units hold unit u of a key head (cum[b] <= u < cum[b + 1]).
-__device__ __forceinline__ int find_seq(const int* cum, int B, int u) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= u)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
 }
 
 // A place on the work line: unit `tile` (of `tiles`) of item (hkv, b, rt).
 struct Place {
   int hkv, b, rt, tile;
   int tiles, rts;  // key tiles and row tiles of the sequence
-  SeqInfo s;
+  int i0;          // the item's first unit
+  Seq s;
 };
 
-__device__ __forceinline__ void load_seq(const DecodeParams& p, Place& c) {
-  bool bad;
-  c.s = seq_info(p.a, c.b, &bad);
-  c.tiles = ceil_div(walk_keys(p.a, c.s, p.walk_prefix), kKeyTile);
-  c.rts = ceil_div(c.s.n * p.Gp, p.Rt);
+__device__ __forceinline__ void load_seq(const DecodeParams& p, const Seq* seqs, Place& c) {
+  c.s = seqs[c.b];
+  c.tiles = c.s.own < 0 ? 0 : ceil_div(c.s.own + (p.walk_prefix ? p.a.prefix_len : 0), kKeyTile);
+  c.rts = (c.s.n * p.Gp + p.Rt - 1) / p.Rt;
 }
 
-// Unit u of the line (0 <= u < cum[B] * Hkv).
-__device__ __forceinline__ Place place_of(const DecodeParams& p, const int* cum, int u) {
+// Unit u of the line (0 <= u < total).
+static __device__ __noinline__ Place place_of(const DecodeParams& p, const Seq* seqs, int u) {
   Place c;
-  const int per_head = cum[p.a.B];
+  const int per_head = seqs[p.a.B].u0;
   c.hkv = u / per_head;
-  u -= c.hkv * per_head;
-  c.b = find_seq(cum, p.a.B, u);
-  load_seq(p, c);
-  u -= cum[c.b];
-  c.rt = u / c.tiles;
-  c.tile = u - c.rt * c.tiles;
+  const int in_head = u - c.hkv * per_head;
+  int lo = 0, hi = p.a.B;  // seqs[lo].u0 <= in_head < seqs[hi].u0
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (seqs[mid].u0 <= in_head)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  c.b = lo;
+  load_seq(p, seqs, c);
+  const int in_seq = in_head - c.s.u0;
+  c.rt = in_seq / c.tiles;
+  c.tile = in_seq - c.rt * c.tiles;
+  c.i0 = u - c.tile;
   return c;
 }
 
-// `by` units on, which the item has; then the next item's first unit, where that was its last and more
-// units follow on the line.
-__device__ __forceinline__ void advance(const DecodeParams& p, Place& c, int by, bool more) {
-  c.tile += by;
-  if (c.tile < c.tiles || !more) return;
+// The first unit of the next item; there is one.
+static __device__ __noinline__ void next_item(const DecodeParams& p, const Seq* seqs, Place& c) {
+  c.i0 += c.tiles;
   c.tile = 0;
   if (++c.rt < c.rts) return;
   c.rt = 0;
+#pragma unroll 1
   do {
     if (++c.b == p.a.B) {
       c.b = 0;
       ++c.hkv;
     }
-    load_seq(p, c);
+    load_seq(p, seqs, c);
   } while (c.tiles == 0 || c.rts == 0);
 }
 
@@ -157,20 +163,36 @@ __device__ __forceinline__ int own_page_or_0(const PagedArgs& a, int b, int p) {
   return max(page, 0);
 }
 
+// Four channels to O.
 template <typename T>
-__device__ __forceinline__ void put_out(T* dst, const float* f, int n);
+__device__ __forceinline__ void put4(T* dst, float4 v);
 template <>
-__device__ __forceinline__ void put_out<float>(float* dst, const float* f, int n) {
-  for (int i = 0; i < n; i += 2) *reinterpret_cast<float2*>(dst + i) = make_float2(f[i], f[i + 1]);
+__device__ __forceinline__ void put4<float>(float* dst, float4 v) {
+  *reinterpret_cast<float4*>(dst) = v;
 }
 template <>
-__device__ __forceinline__ void put_out<__nv_bfloat16>(__nv_bfloat16* dst, const float* f, int n) {
-  for (int i = 0; i < n; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(f[i], f[i + 1]);
+__device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16* dst, float4 v) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 // Slot of a worker's partial result of an item, in rows of ml and po.
-__device__ __forceinline__ size_t slot_of(const DecodeParams& p, int worker, int hkv, int b, int rt) {
-  return (size_t)(worker + ((long long)hkv * p.a.B + b) * p.RTmax + rt) * p.Rs;
+__device__ __forceinline__ int slot_of(const DecodeParams& p, int worker, const Place& at) {
+  return (worker + (at.hkv * p.a.B + at.b) * p.RTmax + at.rt) * p.Rs;
+}
+// Rows that a row tile has.
+__device__ __forceinline__ int rows_of(const DecodeParams& p, const Place& at) {
+  return min(p.Rt, at.s.n * p.Gp - at.rt * p.Rt);
+}
+
+// One float4 column of a row of an item to O, and with c4 == 0 the row's LSE.
+template <typename T, int D>
+__device__ __noinline__ void put_column(const DecodeParams& p, const Place& at, int r, int c4, float4 v, float m, float l) {
+  const int G = p.a.H / p.a.Hkv, rr = at.rt * p.Rt + r, t = token_of(p, rr), g = rr - t * p.Gp;
+  if (g >= G) return;  // an empty row
+  const size_t row = (size_t)(at.s.row0 + t) * p.a.H + at.hkv * G + g;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  put4<T>(static_cast<T*>(p.o) + row * D + c4 * 4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+  if (c4 == 0) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
 
 // ---- items that reach past one worker's range ----
@@ -184,187 +206,180 @@ template <int kRows, int kWarps>
 struct Kept {
   int i0[kWarps];  // the kept segment's item, by its first unit; -1: none
   Place at[kWarps];
-  float m[kWarps][kRows], l[kWarps][kRows];
+  float m[kWarps][kRows], l[kWarps][kRows];  // of the warp's latest segment
 };
 
-constexpr int kJoinMost = 32;  // partial results whose weights stand in shared memory at a time
-
-// One float4 column of one row of an item to O; with c4 == 0 the row's LSE as well.
+// A finished segment's rows (rows + r * pitch, floats of shared memory) by one warp: to O where the worker
+// had the whole item, else to its slot.
 template <typename T, int D>
-__device__ __forceinline__ void put_column(const DecodeParams& p, const Place& at, int r, int c4, float4 v, float m, float l) {
-  const int G = p.a.H / p.a.Hkv, rr = at.rt * p.Rt + r, t = rr / p.Gp, g = rr - t * p.Gp;
-  if (g >= G) return;
-  const size_t row = (size_t)(at.s.row0 + t) * p.a.H + at.hkv * G + g;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-  put_out<T>(static_cast<T*>(p.o) + row * D + c4 * 4, o, 4);
-  if (c4 == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+__device__ __forceinline__ void leave_rows(const DecodeParams& p, const Place& at, int worker, bool whole, const float* rows,
+                                           int pitch, const float* m, const float* l) {
+  constexpr int C4 = D / 4;
+  const int lane = threadIdx.x & 31, slot = slot_of(p, worker, at), F = rows_of(p, at) * C4;
+#pragma unroll 1
+  for (int f = lane; f < F; f += 32) {
+    const int r = f / C4, c4 = f % C4;
+    const float4 v = *reinterpret_cast<const float4*>(rows + r * pitch + c4 * 4);
+    if (whole) {
+      put_column<T, D>(p, at, r, c4, v, m[r], l[r]);
+    } else {
+      *reinterpret_cast<float4*>(p.po + (size_t)(slot + r) * D + c4 * 4) = v;
+      if (c4 == 0) p.ml[slot + r] = make_float2(m[r], l[r]);
+    }
+  }
 }
 
-// Adds a partial result's column to (v, m, l), whose maximum follows.
-__device__ __forceinline__ void add_column(float4& v, float& m, float& l, float4 x, float xm, float xl) {
-  const float top = fmaxf(m, xm), safe = top == -INFINITY ? 0.f : top;
-  const float a = ex2_approx(m - safe), b = ex2_approx(xm - safe);
-  v.x = v.x * a + x.x * b;
-  v.y = v.y * a + x.y * b;
-  v.z = v.z * a + x.z * b;
-  v.w = v.w * a + x.w * b;
-  l = l * a + xl * b;
-  m = top;
+// Columns with their row's maximum and sum, joined to one.
+struct Column {
+  float4 v;
+  float m, l;
+};
+__device__ __forceinline__ void add_column(Column& a, float4 x, float xm, float xl) {
+  const float top = fmaxf(a.m, xm), safe = top == -INFINITY ? 0.f : top;
+  const float s = ex2_approx(a.m - safe), t = ex2_approx(xm - safe);
+  a.v.x = a.v.x * s + x.x * t;
+  a.v.y = a.v.y * s + x.y * t;
+  a.v.z = a.v.z * s + x.z * t;
+  a.v.w = a.v.w * s + x.w * t;
+  a.l = a.l * s + xl * t;
+  a.m = top;
 }
 
 // By the whole block, at its end. Row r of warp w's kept segment lies at rows + w * warp_pitch + r * row_pitch
-// (floats). `wgt`: [kJoinMost][kRows], `part`: [threads] of shared memory, clear of the kept rows.
+// (floats). `offs`: [CTAs + 1] and `part`: [threads] of shared memory, clear of the kept rows.
 // With a shared prefix every item is left to the merge that follows, its partial results as above.
 template <typename T, int D, int kRows, int kWarps>
-__device__ __forceinline__ void join_items(const DecodeParams& p, const int* cum, int total, int each,
+__device__ __forceinline__ void join_items(const DecodeParams& p, const Seq* seqs, int total, int each,
                                            const Kept<kRows, kWarps>& kept, const float* rows, int warp_pitch,
-                                           int row_pitch, float* wgt, float4* part) {
+                                           int row_pitch, int* offs, Column* part) {
   constexpr int kThreads = 32 * kWarps, C4 = D / 4;
   __shared__ Place ends[2];
-  __shared__ int first_block[2], blocks[2], last[2];
-  __shared__ float row_m[kRows], row_l[kRows];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-  const bool shared = p.pre.key_tiles > 0;  // the merge with the prefix's results follows: nothing is final here
+  __shared__ int results[2];
+  const int tid = threadIdx.x, cta = blockIdx.x, w_cta = cta * kWarps;
+  const bool shared = p.pre.key_tiles > 0;
+  const int U0 = min(total, w_cta * each), U1 = min(total, U0 + kWarps * each);
+  // The items that the block's range begins and ends inside of: at most one each, perhaps the same.
+  Place end;
+  int blocks = 0, first = 0;  // CTAs of the item, its first
+  if (tid < 2 && U0 < U1 && !shared) {
+    end = place_of(p, seqs, tid ? U1 - 1 : U0);
+    const int i1 = end.i0 + end.tiles - 1;
+    // cut at this end, and not the other end's item too
+    if (tid ? i1 >= U1 && end.i0 >= U0 : end.i0 < U0) {
+      first = end.i0 / (each * kWarps);
+      blocks = i1 / (each * kWarps) - first + 1;
+    }
+    ends[tid] = end;
+  }
   __syncthreads();
   // 1. The kept segments of each item.
-  for (int i = 0; i < kWarps; ++i) {
+#pragma unroll 1
+  for (int i = 0, k1; i < kWarps; i = k1) {
+    k1 = i + 1;
     const int i0 = kept.i0[i];
-    if (i0 < 0 || (i > 0 && kept.i0[i - 1] == i0)) continue;
-    int k1 = i + 1;
+    if (i0 < 0) continue;
     while (k1 < kWarps && kept.i0[k1] == i0) ++k1;
     const Place& at = kept.at[i];
-    const int i1 = i0 + at.tiles - 1, w1 = i1 / each;
-    // the item's last worker left a first segment in its slot
-    const bool more = min(total, (w1 + 1) * each) > i1 + 1;
-    const bool here = !shared && i0 / each / kWarps == cta && w1 / kWarps == cta;
-    const size_t slot = slot_of(p, cta * kWarps + i, at.hkv, at.b, at.rt);
-    const size_t slot1 = slot_of(p, w1, at.hkv, at.b, at.rt);
-    const int R = min(p.Rt, at.s.n * p.Gp - at.rt * p.Rt);
-    for (int f = tid; f < R * C4; f += kThreads) {
-      const int r = f / C4, c4 = f - r * C4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      float m = -INFINITY, l = 0.f;
+    const int slot = slot_of(p, w_cta + i, at), i_end = i0 + at.tiles;
+    const bool here = !shared && i0 >= U0 && i_end <= U1;
+    // the item ends inside the next worker's range, which left that part in its slot
+    const int more = here && i_end > (w_cta + k1) * each ? slot_of(p, w_cta + k1, at) : -1;
+    const int F = rows_of(p, at) * C4;
+#pragma unroll 1
+    for (int f = tid; f < F; f += kThreads) {
+      const int r = f / C4, c4 = f % C4;
+      Column c = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+#pragma unroll 1
       for (int k = i; k < k1; ++k)
-        add_column(v, m, l, *reinterpret_cast<const float4*>(rows + k * warp_pitch + r * row_pitch + c4 * 4), kept.m[k][r],
+        add_column(c, *reinterpret_cast<const float4*>(rows + k * warp_pitch + r * row_pitch + c4 * 4), kept.m[k][r],
                    kept.l[k][r]);
+      if (more >= 0) {
+        const float2 y = __ldcg(p.ml + more + r);
+        add_column(c, __ldcg(reinterpret_cast<const float4*>(p.po + (size_t)(more + r) * D) + c4), y.x, y.y);
+      }
       if (here) {
-        if (more) {
-          const float2 y = __ldcg(p.ml + slot1 + r);
-          add_column(v, m, l, __ldcg(reinterpret_cast<const float4*>(p.po + (slot1 + r) * D) + c4), y.x, y.y);
-        }
-        put_column<T, D>(p, at, r, c4, v, m, l);
+        put_column<T, D>(p, at, r, c4, c.v, c.m, c.l);
       } else {
-        *reinterpret_cast<float4*>(p.po + (slot + r) * D + c4 * 4) = v;
-        if (c4 == 0) p.ml[slot + r] = make_float2(m, l);
+        *reinterpret_cast<float4*>(p.po + (size_t)(slot + r) * D + c4 * 4) = c.v;
+        if (c4 == 0) p.ml[slot + r] = make_float2(c.m, c.l);
       }
     }
   }
   if (shared) return;
-  // 2. The items that the block's range begins and ends inside of: at most one each, perhaps the same.
-  const int U0 = min(total, cta * kWarps * each), U1 = min(total, U0 + kWarps * each);
   __syncthreads();
+  // 2. Which of the block's cut items it brings the last part of, and where that item's parts lie.
   if (tid < 2) {
-    int f = -1, n = 0;
-    if (U0 < U1) {
-      const Place at = place_of(p, cum, tid ? U1 - 1 : U0);
-      const int i0 = at.hkv * cum[p.a.B] + cum[at.b] + at.rt * at.tiles, i1 = i0 + at.tiles - 1;
-      f = i0 / each / kWarps;
-      n = i1 / each / kWarps - f + 1;
-      if (tid == 0 ? i0 >= U0 : (i1 < U1 || i0 < U0)) n = 0;  // not cut at this end, or the other end's too
-      ends[tid] = at;
-    }
-    int is_last = 0;
-    if (n > 1) {
+    int n = 0;
+    if (blocks > 1) {
       __threadfence();
-      if (static_cast<int>(atomicAdd(p.count + f, 1u)) + 1 == n) {
-        p.count[f] = 0u;
-        is_last = 1;
+      if (static_cast<int>(atomicAdd(p.count + first, 1u)) + 1 == blocks) {
+        p.count[first] = 0u;
         __threadfence();
+        n = blocks;
       }
     }
-    first_block[tid] = f;
-    blocks[tid] = n;
-    last[tid] = is_last;
+    results[tid] = n;
   }
   __syncthreads();
+#pragma unroll 1
   for (int e = 0; e < 2; ++e) {
-    if (!last[e]) continue;
+    const int nb = results[e];
+    if (nb == 0) continue;
     const Place& at = ends[e];
-    const int i0 = at.hkv * cum[p.a.B] + cum[at.b] + at.rt * at.tiles, i1 = i0 + at.tiles - 1;
-    const int w0 = i0 / each, w1 = i1 / each, c0 = first_block[e], nb = blocks[e], c1 = c0 + nb - 1;
-    const int n = nb + (min(total, (w1 + 1) * each) > i1 + 1 && w1 > c1 * kWarps);
-    const size_t slot = slot_of(p, 0, at.hkv, at.b, at.rt);
-    // rows of ml and po where partial result k begins
-    auto row_of = [&](int k) {
-      const int w = k == 0 ? w0 : k < nb ? (c0 + k) * kWarps : w1;
-      return slot + (size_t)w * p.Rs;
-    };
-    const int R = min(p.Rt, at.s.n * p.Gp - at.rt * p.Rt), F = R * C4;
-    const int deal = F <= kThreads / 2 ? kThreads / F : 1, mine = deal > 1 ? tid / F : 0;
-    for (int r = warp; r < R; r += kWarps) {
-      float m = -INFINITY, l = 0.f;
-      for (int k = lane; k < n; k += 32) {
-        const float2 y = __ldcg(p.ml + row_of(k) + r);
-        const float top = fmaxf(m, y.x), safe = top == -INFINITY ? 0.f : top;
-        l = l * ex2_approx(m - safe) + y.y * ex2_approx(y.x - safe);
-        m = top;
-      }
-      float top = m;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float safe = top == -INFINITY ? 0.f : top;
-      l *= ex2_approx(m - safe);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) {
-        row_m[r] = safe;
-        row_l[r] = l;
-      }
-      // the first ones' weights
-      if (lane < n) wgt[lane * kRows + r] = ex2_approx(__ldcg(p.ml + row_of(lane) + r).x - safe);
-    }
+    const int i_end = at.i0 + at.tiles, w0 = at.i0 / each, w1 = (i_end - 1) / each, c0 = w0 / kWarps;
+    const int n = nb + (w1 > (c0 + nb - 1) * kWarps && i_end < min(total, (w1 + 1) * each));
+    for (int k = tid; k < n; k += kThreads)
+      offs[k] = slot_of(p, k == 0 ? w0 : k < nb ? (c0 + k) * kWarps : w1, at);
     __syncthreads();
     // Columns of four channels; with few of them the partial results are dealt out to the threads too.
-    for (int f = deal > 1 ? tid - mine * F : tid; f < F; f += kThreads) {
-      if (mine >= deal) break;
-      const int r = f / C4, c4 = f - r * C4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kBatch = 12;  // loads in flight
+    const int F = rows_of(p, at) * C4, deal = F <= kThreads / 2 ? kThreads / F : 1;
+    const int mine = deal > 1 ? tid / F : 0;
+#pragma unroll 1
+    for (int f = tid - mine * F; f < F && mine < deal; f += kThreads) {
+      const int r = f / C4, c4 = f % C4;
+      Column c = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+      constexpr int kBatch = 8;  // partial results whose loads are in flight together
+#pragma unroll 1
       for (int k = mine; k < n; k += kBatch * deal) {
         float4 y[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          y[j] = __ldcg(reinterpret_cast<const float4*>(p.po + (row_of(min(k + j * deal, n - 1)) + r) * D) + c4);
+        float2 z[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const int kk = k + j * deal;
-          float w = 0.f;
-          if (kk < n)
-            w = kk < kJoinMost ? wgt[kk * kRows + r] : ex2_approx(__ldcg(p.ml + row_of(kk) + r).x - row_m[r]);
-          v.x = fmaf(w, y[j].x, v.x);
-          v.y = fmaf(w, y[j].y, v.y);
-          v.z = fmaf(w, y[j].z, v.z);
-          v.w = fmaf(w, y[j].w, v.w);
+          const int row = offs[min(k + j * deal, n - 1)] + r;
+          y[j] = __ldcg(reinterpret_cast<const float4*>(p.po + (size_t)row * D) + c4);
+          z[j] = __ldcg(p.ml + row);
+        }
+        float top = c.m;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) top = fmaxf(top, z[j].x);  // one counted twice changes no maximum
+        const float safe = top == -INFINITY ? 0.f : top, s = ex2_approx(c.m - safe);
+        c.v = make_float4(c.v.x * s, c.v.y * s, c.v.z * s, c.v.w * s);
+        c.l *= s;
+        c.m = top;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const float t = k + j * deal < n ? ex2_approx(z[j].x - safe) : 0.f;
+          c.v.x = fmaf(t, y[j].x, c.v.x);
+          c.v.y = fmaf(t, y[j].y, c.v.y);
+          c.v.z = fmaf(t, y[j].z, c.v.z);
+          c.v.w = fmaf(t, y[j].w, c.v.w);
+          c.l = fmaf(t, z[j].y, c.l);
         }
       }
-      if (deal == 1)
-        put_column<T, D>(p, at, r, c4, v, row_m[r], row_l[r]);
+      if (deal > 1)
+        part[tid] = c;
       else
-        part[tid] = v;
+        put_column<T, D>(p, at, r, c4, c.v, c.m, c.l);
     }
     __syncthreads();
     if (deal > 1 && tid < F) {
-      float4 v = part[tid];
+      Column c = part[tid];
+#pragma unroll 1
       for (int k = 1; k < deal; ++k) {
-        const float4 y = part[k * F + tid];
-        v.x += y.x;
-        v.y += y.y;
-        v.z += y.z;
-        v.w += y.w;
+        const Column& o = part[k * F + tid];
+        add_column(c, o.v, o.m, o.l);
       }
-      const int r = tid / C4;
-      put_column<T, D>(p, at, r, tid - r * C4, v, row_m[r], row_l[r]);
+      put_column<T, D>(p, at, tid / C4, tid % C4, c.v, c.m, c.l);
     }
     __syncthreads();
   }
@@ -372,14 +387,16 @@ __device__ __forceinline__ void join_items(const DecodeParams& p, const int* cum
 
 // Rows of idle sequences: O = 0, LSE = -inf. The blocks share the sequences out.
 template <typename T, int D>
-__device__ __forceinline__ void clear_idle_rows(const DecodeParams& p) {
+__device__ __forceinline__ void clear_idle_rows(const DecodeParams& p, const Seq* seqs) {
+#pragma unroll 1
   for (int b = blockIdx.x; b < p.a.B; b += gridDim.x) {
-    bool bad;
-    const SeqInfo s = seq_info(p.a, b, &bad);
+    const Seq s = seqs[b];
     if (s.own >= 0) continue;
     const size_t at = (size_t)s.row0 * p.a.H, n = (size_t)s.n * p.a.H;
-    const float zero[2] = {0.f, 0.f};
-    for (size_t e = threadIdx.x; e < n * (D / 2); e += blockDim.x) put_out<T>(static_cast<T*>(p.o) + at * D + 2 * e, zero, 2);
+#pragma unroll 1
+    for (size_t e = threadIdx.x; e < n * (D / 4); e += blockDim.x)
+      put4<T>(static_cast<T*>(p.o) + (at * D + 4 * e), make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll 1
     for (size_t e = threadIdx.x; e < n; e += blockDim.x) p.lse[at + e] = -INFINITY;
   }
 }

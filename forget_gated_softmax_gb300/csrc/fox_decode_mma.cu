@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   const int stages = x.stages;
   uint8_t* ring = sm + warp * stages * (2 * L::kTileBytes);
   uint8_t* gates = sm + W * stages * (2 * L::kTileBytes) + warp * stages * x.gstage;
-  int* cum = reinterpret_cast<int*>(sm + W * stages * (2 * L::kTileBytes + x.gstage));
+  Seq* seqs = reinterpret_cast<Seq*>(sm + W * stages * (2 * L::kTileBytes + x.gstage));
 
   grid_dep_trigger();
   if (threadIdx.x == 0) abort_word = 0;
@@ -113,74 +113,18 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     for (int s = 0; s < stages; ++s) mbar_init(&bars[warp][s], 1);
     fence_mbar_init();
   }
-  scan_units(p, cum, scratch);  // ends with a block barrier
+  scan_sequences(p, seqs, scratch);  // ends with a block barrier
   const bool shared = p.pre.key_tiles > 0;
   if (shared && blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) p.cum[b] = cum[b];
+    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) p.cum[b] = seqs[b].u0;
 
   const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size;
   const int KS = S < kKeyTile ? S : kKeyTile;      // tokens of a sub-page
   const int heads = x.heads, gpitch = x.gpitch;
   const int base_off = (S == 16 ? 2 : 1) * x.gsub;
-  const int total = cum[a.B] * a.Hkv, each = units_per_worker(total, p.workers);
+  const int total = seqs[a.B].u0 * a.Hkv, each = units_per_worker(total, p.workers);
   const int w = blockIdx.x * W + warp;
   const int u0 = min(total, w * each), count = min(total, u0 + each) - u0;
-
-  // The consumer's place, and the producer's, which runs ahead by a window or two.
-  Place cur = {}, pro = {};
-  int left = count;  // units that no window holds yet
-  auto load_window = [&]() {
-    Window v = {};
-    if (left == 0) return v;
-    v.hkv = pro.hkv;
-    v.b = pro.b;
-    v.rt = pro.rt;
-    v.tile = pro.tile;
-    v.n = min(min(32, pro.tiles - pro.tile), left);
-    v.id1 = -1;
-    if (lane < v.n) {
-      const int j = (v.tile + lane) * kKeyTile;
-      v.id0 = own_page_or_0(a, v.b, j);
-      if (S == 16 && j + 16 < pro.s.own) v.id1 = own_page_or_0(a, v.b, j + 16);
-    }
-    left -= v.n;
-    advance(p, pro, v.n, left > 0);
-    return v;
-  };
-  Window now = {}, next = {};
-  int at = 0;  // the producer's next tile of `now`
-
-  // Copies of the producer's next tile into `stage`.
-  auto issue = [&](int stage) {
-    const int id0 = __shfl_sync(0xffffffffu, now.id0, at), id1 = __shfl_sync(0xffffffffu, now.id1, at);
-    uint8_t* st = ring + stage * (2 * L::kTileBytes);
-    uint8_t* sg = gates + stage * x.gstage;
-    const int h0 = now.hkv * G + (G > L::kRows ? now.rt * p.Rt % Gp : 0);
-    const int slot = S == 16 ? 0 : (now.tile + at) * kKeyTile & (S - 1);
-    const int subs = id1 >= 0 ? 2 : 1;
-    if (lane == 0) {
-      uint64_t* bar = &bars[warp][stage];
-      mbar_arrive_expect_tx(bar, subs * (2 * KS * D * 2 + heads * gpitch * 4));
-      for (int i = 0; i < subs; ++i) {
-        const int id = i ? id1 : id0;
-#pragma unroll
-        for (int y = 0; y < D / 64; ++y) {
-          tma_load_4d(st + y * (kKeyTile * 128) + i * (16 * 128), &tmap_k, bar, y * 64, slot, now.hkv, id);
-          tma_load_4d(st + L::kTileBytes + y * (kKeyTile * 128) + i * (16 * 128), &tmap_v, bar, y * 64, slot, now.hkv,
-                      id);
-        }
-        tma_load_3d(sg + i * x.gsub, &tmap_g, bar, slot - 4, h0, id);
-      }
-    }
-    for (int i = 0; i < subs; ++i)
-      if (lane < heads && h0 + lane < a.H)
-        cp_async8(smem_u32(sg + base_off) + (i * heads + lane) * 8, a.gbase + gbase_offset(a, i ? id1 : id0, h0 + lane));
-    if (++at == now.n) {
-      now = next.n > 0 ? next : load_window();
-      at = 0;
-      next = load_window();
-    }
-  };
 
   const int g8 = lane >> 2, t4 = lane & 3;
   uint32_t qf[D / 16][NT][2];
@@ -188,82 +132,46 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   float m[NT][2], l[NT][2];
   Gate2 ci[NT][2];
   int pos[NT][2], gidx[NT][2];
-  // An item's rows: Q fragments (row g8 of each eight), and the pages of this thread's columns of S^T,
-  // rows 2 t4 and 2 t4 + 1.
   int pg[NT][2];
-  auto open_rows = [&]() {
-    const int r0 = cur.rt * p.Rt;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = r0 + nt * 8 + 2 * t4 + e, t = r / Gp, g = r - t * Gp;
-        const bool here = t < cur.s.n && g < G;
-        pos[nt][e] = cur.s.own - cur.s.n + t;
-        gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : -1;
-        pg[nt][e] = here ? own_page_or_0(a, cur.b, pos[nt][e]) : 0;
-      }
-      const int r = r0 + nt * 8 + g8, t = r / Gp, g = r - t * Gp;
-      const bool in = t < cur.s.n && g < G;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(cur.s.row0 + (in ? t : 0)) * p.q_stride +
-                                 (size_t)(cur.hkv * G + (in ? g : 0)) * D + 2 * t4;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
-        qf[ks][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
-      }
-    }
-  };
-  // Their cumulative gates, and nothing summed yet.
-  auto open_sums = [&]() {
-    const int h0 = cur.hkv * G + (G > L::kRows ? cur.rt * p.Rt % Gp : 0);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        ci[nt][e] = {-INFINITY, 0.f};  // an empty row's scores are -inf
-        if (gidx[nt][e] >= 0)
-          ci[nt][e] = gate_sum(a, pg[nt][e], pos[nt][e] & (S - 1), h0 + gidx[nt][e]);
-        else
-          gidx[nt][e] = 0;
-        m[nt][e] = -INFINITY;
-        l[nt][e] = 0.f;
-      }
-#pragma unroll
-    for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[dt][nt][e] = 0.f;
-  };
-
-  if (count > 0) {
-    // Loads that need nothing of each other first: the tiles' pages, then the rows'.
-    cur = pro = place_of(p, cum, u0);
-    now = load_window();
-    open_rows();
-  }
-  for (int n = 0; n < stages; ++n) {
-    if (n < count) issue(n);
-    cp_async_commit();
-  }
-  if (count > 0) {
-    open_sums();
-    if (next.n == 0) next = load_window();
-  }
-
   // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
   const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
-  bool fresh = false, ok = true;
+
+  // The consumer's place, and the producer's, which runs ahead by a window or two.
+  Place cur = {}, pro = {};
+  if (count > 0) cur = pro = place_of(p, seqs, u0);
+  Window now = {}, next = {};
+  int left = count, at = 0;  // units that no window holds yet; the producer's next tile of `now`
+  bool fresh = true, opened = false, ok = true;
   int stage = 0;
   uint32_t phase = 0;
 
-  for (int n = 0; n < count; ++n) {
-    if (fresh) {
-      open_rows();
-      open_sums();
-      fresh = false;
+  // Step n consumes tile n and then issues the copies of tile n + stages; the first `stages` only issue.
+#pragma unroll 1
+  for (int n = -stages; n < count; ++n) {
+    if (n >= 0) {
+    if (!opened) {
+      // The item's rows: their cumulative gates, and nothing summed yet.
+      opened = true;
+      const int h0 = cur.hkv * G + (G > L::kRows ? cur.rt * p.Rt % Gp : 0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ci[nt][e] = {-INFINITY, 0.f};  // an empty row's scores are -inf
+          if (gidx[nt][e] >= 0)
+            ci[nt][e] = gate_sum(a, pg[nt][e], pos[nt][e] & (S - 1), h0 + gidx[nt][e]);
+          else
+            gidx[nt][e] = 0;
+          m[nt][e] = -INFINITY;
+          l[nt][e] = 0.f;
+        }
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[dt][nt][e] = 0.f;
     }
     uint8_t* st = ring + stage * (2 * L::kTileBytes);
     ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][stage], phase, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA));
@@ -387,12 +295,8 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     if (cur.tile + 1 == cur.tiles || n + 1 == count) {
       // Results: O^T through shared memory to rows, finished or the worker's part of them: by the stage just
       // read, or, for the block to join with its neighbours', kept at the ring's start (all copies were read).
-      const int i0 = cur.hkv * cum[a.B] + cum[cur.b] + cur.rt * cur.tiles;
-      const bool alone = i0 / each == (i0 + cur.tiles - 1) / each, whole = alone && !shared;
-      const bool keep = !alone && n + 1 == count;
+      const bool alone = cur.i0 >= u0 && cur.i0 + cur.tiles <= u0 + count, keep = !alone && n + 1 == count;
       float* out = reinterpret_cast<float*>(keep ? ring : st);
-      const size_t slot = slot_of(p, w, cur.hkv, cur.b, cur.rt);
-      const int r0 = cur.rt * p.Rt, R = min(L::kRows, cur.s.n * Gp - r0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -400,68 +304,132 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
           float y = l[nt][e];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-          const float f = whole ? (y > 0.f ? 1.f / y : 0.f) : 1.f;
           const int rl = nt * 8 + 2 * t4 + e;
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
-            out[rl * L::kOutStride + dt * 16 + g8] = acc[dt][nt][e] * f;
-            out[rl * L::kOutStride + dt * 16 + g8 + 8] = acc[dt][nt][e + 2] * f;
+            out[rl * L::kOutStride + dt * 16 + g8] = acc[dt][nt][e];
+            out[rl * L::kOutStride + dt * 16 + g8 + 8] = acc[dt][nt][e + 2];
           }
-          if (g8 == 0 && rl < R) {
-            const int r = r0 + rl, t = r / Gp, g = r - t * Gp;
-            if (keep) {
-              kept.m[warp][rl] = m[nt][e];
-              kept.l[warp][rl] = y;
-            } else if (!whole) {
-              p.ml[slot + rl] = make_float2(m[nt][e], y);
-            } else if (g < G)
-              p.lse[(size_t)(cur.s.row0 + t) * a.H + cur.hkv * G + g] =
-                  y > 0.f ? (m[nt][e] + log2f(y)) * kLn2 : -INFINITY;
+          if (g8 == 0) {
+            kept.m[warp][rl] = m[nt][e];
+            kept.l[warp][rl] = y;
           }
         }
-      __syncwarp();
-      constexpr int E = D / 32;
       if (keep && lane == 0) {
-        kept.i0[warp] = i0;
+        kept.i0[warp] = cur.i0;
         kept.at[warp] = cur;
       }
-#pragma unroll 1
-      for (int rl = 0; rl < R && !keep; ++rl) {
-        float f[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = out[rl * L::kOutStride + lane * E + e];
-        if (whole) {
-          const int r = r0 + rl, t = r / Gp, g = r - t * Gp;
-          if (g < G)
-            put_out<__nv_bfloat16>(
-                static_cast<__nv_bfloat16*>(p.o) + ((size_t)(cur.s.row0 + t) * a.H + cur.hkv * G + g) * D + lane * E, f, E);
-        } else {
-          put_out<float>(p.po + (slot + rl) * D + lane * E, f, E);
-        }
-      }
+      __syncwarp();
+      if (!keep)
+        leave_rows<__nv_bfloat16, D>(p, cur, w, alone && !shared, out, L::kOutStride, kept.m[warp], kept.l[warp]);
       fence_proxy_async_smem();  // before the next copy into this stage
       __syncwarp();
+      opened = false;
       fresh = true;
     }
-    advance(p, cur, 1, n + 1 < count);
-    if (n + stages < count) issue(stage);
-    cp_async_commit();
+    if (++cur.tile == cur.tiles && n + 1 < count) next_item(p, seqs, cur);
     if (++stage == stages) {
       stage = 0;
       phase ^= 1;
     }
+    }
+
+    if (n + stages < count) {
+      // A window of the producer's next tiles, whose pages are read long before they are needed.
+      if (at == now.n) {
+        at = 0;
+#pragma unroll 1
+        do {
+          now = next;
+          next.n = 0;
+          if (left > 0) {
+            next.hkv = pro.hkv;
+            next.b = pro.b;
+            next.rt = pro.rt;
+            next.tile = pro.tile;
+            next.n = min(min(32, pro.tiles - pro.tile), left);
+            next.id0 = 0;
+            next.id1 = -1;
+            if (lane < next.n) {
+              const int j = (pro.tile + lane) * kKeyTile;
+              next.id0 = own_page_or_0(a, pro.b, j);
+              if (S == 16 && j + 16 < pro.s.own) next.id1 = own_page_or_0(a, pro.b, j + 16);
+            }
+            left -= next.n;
+            pro.tile += next.n;
+            if (pro.tile == pro.tiles && left > 0) next_item(p, seqs, pro);
+          }
+        } while (now.n == 0);
+      }
+    }
+    if (fresh && n + 1 < count) {
+      // The next item's rows: Q fragments (row g8 of each eight), and the pages of this thread's columns of
+      // S^T, rows 2 t4 and 2 t4 + 1.
+      fresh = false;
+      const int r0 = cur.rt * p.Rt;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + nt * 8 + 2 * t4 + e, t = token_of(p, r), g = r - t * Gp;
+          const bool here = t < cur.s.n && g < G;
+          pos[nt][e] = cur.s.own - cur.s.n + t;
+          gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : -1;
+          pg[nt][e] = here ? own_page_or_0(a, cur.b, pos[nt][e]) : 0;
+        }
+        const int r = r0 + nt * 8 + g8, t = token_of(p, r), g = r - t * Gp;
+        const bool in = t < cur.s.n && g < G;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(cur.s.row0 + (in ? t : 0)) * p.q_stride +
+                                   (size_t)(cur.hkv * G + (in ? g : 0)) * D + 2 * t4;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          qf[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+          qf[ks][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+        }
+      }
+    }
+    if (n + stages < count) {
+      // Copies of the producer's next tile; the stage is the one just read, and in the first steps the n-th.
+      const int to = n < 0 ? n + stages : (stage == 0 ? stages : stage) - 1;
+      const int id0 = __shfl_sync(0xffffffffu, now.id0, at), id1 = __shfl_sync(0xffffffffu, now.id1, at);
+      uint8_t* dst = ring + to * (2 * L::kTileBytes);
+      uint8_t* sg = gates + to * x.gstage;
+      const int h0 = now.hkv * G + (G > L::kRows ? now.rt * p.Rt % Gp : 0);
+      const int slot = S == 16 ? 0 : (now.tile + at) * kKeyTile & (S - 1);
+      const int subs = id1 >= 0 ? 2 : 1;
+      if (lane == 0) mbar_arrive_expect_tx(&bars[warp][to], subs * (2 * KS * D * 2 + heads * gpitch * 4));
+      __syncwarp();
+#pragma unroll 1
+      for (int i = 0; i < subs; ++i) {
+        const int id = i ? id1 : id0;
+        // One lane a copy: K and V of 64 channels each, and the gates.
+        if (lane < D / 32) {
+          const int y = lane >> 1;
+          tma_load_4d(dst + (lane & 1) * L::kTileBytes + y * (kKeyTile * 128) + i * (16 * 128), lane & 1 ? &tmap_v : &tmap_k,
+                      &bars[warp][to], y * 64, slot, now.hkv, id);
+        } else if (lane == 31) {
+          tma_load_3d(sg + i * x.gsub, &tmap_g, &bars[warp][to], slot - 4, h0, id);
+        }
+        if (lane < heads && h0 + lane < a.H)
+          cp_async8(smem_u32(sg + base_off) + (i * heads + lane) * 8, a.gbase + gbase_offset(a, id, h0 + lane));
+      }
+      ++at;
+    }
+    cp_async_commit();
   }
   if (!ok) {
     // A wait gave up: every copy issued must still land before shared memory is used or released.
     for (int s = 0; s < stages; ++s) mbar_wait_drain(&bars[warp][s], s < stage ? phase ^ 1 : phase);
     cp_async_wait<0>();
   }
-  clear_idle_rows<__nv_bfloat16, D>(p);
-  float* wgt = reinterpret_cast<float*>(sm + 2 * L::kTileBytes);  // the first warp's second stage
-  static_assert(L::kRows * kJoinMost * 4 + 32 * W * 16 <= 2 * L::kTileBytes, "weights and sums fit there");
-  join_items<__nv_bfloat16, D, L::kRows, W>(p, cum, total, each, kept, reinterpret_cast<const float*>(sm),
-                                            stages * (2 * L::kTileBytes) / 4, L::kOutStride, wgt,
-                                            reinterpret_cast<float4*>(wgt + L::kRows * kJoinMost));
+  clear_idle_rows<__nv_bfloat16, D>(p, seqs);
+  // Sums and offsets stand in the first and the second warp's second stage.
+  const int warp_bytes = stages * (2 * L::kTileBytes);
+  static_assert(32 * W * sizeof(Column) <= 2 * L::kTileBytes && (kSMs + 1) * 4 <= 2 * L::kTileBytes, "they fit there");
+  join_items<__nv_bfloat16, D, L::kRows, W>(p, seqs, total, each, kept, reinterpret_cast<const float*>(sm),
+                                            warp_bytes / 4, L::kOutStride,
+                                            reinterpret_cast<int*>(sm + warp_bytes + 2 * L::kTileBytes),
+                                            reinterpret_cast<Column*>(sm + 2 * L::kTileBytes));
   // With a shared prefix a merge follows, launched as a dependent of this kernel as this one is of the
   // prefix's; it needs both grids to be through, so this one ends after that one.
   if (shared) grid_dep_wait();
@@ -478,13 +446,13 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
   x.gsub = (x.heads * x.gpitch * 4 + 127) / 128 * 128;
   x.gstage = subs * x.gsub + (subs * x.heads * 8 + 127) / 128 * 128;
   constexpr int kMostGates = 2 * ((L::kRows * 20 * 4 + 127) / 128 * 128) + 256;
-  constexpr size_t kMost = 232448 - 3072;  // of an SM's shared memory, less the static part
-  const size_t fixed = 1024 + sizeof(int) * ((size_t)p.a.B + 1);
+  constexpr size_t kMost = 232448 - 4096;  // of an SM's shared memory, less the static part
+  const size_t fixed = 1024 + sizeof(Seq) * ((size_t)p.a.B + 1);
   const size_t one = (size_t)L::kWarps * (2 * L::kTileBytes + x.gstage);
   // Three stages where they fit beside the gates and the sequences' offsets.
   x.stages = fixed + 3 * one <= kMost ? 3 : 2;
   const size_t smem = fixed + x.stages * one;
-  static_assert(1024 + 4 * (kMaxSeqs + 1) + 2 * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
+  static_assert(1024 + sizeof(Seq) * (kMaxSeqs + 1) + 2 * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;

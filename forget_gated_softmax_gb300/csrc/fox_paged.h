@@ -13,7 +13,7 @@
 
 namespace fox {
 
-constexpr int kMaxSeqs = 4096;  // sequences of one call: every CTA holds their work offsets in shared memory
+constexpr int kMaxSeqs = 2048;  // sequences of one call: every CTA holds their work offsets in shared memory
 
 struct PagedArgs {
   int num_pages, page_size, page_shift, H, Hkv, d;  // page_size = 1 << page_shift

@@ -274,7 +274,7 @@ typedef struct fox_cache {
  * Two sequences of one append must not name the same page for their new tokens.
  */
 typedef struct fox_batch {
-  int B;                       /* sequences, 0 .. 4096 */
+  int B;                       /* sequences, 0 .. 2048 */
   int max_new;                 /* >= the new tokens of any sequence (ignored without cu_new), >= 1 */
   int table_stride;            /* entries of a sequence's row of `table`, >= 1 */
   int prefix_len;              /* tokens of the shared prefix; 0: none */

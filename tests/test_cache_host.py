@@ -47,7 +47,7 @@ BAD_CACHE = [
     (dict(k=None), 1), (dict(v=FAKE + 8), 1), (dict(g=None), 1), (dict(gbase=FAKE + 4), 1),
 ]
 BAD_BATCH = [
-    (dict(B=-1), 1), (dict(B=4097), 2), (dict(table_stride=0), 1), (dict(prefix_len=-1), 1),
+    (dict(B=-1), 1), (dict(B=2049), 2), (dict(table_stride=0), 1), (dict(prefix_len=-1), 1),
     (dict(prefix_len=5), 1), (dict(lens=None), 1), (dict(lens=FAKE + 2), 1), (dict(table=None), 1),
     (dict(cu_new=FAKE, max_new=0), 1), (dict(cu_new=FAKE + 1), 1), (dict(table_stride=1 << 30), 2),
     (dict(B=3), 1),  # two rows do not go around three sequences
@@ -84,11 +84,11 @@ def test_bad_rows_scales_and_workspaces_are_refused(L):
 
 
 def test_more_work_than_ints_count_is_refused(L):
-    big = _batch(B=4096, table_stride=1 << 20)  # 67 million tokens a sequence
-    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(big), 4096) == 0
-    assert _decode(L, s=big, rows=4096) == 2
-    fits = _batch(B=4096, table_stride=1 << 11)
-    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(fits), 4096) > 0
+    big = _batch(B=2048, table_stride=1 << 21)  # 134 million tokens a sequence
+    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(big), 2048) == 0
+    assert _decode(L, s=big, rows=2048) == 2
+    fits = _batch(B=2048, table_stride=1 << 11)
+    assert L.fox_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(fits), 2048) > 0
 
 
 def test_bad_rotations_are_refused(L):
