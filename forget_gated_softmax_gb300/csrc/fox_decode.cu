@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
   __shared__ Gate2 ci[kSimtWarps][kSimtRows];
   __shared__ int offs[kSMs * kSimtCtas + 1];
   __shared__ Column part[32 * kSimtWarps];
+  __shared__ BlockEnds ends;
   __shared__ Kept<kSimtRows, kSimtWarps> kept;
   const PagedArgs& a = p.a;
   scan_sequences(p, seqs, scratch);
@@ -49,6 +50,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
   Place at;
   if (left > 0) at = place_of(p, seqs, u0);
   if (lane == 0) kept.i0[warp] = -1;
+  find_ends<kSimtWarps>(p, seqs, total, each, ends);
   while (left > 0) {
     // A segment: key tiles tile0 .. tile1 - 1 of one item.
     const Seq s = at.s;
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
     if (tile1 == at.tiles && left > 0) next_item(p, seqs, at);
   }
   clear_idle_rows<float, D>(p, seqs);
-  join_items<float, D, kSimtRows, kSimtWarps>(p, seqs, total, each, kept, &qs[0][0][0], kSimtRows * D, D, offs, part);
+  join_items<float, D, kSimtRows, kSimtWarps>(p, seqs, total, each, kept, ends, &qs[0][0][0], kSimtRows * D, D, offs, part);
 }
 
 // One output row by one warp: the partial results of its own item and of the shared prefix joined, in the

@@ -156,6 +156,12 @@ __device__ __forceinline__ Gate2 gate_sum(const PagedArgs& a, int page, int slot
   return {s, e + base.y};
 }
 
+// A table entry as a page; page 0 with a report where it is none.
+__device__ __forceinline__ int checked_page(const PagedArgs& a, int id) {
+  const bool ok = id >= 0 && id < a.num_pages;
+  if (!ok && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
+  return ok ? id : 0;
+}
 // The page of own token p, page 0 with a report where the table has none.
 __device__ __forceinline__ int own_page_or_0(const PagedArgs& a, int b, int p) {
   const int page = own_page(a, b, p);
@@ -245,32 +251,42 @@ __device__ __forceinline__ void add_column(Column& a, float4 x, float xm, float 
   a.m = top;
 }
 
+// The items that a block's range of the line begins and ends inside of: at most one each, perhaps the same.
+struct BlockEnds {
+  Place at[2];
+  int first[2], blocks[2];  // first CTA of the item; its CTAs, 0 where none is cut there (or it is the other end's)
+};
+template <int kWarps>
+__device__ __forceinline__ void find_ends(const DecodeParams& p, const Seq* seqs, int total, int each, BlockEnds& x) {
+  const int tid = threadIdx.x, U0 = min(total, static_cast<int>(blockIdx.x) * kWarps * each);
+  const int U1 = min(total, U0 + kWarps * each);
+  if (tid >= 2) return;
+  int first = 0, blocks = 0;
+  if (U0 < U1) {
+    const Place at = place_of(p, seqs, tid ? U1 - 1 : U0);
+    const int i1 = at.i0 + at.tiles - 1;
+    if (tid ? i1 >= U1 && at.i0 >= U0 : at.i0 < U0) {
+      first = at.i0 / (each * kWarps);
+      blocks = i1 / (each * kWarps) - first + 1;
+    }
+    x.at[tid] = at;
+  }
+  x.first[tid] = first;
+  x.blocks[tid] = blocks;
+}
+
 // By the whole block, at its end. Row r of warp w's kept segment lies at rows + w * warp_pitch + r * row_pitch
 // (floats). `offs`: [CTAs + 1] and `part`: [threads] of shared memory, clear of the kept rows.
 // With a shared prefix every item is left to the merge that follows, its partial results as above.
 template <typename T, int D, int kRows, int kWarps>
 __device__ __forceinline__ void join_items(const DecodeParams& p, const Seq* seqs, int total, int each,
-                                           const Kept<kRows, kWarps>& kept, const float* rows, int warp_pitch,
+                                           const Kept<kRows, kWarps>& kept, const BlockEnds& ends, const float* rows, int warp_pitch,
                                            int row_pitch, int* offs, Column* part) {
   constexpr int kThreads = 32 * kWarps, C4 = D / 4;
-  __shared__ Place ends[2];
   __shared__ int results[2];
   const int tid = threadIdx.x, cta = blockIdx.x, w_cta = cta * kWarps;
   const bool shared = p.pre.key_tiles > 0;
   const int U0 = min(total, w_cta * each), U1 = min(total, U0 + kWarps * each);
-  // The items that the block's range begins and ends inside of: at most one each, perhaps the same.
-  Place end;
-  int blocks = 0, first = 0;  // CTAs of the item, its first
-  if (tid < 2 && U0 < U1 && !shared) {
-    end = place_of(p, seqs, tid ? U1 - 1 : U0);
-    const int i1 = end.i0 + end.tiles - 1;
-    // cut at this end, and not the other end's item too
-    if (tid ? i1 >= U1 && end.i0 >= U0 : end.i0 < U0) {
-      first = end.i0 / (each * kWarps);
-      blocks = i1 / (each * kWarps) - first + 1;
-    }
-    ends[tid] = end;
-  }
   __syncthreads();
   // 1. The kept segments of each item.
 #pragma unroll 1
@@ -310,6 +326,7 @@ __device__ __forceinline__ void join_items(const DecodeParams& p, const Seq* seq
   // 2. Which of the block's cut items it brings the last part of, and where that item's parts lie.
   if (tid < 2) {
     int n = 0;
+    const int blocks = U0 < U1 ? ends.blocks[tid] : 0, first = ends.first[tid];
     if (blocks > 1) {
       __threadfence();
       if (static_cast<int>(atomicAdd(p.count + first, 1u)) + 1 == blocks) {
@@ -325,7 +342,7 @@ __device__ __forceinline__ void join_items(const DecodeParams& p, const Seq* seq
   for (int e = 0; e < 2; ++e) {
     const int nb = results[e];
     if (nb == 0) continue;
-    const Place& at = ends[e];
+    const Place& at = ends.at[e];
     const int i_end = at.i0 + at.tiles, w0 = at.i0 / each, w1 = (i_end - 1) / each, c0 = w0 / kWarps;
     const int n = nb + (w1 > (c0 + nb - 1) * kWarps && i_end < min(total, (w1 + 1) * each));
     for (int k = tid; k < n; k += kThreads)

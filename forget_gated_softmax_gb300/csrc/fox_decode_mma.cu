@@ -55,6 +55,9 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -64,25 +67,29 @@ __device__ __forceinline__ void cp_async_wait() {
 template <int D, int NT>
 struct MmaLayout {
   static constexpr int kWarps = D == 128 ? 4 : 8;
-  static constexpr int kMaxStages = 3;
+  // 128 KB on the way to an SM. A third stage measured no faster where bandwidth decides, and the SMs'
+  // shares of it less equal, so that the last finished later (one sequence of 65536: 52 against 49 us).
+  static constexpr int kStages = 2;
   static constexpr int kRows = 8 * NT;
   static constexpr int kTileBytes = kKeyTile * D * 2;  // K or V of a stage
   static constexpr int kOutStride = D + 4;             // a result row in shared memory, in floats
   static_assert(kRows * kOutStride * 4 <= 2 * kTileBytes, "results pass through a stage that was read");
 };
 
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Shared memory: K and V of every (warp, stage), then its gates, then the sequences' work offsets.
 // Gates of a stage: per sub-page (32 slots, or two of 16) [heads][slots + 4] sums, then [heads] bases.
 struct MmaShape {
-  int stages, heads, gpitch;  // heads of a row tile; floats from one head's sums to the next's
+  int heads, gpitch;          // heads of a row tile; floats from one head's sums to the next's
   int gsub, gstage;           // bytes of a sub-page's sums (a TMA destination: 128-byte steps); of a stage's gates
 };
 
-// Up to 32 successive key tiles of one item, and the page that lane i's tile lies in (with pages of 16
-// tokens, its two pages; -1: the second starts behind the sequence's end).
+// Up to 32 successive key tiles of one item. The table's entries for them (with pages of 16 tokens two a
+// tile) come to shared memory by asynchronous copies, so that no instruction waits for them before their use.
 struct Window {
-  int hkv, b, rt, tile, n;
-  int id0, id1;
+  int hkv, rt, tile, n;
+  bool half;  // the last tile's second page of 16 lies behind the sequence's end
 };
 
 template <int D, int NT>
@@ -94,14 +101,16 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   constexpr int W = L::kWarps;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int scratch[W];
-  __shared__ __align__(8) uint64_t bars[W][L::kMaxStages];
+  __shared__ __align__(8) uint64_t bars[W][L::kStages];
   __shared__ int abort_word;
   __shared__ Kept<L::kRows, W> kept;
+  __shared__ int ids[W][2][64];
+  __shared__ BlockEnds ends;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &abort_word;
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = x.stages;
+  constexpr int stages = L::kStages;
   uint8_t* ring = sm + warp * stages * (2 * L::kTileBytes);
   uint8_t* gates = sm + W * stages * (2 * L::kTileBytes) + warp * stages * x.gstage;
   Seq* seqs = reinterpret_cast<Seq*>(sm + W * stages * (2 * L::kTileBytes + x.gstage));
@@ -132,7 +141,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   float m[NT][2], l[NT][2];
   Gate2 ci[NT][2];
   int pos[NT][2], gidx[NT][2];
-  int pg[NT][2];
+  int pg[NT][2];  // table entries, as they are: nothing waits for them before `opened`
   // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
   const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   Place cur = {}, pro = {};
   if (count > 0) cur = pro = place_of(p, seqs, u0);
   Window now = {}, next = {};
-  int left = count, at = 0;  // units that no window holds yet; the producer's next tile of `now`
+  int left = count, at = 0, buf = 0;  // units that no window holds yet; the producer's next tile of `now`; now's ids
   bool fresh = true, opened = false, ok = true;
   int stage = 0;
   uint32_t phase = 0;
@@ -149,6 +158,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   // Step n consumes tile n and then issues the copies of tile n + stages; the first `stages` only issue.
 #pragma unroll 1
   for (int n = -stages; n < count; ++n) {
+    if (n == 0 && warp == 0) find_ends<W>(p, seqs, total, each, ends);  // while the first copies are on their way
     if (n >= 0) {
     if (!opened) {
       // The item's rows: their cumulative gates, and nothing summed yet.
@@ -160,7 +170,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
         for (int e = 0; e < 2; ++e) {
           ci[nt][e] = {-INFINITY, 0.f};  // an empty row's scores are -inf
           if (gidx[nt][e] >= 0)
-            ci[nt][e] = gate_sum(a, pg[nt][e], pos[nt][e] & (S - 1), h0 + gidx[nt][e]);
+            ci[nt][e] = gate_sum(a, checked_page(a, pg[nt][e]), pos[nt][e] & (S - 1), h0 + gidx[nt][e]);
           else
             gidx[nt][e] = 0;
           m[nt][e] = -INFINITY;
@@ -176,11 +186,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     uint8_t* st = ring + stage * (2 * L::kTileBytes);
     ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][stage], phase, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA));
     if (!ok) break;
-    // the stage's bases: the groups committed after this stage's are `stages - 1`
-    if (stages == 3)
-      cp_async_wait<2>();
-    else
-      cp_async_wait<1>();
+    cp_async_wait<L::kStages - 1>();  // the stage's bases: so many groups were committed after theirs
     __syncwarp();
 
     const int j0 = cur.tile * kKeyTile;
@@ -334,34 +340,6 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     }
     }
 
-    if (n + stages < count) {
-      // A window of the producer's next tiles, whose pages are read long before they are needed.
-      if (at == now.n) {
-        at = 0;
-#pragma unroll 1
-        do {
-          now = next;
-          next.n = 0;
-          if (left > 0) {
-            next.hkv = pro.hkv;
-            next.b = pro.b;
-            next.rt = pro.rt;
-            next.tile = pro.tile;
-            next.n = min(min(32, pro.tiles - pro.tile), left);
-            next.id0 = 0;
-            next.id1 = -1;
-            if (lane < next.n) {
-              const int j = (pro.tile + lane) * kKeyTile;
-              next.id0 = own_page_or_0(a, pro.b, j);
-              if (S == 16 && j + 16 < pro.s.own) next.id1 = own_page_or_0(a, pro.b, j + 16);
-            }
-            left -= next.n;
-            pro.tile += next.n;
-            if (pro.tile == pro.tiles && left > 0) next_item(p, seqs, pro);
-          }
-        } while (now.n == 0);
-      }
-    }
     if (fresh && n + 1 < count) {
       // The next item's rows: Q fragments (row g8 of each eight), and the pages of this thread's columns of
       // S^T, rows 2 t4 and 2 t4 + 1.
@@ -375,7 +353,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
           const bool here = t < cur.s.n && g < G;
           pos[nt][e] = cur.s.own - cur.s.n + t;
           gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : -1;
-          pg[nt][e] = here ? own_page_or_0(a, cur.b, pos[nt][e]) : 0;
+          pg[nt][e] = here ? a.table[(size_t)cur.b * a.table_stride + (pos[nt][e] >> a.page_shift)] : 0;
         }
         const int r = r0 + nt * 8 + g8, t = token_of(p, r), g = r - t * Gp;
         const bool in = t < cur.s.n && g < G;
@@ -389,19 +367,49 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
       }
     }
     if (n + stages < count) {
+      // A window of the producer's next tiles, whose pages are read long before they are needed.
+      if (at == now.n) {
+        at = 0;
+#pragma unroll 1
+        do {
+          now = next;
+          buf ^= 1;
+          cp_async_wait_all();  // now's ids; they were asked for a window ago
+          __syncwarp();
+          next.n = 0;
+          if (left > 0) {
+            next.hkv = pro.hkv;
+            next.rt = pro.rt;
+            next.tile = pro.tile;
+            next.n = min(min(32, pro.tiles - pro.tile), left);
+            const int last = (next.tile + next.n) * kKeyTile;
+            next.half = last - 16 >= pro.s.own;
+            const int* row = a.table + (size_t)pro.b * a.table_stride;
+            if (lane < next.n) {
+              const int j = (pro.tile + lane) * kKeyTile;
+              cp_async4(smem_u32(&ids[warp][buf ^ 1][lane]), row + (j >> a.page_shift));
+              if (S == 16 && j + 16 < pro.s.own) cp_async4(smem_u32(&ids[warp][buf ^ 1][32 + lane]), row + (j >> 4) + 1);
+            }
+            left -= next.n;
+            pro.tile += next.n;
+            if (pro.tile == pro.tiles && left > 0) next_item(p, seqs, pro);
+          }
+        } while (now.n == 0);
+      }
+    }
+    if (n + stages < count) {
       // Copies of the producer's next tile; the stage is the one just read, and in the first steps the n-th.
       const int to = n < 0 ? n + stages : (stage == 0 ? stages : stage) - 1;
-      const int id0 = __shfl_sync(0xffffffffu, now.id0, at), id1 = __shfl_sync(0xffffffffu, now.id1, at);
       uint8_t* dst = ring + to * (2 * L::kTileBytes);
       uint8_t* sg = gates + to * x.gstage;
       const int h0 = now.hkv * G + (G > L::kRows ? now.rt * p.Rt % Gp : 0);
       const int slot = S == 16 ? 0 : (now.tile + at) * kKeyTile & (S - 1);
-      const int subs = id1 >= 0 ? 2 : 1;
+      const int subs = S == 16 && !(now.half && at + 1 == now.n) ? 2 : 1;
       if (lane == 0) mbar_arrive_expect_tx(&bars[warp][to], subs * (2 * KS * D * 2 + heads * gpitch * 4));
       __syncwarp();
 #pragma unroll 1
       for (int i = 0; i < subs; ++i) {
-        const int id = i ? id1 : id0;
+        const int id = checked_page(a, ids[warp][buf][32 * i + at]);
         // One lane a copy: K and V of 64 channels each, and the gates.
         if (lane < D / 32) {
           const int y = lane >> 1;
@@ -420,13 +428,13 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   if (!ok) {
     // A wait gave up: every copy issued must still land before shared memory is used or released.
     for (int s = 0; s < stages; ++s) mbar_wait_drain(&bars[warp][s], s < stage ? phase ^ 1 : phase);
-    cp_async_wait<0>();
+    cp_async_wait_all();
   }
   clear_idle_rows<__nv_bfloat16, D>(p, seqs);
   // Sums and offsets stand in the first and the second warp's second stage.
   const int warp_bytes = stages * (2 * L::kTileBytes);
   static_assert(32 * W * sizeof(Column) <= 2 * L::kTileBytes && (kSMs + 1) * 4 <= 2 * L::kTileBytes, "they fit there");
-  join_items<__nv_bfloat16, D, L::kRows, W>(p, seqs, total, each, kept, reinterpret_cast<const float*>(sm),
+  join_items<__nv_bfloat16, D, L::kRows, W>(p, seqs, total, each, kept, ends, reinterpret_cast<const float*>(sm),
                                             warp_bytes / 4, L::kOutStride,
                                             reinterpret_cast<int*>(sm + warp_bytes + 2 * L::kTileBytes),
                                             reinterpret_cast<Column*>(sm + 2 * L::kTileBytes));
@@ -446,13 +454,11 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
   x.gsub = (x.heads * x.gpitch * 4 + 127) / 128 * 128;
   x.gstage = subs * x.gsub + (subs * x.heads * 8 + 127) / 128 * 128;
   constexpr int kMostGates = 2 * ((L::kRows * 20 * 4 + 127) / 128 * 128) + 256;
-  constexpr size_t kMost = 232448 - 4096;  // of an SM's shared memory, less the static part
+  constexpr size_t kMost = 232448 - 6144;  // of an SM's shared memory, less the static part
   const size_t fixed = 1024 + sizeof(Seq) * ((size_t)p.a.B + 1);
   const size_t one = (size_t)L::kWarps * (2 * L::kTileBytes + x.gstage);
-  // Three stages where they fit beside the gates and the sequences' offsets.
-  x.stages = fixed + 3 * one <= kMost ? 3 : 2;
-  const size_t smem = fixed + x.stages * one;
-  static_assert(1024 + sizeof(Seq) * (kMaxSeqs + 1) + 2 * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
+  const size_t smem = fixed + L::kStages * one;
+  static_assert(1024 + sizeof(Seq) * (kMaxSeqs + 1) + L::kStages * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
