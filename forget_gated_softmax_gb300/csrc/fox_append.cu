@@ -11,9 +11,7 @@
 // are a warp scan that goes on from the page's last held value; a page that opens in this call
 // takes its base from the page before.
 //
-// Bound by memory: each of k, v (q) read once and written once. One thread makes one 16-byte chunk
-// of the output; a rotated chunk reads its partner chunk as well, which another thread of the warp
-// has in L1.
+// Bound by memory: each of k, v (q) read once and written once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,7 +36,7 @@ struct AppendParams {
   const float* cos;
   const float* sin;
   int max_pos, rot, pairs;
-  int copy_blocks, blocks_per_row;  // blocks [0, copy_blocks) copy, the others scan gates
+  int copy_blocks;                  // blocks [0, copy_blocks) copy, the others scan gates
   int page_chunks, head_groups;     // gate block: (sequence, page chunk, head group)
   int scan_bases;                   // bases of pages after a sequence's first are left to base_scan_kernel
 };
@@ -75,82 +73,126 @@ struct Vec<float> {
   }
 };
 
-// The chunk of channels [c, c + kN) of one head, rotated. `src` points at the head's channel 0.
+// Work of the copy: units of two 16-byte chunks of one head of a row, (k, v, q heads) x (chunk pairs). A
+// pair is a channel range and its partner in the rotation, so that each chunk is read once; channels that
+// are not rotated, or whose partners are in the same chunk, go in neighbouring pairs.
+__device__ __forceinline__ void pair_of(int j, int rot_chunks, bool apart, int* c0, int* c1) {
+  const bool turned = apart && 2 * j < rot_chunks;
+  *c0 = turned ? j : 2 * j;
+  *c1 = turned ? j + rot_chunks / 2 : 2 * j + 1;
+}
+
+// Rotates two chunks (x at channel c0, y at c1 of the head).
 template <typename T>
-__device__ __forceinline__ uint4 turned_chunk(const T* src, int c, const float* cs, const float* sn, int rot,
-                                              int pairs) {
+__device__ __forceinline__ void turn(uint4& wx, uint4& wy, int c0, int c1, const float* cs, const float* sn, int rot,
+                                     int pairs) {
   constexpr int kN = Vec<T>::kN;
-  const uint4 w = *reinterpret_cast<const uint4*>(src + c);
-  if (c >= rot) return w;
-  float x[kN], y[kN];
-  Vec<T>::unpack(w, x);
+  if (c0 >= rot) return;
+  float x[kN], y[kN], u[kN], v[kN];
+  Vec<T>::unpack(wx, x);
+  Vec<T>::unpack(wy, y);
   if (pairs) {
 #pragma unroll
     for (int i = 0; i < kN; i += 2) {
-      const float co = cs[(c + i) / 2], si = sn[(c + i) / 2];
-      y[i] = x[i] * co - x[i + 1] * si;
-      y[i + 1] = x[i + 1] * co + x[i] * si;
+      const float ca = cs[(c0 + i) / 2], sa = sn[(c0 + i) / 2], cb = cs[(c1 + i) / 2], sb = sn[(c1 + i) / 2];
+      u[i] = x[i] * ca - x[i + 1] * sa;
+      u[i + 1] = x[i + 1] * ca + x[i] * sa;
+      v[i] = y[i] * cb - y[i + 1] * sb;
+      v[i + 1] = y[i + 1] * cb + y[i] * sb;
     }
   } else {
-    const int half = rot / 2;
-    const bool low = c < half;
-    float p[kN];
-    Vec<T>::unpack(*reinterpret_cast<const uint4*>(src + (low ? c + half : c - half)), p);
-    const int a0 = low ? c : c - half;
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
-      const float4 co = *reinterpret_cast<const float4*>(cs + a0 + i);
-      const float4 si = *reinterpret_cast<const float4*>(sn + a0 + i);
+      const float4 co = *reinterpret_cast<const float4*>(cs + c0 + i);
+      const float4 si = *reinterpret_cast<const float4*>(sn + c0 + i);
       const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[i + j] = x[i + j] * cc[j] + (low ? -p[i + j] : p[i + j]) * ss[j];
+      for (int j = 0; j < 4; ++j) {
+        u[i + j] = x[i + j] * cc[j] - y[i + j] * ss[j];
+        v[i + j] = y[i + j] * cc[j] + x[i + j] * ss[j];
+      }
     }
   }
-  return Vec<T>::pack(y);
+  wx = Vec<T>::pack(u);
+  wy = Vec<T>::pack(v);
 }
 
-template <typename T>
-__device__ __forceinline__ void copy_row(const AppendParams& p) {
-  constexpr int kN = Vec<T>::kN;
+// Where a row's copies go.
+struct RowPlace {
+  int page, slot, pos;  // page -1: the row is not appended
+};
+
+__device__ __forceinline__ RowPlace row_place(const AppendParams& p, int row) {
   const PagedArgs& a = p.a;
-  const int row = blockIdx.x / p.blocks_per_row, part = blockIdx.x % p.blocks_per_row;
+  RowPlace x = {-1, 0, 0};
   const int b = seq_of_row(a, row);
-  if (b < 0) return;
+  if (b < 0) return x;
   bool bad;
   const SeqInfo s = seq_info(a, b, &bad);
-  if (bad || row < s.row0 || row >= s.row0 + s.n) {
-    if (bad && threadIdx.x == 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
-    return;
+  if (!bad && row >= s.row0 && row < s.row0 + s.n && s.own >= 0) {
+    const int own = s.own - s.n + (row - s.row0);
+    x.page = own_page(a, b, own);
+    x.slot = own & (a.page_size - 1);
+    x.pos = a.prefix_len + own;
+    bad = x.page < 0 || (p.rot > 0 && x.pos >= p.max_pos);
+    if (bad) x.page = -1;
   }
-  if (s.own < 0) return;  // idle
-  const int own = s.own - s.n + (row - s.row0);
-  const int page = own_page(a, b, own), slot = own % a.page_size;
-  const int pos = a.prefix_len + own;
-  const bool no_page = page < 0, no_pos = p.rot > 0 && pos >= p.max_pos;
-  if (no_page || no_pos) {
-    if (threadIdx.x == 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
-    return;
-  }
-  const int ch = a.d / kN;  // chunks of a head
-  const int nk = a.Hkv * ch, nq = p.qn ? a.H * ch : 0;
-  const float* cs = p.rot ? p.cos + (size_t)pos * (p.rot / 2) : nullptr;
-  const float* sn = p.rot ? p.sin + (size_t)pos * (p.rot / 2) : nullptr;
-  const T* kn = static_cast<const T*>(p.kn) + (size_t)row * p.k_stride;
-  const T* vn = static_cast<const T*>(p.vn) + (size_t)row * p.v_stride;
-  for (int u = part * kThreads + threadIdx.x; u < 2 * nk + nq; u += p.blocks_per_row * kThreads) {
-    if (u < 2 * nk) {
-      const int w = u < nk ? u : u - nk, h = w / ch, c = (w % ch) * kN;
-      T* dst = static_cast<T*>(u < nk ? a.k : a.v) + kv_offset(a, page, h, slot) + c;
-      const T* src = (u < nk ? kn : vn) + (size_t)h * a.d;
-      const uint4 val = u < nk ? turned_chunk<T>(src, c, cs, sn, p.rot, p.pairs)
-                               : *reinterpret_cast<const uint4*>(src + c);
-      *reinterpret_cast<uint4*>(dst) = val;
-    } else {
-      const int w = u - 2 * nk, h = w / ch, c = (w % ch) * kN;
-      const T* src = static_cast<const T*>(p.qn) + (size_t)row * p.q_stride + (size_t)h * a.d;
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.qo) + ((size_t)row * a.H + h) * a.d + c) =
-          turned_chunk<T>(src, c, cs, sn, p.rot, p.pairs);
+  if (bad && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
+  return x;
+}
+
+constexpr int kUnits = 4;                  // units of a thread, their loads in flight together
+constexpr int kBlockRows = kThreads * kUnits / 8 + 2;  // most rows that a block's units touch (8 a row at least)
+
+// A block's units lie side by side on the line of all rows' units. The loads of k, v, q need only that; they
+// are asked for first, and the look-ups of the rows' pages and positions run meanwhile.
+template <typename T>
+__device__ __forceinline__ void copy_units(const AppendParams& p, RowPlace* places) {
+  constexpr int kN = Vec<T>::kN;
+  const PagedArgs& a = p.a;
+  const int hs = (kN == 8 ? 2 : 3) + (a.d == 128), hp = 1 << hs;  // units of a head
+  const int nk = a.Hkv * hp, per_row = 2 * nk + (p.qn ? a.H * hp : 0);
+  const long long first = (long long)blockIdx.x * (kThreads * kUnits);
+  const int row0 = first < 0x7fffffffLL ? static_cast<int>(first) / per_row : static_cast<int>(first / per_row);
+  const int off = static_cast<int>(first - (long long)row0 * per_row);
+  const int rot_chunks = p.rot / kN;
+  uint4 x[kUnits], y[kUnits];
+  int row[kUnits], at[kUnits];  // at: the unit in its row
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int u = off + i * kThreads + threadIdx.x;
+    row[i] = u / per_row;
+    at[i] = u - row[i] * per_row;
+    const int w = at[i] < nk ? at[i] : at[i] < 2 * nk ? at[i] - nk : at[i] - 2 * nk;
+    int c0, c1;
+    pair_of(w & (hp - 1), at[i] >= nk && at[i] < 2 * nk ? 0 : rot_chunks, !p.pairs, &c0, &c1);
+    const bool is_v = at[i] >= nk && at[i] < 2 * nk, is_q = at[i] >= 2 * nk;
+    const T* src = static_cast<const T*>(is_q ? p.qn : is_v ? p.vn : p.kn) +
+                   (size_t)(row0 + row[i]) * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) + (size_t)(w >> hs) * a.d;
+    if (row0 + row[i] < a.rows) {
+      x[i] = __ldcs(reinterpret_cast<const uint4*>(src + c0 * kN));
+      y[i] = __ldcs(reinterpret_cast<const uint4*>(src + c1 * kN));
     }
+  }
+  const int rows = min((off + kThreads * kUnits - 1) / per_row + 1, a.rows - row0);
+  for (int r = threadIdx.x; r < rows; r += kThreads) places[r] = row_place(p, row0 + r);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (row0 + row[i] >= a.rows) continue;
+    const RowPlace g = places[row[i]];
+    if (g.page < 0) continue;
+    const bool is_v = at[i] >= nk && at[i] < 2 * nk, is_q = at[i] >= 2 * nk;
+    const int w = is_q ? at[i] - 2 * nk : is_v ? at[i] - nk : at[i], h = w >> hs;
+    int c0, c1;
+    pair_of(w & (hp - 1), is_v ? 0 : rot_chunks, !p.pairs, &c0, &c1);
+    if (!is_v && p.rot)
+      turn<T>(x[i], y[i], c0 * kN, c1 * kN, p.cos + (size_t)g.pos * (p.rot / 2), p.sin + (size_t)g.pos * (p.rot / 2), p.rot,
+              p.pairs);
+    T* dst = is_q ? static_cast<T*>(p.qo) + ((size_t)(row0 + row[i]) * a.H + h) * a.d
+                  : static_cast<T*>(is_v ? a.v : a.k) + kv_offset(a, g.page, h, g.slot);
+    *reinterpret_cast<uint4*>(dst + c0 * kN) = x[i];
+    *reinterpret_cast<uint4*>(dst + c1 * kN) = y[i];
   }
 }
 
@@ -287,12 +329,15 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams p) {
-  __shared__ float zs[128][kGateHeads + 1];
+  __shared__ union {
+    float zs[128][kGateHeads + 1];
+    RowPlace places[kBlockRows];
+  } sh;
   grid_dep_trigger();
   if (static_cast<int>(blockIdx.x) < p.copy_blocks)
-    copy_row<T>(p);
+    copy_units<T>(p, sh.places);
   else
-    gate_block(p, zs);
+    gate_block(p, sh.zs);
 }
 
 // Bases of the pages after a sequence's first one: base_k = base_0 + sum of the full pages' sums.
@@ -314,28 +359,36 @@ __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams 
   if (id0 < 0) return;  // reported by its gate block
   const float2 base0 = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, id0, h));
   double carry = static_cast<double>(base0.x) + base0.y;
-  for (int k = p0 + 1; k <= pl; k += 32) {
-    const int kk = k + lane;
-    const bool in = kk <= pl;
-    const int prev = in ? own_page(a, b, (kk - 1) * S) : -1, id = in ? own_page(a, b, kk * S) : -1;
-    double x = prev >= 0 ? static_cast<double>(a.g[g_offset(a, prev, h, S - 1)]) : 0.0;
+  constexpr int kSteps = 4;  // of 32 pages, their loads in flight together
+  for (int k = p0 + 1; k <= pl; k += 32 * kSteps) {
+    float full[kSteps];
+    int id[kSteps];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    for (int i = 0; i < kSteps; ++i) {
+      const int kk = k + 32 * i + lane;
+      const int prev = kk <= pl ? own_page(a, b, (kk - 1) * S) : -1;
+      id[i] = kk <= pl ? own_page(a, b, kk * S) : -1;
+      full[i] = prev >= 0 ? a.g[g_offset(a, prev, h, S - 1)] : 0.f;
     }
-    if (id >= 0) put_base(a.gbase, gbase_offset(a, id, h), carry + x);
-    carry += __shfl_sync(0xffffffffu, x, 31);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      double x = full[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (id[i] >= 0) put_base(a.gbase, gbase_offset(a, id[i], h), carry + x);
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
   }
 }
 
 template <typename T>
 cudaError_t launch(AppendParams p, cudaStream_t s) {
   const PagedArgs& a = p.a;
-  const int units = (2 * a.Hkv + (p.qn ? a.H : 0)) * (a.d / Vec<T>::kN);
-  // Up to four chunks a thread: fewer leave the row's index look-up standing out.
-  p.blocks_per_row = ceil_div(units, 4 * kThreads);
-  const long long copy = (long long)a.rows * p.blocks_per_row;
+  const long long units = (long long)a.rows * ((2 * a.Hkv + (p.qn ? a.H : 0)) * (a.d / Vec<T>::kN / 2));
+  const long long copy = (units + kThreads * kUnits - 1) / (kThreads * kUnits);
   p.page_chunks = ceil_div(a.max_new, a.page_size) + 1;
   p.head_groups = ceil_div(a.H, kGateHeads);
   p.scan_bases = a.max_new > a.page_size;

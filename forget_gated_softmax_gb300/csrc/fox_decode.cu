@@ -190,17 +190,22 @@ __global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel
   join_items<float, D, kSimtRows, kSimtWarps>(p, seqs, total, each, kept, ends, &qs[0][0][0], kSimtRows * D, D, offs, part);
 }
 
-// One output row by one warp: the partial results of its own item and of the shared prefix joined, in the
-// workers' order. One warp a (row, query head).
+// One output row (query row, query head): the partial results of its own item and of the shared prefix
+// joined, in a fixed order, by one warp, or with few rows (deal = kMergeWarps) by a block's warps, which
+// deal them out. What bounds it is latency: a row has up to some dozens of results of 4 d bytes.
 constexpr int kMergeWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __grid_constant__ DecodeParams p,
+                                                                       const int deal) {
   constexpr int E = D / 32;
   const PagedArgs& a = p.a;
-  const int id = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  __shared__ float sums[kMergeWarps][D];
+  __shared__ float2 mls[kMergeWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int id = deal > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + warp, part = deal > 1 ? warp : 0;
   const int row = id / a.H, h = id - row * a.H;
-  if (row >= a.rows) return;
+  if (row >= a.rows) return;  // whole blocks where the warps deal
   // What the call was given may be read before the kernels ahead are through.
   const int b = seq_of_row(a, row);
   if (b < 0) return;
@@ -208,20 +213,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
   const SeqInfo s = seq_info(a, b, &bad);
   if (bad || row < s.row0 || row >= s.row0 + s.n || s.own < 0) return;  // idle rows are written already
   const int G = a.H / a.Hkv, hkv = h / G, hl = h - hkv * G;
-  const int pos = s.own - s.n + (row - s.row0);
-  const int last = a.prefix_len - 1, lpage = max(prefix_page(a, last), 0);
-  const Gate2 ci = gate_sum(a, own_page_or_0(a, b, pos), pos % a.page_size, h);
-  const Gate2 cl = gate_sum(a, lpage, last % a.page_size, h);
+  const int pos = s.own - s.n + (row - s.row0), last = a.prefix_len - 1, mask = a.page_size - 1;
+  const Gate2 ci = gate_sum(a, own_page_or_0(a, b, pos), pos & mask, h);
+  const Gate2 cl = gate_sum(a, max(prefix_page(a, last), 0), last & mask, h);
   const float shift = ((ci.hi - cl.hi) + (ci.lo - cl.lo)) * kLog2e;  // what the row's prefix scores lack
   // The prefix's partial results: of result i, ml and po lie `step` rows further on.
   const PrefixPlan& x = p.pre;
   const int tile = row / x.tpt * x.head_chunks + hl / x.hp;
   const bool both = x.row_tiles == 1;  // the streams are two results, else this row is one stream's
   const int item = hkv * x.items + (both ? 0 : tile / 2);
-  const int peach = units_per_worker(a.Hkv * x.items * x.key_tiles, x.workers);
-  const int v0 = item * x.key_tiles / peach, v1 = ((item + 1) * x.key_tiles - 1) / peach;
+  const int v0 = item * x.line / x.each, v1 = (item * x.line + x.key_tiles - 1) / x.each;
   const int n_pre = (v1 - v0 + 1) * (both ? 2 : 1), step = both ? kTile : 2 * kTile;
-  const size_t pre0 = ((size_t)(v0 + item) * 2 + (both ? 0 : tile & 1)) * kTile + row % x.tpt * x.hp + hl % x.hp;
+  const size_t pre0 = ((size_t)(v0 + item) * 2 + (both ? 0 : tile & 1)) * kTile + hl % x.hp * x.tpt + row % x.tpt;
   grid_dep_wait();
   const int tiles = ceil_div(s.own, kKeyTile), r = (row - s.row0) * p.Gp + hl, rt = r / p.Rt;
   const int per_head = __ldcg(p.cum + a.B), each = units_per_worker(per_head * a.Hkv, p.workers);
@@ -232,10 +235,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
   const int n = n_own + n_pre, own0 = ((hkv * a.B + b) * p.RTmax + rt) * p.Rs + r - rt * p.Rt;
   float m = -INFINITY, l = 0.f, acc[E] = {};
 #pragma unroll 1
-  for (int first = 0; first < n; first += 32) {
-    // lane i: where result first + i lies, its maximum and sum
-    const int i = first + lane;
-    const float* src = p.po;
+  for (int first = 0; first < n; first += 32 * deal) {
+    // lane i: where this warp's i-th result lies, its maximum and sum
+    const int i = first + lane * deal + part;
+    const float* src = nullptr;
     float2 ml = make_float2(-INFINITY, 0.f);
     if (i < n_own) {
       const int at = own0 + (i == 0 ? w0 : i < nb ? (c0 + i) * p.warps : w1) * p.Rs;
@@ -257,43 +260,73 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     l = l * alpha + ml.y * wgt;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= alpha;
-    // Of a result without weight (a stream without keys wrote no sums of V) a written one is read instead.
-    const unsigned has = __ballot_sync(0xffffffffu, wgt != 0.f);
-    if (has == 0) continue;
-    unsigned long long addr = reinterpret_cast<unsigned long long>(src);
-    addr = wgt != 0.f ? addr : 0ull;
-    const unsigned long long some = __shfl_sync(0xffffffffu, addr, __ffs(has) - 1);
-    if (addr == 0ull) addr = some;
-    const int c = min(32, n - first);
-#pragma unroll 8
-    for (int j = 0; j < c; ++j) {
-      const float f = __shfl_sync(0xffffffffu, wgt, j);
-      const float2* y = reinterpret_cast<const float2*>(__shfl_sync(0xffffffffu, addr, j)) + lane * (E / 2);
+    // A result without weight is not read: a stream without keys wrote no sums of V.
+    unsigned has = __ballot_sync(0xffffffffu, wgt != 0.f);
+#pragma unroll 1
+    while (has) {
+      constexpr int kBatch = 8;  // results whose loads are in flight together
+      float2 z[kBatch][E / 2];
+      float f[kBatch];
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const float2 z = __ldcg(y + e);
-        acc[2 * e] = fmaf(f, z.x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(f, z.y, acc[2 * e + 1]);
+      for (int j = 0; j < kBatch; ++j) {
+        const int k = has ? __ffs(has) - 1 : 0;
+        f[j] = has ? __shfl_sync(0xffffffffu, wgt, k) : 0.f;
+        const float* at = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+          z[j][e] = has ? __ldcg(reinterpret_cast<const float2*>(at + lane * E) + e) : make_float2(0.f, 0.f);
+        has &= has - 1;
       }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          acc[2 * e] = fmaf(f[j], z[j][e].x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(f[j], z[j][e].y, acc[2 * e + 1]);
+        }
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] *= inv;
+  for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[e];
+  if (lane == 0) mls[warp] = make_float2(m, l);
+  if (deal > 1)
+    __syncthreads();
+  else
+    __syncwarp();
+  // Two channels a thread; with one warp a row, its lanes take them in turn.
+#pragma unroll 1
+  for (int ch = (deal > 1 ? threadIdx.x : lane) * 2; ch < D; ch += 64 * deal) {
+  const int w0_ = deal > 1 ? 0 : warp, w1_ = deal > 1 ? kMergeWarps : warp + 1;
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int w = w0_; w < w1_; ++w) top = fmaxf(top, mls[w].x);
+  const float safe = top == -INFINITY ? 0.f : top;
+  float o0 = 0.f, o1 = 0.f, sum = 0.f;
+#pragma unroll 1
+  for (int w = w0_; w < w1_; ++w) {
+    const float t = ex2_approx(mls[w].x - safe);
+    o0 = fmaf(t, sums[w][ch], o0);
+    o1 = fmaf(t, sums[w][ch + 1], o1);
+    sum = fmaf(t, mls[w].y, sum);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const size_t at = (size_t)row * a.H + h;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + at * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(acc[e], acc[e + 1]);
-  if (lane == 0) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch) = pack_bf16x2(o0 * inv, o1 * inv);
+  if (ch == 0) p.lse[at] = sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+  }
 }
 
 template <int D>
 cudaError_t launch_merge(const DecodeParams& p, cudaStream_t s) {
   TraceScope trace("decode_merge", s);
-  const cudaError_t e = launch_dependent(prefix_merge_kernel<D>, dim3(ceil_div(p.a.rows * p.a.H, kMergeWarps)),
-                                         dim3(32 * kMergeWarps), 0, s, p);
+  // Dealing pays while its blocks are on the SMs at once (32 x 32 rows: 17 -> 12 us; 256 x 32: 21 -> 37 us).
+  const int rows = p.a.rows * p.a.H, deal = rows <= kSMs * 12 ? kMergeWarps : 1;
+  const cudaError_t e =
+      launch_dependent(prefix_merge_kernel<D>, dim3(deal > 1 ? rows : ceil_div(rows, kMergeWarps)),
+                       dim3(32 * kMergeWarps), 0, s, p, deal);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -347,7 +380,7 @@ bool decode_fits(const PagedArgs& a, bool f32) {
   const DecodeLayout L = decode_layout(a, f32);
   return most_units(a, L.Rt, L.Gp) < 0x7fffffffLL - L.workers &&
          (unsigned long long)a.max_new * L.Gp * L.Gp < (1ull << 32) && L.po_rows < 0x7fffffffLL &&
-         (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.key_tiles < 0x7fffffffLL - L.pre.workers);
+         (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.line < 0x7fffffffLL - L.pre.each);
 }
 
 size_t decode_workspace_bytes(const PagedArgs& a, bool f32) { return decode_layout(a, f32).end; }

@@ -13,11 +13,12 @@ namespace fox {
 // Work on the shared prefix (fox_prefix.cu).
 struct PrefixPlan {
   int hp, head_chunks;  // query heads of a row tile; such chunks of a key head's group
-  int tpt;              // tokens of a row tile: its row r is token r / hp, head r % hp
+  int tpt;              // tokens of a row tile: its row r is head r / tpt, token r % tpt
   int row_tiles;        // of one key head: token blocks x head chunks, the chunks of a block side by side
   int items;            // of one key head: pairs of row tiles, or the only row tile
   int kap_tiles;        // gate terms of a stage: one set, or one a row tile
   int key_tiles;        // 0: no shared prefix
+  int line, each;       // units of an item on the work line (its key tiles, then perhaps empty ones); of a CTA
   int workers;
   float2* ml;           // [(worker + item) * 2 + stream][128] maximum (against c_last) and sum
   float* po;            // [(worker + item) * 2 + stream][128][d]

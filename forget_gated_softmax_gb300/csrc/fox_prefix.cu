@@ -7,21 +7,22 @@
 // instead of once a sequence. The rows leave unnormalised partial results, which the merge joins with
 // those of the sequences' own keys; the row's c_i - c_last enters there.
 //
-// A row tile is `tpt` tokens x `hp` query heads of the key head's group: rows are (token, head), one
-// TMA box. Key tiles of an item (key head, row tiles) run from the last to the first: the bias falls
+// A row tile is `hp` query heads of the key head's group x `tpt` tokens: row r is head r / tpt, token
+// r % tpt, so that most warps' rows have one head and read its gate terms by one address. Key tiles of an item (key head, row tiles) run from the last to the first: the bias falls
 // with distance, so the first tile nearly always holds the row maximum. Work is split like the own
 // keys' (fox_paged.h): the items' key tiles on one line, equal ranges of it to the CTAs, one CTA an SM.
 //
 // Two streams of softmax warps share the tensor core, each with its S and O in tensor memory:
 //   more than one row tile a key head: an item is two row tiles, one a stream, on the same key tiles;
 //   one row tile: the streams take alternate key tiles, and leave a partial result each.
+// A stream's P goes to the tensor core in two halves of 64 keys, so that one half's P V runs during the
+// other's softmax.
 // Warp roles (384 threads): warps 0-3 and 4-7 the streams' softmax (thread = row = TMEM lane), warp 8
-// TMA producer, warp 9 TMEM allocator and MMA issuer, warps 10-11 the gates: log2 e (c_j - c_last) of
-// a key tile's keys and the row tile's heads into shared memory, alternate key tiles.
+// loads Q and K, warp 9 allocates TMEM and issues the MMAs, warps 10-11 load V and make the gate terms
+// log2 e (c_j - c_last) of a key tile's keys and the row tile's heads, a stage each.
 //
 // P V: P = hi + lo in bf16, two products (see fox_decode_mma.cu). A 32-column chunk of S, once read,
-// takes its own 16 columns of hi and 16 of lo, so P needs no memory beside S; the row maximum is
-// found in a pass of its own, because S is gone after the second.
+// takes its own 16 columns of hi and 16 of lo, so P needs no memory beside S.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -53,85 +54,14 @@ enum PBar {
   P_GFULL = 9,   // +stage: the key tile's gate terms (and the tail of V) are in place
   P_GEMPTY = 11,
   P_SFULL = 13,  // +stream
-  P_PFULL = 15,
-  P_OFINAL = 17,
-  P_DONE = 19,
-  P_COUNT = 20,
+  P_OFINAL = 15,
+  P_PFULL = 17,  // +2 stream + half
+  P_PVDONE = 21,
+  P_DONE = 25,
+  P_COUNT = 26,
 };
 
-// Row maximum of x_j = scale2 S_j - kap_j; columns from `lim` on are not keys.
-template <bool kTail>
-__device__ __forceinline__ float row_top(uint32_t tS, const float* kap, float scale2, int lim) {
-  const float2 nsc = make_float2(-scale2, -scale2);
-  float mn = INFINITY;  // min of kap_j - scale2 S_j
-  uint32_t rawb[2][32];
-  tmem_ld32(tS, rawb[0]);
-#pragma unroll
-  for (int qt = 0; qt < 4; ++qt) {
-    tmem_ld_wait();
-    if (qt + 1 < 4) tmem_ld32(tS + 32 * (qt + 1), rawb[(qt + 1) & 1]);
-    const uint32_t* raw = rawb[qt & 1];
-#pragma unroll
-    for (int j4 = 0; j4 < 8; ++j4) {
-      const int j = 32 * qt + 4 * j4;
-      const float4 kk = lds_f4(kap + j);
-      float2 a = ffma2(make_float2(__uint_as_float(raw[4 * j4]), __uint_as_float(raw[4 * j4 + 1])), nsc,
-                       make_float2(kk.x, kk.y));
-      float2 c = ffma2(make_float2(__uint_as_float(raw[4 * j4 + 2]), __uint_as_float(raw[4 * j4 + 3])), nsc,
-                       make_float2(kk.z, kk.w));
-      if (kTail) {
-        if (j >= lim) a.x = INFINITY;
-        if (j + 1 >= lim) a.y = INFINITY;
-        if (j + 2 >= lim) c.x = INFINITY;
-        if (j + 3 >= lim) c.y = INFINITY;
-      }
-      mn = fmin3(fmin3(mn, a.x, a.y), c.x, c.y);
-    }
-  }
-  return -mn;
-}
-
-// P_j = 2^(x_j - off) over the row's S: chunk q's hi to columns 32 q .. 32 q + 15, lo to the next 16
-// (two columns of P a 32-bit column). Returns the sum of the P_j, in fp32.
-template <bool kTail>
-__device__ __forceinline__ float row_exp(uint32_t tS, const float* kap, float scale2, float off, int lim) {
-  const float2 nsc = make_float2(-scale2, -scale2), noff = make_float2(-off, -off);
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int qt = 0; qt < 4; ++qt) {
-    uint32_t raw[32];
-    tmem_ld32(tS + 32 * qt, raw);
-    tmem_ld_wait();
-    uint32_t pk[32];
-#pragma unroll
-    for (int j4 = 0; j4 < 8; ++j4) {
-      const int j = 32 * qt + 4 * j4;
-      const float4 kk = lds_f4(kap + j);
-      float2 wa = fsub2(noff, ffma2(make_float2(__uint_as_float(raw[4 * j4]), __uint_as_float(raw[4 * j4 + 1])), nsc,
-                                    make_float2(kk.x, kk.y)));
-      float2 wc = fsub2(noff, ffma2(make_float2(__uint_as_float(raw[4 * j4 + 2]), __uint_as_float(raw[4 * j4 + 3])),
-                                    nsc, make_float2(kk.z, kk.w)));
-      if (kTail) {
-        if (j >= lim) wa.x = -INFINITY;
-        if (j + 1 >= lim) wa.y = -INFINITY;
-        if (j + 2 >= lim) wc.x = -INFINITY;
-        if (j + 3 >= lim) wc.y = -INFINITY;
-      }
-      const float2 pa = make_float2(ex2_approx(wa.x), ex2_approx(wa.y));
-      const float2 pc = make_float2(ex2_approx(wc.x), ex2_approx(wc.y));
-      s = fadd2(s, fadd2(pa, pc));
-      const uint32_t ha = pack_bf16x2(pa.x, pa.y), hc = pack_bf16x2(pc.x, pc.y);
-      const float2 la = fsub2(pa, make_float2(__uint_as_float(ha << 16), __uint_as_float(ha & 0xFFFF0000u)));
-      const float2 lc = fsub2(pc, make_float2(__uint_as_float(hc << 16), __uint_as_float(hc & 0xFFFF0000u)));
-      pk[2 * j4] = ha;
-      pk[2 * j4 + 1] = hc;
-      pk[16 + 2 * j4] = pack_bf16x2(la.x, la.y);
-      pk[16 + 2 * j4 + 1] = pack_bf16x2(lc.x, lc.y);
-    }
-    tmem_st32(tS + 32 * qt, pk);
-  }
-  return s.x + s.y;
-}
+__host__ __device__ constexpr int e_bar(int stream, int half) { return 2 * stream + half; }
 
 template <int D>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
@@ -152,14 +82,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   const int step = split_keys ? 2 : 1;        // key tiles from one of a stream's to its next
 
   grid_dep_trigger();  // the own keys' kernel may start where this one leaves room: it needs nothing from here
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < P_COUNT; ++i)
-      mbar_init(&bars[i], i == P_PFULL || i == P_PFULL + 1 ? 4
-                          : i == P_GEMPTY || i == P_GEMPTY + 1 ? (split_keys ? 4 : 8)
-                                                               : 1);
-    abort_word = 0;
+  if (threadIdx.x < P_COUNT) {
+    const int i = threadIdx.x;
+    mbar_init(&bars[i], i >= P_PFULL && i < P_PFULL + 4 ? 4
+                        : i >= P_GEMPTY && i < P_GEMPTY + 2 ? (split_keys ? 4 : 8)
+                                                            : 1);
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) abort_word = 0;
   if (warp == 9) {
     tmem_alloc(&tmem_word, 512);
     tmem_relinquish();
@@ -169,9 +99,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   tc_fence_after();
   const uint32_t tbase = tmem_word;
 
-  const int total = a.Hkv * pp.items * pp.key_tiles, each = units_per_worker(total, pp.workers);
-  const int u_end = min(total, static_cast<int>(blockIdx.x + 1) * each);
-  int u = blockIdx.x * each;
+  const int u_end = min(a.Hkv * pp.items * pp.line, static_cast<int>(blockIdx.x + 1) * pp.each);
+  int u = blockIdx.x * pp.each;
 
   bool ok = true;              // of this thread's role
   int c0 = 0;                  // key tiles before this segment (ring position)
@@ -180,41 +109,41 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   int seg = 0;
   while (u < u_end) {
     // A segment: key tiles t1 - 1 down to t0 of item (hkv, it).
-    const int item = u / pp.key_tiles, hkv = item / pp.items, it = item % pp.items;
-    const int t0 = u % pp.key_tiles, t1 = min(pp.key_tiles, t0 + (u_end - u));
+    const int item = u / pp.line, hkv = item / pp.items, it = item % pp.items;
+    const int t0 = u % pp.line, t1 = min(pp.key_tiles, t0 + (u_end - u));
+    if (t0 >= t1) break;  // empty units: a CTA has them at its end
     const int nT = t1 - t0;
     const int T0 = split_keys ? 0 : 2 * it;  // row tile of stream 0; stream 1 has the next, or the same
     const bool has1 = split_keys ? nT > 1 : T0 + 1 < pp.row_tiles;
     const int n0 = split_keys ? (nT + 1) / 2 : nT, n1 = split_keys ? nT / 2 : (has1 ? nT : 0);
-    const int npages = (P + S - 1) / S;
-
+    const int npages = ceil_div(P, S);
+    // Lane i: page i of key tile t, -1 where the prefix has ended.
+    auto page_of = [&](int t) {
+      const int i = t * (kTile >> a.page_shift) + lane;
+      return t >= 0 && lane < kTile >> a.page_shift && i < npages ? checked_page(a, a.prefix[i]) : -1;
+    };
     if (warp == 8) {
-      // --------------------------------------------------------- producer
-      auto page_of = [&](int t) {  // lane i: page i of key tile t, or -1
-        const int i = t * (kTile / S) + lane;
-        if (lane >= kTile / S || i >= npages) return -1;
-        int id = prefix_page(a, i * S);
-        if (id < 0) {
-          if (a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
-          id = 0;
-        }
-        return id;
-      };
-      int id = ok ? page_of(t1 - 1) : -1;
+      // -------------------------------------------------------- Q and K
+      int id = ok ? page_of(t1 - 1) : -1, issued = 0;
       const bool began = ok;
-      int issued = 0;
-      if (ok && lane == 0) {
+      if (ok) {
         const int rt1 = !split_keys && has1;
-        mbar_arrive_expect_tx(&bars[P_Q], (1 + rt1) * pp.tpt * pp.hp * D * 2);
-        for (int k = 0; k <= rt1; ++k) {
-          const int T = T0 + k, tok = T / pp.head_chunks * pp.tpt, h = hkv * G + T % pp.head_chunks * pp.hp;
-          for (int x = 0; x < D / 64; ++x)
-            tma_load_3d(sm + L::kQ + k * L::kTileBytes + x * 16384, &tmap_q, &bars[P_Q], x * 64, h, tok);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(&bars[P_Q], (1 + rt1) * pp.tpt * pp.hp * D * 2);
+        __syncwarp();
+        if (lane < pp.hp)  // a head a lane
+#pragma unroll 1
+          for (int k = 0; k <= rt1; ++k) {
+            const int T = T0 + k, tok = T / pp.head_chunks * pp.tpt, h = hkv * G + T % pp.head_chunks * pp.hp + lane;
+#pragma unroll 1
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_3d(sm + L::kQ + k * L::kTileBytes + x * 16384 + lane * pp.tpt * 128, &tmap_q, &bars[P_Q], x * 64, h,
+                          tok);
+          }
+        __syncwarp();
       }
+#pragma unroll 1
       for (int s = 0; s < nT && ok; ++s) {
-        const int c = c0 + s, st = c & 1, n = c >> 1;
-        const int here = id;
+        const int c = c0 + s, st = c & 1, n = c >> 1, here = id;
         if (s + 1 < nT) id = page_of(t1 - 2 - s);
         const int loaded = __popc(__ballot_sync(0xffffffffu, here >= 0));
         ok = n == 0 || mbar_wait(&bars[P_KEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
@@ -223,141 +152,161 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&bars[P_KFULL + st], loaded * S * D * 2);
         __syncwarp();
         if (here >= 0)
+#pragma unroll 1
           for (int x = 0; x < D / 64; ++x)
             tma_load_4d(sm + L::kK + st * L::kTileBytes + x * 16384 + lane * S * 128, &tmap_k, &bars[P_KFULL + st],
-                        x * 64, 0, hkv, here);
-        ok = n == 0 || mbar_wait(&bars[P_VEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          mbar_wait_drain(&bars[P_KFULL + st], n & 1);
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&bars[P_VFULL + st], loaded * S * D * 2);
-        __syncwarp();
-        if (here >= 0)
-          for (int x = 0; x < D / 64; ++x)
-            tma_load_4d(sm + L::kV + st * L::kTileBytes + x * 16384 + lane * S * 128, &tmap_v, &bars[P_VFULL + st],
                         x * 64, 0, hkv, here);
         ++issued;
       }
       // Every copy issued lands before the segment ends, also where a wait gave up.
       if (began) mbar_wait_drain(&bars[P_Q], seg & 1);
-      for (int s = max(issued - 2, 0); s < issued; ++s) {
-        const int c = c0 + s;
-        mbar_wait_drain(&bars[P_KFULL + (c & 1)], (c >> 1) & 1);
-        mbar_wait_drain(&bars[P_VFULL + (c & 1)], (c >> 1) & 1);
-      }
+#pragma unroll 1
+      for (int s = max(issued - 2, 0); s < issued; ++s)
+        mbar_wait_drain(&bars[P_KFULL + ((c0 + s) & 1)], ((c0 + s) >> 1) & 1);
     } else if (warp == 9) {
       // ------------------------------------------------------- MMA issuer
       const uint32_t leader = elect_lane();
       constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idO = idesc_bf16(128, D, false, true);
-      const uint32_t tS[2] = {tbase, tbase + 128};
-      const uint32_t tO[2] = {tbase + 256, tbase + 256 + D};
-      const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::kQ), 16, 1024);
-      const uint64_t dK = sdesc_sw128(smem_u32(sm + L::kK), 16, 1024);
-      const uint64_t dV = sdesc_sw128(smem_u32(sm + L::kV), 16384, 1024);
-      auto issue_s = [&](int k, int st) {
-        const uint64_t q = desc_plus(dQ, split_keys ? 0 : k * L::kTileBytes), b = desc_plus(dK, st * L::kTileBytes);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-          umma_ss_e(leader, tS[k], desc_plus(q, off), desc_plus(b, off), idS, ks > 0);
-        }
-        umma_commit_e(leader, &bars[P_SFULL + k]);
-      };
-      auto issue_pv = [&](int k, int st, bool acc) {
-        const uint64_t v = desc_plus(dV, st * L::kTileBytes);
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks) {
-          const uint32_t pc = tS[k] + 32 * (ks >> 1) + 8 * (ks & 1);
-          const uint64_t dv = desc_plus(v, ks * 2048);
-          umma_ts_e(leader, tO[k], pc, dv, idO, (acc || ks > 0) ? 1u : 0u);
-          umma_ts_e(leader, tO[k], pc + 16, dv, idO, 1u);
-        }
-      };
-      auto wait_k = [&](int s) {
-        const int c = c0 + s;
-        if (!mbar_wait(&bars[P_KFULL + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA)) return false;
-        tc_fence_after();
-        return true;
-      };
+      // The issue loop is on the critical path: descriptors are a tile's base plus constants.
+      const uint64_t dQ[2] = {sdesc_sw128(smem_u32(sm + L::kQ), 16, 1024),
+                              sdesc_sw128(smem_u32(sm + L::kQ + (split_keys ? 0 : L::kTileBytes)), 16, 1024)};
+      const uint64_t dK[2] = {sdesc_sw128(smem_u32(sm + L::kK), 16, 1024),
+                              sdesc_sw128(smem_u32(sm + L::kK + L::kTileBytes), 16, 1024)};
+      const uint64_t dV[2] = {sdesc_sw128(smem_u32(sm + L::kV), 16384, 1024),
+                              sdesc_sw128(smem_u32(sm + L::kV + L::kTileBytes), 16384, 1024)};
       auto takes = [&](int k, int s) { return split_keys ? (s & 1) == k : (k == 0 || has1); };
-      ok = ok && mbar_wait(&bars[P_Q], seg & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-      for (int s = 0; s < step && s < nT && ok; ++s) {
-        if (!(ok = wait_k(s))) break;
-        for (int k = 0; k < 2; ++k)
-          if (takes(k, s)) issue_s(k, (c0 + s) & 1);
-        umma_commit_e(leader, &bars[P_KEMPTY + ((c0 + s) & 1)]);
-      }
       int done[2] = {0, 0};
-      for (int s = 0; s < nT && ok; ++s) {
-        const int c = c0 + s, st = c & 1;
-        ok = mbar_wait(&bars[P_VFULL + st], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-        bool kready = false;
-        for (int k = 0; k < 2 && ok; ++k) {
-          if (!takes(k, s)) continue;
-          ok = mbar_wait(&bars[P_PFULL + k], (sc[k] + done[k]) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(k, st, done[k] > 0);
-          ++done[k];
-          if (s + step < nT) {
-            if (!kready && !(ok = wait_k(s + step))) break;
-            kready = true;
-            issue_s(k, (c + step) & 1);
-          } else {
+      ok = ok && mbar_wait(&bars[P_Q], seg & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+      // Step s: P V of key tile s, and S of key tile s + step; the first `step` steps only have an S.
+#pragma unroll 1
+      for (int s = -step; s < nT && ok; ++s) {
+        const int c = c0 + s, sn = s + step, cn = c + step;
+        const bool pv = s >= 0, next = sn < nT;
+        if (pv) ok = mbar_wait(&bars[P_VFULL + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+        if (ok && next)
+          ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+        const uint64_t kd = (cn & 1) ? dK[1] : dK[0], vd = (c & 1) ? dV[1] : dV[0];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = e & 1, h = e >> 1;
+          if (!ok || !takes(k, pv ? s : sn)) continue;
+          if (pv) {
+            ok = mbar_wait(&bars[P_PFULL + e_bar(k, h)], (sc[k] + done[k]) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+            if (!ok) continue;
+            tc_fence_after();
+            // O += P V over 64 keys: rows 64 h on of V, hi and lo of P
+            const uint32_t o = tbase + 256 + k * D;
+            const uint32_t acc = done[k] > 0 || h > 0;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint32_t col = tbase + k * 128 + h * 64 + 32 * (ks >> 1) + 8 * (ks & 1);
+              const uint64_t dv = vd + static_cast<uint64_t>((h * 8192 + ks * 2048) >> 4);
+              if (ks == 0)
+                umma_ts_e(leader, o, col, dv, idO, acc);
+              else
+                umma_ts_e(leader, o, col, dv, idO, 1u);
+              umma_ts_e(leader, o, col + 16, dv, idO, 1u);
+            }
+            umma_commit_e(leader, &bars[P_PVDONE + e_bar(k, h)]);
+            if (h == 1) ++done[k];
+          }
+          if (next && h == 1) {
+            if (!pv) tc_fence_after();
+            // S of the stream's next key tile
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint64_t off = static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+              umma_ss_e(leader, tbase + k * 128, dQ[k] + off, kd + off, idS, ks > 0);
+            }
+            umma_commit_e(leader, &bars[P_SFULL + k]);
+          } else if (pv && h == 1) {
             umma_commit_e(leader, &bars[P_OFINAL + k]);
           }
         }
         if (!ok) break;
-        umma_commit_e(leader, &bars[P_VEMPTY + st]);
-        if (kready) umma_commit_e(leader, &bars[P_KEMPTY + ((c + step) & 1)]);
+        if (pv) umma_commit_e(leader, &bars[P_VEMPTY + (c & 1)]);
+        if (next) umma_commit_e(leader, &bars[P_KEMPTY + (cn & 1)]);
       }
     } else if (warp >= 10) {
-      // ------------------------------------------------------------ gates
-      const int head0 = hkv * G;
-      for (int s = 0; s < nT && ok; ++s) {
-        const int c = c0 + s, st = c & 1, n = c >> 1;
-        if ((c & 1) != warp - 10) continue;
+      // ------------------------------------------------------ V and gates
+      const int head0 = hkv * G, mine = warp - 10;  // the stage of this warp
+      const int s0 = (c0 & 1) == mine ? 0 : 1;
+      const int last = P - 1, lpage = checked_page(a, a.prefix[last >> a.page_shift]);
+      int id = ok ? page_of(t1 - 1 - s0) : -1, issued = 0;
+#pragma unroll 1
+      for (int s = s0; s < nT && ok; s += 2) {
+        const int c = c0 + s, st = c & 1, n = c >> 1, here = id;
         const int t = t1 - 1 - s, j0 = t * kTile, j = j0 + lane * 4;
         const bool in = j < P;
-        const int page = in ? max(prefix_page(a, j), 0) : 0, slot = j % S;
-        const int last = P - 1, lpage = max(prefix_page(a, last), 0);
-        ok = n == 0 || mbar_wait(&bars[P_GEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        id = page_of(s + 2 < nT ? t - 2 : -1);
+        const int loaded = __popc(__ballot_sync(0xffffffffu, here >= 0));
+        const int page = max(__shfl_sync(0xffffffffu, here, (lane * 4) >> a.page_shift), 0), slot = j & (S - 1);
         float* kap = reinterpret_cast<float*>(sm + L::kKap) + st * pp.hp * kKapPitch * pp.kap_tiles;
-        for (int k = 0; k < pp.kap_tiles; ++k) {
-          // the heads of row tile T0 + k; the same as T0's where a group is one chunk (kap_tiles 1)
-          const int h0 = head0 + (T0 + k) % pp.head_chunks * pp.hp;
-#pragma unroll 4
-          for (int g = 0; g < pp.hp; ++g) {
-            const int h = min(h0 + g, head0 + G - 1);
-            const float2 cl = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, lpage, h));
-            const float gl = a.g[g_offset(a, lpage, h, last % S)];
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            float2 base = make_float2(0.f, 0.f);
+        bool first = true;
+#pragma unroll 1
+        for (int g0 = 0; g0 < pp.hp * pp.kap_tiles && ok; g0 += 4) {
+          // Four heads at a time, their loads on the way before anything is waited for.
+          float4 x[4];
+          float2 base[4], cl[4];
+          float gl[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // of row tile T0 + k, or of either where a group is one chunk (kap_tiles 1)
+            const int g = min(g0 + i, pp.hp * pp.kap_tiles - 1), k = g / pp.hp;
+            const int h = min(head0 + (T0 + k) % pp.head_chunks * pp.hp + g - k * pp.hp, head0 + G - 1);
+            cl[i] = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, lpage, h));
+            gl[i] = a.g[g_offset(a, lpage, h, last & (S - 1))];
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            base[i] = make_float2(0.f, 0.f);
             if (in) {
-              x = *reinterpret_cast<const float4*>(a.g + g_offset(a, page, h, slot));
-              base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
+              x[i] = *reinterpret_cast<const float4*>(a.g + g_offset(a, page, h, slot));
+              base[i] = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
             }
+          }
+          if (first) {
+            first = false;
+            ok = n == 0 || mbar_wait(&bars[P_VEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars[P_VFULL + st], loaded * S * D * 2);
+            __syncwarp();
+            if (here >= 0)
+#pragma unroll 1
+              for (int y = 0; y < D / 64; ++y)
+                tma_load_4d(sm + L::kV + st * L::kTileBytes + y * 16384 + lane * S * 128, &tmap_v, &bars[P_VFULL + st],
+                            y * 64, 0, hkv, here);
+            ++issued;
+            ok = n == 0 || mbar_wait(&bars[P_GEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (g0 + i >= pp.hp * pp.kap_tiles) break;
+            float4 y = x[i];
             if (p.bias_from_j) {
-              const float before = __shfl_up_sync(0xffffffffu, x.w, 1);
-              x = make_float4(slot == 0 ? 0.f : before, x.x, x.y, x.z);
+              const float before = __shfl_up_sync(0xffffffffu, y.w, 1);
+              y = make_float4(slot == 0 ? 0.f : before, y.x, y.y, y.z);
             }
+            // A slot behind the prefix's end may hold anything: some finite value instead (its S is masked).
+            if (j + 1 >= P) y.y = 0.f;
+            if (j + 2 >= P) y.z = 0.f;
+            if (j + 3 >= P) y.w = 0.f;
             // (base - c_last) in two parts each, then the sum within the page
-            const float d = ((base.x - cl.x) + (base.y - cl.y)) - gl;
-            *reinterpret_cast<float4*>(kap + (k * pp.hp + g) * kKapPitch + lane * 4) =
-                make_float4((d + x.x) * kLog2e, (d + x.y) * kLog2e, (d + x.z) * kLog2e, (d + x.w) * kLog2e);
+            const float d = ((base[i].x - cl[i].x) + (base[i].y - cl[i].y)) - gl[i];
+            *reinterpret_cast<float4*>(kap + (g0 + i) * kKapPitch + lane * 4) =
+                make_float4((d + y.x) * kLog2e, (d + y.y) * kLog2e, (d + y.z) * kLog2e, (d + y.w) * kLog2e);
           }
         }
+        if (!ok) break;
         if (j0 + kTile > P) {
           // Slots behind the prefix's end may hold anything: V there becomes 0 (its weights are 0).
           ok = mbar_wait(&bars[P_VFULL + st], n & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t sv = smem_u32(sm + L::kV + st * L::kTileBytes);
+#pragma unroll 1
           for (int e = lane; e < (j0 + kTile - P) * (D / 8); e += 32) {
             const int row = P - j0 + e / (D / 8), x = e % (D / 8);
             sts_v4(sv + (x >> 3) * 16384 + row * 128 + (x & 7) * 16, 0, 0, 0, 0);
@@ -367,56 +316,112 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[P_GFULL + st]);
       }
+      if (issued > 0) {
+        const int c = c0 + s0 + 2 * (issued - 1);
+        mbar_wait_drain(&bars[P_VFULL + (c & 1)], (c >> 1) & 1);
+      }
     } else {
       // ----------------------------------------------- softmax, epilogue
       const int k = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
       const int mine = k ? n1 : n0;
       const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-      const uint32_t tS = tbase + k * 128 + lane_off, tO = tbase + 256 + k * D + lane_off;
-      const int kap_row = (pp.kap_tiles > 1 ? k * pp.hp : 0) + r % pp.hp;
+      const uint32_t tO = tbase + 256 + k * D + lane_off;
+      const int kap_row = (pp.kap_tiles > 1 ? k * pp.hp : 0) + min(r / pp.tpt, pp.hp - 1);
+      const float2 nsc = make_float2(-p.scale2, -p.scale2);
       float m = -INFINITY, l = 0.f;
       int q = 0;  // tiles of this stream so far
+#pragma unroll 1
       for (int s = 0; s < nT && ok; ++s) {
         if (split_keys && (s & 1) != k) continue;
-        const int c = c0 + s, st = c & 1, t = t1 - 1 - s;
-        const bool work = mine > 0;
-        ok = (!work || mbar_wait(&bars[P_SFULL + k], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA)) &&
+        const int c = c0 + s, st = c & 1;
+        ok = (mine == 0 || mbar_wait(&bars[P_SFULL + k], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA)) &&
              mbar_wait(&bars[P_GFULL + st], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, ok);  // the tcgen05 loads below are warp-collective
         if (!ok) break;
-        if (work) {
-          tc_fence_after();
-          const float* kap = reinterpret_cast<const float*>(sm + L::kKap) +
-                             ((size_t)st * pp.hp * pp.kap_tiles + kap_row) * kKapPitch;
-          const int lim = P - t * kTile;
-          const float top = lim < kTile ? row_top<true>(tS, kap, p.scale2, lim) : row_top<false>(tS, kap, p.scale2, 0);
-          const bool raise = top > m + kRaise;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float alpha = raise ? ex2_approx(m - top) : 1.f;
-            l *= alpha;
-            if (q > 0) {  // O is settled: this S was committed after the previous P V
+        tc_fence_after();
 #pragma unroll 1
-              for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
-                tmem_ld32(tO + x, o);
-                tmem_ld_wait();
+        for (int h = 0; h < 2 && mine > 0 && ok; ++h) {
+          const uint32_t tS = tbase + k * 128 + h * 64 + lane_off;
+          const float* kap = reinterpret_cast<const float*>(sm + L::kKap) +
+                             (st * pp.hp * pp.kap_tiles + kap_row) * kKapPitch + h * 64;
+          const int lim = P - (t1 - 1 - s) * kTile - h * 64;  // columns from lim on are not keys
+          // P and the row's maximum in one pass, with the running maximum; where a row has passed that by more
+          // than 2^8 (rare after the first tile), once more with the new one: S is still there.
+          uint32_t pk[64];  // of 32 columns hi, lo; twice
+          float2 sum;
+#pragma unroll 1
+          for (int again = 0;; ++again) {
+            const float off = m == -INFINITY ? 0.f : m;
+            const float2 noff = make_float2(-off, -off);
+            float mn = INFINITY;  // of tn_j = kap_j - scale2 S_j = -x_j
+            sum = make_float2(0.f, 0.f);
+            uint32_t rawb[2][32];
+            tmem_ld32(tS, rawb[0]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st32(tO + x, o);
+            for (int x = 0; x < 2; ++x) {
+              tmem_ld_wait();
+              if (x == 0) tmem_ld32(tS + 32, rawb[1]);
+              float2* tn = reinterpret_cast<float2*>(rawb[x]);
+              if (lim < 64) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {  // S of no key is the least there is
+                  if (32 * x + 2 * j >= lim) tn[j].x = -INFINITY;
+                  if (32 * x + 2 * j + 1 >= lim) tn[j].y = -INFINITY;
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float4 kk = lds_f4(kap + 32 * x + 2 * j);
+                const float2 ta = ffma2(tn[j], nsc, make_float2(kk.x, kk.y));
+                const float2 tc = ffma2(tn[j + 1], nsc, make_float2(kk.z, kk.w));
+                mn = fmin3(fmin3(mn, ta.x, ta.y), tc.x, tc.y);
+                const float2 wa = fsub2(noff, ta), wc = fsub2(noff, tc);
+                const float2 pa = make_float2(ex2_approx(wa.x), ex2_approx(wa.y));
+                const float2 pc = make_float2(ex2_approx(wc.x), ex2_approx(wc.y));
+                sum = fadd2(sum, fadd2(pa, pc));
+                const uint32_t ha = pack_bf16x2(pa.x, pa.y), hc = pack_bf16x2(pc.x, pc.y);
+                const float2 la = fsub2(pa, make_float2(__uint_as_float(ha << 16), __uint_as_float(ha & 0xFFFF0000u)));
+                const float2 lc = fsub2(pc, make_float2(__uint_as_float(hc << 16), __uint_as_float(hc & 0xFFFF0000u)));
+                pk[32 * x + j] = ha;
+                pk[32 * x + j + 1] = hc;
+                pk[32 * x + 16 + j] = pack_bf16x2(la.x, la.y);
+                pk[32 * x + 17 + j] = pack_bf16x2(lc.x, lc.y);
               }
             }
-            if (raise) m = top;
+            const bool raise = again == 0 && -mn > m + kRaise;
+            if (!__any_sync(0xffffffffu, raise)) break;
+            const float alpha = raise ? ex2_approx(m + mn) : 1.f;
+            l *= alpha;
+            if (q > 0 || h > 0) {
+              // O has to be settled: the P V of the half before this one is through.
+              ok = mbar_wait(&bars[P_PVDONE + e_bar(k, h ^ 1)], (sc[k] + q - (h ? 0 : 1)) & 1, abort_flag, a.err,
+                             DEV_ERR_TIMEOUT_MMA);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int x = 0; x < D; x += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + x, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16(tO + x, o);
+              }
+            }
+            if (raise) m = -mn;
           }
-          const float off = m == -INFINITY ? 0.f : m;
-          l += lim < kTile ? row_exp<true>(tS, kap, p.scale2, off, lim) : row_exp<false>(tS, kap, p.scale2, off, 0);
+          if (!ok) break;
+          tmem_st32(tS, pk);
+          tmem_st32(tS + 32, pk + 32);
+          l += sum.x + sum.y;
           tmem_st_wait();
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[P_PFULL + e_bar(k, h)]);
         }
-        __syncwarp();
-        if (lane == 0) {
-          if (work) mbar_arrive(&bars[P_PFULL + k]);
-          mbar_arrive(&bars[P_GEMPTY + st]);
-        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&bars[P_GEMPTY + st]);
         ++q;
       }
       const size_t slot = ((size_t)(blockIdx.x + item) * 2 + k) * kTile + r;
@@ -489,21 +494,34 @@ PrefixPlan prefix_plan(const PagedArgs& a) {
   const int G = a.H / a.Hkv;
   x.hp = G < kMaxHp ? G : kMaxHp;
   x.head_chunks = ceil_div(G, x.hp);
-  x.tpt = kTile / x.hp;
-  if (x.tpt > a.rows) x.tpt = a.rows;
+  x.tpt = kTile / x.hp / 8 * 8;  // each head's rows start at a whole swizzle block of shared memory
   x.row_tiles = ceil_div(a.rows, x.tpt) * x.head_chunks;
   x.items = x.row_tiles == 1 ? 1 : ceil_div(x.row_tiles, 2);
   // Two row tiles of an item have different heads where a group is several chunks.
   x.kap_tiles = x.head_chunks > 1 ? 2 : 1;
   x.key_tiles = ceil_div(a.prefix_len, kTile);
   x.workers = kSMs;
+  // Equal ranges of all items' key tiles, or, where that leaves the longest range no longer, a whole number
+  // of CTAs an item: no CTA then begins a second item, which costs it about four tiles' time (its pipeline
+  // runs empty and fills again).
+  const int n = a.Hkv * x.items;
+  x.line = x.key_tiles;
+  x.each = units_per_worker(n * x.key_tiles, x.workers);
+  const int ctas = x.workers / n;
+  if (ctas > 0) {
+    const int whole = ceil_div(x.key_tiles, ctas);
+    if (whole <= x.each + 4) {
+      x.each = whole;
+      x.line = whole * ceil_div(x.key_tiles, whole);
+    }
+  }
   return x;
 }
 
 cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s) {
   const PagedArgs& a = p.a;
   CUtensorMap maps[3];
-  if (!make_q_rows_map(&maps[0], p.q, a.d, a.H, a.rows, p.q_stride, p.pre.hp, p.pre.tpt) ||
+  if (!make_q_rows_map(&maps[0], p.q, a.d, a.H, a.rows, p.q_stride, 1, p.pre.tpt) ||
       !make_page_map(&maps[1], a.k, a.d, a.page_size, a.Hkv, a.num_pages, a.page_size) ||
       !make_page_map(&maps[2], a.v, a.d, a.page_size, a.Hkv, a.num_pages, a.page_size))
     return cudaErrorInvalidValue;

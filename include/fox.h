@@ -279,7 +279,7 @@ typedef struct fox_batch {
   int table_stride;            /* entries of a sequence's row of `table`, >= 1 */
   int prefix_len;              /* tokens of the shared prefix; 0: none */
   const int32_t* cu_new;       /* [B + 1] first row of each sequence, rising from 0; rows behind cu_new[B] are
-                                  neither read nor written. NULL: rows / B rows each (rows a multiple of B) */
+                                  left as they are. NULL: rows / B rows each (rows a multiple of B) */
   const int32_t* lens;         /* [B] tokens of each sequence, the prefix and the new ones among them.
                                   0: an idle sequence (padding); its rows are not appended, and attend to nothing */
   const int32_t* table;        /* [B, table_stride] page ids */
