@@ -1,10 +1,13 @@
-// Appending new tokens to the paged cache: K (rotated by its position where asked), V and the
-// gates, in one launch, or two where a sequence can bring more tokens than a page holds.
+// Appending new tokens to the paged cache: K (rotated by its position where asked), V and the gates.
 //
 // Rotation of the first `dim` channels of a head by the angles of the token's position, given as
 // tables cos, sin [max_pos, dim / 2]:  (x_a, x_b) -> (x_a cos - x_b sin, x_b cos + x_a sin) with
 // (a, b) = (i, i + dim / 2), or (2i, 2i + 1) with `pairs`. The products and the sum are fp32 and
 // round once, to the cache's type.
+//
+// With one page a sequence at most (steps of generation) one launch does it all, copies and gates in
+// different blocks. Longer ones take three: gates, then the scan of the pages' bases, and the copies, which
+// need neither and run beside both (programmatic dependents that wait for their forerunner only at the end).
 //
 // Gates: with a_t = log sigmoid(z_t), g of a token is the sum of a from its page's first token on
 // (fp32) and gbase of a page the sum before it (fp64 arithmetic, kept as two fp32). A page's sums
@@ -22,8 +25,9 @@
 namespace fox {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kGateHeads = 32;  // heads of one gate block
+constexpr int kFewTokens = 8;   // up to so many a gate block sums token after token, not by scans
 
 struct AppendParams {
   PagedArgs a;
@@ -73,32 +77,29 @@ struct Vec<float> {
   }
 };
 
-// Work of the copy: units of two 16-byte chunks of one head of a row, (k, v, q heads) x (chunk pairs). A
-// pair is a channel range and its partner in the rotation, so that each chunk is read once; channels that
-// are not rotated, or whose partners are in the same chunk, go in neighbouring pairs.
-__device__ __forceinline__ void pair_of(int j, int rot_chunks, bool apart, int* c0, int* c1) {
-  const bool turned = apart && 2 * j < rot_chunks;
-  *c0 = turned ? j : 2 * j;
-  *c1 = turned ? j + rot_chunks / 2 : 2 * j + 1;
-}
-
-// Rotates two chunks (x at channel c0, y at c1 of the head).
+// Work of the copy: units of two 16-byte chunks of one head of a row, in the order k, v, q heads.
+// Rotates two chunks: wx at channel c0 of the head, wy its partner's, or its neighbour with `pairs`.
 template <typename T>
-__device__ __forceinline__ void turn(uint4& wx, uint4& wy, int c0, int c1, const float* cs, const float* sn, int rot,
-                                     int pairs) {
+__device__ __forceinline__ void turn(uint4& wx, uint4& wy, int c0, const float* cs, const float* sn, int pairs) {
   constexpr int kN = Vec<T>::kN;
-  if (c0 >= rot) return;
   float x[kN], y[kN], u[kN], v[kN];
   Vec<T>::unpack(wx, x);
   Vec<T>::unpack(wy, y);
   if (pairs) {
+    // neighbouring chunks: kN angles side by side
+    float co[kN], si[kN];
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) {
+      *reinterpret_cast<float4*>(co + i) = *reinterpret_cast<const float4*>(cs + c0 / 2 + i);
+      *reinterpret_cast<float4*>(si + i) = *reinterpret_cast<const float4*>(sn + c0 / 2 + i);
+    }
 #pragma unroll
     for (int i = 0; i < kN; i += 2) {
-      const float ca = cs[(c0 + i) / 2], sa = sn[(c0 + i) / 2], cb = cs[(c1 + i) / 2], sb = sn[(c1 + i) / 2];
-      u[i] = x[i] * ca - x[i + 1] * sa;
-      u[i + 1] = x[i + 1] * ca + x[i] * sa;
-      v[i] = y[i] * cb - y[i + 1] * sb;
-      v[i + 1] = y[i + 1] * cb + y[i] * sb;
+      const int j = i / 2, k = (kN + i) / 2;
+      u[i] = x[i] * co[j] - x[i + 1] * si[j];
+      u[i + 1] = x[i + 1] * co[j] + x[i] * si[j];
+      v[i] = y[i] * co[k] - y[i + 1] * si[k];
+      v[i + 1] = y[i + 1] * co[k] + y[i] * si[k];
     }
   } else {
 #pragma unroll
@@ -135,64 +136,72 @@ __device__ __forceinline__ RowPlace row_place(const AppendParams& p, int row) {
     x.slot = own & (a.page_size - 1);
     x.pos = a.prefix_len + own;
     bad = x.page < 0 || (p.rot > 0 && x.pos >= p.max_pos);
-    if (bad) x.page = -1;
+    if (bad) x = {-1, 0, 0};
   }
   if (bad && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
   return x;
 }
 
-constexpr int kUnits = 4;                  // units of a thread, their loads in flight together
-constexpr int kBlockRows = kThreads * kUnits / 8 + 2;  // most rows that a block's units touch (8 a row at least)
+constexpr int kRows = 4;                        // rows of a thread, their loads in flight together
+constexpr int kBlockRows = kRows * kThreads / 8;  // most rows of a block (8 units a row at least)
 
-// A block's units lie side by side on the line of all rows' units. The loads of k, v, q need only that; they
-// are asked for first, and the look-ups of the rows' pages and positions run meanwhile.
+// How a block's threads go over a row's units: a chunk of them, or, with fewer units than threads, several
+// rows side by side.
+struct CopyShape {
+  int per_row, chunks, side;  // units of a row; chunks of a row; rows side by side
+};
+__host__ __device__ __forceinline__ CopyShape copy_shape(int per_row) {
+  return {per_row, ceil_div(per_row, kThreads), per_row < kThreads ? kThreads / per_row : 1};
+}
+
+// A thread has one unit of kRows rows: what it copies is worked out once, since instructions are what bounds
+// this copy besides memory. The loads of k, v, q come first; the look-ups of the rows' pages and positions
+// run meanwhile.
 template <typename T>
-__device__ __forceinline__ void copy_units(const AppendParams& p, RowPlace* places) {
+__device__ __forceinline__ void copy_rows(const AppendParams& p, RowPlace* places) {
   constexpr int kN = Vec<T>::kN;
   const PagedArgs& a = p.a;
   const int hs = (kN == 8 ? 2 : 3) + (a.d == 128), hp = 1 << hs;  // units of a head
-  const int nk = a.Hkv * hp, per_row = 2 * nk + (p.qn ? a.H * hp : 0);
-  const long long first = (long long)blockIdx.x * (kThreads * kUnits);
-  const int row0 = first < 0x7fffffffLL ? static_cast<int>(first) / per_row : static_cast<int>(first / per_row);
-  const int off = static_cast<int>(first - (long long)row0 * per_row);
-  const int rot_chunks = p.rot / kN;
-  uint4 x[kUnits], y[kUnits];
-  int row[kUnits], at[kUnits];  // at: the unit in its row
+  const int nk = a.Hkv << hs;
+  const CopyShape x = copy_shape(2 * nk + (p.qn ? a.H << hs : 0));
+  const int tid = threadIdx.x, chunk = blockIdx.x % x.chunks, row0 = blockIdx.x / x.chunks * (kRows * x.side);
+  const int sub = x.side > 1 ? tid / x.per_row : 0, at = x.side > 1 ? tid - sub * x.per_row : chunk * kThreads + tid;
+  const bool live = at < x.per_row && sub < x.side, is_v = at >= nk && at < 2 * nk, is_q = at >= 2 * nk;
+  const int w = is_q ? at - 2 * nk : is_v ? at - nk : at, h = w >> hs, j = w & (hp - 1);
+  // The unit's chunks: a channel range and its partner in the rotation, or two neighbours.
+  const int half_chunks = p.rot / kN / 2;
+  const bool apart = !is_v && !p.pairs && j < half_chunks;
+  const int c0 = (apart ? j : 2 * j) * kN, c1 = apart ? c0 + half_chunks * kN : c0 + kN;
+  const long long stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
+  const T* src = static_cast<const T*>(is_q ? p.qn : is_v ? p.vn : p.kn) + (size_t)(row0 + sub) * stride + h * a.d;
+  uint4 u[kRows], v[kRows];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int u = off + i * kThreads + threadIdx.x;
-    row[i] = u / per_row;
-    at[i] = u - row[i] * per_row;
-    const int w = at[i] < nk ? at[i] : at[i] < 2 * nk ? at[i] - nk : at[i] - 2 * nk;
-    int c0, c1;
-    pair_of(w & (hp - 1), at[i] >= nk && at[i] < 2 * nk ? 0 : rot_chunks, !p.pairs, &c0, &c1);
-    const bool is_v = at[i] >= nk && at[i] < 2 * nk, is_q = at[i] >= 2 * nk;
-    const T* src = static_cast<const T*>(is_q ? p.qn : is_v ? p.vn : p.kn) +
-                   (size_t)(row0 + row[i]) * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) + (size_t)(w >> hs) * a.d;
-    if (row0 + row[i] < a.rows) {
-      x[i] = __ldcs(reinterpret_cast<const uint4*>(src + c0 * kN));
-      y[i] = __ldcs(reinterpret_cast<const uint4*>(src + c1 * kN));
+  for (int i = 0; i < kRows; ++i) {
+    if (live && row0 + sub + i * x.side < a.rows) {
+      u[i] = __ldcs(reinterpret_cast<const uint4*>(src + c0));
+      v[i] = __ldcs(reinterpret_cast<const uint4*>(src + c1));
     }
+    src += x.side * stride;
   }
-  const int rows = min((off + kThreads * kUnits - 1) / per_row + 1, a.rows - row0);
-  for (int r = threadIdx.x; r < rows; r += kThreads) places[r] = row_place(p, row0 + r);
+  const int rows = min(kRows * x.side, a.rows - row0);
+  for (int r = tid; r < rows; r += kThreads) places[r] = row_place(p, row0 + r);
   __syncthreads();
+  if (!live) return;
+  const bool turned = !is_v && c0 < p.rot;
+  T* base = is_q ? static_cast<T*>(p.qo) + ((size_t)(row0 + sub) * a.H + h) * a.d
+                 : static_cast<T*>(is_v ? a.v : a.k) + (size_t)h * a.page_size * a.d;
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    if (row0 + row[i] >= a.rows) continue;
-    const RowPlace g = places[row[i]];
+  for (int i = 0; i < kRows; ++i) {
+    const int r = i * x.side + sub;
+    if (r >= rows) break;
+    const RowPlace g = places[r];
     if (g.page < 0) continue;
-    const bool is_v = at[i] >= nk && at[i] < 2 * nk, is_q = at[i] >= 2 * nk;
-    const int w = is_q ? at[i] - 2 * nk : is_v ? at[i] - nk : at[i], h = w >> hs;
-    int c0, c1;
-    pair_of(w & (hp - 1), is_v ? 0 : rot_chunks, !p.pairs, &c0, &c1);
-    if (!is_v && p.rot)
-      turn<T>(x[i], y[i], c0 * kN, c1 * kN, p.cos + (size_t)g.pos * (p.rot / 2), p.sin + (size_t)g.pos * (p.rot / 2), p.rot,
-              p.pairs);
-    T* dst = is_q ? static_cast<T*>(p.qo) + ((size_t)(row0 + row[i]) * a.H + h) * a.d
-                  : static_cast<T*>(is_v ? a.v : a.k) + kv_offset(a, g.page, h, g.slot);
-    *reinterpret_cast<uint4*>(dst + c0 * kN) = x[i];
-    *reinterpret_cast<uint4*>(dst + c1 * kN) = y[i];
+    if (turned)
+      turn<T>(u[i], v[i], c0, p.cos + (size_t)g.pos * (p.rot / 2), p.sin + (size_t)g.pos * (p.rot / 2), p.pairs);
+    T* dst = base + (is_q ? (size_t)i * x.side * a.H * a.d : kv_offset(a, g.page, 0, g.slot));
+    // stored as data that is not needed next: the other way measured 9 % slower on long prompts
+    __stcs(reinterpret_cast<uint4*>(dst + c0), u[i]);
+    __stcs(reinterpret_cast<uint4*>(dst + c1), v[i]);
   }
 }
 
@@ -201,6 +210,7 @@ __device__ __forceinline__ float log_sigmoid(float z) { return fminf(z, 0.f) - l
 // Log gates of tokens [t0, t0 + m) (rows row0 + t) and heads [h0, h0 + nh) into zs[token][head]; 0 past m.
 __device__ __forceinline__ void stage_gates(const AppendParams& p, int row0, int m, int h0, int nh,
                                             float (*zs)[kGateHeads + 1]) {
+#pragma unroll 4
   for (int e = threadIdx.x; e < m * kGateHeads; e += kThreads) {
     const int t = e / kGateHeads, h = e % kGateHeads;
     zs[t][h] = h < nh ? log_sigmoid(p.z[(size_t)(row0 + t) * p.z_stride + h0 + h]) : 0.f;
@@ -234,6 +244,11 @@ __device__ __forceinline__ void put_base(float* gbase, size_t at, double c) {
   *reinterpret_cast<float2*>(gbase + at) = make_float2(hi, static_cast<float>(c - static_cast<double>(hi)));
 }
 
+__device__ __forceinline__ double base_of(const PagedArgs& a, int page, int h) {
+  const float2 x = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
+  return static_cast<double>(x.x) + x.y;
+}
+
 // c of the last token before own token `own`, head h: 0 where there is none.
 __device__ __forceinline__ double gate_before(const PagedArgs& a, int b, int own, int h, bool* bad) {
   const int before = a.prefix_len + own - 1;
@@ -243,9 +258,8 @@ __device__ __forceinline__ double gate_before(const PagedArgs& a, int b, int own
     *bad = true;
     return 0.0;
   }
-  const int slot = (own > 0 ? own - 1 : before) % a.page_size;
-  const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
-  return static_cast<double>(base.x) + base.y + a.g[g_offset(a, page, h, slot)];
+  const int slot = (own > 0 ? own - 1 : before) & (a.page_size - 1);
+  return base_of(a, page, h) + a.g[g_offset(a, page, h, slot)];
 }
 
 // Gates of the new tokens of one sequence that fall into one page.
@@ -264,10 +278,10 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
   }
   if (s.own < 0 || s.n == 0) return;
   const int first = s.own - s.n;                // own index of the first new token
-  const int p0 = first / S * S;                 // first page's first token
+  const int p0 = first & ~(S - 1);              // first page's first token
   const int lo = max(first, p0 + chunk * S), hi = min(s.own, p0 + (chunk + 1) * S);
   if (lo >= hi) return;
-  const int m = hi - lo, slot0 = lo % S;
+  const int m = hi - lo, slot0 = lo & (S - 1);
   const int page = own_page(a, b, lo);
   const int page_before = chunk > 0 ? own_page(a, b, lo - 1) : 0;
   if (page < 0 || page_before < 0) {
@@ -279,70 +293,80 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
   // With one page before this one in the call (no base scan follows), its new tokens are summed
   // here once more: their block may not have written yet. Its base and the value it goes on from
   // were there before the call, as it would otherwise hold a whole page of new tokens.
-  const bool redo = chunk > 0 && !p.scan_bases;
-  const int m1 = lo - first, slot1 = first % S;
-  double open[kGateHeads / (kThreads / 32)];
+  const bool redo = chunk > 0 && !p.scan_bases, opens = slot0 == 0 && (chunk == 0 || redo);
+  const int m1 = redo ? lo - first : 0, slot1 = first & (S - 1);
   bool no_page = false;
-  if (redo) {
-    stage_gates(p, s.row0, m1, h0, nh, zs);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < kGateHeads / (kThreads / 32); ++i) {
-    const int hl = warp + i * (kThreads / 32), h = h0 + hl;
-    open[i] = 0.0;
-    if (hl >= nh) continue;
-    if (redo) {
-      float incl[4];
-      const float was = slot1 > 0 ? a.g[g_offset(a, page_before, h, slot1 - 1)] : 0.f;
-      scan_column(zs, m1, hl, lane, was, incl);
-      // the sum over the whole page stands in lane 31, whatever m1 is
-      const float last = __shfl_sync(0xffffffffu, incl[3], 31);
-      if (slot1 > 0) {
-        const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page_before, h));
-        open[i] = static_cast<double>(base.x) + base.y + last;
-      } else {
-        open[i] = gate_before(a, b, first, h, &no_page) + last;
-      }
-    } else if (chunk == 0 && slot0 == 0) {
-      open[i] = gate_before(a, b, first, h, &no_page);
+  if (m + m1 <= kFewTokens) {
+    // Steps of generation: a lane a head, token after token.
+    if (warp > 0 || lane >= nh) return;
+    const int h = h0 + lane;
+    const float* z = p.z + (size_t)s.row0 * p.z_stride + h;
+    float run = slot0 > 0 ? a.g[g_offset(a, page, h, slot0 - 1)] : 0.f;
+    if (opens) {
+      double c = redo && slot1 > 0 ? base_of(a, page_before, h) : gate_before(a, b, first, h, &no_page);
+      float before = redo && slot1 > 0 ? a.g[g_offset(a, page_before, h, slot1 - 1)] : 0.f;
+#pragma unroll 1
+      for (int t = 0; t < m1; ++t) before += log_sigmoid(z[(size_t)t * p.z_stride]);
+      put_base(a.gbase, gbase_offset(a, page, h), c + before);
     }
+    float* dst = a.g + g_offset(a, page, h, slot0);
+    z += (size_t)(lo - first) * p.z_stride;
+#pragma unroll 1
+    for (int t = 0; t < m; ++t) dst[t] = run += log_sigmoid(z[(size_t)t * p.z_stride]);
+    if (no_page && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
+    return;
   }
-  if (redo) __syncthreads();
+  if (opens) {
+    if (redo) {
+      stage_gates(p, s.row0, m1, h0, nh, zs);
+      __syncthreads();
+    }
+#pragma unroll 2
+    for (int hl = warp; hl < nh; hl += kThreads / 32) {
+      const int h = h0 + hl;
+      double c = redo && slot1 > 0 ? base_of(a, page_before, h) : gate_before(a, b, first, h, &no_page);
+      if (redo) {
+        float incl[4];
+        scan_column(zs, m1, hl, lane, slot1 > 0 ? a.g[g_offset(a, page_before, h, slot1 - 1)] : 0.f, incl);
+        c += __shfl_sync(0xffffffffu, incl[3], 31);  // the sum over the whole page, whatever m1 is
+      }
+      if (lane == 0) put_base(a.gbase, gbase_offset(a, page, h), c);
+    }
+    if (redo) __syncthreads();
+  }
   stage_gates(p, s.row0 + (lo - first), m, h0, nh, zs);
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kGateHeads / (kThreads / 32); ++i) {
-    const int hl = warp + i * (kThreads / 32), h = h0 + hl;
-    if (hl >= nh) continue;
+#pragma unroll 2
+  for (int hl = warp; hl < nh; hl += kThreads / 32) {
+    const int h = h0 + hl;
     float incl[4];
-    const float was = slot0 > 0 ? a.g[g_offset(a, page, h, slot0 - 1)] : 0.f;
-    scan_column(zs, m, hl, lane, was, incl);
+    scan_column(zs, m, hl, lane, slot0 > 0 ? a.g[g_offset(a, page, h, slot0 - 1)] : 0.f, incl);
     float* dst = a.g + g_offset(a, page, h, slot0);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (lane * 4 + e < m) dst[lane * 4 + e] = incl[e];
-    if (slot0 == 0 && (chunk == 0 || redo) && lane == 0) put_base(a.gbase, gbase_offset(a, page, h), open[i]);
   }
   if (no_page && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendParams p) {
   __shared__ union {
     float zs[128][kGateHeads + 1];
     RowPlace places[kBlockRows];
   } sh;
   grid_dep_trigger();
   if (static_cast<int>(blockIdx.x) < p.copy_blocks)
-    copy_units<T>(p, sh.places);
+    copy_rows<T>(p, sh.places);
   else
     gate_block(p, sh.zs);
+  grid_dep_wait();  // as a dependent: what follows this grid follows its forerunners too
 }
 
 // Bases of the pages after a sequence's first one: base_k = base_0 + sum of the full pages' sums.
 // One warp a (sequence, head), 32 pages a step, fp64.
 __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams p) {
+  grid_dep_trigger();
   grid_dep_wait();
   const PagedArgs& a = p.a;
   const int S = a.page_size;
@@ -357,8 +381,7 @@ __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams 
   if (pl == p0) return;
   const int id0 = own_page(a, b, p0 * S);
   if (id0 < 0) return;  // reported by its gate block
-  const float2 base0 = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, id0, h));
-  double carry = static_cast<double>(base0.x) + base0.y;
+  double carry = base_of(a, id0, h);
   constexpr int kSteps = 4;  // of 32 pages, their loads in flight together
   for (int k = p0 + 1; k <= pl; k += 32 * kSteps) {
     float full[kSteps];
@@ -387,24 +410,35 @@ __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams 
 template <typename T>
 cudaError_t launch(AppendParams p, cudaStream_t s) {
   const PagedArgs& a = p.a;
-  const long long units = (long long)a.rows * ((2 * a.Hkv + (p.qn ? a.H : 0)) * (a.d / Vec<T>::kN / 2));
-  const long long copy = (units + kThreads * kUnits - 1) / (kThreads * kUnits);
+  const CopyShape x = copy_shape((2 * a.Hkv + (p.qn ? a.H : 0)) * (a.d / Vec<T>::kN / 2));
+  const long long copy = (long long)ceil_div(a.rows, kRows * x.side) * x.chunks;
   p.page_chunks = ceil_div(a.max_new, a.page_size) + 1;
   p.head_groups = ceil_div(a.H, kGateHeads);
   p.scan_bases = a.max_new > a.page_size;
   const long long gates = (long long)a.B * p.page_chunks * p.head_groups;
   if (copy + gates > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  p.copy_blocks = static_cast<int>(copy);
-  {
+  if (!p.scan_bases) {
+    p.copy_blocks = static_cast<int>(copy);
     TraceScope trace("cache_append", s);
     cache_append_kernel<T><<<static_cast<unsigned>(copy + gates), kThreads, 0, s>>>(p);
+    return cudaGetLastError();
   }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !p.scan_bases) return e;
-  const long long warps = (long long)a.B * a.H;
+  cudaError_t e;
   {
+    p.copy_blocks = 0;
+    TraceScope trace("cache_gates", s);
+    cache_append_kernel<T><<<static_cast<unsigned>(gates), kThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) {
     TraceScope trace("cache_base_scan", s);
-    e = launch_dependent(base_scan_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(kThreads), 0, s, p);
+    const long long warps = (long long)a.B * a.H;
+    e = launch_dependent(base_scan_kernel, dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32))), dim3(kThreads), 0, s, p);
+  }
+  if (e == cudaSuccess) {
+    p.copy_blocks = static_cast<int>(copy);
+    TraceScope trace("cache_copy", s);
+    e = launch_dependent(cache_append_kernel<T>, dim3(static_cast<unsigned>(copy)), dim3(kThreads), 0, s, p);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
