@@ -1,194 +1,8 @@
-// Attention of the newest tokens of every sequence over the paged cache in fp32, on CUDA cores, and
-// the launches of fox_decode.
-//
-// Math ("Forgetting Transformer (FoX) Attention" module source, ForgettingAttention.forward, for
-// the rows of the newest tokens): x_ij = scale q_i . k_j + c_i - c_j over the keys j <= pos_i of
-// the row's sequence, O_i = softmax_j(x_ij) V, LSE_i = ln sum_j exp(x_ij). One pass over the keys
-// with the running maximum and sum, in log2 units; c_i - c_j is formed as
-// (c_i - base of key j's page, in fp64) - (the key's sum within the page), so that it keeps fp32
-// accuracy at any length.
-//
-// One warp is one worker of the work line (fox_paged.h). Scores: a lane owns a key, the rows'
-// dot products run over its row of K. Values: a lane owns d / 32 channels.
+// fox_decode: workspace layout, launches, and the merge of a shared prefix's partial results.
 #include "fox_decode.h"
 
 namespace fox {
 namespace {
-
-constexpr int kSimtWarps = 4;
-constexpr int kSimtRows = 8;
-constexpr int kSimtCtas = 4;  // CTAs of an SM
-
-__device__ __forceinline__ void load4(const float* p, float* f) {
-  const float4 w = *reinterpret_cast<const float4*>(p);
-  f[0] = w.x;
-  f[1] = w.y;
-  f[2] = w.z;
-  f[3] = w.w;
-}
-
-template <int D>
-__global__ void __launch_bounds__(32 * kSimtWarps, kSimtCtas) decode_simt_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int E = D / 32;
-  extern __shared__ Seq seqs[];  // [B + 1]
-  __shared__ int scratch[kSimtWarps];
-  __shared__ __align__(16) float qs[kSimtWarps][kSimtRows][D];  // scaled queries; at the end the kept rows
-  __shared__ Gate2 ci[kSimtWarps][kSimtRows];
-  __shared__ int offs[kSMs * kSimtCtas + 1];
-  __shared__ Column part[32 * kSimtWarps];
-  __shared__ BlockEnds ends;
-  __shared__ Kept<kSimtRows, kSimtWarps> kept;
-  const PagedArgs& a = p.a;
-  scan_sequences(p, seqs, scratch);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size, P = a.prefix_len;
-  const int total = seqs[a.B].u0 * a.Hkv, each = units_per_worker(total, p.workers);
-  const int w = blockIdx.x * kSimtWarps + warp;
-  const int u0 = min(total, w * each);
-  const int u1 = min(total, u0 + each);
-  int left = u1 - u0;
-  Place at;
-  if (left > 0) at = place_of(p, seqs, u0);
-  if (lane == 0) kept.i0[warp] = -1;
-  find_ends<kSimtWarps>(p, seqs, total, each, ends);
-  while (left > 0) {
-    // A segment: key tiles tile0 .. tile1 - 1 of one item.
-    const Seq s = at.s;
-    const int b = at.b, hkv = at.hkv, rt = at.rt;
-    const int keys = s.own + P, tile0 = at.tile, tile1 = min(at.tiles, tile0 + left);
-    const int R = rows_of(p, at);
-
-    __syncwarp();
-#pragma unroll 1
-    for (int r = 0; r < R; ++r) {
-      const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
-      const float* src = static_cast<const float*>(p.q) + (size_t)(s.row0 + t) * p.q_stride + (size_t)h * D;
-      for (int c = lane * 4; c < D; c += 128) {
-        float f[4];
-        load4(src + c, f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qs[warp][r][c + e] = f[e] * p.scale2;
-      }
-      if (lane == 0) {
-        const int i = s.own - s.n + t;
-        ci[warp][r] = gate_sum(a, own_page_or_0(a, b, i), i & (S - 1), h);
-      }
-    }
-    __syncwarp();
-
-    float m[kSimtRows], l[kSimtRows], acc[kSimtRows][E];
-#pragma unroll
-    for (int r = 0; r < kSimtRows; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
-    }
-    for (int tile = tile0; tile < tile1; ++tile) {
-      const int j = tile * kKeyTile + lane;
-      const bool in = j < keys;
-      int page = -1, slot = 0;
-      if (in) {
-        const int own = j - P;
-        page = j < P ? prefix_page(a, j) : own_page(a, b, own);
-        slot = (j < P ? j : own) & (S - 1);
-        if (page < 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
-      }
-      const size_t kv = page >= 0 ? kv_offset(a, page, hkv, slot) : 0;
-      float sc[kSimtRows];
-#pragma unroll
-      for (int r = 0; r < kSimtRows; ++r) sc[r] = 0.f;
-      if (page >= 0) {
-        const float* kp = static_cast<const float*>(a.k) + kv;
-#pragma unroll 4
-        for (int c = 0; c < D; c += 4) {
-          float f[4];
-          load4(kp + c, f);
-#pragma unroll
-          for (int r = 0; r < kSimtRows; ++r) {
-            const float4 qv = *reinterpret_cast<const float4*>(&qs[warp][r][c]);
-            sc[r] = fmaf(qv.x, f[0], fmaf(qv.y, f[1], fmaf(qv.z, f[2], fmaf(qv.w, f[3], sc[r]))));
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < kSimtRows; ++r) {
-        float x = -INFINITY;
-        if (r < R && page >= 0) {
-          const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
-          if (j <= P + s.own - s.n + t) {
-            const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
-            const float beta = (ci[warp][r].hi - base.x) + (ci[warp][r].lo - base.y);
-            const int gs = p.bias_from_j ? slot - 1 : slot;
-            const float gj = gs >= 0 ? a.g[g_offset(a, page, h, gs)] : 0.f;
-            x = fmaf(beta - gj, kLog2e, sc[r]);
-          }
-        }
-        float top = x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float mn = fmaxf(m[r], top);
-        const float safe = mn == -INFINITY ? 0.f : mn;
-        const float alpha = ex2_approx(m[r] - safe);
-        const float w_ = ex2_approx(x - safe);
-        m[r] = mn;
-        l[r] = l[r] * alpha + w_;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[r][e] *= alpha;
-        sc[r] = w_;
-      }
-      const int nk = min(kKeyTile, keys - tile * kKeyTile);
-#pragma unroll 4
-      for (int jj = 0; jj < nk; ++jj) {
-        const size_t at = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(kv), jj);
-        const int pg = __shfl_sync(0xffffffffu, page, jj);
-        if (pg < 0) continue;
-        const float* vp = static_cast<const float*>(a.v) + at + lane * E;
-        float f[E];
-        if (E == 4) {
-          load4(vp, f);
-        } else {
-          const float2 wv = *reinterpret_cast<const float2*>(vp);
-          f[0] = wv.x;
-          f[1] = wv.y;
-        }
-#pragma unroll
-        for (int r = 0; r < kSimtRows; ++r) {
-          const float pr = __shfl_sync(0xffffffffu, sc[r], jj);
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[r][e] = fmaf(pr, f[e], acc[r][e]);
-        }
-      }
-    }
-    // Results: rows in shared memory, where the queries were, for the block to join with its neighbours', or
-    // finished, or to the worker's slot.
-    const bool alone = at.i0 >= u0 && at.i0 + at.tiles <= u1, keep = !alone && tile1 - tile0 == left;
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < kSimtRows; ++r) {
-      float sum = l[r];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) {
-        kept.m[warp][r] = m[r];
-        kept.l[warp][r] = sum;
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) qs[warp][r][lane * E + e] = acc[r][e];
-    }
-    if (keep && lane == 0) {
-      kept.i0[warp] = at.i0;
-      kept.at[warp] = at;
-    }
-    __syncwarp();
-    if (!keep) leave_rows<float, D>(p, at, w, alone, &qs[warp][0][0], D, kept.m[warp], kept.l[warp]);
-    left -= tile1 - tile0;
-    at.tile = tile1;
-    if (tile1 == at.tiles && left > 0) next_item(p, seqs, at);
-  }
-  clear_idle_rows<float, D>(p, seqs);
-  join_items<float, D, kSimtRows, kSimtWarps>(p, seqs, total, each, kept, ends, &qs[0][0][0], kSimtRows * D, D, offs, part);
-}
 
 // One output row (query row, query head): the partial results of its own item and of the shared prefix
 // joined, in a fixed order, by one warp, or with few rows (deal = kMergeWarps) by a block's warps, which
@@ -340,12 +154,12 @@ struct DecodeLayout {
 DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   DecodeLayout L;
   const int G = a.H / a.Hkv;
-  L.Rt = f32 ? kSimtRows : decode_mma_rows(a.max_new * G);
+  L.Rt = f32 ? kF32Rows : decode_mma_rows(a.max_new * G);
   L.Gp = padded_group(G, L.Rt);
   const int most = a.max_new * L.Gp;
   L.Rs = most < L.Rt ? most : L.Rt;
   L.RTmax = ceil_div(most, L.Rt);
-  L.workers = f32 ? kSMs * kSimtCtas * kSimtWarps : kSMs * decode_mma_warps(a.d);
+  L.workers = kSMs * (f32 ? kF32Warps : decode_mma_warps(a.d));
   const size_t slots = (size_t)L.workers + (size_t)a.B * a.Hkv * L.RTmax;
   L.cum = kCacheHeaderBytes;
   L.po_rows = (long long)slots * L.Rs;
@@ -361,17 +175,6 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
     L.end = align_up(L.ppo + sizeof(float) * rows * a.d, 256);
   }
   return L;
-}
-
-template <int D>
-cudaError_t launch_simt(const DecodeParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Seq) * ((size_t)p.a.B + 1);
-  const cudaError_t e =
-      cudaFuncSetAttribute(decode_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  TraceScope trace("decode", s);
-  decode_simt_kernel<D><<<kSMs * kSimtCtas, 32 * kSimtWarps, smem, s>>>(p);
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -402,7 +205,7 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.Gp = L.Gp;
   p.gp_inv = L.Gp > 1 ? static_cast<uint32_t>(((1ull << 32) + L.Gp - 1) / L.Gp) : 0u;
   p.workers = L.workers;
-  p.warps = f32 ? kSimtWarps : decode_mma_warps(x.a.d);
+  p.warps = f32 ? kF32Warps : decode_mma_warps(x.a.d);
   p.cum = reinterpret_cast<int*>(ws + L.cum);
   p.count = reinterpret_cast<uint32_t*>(ws + kErrWordBytes);
   p.ml = reinterpret_cast<float2*>(ws + L.ml);
@@ -410,10 +213,10 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.pre = L.pre;
   p.pre.ml = reinterpret_cast<float2*>(ws + L.pml);
   p.pre.po = reinterpret_cast<float*>(ws + L.ppo);
-  static_assert(kErrWordBytes + 4 * kSMs * kSimtCtas * kSimtWarps <= kCacheHeaderBytes, "counters of all workers");
+  static_assert(kErrWordBytes + 4 * kSMs <= kCacheHeaderBytes, "a counter a CTA");
   const cudaError_t e = p.pre.key_tiles > 0 ? launch_prefix(p, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  if (f32) return x.a.d == 64 ? launch_simt<64>(p, s) : launch_simt<128>(p, s);
+  if (f32) return launch_decode_f32(p, s);
   const cudaError_t f = launch_decode_mma(p, s);
   if (f != cudaSuccess || p.pre.key_tiles == 0) return f;
   return x.a.d == 64 ? launch_merge<64>(p, s) : launch_merge<128>(p, s);

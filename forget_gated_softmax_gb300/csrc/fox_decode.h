@@ -170,6 +170,37 @@ __device__ __forceinline__ int own_page_or_0(const PagedArgs& a, int b, int p) {
   return max(page, 0);
 }
 
+// ---- asynchronous copies to shared memory, in groups of the thread ----
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros where there are none to copy (src is then not read).
+__device__ __forceinline__ void cp_async16_or_0(uint32_t dst, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D, int NT>
+struct MmaLayout {
+  static constexpr int kWarps = D == 128 ? 4 : 8;
+  // 128 KB on the way to an SM. A third stage measured no faster where bandwidth decides, and the SMs'
+  // shares of it less equal, so that the last finished later (one sequence of 65536: 52 against 49 us).
+  static constexpr int kStages = 2;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTileBytes = kKeyTile * D * 2;  // K or V of a stage
+  static constexpr int kOutStride = D + 4;             // a result row in shared memory, in floats
+  static_assert(kRows * kOutStride * 4 <= 2 * kTileBytes, "results pass through a stage that was read");
+};
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Four channels to O.
 template <typename T>
 __device__ __forceinline__ void put4(T* dst, float4 v);
@@ -424,6 +455,10 @@ __device__ __forceinline__ void clear_idle_rows(const DecodeParams& p, const Seq
 int decode_mma_rows(int rows);
 int decode_mma_warps(int d);
 cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t s);
+// The fp32 kernel (fox_decode_f32.cu): row tile, workers of a CTA, CTAs of an SM, launch.
+constexpr int kF32Rows = 8;
+constexpr int kF32Warps = 4;
+cudaError_t launch_decode_f32(const DecodeParams& p, cudaStream_t s);
 PrefixPlan prefix_plan(const PagedArgs& a);
 cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s);
 

@@ -52,32 +52,6 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <int D, int NT>
-struct MmaLayout {
-  static constexpr int kWarps = D == 128 ? 4 : 8;
-  // 128 KB on the way to an SM. A third stage measured no faster where bandwidth decides, and the SMs'
-  // shares of it less equal, so that the last finished later (one sequence of 65536: 52 against 49 us).
-  static constexpr int kStages = 2;
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kTileBytes = kKeyTile * D * 2;  // K or V of a stage
-  static constexpr int kOutStride = D + 4;             // a result row in shared memory, in floats
-  static_assert(kRows * kOutStride * 4 <= 2 * kTileBytes, "results pass through a stage that was read");
-};
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // Shared memory: K and V of every (warp, stage), then its gates, then the sequences' work offsets.
 // Gates of a stage: per sub-page (32 slots, or two of 16) [heads][slots + 4] sums, then [heads] bases.
 struct MmaShape {
