@@ -227,10 +227,16 @@ def fox_bwd_workspace_bytes(params: fox_params) -> int:
     return int(lib().fox_bwd_workspace_bytes(ctypes.byref(params)))
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -602,11 +608,10 @@ def cache_workspace(cache: Cache, batch: Batch, rows: int):
 
 
 def _cache_call_device(where: str, cache: Cache, batch: Batch) -> int:
-    torch = _torch()
     index = cache.device.index
     if batch.device != cache.device:
         raise ValueError(f"{where}: cache and batch are on different devices")
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         raise ValueError(f"{where}: the cache is not on the current CUDA device")
     if batch.prefix_table is not None and batch.prefix_table.shape[0] * cache.page_size < batch.params.prefix_len:
         raise ValueError(f"{where}: prefix_table has too few pages")
@@ -627,19 +632,29 @@ def _row_stride(where: str, name: str, t, cache: Cache, heads: int, rows: int) -
     return s0
 
 
+# torch.cuda.current_device() and the current stream's handle, by torch's own short ways where it has them: a
+# step of generation is some microseconds of GPU time, of which these would otherwise take three.
+def _current_device() -> int:
+    global _current_device
+    C = _torch()._C
+    _current_device = getattr(C, "_cuda_getDevice", None) or _torch().cuda.current_device
+    return _current_device()
+
+
+def _current_stream(index: int) -> int:
+    global _current_stream
+    torch = _torch()
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _current_stream(index)
+
+
 def _alloc_on(stream, make):
     """A tensor that the call allocates itself, made in the allocator's order of the stream that uses it."""
+    if stream is None:
+        return make()
     with _torch().cuda.stream(stream):
         return make()
-
-
-def _launch_stream(stream, index: int) -> int:
-    """The handle to launch on; the current stream's without building a Stream object where torch offers it."""
-    if stream is not None:
-        return stream.cuda_stream
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
 def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, sin=None, pairs: bool = False,
@@ -673,8 +688,10 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
         if q is not None:
             qs = _row_stride(where, "q", q, cache, cache.H, rows)
             if q_out is None:
-                q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else _alloc_on(
-                    stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
+                if stream is None and q.is_contiguous():
+                    q_out = torch.empty_like(q)
+                else:
+                    q_out = _alloc_on(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
             else:
                 _row_stride(where, "q_out", q_out, cache, cache.H, rows)
                 if not q_out.is_contiguous():
@@ -686,9 +703,9 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
                                       _ptr(q), qs, _ptr(q_out)))
     if ws is None:
         ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
-    st = lib().fox_cache_append(
+    st = (_lib or lib()).fox_cache_append(
         cache.ref, batch.ref, rows, k.data_ptr(), ks, v.data_ptr(), vs, z.data_ptr(), zs, rot, ws.data_ptr(), ws.numel(),
-        _launch_stream(stream, index),
+        _current_stream(index) if stream is None else stream.cuda_stream,
     )
     if st != 0:
         raise FoxError(st, where)
@@ -706,9 +723,10 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
     rows = q.shape[0]
     qs = _row_stride(where, "q", q, cache, cache.H, rows)
     if o is None:
-        fmt = torch.contiguous_format
-        o = torch.empty_like(q, memory_format=fmt) if stream is None else _alloc_on(
-            stream, lambda: torch.empty_like(q, memory_format=fmt))
+        if stream is None and q.is_contiguous():
+            o = torch.empty_like(q)
+        else:
+            o = _alloc_on(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     else:
         _row_stride(where, "o", o, cache, cache.H, rows)
         if not o.is_contiguous():
@@ -720,9 +738,9 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
         raise ValueError(f"{where}: lse must be contiguous [{rows}, {cache.H}] float32 on the cache's device")
     if ws is None:
         ws = _alloc_on(stream, lambda: cache_workspace(cache, batch, rows))
-    st = lib().fox_decode(
+    st = (_lib or lib()).fox_decode(
         cache.ref, batch.ref, rows, q.data_ptr(), qs, scale, 1 if bias_from_j else 0, o.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), ws.numel(), _launch_stream(stream, index),
+        ws.data_ptr(), ws.numel(), _current_stream(index) if stream is None else stream.cuda_stream,
     )
     if st != 0:
         raise FoxError(st, where)

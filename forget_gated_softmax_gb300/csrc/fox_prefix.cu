@@ -17,12 +17,16 @@
 //   one row tile: the streams take alternate key tiles, and leave a partial result each.
 // A stream's P goes to the tensor core in two halves of 64 keys, so that one half's P V runs during the
 // other's softmax.
-// Warp roles (384 threads): warps 0-3 and 4-7 the streams' softmax (thread = row = TMEM lane), warp 8
-// loads Q and K, warp 9 allocates TMEM and issues the MMAs, warps 10-11 load V and make the gate terms
-// log2 e (c_j - c_last) of a key tile's keys and the row tile's heads, a stage each.
+// Warp roles (480 threads): warps 0-3 and 4-7 the streams' softmax (thread = row = TMEM lane), warp 8
+// loads Q and K, warps 9 and 14 issue the streams' MMAs (one warp for both spent 1.7 us a key tile on
+// waits, fences and commits that two have side by side), warps 10-11 load V and make the gate terms
+// log2 e (c_j - c_last) of a key tile's keys and the row tile's heads, a stage each, and warps 12-13 turn
+// each V tile from bf16 to fp16 in place.
 //
-// P V: P = hi + lo in bf16, two products (see fox_decode_mma.cu). A 32-column chunk of S, once read,
-// takes its own 16 columns of hi and 16 of lo, so P needs no memory beside S.
+// P V runs in fp16, as in fox_attn_fwd_kernel and for its reason: with bf16 P its 8 significant bits add an
+// error as large as O's own rounding. Two bf16 terms a weight (as in fox_decode_mma.cu, where products
+// cost nothing) made the tensor core the bound: 2.8 us a pair of 128 x 128 tiles. A magnitude of 65536 or
+// more in V (outside fp16) sets DEV_ERR_RANGE. A 32-column chunk of S, once read, holds its P.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,7 +35,7 @@
 namespace fox {
 namespace {
 
-constexpr int kPrefixThreads = 384;
+constexpr int kPrefixThreads = 480;
 constexpr int kMaxHp = 16;
 constexpr int kKapPitch = kTile + 4;  // floats: the heads' rows start in different banks
 constexpr float kRaise = 8.0f;        // log2 units that a row may pass its running maximum by
@@ -51,14 +55,16 @@ enum PBar {
   P_KEMPTY = 3,
   P_VFULL = 5,
   P_VEMPTY = 7,
-  P_GFULL = 9,   // +stage: the key tile's gate terms (and the tail of V) are in place
+  P_GFULL = 9,   // +stage: the key tile's gate terms are in place
   P_GEMPTY = 11,
   P_SFULL = 13,  // +stream
   P_OFINAL = 15,
   P_PFULL = 17,  // +2 stream + half
-  P_PVDONE = 21,
-  P_DONE = 25,
-  P_COUNT = 26,
+  P_PVDONE = 21,  // +stream: P V of the first half
+  P_VREADY = 23,  // +stage: V in fp16, and 0 behind the prefix's end
+  P_START = 25,   // stream 0 has its first P of the segment: stream 1 may begin
+  P_DONE = 26,
+  P_COUNT = 27,
 };
 
 __host__ __device__ constexpr int e_bar(int stream, int half) { return 2 * stream + half; }
@@ -84,9 +90,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   grid_dep_trigger();  // the own keys' kernel may start where this one leaves room: it needs nothing from here
   if (threadIdx.x < P_COUNT) {
     const int i = threadIdx.x;
-    mbar_init(&bars[i], i >= P_PFULL && i < P_PFULL + 4 ? 4
+    mbar_init(&bars[i], (i >= P_PFULL && i < P_PFULL + 4) || i == P_START ? 4
                         : i >= P_GEMPTY && i < P_GEMPTY + 2 ? (split_keys ? 4 : 8)
-                                                            : 1);
+                        : i >= P_VREADY && i < P_VREADY + 2                                     ? 2
+                        : i == P_KEMPTY || i == P_KEMPTY + 1 || i == P_VEMPTY || i == P_VEMPTY + 1
+                            ? (split_keys ? 1 : 2)  // the streams that use a key tile
+                        : i == P_DONE ? 2
+                                      : 1);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_word = 0;
@@ -103,6 +113,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   int u = blockIdx.x * pp.each;
 
   bool ok = true;              // of this thread's role
+  uint32_t vmax = 0u;          // converters: largest |v| bit pattern seen, per bf16 half
   int c0 = 0;                  // key tiles before this segment (ring position)
   int sc[2] = {0, 0};          // tiles of each stream before this segment
   int oc[2] = {0, 0};          // segments in which each stream had tiles
@@ -163,70 +174,105 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll 1
       for (int s = max(issued - 2, 0); s < issued; ++s)
         mbar_wait_drain(&bars[P_KFULL + ((c0 + s) & 1)], ((c0 + s) >> 1) & 1);
-    } else if (warp == 9) {
-      // ------------------------------------------------------- MMA issuer
+    } else if (warp == 9 || warp == 14) {
+      // ------------------------------------------------------ MMA issuers
+      const int k = warp == 14;  // the stream
+      const int mine = k ? n1 : n0;
       const uint32_t leader = elect_lane();
       constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
-      // The issue loop is on the critical path: descriptors are a tile's base plus constants.
-      const uint64_t dQ[2] = {sdesc_sw128(smem_u32(sm + L::kQ), 16, 1024),
-                              sdesc_sw128(smem_u32(sm + L::kQ + (split_keys ? 0 : L::kTileBytes)), 16, 1024)};
-      const uint64_t dK[2] = {sdesc_sw128(smem_u32(sm + L::kK), 16, 1024),
-                              sdesc_sw128(smem_u32(sm + L::kK + L::kTileBytes), 16, 1024)};
-      const uint64_t dV[2] = {sdesc_sw128(smem_u32(sm + L::kV), 16384, 1024),
-                              sdesc_sw128(smem_u32(sm + L::kV + L::kTileBytes), 16384, 1024)};
-      auto takes = [&](int k, int s) { return split_keys ? (s & 1) == k : (k == 0 || has1); };
-      int done[2] = {0, 0};
+      constexpr uint32_t idO = idesc_f16(128, D, false, true);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::kQ + (split_keys ? 0 : k * L::kTileBytes)), 16, 1024);
+      const uint64_t dK = sdesc_sw128(smem_u32(sm + L::kK), 16, 1024);
+      const uint64_t dV = sdesc_sw128(smem_u32(sm + L::kV), 16384, 1024);
+      const uint32_t tS = tbase + k * 128, tO = tbase + 256 + k * D;
       ok = ok && mbar_wait(&bars[P_Q], seg & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-      // Step s: P V of key tile s, and S of key tile s + step; the first `step` steps only have an S.
+      // On the same key tiles the streams keep out of step, each on the tensor core during the other's softmax:
+      // in step, both did the same at once (2.6 us a pair of tiles, X with stream 1 begun half a tile later).
+      if (ok && k == 1 && mine > 0 && !split_keys)
+        ok = mbar_wait(&bars[P_START], seg & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+      // Step s: P V of the stream's key tile s, and S of its next; the step before the first only has the S.
 #pragma unroll 1
-      for (int s = -step; s < nT && ok; ++s) {
-        const int c = c0 + s, sn = s + step, cn = c + step;
-        const bool pv = s >= 0, next = sn < nT;
-        if (pv) ok = mbar_wait(&bars[P_VFULL + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-        if (ok && next)
-          ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-        const uint64_t kd = (cn & 1) ? dK[1] : dK[0], vd = (c & 1) ? dV[1] : dV[0];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = e & 1, h = e >> 1;
-          if (!ok || !takes(k, pv ? s : sn)) continue;
-          if (pv) {
-            ok = mbar_wait(&bars[P_PFULL + e_bar(k, h)], (sc[k] + done[k]) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-            if (!ok) continue;
-            tc_fence_after();
-            // O += P V over 64 keys: rows 64 h on of V, hi and lo of P
-            const uint32_t o = tbase + 256 + k * D;
-            const uint32_t acc = done[k] > 0 || h > 0;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint32_t col = tbase + k * 128 + h * 64 + 32 * (ks >> 1) + 8 * (ks & 1);
-              const uint64_t dv = vd + static_cast<uint64_t>((h * 8192 + ks * 2048) >> 4);
-              if (ks == 0)
-                umma_ts_e(leader, o, col, dv, idO, acc);
-              else
-                umma_ts_e(leader, o, col, dv, idO, 1u);
-              umma_ts_e(leader, o, col + 16, dv, idO, 1u);
-            }
-            umma_commit_e(leader, &bars[P_PVDONE + e_bar(k, h)]);
-            if (h == 1) ++done[k];
+      for (int s = split_keys ? k - 2 : -1, q = -1; s < nT && ok; s += step, ++q) {
+        const int c = c0 + s, cn = c + step;
+        const bool pv = q >= 0, next = s + step < nT;
+        if (mine == 0) {  // an item's missing second row tile: the stages are let go as they come
+          if (next) {
+            ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+            if (ok && lane == 0) mbar_arrive(&bars[P_KEMPTY + (cn & 1)]);
           }
-          if (next && h == 1) {
-            if (!pv) tc_fence_after();
-            // S of the stream's next key tile
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint64_t off = static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
-              umma_ss_e(leader, tbase + k * 128, dQ[k] + off, kd + off, idS, ks > 0);
-            }
-            umma_commit_e(leader, &bars[P_SFULL + k]);
-          } else if (pv && h == 1) {
-            umma_commit_e(leader, &bars[P_OFINAL + k]);
+          if (ok && pv) {
+            ok = mbar_wait(&bars[P_VREADY + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+            if (ok && lane == 0) mbar_arrive(&bars[P_VEMPTY + (c & 1)]);
           }
+          continue;
+        }
+        const uint64_t vd = dV + ((c & 1) ? L::kTileBytes >> 4 : 0), kd = dK + ((cn & 1) ? L::kTileBytes >> 4 : 0);
+        // O += P V over 64 keys: rows 64 h on of V
+        auto issue_pv = [&](int h, uint32_t acc) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ts_e(leader, tO, tS + h * 64 + 32 * (ks >> 1) + 8 * (ks & 1),
+                      vd + static_cast<uint64_t>((h * 8192 + ks * 2048) >> 4), idO, ks > 0 ? 1u : acc);
+        };
+        if (pv) {
+          ok = mbar_wait(&bars[P_VREADY + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC) &&
+               mbar_wait(&bars[P_PFULL + e_bar(k, 0)], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(0, q > 0);
+          umma_commit_e(leader, &bars[P_PVDONE + k]);
+        }
+        if (next) ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+        if (pv) {
+          ok = ok && mbar_wait(&bars[P_PFULL + e_bar(k, 1)], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(1, 1u);
         }
         if (!ok) break;
         if (pv) umma_commit_e(leader, &bars[P_VEMPTY + (c & 1)]);
-        if (next) umma_commit_e(leader, &bars[P_KEMPTY + (cn & 1)]);
+        if (next) {
+          if (!pv) tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t off = static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+            umma_ss_e(leader, tS, dQ + off, kd + off, idS, ks > 0);
+          }
+          umma_commit_e(leader, &bars[P_SFULL + k]);
+          umma_commit_e(leader, &bars[P_KEMPTY + (cn & 1)]);
+        } else {
+          umma_commit_e(leader, &bars[P_OFINAL + k]);
+        }
+      }
+    } else if (warp == 12 || warp == 13) {
+      // --------------------------------------------- V from bf16 to fp16
+      // The two warps take alternate 16-byte pieces of the swizzled layout TMA wrote; the conversion is per
+      // element, so the layout is unchanged. Slots behind the prefix's end may hold anything: V there
+      // becomes 0 (its weights are 0).
+#pragma unroll 1
+      for (int s = 0; s < nT && ok; ++s) {
+        const int c = c0 + s, st = c & 1, keys = P - (t1 - 1 - s) * kTile;
+        ok = mbar_wait(&bars[P_VFULL + st], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint4* tile = reinterpret_cast<uint4*>(sm + L::kV + st * L::kTileBytes);
+#pragma unroll 8
+        for (int e = (warp - 12) * 32 + lane; e < L::kTileBytes / 16; e += 64) {
+          const uint4 w = tile[e];
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          uint32_t out[4];
+          const bool key = ((e >> 3) & (kTile - 1)) < keys;  // eight pieces a row of 64 channels
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = key ? in[i] : 0u;
+            out[i] = pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(vmax) : "r"(x & 0x7FFF7FFFu));
+          }
+          tile[e] = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[P_VREADY + st]);
       }
     } else if (warp >= 10) {
       // ------------------------------------------------------ V and gates
@@ -300,19 +346,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
         }
         if (!ok) break;
-        if (j0 + kTile > P) {
-          // Slots behind the prefix's end may hold anything: V there becomes 0 (its weights are 0).
-          ok = mbar_wait(&bars[P_VFULL + st], n & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint32_t sv = smem_u32(sm + L::kV + st * L::kTileBytes);
-#pragma unroll 1
-          for (int e = lane; e < (j0 + kTile - P) * (D / 8); e += 32) {
-            const int row = P - j0 + e / (D / 8), x = e % (D / 8);
-            sts_v4(sv + (x >> 3) * 16384 + row * 128 + (x & 7) * 16, 0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[P_GFULL + st]);
       }
@@ -347,7 +380,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           const int lim = P - (t1 - 1 - s) * kTile - h * 64;  // columns from lim on are not keys
           // P and the row's maximum in one pass, with the running maximum; where a row has passed that by more
           // than 2^8 (rare after the first tile), once more with the new one: S is still there.
-          uint32_t pk[64];  // of 32 columns hi, lo; twice
+          uint32_t pk[32];
           float2 sum;
 #pragma unroll 1
           for (int again = 0;; ++again) {
@@ -379,13 +412,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 const float2 pa = make_float2(ex2_approx(wa.x), ex2_approx(wa.y));
                 const float2 pc = make_float2(ex2_approx(wc.x), ex2_approx(wc.y));
                 sum = fadd2(sum, fadd2(pa, pc));
-                const uint32_t ha = pack_bf16x2(pa.x, pa.y), hc = pack_bf16x2(pc.x, pc.y);
-                const float2 la = fsub2(pa, make_float2(__uint_as_float(ha << 16), __uint_as_float(ha & 0xFFFF0000u)));
-                const float2 lc = fsub2(pc, make_float2(__uint_as_float(hc << 16), __uint_as_float(hc & 0xFFFF0000u)));
-                pk[32 * x + j] = ha;
-                pk[32 * x + j + 1] = hc;
-                pk[32 * x + 16 + j] = pack_bf16x2(la.x, la.y);
-                pk[32 * x + 17 + j] = pack_bf16x2(lc.x, lc.y);
+                pk[16 * x + j] = pack_f16x2(pa.x, pa.y);
+                pk[16 * x + j + 1] = pack_f16x2(pc.x, pc.y);
               }
             }
             const bool raise = again == 0 && -mn > m + kRaise;
@@ -393,12 +421,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const float alpha = raise ? ex2_approx(m + mn) : 1.f;
             l *= alpha;
             if (q > 0 || h > 0) {
-              // O has to be settled: the P V of the half before this one is through.
-              ok = mbar_wait(&bars[P_PVDONE + e_bar(k, h ^ 1)], (sc[k] + q - (h ? 0 : 1)) & 1, abort_flag, a.err,
-                             DEV_ERR_TIMEOUT_MMA);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              tc_fence_after();
+              // O has to be settled. This S was committed after the P V of the tile before it; in its second
+              // half the first's P V has to be through as well.
+              if (h == 1) {
+                ok = mbar_wait(&bars[P_PVDONE + k], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+              }
 #pragma unroll 1
               for (int x = 0; x < D; x += 16) {
                 uint32_t o[16];
@@ -412,13 +442,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (raise) m = -mn;
           }
           if (!ok) break;
-          tmem_st32(tS, pk);
-          tmem_st32(tS + 32, pk + 32);
+          tmem_st16(tS, pk);
+          tmem_st16(tS + 32, pk + 16);
           l += sum.x + sum.y;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[P_PFULL + e_bar(k, h)]);
+          if (lane == 0 && k == 0 && q == 0 && h == 1 && !split_keys) mbar_arrive(&bars[P_START]);
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(&bars[P_GEMPTY + st]);
@@ -457,7 +488,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     ++seg;
     u += nT;
   }
-  if (warp == 9) {
+  if (warp == 12 || warp == 13) {
+    // |v| >= 65536 (bf16 pattern 0x4780 and above, infinities included) is outside fp16.
+    const bool over = (vmax & 0xFFFFu) >= 0x4780u || (vmax >> 16) >= 0x4780u;
+    if (__any_sync(0xffffffffu, over) && lane == 0 && a.err) atomicOr(a.err, DEV_ERR_RANGE);
+  }
+  if (warp == 9 || warp == 14) {
     // Every MMA issued must retire before tensor memory is freed.
     umma_commit_e(elect_lane(), &bars[P_DONE]);
     mbar_wait_drain(&bars[P_DONE], 0);
