@@ -151,6 +151,13 @@ struct DecodeLayout {
   long long po_rows;
 };
 
+// Whether a prefix is worth sharing out: one kernel that walks it for every sequence takes as long as its
+// K and V take to come (mostly from the L2 cache) so many times; sharing takes two more kernels, some ten
+// microseconds here and there. At 96 MB both took XXX.
+bool share_prefix(const PagedArgs& a, int row_tiles) {
+  return (long long)a.B * row_tiles * a.prefix_len * a.Hkv * a.d * 4 > (96ll << 20);
+}
+
 DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   DecodeLayout L;
   const int G = a.H / a.Hkv;
@@ -168,7 +175,7 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   L.pml = align_up(L.po + sizeof(float) * slots * L.Rs * a.d, 256);
   L.ppo = L.end = L.pml;
   L.pre = PrefixPlan{};
-  if (!f32 && a.prefix_len > 0) {
+  if (!f32 && a.prefix_len > 0 && share_prefix(a, L.RTmax)) {
     L.pre = prefix_plan(a);
     const size_t rows = ((size_t)L.pre.workers + (size_t)a.Hkv * L.pre.items) * 2 * kTile;
     L.ppo = align_up(L.pml + sizeof(float2) * rows, 256);
@@ -196,7 +203,7 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.q_stride = x.q_stride;
   p.scale2 = x.scale * kLog2e;
   p.bias_from_j = x.bias_from_j;
-  p.walk_prefix = f32;
+  p.walk_prefix = x.a.prefix_len > 0 && L.pre.key_tiles == 0;
   p.o = x.o;
   p.lse = x.lse;
   p.Rt = L.Rt;

@@ -100,7 +100,7 @@ struct Place {
 
 __device__ __forceinline__ void load_seq(const DecodeParams& p, const Seq* seqs, Place& c) {
   c.s = seqs[c.b];
-  c.tiles = c.s.own < 0 ? 0 : ceil_div(c.s.own + (p.walk_prefix ? p.a.prefix_len : 0), kKeyTile);
+  c.tiles = walk_tiles(p.a, c.s.own, p.walk_prefix);
   c.rts = (c.s.n * p.Gp + p.Rt - 1) / p.Rt;
 }
 

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
   Seq* seqs = reinterpret_cast<Seq*>(smem + W * L::kWarpFloats);
   const PagedArgs& a = p.a;
   scan_sequences(p, seqs, scratch);
-  const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size, P = a.prefix_len;
+  const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size, P = a.prefix_len, tp = ceil_div(P, kKeyTile);
   const int total = seqs[a.B].u0 * a.Hkv, each = units_per_worker(total, p.workers);
   const int w = blockIdx.x * W + warp;
   const int u0 = min(total, w * each), u1 = min(total, u0 + each);
@@ -55,12 +55,12 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
   int page = -1, slot = 0;
   size_t kv = 0;
   auto find_key = [&](int tile) {
-    const int j = tile * kKeyTile + lane;
+    const bool pre = tile < tp;
+    const int j = (pre ? tile : tile - tp) * kKeyTile + lane;
     page = -1;
-    if (j < at.s.own + P) {
-      const int own = j - P;
-      page = j < P ? prefix_page(a, j) : own_page(a, at.b, own);
-      slot = (j < P ? j : own) & (S - 1);
+    slot = j & (S - 1);
+    if (j < (pre ? P : at.s.own)) {
+      page = pre ? prefix_page(a, j) : own_page(a, at.b, j);
       if (page < 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
     }
     kv = page < 0 ? 0 : kv_offset(a, page, at.hkv, slot);
@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
     }
 #pragma unroll 1
     for (int tile = tile0; tile < tile1; ++tile) {
-      const int j = tile * kKeyTile + lane, my_page = page, my_slot = slot;
+      // own place of this lane's key: before every row's for the prefix
+      const int j = tile < tp ? -1 : (tile - tp) * kKeyTile + lane, my_page = page, my_slot = slot;
       cp_async_wait<1>();  // K
       __syncwarp();
       float sc[kF32Rows];
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
         if (r >= R) break;
         float x = -INFINITY;
         const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
-        if (my_page >= 0 && j <= P + s.own - s.n + t) {
+        if (my_page >= 0 && j <= s.own - s.n + t) {
           const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, my_page, h));
           const int gs = p.bias_from_j ? my_slot - 1 : my_slot;
           const float gj = gs >= 0 ? a.g[g_offset(a, my_page, h, gs)] : 0.f;

@@ -62,8 +62,7 @@ struct MmaShape {
 // Up to 32 successive key tiles of one item. The table's entries for them (with pages of 16 tokens two a
 // tile) come to shared memory by asynchronous copies, so that no instruction waits for them before their use.
 struct Window {
-  int hkv, rt, tile, n;
-  bool half;  // the last tile's second page of 16 lies behind the sequence's end
+  int hkv, rt, tile, n, own;
 };
 
 template <int D, int NT>
@@ -105,6 +104,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   const int KS = S < kKeyTile ? S : kKeyTile;      // tokens of a sub-page
   const int heads = x.heads, gpitch = x.gpitch;
   const int base_off = (S == 16 ? 2 : 1) * x.gsub;
+  const int P = a.prefix_len, tp = p.walk_prefix ? ceil_div(P, kKeyTile) : 0;  // the prefix's tiles come first
   const int total = seqs[a.B].u0 * a.Hkv, each = units_per_worker(total, p.workers);
   const int w = blockIdx.x * W + warp;
   const int u0 = min(total, w * each), count = min(total, u0 + each) - u0;
@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     cp_async_wait<L::kStages - 1>();  // the stage's bases: so many groups were committed after theirs
     __syncwarp();
 
-    const int j0 = cur.tile * kKeyTile;
+    // The tile's keys are [j0, end) of the prefix, or of the sequence's own, which end for each row with its own.
+    const bool pre = cur.tile < tp;
+    const int j0 = (pre ? cur.tile : cur.tile - tp) * kKeyTile, end = pre ? P : cur.s.own;
     const uint32_t sk = smem_u32(st), sv = sk + L::kTileBytes;
     float s[2][NT][4];
 #pragma unroll
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     // Scores of keys mt * 16 + g8 (+ 8) and rows 2 t4 (+ 1), in log2 units.
     const uint8_t* sg = gates + stage * x.gstage;
     const float2* bs = reinterpret_cast<const float2*>(sg + base_off);
-    const bool edge = j0 + kKeyTile > cur.s.own - cur.s.n;  // some key is behind some row
+    const bool edge = j0 + kKeyTile > (pre ? P : cur.s.own - cur.s.n);  // some slot is no key of some row
     bool grow = false;
     float top[NT][2];
 #pragma unroll
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
           for (int k8 = 0; k8 < 2; ++k8) {
             const int key = g8 + k8 * 8;
             float x = fmaf(beta - gr[key], kLog2e, s[mt][nt][k8 * 2 + e] * p.scale2);
-            if (edge && j0 + mt * 16 + key > pos[nt][e]) x = -INFINITY;
+            if (edge && j0 + mt * 16 + key > (pre ? P - 1 : pos[nt][e])) x = -INFINITY;
             s[mt][nt][k8 * 2 + e] = x;
             top[nt][e] = fmaxf(top[nt][e], x);
           }
@@ -231,10 +233,10 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
           }
         }
     }
-    if (j0 + kKeyTile > cur.s.own) {
-      // Slots behind the sequence's end may hold anything: V there becomes 0 (its weights are 0).
-      for (int e = lane; e < (j0 + kKeyTile - cur.s.own) * (D / 8); e += 32) {
-        const int row = cur.s.own - j0 + e / (D / 8), c = e % (D / 8);
+    if (j0 + kKeyTile > end) {
+      // Slots behind the end may hold anything: V there becomes 0 (its weights are 0).
+      for (int e = lane; e < (j0 + kKeyTile - end) * (D / 8); e += 32) {
+        const int row = end - j0 + e / (D / 8), c = e % (D / 8);
         sts_v4(sv + (c >> 3) * (kKeyTile * 128) + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
       }
       fence_proxy_async_smem();  // before the next copy into this stage
@@ -356,13 +358,13 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
             next.rt = pro.rt;
             next.tile = pro.tile;
             next.n = min(min(32, pro.tiles - pro.tile), left);
-            const int last = (next.tile + next.n) * kKeyTile;
-            next.half = last - 16 >= pro.s.own;
-            const int* row = a.table + (size_t)pro.b * a.table_stride;
+            next.own = pro.s.own;
             if (lane < next.n) {
-              const int j = (pro.tile + lane) * kKeyTile;
+              const int t = pro.tile + lane, j = (t < tp ? t : t - tp) * kKeyTile;
+              const int* row = t < tp ? a.prefix : a.table + (size_t)pro.b * a.table_stride;
               cp_async4(smem_u32(&ids[warp][buf ^ 1][lane]), row + (j >> a.page_shift));
-              if (S == 16 && j + 16 < pro.s.own) cp_async4(smem_u32(&ids[warp][buf ^ 1][32 + lane]), row + (j >> 4) + 1);
+              if (S == 16 && j + 16 < (t < tp ? P : pro.s.own))
+                cp_async4(smem_u32(&ids[warp][buf ^ 1][32 + lane]), row + (j >> 4) + 1);
             }
             left -= next.n;
             pro.tile += next.n;
@@ -377,8 +379,8 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
       uint8_t* dst = ring + to * (2 * L::kTileBytes);
       uint8_t* sg = gates + to * x.gstage;
       const int h0 = now.hkv * G + (G > L::kRows ? now.rt * p.Rt % Gp : 0);
-      const int slot = S == 16 ? 0 : (now.tile + at) * kKeyTile & (S - 1);
-      const int subs = S == 16 && !(now.half && at + 1 == now.n) ? 2 : 1;
+      const int t = now.tile + at, j = (t < tp ? t : t - tp) * kKeyTile, slot = j & (S - 1);
+      const int subs = S == 16 && j + 16 < (t < tp ? P : now.own) ? 2 : 1;  // pages of 16: the second may be none
       if (lane == 0) mbar_arrive_expect_tx(&bars[warp][to], subs * (2 * KS * D * 2 + heads * gpitch * 4));
       __syncwarp();
 #pragma unroll 1

@@ -115,20 +115,21 @@ constexpr int kKeyTile = 32;
 
 FOX_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Keys that the item's own walk covers: the prefix too when nothing shares it out (`walk_prefix`).
-FOX_HD int walk_keys(const PagedArgs& a, const SeqInfo& s, bool walk_prefix) {
-  return s.own < 0 ? 0 : s.own + (walk_prefix ? a.prefix_len : 0);
+// Key tiles that a sequence's items walk: with `walk_prefix` (nothing shares the prefix out) the prefix's
+// first, then its own, each from a tile's start.
+FOX_HD int walk_tiles(const PagedArgs& a, int own, bool walk_prefix) {
+  return own < 0 ? 0 : (walk_prefix ? ceil_div(a.prefix_len, kKeyTile) : 0) + ceil_div(own, kKeyTile);
 }
 FOX_HD int padded_group(int G, int Rt) { return G <= Rt ? G : ceil_div(G, Rt) * Rt; }
 FOX_HD int seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, int Gp, bool walk_prefix) {
-  return ceil_div(walk_keys(a, s, walk_prefix), kKeyTile) * ceil_div(s.n * Gp, Rt);
+  return walk_tiles(a, s.own, walk_prefix) * ceil_div(s.n * Gp, Rt);
 }
 // The most units that the batch's tables and row counts allow: has to stay below 2^31 - workers, so
 // that places on the line are ints.
 FOX_HD long long most_units(const PagedArgs& a, int Rt, int Gp) {
   const long long cap = (long long)a.prefix_len + (long long)a.table_stride * a.page_size;
   const long long rows = (long long)a.max_new * Gp;
-  return (cap / kKeyTile + 1) * ((rows + Rt - 1) / Rt) * a.B * a.Hkv;
+  return (cap / kKeyTile + 2) * ((rows + Rt - 1) / Rt) * a.B * a.Hkv;
 }
 FOX_HD int units_per_worker(int total, int workers) {
   const int q = (total + workers - 1) / workers;

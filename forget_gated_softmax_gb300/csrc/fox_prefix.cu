@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               y = make_float4(slot == 0 ? 0.f : before, y.x, y.y, y.z);
             }
             // A slot behind the prefix's end may hold anything: some finite value instead (its S is masked).
+            if (j >= P) y.x = 0.f;
             if (j + 1 >= P) y.y = 0.f;
             if (j + 2 >= P) y.z = 0.f;
             if (j + 3 >= P) y.w = 0.f;

@@ -258,13 +258,16 @@ def test_work_line_gives_every_pair_of_worker_and_item_its_own_slot(H, workers):
         cu = [0]
         for x in new:
             cu.append(cu[-1] + x)
-        lens = [rng.choice([0, x + rng.randint(0, 1000)]) if x else rng.randint(0, 50) for x in new]
+        P, walk = rng.choice([0, 45]), rng.choice([0, 1])
+        own = [rng.choice([None, x + rng.randint(0, 1000)]) if x else rng.randint(1, 50) for x in new]
+        lens = [0 if y is None else P + y for y in own]
         Rt = rng.choice([8, 16, 32])
-        n = _n(H=G * Hkv, Hkv=Hkv, B=B, rows=max(1, cu[-1]), max_new=max(new + [1]), stride=100)
-        units = [H.t_units(n, _ints(cu), _ints(lens), b, Rt, 1) for b in range(B)]
+        n = _n(H=G * Hkv, Hkv=Hkv, B=B, rows=max(1, cu[-1]), max_new=max(new + [1]), stride=100, prefix=P)
+        units = [H.t_units(n, _ints(cu), _ints(lens), b, Rt, walk) for b in range(B)]
+        tiles_of = [0 if y is None else -(-y // 32) + (-(-P // 32) if walk else 0) for y in own]
         Gp = G if G <= Rt else -(-G // Rt) * Rt  # a token's rows fill whole row tiles, or lie in one
         rts = [-(-x * Gp // Rt) for x in new]
-        assert units == [(-(-y // 32)) * r for y, r in zip(lens, rts)]
+        assert units == [y * r for y, r in zip(tiles_of, rts)]
         total = sum(units) * Hkv
         each = H.t_each(total, workers)
         assert each * workers >= total and each >= 1
@@ -272,7 +275,7 @@ def test_work_line_gives_every_pair_of_worker_and_item_its_own_slot(H, workers):
         for h in range(Hkv):
             for b in range(B):
                 for rt in range(rts[b]):
-                    tiles, item = -(-lens[b] // 32), (h * B + b) * RTmax + rt
+                    tiles, item = tiles_of[b], (h * B + b) * RTmax + rt
                     if not tiles:
                         continue
                     for w in range(u // each, (u + tiles - 1) // each + 1):

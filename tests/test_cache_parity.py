@@ -225,6 +225,73 @@ def test_decode(fox, n, dtype):
     assert torch.equal(bits(o2[:last]), bits(o[:last])) and torch.equal(bits(lse2[:last]), bits(lse[:last]))
 
 
+# Behind prefixes long enough for the batch that they are shared out (one kernel for all sequences).
+SHARED = [
+    ([13, 1], [1, 1], 8, 8, 128, 64, 13001, dict(uniform=True, bias_from_j=True)),       # one row tile, keys split
+    ([3] * 40, [1] * 40, 4, 1, 128, 16, 5003, dict(uniform=True)),                        # two row tiles
+    ([20 + i % 3 for i in range(70)], [2] * 70, 12, 4, 64, 64, 1537, dict(tail=3)),       # five, a tail of one key
+    ([None if i % 5 == 2 else 6 + 11 * (i % 4) for i in range(64)], [1 + i % 5 for i in range(64)], 14, 2, 128, 32, 1664,
+     dict(tail=1)),                                                                       # odd group, idle ones, no tail
+    ([9] * 9, [1] * 9, 20, 1, 128, 128, 22001, dict(uniform=True, scale=0.2)),            # a group of two head chunks
+    ([40, 5, 77, 300], [33, 5, 40, 1], 6, 2, 64, 16, 10002, dict(bias_from_j=True)),      # many new tokens
+]
+
+
+@pytest.mark.parametrize("n", range(len(SHARED)))
+def test_decode_behind_a_shared_prefix(fox, n):
+    own, new, H, Hkv, d, S, P, more = SHARED[n]
+    more = dict(more)
+    bj, scale = more.pop("bias_from_j", False), more.pop("scale", None)
+    c = Case(own, new, H, Hkv, d, S, seed=150 + n, prefix=P, **more)
+    c.put()
+    cache, batch = c.cache(fox), c.batch(fox)
+    ws = fox.cache_workspace(cache, batch, c.rows)
+    ws[fox.FOX_CACHE_ZERO_BYTES :] = 0xFF
+    o, lse = torch.full_like(c.q, float("nan")), torch.full((c.rows, H), float("nan"), device="cuda")
+    fox.trace_begin()
+    fox.fox_decode(cache, batch, c.q, scale=scale or 0.0, bias_from_j=bj, o=o, lse=lse, ws=ws)
+    assert "prefix" in [k for k, _ in fox.trace_end()]
+    assert fox.fox_check_error(ws) == 0
+    last = sum(new)
+    assert torch.isnan(o[last:]).all() and torch.isnan(lse[last:]).all()
+    ro, rl = c.attend(bias_from_j=bj, scale=scale)
+    idle = torch.isinf(rl[:last])
+    assert torch.equal(idle, torch.isinf(lse[:last])) and (o[:last][idle] == 0).all()
+    assert_o(tensor_f64(o[:last]), tensor_f64(ro[:last]), "bf16", f"decode shared {n}")
+    assert (lse[:last].double() - rl[:last])[~idle].abs().max().item() <= foxtest.TOL_LSE_BF16
+    o2, lse2 = fox.fox_decode(cache, batch, c.q, scale=scale or 0.0, bias_from_j=bj, ws=ws)
+    assert torch.equal(bits(o2[:last]), bits(o[:last])) and torch.equal(bits(lse2[:last]), bits(lse[:last]))
+
+
+@pytest.mark.parametrize("B,P", [(3, 100), (40, 5003)])
+def test_bad_pages_of_a_prefix_are_reported(fox, B, P):
+    """Page ids of the prefix outside the pool: reported, read as page 0 (finite here), nothing else."""
+    c = Case([9] * B, [1] * B, 4, 1, 128, 16, uniform=True, prefix=P, seed=6)
+    c.put()
+    for t in (c.k, c.v, c.g, c.gbase):
+        t.nan_to_num_(0.0)
+    c.ptable[1], c.ptable[2] = c.k.shape[0], -1
+    cache, batch = c.cache(fox), c.batch(fox)
+    ws = fox.cache_workspace(cache, batch, c.rows)
+    fox.fox_decode(cache, batch, c.q, ws=ws)
+    assert fox.fox_check_error(ws) == FOX_ERR_DEVICE
+    assert fox.fox_check_error(ws) == 0
+
+
+def test_shared_values_outside_fp16_are_reported(fox):
+    """The shared prefix's P V runs in fp16, like fox_fwd's: a V of 65536 or more there sets the error word; the
+    same value among a sequence's own tokens, or in a prefix that is walked, is no error."""
+    for B, P, status in ((40, 5003, FOX_ERR_DEVICE), (3, 100, 0)):
+        for where in ("prefix", "own"):
+            c = Case([9] * B, [1] * B, 4, 1, 128, 16, uniform=True, prefix=P, seed=6)
+            (c.pre if where == "prefix" else c.seq[1])[1][5, 0, 7] = 1.0e6
+            c.put()
+            cache, batch = c.cache(fox), c.batch(fox)
+            ws = fox.cache_workspace(cache, batch, c.rows)
+            fox.fox_decode(cache, batch, c.q, ws=ws)
+            assert fox.fox_check_error(ws) == (status if where == "prefix" else 0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("own,new,H,Hkv,d,prefix", [
     ([70001], [1], 4, 1, 128, 0), ([30011, 5, 9000], [1, 3, 2], 8, 2, 64, 0), ([11], [1], 16, 16, 64, 20000),
@@ -404,9 +471,10 @@ def test_prompt_then_tokens_as_the_forward_sees_them(fox, d, S, bias_from_j):
     assert fox.fox_check_error(ws) == 0
 
 
-def test_a_shared_prefix_gives_what_copies_of_it_give(fox):
+@pytest.mark.parametrize("P", [200, 25001])
+def test_a_shared_prefix_gives_what_copies_of_it_give(fox, P):
     """Sequences behind one shared prefix, and the same sequences each with the prefix's tokens of its own."""
-    P, own, H, Hkv, d, S = 200, [40, 1, 17, 90], 8, 2, 128, 32
+    own, H, Hkv, d, S = [40, 1, 17, 90], 8, 2, 128, 32
     c = Case(own, [1] * 4, H, Hkv, d, S, prefix=P, uniform=True, seed=14)
     c.put()
     o, lse = fox.fox_decode(c.cache(fox), c.batch(fox), c.q)
@@ -422,7 +490,7 @@ def test_a_shared_prefix_gives_what_copies_of_it_give(fox):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("prefix,B", [(0, 5), (130, 5), (300, 40)])
+@pytest.mark.parametrize("prefix,B", [(0, 5), (130, 5), (300, 40), (7000, 40)])
 def test_captured_steps_replay_on_new_contents(fox, dtype, prefix, B):
     """Append and decode captured once and replayed while the lengths grow: bit for bit the eager calls."""
     H, Hkv, d, S, first, steps = 8, 2, 64, 16, 30, 5
@@ -473,7 +541,7 @@ def test_captured_steps_replay_on_new_contents(fox, dtype, prefix, B):
 
 
 def test_calls_on_another_stream_and_two_at_once(fox):
-    cases = [Case([3000, 50], [1, 1], 8, 2, 128, 64, uniform=True, seed=s, prefix=p) for s, p in ((1, 0), (2, 500))]
+    cases = [Case([3000, 50], [1, 1], 8, 2, 128, 64, uniform=True, seed=s, prefix=p) for s, p in ((1, 0), (2, 500), (3, 26000))]
     want = []
     for c in cases:
         c.put()
@@ -494,7 +562,7 @@ def test_calls_on_another_stream_and_two_at_once(fox):
 
 def test_back_to_back_calls_on_one_workspace(fox):
     cases = [Case(own, [1] * len(own), 8, 2, 128, 64, uniform=True, seed=40 + i, prefix=p)
-             for i, (own, p) in enumerate([([900] * 3, 0), ([10] * 3, 700), ([2000, 1, 1], 0)])]
+             for i, (own, p) in enumerate([([900] * 3, 0), ([10] * 3, 40000), ([2000, 1, 1], 0), ([10] * 3, 700)])]
     for c in cases:
         c.put()
     hs = [(c.cache(fox), c.batch(fox), c.q) for c in cases]
