@@ -153,9 +153,10 @@ struct DecodeLayout {
 
 // Whether a prefix is worth sharing out: one kernel that walks it for every sequence takes as long as its
 // K and V take to come (mostly from the L2 cache) so many times; sharing takes two more kernels, some ten
-// microseconds here and there. At 96 MB both took XXX.
+// microseconds here and there. At 50 MB walking took 26 to 27 us against 28 to 30, at 100 MB 29 to 34
+// against 30 to 33 (with 64 channels 50 against 40), at 200 MB 46 to 62 against 32 to 41.
 bool share_prefix(const PagedArgs& a, int row_tiles) {
-  return (long long)a.B * row_tiles * a.prefix_len * a.Hkv * a.d * 4 > (96ll << 20);
+  return (long long)a.B * row_tiles * a.prefix_len * a.Hkv * a.d * 4 > (72ll << 20);
 }
 
 DecodeLayout decode_layout(const PagedArgs& a, bool f32) {

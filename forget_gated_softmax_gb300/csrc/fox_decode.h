@@ -51,14 +51,19 @@ __device__ __forceinline__ int token_of(const DecodeParams& p, int r) {
 }
 
 // The sequences as every CTA holds them in shared memory, [B + 1]: units of one key head before the
-// sequence, its rows, its tokens after the prefix (SeqInfo). The kernels run most of their code once a
-// launch, and then wait for instructions as much as for data: what they look up is made compact here once.
+// sequence, its first row (its rows end where the next one's begin), its tokens after the prefix (SeqInfo;
+// kBadSeq: left out). The kernels run most of their code once a launch, and then wait for instructions as
+// much as for data: what they look up is made compact here once.
+struct SeqEntry {
+  int u0, row0, own;
+};
+constexpr int kBadSeq = -2;
 struct Seq {
   int u0, row0, n, own;
 };
 
 // Fills seqs[0 .. B] by the whole block; `scratch` holds one value a warp. Ends with a block barrier.
-__device__ __forceinline__ void scan_sequences(const DecodeParams& p, Seq* seqs, int* scratch) {
+__device__ __forceinline__ void scan_sequences(const DecodeParams& p, SeqEntry* seqs, int* scratch) {
   const PagedArgs& a = p.a;
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = ceil_div(a.B, nt), b0 = tid * each, b1 = min(a.B, b0 + each);
@@ -69,7 +74,7 @@ __device__ __forceinline__ void scan_sequences(const DecodeParams& p, Seq* seqs,
     bool bad;
     const SeqInfo s = seq_info(a, b, &bad);
     any_bad |= bad;
-    seqs[b] = {mine, s.row0, s.n, s.own};
+    seqs[b] = {mine, first_row(a, b), bad ? kBadSeq : s.own};
     mine += seq_units(a, s, p.Rt, p.Gp, p.walk_prefix);
   }
   if (any_bad && blockIdx.x == 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
@@ -86,7 +91,7 @@ __device__ __forceinline__ void scan_sequences(const DecodeParams& p, Seq* seqs,
   for (int w = 0; w < warp; ++w) before += scratch[w];
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) seqs[b].u0 += before;
-  if (b0 < a.B && b1 == a.B) seqs[a.B].u0 = before + mine;
+  if (b0 < a.B && b1 == a.B) seqs[a.B] = {before + mine, first_row(a, a.B), kBadSeq};
   __syncthreads();
 }
 
@@ -98,14 +103,15 @@ struct Place {
   Seq s;
 };
 
-__device__ __forceinline__ void load_seq(const DecodeParams& p, const Seq* seqs, Place& c) {
-  c.s = seqs[c.b];
+__device__ __forceinline__ void load_seq(const DecodeParams& p, const SeqEntry* seqs, Place& c) {
+  const SeqEntry e = seqs[c.b];
+  c.s = {e.u0, e.row0, seqs[c.b + 1].row0 - e.row0, e.own};
   c.tiles = walk_tiles(p.a, c.s.own, p.walk_prefix);
   c.rts = (c.s.n * p.Gp + p.Rt - 1) / p.Rt;
 }
 
 // Unit u of the line (0 <= u < total).
-static __device__ __noinline__ Place place_of(const DecodeParams& p, const Seq* seqs, int u) {
+static __device__ __noinline__ Place place_of(const DecodeParams& p, const SeqEntry* seqs, int u) {
   Place c;
   const int per_head = seqs[p.a.B].u0;
   c.hkv = u / per_head;
@@ -129,7 +135,7 @@ static __device__ __noinline__ Place place_of(const DecodeParams& p, const Seq* 
 }
 
 // The first unit of the next item; there is one.
-static __device__ __noinline__ void next_item(const DecodeParams& p, const Seq* seqs, Place& c) {
+static __device__ __noinline__ void next_item(const DecodeParams& p, const SeqEntry* seqs, Place& c) {
   c.i0 += c.tiles;
   c.tile = 0;
   if (++c.rt < c.rts) return;
@@ -148,13 +154,14 @@ static __device__ __noinline__ void next_item(const DecodeParams& p, const Seq* 
 struct Gate2 {
   float hi, lo;
 };
-__device__ __forceinline__ Gate2 gate_sum(const PagedArgs& a, int page, int slot, int h) {
-  const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
-  const float g = a.g[g_offset(a, page, h, slot)];
+__device__ __forceinline__ Gate2 gate_sum(float2 base, float g) {
   // base.x + g = s + e exactly (the rounding error of an fp32 sum is an fp32 value)
   const float s = __fadd_rn(base.x, g), t = __fsub_rn(s, base.x);
   const float e = __fadd_rn(__fsub_rn(base.x, __fsub_rn(s, t)), __fsub_rn(g, t));
   return {s, e + base.y};
+}
+__device__ __forceinline__ Gate2 gate_sum(const PagedArgs& a, int page, int slot, int h) {
+  return gate_sum(*reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h)), a.g[g_offset(a, page, h, slot)]);
 }
 
 // A table entry as a page; page 0 with a report where it is none.
@@ -195,6 +202,7 @@ struct MmaLayout {
   static constexpr int kStages = 2;
   static constexpr int kRows = 8 * NT;
   static constexpr int kTileBytes = kKeyTile * D * 2;  // K or V of a stage
+  static constexpr int kQBytes = kRows * D * 2;        // an item's Q: chunk c (16 bytes) of row r at c ^ (r & 7)
   static constexpr int kOutStride = D + 4;             // a result row in shared memory, in floats
   static_assert(kRows * kOutStride * 4 <= 2 * kTileBytes, "results pass through a stage that was read");
 };
@@ -289,7 +297,7 @@ struct BlockEnds {
   int first[2], blocks[2];  // first CTA of the item; its CTAs, 0 where none is cut there (or it is the other end's)
 };
 template <int kWarps>
-__device__ __forceinline__ void find_ends(const DecodeParams& p, const Seq* seqs, int total, int each, BlockEnds& x) {
+__device__ __forceinline__ void find_ends(const DecodeParams& p, const SeqEntry* seqs, int total, int each, BlockEnds& x) {
   const int tid = threadIdx.x, U0 = min(total, static_cast<int>(blockIdx.x) * kWarps * each);
   const int U1 = min(total, U0 + kWarps * each);
   if (tid >= 2) return;
@@ -311,7 +319,7 @@ __device__ __forceinline__ void find_ends(const DecodeParams& p, const Seq* seqs
 // (floats). `offs`: [CTAs + 1] and `part`: [threads] of shared memory, clear of the kept rows.
 // With a shared prefix every item is left to the merge that follows, its partial results as above.
 template <typename T, int D, int kRows, int kWarps>
-__device__ __forceinline__ void join_items(const DecodeParams& p, const Seq* seqs, int total, int each,
+__device__ __forceinline__ void join_items(const DecodeParams& p, const SeqEntry* seqs, int total, int each,
                                            const Kept<kRows, kWarps>& kept, const BlockEnds& ends, const float* rows, int warp_pitch,
                                            int row_pitch, int* offs, Column* part) {
   constexpr int kThreads = 32 * kWarps, C4 = D / 4;
@@ -436,12 +444,12 @@ __device__ __forceinline__ void join_items(const DecodeParams& p, const Seq* seq
 
 // Rows of idle sequences: O = 0, LSE = -inf. The blocks share the sequences out.
 template <typename T, int D>
-__device__ __forceinline__ void clear_idle_rows(const DecodeParams& p, const Seq* seqs) {
+__device__ __forceinline__ void clear_idle_rows(const DecodeParams& p, const SeqEntry* seqs) {
 #pragma unroll 1
   for (int b = blockIdx.x; b < p.a.B; b += gridDim.x) {
-    const Seq s = seqs[b];
-    if (s.own >= 0) continue;
-    const size_t at = (size_t)s.row0 * p.a.H, n = (size_t)s.n * p.a.H;
+    const SeqEntry s = seqs[b];
+    if (s.own >= 0 || s.own == kBadSeq) continue;
+    const size_t at = (size_t)s.row0 * p.a.H, n = (size_t)(seqs[b + 1].row0 - s.row0) * p.a.H;
 #pragma unroll 1
     for (size_t e = threadIdx.x; e < n * (D / 4); e += blockDim.x)
       put4<T>(static_cast<T*>(p.o) + (at * D + 4 * e), make_float4(0.f, 0.f, 0.f, 0.f));

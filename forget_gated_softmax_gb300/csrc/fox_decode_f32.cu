@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
   float* ks = smem + warp * L::kWarpFloats;
   float* vs = ks + kKeyTile * L::kKPitch;
   float* qs = vs + kKeyTile * D;  // [kF32Rows][D] scaled queries; at a segment's end its rows of O
-  Seq* seqs = reinterpret_cast<Seq*>(smem + W * L::kWarpFloats);
+  SeqEntry* seqs = reinterpret_cast<SeqEntry*>(smem + W * L::kWarpFloats);
   const PagedArgs& a = p.a;
   scan_sequences(p, seqs, scratch);
   const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size, P = a.prefix_len, tp = ceil_div(P, kKeyTile);
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
 template <int D>
 cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
   using L = F32Layout<D>;
-  const size_t smem = sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(Seq) * ((size_t)p.a.B + 1);
-  static_assert(sizeof(float) * kF32Warps * F32Layout<128>::kWarpFloats + sizeof(Seq) * (kMaxSeqs + 1) <= 232448 - 8192,
+  const size_t smem = sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * ((size_t)p.a.B + 1);
+  static_assert(sizeof(float) * kF32Warps * F32Layout<128>::kWarpFloats + sizeof(SeqEntry) * (kMaxSeqs + 1) <= 232448 - 8192,
                 "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(decode_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

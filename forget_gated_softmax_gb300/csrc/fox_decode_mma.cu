@@ -65,6 +65,18 @@ struct Window {
   int hkv, rt, tile, n, own;
 };
 
+// An item's rows are asked for by asynchronous copies while the item before is computed: Q and the gates when
+// that one begins, for which the table's entries for the rows' own tokens are there, asked for an item earlier.
+// Against loads when the item begins: 256 sequences of about 500 87 -> 81 us, one of 65536 61 -> 59, five guessed
+// tokens behind 8 long ones 70.6 -> 69.1; 128 of about 200 with 64 channels 37.9 -> 39.4.
+template <int kRows>
+struct ItemRows {
+  Place at[2];         // by the item's number & 1, as the entries are
+  int page[2][kRows];
+  float g[kRows];
+  float2 base[kRows];
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -79,14 +91,17 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   __shared__ Kept<L::kRows, W> kept;
   __shared__ int ids[W][2][64];
   __shared__ BlockEnds ends;
+  __shared__ ItemRows<L::kRows> rows_of[W];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &abort_word;
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ItemRows<L::kRows>& it = rows_of[warp];
   constexpr int stages = L::kStages;
   uint8_t* ring = sm + warp * stages * (2 * L::kTileBytes);
   uint8_t* gates = sm + W * stages * (2 * L::kTileBytes) + warp * stages * x.gstage;
-  Seq* seqs = reinterpret_cast<Seq*>(sm + W * stages * (2 * L::kTileBytes + x.gstage));
+  uint8_t* q_of = sm + W * stages * (2 * L::kTileBytes + x.gstage) + warp * L::kQBytes;
+  SeqEntry* seqs = reinterpret_cast<SeqEntry*>(sm + W * (stages * (2 * L::kTileBytes + x.gstage) + L::kQBytes));
 
   grid_dep_trigger();
   if (threadIdx.x == 0) abort_word = 0;
@@ -115,13 +130,15 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   float m[NT][2], l[NT][2];
   Gate2 ci[NT][2];
   int pos[NT][2], gidx[NT][2];
-  int pg[NT][2];  // table entries, as they are: nothing waits for them before `opened`
   // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
   const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
 
   // The consumer's place, and the producer's, which runs ahead by a window or two.
   Place cur = {}, pro = {};
+  // The step that opened the item; items whose entries, and whose Q and gates, were asked for;
+  // the units of the first `asked` ones.
+  int since = -stages, asked = 0, filled = 0, ahead = 0;
   if (count > 0) cur = pro = place_of(p, seqs, u0);
   Window now = {}, next = {};
   int left = count, at = 0, buf = 0;  // units that no window holds yet; the producer's next tile of `now`; now's ids
@@ -135,21 +152,42 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     if (n == 0 && warp == 0) find_ends<W>(p, seqs, total, each, ends);  // while the first copies are on their way
     if (n >= 0) {
     if (!opened) {
-      // The item's rows: their cumulative gates, and nothing summed yet.
+      // The item's rows: Q fragments, and places and cumulative gates of this thread's columns of S^T, rows
+      // 2 t4 and 2 t4 + 1; nothing summed yet.
       opened = true;
-      const int h0 = cur.hkv * G + (G > L::kRows ? cur.rt * p.Rt % Gp : 0);
+      if (n - since > 1)
+        cp_async_wait<1>();  // asked for before the last step
+      else
+        cp_async_wait<0>();
+      __syncwarp();
+      since = n;
+      fresh = true;
+      const uint32_t qa = smem_u32(q_of);
+      const int r0 = cur.rt * p.Rt;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += 2) {
+          uint32_t f[4];
+          const int row = nt * 8 + (lane & 7), chunk = ks * 2 + (lane >> 3);
+          ldsm4(qa + row * (D * 2) + ((chunk ^ (row & 7)) << 4), f);
+          qf[ks][nt][0] = f[0];
+          qf[ks][nt][1] = f[1];
+          qf[ks + 1][nt][0] = f[2];
+          qf[ks + 1][nt][1] = f[3];
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const int rl = nt * 8 + 2 * t4 + e, r = r0 + rl, t = token_of(p, r), g = r - t * Gp;
+          const bool here = t < cur.s.n && g < G;
+          pos[nt][e] = cur.s.own - cur.s.n + t;
+          gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : 0;
           ci[nt][e] = {-INFINITY, 0.f};  // an empty row's scores are -inf
-          if (gidx[nt][e] >= 0)
-            ci[nt][e] = gate_sum(a, checked_page(a, pg[nt][e]), pos[nt][e] & (S - 1), h0 + gidx[nt][e]);
-          else
-            gidx[nt][e] = 0;
+          if (here) ci[nt][e] = gate_sum(it.base[rl], it.g[rl]);
           m[nt][e] = -INFINITY;
           l[nt][e] = 0.f;
         }
+      }
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
@@ -307,7 +345,6 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
       fence_proxy_async_smem();  // before the next copy into this stage
       __syncwarp();
       opened = false;
-      fresh = true;
     }
     if (++cur.tile == cur.tiles && n + 1 < count) next_item(p, seqs, cur);
     if (++stage == stages) {
@@ -316,30 +353,26 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     }
     }
 
-    if (fresh && n + 1 < count) {
-      // The next item's rows: Q fragments (row g8 of each eight), and the pages of this thread's columns of
-      // S^T, rows 2 t4 and 2 t4 + 1.
-      fresh = false;
-      const int r0 = cur.rt * p.Rt;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = r0 + nt * 8 + 2 * t4 + e, t = token_of(p, r), g = r - t * Gp;
-          const bool here = t < cur.s.n && g < G;
-          pos[nt][e] = cur.s.own - cur.s.n + t;
-          gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : -1;
-          pg[nt][e] = here ? a.table[(size_t)cur.b * a.table_stride + (pos[nt][e] >> a.page_shift)] : 0;
+    if (fresh) {
+      // Table entries of the rows of the item after the next.
+      __syncwarp();
+#pragma unroll 1
+      while (asked < filled + 2 && ahead < count) {
+        Place at_item = cur;
+        if (asked > 0) {
+          at_item = it.at[(asked - 1) & 1];
+          next_item(p, seqs, at_item);
         }
-        const int r = r0 + nt * 8 + g8, t = token_of(p, r), g = r - t * Gp;
-        const bool in = t < cur.s.n && g < G;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(cur.s.row0 + (in ? t : 0)) * p.q_stride +
-                                   (size_t)(cur.hkv * G + (in ? g : 0)) * D + 2 * t4;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          qf[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
-          qf[ks][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+        const int slot = asked & 1;
+        ahead += at_item.tiles - at_item.tile;
+        ++asked;
+        if (lane == 0) it.at[slot] = at_item;
+        const int r = at_item.rt * p.Rt + lane, t = token_of(p, r), g = r - t * Gp;
+        if (lane < L::kRows && t < at_item.s.n && g < G) {
+          const int j = at_item.s.own - at_item.s.n + t;
+          cp_async4(smem_u32(&it.page[slot][lane]), a.table + (size_t)at_item.b * a.table_stride + (j >> a.page_shift));
         }
+        __syncwarp();
       }
     }
     if (n + stages < count) {
@@ -350,7 +383,8 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
         do {
           now = next;
           buf ^= 1;
-          cp_async_wait_all();  // now's ids; they were asked for a window ago
+          if (n < 0) cp_async_commit();
+          cp_async_wait<0>();  // now's ids; they were asked for a window ago
           __syncwarp();
           next.n = 0;
           if (left > 0) {
@@ -371,6 +405,36 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
             if (pro.tile == pro.tiles && left > 0) next_item(p, seqs, pro);
           }
         } while (now.n == 0);
+      }
+    }
+    if (fresh) {
+      // Q and gates of the rows of the next item, at the start of the first.
+      fresh = false;
+      if (n < 0) cp_async_commit();
+      cp_async_wait<0>();  // the entries, asked for in an earlier step (but the first item's)
+      __syncwarp();
+      if (filled < asked) {
+        const int slot = filled & 1;
+        const Place at_item = it.at[slot];
+        const int r0 = at_item.rt * p.Rt;
+        {
+          const int r = r0 + lane, t = token_of(p, r), g = r - t * Gp, h = at_item.hkv * G + g;
+          if (lane < L::kRows && t < at_item.s.n && g < G) {
+            const int page = checked_page(a, it.page[slot][lane]);
+            cp_async8(smem_u32(&it.base[lane]), a.gbase + gbase_offset(a, page, h));
+            cp_async4(smem_u32(&it.g[lane]), a.g + g_offset(a, page, h, (at_item.s.own - at_item.s.n + t) & (S - 1)));
+          }
+        }
+#pragma unroll 1
+        for (int e = lane; e < L::kRows * (D / 8); e += 32) {
+          const int rl = e / (D / 8), chunk = e % (D / 8), r = r0 + rl, t = token_of(p, r), g = r - t * Gp;
+          const bool in = t < at_item.s.n && g < G;
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                     (size_t)(at_item.s.row0 + (in ? t : 0)) * p.q_stride +
+                                     (size_t)(at_item.hkv * G + (in ? g : 0)) * D + chunk * 8;
+          cp_async16_or_0(smem_u32(q_of + rl * (D * 2) + ((chunk ^ (rl & 7)) << 4)), src, in);
+        }
+        ++filled;
       }
     }
     if (n + stages < count) {
@@ -430,11 +494,13 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
   x.gsub = (x.heads * x.gpitch * 4 + 127) / 128 * 128;
   x.gstage = subs * x.gsub + (subs * x.heads * 8 + 127) / 128 * 128;
   constexpr int kMostGates = 2 * ((L::kRows * 20 * 4 + 127) / 128 * 128) + 256;
-  constexpr size_t kMost = 232448 - 6144;  // of an SM's shared memory, less the static part
-  const size_t fixed = 1024 + sizeof(Seq) * ((size_t)p.a.B + 1);
+  constexpr size_t kMost = 232448 - 12288;  // of an SM's shared memory, less the static part
+  const size_t fixed = 1024 + (size_t)L::kWarps * L::kQBytes + sizeof(SeqEntry) * ((size_t)p.a.B + 1);
   const size_t one = (size_t)L::kWarps * (2 * L::kTileBytes + x.gstage);
   const size_t smem = fixed + L::kStages * one;
-  static_assert(1024 + sizeof(Seq) * (kMaxSeqs + 1) + L::kStages * L::kWarps * (2 * L::kTileBytes + kMostGates) <= kMost, "shared memory");
+  static_assert(1024 + sizeof(SeqEntry) * (kMaxSeqs + 1) +
+                        L::kWarps * (L::kQBytes + L::kStages * (2 * L::kTileBytes + kMostGates)) <= kMost,
+                "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;

@@ -38,17 +38,12 @@ struct SeqInfo {
   int row0, n, own;
 };
 
+FOX_HD int first_row(const PagedArgs& a, int b) { return a.cu ? a.cu[b] : a.rows / a.B * b; }
+
 FOX_HD SeqInfo seq_info(const PagedArgs& a, int b, bool* bad) {
   SeqInfo s;
-  int r1;
-  if (a.cu) {
-    s.row0 = a.cu[b];
-    r1 = a.cu[b + 1];
-  } else {
-    const int each = a.rows / a.B;
-    s.row0 = b * each;
-    r1 = s.row0 + each;
-  }
+  s.row0 = first_row(a, b);
+  const int r1 = first_row(a, b + 1);
   const int len = a.lens[b];
   const long long cap = (long long)a.prefix_len + (long long)a.table_stride * a.page_size;
   const bool rows_ok = s.row0 >= 0 && r1 >= s.row0 && r1 <= a.rows && r1 - s.row0 <= a.max_new;
