@@ -8,25 +8,33 @@
 // those of the sequences' own keys; the row's c_i - c_last enters there.
 //
 // A row tile is `hp` query heads of the key head's group x `tpt` tokens: row r is head r / tpt, token
-// r % tpt, so that most warps' rows have one head and read its gate terms by one address. Key tiles of an item (key head, row tiles) run from the last to the first: the bias falls
-// with distance, so the first tile nearly always holds the row maximum. Work is split like the own
-// keys' (fox_paged.h): the items' key tiles on one line, equal ranges of it to the CTAs, one CTA an SM.
+// r % tpt, so that most warps' rows have one head and read its gate terms by one address. Key tiles of an
+// item (key head, row tiles) run from the last to the first: the bias falls with distance, so the first
+// tile nearly always holds the row maximum. Work is split like the own keys' (fox_paged.h): the items' key
+// tiles on one line, equal ranges of it to the CTAs, one CTA an SM.
 //
 // Two streams of softmax warps share the tensor core, each with its S and O in tensor memory:
 //   more than one row tile a key head: an item is two row tiles, one a stream, on the same key tiles;
 //   one row tile: the streams take alternate key tiles, and leave a partial result each.
-// A stream's P goes to the tensor core in two halves of 64 keys, so that one half's P V runs during the
-// other's softmax.
-// Warp roles (480 threads): warps 0-3 and 4-7 the streams' softmax (thread = row = TMEM lane), warp 8
+// A tile passes between softmax and tensor core in two halves of 64 keys: once a half's P V is issued, S of
+// the same half of the next tile is, into the columns that P leaves. So the softmax of one half runs while
+// the other is multiplied (S of whole tiles: 162 against 150 us at 32768 keys and 1024 rows a key head,
+// although MMAs 64 columns wide read Q twice).
+// Warp roles (512 threads): warps 0-3 and 4-7 the streams' softmax (thread = row = TMEM lane), warp 8
 // loads Q and K, warps 9 and 14 issue the streams' MMAs (one warp for both spent 1.7 us a key tile on
 // waits, fences and commits that two have side by side), warps 10-11 load V and make the gate terms
-// log2 e (c_j - c_last) of a key tile's keys and the row tile's heads, a stage each, and warps 12-13 turn
-// each V tile from bf16 to fp16 in place.
+// log2 e (c_j - c_last) of a key tile's keys and the row tile's heads, a stage each, and warps 12, 13 and 15
+// turn each V tile from bf16 to fp16 in place.
 //
 // P V runs in fp16, as in fox_attn_fwd_kernel and for its reason: with bf16 P its 8 significant bits add an
 // error as large as O's own rounding. Two bf16 terms a weight (as in fox_decode_mma.cu, where products
-// cost nothing) made the tensor core the bound: 2.8 us a pair of 128 x 128 tiles. A magnitude of 65536 or
-// more in V (outside fp16) sets DEV_ERR_RANGE. A 32-column chunk of S, once read, holds its P.
+// cost nothing) made the tensor core the bound: 2.8 us a pair of 128 x 128 tiles, against 2.2 now. A magnitude
+// of 65536 or more in V (outside fp16) sets DEV_ERR_RANGE. A 32-column chunk of S, once read, holds its P.
+//
+// 32768 keys, 256 sequences x 4 heads a key head, 8 of these, d = 128: 137 us, 1000 TFLOP/s, half of cuBLAS's
+// bf16 peak. What bounds it: the softmax warps' issue, two of them a scheduler at about four cycles an
+// instruction while both streams compute. Without the conversion of V it would take 132 us; 168 registers for
+// the softmax (88 for the others) took no less.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,7 +43,8 @@
 namespace fox {
 namespace {
 
-constexpr int kPrefixThreads = 480;
+constexpr int kPrefixThreads = 512;
+constexpr int kConverters = 3;  // two: 142 us where three take 137
 constexpr int kMaxHp = 16;
 constexpr int kKapPitch = kTile + 4;  // floats: the heads' rows start in different banks
 constexpr float kRaise = 8.0f;        // log2 units that a row may pass its running maximum by
@@ -57,14 +66,13 @@ enum PBar {
   P_VEMPTY = 7,
   P_GFULL = 9,   // +stage: the key tile's gate terms are in place
   P_GEMPTY = 11,
-  P_SFULL = 13,  // +stream
-  P_OFINAL = 15,
-  P_PFULL = 17,  // +2 stream + half
-  P_PVDONE = 21,  // +stream: P V of the first half
-  P_VREADY = 23,  // +stage: V in fp16, and 0 behind the prefix's end
-  P_START = 25,   // stream 0 has its first P of the segment: stream 1 may begin
-  P_DONE = 26,
-  P_COUNT = 27,
+  P_SFULL = 13,   // +2 stream + half of the tile's keys
+  P_PFULL = 17,   // +2 stream + half
+  P_PVDONE = 21,  // +2 stream + half: that P V is through
+  P_OFINAL = 25,  // +stream
+  P_VREADY = 27,  // +stage: V in fp16, and 0 behind the prefix's end
+  P_DONE = 29,
+  P_COUNT = 30,
 };
 
 __host__ __device__ constexpr int e_bar(int stream, int half) { return 2 * stream + half; }
@@ -90,9 +98,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   grid_dep_trigger();  // the own keys' kernel may start where this one leaves room: it needs nothing from here
   if (threadIdx.x < P_COUNT) {
     const int i = threadIdx.x;
-    mbar_init(&bars[i], (i >= P_PFULL && i < P_PFULL + 4) || i == P_START ? 4
+    mbar_init(&bars[i], i >= P_PFULL && i < P_PFULL + 4 ? 4
                         : i >= P_GEMPTY && i < P_GEMPTY + 2 ? (split_keys ? 4 : 8)
-                        : i >= P_VREADY && i < P_VREADY + 2                                     ? 2
+                        : i >= P_VREADY && i < P_VREADY + 2                                     ? kConverters
                         : i == P_KEMPTY || i == P_KEMPTY + 1 || i == P_VEMPTY || i == P_VEMPTY + 1
                             ? (split_keys ? 1 : 2)  // the streams that use a key tile
                         : i == P_DONE ? 2
@@ -179,17 +187,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int k = warp == 14;  // the stream
       const int mine = k ? n1 : n0;
       const uint32_t leader = elect_lane();
-      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
       constexpr uint32_t idO = idesc_f16(128, D, false, true);
       const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::kQ + (split_keys ? 0 : k * L::kTileBytes)), 16, 1024);
       const uint64_t dK = sdesc_sw128(smem_u32(sm + L::kK), 16, 1024);
       const uint64_t dV = sdesc_sw128(smem_u32(sm + L::kV), 16384, 1024);
       const uint32_t tS = tbase + k * 128, tO = tbase + 256 + k * D;
       ok = ok && mbar_wait(&bars[P_Q], seg & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-      // On the same key tiles the streams keep out of step, each on the tensor core during the other's softmax:
-      // in step, both did the same at once (2.6 us a pair of tiles, X with stream 1 begun half a tile later).
-      if (ok && k == 1 && mine > 0 && !split_keys)
-        ok = mbar_wait(&bars[P_START], seg & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
       // Step s: P V of the stream's key tile s, and S of its next; the step before the first only has the S.
 #pragma unroll 1
       for (int s = split_keys ? k - 2 : -1, q = -1; s < nT && ok; s += step, ++q) {
@@ -207,48 +211,43 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           continue;
         }
         const uint64_t vd = dV + ((c & 1) ? L::kTileBytes >> 4 : 0), kd = dK + ((cn & 1) ? L::kTileBytes >> 4 : 0);
-        // O += P V over 64 keys: rows 64 h on of V
-        auto issue_pv = [&](int h, uint32_t acc) {
+        if (pv) ok = mbar_wait(&bars[P_VREADY + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+#pragma unroll 1
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (pv) {
+            ok = mbar_wait(&bars[P_PFULL + e_bar(k, h)], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+            if (!ok) break;
+            tc_fence_after();
+            // O += P V over 64 keys: rows 64 h on of V
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_ts_e(leader, tO, tS + h * 64 + 32 * (ks >> 1) + 8 * (ks & 1),
-                      vd + static_cast<uint64_t>((h * 8192 + ks * 2048) >> 4), idO, ks > 0 ? 1u : acc);
-        };
-        if (pv) {
-          ok = mbar_wait(&bars[P_VREADY + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC) &&
-               mbar_wait(&bars[P_PFULL + e_bar(k, 0)], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(0, q > 0);
-          umma_commit_e(leader, &bars[P_PVDONE + k]);
-        }
-        if (next) ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
-        if (pv) {
-          ok = ok && mbar_wait(&bars[P_PFULL + e_bar(k, 1)], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(1, 1u);
-        }
-        if (!ok) break;
-        if (pv) umma_commit_e(leader, &bars[P_VEMPTY + (c & 1)]);
-        if (next) {
-          if (!pv) tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t off = static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
-            umma_ss_e(leader, tS, dQ + off, kd + off, idS, ks > 0);
+            for (int ks = 0; ks < 4; ++ks)
+              umma_ts_e(leader, tO, tS + h * 64 + 32 * (ks >> 1) + 8 * (ks & 1),
+                        vd + static_cast<uint64_t>((h * 8192 + ks * 2048) >> 4), idO, q > 0 || h > 0 || ks > 0);
+            umma_commit_e(leader, &bars[P_PVDONE + e_bar(k, h)]);
+            if (h == 1) umma_commit_e(leader, &bars[P_VEMPTY + (c & 1)]);
           }
-          umma_commit_e(leader, &bars[P_SFULL + k]);
-          umma_commit_e(leader, &bars[P_KEMPTY + (cn & 1)]);
-        } else {
-          umma_commit_e(leader, &bars[P_OFINAL + k]);
+          if (next) {
+            if (h == 0) ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+            if (!ok) break;
+            if (!pv) tc_fence_after();
+            // S of the same 64 columns, whose P is read by then (MMAs run in order)
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_ss_e(leader, tS + h * 64, dQ + static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                        kd + static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32 + h * 8192) >> 4), idS, ks > 0);
+            umma_commit_e(leader, &bars[P_SFULL + e_bar(k, h)]);
+            if (h == 1) umma_commit_e(leader, &bars[P_KEMPTY + (cn & 1)]);
+          } else if (h == 1) {
+            umma_commit_e(leader, &bars[P_OFINAL + k]);
+          }
         }
       }
-    } else if (warp == 12 || warp == 13) {
+    } else if (warp >= 12) {
       // --------------------------------------------- V from bf16 to fp16
-      // The two warps take alternate 16-byte pieces of the swizzled layout TMA wrote; the conversion is per
-      // element, so the layout is unchanged. Slots behind the prefix's end may hold anything: V there
-      // becomes 0 (its weights are 0).
+      // The warps take 16-byte pieces of the swizzled layout TMA wrote in turn; the conversion is per element,
+      // so the layout is unchanged. Slots behind the prefix's end may hold anything: V there becomes 0 (its
+      // weights are 0).
+      const int first = (warp == 15 ? kConverters - 1 : warp - 12) * 32 + lane;
 #pragma unroll 1
       for (int s = 0; s < nT && ok; ++s) {
         const int c = c0 + s, st = c & 1, keys = P - (t1 - 1 - s) * kTile;
@@ -256,15 +255,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint4* tile = reinterpret_cast<uint4*>(sm + L::kV + st * L::kTileBytes);
-#pragma unroll 8
-        for (int e = (warp - 12) * 32 + lane; e < L::kTileBytes / 16; e += 64) {
+        if (keys < kTile)
+#pragma unroll 1
+          for (int e = first; e < L::kTileBytes / 16; e += 32 * kConverters)  // eight pieces a row of 64 channels
+            if (((e >> 3) & (kTile - 1)) >= keys) tile[e] = make_uint4(0, 0, 0, 0);
+        // No further unrolled: in bursts the softmax waits for its loads of shared memory (by 2 137 us, by 4 153,
+        // by 8 171 at 32768 keys and 1024 rows a key head).
+#pragma unroll 2
+        for (int e = first; e < L::kTileBytes / 16; e += 32 * kConverters) {
           const uint4 w = tile[e];
           const uint32_t in[4] = {w.x, w.y, w.z, w.w};
           uint32_t out[4];
-          const bool key = ((e >> 3) & (kTile - 1)) < keys;  // eight pieces a row of 64 channels
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t x = key ? in[i] : 0u;
+            const uint32_t x = in[i];
             out[i] = pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
             asm("max.u16x2 %0, %0, %1;" : "+r"(vmax) : "r"(x & 0x7FFF7FFFu));
           }
@@ -368,13 +372,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       for (int s = 0; s < nT && ok; ++s) {
         if (split_keys && (s & 1) != k) continue;
         const int c = c0 + s, st = c & 1;
-        ok = (mine == 0 || mbar_wait(&bars[P_SFULL + k], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA)) &&
-             mbar_wait(&bars[P_GFULL + st], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-        ok = __all_sync(0xffffffffu, ok);  // the tcgen05 loads below are warp-collective
-        if (!ok) break;
-        tc_fence_after();
+        ok = mbar_wait(&bars[P_GFULL + st], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
 #pragma unroll 1
         for (int h = 0; h < 2 && mine > 0 && ok; ++h) {
+          ok = mbar_wait(&bars[P_SFULL + e_bar(k, h)], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
+          ok = __all_sync(0xffffffffu, ok);  // the tcgen05 loads below are warp-collective
+          if (!ok) break;
+          tc_fence_after();
           const uint32_t tS = tbase + k * 128 + h * 64 + lane_off;
           const float* kap = reinterpret_cast<const float*>(sm + L::kKap) +
                              (st * pp.hp * pp.kap_tiles + kap_row) * kKapPitch + h * 64;
@@ -422,14 +426,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const float alpha = raise ? ex2_approx(m + mn) : 1.f;
             l *= alpha;
             if (q > 0 || h > 0) {
-              // O has to be settled. This S was committed after the P V of the tile before it; in its second
-              // half the first's P V has to be through as well.
-              if (h == 1) {
-                ok = mbar_wait(&bars[P_PVDONE + k], (sc[k] + q) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-              }
+              // O has to be settled: the P V before this half's, issued after its S, through.
+              ok = mbar_wait(&bars[P_PVDONE + e_bar(k, h ^ 1)], (sc[k] + q - (h == 0)) & 1, abort_flag, a.err,
+                             DEV_ERR_TIMEOUT_MMA);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
               for (int x = 0; x < D; x += 16) {
                 uint32_t o[16];
@@ -450,7 +452,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[P_PFULL + e_bar(k, h)]);
-          if (lane == 0 && k == 0 && q == 0 && h == 1 && !split_keys) mbar_arrive(&bars[P_START]);
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(&bars[P_GEMPTY + st]);
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     ++seg;
     u += nT;
   }
-  if (warp == 12 || warp == 13) {
+  if (warp >= 12 && warp != 14) {
     // |v| >= 65536 (bf16 pattern 0x4780 and above, infinities included) is outside fp16.
     const bool over = (vmax & 0xFFFFu) >= 0x4780u || (vmax >> 16) >= 0x4780u;
     if (__any_sync(0xffffffffu, over) && lane == 0 && a.err) atomicOr(a.err, DEV_ERR_RANGE);
