@@ -559,16 +559,20 @@ def new_cache(pages: int, page_size: int, H: int, Hkv: int, d: int, *, dtype=Non
     return make_cache(k, v, g, torch.empty((pages, H, 2), dtype=torch.float32, device=device))
 
 
-def make_batch(lens, table, *, cu_new=None, max_new: int = 1, prefix_table=None, prefix_len: int = 0) -> Batch:
+def make_batch(lens, table, *, cu_new=None, max_new: Optional[int] = None, prefix_table=None,
+               prefix_len: int = 0) -> Batch:
     """A handle on a batch: lens [B], table [B, entries], cu_new [B + 1] (None: the same number of rows each),
     prefix_table [ceil(prefix_len / page_size)], int32 on one CUDA device. lens counts every token of a
-    sequence, the shared prefix and the new ones among them; 0 is an idle sequence."""
+    sequence, the shared prefix and the new ones among them; 0 is an idle sequence. With cu_new, max_new
+    has to say the most new tokens that a sequence may have."""
     torch = _torch()
     B = lens.shape[0]
     if lens.dim() != 1 or table.dim() != 2 or table.shape[0] != B:
         raise ValueError("make_batch: lens must be [B] and table [B, entries]")
     if cu_new is not None and tuple(cu_new.shape) != (B + 1,):
         raise ValueError("make_batch: cu_new must be [B + 1]")
+    if cu_new is not None and max_new is None:
+        raise ValueError("make_batch: cu_new needs max_new")
     if (prefix_table is None) != (int(prefix_len) == 0):
         raise ValueError("make_batch: prefix_table and prefix_len come together")
     for t in (lens, table, cu_new, prefix_table):
@@ -587,7 +591,7 @@ def make_batch(lens, table, *, cu_new=None, max_new: int = 1, prefix_table=None,
         raise ValueError("make_batch: table must be contiguous")
     if prefix_table is not None and prefix_table.dim() != 1:
         raise ValueError("make_batch: prefix_table must be one-dimensional")
-    b.params = fox_batch(B, int(max_new), stride, int(prefix_len), _ptr(cu_new), _ptr(lens), _ptr(table),
+    b.params = fox_batch(B, 1 if max_new is None else int(max_new), stride, int(prefix_len), _ptr(cu_new), _ptr(lens), _ptr(table),
                          _ptr(prefix_table))
     b.ref = ctypes.byref(b.params)
     return b
@@ -663,7 +667,8 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
 
     cos, sin [positions, r / 2] fp32 rotate the first r channels of k by each token's position on the way
     (channel i with i + r / 2; `pairs`: 2i with 2i + 1), and those of q [rows, H, d] into q_out, which is
-    returned (None without q). Rows may be strided views, as those of a joint projection's output."""
+    returned (None without q) and must not overlap q. Rows may be strided views, as those of a joint projection's
+    output."""
     torch = _torch()
     where = "fox_cache_append"
     index = _cache_call_device(where, cache, batch)
@@ -715,7 +720,7 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
 def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
                ws=None, stream=None) -> Tuple[object, object]:
     """Attention of the batch's newest tokens, appended before, over the cache: q [rows, H, d] -> (O [rows, H, d],
-    LSE [rows, H] fp32). A shared prefix of the batch is read and multiplied once for all its sequences (bf16).
+    LSE [rows, H] fp32), o apart from q. A long shared prefix is read and multiplied once for all sequences (bf16).
     Rows of idle sequences get O = 0 and LSE = -inf; rows behind the last sequence are not written."""
     torch = _torch()
     where = "fox_decode"

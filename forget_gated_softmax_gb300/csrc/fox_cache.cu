@@ -82,6 +82,14 @@ bool row_ok(const void* p, int64_t stride, int heads, const fox_cache* c, int ro
   return rows <= 1 || (stride >= (int64_t)heads * c->d && stride < (1LL << 40) && stride * es % 16 == 0);
 }
 
+// Whether a call's output, rows of `heads` heads one after the other, lies within the span of the rows it reads.
+bool overlaps(const void* out, const void* in, int64_t in_stride, int heads, const fox_cache* c, int rows) {
+  const int es = c->dtype == FOX_DTYPE_BF16 ? 2 : 4;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+  const __int128 row = (__int128)heads * c->d * es, last = rows > 1 ? (__int128)(rows - 1) * in_stride * es : 0;
+  return o < i + last + row && i < o + row * rows;
+}
+
 fox_status check_ws(void* ws, size_t bytes, size_t need) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || bytes < need) return FOX_ERR_WORKSPACE;
   return FOX_OK;
@@ -132,6 +140,7 @@ fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, co
   }
   st = check_ws(workspace, workspace_bytes, kErrWordBytes);
   if (st != FOX_OK) return st;
+  if (rot && rot->q && overlaps(rot->q_out, rot->q, rot->q_stride, c->H, c, rows)) return FOX_ERR_INVALID_ARG;
   x.a.err = static_cast<uint32_t*>(workspace);
   x.k = k;
   x.v = v;
@@ -162,6 +171,7 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
   if (!decode_fits(x.a, f32)) return FOX_ERR_UNSUPPORTED;
   st = check_ws(workspace, workspace_bytes, decode_workspace_bytes(x.a, f32));
   if (st != FOX_OK) return st;
+  if (overlaps(o, q, q_stride, c->H, c, rows)) return FOX_ERR_INVALID_ARG;  // a row is read by several workers
   x.a.err = static_cast<uint32_t*>(workspace);
   x.q = q;
   x.q_stride = q_stride;

@@ -295,6 +295,8 @@ typedef struct fox_batch {
  * first 4 bytes, which fox_check_error reads and clears: a length, row range, page id or position
  * outside what the arguments allow sets one. The sequence, or the token, is then skipped, or an
  * unknown page read as page 0; its outputs are not meaningful, and no other sequence is touched.
+ * Calls that may run at the same time (other streams, captured graphs) need workspaces of their own.
+ * After a call whose device wait gave up (FOX_ERR_TIMEOUT) the header has to be made zero again.
  */
 #define FOX_CACHE_ZERO_BYTES 16384
 size_t fox_cache_workspace_bytes(const fox_cache* c, const fox_batch* s, int rows);
@@ -308,7 +310,7 @@ typedef struct fox_rotary {
   int pairs;         /* 0: channel i with i + dim / 2;  1: channel 2i with 2i + 1 */
   const void* q;     /* [rows, H, d] to rotate with the same angles, or NULL */
   int64_t q_stride;  /* elements from one row of q to the next */
-  void* q_out;       /* [rows, H, d] contiguous */
+  void* q_out;       /* [rows, H, d] contiguous, apart from q */
 } fox_rotary;
 
 /*
@@ -327,8 +329,12 @@ fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, co
  * sequence b at position pos attends to the sequence's keys 0 .. pos with the scores of fox_fwd,
  *   x_ij = scale q_i . k_j + c_i - c_j   (c_{j-1} under bias_from_j = 1).
  * q: rows of [H, d], q_stride elements apart (multiples of 16 bytes; 16-byte aligned).
- * o: [rows, H, d] of the cache's type, lse: [rows, H] fp32, natural log. Rows of idle sequences get
- * O = 0 and LSE = -inf. scale 0 selects d^-1/2.
+ * o: [rows, H, d] of the cache's type, apart from q; lse: [rows, H] fp32, natural log. Rows of idle
+ * sequences get O = 0 and LSE = -inf. scale 0 selects d^-1/2.
+ * A shared prefix of a bf16 cache is, where that saves more than it costs (B * prefix_len * Hkv * d * 4 bytes
+ * above 72 MB, counted once for every 16 rows that a sequence brings a key head), multiplied once with the rows of
+ * all sequences: its weights and V then pass through fp16 as in fox_fwd, so that |v| >= 65536 in its pages sets the
+ * error word. Otherwise, and in fp32, every sequence walks it.
  * A K or V slot behind the sequence's end is never used, whatever it holds. The same arguments and
  * contents give the same bits; how a row's sums are ordered follows from the lengths of the whole batch.
  */

@@ -103,6 +103,15 @@ def test_bad_rotations_are_refused(L):
         assert _append(L, rot=rot(**kw)) == status, kw
 
 
+def test_outputs_over_the_rows_they_are_made_from_are_refused(L):
+    row = 8 * 128 * 2
+    for o in (FAKE, FAKE + 16, FAKE + 2 * row - 16, FAKE - 2 * row + 16):
+        assert _decode(L, q=FAKE, o=o) == 1
+        rot = fox.fox_rotary(FAKE, FAKE, 100, 64, 0, FAKE, 1024, o)
+        assert _append(L, rot=rot) == 1
+    assert _decode(L, q=FAKE, qs=1 << 39, rows=2, o=FAKE + (1 << 38)) == 1  # between rows that lie far apart
+
+
 def test_nothing_to_do_is_ok(L):
     assert _decode(L, s=_batch(B=0), rows=0, q=None, o=None, lse=None, ws=None, nbytes=0) == 0
     assert _decode(L, rows=0, q=None, ws=None, nbytes=0) == 0
@@ -126,6 +135,8 @@ def test_binding_refuses_what_is_not_on_the_gpu():
     lens, table = torch.ones(2, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         fox.make_batch(lens, table)
+    with pytest.raises(ValueError, match="max_new"):
+        fox.make_batch(lens, table, cu_new=torch.zeros(3, dtype=torch.int32))
     with pytest.raises(TypeError):
         fox.make_batch(lens.long(), table)
     with pytest.raises(ValueError):

@@ -316,6 +316,21 @@ def test_decode_of_many_sequences(fox):
     assert (lse.double() - rl)[live].abs().max().item() <= foxtest.TOL_LSE_BF16 and torch.isinf(lse[~live]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,d,S", [(16, 64, 16), (9, 128, 32)])
+def test_decode_of_the_most_sequences(fox, dtype, H, d, S):
+    """2048 of them, in the widest row tile: the most shared memory that a call takes."""
+    own = [b % 35 + 1 if b % 7 else None for b in range(2048)]
+    c = Case(own, [1] * 2048, H, 1, d, S, dtype=dtype, uniform=True, seed=10)
+    c.put()
+    o, lse = fox.fox_decode(c.cache(fox), c.batch(fox), c.q)
+    ro, rl = c.attend()
+    assert_o(tensor_f64(o), tensor_f64(ro), dtype, "decode most")
+    live = ~torch.isinf(rl)
+    tol = foxtest.TOL_LSE_BF16 if dtype == "bf16" else foxtest.TOL_LSE_F32
+    assert (lse.double() - rl)[live].abs().max().item() <= tol and torch.isinf(lse[~live]).all()
+
+
 @pytest.mark.parametrize("prefix", [0, 40])
 def test_pages_beyond_32_bit_offsets(fox, prefix):
     """A pool of 2^31 elements and more, the pages in use at its end."""
