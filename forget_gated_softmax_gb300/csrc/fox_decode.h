@@ -4,8 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "fox_internal.h"
-#include "fox_paged.h"
+#include "fox_cache.h"
 #include "fox_ptx.cuh"
 
 namespace fox {

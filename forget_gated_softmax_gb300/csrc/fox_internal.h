@@ -6,13 +6,10 @@
 #include <cuda_runtime.h>
 #include <cuda.h>
 
-#include "fox_paged.h"
-
 namespace fox {
 
 constexpr int kTile = 128;          // tokens per sequence tile (MMA M and KV tile)
 constexpr int kColRec = kTile + 4;  // floats per column record: 128 column terms + base hi, base lo, 2 pad
-constexpr int kSMs = 152;           // of one GB300: grids of resident workers are sized for it, any count works
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -243,35 +240,6 @@ cudaError_t launch_tile_span(const void* q, const void* k, int B, int N, int H, 
 cudaError_t launch_window(const float* z, int B, int N, int H, double eps, int* out, void* ws, cudaStream_t s);
 size_t window_workspace_bytes(int B, int N, int H);
 
-// Paged cache: new tokens into the cache (k, v rotated and gates), and attention over it.
-// Strides are elements from one token's row to the next.
-constexpr size_t kCacheHeaderBytes = 16384;  // error word, then a counter a decode worker: all zero between calls
-struct CacheAppendArgs {
-  PagedArgs a;
-  const void* k;
-  const void* v;
-  const float* z;
-  const void* q;  // rotated into q_out, or null
-  void* q_out;
-  long long k_stride, v_stride, z_stride, q_stride;
-  const float* cos;
-  const float* sin;
-  int max_pos, rot, pairs;
-};
-cudaError_t launch_cache_append(const CacheAppendArgs& x, bool f32, cudaStream_t s);
-struct DecodeArgs {
-  PagedArgs a;
-  const void* q;
-  long long q_stride;
-  float scale;
-  int bias_from_j;
-  void* o;
-  float* lse;
-};
-bool decode_fits(const PagedArgs& a, bool f32);  // its work is counted in ints
-size_t decode_workspace_bytes(const PagedArgs& a, bool f32);
-cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t s);
-
 // Host helper: 4-D bf16 tensor map over [B, N, H, d] with a box of 64 channels x 1 head x
 // box_rows tokens x 1 batch and 128-byte swizzle. Returns false when the driver entry point is
 // unavailable or encoding fails.
@@ -280,11 +248,6 @@ bool make_f32_3d_map(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d
                      uint64_t pitch2, uint32_t box0, uint32_t box1);
 bool make_bnhd_map(CUtensorMap* map, const void* base, int B, int N, int H, int d, int box_rows = kTile,
                    bool f16 = false);
-// 4-D bf16 tensor map over a paged pool [pages, Hkv, page_size, d], box 64 channels x box_rows tokens, 128-byte swizzle.
-bool make_page_map(CUtensorMap* map, const void* base, int d, int page_size, int Hkv, int pages, int box_rows);
-// 3-D bf16 tensor map over query rows [rows, H, d], `stride` elements a row, box 64 channels x box_heads x box_rows.
-bool make_q_rows_map(CUtensorMap* map, const void* base, int d, int H, int rows, long long stride, int box_heads,
-                     int box_rows);
 // Host helpers for the gate projection: x [B, N, hidden] with a box of 64 x 128 x 1, and
 // W_f [H, hidden] with a box of 64 x (H rounded up to 16); bf16, 128-byte swizzle.
 bool make_x_map(CUtensorMap* map, const void* base, int B, int N, int hidden);
