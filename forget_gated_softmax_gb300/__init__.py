@@ -515,7 +515,7 @@ def fox_tile_span(q, k, z, *, scale: float = 0.0, bias_from_j: bool = False, ws=
 class Cache:
     """A paged cache over the caller's tensors (see fox_cache in include/fox.h). Made by make_cache or new_cache."""
 
-    __slots__ = ("k", "v", "g", "gbase", "params", "ref", "device", "dtype", "H", "Hkv", "d", "page_size")
+    __slots__ = ("k", "v", "g", "gbase", "params", "ref", "device", "index", "dtype", "H", "Hkv", "d", "page_size")
 
 
 class Batch:
@@ -543,7 +543,7 @@ def make_cache(k, v, g, gbase) -> Cache:
         if not t.is_cuda or t.device != k.device:
             raise ValueError("make_cache needs tensors on one CUDA device")
     c = Cache()
-    c.k, c.v, c.g, c.gbase, c.device, c.dtype = k, v, g, gbase, k.device, k.dtype
+    c.k, c.v, c.g, c.gbase, c.device, c.index, c.dtype = k, v, g, gbase, k.device, k.device.index, k.dtype
     c.H, c.Hkv, c.d, c.page_size = H, Hkv, d, S
     c.params = fox_cache(pages, S, H, Hkv, d, _dtype_code(k), _ptr(k), _ptr(v), _ptr(g), _ptr(gbase))
     c.ref = ctypes.byref(c.params)
@@ -612,7 +612,7 @@ def cache_workspace(cache: Cache, batch: Batch, rows: int):
 
 
 def _cache_call_device(where: str, cache: Cache, batch: Batch) -> int:
-    index = cache.device.index
+    index = cache.index
     if batch.device != cache.device:
         raise ValueError(f"{where}: cache and batch are on different devices")
     if index != _current_device():
@@ -622,13 +622,13 @@ def _cache_call_device(where: str, cache: Cache, batch: Batch) -> int:
     return index
 
 
-def _row_stride(where: str, name: str, t, cache: Cache, heads: int, rows: int) -> int:
+def _row_stride(where: str, name: str, t, cache: Cache, heads: int, rows: int, index: int) -> int:
     """The stride of t's rows; t is [rows, heads, d] with contiguous rows, in the cache's type, on its device."""
     if t.shape != (rows, heads, cache.d):
         raise ValueError(f"{where}: {name} must be [{rows}, {heads}, {cache.d}], got {tuple(t.shape)}")
-    if t.dtype != cache.dtype:
+    if t.dtype is not cache.dtype:
         raise TypeError(f"{where}: {name} must be {cache.dtype}, got {t.dtype}")
-    if t.device != cache.device:
+    if t.get_device() != index:
         raise ValueError(f"{where}: {name} is not on the cache's device")
     s0, s1, s2 = t.stride()
     if (s2 != 1 or (heads > 1 and s1 != cache.d)) and rows:
@@ -673,9 +673,10 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
     where = "fox_cache_append"
     index = _cache_call_device(where, cache, batch)
     rows = k.shape[0]
-    ks = _row_stride(where, "k", k, cache, cache.Hkv, rows)
-    vs = _row_stride(where, "v", v, cache, cache.Hkv, rows)
-    if z.shape != (rows, cache.H) or z.dtype != torch.float32 or z.device != cache.device:
+    ks = _row_stride(where, "k", k, cache, cache.Hkv, rows, index)
+    vs = _row_stride(where, "v", v, cache, cache.Hkv, rows, index)
+    f32 = torch.float32
+    if z.shape != (rows, cache.H) or z.dtype is not f32 or z.get_device() != index:
         raise ValueError(f"{where}: z must be [{rows}, {cache.H}] float32 on the cache's device")
     zs, z1 = z.stride()
     if z1 != 1 and cache.H > 1 and rows:
@@ -685,26 +686,26 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
         if cos is not None or sin is not None or q is not None or q_out is not None:
             raise ValueError(f"{where}: cos and sin come together, and q only with them")
     else:
-        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32:
+        shape = cos.shape
+        if len(shape) != 2 or shape != sin.shape or cos.dtype is not f32 or sin.dtype is not f32:
             raise ValueError(f"{where}: cos and sin must be float32 [positions, r / 2]")
-        if not cos.is_contiguous() or not sin.is_contiguous() or cos.device != cache.device or sin.device != cache.device:
+        if not (cos.is_contiguous() and sin.is_contiguous() and cos.get_device() == index == sin.get_device()):
             raise ValueError(f"{where}: cos and sin must be contiguous on the cache's device")
         qs = 0
         if q is not None:
-            qs = _row_stride(where, "q", q, cache, cache.H, rows)
+            qs = _row_stride(where, "q", q, cache, cache.H, rows, index)
             if q_out is None:
                 if stream is None and q.is_contiguous():
                     q_out = torch.empty_like(q)
                 else:
                     q_out = _alloc_on(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
             else:
-                _row_stride(where, "q_out", q_out, cache, cache.H, rows)
+                _row_stride(where, "q_out", q_out, cache, cache.H, rows, index)
                 if not q_out.is_contiguous():
                     raise ValueError(f"{where}: q_out must be contiguous")
         elif q_out is not None:
             raise ValueError(f"{where}: q_out without q")
-        positions, half = cos.shape
-        rot = ctypes.byref(fox_rotary(cos.data_ptr(), sin.data_ptr(), positions, 2 * half, int(bool(pairs)),
+        rot = ctypes.byref(fox_rotary(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if pairs else 0,
                                       _ptr(q), qs, _ptr(q_out)))
     if ws is None:
         ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
@@ -726,20 +727,20 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
     where = "fox_decode"
     index = _cache_call_device(where, cache, batch)
     rows = q.shape[0]
-    qs = _row_stride(where, "q", q, cache, cache.H, rows)
+    qs = _row_stride(where, "q", q, cache, cache.H, rows, index)
     if o is None:
         if stream is None and q.is_contiguous():
             o = torch.empty_like(q)
         else:
             o = _alloc_on(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     else:
-        _row_stride(where, "o", o, cache, cache.H, rows)
+        _row_stride(where, "o", o, cache, cache.H, rows, index)
         if not o.is_contiguous():
             raise ValueError(f"{where}: o must be contiguous")
     if lse is None:
         lse = torch.empty((rows, cache.H), dtype=torch.float32, device=cache.device) if stream is None else _alloc_on(
             stream, lambda: torch.empty((rows, cache.H), dtype=torch.float32, device=cache.device))
-    elif lse.shape != (rows, cache.H) or lse.dtype != torch.float32 or lse.device != cache.device or not lse.is_contiguous():
+    elif lse.shape != (rows, cache.H) or lse.dtype is not torch.float32 or lse.get_device() != index or not lse.is_contiguous():
         raise ValueError(f"{where}: lse must be contiguous [{rows}, {cache.H}] float32 on the cache's device")
     if ws is None:
         ws = _alloc_on(stream, lambda: cache_workspace(cache, batch, rows))

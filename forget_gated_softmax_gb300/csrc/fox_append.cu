@@ -354,12 +354,15 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendP
     float zs[128][kGateHeads + 1];
     RowPlace places[kBlockRows];
   } sh;
+  // The copies of a call of three launches need nothing of the other two, but what follows them needs these.
+  const bool last = p.scan_bases && p.copy_blocks > 0;
+  if (!last) grid_dep_wait();
   grid_dep_trigger();
   if (static_cast<int>(blockIdx.x) < p.copy_blocks)
     copy_rows<T>(p, sh.places);
   else
     gate_block(p, sh.zs);
-  grid_dep_wait();  // as a dependent: what follows this grid follows its forerunners too
+  if (last) grid_dep_wait();
 }
 
 // Bases of the pages after a sequence's first one: base_k = base_0 + sum of the full pages' sums.
@@ -419,15 +422,15 @@ cudaError_t launch(AppendParams p, cudaStream_t s) {
   if (!p.scan_bases) {
     p.copy_blocks = static_cast<int>(copy);
     TraceScope trace("cache_append", s);
-    cache_append_kernel<T><<<static_cast<unsigned>(copy + gates), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    const cudaError_t f =
+        launch_dependent(cache_append_kernel<T>, dim3(static_cast<unsigned>(copy + gates)), dim3(kThreads), 0, s, p);
+    return f != cudaSuccess ? f : cudaGetLastError();
   }
   cudaError_t e;
   {
     p.copy_blocks = 0;
     TraceScope trace("cache_gates", s);
-    cache_append_kernel<T><<<static_cast<unsigned>(gates), kThreads, 0, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_dependent(cache_append_kernel<T>, dim3(static_cast<unsigned>(gates)), dim3(kThreads), 0, s, p);
   }
   if (e == cudaSuccess) {
     TraceScope trace("cache_base_scan", s);

@@ -8,7 +8,11 @@ namespace fox {
 
 constexpr int kSMs = 152;  // of one GB300: grids of resident workers are sized for it, any count works
 
-// Paged cache: new tokens into the cache (k, v rotated and gates), and attention over it.
+// New tokens into the cache (k, v rotated and gates), and attention over it. Every kernel is launched as a
+// programmatic dependent of what is ahead of it on the stream; the first of a call waits for that before it
+// reads or writes anything in memory (and only then lets the next start), so that its launch and set-up
+// overlap the end of the call before (step after step: one token appended 16.0 -> 14.3 us, a decode of 65536 keys
+// 59.0 -> 57.5, one behind a prefix of 16384 tokens 55.8 -> 53.5).
 // Strides are elements from one token's row to the next.
 constexpr size_t kCacheHeaderBytes = 16384;  // error word, then a counter a decode worker: all zero between calls
 struct CacheAppendArgs {

@@ -17,15 +17,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
   __shared__ float sums[kMergeWarps][D];
   __shared__ float2 mls[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_trigger();
   const int id = deal > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + warp, part = deal > 1 ? warp : 0;
   const int row = id / a.H, h = id - row * a.H;
-  if (row >= a.rows) return;  // whole blocks where the warps deal
   // What the call was given may be read before the kernels ahead are through.
-  const int b = seq_of_row(a, row);
-  if (b < 0) return;
-  bool bad;
-  const SeqInfo s = seq_info(a, b, &bad);
-  if (bad || row < s.row0 || row >= s.row0 + s.n || s.own < 0) return;  // idle rows are written already
+  const int b = row < a.rows ? seq_of_row(a, row) : -1;
+  SeqInfo s;
+  bool bad = b < 0;
+  if (!bad) s = seq_info(a, b, &bad);
+  if (bad || row < s.row0 || row >= s.row0 + s.n || s.own < 0) {  // whole blocks where the warps deal
+    grid_dep_wait();  // idle rows are written already; but what follows this grid follows the others too
+    return;
+  }
   const int G = a.H / a.Hkv, hkv = h / G, hl = h - hkv * G;
   const int pos = s.own - s.n + (row - s.row0), last = a.prefix_len - 1, mask = a.page_size - 1;
   const Gate2 ci = gate_sum(a, own_page_or_0(a, b, pos), pos & mask, h);

@@ -40,6 +40,8 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
   float* qs = vs + kKeyTile * D;  // [kF32Rows][D] scaled queries; at a segment's end its rows of O
   SeqEntry* seqs = reinterpret_cast<SeqEntry*>(smem + W * L::kWarpFloats);
   const PagedArgs& a = p.a;
+  grid_dep_wait();
+  grid_dep_trigger();
   scan_sequences(p, seqs, scratch);
   const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size, P = a.prefix_len, tp = ceil_div(P, kKeyTile);
   const int total = seqs[a.B].u0 * a.Hkv, each = units_per_worker(total, p.workers);
@@ -225,8 +227,8 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
       cudaFuncSetAttribute(decode_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode", s);
-  decode_f32_kernel<D><<<kSMs, 32 * kF32Warps, smem, s>>>(p);
-  return cudaGetLastError();
+  const cudaError_t f = launch_dependent(decode_f32_kernel<D>, dim3(kSMs), dim3(32 * kF32Warps), smem, s, p);
+  return f != cudaSuccess ? f : cudaGetLastError();
 }
 
 }  // namespace

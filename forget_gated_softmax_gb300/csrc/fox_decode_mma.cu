@@ -103,15 +103,18 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   uint8_t* q_of = sm + W * stages * (2 * L::kTileBytes + x.gstage) + warp * L::kQBytes;
   SeqEntry* seqs = reinterpret_cast<SeqEntry*>(sm + W * (stages * (2 * L::kTileBytes + x.gstage) + L::kQBytes));
 
-  grid_dep_trigger();
+  const bool shared = p.pre.key_tiles > 0;
   if (threadIdx.x == 0) abort_word = 0;
   if (lane == 0) {
     kept.i0[warp] = -1;
     for (int s = 0; s < stages; ++s) mbar_init(&bars[warp][s], 1);
     fence_mbar_init();
   }
+  // Behind a shared prefix's kernel, which nothing here needs and which let this one start once all before it
+  // were through, the wait comes last.
+  if (!shared) grid_dep_wait();
+  grid_dep_trigger();
   scan_sequences(p, seqs, scratch);  // ends with a block barrier
-  const bool shared = p.pre.key_tiles > 0;
   if (shared && blockIdx.x == 0)
     for (int b = threadIdx.x; b <= a.B; b += blockDim.x) p.cum[b] = seqs[b].u0;
 
@@ -505,10 +508,6 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode", s);
-  if (p.pre.key_tiles == 0) {
-    kernel<<<kSMs, 32 * L::kWarps, smem, s>>>(maps[0], maps[1], maps[2], p, x);
-    return cudaGetLastError();
-  }
   const cudaError_t f =
       launch_dependent(kernel, dim3(kSMs), dim3(32 * L::kWarps), smem, s, maps[0], maps[1], maps[2], p, x);
   return f != cudaSuccess ? f : cudaGetLastError();

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   const bool split_keys = pp.row_tiles == 1;  // the streams take alternate key tiles
   const int step = split_keys ? 2 : 1;        // key tiles from one of a stream's to its next
 
+  grid_dep_wait();     // before tensor memory is taken, which what is ahead may still have to take itself
   grid_dep_trigger();  // the own keys' kernel may start where this one leaves room: it needs nothing from here
   if (threadIdx.x < P_COUNT) {
     const int i = threadIdx.x;
@@ -521,8 +522,9 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   TraceScope trace("prefix", s);
-  kernel<<<kSMs, kPrefixThreads, smem, s>>>(maps[0], maps[1], maps[2], p);
-  return cudaGetLastError();
+  const cudaError_t f =
+      launch_dependent(kernel, dim3(kSMs), dim3(kPrefixThreads), smem, s, maps[0], maps[1], maps[2], p);
+  return f != cudaSuccess ? f : cudaGetLastError();
 }
 
 }  // namespace

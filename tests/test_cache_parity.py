@@ -555,6 +555,58 @@ def test_captured_steps_replay_on_new_contents(fox, dtype, prefix, B):
     assert fox.fox_check_error(ws) == 0 and fox.fox_check_error(ws2) == 0
 
 
+@pytest.mark.parametrize("prefix", [0, 26000])
+def test_captured_calls_behind_a_fork_and_a_join(fox, prefix):
+    """In a graph: k and v made on one stream, z on another, append behind both, two decodes side by side."""
+    H, Hkv, d, S, nan = 8, 2, 128, 64, float("nan")
+    c = Case([70, 300], [1, 1], H, Hkv, d, S, uniform=True, prefix=prefix, seed=32)
+    c.put()
+    want = fox.fox_decode(c.cache(fox), c.batch(fox), c.q)
+    k0, v0, z0 = c.new_rows()
+    for b in range(2):  # the new tokens out of the cache again
+        page, slot = int(c.table[b, (c.own[b] - 1) // S]), (c.own[b] - 1) % S
+        c.k[page, :, slot] = nan
+        c.v[page, :, slot] = nan
+        c.g[page, :, slot] = nan
+    k, v, z = torch.zeros_like(k0), torch.zeros_like(v0), torch.zeros_like(z0)
+    outs = [(torch.empty_like(c.q), torch.empty(2, H, device="cuda")) for _ in range(2)]
+    cache, batch = c.cache(fox), c.batch(fox)
+    ws = [fox.cache_workspace(cache, batch, 2) for _ in range(2)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            z.copy_(z0)
+            z.mul_(1.0)
+        k.copy_(k0)
+        v.copy_(v0)
+        main.wait_stream(side)
+        fox.fox_cache_append(cache, batch, k, v, z, ws=ws[0])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            fox.fox_decode(cache, batch, c.q, o=outs[1][0], lse=outs[1][1], ws=ws[1])
+        fox.fox_decode(cache, batch, c.q, o=outs[0][0], lse=outs[0][1], ws=ws[0])
+        main.wait_stream(side)
+    for _ in range(3):
+        for o, lse in outs:
+            o.fill_(nan)
+            lse.fill_(nan)
+        k.fill_(nan)
+        z.fill_(nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, lse in outs:
+            assert torch.equal(bits(o), bits(outs[0][0])) and torch.equal(bits(lse), bits(outs[0][1]))
+            # The new token's g is one fp32 sum here, rounded from 64 bits there: below 128, so 2^-17 apart and
+            # some ulps of log sigmoid; O may then round to the neighbouring value.
+            assert (lse - want[1]).abs().max() <= 2.0**-15
+            x, y = o.float(), want[0].float()
+            assert ((x - y).abs() <= 2.0**-7 * torch.maximum(x.abs(), y.abs()) + 2.0**-15).all()
+    assert fox.fox_check_error(ws[0]) == 0 and fox.fox_check_error(ws[1]) == 0
+
+
 def test_calls_on_another_stream_and_two_at_once(fox):
     cases = [Case([3000, 50], [1, 1], 8, 2, 128, 64, uniform=True, seed=s, prefix=p) for s, p in ((1, 0), (2, 500), (3, 26000))]
     want = []
