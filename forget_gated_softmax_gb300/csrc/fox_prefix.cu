@@ -31,9 +31,9 @@
 // cost nothing) made the tensor core the bound: 2.8 us a pair of 128 x 128 tiles, against 2.2 now. A magnitude
 // of 65536 or more in V (outside fp16) sets DEV_ERR_RANGE. A 32-column chunk of S, once read, holds its P.
 //
-// 32768 keys, 256 sequences x 4 heads a key head, 8 of these, d = 128: 137 us, 1000 TFLOP/s, half of cuBLAS's
-// bf16 peak. What bounds it: the softmax warps' issue, two of them a scheduler at about four cycles an
-// instruction while both streams compute. Without the conversion of V it would take 132 us; 168 registers for
+// 32768 keys, 256 sequences x 4 heads a key head, 8 of these, d = 128: 133 us, 1030 TFLOP/s, 53 % of
+// cuBLAS's burst bf16 rate. What bounds it: the softmax warps' issue, two of them a scheduler at about four cycles an
+// instruction while both streams compute. Without the conversion of V it took 5 us less; 168 registers for
 // the softmax (88 for the others) took no less.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,6 +46,7 @@ namespace {
 constexpr int kPrefixThreads = 512;
 constexpr int kConverters = 3;  // two: 142 us where three take 137
 constexpr int kMaxHp = 16;
+constexpr int kOpening = 4;  // key tiles' time
 constexpr int kKapPitch = kTile + 4;  // floats: the heads' rows start in different banks
 constexpr float kRaise = 8.0f;        // log2 units that a row may pass its running maximum by
 
@@ -131,7 +132,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // A segment: key tiles t1 - 1 down to t0 of item (hkv, it).
     const int item = u / pp.line, hkv = item / pp.items, it = item % pp.items;
     const int t0 = u % pp.line, t1 = min(pp.key_tiles, t0 + (u_end - u));
-    if (t0 >= t1) break;  // empty units: a CTA has them at its end
+    if (t0 >= t1) {  // an item's empty units
+      u = (item + 1) * pp.line;
+      continue;
+    }
     const int nT = t1 - t0;
     const int T0 = split_keys ? 0 : 2 * it;  // row tile of stream 0; stream 1 has the next, or the same
     const bool has1 = split_keys ? nT > 1 : T0 + 1 < pp.row_tiles;
@@ -541,16 +545,17 @@ PrefixPlan prefix_plan(const PagedArgs& a) {
   x.kap_tiles = x.head_chunks > 1 ? 2 : 1;
   x.key_tiles = ceil_div(a.prefix_len, kTile);
   x.workers = kSMs;
-  // Equal ranges of all items' key tiles, or, where that leaves the longest range no longer, a whole number
-  // of CTAs an item: no CTA then begins a second item, which costs it about four tiles' time (its pipeline
-  // runs empty and fills again).
+  // Equal ranges of all items' key tiles and of kOpening empty units behind each item, the time that beginning
+  // a second item costs a CTA (its pipeline runs empty and fills again); or, where that leaves the longest range
+  // no longer, a whole number of CTAs an item, none of which begins a second. (Four such units or ten: 133 to 135 us
+  // at 32768 keys and 4 items a key head, without them 137.)
   const int n = a.Hkv * x.items;
-  x.line = x.key_tiles;
-  x.each = units_per_worker(n * x.key_tiles, x.workers);
+  x.line = x.key_tiles + kOpening;
+  x.each = units_per_worker(n * x.line, x.workers);
   const int ctas = x.workers / n;
   if (ctas > 0) {
     const int whole = ceil_div(x.key_tiles, ctas);
-    if (whole <= x.each + 4) {
+    if (whole <= x.each) {
       x.each = whole;
       x.line = whole * ceil_div(x.key_tiles, whole);
     }
