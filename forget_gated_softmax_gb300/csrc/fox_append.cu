@@ -26,7 +26,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kGateHeads = 32;  // heads of one gate block
-constexpr int kFewTokens = 8;   // up to so many a gate block sums token after token, not by scans
+constexpr int kFewTokens = 8;   // up to so many a gate block sums token after token, not by scans (one token of
+                                // 128 sequences: 8.9 us, by scans 13.3; 8 of 32: 9.3 and 10.5; 16 of 32: 11.5 and 10.9)
 
 struct AppendParams {
   PagedArgs a;

@@ -52,6 +52,25 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// K and V pass through the L2 cache as what may go first where a step reads them once: what every call needs
+// again (its code, the tables, partial results) then stays. A prefix walked by every sequence is read again.
+__device__ __forceinline__ uint64_t stream_policy(bool again) {
+  uint64_t x;
+  if (again)
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(x));
+  else
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(x));
+  return x;
+}
+__device__ __forceinline__ void tma_load_4d_by(uint64_t policy, void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                               int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+      : "memory");
+}
+
 // Shared memory: K and V of every (warp, stage), then its gates, then the sequences' work offsets.
 // Gates of a stage: per sub-page (32 slots, or two of 16) [heads][slots + 4] sums, then [heads] bases.
 struct MmaShape {
@@ -134,6 +153,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   Gate2 ci[NT][2];
   int pos[NT][2], gidx[NT][2];
   // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
+  const uint64_t policy = stream_policy(p.walk_prefix);
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
   const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
 
@@ -456,7 +476,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
         // One lane a copy: K and V of 64 channels each, and the gates.
         if (lane < D / 32) {
           const int y = lane >> 1;
-          tma_load_4d(dst + (lane & 1) * L::kTileBytes + y * (kKeyTile * 128) + i * (16 * 128), lane & 1 ? &tmap_v : &tmap_k,
+          tma_load_4d_by(policy, dst + (lane & 1) * L::kTileBytes + y * (kKeyTile * 128) + i * (16 * 128), lane & 1 ? &tmap_v : &tmap_k,
                       &bars[warp][to], y * 64, slot, now.hkv, id);
         } else if (lane == 31) {
           tma_load_3d(sg + i * x.gsub, &tmap_g, &bars[warp][to], slot - 4, h0, id);
