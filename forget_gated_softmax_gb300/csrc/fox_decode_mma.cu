@@ -52,25 +52,6 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// K and V pass through the L2 cache as what may go first where a step reads them once: what every call needs
-// again (its code, the tables, partial results) then stays. A prefix walked by every sequence is read again.
-__device__ __forceinline__ uint64_t stream_policy(bool again) {
-  uint64_t x;
-  if (again)
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(x));
-  else
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(x));
-  return x;
-}
-__device__ __forceinline__ void tma_load_4d_by(uint64_t policy, void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                               int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
-      : "memory");
-}
-
 // Shared memory: K and V of every (warp, stage), then its gates, then the sequences' work offsets.
 // Gates of a stage: per sub-page (32 slots, or two of 16) [heads][slots + 4] sums, then [heads] bases.
 struct MmaShape {

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.page_size, G = a.H / a.Hkv, P = a.prefix_len;
   const bool split_keys = pp.row_tiles == 1;  // the streams take alternate key tiles
+  const uint64_t policy = stream_policy(false);
   const int step = split_keys ? 2 : 1;        // key tiles from one of a stream's to its next
 
   grid_dep_wait();     // before tensor memory is taken, which what is ahead may still have to take itself
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (here >= 0)
 #pragma unroll 1
           for (int x = 0; x < D / 64; ++x)
-            tma_load_4d(sm + L::kK + st * L::kTileBytes + x * 16384 + lane * S * 128, &tmap_k, &bars[P_KFULL + st],
+            tma_load_4d_by(policy, sm + L::kK + st * L::kTileBytes + x * 16384 + lane * S * 128, &tmap_k, &bars[P_KFULL + st],
                         x * 64, 0, hkv, here);
         ++issued;
       }
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (here >= 0)
 #pragma unroll 1
               for (int y = 0; y < D / 64; ++y)
-                tma_load_4d(sm + L::kV + st * L::kTileBytes + y * 16384 + lane * S * 128, &tmap_v, &bars[P_VFULL + st],
+                tma_load_4d_by(policy, sm + L::kV + st * L::kTileBytes + y * 16384 + lane * S * 128, &tmap_v, &bars[P_VFULL + st],
                             y * 64, 0, hkv, here);
             ++issued;
             ok = n == 0 || mbar_wait(&bars[P_GEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
