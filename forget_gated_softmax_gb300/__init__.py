@@ -131,11 +131,12 @@ class fox_trace_record(ctypes.Structure):
 
 
 _lib = None
+_call = None  # fox_cache_append and fox_decode by way of _foxcall.so (csrc/fox_call.c)
 
 
 def lib() -> ctypes.CDLL:
     """The loaded libfox.so; raises if it has not been built."""
-    global _lib
+    global _lib, _call
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(
@@ -194,12 +195,23 @@ def lib() -> ctypes.CDLL:
         L.fox_cache_append.restype = i
         L.fox_decode.argtypes = [pc, pb, i, vp, i64, ctypes.c_float, i, vp, vp, vp, sz, vp]
         L.fox_decode.restype = i
+        try:
+            from . import _foxcall
+        except ImportError as e:
+            raise RuntimeError("_foxcall.so is not built; run `python -m forget_gated_softmax_gb300.build`") from e
+        _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append, L.fox_decode)))
+        _call = _foxcall
         L.fox_trace_begin.argtypes = []
         L.fox_trace_begin.restype = i
         L.fox_trace_end.argtypes = [ctypes.POINTER(fox_trace_record), i]
         L.fox_trace_end.restype = i
         _lib = L
     return _lib
+
+
+def _load_call():
+    lib()
+    return _call
 
 
 def fox_status_string(status: int) -> str:
@@ -515,14 +527,14 @@ def fox_tile_span(q, k, z, *, scale: float = 0.0, bias_from_j: bool = False, ws=
 class Cache:
     """A paged cache over the caller's tensors (see fox_cache in include/fox.h). Made by make_cache or new_cache."""
 
-    __slots__ = ("k", "v", "g", "gbase", "params", "ref", "device", "index", "dtype", "H", "Hkv", "d", "page_size")
+    __slots__ = ("k", "v", "g", "gbase", "params", "ref", "addr", "device", "index", "dtype", "H", "Hkv", "d", "page_size")
 
 
 class Batch:
     """One step's sequences over the caller's tensors (see fox_batch in include/fox.h). Made by make_batch.
     The contents of its tensors may change between calls; their storage may not."""
 
-    __slots__ = ("lens", "table", "cu_new", "prefix_table", "params", "ref", "device", "B")
+    __slots__ = ("lens", "table", "cu_new", "prefix_table", "params", "ref", "addr", "device", "B")
 
 
 def make_cache(k, v, g, gbase) -> Cache:
@@ -546,7 +558,7 @@ def make_cache(k, v, g, gbase) -> Cache:
     c.k, c.v, c.g, c.gbase, c.device, c.index, c.dtype = k, v, g, gbase, k.device, k.device.index, k.dtype
     c.H, c.Hkv, c.d, c.page_size = H, Hkv, d, S
     c.params = fox_cache(pages, S, H, Hkv, d, _dtype_code(k), _ptr(k), _ptr(v), _ptr(g), _ptr(gbase))
-    c.ref = ctypes.byref(c.params)
+    c.ref, c.addr = ctypes.byref(c.params), ctypes.addressof(c.params)
     return c
 
 
@@ -593,7 +605,7 @@ def make_batch(lens, table, *, cu_new=None, max_new: Optional[int] = None, prefi
         raise ValueError("make_batch: prefix_table must be one-dimensional")
     b.params = fox_batch(B, 1 if max_new is None else int(max_new), stride, int(prefix_len), _ptr(cu_new), _ptr(lens), _ptr(table),
                          _ptr(prefix_table))
-    b.ref = ctypes.byref(b.params)
+    b.ref, b.addr = ctypes.byref(b.params), ctypes.addressof(b.params)
     return b
 
 
@@ -681,7 +693,7 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
     zs, z1 = z.stride()
     if z1 != 1 and cache.H > 1 and rows:
         raise ValueError(f"{where}: z needs contiguous rows")
-    rot = None
+    rot = ()
     if cos is None or sin is None:
         if cos is not None or sin is not None or q is not None or q_out is not None:
             raise ValueError(f"{where}: cos and sin come together, and q only with them")
@@ -705,13 +717,13 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
                     raise ValueError(f"{where}: q_out must be contiguous")
         elif q_out is not None:
             raise ValueError(f"{where}: q_out without q")
-        rot = ctypes.byref(fox_rotary(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if pairs else 0,
-                                      _ptr(q), qs, _ptr(q_out)))
+        rot = (cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if pairs else 0,
+               0 if q is None else q.data_ptr(), qs, 0 if q is None else q_out.data_ptr())
     if ws is None:
         ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
-    st = (_lib or lib()).fox_cache_append(
-        cache.ref, batch.ref, rows, k.data_ptr(), ks, v.data_ptr(), vs, z.data_ptr(), zs, rot, ws.data_ptr(), ws.numel(),
-        _current_stream(index) if stream is None else stream.cuda_stream,
+    st = (_call or _load_call()).append(
+        cache.addr, batch.addr, rows, k.data_ptr(), ks, v.data_ptr(), vs, z.data_ptr(), zs, ws.data_ptr(), ws.numel(),
+        _current_stream(index) if stream is None else stream.cuda_stream, *rot,
     )
     if st != 0:
         raise FoxError(st, where)
@@ -744,8 +756,8 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
         raise ValueError(f"{where}: lse must be contiguous [{rows}, {cache.H}] float32 on the cache's device")
     if ws is None:
         ws = _alloc_on(stream, lambda: cache_workspace(cache, batch, rows))
-    st = (_lib or lib()).fox_decode(
-        cache.ref, batch.ref, rows, q.data_ptr(), qs, scale, 1 if bias_from_j else 0, o.data_ptr(), lse.data_ptr(),
+    st = (_call or _load_call()).decode(
+        cache.addr, batch.addr, rows, q.data_ptr(), qs, scale, 1 if bias_from_j else 0, o.data_ptr(), lse.data_ptr(),
         ws.data_ptr(), ws.numel(), _current_stream(index) if stream is None else stream.cuda_stream,
     )
     if st != 0:

@@ -1,4 +1,5 @@
-"""Builds libfox.so in place from csrc/*.cu for sm_103a with nvcc.
+"""Builds libfox.so in place from csrc/*.cu for sm_103a with nvcc, and the binding's
+_foxcall.so from csrc/fox_call.c with the C compiler.
 
 Each translation unit is compiled in parallel; the runtime is linked
 statically so the library only needs the NVIDIA driver at load time.
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfox.so")
+CALL = os.path.join(PKG, "_foxcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -45,8 +48,21 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_call() -> None:
+    src = os.path.join(CSRC, "fox_call.c")
+    if not _stale(CALL, [src, os.path.join(ROOT, "include", "fox.h")]):
+        return
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler found: it is required to build _foxcall.so")
+    cmd = [cc, "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], src, "-o", CALL]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"build of _foxcall.so failed:\n{r.stdout}{r.stderr}")
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Compile (if stale) and link libfox.so; returns its path."""
+    """Compile (if stale) and link libfox.so, and _foxcall.so; returns the former's path."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
@@ -72,6 +88,7 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link of libfox.so failed:\n{r.stdout}{r.stderr}")
+    _build_call()
     return LIB
 
 

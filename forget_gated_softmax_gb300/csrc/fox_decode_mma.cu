@@ -1,7 +1,9 @@
 // Attention of the newest tokens over the paged cache, bf16, on the tensor cores.
 //
 // Bound by memory: K and V of every key are read once, 2 bytes an element, for at most 16 query rows
-// of work each. So the kernel is built to keep copies in flight, and uses the small register MMAs
+// of work each: 64 sequences of up to 16384 tokens on 8 key heads (2.5 GB) take 381 us, 97 % of a copy's rate, one of
+// 65536 (277 MB) 53 us, 12 of them launch, first look-ups and join; one of 1000 is these alone, 13 us. So the kernel
+// is built to keep copies in flight, and uses the small register MMAs
 // (16 x 8 x 16), of which it needs too few to matter: 128-row tensor-memory tiles would be 8 to
 // 128 times padding here.
 //

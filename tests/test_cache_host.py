@@ -295,3 +295,33 @@ def test_work_line_gives_every_pair_of_worker_and_item_its_own_slot(H, workers):
                     u += tiles
         assert u == total
         assert not slots or max(slots) < workers + Hkv * B * RTmax
+
+
+def test_the_short_way_passes_the_same_arguments(L):
+    """_foxcall's append and decode against ctypes: the same statuses, each argument in its place."""
+    from forget_gated_softmax_gb300 import _foxcall
+
+    c, s = _cache(), _batch()
+    need = L.fox_cache_workspace_bytes(ctypes.byref(c), ctypes.byref(s), 2)
+    at = (ctypes.addressof(c), ctypes.addressof(s))
+    good = [*at, 2, FAKE, 1024, 0.5, 1, 1 << 30, FAKE, FAKE, need, 0]
+    for i, v, status in [(2, -2, 1), (2, 3, 1), (3, 0, 1), (3, FAKE + 8, 1), (4, 1023, 1), (5, -1.0, 1), (5, float("nan"), 1),
+                         (6, 2, 1), (7, 0, 1), (7, FAKE + 16, 1), (8, FAKE + 2, 1), (9, FAKE + 64, 3), (10, need - 1, 3)]:
+        a = list(good)
+        a[i] = v
+        assert _foxcall.decode(*a) == status, (i, v)
+    good = [*at, 2, FAKE, 256, FAKE, 256, FAKE, 8, FAKE, 256, 0, FAKE, FAKE, 100, 64, 0, FAKE, 1024, 1 << 30]
+    for i, v, status in [(2, -2, 1), (3, FAKE + 2, 1), (4, 255, 1), (5, 0, 1), (6, 260, 1), (7, 0, 1), (8, 7, 1), (9, 0, 3),
+                         (10, 255, 3), (12, 0, 1), (13, FAKE + 4, 1), (14, -1, 1), (15, 24, 2), (15, -16, 1), (16, 2, 1),
+                         (17, FAKE + 2, 1), (18, 8, 1), (19, 0, 1), (19, FAKE + 16, 1)]:
+        a = list(good)
+        a[i] = v
+        assert _foxcall.append(*a) == status, (i, v)
+    assert _foxcall.append(*good[:9], 0, 0, 0) == 3
+    for bad in ([1], [*good[:11]], ["x"] * 12, [1 << 70] * 12):
+        with pytest.raises((TypeError, OverflowError)):
+            _foxcall.decode(*bad)
+        with pytest.raises((TypeError, OverflowError)):
+            _foxcall.append(*bad)
+    with pytest.raises(OverflowError):
+        _foxcall.decode(*at, 1 << 31, FAKE, 1024, 0.5, 1, 1 << 30, FAKE, FAKE, need, 0)
