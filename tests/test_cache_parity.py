@@ -263,6 +263,27 @@ def test_decode_behind_a_shared_prefix(fox, n):
     assert torch.equal(bits(o2[:last]), bits(o[:last])) and torch.equal(bits(lse2[:last]), bits(lse[:last]))
 
 
+@pytest.mark.parametrize("own,H,Hkv,d,S,P", [
+    ([3, 70], 8, 2, 128, 64, 50001),            # one row tile: the streams share the keys out
+    ([3] * 40, 4, 1, 64, 16, 12003),            # two row tiles
+    ([5] * 90, 16, 4, 128, 128, 5000),          # three, the last item's second missing
+])
+def test_scores_that_rise_towards_the_prefix_s_start(fox, own, H, Hkv, d, S, P):
+    """The prefix's keys are taken from the last on: here the row maximum is passed over and over, in every part."""
+    c = Case(own, [1] * len(own), H, Hkv, d, S, prefix=P, uniform=True, seed=77, z_mean=9.0)
+    k, v, z = c.pre
+    grow = 1 + 12 * (1 - torch.arange(P, device="cuda") / P)
+    c.pre = ((k.float() * grow[:, None, None]).to(k.dtype), v, z + 9)
+    c.put()
+    cache, batch = c.cache(fox), c.batch(fox)
+    ws = fox.cache_workspace(cache, batch, c.rows)
+    o, lse = fox.fox_decode(cache, batch, c.q, ws=ws)
+    assert fox.fox_check_error(ws) == 0
+    ro, rl = c.attend()
+    assert_o(tensor_f64(o), tensor_f64(ro), "bf16", "decode rising scores")
+    assert (lse.double() - rl).abs().max().item() <= foxtest.TOL_LSE_BF16
+
+
 @pytest.mark.parametrize("B,P", [(3, 100), (40, 5003)])
 def test_bad_pages_of_a_prefix_are_reported(fox, B, P):
     """Page ids of the prefix outside the pool: reported, read as page 0 (finite here), nothing else."""
