@@ -15,7 +15,7 @@
 //
 // Two streams of softmax warps share the tensor core, each with its S and O in tensor memory:
 //   more than one row tile a key head: an item is two row tiles, one a stream, on the same key tiles;
-//   one row tile: the streams take alternate key tiles, and leave a partial result each.
+//   one row tile (kSplit): the streams take alternate key tiles, and leave a partial result each.
 // A tile passes between softmax and tensor core in two halves of 64 keys: once a half's P V is issued, S of
 // the same half of the next tile is, into the columns that P leaves. So the softmax of one half runs while
 // the other is multiplied (S of whole tiles: 162 against 150 us at 32768 keys and 1024 rows a key head,
@@ -63,22 +63,22 @@ enum PBar {
   P_Q = 0,
   P_KFULL = 1,   // +stage
   P_KEMPTY = 3,
-  P_VFULL = 5,
-  P_VEMPTY = 7,
-  P_GFULL = 9,   // +stage: the key tile's gate terms are in place
-  P_GEMPTY = 11,
-  P_SFULL = 13,   // +2 stream + half of the tile's keys
-  P_PFULL = 17,   // +2 stream + half
-  P_PVDONE = 21,  // +2 stream + half: that P V is through
-  P_OFINAL = 25,  // +stream
-  P_VREADY = 27,  // +stage: V in fp16, and 0 behind the prefix's end
-  P_DONE = 29,
-  P_COUNT = 30,
+  P_VFULL = 5,    // +V stage
+  P_VEMPTY = 8,
+  P_VREADY = 11,  // V in fp16, and 0 behind the prefix's end
+  P_GFULL = 14,   // +stage: the key tile's gate terms are in place
+  P_GEMPTY = 16,
+  P_SFULL = 18,   // +2 stream + half of the tile's keys
+  P_PFULL = 22,   // +2 stream + half
+  P_PVDONE = 26,  // +2 stream + half: that P V is through
+  P_OFINAL = 30,  // +stream
+  P_DONE = 32,
+  P_COUNT = 33,
 };
 
 __host__ __device__ constexpr int e_bar(int stream, int half) { return 2 * stream + half; }
 
-template <int D>
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ DecodeParams p) {
@@ -93,19 +93,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   const PrefixPlan& pp = p.pre;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.page_size, G = a.H / a.Hkv, P = a.prefix_len;
-  const bool split_keys = pp.row_tiles == 1;  // the streams take alternate key tiles
-  const uint64_t policy = stream_policy(false);
-  const int step = split_keys ? 2 : 1;        // key tiles from one of a stream's to its next
+  constexpr int step = kSplit ? 2 : 1;  // key tiles from one of a stream's to its next
 
   grid_dep_wait();     // before tensor memory is taken, which what is ahead may still have to take itself
   grid_dep_trigger();  // the own keys' kernel may start where this one leaves room: it needs nothing from here
   if (threadIdx.x < P_COUNT) {
     const int i = threadIdx.x;
     mbar_init(&bars[i], i >= P_PFULL && i < P_PFULL + 4 ? 4
-                        : i >= P_GEMPTY && i < P_GEMPTY + 2 ? (split_keys ? 4 : 8)
-                        : i >= P_VREADY && i < P_VREADY + 2                                     ? kConverters
-                        : i == P_KEMPTY || i == P_KEMPTY + 1 || i == P_VEMPTY || i == P_VEMPTY + 1
-                            ? (split_keys ? 1 : 2)  // the streams that use a key tile
+                        : i >= P_GEMPTY && i < P_GEMPTY + 2 ? (kSplit ? 4 : 8)
+                        : i >= P_VREADY && i < P_VREADY + 3 ? kConverters
+                        : i == P_KEMPTY || i == P_KEMPTY + 1 || (i >= P_VEMPTY && i < P_VEMPTY + 3)
+                            ? (kSplit ? 1 : 2)  // the streams that use a key tile
                         : i == P_DONE ? 2
                                       : 1);
     fence_mbar_init();
@@ -123,6 +121,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   const int u_end = min(a.Hkv * pp.items * pp.line, static_cast<int>(blockIdx.x + 1) * pp.each);
   int u = blockIdx.x * pp.each;
 
+  // V's stages: with one row tile three, the third in the place of a second row tile's Q, since a stream then has
+  // every other tile and would wait for its next V from the end of its last P V on (52.5 -> 50.5 us at 32 sequences behind 16384 tokens,
+  // 72 -> 66 at 30 behind 50000).
+  auto v_round = [](int c) { return kSplit ? c / 3 : c >> 1; };  // of key tile c, and its stage
+  auto v_stage = [](int c) { return kSplit ? c % 3 : c & 1; };
+  auto v_at = [](int st) { return kSplit && st == 2 ? L::kQ + L::kTileBytes : L::kV + st * L::kTileBytes; };
+
   bool ok = true;              // of this thread's role
   uint32_t vmax = 0u;          // converters: largest |v| bit pattern seen, per bf16 half
   int c0 = 0;                  // key tiles before this segment (ring position)
@@ -138,9 +143,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       continue;
     }
     const int nT = t1 - t0;
-    const int T0 = split_keys ? 0 : 2 * it;  // row tile of stream 0; stream 1 has the next, or the same
-    const bool has1 = split_keys ? nT > 1 : T0 + 1 < pp.row_tiles;
-    const int n0 = split_keys ? (nT + 1) / 2 : nT, n1 = split_keys ? nT / 2 : (has1 ? nT : 0);
+    const int T0 = kSplit ? 0 : 2 * it;  // row tile of stream 0; stream 1 has the next, or the same
+    const bool has1 = kSplit ? nT > 1 : T0 + 1 < pp.row_tiles;
+    const int n0 = kSplit ? (nT + 1) / 2 : nT, n1 = kSplit ? nT / 2 : (has1 ? nT : 0);
     const int npages = ceil_div(P, S);
     // Lane i: page i of key tile t, -1 where the prefix has ended.
     auto page_of = [&](int t) {
@@ -149,10 +154,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     };
     if (warp == 8) {
       // -------------------------------------------------------- Q and K
+      const uint64_t policy = stream_policy(false);
       int id = ok ? page_of(t1 - 1) : -1, issued = 0;
       const bool began = ok;
       if (ok) {
-        const int rt1 = !split_keys && has1;
+        const int rt1 = !kSplit && has1;
         if (lane == 0) mbar_arrive_expect_tx(&bars[P_Q], (1 + rt1) * pp.tpt * pp.hp * D * 2);
         __syncwarp();
         if (lane < pp.hp)  // a head a lane
@@ -195,29 +201,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const uint32_t leader = elect_lane();
       constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
       constexpr uint32_t idO = idesc_f16(128, D, false, true);
-      const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::kQ + (split_keys ? 0 : k * L::kTileBytes)), 16, 1024);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::kQ + (kSplit ? 0 : k * L::kTileBytes)), 16, 1024);
       const uint64_t dK = sdesc_sw128(smem_u32(sm + L::kK), 16, 1024);
       const uint64_t dV = sdesc_sw128(smem_u32(sm + L::kV), 16384, 1024);
       const uint32_t tS = tbase + k * 128, tO = tbase + 256 + k * D;
       ok = ok && mbar_wait(&bars[P_Q], seg & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
       // Step s: P V of the stream's key tile s, and S of its next; the step before the first only has the S.
 #pragma unroll 1
-      for (int s = split_keys ? k - 2 : -1, q = -1; s < nT && ok; s += step, ++q) {
+      for (int s = kSplit ? k - 2 : -1, q = -1; s < nT && ok; s += step, ++q) {
         const int c = c0 + s, cn = c + step;
         const bool pv = q >= 0, next = s + step < nT;
+        const int vn = v_round(c), vs = v_stage(c);
         if (mine == 0) {  // an item's missing second row tile: the stages are let go as they come
           if (next) {
             ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
             if (ok && lane == 0) mbar_arrive(&bars[P_KEMPTY + (cn & 1)]);
           }
           if (ok && pv) {
-            ok = mbar_wait(&bars[P_VREADY + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
-            if (ok && lane == 0) mbar_arrive(&bars[P_VEMPTY + (c & 1)]);
+            ok = mbar_wait(&bars[P_VREADY + vs], vn & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+            if (ok && lane == 0) mbar_arrive(&bars[P_VEMPTY + vs]);
           }
           continue;
         }
-        const uint64_t vd = dV + ((c & 1) ? L::kTileBytes >> 4 : 0), kd = dK + ((cn & 1) ? L::kTileBytes >> 4 : 0);
-        if (pv) ok = mbar_wait(&bars[P_VREADY + (c & 1)], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+        const uint64_t vd = dV + static_cast<int64_t>((v_at(vs) - L::kV) >> 4), kd = dK + ((cn & 1) ? L::kTileBytes >> 4 : 0);
+        if (pv) ok = mbar_wait(&bars[P_VREADY + vs], vn & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
 #pragma unroll 1
         for (int h = 0; h < 2 && ok; ++h) {
           if (pv) {
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               umma_ts_e(leader, tO, tS + h * 64 + 32 * (ks >> 1) + 8 * (ks & 1),
                         vd + static_cast<uint64_t>((h * 8192 + ks * 2048) >> 4), idO, q > 0 || h > 0 || ks > 0);
             umma_commit_e(leader, &bars[P_PVDONE + e_bar(k, h)]);
-            if (h == 1) umma_commit_e(leader, &bars[P_VEMPTY + (c & 1)]);
+            if (h == 1) umma_commit_e(leader, &bars[P_VEMPTY + vs]);
           }
           if (next) {
             if (h == 0) ok = mbar_wait(&bars[P_KFULL + (cn & 1)], (cn >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
@@ -256,11 +263,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int first = (warp == 15 ? kConverters - 1 : warp - 12) * 32 + lane;
 #pragma unroll 1
       for (int s = 0; s < nT && ok; ++s) {
-        const int c = c0 + s, st = c & 1, keys = P - (t1 - 1 - s) * kTile;
-        ok = mbar_wait(&bars[P_VFULL + st], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
+        const int c = c0 + s, vn = v_round(c), vs = v_stage(c), keys = P - (t1 - 1 - s) * kTile;
+        ok = mbar_wait(&bars[P_VFULL + vs], vn & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        uint4* tile = reinterpret_cast<uint4*>(sm + L::kV + st * L::kTileBytes);
+        uint4* tile = reinterpret_cast<uint4*>(sm + v_at(vs));
         if (keys < kTile)
 #pragma unroll 1
           for (int e = first; e < L::kTileBytes / 16; e += 32 * kConverters)  // eight pieces a row of 64 channels
@@ -282,17 +289,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[P_VREADY + st]);
+        if (lane == 0) mbar_arrive(&bars[P_VREADY + vs]);
       }
     } else if (warp >= 10) {
       // ------------------------------------------------------ V and gates
       const int head0 = hkv * G, mine = warp - 10;  // the stage of this warp
       const int s0 = (c0 & 1) == mine ? 0 : 1;
       const int last = P - 1, lpage = checked_page(a, a.prefix[last >> a.page_shift]);
+      const uint64_t policy = stream_policy(false);
       int id = ok ? page_of(t1 - 1 - s0) : -1, issued = 0;
 #pragma unroll 1
       for (int s = s0; s < nT && ok; s += 2) {
-        const int c = c0 + s, st = c & 1, n = c >> 1, here = id;
+        const int c = c0 + s, st = c & 1, n = c >> 1, vn = v_round(c), vs = v_stage(c), here = id;
         const int t = t1 - 1 - s, j0 = t * kTile, j = j0 + lane * 4;
         const bool in = j < P;
         id = page_of(s + 2 < nT ? t - 2 : -1);
@@ -322,15 +330,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
           if (first) {
             first = false;
-            ok = n == 0 || mbar_wait(&bars[P_VEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
+            ok = vn == 0 || mbar_wait(&bars[P_VEMPTY + vs], (vn - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bars[P_VFULL + st], loaded * S * D * 2);
+            if (lane == 0) mbar_arrive_expect_tx(&bars[P_VFULL + vs], loaded * S * D * 2);
             __syncwarp();
             if (here >= 0)
 #pragma unroll 1
               for (int y = 0; y < D / 64; ++y)
-                tma_load_4d_by(policy, sm + L::kV + st * L::kTileBytes + y * 16384 + lane * S * 128, &tmap_v, &bars[P_VFULL + st],
+                tma_load_4d_by(policy, sm + v_at(vs) + y * 16384 + lane * S * 128, &tmap_v, &bars[P_VFULL + vs],
                             y * 64, 0, hkv, here);
             ++issued;
             ok = n == 0 || mbar_wait(&bars[P_GEMPTY + st], (n - 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
@@ -360,10 +368,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[P_GFULL + st]);
       }
-      if (issued > 0) {
-        const int c = c0 + s0 + 2 * (issued - 1);
-        mbar_wait_drain(&bars[P_VFULL + (c & 1)], (c >> 1) & 1);
-      }
+      // Every copy issued lands before the segment ends, also where a wait gave up (of this warp's last two, one
+      // may be through and its stage taken by the other warp's next: then the wait only runs out). Where none did, the conversion has seen them all.
+      if (!ok || *abort_flag)
+#pragma unroll 1
+        for (int i = max(issued - 2, 0); i < issued; ++i) {
+          const int c = c0 + s0 + 2 * i;
+          mbar_wait_drain(&bars[P_VFULL + v_stage(c)], v_round(c) & 1);
+        }
     } else {
       // ----------------------------------------------- softmax, epilogue
       const int k = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       int q = 0;  // tiles of this stream so far
 #pragma unroll 1
       for (int s = 0; s < nT && ok; ++s) {
-        if (split_keys && (s & 1) != k) continue;
+        if (kSplit && (s & 1) != k) continue;
         const int c = c0 + s, st = c & 1;
         ok = mbar_wait(&bars[P_GFULL + st], (c >> 1) & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_SYNC);
 #pragma unroll 1
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
           pp.ml[slot] = make_float2(m, l);
         }
-      } else if (split_keys) {
+      } else if (kSplit) {
         pp.ml[slot] = make_float2(-INFINITY, 0.f);  // one key tile: this stream had none
       }
     }
@@ -515,10 +527,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kSplit>
 cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t s) {
   using L = PrefixLayout<D>;
-  auto kernel = prefix_kernel<D>;
+  auto kernel = prefix_kernel<D, kSplit>;
   // At least 116 KB, so that one CTA, which takes all of tensor memory, is ever resident on an SM.
   size_t smem = 1024 + L::kKap + sizeof(float) * 2 * p.pre.kap_tiles * p.pre.hp * kKapPitch;
   static_assert(1024 + PrefixLayout<128>::kKap + 4 * 2 * 2 * kMaxHp * kKapPitch <= 232448 - 512, "shared memory");
@@ -571,7 +583,8 @@ cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s) {
       !make_page_map(&maps[1], a.k, a.d, a.page_size, a.Hkv, a.num_pages, a.page_size) ||
       !make_page_map(&maps[2], a.v, a.d, a.page_size, a.Hkv, a.num_pages, a.page_size))
     return cudaErrorInvalidValue;
-  return a.d == 64 ? launch<64>(p, maps, s) : launch<128>(p, maps, s);
+  if (p.pre.row_tiles == 1) return a.d == 64 ? launch<64, true>(p, maps, s) : launch<128, true>(p, maps, s);
+  return a.d == 64 ? launch<64, false>(p, maps, s) : launch<128, false>(p, maps, s);
 }
 
 }  // namespace fox
