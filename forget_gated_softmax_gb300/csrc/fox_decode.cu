@@ -155,9 +155,9 @@ struct DecodeLayout {
 };
 
 // Whether a prefix is worth sharing out: one kernel that walks it for every sequence takes as long as its
-// K and V take to come (mostly from the L2 cache) so many times; sharing takes two more kernels, some ten
-// microseconds here and there. At 50 MB walking took 26 to 27 us against 28 to 30, at 100 MB 29 to 34
-// against 30 to 33 (with 64 channels 50 against 40), at 200 MB 46 to 62 against 32 to 41.
+// K and V take to come (mostly from the L2 cache) so many times; sharing takes two more kernels, some
+// microseconds here and there. At 47 MB walking took 19 to 23 us against 24 to 25, at 69 MB 24.7 and 28.3 against
+// 24.8 and 28.7, at 78 MB 27.7 against 26.5, at 106 MB 31 against 25.5, at 150 MB 39 against 29.
 bool share_prefix(const PagedArgs& a, int row_tiles) {
   return (long long)a.B * row_tiles * a.prefix_len * a.Hkv * a.d * 4 > (72ll << 20);
 }

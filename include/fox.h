@@ -53,12 +53,14 @@ typedef enum fox_status {
   FOX_OK = 0,
   FOX_ERR_INVALID_ARG = 1, /* null pointer, negative size, misalignment, bad flag or dtype */
   FOX_ERR_UNSUPPORTED = 2, /* well-formed but not implemented (d not in {64, 128}; fp32 backward;
-                              non_causal or tile_skip with fp32; tile_skip with non_causal) */
+                              non_causal or tile_skip with fp32; tile_skip with non_causal;
+                              other page sizes; a batch beyond the limits of its counts) */
   FOX_ERR_WORKSPACE = 3,   /* workspace null, misaligned or smaller than the size query */
   FOX_ERR_CUDA = 4,        /* a CUDA runtime call or kernel launch failed */
   FOX_ERR_TIMEOUT = 5,     /* a device-side bounded wait gave up (from fox_check_error) */
   FOX_ERR_DEVICE = 6       /* another device-side error bit was set (from fox_check_error), e.g. a
-                              V value outside the fp16 range of the forward's P V product */
+                              V value outside the fp16 range of the forward's P V product, or a
+                              length or page id that does not fit (paged cache) */
 } fox_status;
 
 enum { FOX_DTYPE_BF16 = 0, FOX_DTYPE_F32 = 1 };
