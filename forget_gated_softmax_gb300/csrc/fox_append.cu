@@ -5,9 +5,10 @@
 // (a, b) = (i, i + dim / 2), or (2i, 2i + 1) with `pairs`. The products and the sum are fp32 and
 // round once, to the cache's type.
 //
-// With one page a sequence at most (steps of generation) one launch does it all, copies and gates in
-// different blocks. Longer ones take three: gates, then the scan of the pages' bases, and the copies, which
-// need neither and run beside both (programmatic dependents that wait for their forerunner only at the end).
+// One launch does copies and gates, in different blocks (the gates' first: they are few and slow). Where a
+// sequence may bring more than one page, the scan of the pages' bases follows (gates, scan and copies in three
+// launches: 6 prompts of up to 16384 tokens 268 against 262 us, 4 of up to 2000 36.6 against 31, 2 of 257 17 against
+// 15.4).
 //
 // Gates: with a_t = log sigmoid(z_t), g of a token is the sum of a from its page's first token on
 // (fp32) and gbase of a page the sum before it (fp64 arithmetic, kept as two fp32). A page's sums
@@ -15,7 +16,7 @@
 // takes its base from the page before.
 //
 // Bound by memory: each of k, v (q) read once and written once. 6 prompts of up to 16384 tokens (1.44 GB) take
-// 266 us, 5.4 TB/s; one token of 128 sequences 9 us, the launch and a few dependent trips to memory.
+// 262 us, 5.5 TB/s; one token of 128 sequences 9 us, the launch and a few dependent trips to memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,7 +42,7 @@ struct AppendParams {
   const float* cos;
   const float* sin;
   int max_pos, rot, pairs;
-  int copy_blocks;                  // blocks [0, copy_blocks) copy, the others scan gates
+  int gate_blocks;                  // blocks [0, gate_blocks) sum gates, the others copy
   int page_chunks, head_groups;     // gate block: (sequence, page chunk, head group)
   int scan_bases;                   // bases of pages after a sequence's first are left to base_scan_kernel
 };
@@ -165,7 +166,8 @@ __device__ __forceinline__ void copy_rows(const AppendParams& p, RowPlace* place
   const int hs = (kN == 8 ? 2 : 3) + (a.d == 128), hp = 1 << hs;  // units of a head
   const int nk = a.Hkv << hs;
   const CopyShape x = copy_shape(2 * nk + (p.qn ? a.H << hs : 0));
-  const int tid = threadIdx.x, chunk = blockIdx.x % x.chunks, row0 = blockIdx.x / x.chunks * (kRows * x.side);
+  const int tid = threadIdx.x, block = blockIdx.x - p.gate_blocks;
+  const int chunk = block % x.chunks, row0 = block / x.chunks * (kRows * x.side);
   const int sub = x.side > 1 ? tid / x.per_row : 0, at = x.side > 1 ? tid - sub * x.per_row : chunk * kThreads + tid;
   const bool live = at < x.per_row && sub < x.side, is_v = at >= nk && at < 2 * nk, is_q = at >= 2 * nk;
   const int w = is_q ? at - 2 * nk : is_v ? at - nk : at, h = w >> hs, j = w & (hp - 1);
@@ -246,7 +248,7 @@ __device__ __forceinline__ void put_base(float* gbase, size_t at, double c) {
 }
 
 __device__ __forceinline__ double base_of(const PagedArgs& a, int page, int h) {
-  const float2 x = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
+  const float2 x = __ldcg(reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h)));
   return static_cast<double>(x.x) + x.y;
 }
 
@@ -267,7 +269,7 @@ __device__ __forceinline__ double gate_before(const PagedArgs& a, int b, int own
 __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kGateHeads + 1]) {
   const PagedArgs& a = p.a;
   const int S = a.page_size;
-  int idx = blockIdx.x - p.copy_blocks;
+  int idx = blockIdx.x;
   const int hg = idx % p.head_groups;
   idx /= p.head_groups;
   const int chunk = idx % p.page_chunks, b = idx / p.page_chunks;
@@ -356,47 +358,51 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendP
     float zs[128][kGateHeads + 1];
     RowPlace places[kBlockRows];
   } sh;
-  // The copies of a call of three launches need nothing of the other two, but what follows them needs these.
-  const bool last = p.scan_bases && p.copy_blocks > 0;
-  if (!last) grid_dep_wait();
+  grid_dep_wait();
   grid_dep_trigger();
-  if (static_cast<int>(blockIdx.x) < p.copy_blocks)
-    copy_rows<T>(p, sh.places);
-  else
+  if (static_cast<int>(blockIdx.x) < p.gate_blocks)
     gate_block(p, sh.zs);
-  if (last) grid_dep_wait();
+  else
+    copy_rows<T>(p, sh.places);
 }
 
 // Bases of the pages after a sequence's first one: base_k = base_0 + sum of the full pages' sums.
 // One warp a (sequence, head), 32 pages a step, fp64.
 __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams p) {
   grid_dep_trigger();
-  grid_dep_wait();
+  // Lengths and tables are the caller's: only what the gates' blocks write has to be waited for.
   const PagedArgs& a = p.a;
   const int S = a.page_size;
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (w >= (long long)a.B * a.H) return;
-  const int b = static_cast<int>(w / a.H), h = static_cast<int>(w % a.H);
+  const bool live = w < (long long)a.B * a.H;
+  const int b = live ? static_cast<int>(w / a.H) : 0, h = live ? static_cast<int>(w % a.H) : 0;
   bool bad;
   const SeqInfo s = seq_info(a, b, &bad);
-  if (s.own < 0 || s.n == 0) return;
   const int p0 = (s.own - s.n) / S, pl = (s.own - 1) / S;  // first and last page index of the new tokens
-  if (pl == p0) return;
-  const int id0 = own_page(a, b, p0 * S);
-  if (id0 < 0) return;  // reported by its gate block
-  double carry = base_of(a, id0, h);
+  const int id0 = live && s.own >= 0 && s.n > 0 && pl > p0 ? own_page(a, b, p0 * S) : -1;
+  if (id0 < 0) {  // nothing to do, or reported by its gate block
+    grid_dep_wait();
+    return;
+  }
+  double carry = 0.0;
   constexpr int kSteps = 4;  // of 32 pages, their loads in flight together
   for (int k = p0 + 1; k <= pl; k += 32 * kSteps) {
     float full[kSteps];
-    int id[kSteps];
+    int id[kSteps], before[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int kk = k + 32 * i + lane;
       const int prev = kk <= pl ? own_page(a, b, (kk - 1) * S) : -1;
       id[i] = kk <= pl ? own_page(a, b, kk * S) : -1;
-      full[i] = prev >= 0 ? a.g[g_offset(a, prev, h, S - 1)] : 0.f;
+      before[i] = prev;
     }
+    if (k == p0 + 1) {
+      grid_dep_wait();
+      carry = base_of(a, id0, h);
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) full[i] = before[i] >= 0 ? __ldcg(a.g + g_offset(a, before[i], h, S - 1)) : 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       double x = full[i];
@@ -421,28 +427,17 @@ cudaError_t launch(AppendParams p, cudaStream_t s) {
   p.scan_bases = a.max_new > a.page_size;
   const long long gates = (long long)a.B * p.page_chunks * p.head_groups;
   if (copy + gates > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (!p.scan_bases) {
-    p.copy_blocks = static_cast<int>(copy);
-    TraceScope trace("cache_append", s);
-    const cudaError_t f =
-        launch_dependent(cache_append_kernel<T>, dim3(static_cast<unsigned>(copy + gates)), dim3(kThreads), 0, s, p);
-    return f != cudaSuccess ? f : cudaGetLastError();
-  }
+  p.gate_blocks = static_cast<int>(gates);
   cudaError_t e;
   {
-    p.copy_blocks = 0;
-    TraceScope trace("cache_gates", s);
-    e = launch_dependent(cache_append_kernel<T>, dim3(static_cast<unsigned>(gates)), dim3(kThreads), 0, s, p);
+    TraceScope trace("cache_append", s);
+    e = launch_dependent(cache_append_kernel<T>, dim3(static_cast<unsigned>(gates + copy)), dim3(kThreads), 0, s, p);
   }
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && p.scan_bases) {
     TraceScope trace("cache_base_scan", s);
     const long long warps = (long long)a.B * a.H;
-    e = launch_dependent(base_scan_kernel, dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32))), dim3(kThreads), 0, s, p);
-  }
-  if (e == cudaSuccess) {
-    p.copy_blocks = static_cast<int>(copy);
-    TraceScope trace("cache_copy", s);
-    e = launch_dependent(cache_append_kernel<T>, dim3(static_cast<unsigned>(copy)), dim3(kThreads), 0, s, p);
+    e = launch_dependent(base_scan_kernel, dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32))),
+                         dim3(kThreads), 0, s, p);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
