@@ -48,7 +48,10 @@ constexpr int kConverters = 3;  // two: 142 us where three take 137
 constexpr int kMaxHp = 16;
 constexpr int kOpening = 4;  // key tiles' time
 constexpr int kKapPitch = kTile + 4;  // floats: the heads' rows start in different banks
-constexpr float kRaise = 8.0f;        // log2 units that a row may pass its running maximum by
+constexpr float kRaise = 4.0f;        // log2 units that a row may pass its running maximum by
+// P is 2^kLift times the weight against the running maximum (and below 2^15 with what that may be passed by): fp16
+// then holds weights down to 2^-25 with all its bits and the least 2^-35, where a long prefix's many small ones count.
+constexpr float kLift = 11.0f;
 
 template <int D>
 struct PrefixLayout {
@@ -402,12 +405,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                              (st * pp.hp * pp.kap_tiles + kap_row) * kKapPitch + h * 64;
           const int lim = P - (t1 - 1 - s) * kTile - h * 64;  // columns from lim on are not keys
           // P and the row's maximum in one pass, with the running maximum; where a row has passed that by more
-          // than 2^8 (rare after the first tile), once more with the new one: S is still there.
+          // than 2^4 (rare after the first tile), once more with the new one: S is still there.
           uint32_t pk[32];
           float2 sum;
 #pragma unroll 1
           for (int again = 0;; ++again) {
-            const float off = m == -INFINITY ? 0.f : m;
+            const float off = m == -INFINITY ? 0.f : m - kLift;
             const float2 noff = make_float2(-off, -off);
             float mn = INFINITY;  // of tn_j = kap_j - scale2 S_j = -x_j
             sum = make_float2(0.f, 0.f);
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
-          pp.ml[slot] = make_float2(m, l);
+          pp.ml[slot] = make_float2(m - kLift, l);
         }
       } else if (kSplit) {
         pp.ml[slot] = make_float2(-INFINITY, 0.f);  // one key tile: this stream had none

@@ -336,7 +336,8 @@ fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, co
  * A shared prefix of a bf16 cache is, where that saves more than it costs (B * prefix_len * Hkv * d * 4 bytes
  * above 72 MB, counted once for every 16 rows that a sequence brings a key head), multiplied once with the rows of
  * all sequences: its weights and V then pass through fp16 as in fox_fwd, so that |v| >= 65536 in its pages sets the
- * error word. Otherwise, and in fp32, every sequence walks it.
+ * error word, and V below 2^-14 is held in steps of 2^-24. Otherwise, and in fp32, every sequence walks it, with V as
+ * it is.
  * A K or V slot behind the sequence's end is never used, whatever it holds. The same arguments and
  * contents give the same bits; how a row's sums are ordered follows from the lengths of the whole batch.
  */

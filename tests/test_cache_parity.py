@@ -284,6 +284,29 @@ def test_scores_that_rise_towards_the_prefix_s_start(fox, own, H, Hkv, d, S, P):
     assert (lse.double() - rl).abs().max().item() <= foxtest.TOL_LSE_BF16
 
 
+def test_many_small_weights_of_a_shared_prefix_count(fox):
+    """One key of weight 1 and 400000 of 2^-26 whose values agree: O is 0.6 by these alone. Weights in fp16 that go down
+    to 2^-35 are off by 2^-10 of themselves at 2^-26, and O is rounded by 2^-9 of itself: 2e-3."""
+    P, d = 400000, 64
+    c = Case([1, 1], [1, 1], 1, 1, d, 128, prefix=P, uniform=True, seed=5)
+    k, v, z = c.pre
+    k.zero_()
+    k[P // 3] = 2.25  # a score of 18 = 64 * 2.25 / 8 against q of ones; 18 log2 e = 25.97
+    v.fill_(100.0)
+    v[P // 3] = 0.0
+    z.fill_(float("inf"))
+    c.q.fill_(1.0)
+    for own in c.seq:
+        own[0].zero_()
+        own[1].zero_()
+    c.put()
+    o, lse = fox.fox_decode(c.cache(fox), c.batch(fox), c.q)
+    ro, rl = c.attend()
+    assert 0.3 < ro.min().item() and ro.max().item() < 0.7
+    assert (o.double() - ro).abs().max().item() <= 2e-3
+    assert (lse.double() - rl).abs().max().item() <= foxtest.TOL_LSE_BF16
+
+
 @pytest.mark.parametrize("B,P", [(3, 100), (40, 5003)])
 def test_bad_pages_of_a_prefix_are_reported(fox, B, P):
     """Page ids of the prefix outside the pool: reported, read as page 0 (finite here), nothing else."""
