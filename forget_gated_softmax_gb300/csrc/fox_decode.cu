@@ -170,7 +170,7 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   const int most = a.max_new * L.Gp;
   L.Rs = most < L.Rt ? most : L.Rt;
   L.RTmax = ceil_div(most, L.Rt);
-  L.workers = kSMs * (f32 ? kF32Warps : decode_mma_warps(a.d));
+  L.workers = f32 ? f32_ctas(a.d) * kF32Warps : kSMs * decode_mma_warps(a.d);
   const size_t slots = (size_t)L.workers + (size_t)a.B * a.Hkv * L.RTmax;
   L.cum = kCacheHeaderBytes;
   L.po_rows = (long long)slots * L.Rs;
@@ -224,7 +224,7 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.pre = L.pre;
   p.pre.ml = reinterpret_cast<float2*>(ws + L.pml);
   p.pre.po = reinterpret_cast<float*>(ws + L.ppo);
-  static_assert(kErrWordBytes + 4 * kSMs <= kCacheHeaderBytes, "a counter a CTA");
+  static_assert(kErrWordBytes + 4 * 2 * kSMs <= kCacheHeaderBytes, "a counter a CTA");
   const cudaError_t e = p.pre.key_tiles > 0 ? launch_prefix(p, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
   if (f32) return launch_decode_f32(p, s);

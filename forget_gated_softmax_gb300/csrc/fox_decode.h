@@ -485,6 +485,9 @@ cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t s);
 // The fp32 kernel (fox_decode_f32.cu): row tile, workers of a CTA, CTAs of an SM, launch.
 constexpr int kF32Rows = 8;
 constexpr int kF32Warps = 4;
+// CTAs: of 64 channels two fit an SM's shared memory (4 sequences of up to 2000 28 -> 21 us against one; eight warps in
+// one CTA were as fast there, but crowd short calls on few SMs: 14 -> 16.6 us).
+constexpr int f32_ctas(int d) { return d == 128 ? kSMs : 2 * kSMs; }
 cudaError_t launch_decode_f32(const DecodeParams& p, cudaStream_t s);
 PrefixPlan prefix_plan(const PagedArgs& a);
 cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s);

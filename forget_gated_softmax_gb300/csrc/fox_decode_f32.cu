@@ -10,8 +10,9 @@
 // whole, by asynchronous copies (a row of 512 bytes an instruction): K of the next tile while this one's
 // V is used, V of the next while its K is. Scores: a lane owns a key, whose row it reads with the rows
 // padded to different banks. Values: a lane owns d / 32 channels. The prefix's keys, where one is
-// shared, are walked like the sequence's own. Bound by latency at the lengths that fp32 is used for: 2 sequences of
-// 257 take 14 us.
+// shared, are walked like the sequence's own. Bound by latency where they are short (2 sequences of 257: 14 us), by
+// the few warps that shared memory leaves an SM where they are long (16 of up to 1000 with 16 heads of 64 channels,
+// 75 MB: 38 us).
 #include "fox_decode.h"
 
 namespace fox {
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
   extern __shared__ float4 smem4[];
   __shared__ int scratch[W];
   __shared__ Gate2 ci[W][kF32Rows];
-  __shared__ int offs[kSMs + 1];
+  __shared__ int offs[2 * kSMs + 1];
   __shared__ Column part[32 * W];
   __shared__ Kept<kF32Rows, W> kept;
   __shared__ BlockEnds ends;
@@ -57,15 +58,16 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
   // This lane's key of a tile: its place in the pools, as elements and gate slot; page -1: no key.
   int page = -1, slot = 0;
   size_t kv = 0;
-  auto find_key = [&](int tile) {
+  // The table's entry comes a tile ahead of its use: its key's page, -1 (reported) where it is none; -2: no key.
+  auto look_up = [&](int tile) {
     const bool pre = tile < tp;
     const int j = (pre ? tile : tile - tp) * kKeyTile + lane;
-    page = -1;
-    slot = j & (S - 1);
-    if (j < (pre ? P : at.s.own)) {
-      page = pre ? prefix_page(a, j) : own_page(a, at.b, j);
-      if (page < 0 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
-    }
+    return j >= (pre ? P : at.s.own) ? -2 : pre ? prefix_page(a, j) : own_page(a, at.b, j);
+  };
+  auto find_key = [&](int tile, int id) {
+    page = max(id, -1);
+    if (id == -1 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
+    slot = ((tile < tp ? tile : tile - tp) * kKeyTile + lane) & (S - 1);
     kv = page < 0 ? 0 : kv_offset(a, page, at.hkv, slot);
   };
   // Rows of K or V of the tile whose keys the lanes hold; zeros for no key.
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
     // A segment: key tiles tile0 .. tile1 - 1 of one item.
     const Seq s = at.s;
     const int hkv = at.hkv, rt = at.rt, tile0 = at.tile, tile1 = min(at.tiles, tile0 + left), R = rows_of(p, at);
-    find_key(tile0);
+    find_key(tile0, look_up(tile0));
     ask(ks, L::kKPitch, a.k);
     ask(vs, D, a.v);
 #pragma unroll 1
@@ -118,7 +120,22 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
 #pragma unroll 1
     for (int tile = tile0; tile < tile1; ++tile) {
       // own place of this lane's key: before every row's for the prefix
-      const int j = tile < tp ? -1 : (tile - tp) * kKeyTile + lane, my_page = page, my_slot = slot;
+      const int j = tile < tp ? -1 : (tile - tp) * kKeyTile + lane;
+      const int next = tile + 1 < tile1 ? look_up(tile + 1) : -2;
+      // c_i - c_j of the rows, -inf where the key is none of a row's; on their way while K is waited for.
+      float bias[kF32Rows];
+#pragma unroll
+      for (int r = 0; r < kF32Rows; ++r) {
+        bias[r] = -INFINITY;
+        if (r >= R) continue;
+        const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
+        if (page >= 0 && j <= s.own - s.n + t) {
+          const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, page, h));
+          const int gs = slot - p.bias_from_j;
+          const float gj = gs >= 0 ? a.g[g_offset(a, page, h, gs)] : 0.f;
+          bias[r] = (ci[warp][r].hi - base.x) + (ci[warp][r].lo - base.y) - gj;
+        }
+      }
       cp_async_wait<1>();  // K
       __syncwarp();
       float sc[kF32Rows];
@@ -136,7 +153,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
       }
       __syncwarp();
       if (tile + 1 < tile1) {
-        find_key(tile + 1);
+        find_key(tile + 1, next);
         ask(ks, L::kKPitch, a.k);
       } else {
         cp_async_commit();  // nothing: the groups stay in step
@@ -145,15 +162,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
 #pragma unroll
       for (int r = 0; r < kF32Rows; ++r) {
         if (r >= R) break;
-        float x = -INFINITY;
-        const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
-        if (my_page >= 0 && j <= s.own - s.n + t) {
-          const float2 base = *reinterpret_cast<const float2*>(a.gbase + gbase_offset(a, my_page, h));
-          const int gs = p.bias_from_j ? my_slot - 1 : my_slot;
-          const float gj = gs >= 0 ? a.g[g_offset(a, my_page, h, gs)] : 0.f;
-          const float beta = (ci[warp][r].hi - base.x) + (ci[warp][r].lo - base.y);
-          x = fmaf(beta - gj, kLog2e, sc[r]);
-        }
+        const float x = bias[r] == -INFINITY ? -INFINITY : fmaf(bias[r], kLog2e, sc[r]);
         float top = x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -222,13 +231,13 @@ template <int D>
 cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
   using L = F32Layout<D>;
   const size_t smem = sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * ((size_t)p.a.B + 1);
-  static_assert(sizeof(float) * kF32Warps * F32Layout<128>::kWarpFloats + sizeof(SeqEntry) * (kMaxSeqs + 1) <= 232448 - 8192,
-                "shared memory");
+  static_assert(sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * (kMaxSeqs + 1) <= 232448 - 16384,
+                "shared memory, less the static part");
   const cudaError_t e =
       cudaFuncSetAttribute(decode_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode", s);
-  const cudaError_t f = launch_dependent(decode_f32_kernel<D>, dim3(kSMs), dim3(32 * kF32Warps), smem, s, p);
+  const cudaError_t f = launch_dependent(decode_f32_kernel<D>, dim3(f32_ctas(D)), dim3(32 * kF32Warps), smem, s, p);
   return f != cudaSuccess ? f : cudaGetLastError();
 }
 
