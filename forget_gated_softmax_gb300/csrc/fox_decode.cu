@@ -165,7 +165,7 @@ bool share_prefix(const PagedArgs& a, int row_tiles) {
 DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   DecodeLayout L;
   const int G = a.H / a.Hkv;
-  L.Rt = f32 ? kF32Rows : decode_mma_rows(a.max_new * G);
+  L.Rt = f32 ? decode_f32_rows(a.max_new * G) : decode_mma_rows(a.max_new * G);
   L.Gp = padded_group(G, L.Rt);
   const int most = a.max_new * L.Gp;
   L.Rs = most < L.Rt ? most : L.Rt;

@@ -483,7 +483,7 @@ int decode_mma_rows(int rows);
 int decode_mma_warps(int d);
 cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t s);
 // The fp32 kernel (fox_decode_f32.cu): row tile, workers of a CTA, CTAs of an SM, launch.
-constexpr int kF32Rows = 8;
+int decode_f32_rows(int rows);
 constexpr int kF32Warps = 4;
 // CTAs: of 64 channels two fit an SM's shared memory (4 sequences of up to 2000 28 -> 21 us against one; eight warps in
 // one CTA were as fast there, but crowd short calls on few SMs: 14 -> 16.6 us).

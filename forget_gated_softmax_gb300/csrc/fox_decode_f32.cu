@@ -12,34 +12,37 @@
 // padded to different banks. Values: a lane owns d / 32 channels. The prefix's keys, where one is
 // shared, are walked like the sequence's own. Bound by latency where they are short (2 sequences of 257: 14 us), by
 // the few warps that shared memory leaves an SM where they are long (16 of up to 1000 with 16 heads of 64 channels,
-// 75 MB: 38 us).
+// 75 MB: 35 us).
 #include "fox_decode.h"
 
 namespace fox {
 namespace {
 
-template <int D>
+template <int D, int NR>
 struct F32Layout {
   static constexpr int kKPitch = D + 4;  // floats of a K row in shared memory
-  static constexpr int kWarpFloats = kKeyTile * kKPitch + kKeyTile * D + kF32Rows * D;  // K, V, queries or kept rows
+  static constexpr int kWarpFloats = kKeyTile * kKPitch + kKeyTile * D + NR * D;  // K, V, queries or kept rows
 };
 
-template <int D>
+// NR: rows of a row tile. Loops over rows have no other bound: with one known only at run time every row was a
+// branch (8 sequences of up to 3000, 16 rows a key head: 69 -> 41 us; 4 of 2000 with 4 rows: 34 -> 23; 16 of 1000
+// with one, 64 channels: 38 -> 35).
+template <int D, int NR>
 __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid_constant__ DecodeParams p) {
-  using L = F32Layout<D>;
+  using L = F32Layout<D, NR>;
   constexpr int E = D / 32, W = kF32Warps;
   extern __shared__ float4 smem4[];
   __shared__ int scratch[W];
-  __shared__ Gate2 ci[W][kF32Rows];
+  __shared__ Gate2 ci[W][NR];
   __shared__ int offs[2 * kSMs + 1];
   __shared__ Column part[32 * W];
-  __shared__ Kept<kF32Rows, W> kept;
+  __shared__ Kept<NR, W> kept;
   __shared__ BlockEnds ends;
   float* smem = reinterpret_cast<float*>(smem4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* ks = smem + warp * L::kWarpFloats;
   float* vs = ks + kKeyTile * L::kKPitch;
-  float* qs = vs + kKeyTile * D;  // [kF32Rows][D] scaled queries; at a segment's end its rows of O
+  float* qs = vs + kKeyTile * D;  // [NR][D] scaled queries; at a segment's end its rows of O
   SeqEntry* seqs = reinterpret_cast<SeqEntry*>(smem + W * L::kWarpFloats);
   const PagedArgs& a = p.a;
   grid_dep_wait();
@@ -92,11 +95,11 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
     ask(ks, L::kKPitch, a.k);
     ask(vs, D, a.v);
 #pragma unroll 1
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < NR; ++r) {
       const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
       const float* src = static_cast<const float*>(p.q) + (size_t)(s.row0 + t) * p.q_stride + (size_t)h * D;
       if (lane < D / 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src + lane * 4);
+        const float4 f = r < R ? *reinterpret_cast<const float4*>(src + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4*>(qs + r * D + lane * 4) =
             make_float4(f.x * p.scale2, f.y * p.scale2, f.z * p.scale2, f.w * p.scale2);
       }
@@ -109,9 +112,9 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
     first = false;
     __syncwarp();
 
-    float m[kF32Rows], l[kF32Rows], acc[kF32Rows][E];
+    float m[NR], l[NR], acc[NR][E];
 #pragma unroll
-    for (int r = 0; r < kF32Rows; ++r) {
+    for (int r = 0; r < NR; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
 #pragma unroll
@@ -123,9 +126,9 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
       const int j = tile < tp ? -1 : (tile - tp) * kKeyTile + lane;
       const int next = tile + 1 < tile1 ? look_up(tile + 1) : -2;
       // c_i - c_j of the rows, -inf where the key is none of a row's; on their way while K is waited for.
-      float bias[kF32Rows];
+      float bias[NR];
 #pragma unroll
-      for (int r = 0; r < kF32Rows; ++r) {
+      for (int r = 0; r < NR; ++r) {
         bias[r] = -INFINITY;
         if (r >= R) continue;
         const int rr = rt * p.Rt + r, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1);
@@ -138,15 +141,14 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
       }
       cp_async_wait<1>();  // K
       __syncwarp();
-      float sc[kF32Rows];
+      float sc[NR];
 #pragma unroll
-      for (int r = 0; r < kF32Rows; ++r) sc[r] = 0.f;
+      for (int r = 0; r < NR; ++r) sc[r] = 0.f;
 #pragma unroll 2
       for (int c = 0; c < D; c += 4) {
         const float4 f = *reinterpret_cast<const float4*>(ks + lane * L::kKPitch + c);
 #pragma unroll
-        for (int r = 0; r < kF32Rows; ++r) {
-          if (r >= R) break;
+        for (int r = 0; r < NR; ++r) {
           const float4 q = *reinterpret_cast<const float4*>(qs + r * D + c);
           sc[r] = fmaf(q.x, f.x, fmaf(q.y, f.y, fmaf(q.z, f.z, fmaf(q.w, f.w, sc[r]))));
         }
@@ -160,8 +162,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
       }
       // Scores to weights.
 #pragma unroll
-      for (int r = 0; r < kF32Rows; ++r) {
-        if (r >= R) break;
+      for (int r = 0; r < NR; ++r) {
         const float x = bias[r] == -INFINITY ? -INFINITY : fmaf(bias[r], kLog2e, sc[r]);
         float top = x;
 #pragma unroll
@@ -182,8 +183,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < E; ++e) f[e] = vs[jj * D + lane * E + e];
 #pragma unroll
-        for (int r = 0; r < kF32Rows; ++r) {
-          if (r >= R) break;
+        for (int r = 0; r < NR; ++r) {
           const float wt = __shfl_sync(0xffffffffu, sc[r], jj);
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[r][e] = fmaf(wt, f[e], acc[r][e]);
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
     const bool alone = at.i0 >= u0 && at.i0 + at.tiles <= u1, keep = !alone && tile1 - tile0 == left;
     __syncwarp();
 #pragma unroll
-    for (int r = 0; r < kF32Rows; ++r) {
+    for (int r = 0; r < NR; ++r) {
       float sum = l[r];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -223,28 +223,32 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
     if (tile1 == at.tiles && left > 0) next_item(p, seqs, at);
   }
   clear_idle_rows<float, D>(p, seqs);
-  join_items<float, D, kF32Rows, W>(p, seqs, total, each, kept, ends, smem + kKeyTile * (L::kKPitch + D), L::kWarpFloats, D,
+  join_items<float, D, NR, W>(p, seqs, total, each, kept, ends, smem + kKeyTile * (L::kKPitch + D), L::kWarpFloats, D,
                                     offs, part);
 }
 
-template <int D>
+template <int D, int NR>
 cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
-  using L = F32Layout<D>;
+  using L = F32Layout<D, NR>;
   const size_t smem = sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * ((size_t)p.a.B + 1);
   static_assert(sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * (kMaxSeqs + 1) <= 232448 - 16384,
                 "shared memory, less the static part");
   const cudaError_t e =
-      cudaFuncSetAttribute(decode_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      cudaFuncSetAttribute(decode_f32_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode", s);
-  const cudaError_t f = launch_dependent(decode_f32_kernel<D>, dim3(f32_ctas(D)), dim3(32 * kF32Warps), smem, s, p);
+  const cudaError_t f = launch_dependent(decode_f32_kernel<D, NR>, dim3(f32_ctas(D)), dim3(32 * kF32Warps), smem, s, p);
   return f != cudaSuccess ? f : cudaGetLastError();
 }
 
 }  // namespace
 
+// The least that takes the most rows a sequence may bring a key head; more are tiles of 8.
+int decode_f32_rows(int rows) { return rows <= 1 ? 1 : rows <= 4 ? 4 : 8; }
+
 cudaError_t launch_decode_f32(const DecodeParams& p, cudaStream_t s) {
-  return p.a.d == 64 ? launch<64>(p, s) : launch<128>(p, s);
+  if (p.a.d == 64) return p.Rt == 1 ? launch<64, 1>(p, s) : p.Rt == 4 ? launch<64, 4>(p, s) : launch<64, 8>(p, s);
+  return p.Rt == 1 ? launch<128, 1>(p, s) : p.Rt == 4 ? launch<128, 4>(p, s) : launch<128, 8>(p, s);
 }
 
 }  // namespace fox
