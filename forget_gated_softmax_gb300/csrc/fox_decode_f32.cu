@@ -231,10 +231,11 @@ template <int D, int NR>
 cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
   using L = F32Layout<D, NR>;
   const size_t smem = sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * ((size_t)p.a.B + 1);
-  static_assert(sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * (kMaxSeqs + 1) <= 232448 - 16384,
-                "shared memory, less the static part");
-  const cudaError_t e =
-      cudaFuncSetAttribute(decode_f32_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // One limit for every call (launch in fox_decode_mma.cu has the reason).
+  constexpr size_t kLimit = sizeof(float) * kF32Warps * L::kWarpFloats + sizeof(SeqEntry) * (kMaxSeqs + 1);
+  static_assert(kLimit <= 232448 - 16384, "shared memory, less the static part");
+  const cudaError_t e = cudaFuncSetAttribute(decode_f32_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kLimit));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode", s);
   const cudaError_t f = launch_dependent(decode_f32_kernel<D, NR>, dim3(f32_ctas(D)), dim3(32 * kF32Warps), smem, s, p);

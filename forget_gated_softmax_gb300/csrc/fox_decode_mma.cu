@@ -504,11 +504,13 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
   const size_t fixed = 1024 + (size_t)L::kWarps * L::kQBytes + sizeof(SeqEntry) * ((size_t)p.a.B + 1);
   const size_t one = (size_t)L::kWarps * (2 * L::kTileBytes + x.gstage);
   const size_t smem = fixed + L::kStages * one;
-  static_assert(1024 + sizeof(SeqEntry) * (kMaxSeqs + 1) +
-                        L::kWarps * (L::kQBytes + L::kStages * (2 * L::kTileBytes + kMostGates)) <= kMost,
-                "shared memory");
+  // The limit is the function's, not the call's: always the same value, the most that any call takes, so that host
+  // threads with different batches do not lower it between each other's calls here and launches.
+  constexpr size_t kLimit = 1024 + sizeof(SeqEntry) * (kMaxSeqs + 1) +
+                            L::kWarps * (L::kQBytes + L::kStages * (2 * L::kTileBytes + kMostGates));
+  static_assert(kLimit <= kMost, "shared memory");
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLimit));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode", s);
   const cudaError_t f =

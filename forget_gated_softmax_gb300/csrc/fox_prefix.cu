@@ -535,11 +535,15 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
   using L = PrefixLayout<D>;
   auto kernel = prefix_kernel<D, kSplit>;
   // At least 116 KB, so that one CTA, which takes all of tensor memory, is ever resident on an SM.
+  constexpr size_t kLeast = 118784;
   size_t smem = 1024 + L::kKap + sizeof(float) * 2 * p.pre.kap_tiles * p.pre.hp * kKapPitch;
-  static_assert(1024 + PrefixLayout<128>::kKap + 4 * 2 * 2 * kMaxHp * kKapPitch <= 232448 - 512, "shared memory");
-  if (smem < 118784) smem = 118784;
+  if (smem < kLeast) smem = kLeast;
+  // One limit for every call (launch in fox_decode_mma.cu has the reason).
+  constexpr size_t kMost = 1024 + L::kKap + sizeof(float) * 2 * 2 * kMaxHp * kKapPitch;
+  constexpr size_t kLimit = kMost < kLeast ? kLeast : kMost;
+  static_assert(kLimit <= 232448 - 512, "shared memory");
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLimit));
   if (e != cudaSuccess) return e;
   TraceScope trace("prefix", s);
   const cudaError_t f =
