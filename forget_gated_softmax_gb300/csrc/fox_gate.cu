@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(256) gate_tile_scan_kernel(const float* __rest
 //   warps 2-5 epilogue (thread = token = TMEM lane), then one head per warp in the scan
 constexpr int kProjThreads = 192;
 constexpr int kProjStages = 4;
+constexpr int kProjMaxHeads = 256;  // of one call (its columns of tensor memory)
 
 struct ProjParams {
   int B, N, H, Hpad, hidden, nT, Npad, bias_from_j;
@@ -404,7 +405,10 @@ cudaError_t launch_gate_proj_scan(const CUtensorMap* maps /* x, W */, const floa
   p.tiletot = reinterpret_cast<float*>(base + g.tiletot);
   p.err = err;
   const size_t smem = gate_proj_smem_bytes(H);
-  e = cudaFuncSetAttribute(gate_proj_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit is the function's, not the call's: always the most that any call takes, so that host threads with
+  // different head counts do not lower it between each other's calls here and launches.
+  e = cudaFuncSetAttribute(gate_proj_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)gate_proj_smem_bytes(kProjMaxHeads));
   if (e != cudaSuccess) return e;
   {
     TraceScope trace("gate_proj_scan", s);
