@@ -240,6 +240,11 @@ cudaError_t launch_tile_span(const void* q, const void* k, int B, int N, int H, 
 cudaError_t launch_window(const float* z, int B, int N, int H, double eps, int* out, void* ws, cudaStream_t s);
 size_t window_workspace_bytes(int B, int N, int H);
 
+// Host helper behind those below: a tiled tensor map without interleaving, zeros beyond its edges, any element step
+// 1. Makes the current device's context current where the calling thread has none. False when the driver entry point
+// is unavailable or encoding fails.
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, const void* base, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
 // Host helper: 4-D bf16 tensor map over [B, N, H, d] with a box of 64 channels x 1 head x
 // box_rows tokens x 1 batch and 128-byte swizzle. Returns false when the driver entry point is
 // unavailable or encoding fails.
