@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kGateHeads = 32;  // heads of one gate block
-constexpr int kFewTokens = 8;   // up to so many a gate block sums token after token, not by scans (one token of
+constexpr int kFewTokens = 8;   // up to so many of a sequence are summed token after token, not by scans (one token of
                                 // 128 sequences: 8.9 us, by scans 13.3; 8 of 32: 9.3 and 10.5; 16 of 32: 11.5 and 10.9)
 
 struct AppendParams {
@@ -220,8 +220,8 @@ __device__ __forceinline__ void stage_gates(const AppendParams& p, int row0, int
   }
 }
 
-// Inclusive sums of zs[0 .. m)[h] on top of `before`, four tokens a lane. The same sums, in the
-// same order, whoever forms them.
+// Inclusive sums of zs[0 .. m)[h] on top of `before`, four tokens a lane: token t's in lane t / 4, incl[t % 4]. The
+// same sums, in the same order, whoever forms them (further lanes' are of another order, also where they add zeros).
 __device__ __forceinline__ void scan_column(const float (*zs)[kGateHeads + 1], int m, int h, int lane, float before,
                                             float* incl) {
   float run = 0.f;
@@ -299,8 +299,9 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
   const bool redo = chunk > 0 && !p.scan_bases, opens = slot0 == 0 && (chunk == 0 || redo);
   const int m1 = redo ? lo - first : 0, slot1 = first & (S - 1);
   bool no_page = false;
-  if (m + m1 <= kFewTokens) {
-    // Steps of generation: a lane a head, token after token.
+  if (s.n <= kFewTokens) {
+    // Steps of generation: a lane a head, token after token. By the sequence's count, not the block's, so that a page's
+    // sum is the same where the next page's block forms it once more.
     if (warp > 0 || lane >= nh) return;
     const int h = h0 + lane;
     const float* z = p.z + (size_t)s.row0 * p.z_stride + h;
@@ -331,7 +332,8 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
       if (redo) {
         float incl[4];
         scan_column(zs, m1, hl, lane, slot1 > 0 ? a.g[g_offset(a, page_before, h, slot1 - 1)] : 0.f, incl);
-        c += __shfl_sync(0xffffffffu, incl[3], 31);  // the sum over the whole page, whatever m1 is
+        const int t = (m1 - 1) & 3;  // of the page's last token, as its block writes it
+        c += __shfl_sync(0xffffffffu, t < 2 ? (t ? incl[1] : incl[0]) : t < 3 ? incl[2] : incl[3], (m1 - 1) >> 2);
       }
       if (lane == 0) put_base(a.gbase, gbase_offset(a, page, h), c);
     }
