@@ -60,6 +60,7 @@ EXPORTS = (
     "fox_gate_bwd_workspace_bytes",
     "fox_cache_workspace_bytes",
     "fox_cache_append",
+    "fox_cache_append_low",
     "fox_decode",
 )
 
@@ -193,13 +194,15 @@ def lib() -> ctypes.CDLL:
         L.fox_cache_workspace_bytes.restype = sz
         L.fox_cache_append.argtypes = [pc, pb, i, vp, i64, vp, i64, vp, i64, ctypes.POINTER(fox_rotary), vp, sz, vp]
         L.fox_cache_append.restype = i
+        L.fox_cache_append_low.argtypes = [pc, pb, i, vp, i64, vp, i64, vp, i64, ctypes.POINTER(fox_rotary), vp, vp, sz, vp]
+        L.fox_cache_append_low.restype = i
         L.fox_decode.argtypes = [pc, pb, i, vp, i64, ctypes.c_float, i, vp, vp, vp, sz, vp]
         L.fox_decode.restype = i
         try:
             from . import _foxcall
         except ImportError as e:
             raise RuntimeError("_foxcall.so is not built; run `python -m forget_gated_softmax_gb300.build`") from e
-        _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append, L.fox_decode)))
+        _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append_low, L.fox_decode)))
         _call = _foxcall
         L.fox_trace_begin.argtypes = []
         L.fox_trace_begin.restype = i
@@ -527,7 +530,7 @@ def fox_tile_span(q, k, z, *, scale: float = 0.0, bias_from_j: bool = False, ws=
 class Cache:
     """A paged cache over the caller's tensors (see fox_cache in include/fox.h). Made by make_cache or new_cache."""
 
-    __slots__ = ("k", "v", "g", "gbase", "params", "ref", "addr", "device", "index", "dtype", "H", "Hkv", "d", "page_size")
+    __slots__ = ("k", "v", "g", "gbase", "g_low", "params", "ref", "addr", "device", "index", "dtype", "H", "Hkv", "d", "page_size")
 
 
 class Batch:
@@ -537,9 +540,11 @@ class Batch:
     __slots__ = ("lens", "table", "cu_new", "prefix_table", "params", "ref", "addr", "device", "B")
 
 
-def make_cache(k, v, g, gbase) -> Cache:
+def make_cache(k, v, g, gbase, g_low=None) -> Cache:
     """A handle on a paged cache: k, v [pages, Hkv, page_size, d] (bf16 or fp32), g [pages, H, page_size] fp32,
-    gbase [pages, H, 2] fp32, all contiguous on one CUDA device."""
+    gbase [pages, H, 2] fp32, all contiguous on one CUDA device. g_low, like g, holds what g's rounding leaves of the
+    gates' running sums: without it, tokens appended one at a time lose decay behind a strong gate (see fox_cache in
+    include/fox.h)."""
     torch = _torch()
     pages, Hkv, S, d = k.shape
     H = g.shape[1]
@@ -547,14 +552,19 @@ def make_cache(k, v, g, gbase) -> Cache:
         raise ValueError("make_cache: v must have k's shape and type")
     if tuple(g.shape) != (pages, H, S) or tuple(gbase.shape) != (pages, H, 2):
         raise ValueError("make_cache: g must be [pages, H, page_size] and gbase [pages, H, 2]")
-    if g.dtype != torch.float32 or gbase.dtype != torch.float32:
-        raise TypeError("make_cache: g and gbase must be float32")
-    for t in (k, v, g, gbase):
+    if g_low is not None and g_low.shape != g.shape:
+        raise ValueError("make_cache: g_low must have g's shape")
+    if any(t is not None and t.dtype != torch.float32 for t in (g, gbase, g_low)):
+        raise TypeError("make_cache: g, gbase and g_low must be float32")
+    for t in (k, v, g, gbase, g_low):
+        if t is None:
+            continue
         if not t.is_contiguous():
             raise ValueError("make_cache needs contiguous tensors")
         if not t.is_cuda or t.device != k.device:
             raise ValueError("make_cache needs tensors on one CUDA device")
     c = Cache()
+    c.g_low = g_low
     c.k, c.v, c.g, c.gbase, c.device, c.index, c.dtype = k, v, g, gbase, k.device, k.device.index, k.dtype
     c.H, c.Hkv, c.d, c.page_size = H, Hkv, d, S
     c.params = fox_cache(pages, S, H, Hkv, d, _dtype_code(k), _ptr(k), _ptr(v), _ptr(g), _ptr(gbase))
@@ -563,12 +573,12 @@ def make_cache(k, v, g, gbase) -> Cache:
 
 
 def new_cache(pages: int, page_size: int, H: int, Hkv: int, d: int, *, dtype=None, device="cuda") -> Cache:
-    """make_cache over newly allocated (uninitialised) tensors; dtype defaults to bfloat16."""
+    """make_cache over newly allocated (uninitialised) tensors, g_low among them; dtype defaults to bfloat16."""
     torch = _torch()
     dtype = torch.bfloat16 if dtype is None else dtype
     k, v = (torch.empty((pages, Hkv, page_size, d), dtype=dtype, device=device) for _ in range(2))
-    g = torch.empty((pages, H, page_size), dtype=torch.float32, device=device)
-    return make_cache(k, v, g, torch.empty((pages, H, 2), dtype=torch.float32, device=device))
+    g, g_low = (torch.empty((pages, H, page_size), dtype=torch.float32, device=device) for _ in range(2))
+    return make_cache(k, v, g, torch.empty((pages, H, 2), dtype=torch.float32, device=device), g_low)
 
 
 def make_batch(lens, table, *, cu_new=None, max_new: Optional[int] = None, prefix_table=None,
@@ -719,6 +729,8 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
             raise ValueError(f"{where}: q_out without q")
         rot = (cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if pairs else 0,
                0 if q is None else q.data_ptr(), qs, 0 if q is None else q_out.data_ptr())
+    if cache.g_low is not None:
+        rot = (*rot, cache.g_low.data_ptr())
     if ws is None:
         ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
     st = (_call or _load_call()).append(

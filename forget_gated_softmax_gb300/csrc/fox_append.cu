@@ -12,11 +12,14 @@
 //
 // Gates: with a_t = log sigmoid(z_t), g of a token is the sum of a from its page's first token on
 // (fp32) and gbase of a page the sum before it (fp64 arithmetic, kept as two fp32). A page's sums
-// are a warp scan that goes on from the page's last held value; a page that opens in this call
-// takes its base from the page before.
+// go on from the page's last held value, token after token in two fp32 or, of many tokens, by a warp scan in
+// fp32 on top of it; a page that opens in this call takes its base from the page before. A sum that
+// goes on from g alone goes on from a rounded value: token by token, a_t below half a step of g are then
+// lost one after the other. g_low holds what g leaves of the sum, so that every g is rounded once.
 //
 // Bound by memory: each of k, v (q) read once and written once. 6 prompts of up to 16384 tokens (1.44 GB) take
-// 262 us, 5.5 TB/s; one token of 128 sequences 9 us, the launch and a few dependent trips to memory.
+// 258 us, 5.6 TB/s (262 with g_low); one token of 128 sequences 4.0 us of GPU time among others in a graph, the launch and a
+// few dependent trips to memory (with and without g_low).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,6 +45,7 @@ struct AppendParams {
   const float* cos;
   const float* sin;
   int max_pos, rot, pairs;
+  float* g_low;
   int gate_blocks;                  // blocks [0, gate_blocks) sum gates, the others copy
   int page_chunks, head_groups;     // gate block: (sequence, page chunk, head group)
   int scan_bases;                   // bases of pages after a sequence's first are left to base_scan_kernel
@@ -220,10 +224,9 @@ __device__ __forceinline__ void stage_gates(const AppendParams& p, int row0, int
   }
 }
 
-// Inclusive sums of zs[0 .. m)[h] on top of `before`, four tokens a lane: token t's in lane t / 4, incl[t % 4]. The
-// same sums, in the same order, whoever forms them (further lanes' are of another order, also where they add zeros).
-__device__ __forceinline__ void scan_column(const float (*zs)[kGateHeads + 1], int m, int h, int lane, float before,
-                                            float* incl) {
+// Inclusive sums of zs[0 .. m)[h], four tokens a lane: token t's in lane t / 4, incl[t % 4]. The same sums, in the
+// same order, whoever forms them (further lanes' are of another order, also where they add zeros).
+__device__ __forceinline__ void scan_column(const float (*zs)[kGateHeads + 1], int m, int h, int lane, float* incl) {
   float run = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -237,9 +240,34 @@ __device__ __forceinline__ void scan_column(const float (*zs)[kGateHeads + 1], i
     const float y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  const float shift = before + (x - run);
+  const float shift = x - run;
 #pragma unroll
   for (int e = 0; e < 4; ++e) incl[e] += shift;
+}
+
+// A page's running sum in two fp32, |lo| at most half a step of hi.
+struct Sum2 {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum2 add(Sum2 x, float a) {
+  const float s = __fadd_rn(x.hi, a), t = __fsub_rn(s, x.hi);
+  const float e = __fadd_rn(__fsub_rn(x.hi, __fsub_rn(s, t)), __fsub_rn(a, t)) + x.lo;  // x.hi + a = s + rounding error
+  const float hi = __fadd_rn(s, e);
+  return {hi, __fsub_rn(e, __fsub_rn(hi, s))};
+}
+// What a page's slot holds: g and, where it is kept, what g leaves of the sum. That is at most half a step of g;
+// anything else there (of a page's earlier use, or never written) is no such thing and counts as 0.
+__device__ __forceinline__ Sum2 held_sum(const AppendParams& p, size_t at) {
+  const float g = p.a.g[at], low = p.g_low ? p.g_low[at] : 0.f;
+  return {g, fabsf(low) <= fabsf(g) * 0x1p-24f ? low : 0.f};
+}
+// The value of a sum that goes to a slot, as the slot will hold it.
+__device__ __forceinline__ double as_held(const AppendParams& p, Sum2 x) {
+  return p.g_low ? static_cast<double>(x.hi) + x.lo : static_cast<double>(x.hi);
+}
+__device__ __forceinline__ void put_sum(const AppendParams& p, size_t at, Sum2 x) {
+  p.a.g[at] = x.hi;
+  if (p.g_low) p.g_low[at] = x.lo;
 }
 
 __device__ __forceinline__ void put_base(float* gbase, size_t at, double c) {
@@ -253,7 +281,8 @@ __device__ __forceinline__ double base_of(const PagedArgs& a, int page, int h) {
 }
 
 // c of the last token before own token `own`, head h: 0 where there is none.
-__device__ __forceinline__ double gate_before(const PagedArgs& a, int b, int own, int h, bool* bad) {
+__device__ __forceinline__ double gate_before(const AppendParams& p, int b, int own, int h, bool* bad) {
+  const PagedArgs& a = p.a;
   const int before = a.prefix_len + own - 1;
   if (before < 0) return 0.0;
   const int page = own > 0 ? own_page(a, b, own - 1) : prefix_page(a, before);
@@ -262,7 +291,7 @@ __device__ __forceinline__ double gate_before(const PagedArgs& a, int b, int own
     return 0.0;
   }
   const int slot = (own > 0 ? own - 1 : before) & (a.page_size - 1);
-  return base_of(a, page, h) + a.g[g_offset(a, page, h, slot)];
+  return base_of(a, page, h) + as_held(p, held_sum(p, g_offset(a, page, h, slot)));
 }
 
 // Gates of the new tokens of one sequence that fall into one page.
@@ -305,18 +334,23 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
     if (warp > 0 || lane >= nh) return;
     const int h = h0 + lane;
     const float* z = p.z + (size_t)s.row0 * p.z_stride + h;
-    float run = slot0 > 0 ? a.g[g_offset(a, page, h, slot0 - 1)] : 0.f;
+    Sum2 run = {0.f, 0.f};
+    if (slot0 > 0) run = held_sum(p, g_offset(a, page, h, slot0 - 1));
     if (opens) {
-      double c = redo && slot1 > 0 ? base_of(a, page_before, h) : gate_before(a, b, first, h, &no_page);
-      float before = redo && slot1 > 0 ? a.g[g_offset(a, page_before, h, slot1 - 1)] : 0.f;
+      double c = redo && slot1 > 0 ? base_of(a, page_before, h) : gate_before(p, b, first, h, &no_page);
+      Sum2 before = {0.f, 0.f};
+      if (redo && slot1 > 0) before = held_sum(p, g_offset(a, page_before, h, slot1 - 1));
 #pragma unroll 1
-      for (int t = 0; t < m1; ++t) before += log_sigmoid(z[(size_t)t * p.z_stride]);
-      put_base(a.gbase, gbase_offset(a, page, h), c + before);
+      for (int t = 0; t < m1; ++t) before = add(before, log_sigmoid(z[(size_t)t * p.z_stride]));
+      put_base(a.gbase, gbase_offset(a, page, h), c + as_held(p, before));
     }
-    float* dst = a.g + g_offset(a, page, h, slot0);
+    const size_t dst = g_offset(a, page, h, slot0);
     z += (size_t)(lo - first) * p.z_stride;
 #pragma unroll 1
-    for (int t = 0; t < m; ++t) dst[t] = run += log_sigmoid(z[(size_t)t * p.z_stride]);
+    for (int t = 0; t < m; ++t) {
+      run = add(run, log_sigmoid(z[(size_t)t * p.z_stride]));
+      put_sum(p, dst + t, run);
+    }
     if (no_page && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
     return;
   }
@@ -328,12 +362,13 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
 #pragma unroll 2
     for (int hl = warp; hl < nh; hl += kThreads / 32) {
       const int h = h0 + hl;
-      double c = redo && slot1 > 0 ? base_of(a, page_before, h) : gate_before(a, b, first, h, &no_page);
+      double c = redo && slot1 > 0 ? base_of(a, page_before, h) : gate_before(p, b, first, h, &no_page);
       if (redo) {
         float incl[4];
-        scan_column(zs, m1, hl, lane, slot1 > 0 ? a.g[g_offset(a, page_before, h, slot1 - 1)] : 0.f, incl);
+        scan_column(zs, m1, hl, lane, incl);
         const int t = (m1 - 1) & 3;  // of the page's last token, as its block writes it
-        c += __shfl_sync(0xffffffffu, t < 2 ? (t ? incl[1] : incl[0]) : t < 3 ? incl[2] : incl[3], (m1 - 1) >> 2);
+        const float sum = __shfl_sync(0xffffffffu, t < 2 ? (t ? incl[1] : incl[0]) : t < 3 ? incl[2] : incl[3], (m1 - 1) >> 2);
+        c += slot1 > 0 ? as_held(p, add(held_sum(p, g_offset(a, page_before, h, slot1 - 1)), sum)) : sum;
       }
       if (lane == 0) put_base(a.gbase, gbase_offset(a, page, h), c);
     }
@@ -345,11 +380,23 @@ __device__ __forceinline__ void gate_block(const AppendParams& p, float (*zs)[kG
   for (int hl = warp; hl < nh; hl += kThreads / 32) {
     const int h = h0 + hl;
     float incl[4];
-    scan_column(zs, m, hl, lane, slot0 > 0 ? a.g[g_offset(a, page, h, slot0 - 1)] : 0.f, incl);
-    float* dst = a.g + g_offset(a, page, h, slot0);
+    scan_column(zs, m, hl, lane, incl);
+    const size_t dst = g_offset(a, page, h, slot0);
+    if (slot0 == 0) {  // all but a sequence's first page: the scan's sums as they are
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (lane * 4 + e < m) a.g[dst + lane * 4 + e] = incl[e];
+      if (p.g_low) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (lane * 4 + e < m) p.g_low[dst + lane * 4 + e] = 0.f;
+      }
+      continue;
+    }
+    const Sum2 before = held_sum(p, dst - 1);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (lane * 4 + e < m) dst[lane * 4 + e] = incl[e];
+      if (lane * 4 + e < m) put_sum(p, dst + lane * 4 + e, add(before, incl[e]));
   }
   if (no_page && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
 }
@@ -390,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams 
   double carry = 0.0;
   constexpr int kSteps = 4;  // of 32 pages, their loads in flight together
   for (int k = p0 + 1; k <= pl; k += 32 * kSteps) {
-    float full[kSteps];
+    float full[kSteps], low[kSteps];
     int id[kSteps], before[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
@@ -404,10 +451,14 @@ __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams 
       carry = base_of(a, id0, h);
     }
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) full[i] = before[i] >= 0 ? __ldcg(a.g + g_offset(a, before[i], h, S - 1)) : 0.f;
+    for (int i = 0; i < kSteps; ++i) {
+      const size_t at = before[i] >= 0 ? g_offset(a, before[i], h, S - 1) : 0;
+      full[i] = before[i] >= 0 ? __ldcg(a.g + at) : 0.f;
+      low[i] = before[i] >= 0 && p.g_low ? __ldcg(p.g_low + at) : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      double x = full[i];
+      double x = static_cast<double>(full[i]) + low[i];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double y = __shfl_up_sync(0xffffffffu, x, o);
@@ -463,6 +514,7 @@ cudaError_t launch_cache_append(const CacheAppendArgs& x, bool f32, cudaStream_t
   p.max_pos = x.max_pos;
   p.rot = x.rot;
   p.pairs = x.pairs;
+  p.g_low = x.g_low;
   return f32 ? launch<float>(p, s) : launch<__nv_bfloat16>(p, s);
 }
 

@@ -132,6 +132,14 @@ size_t fox_cache_workspace_bytes(const fox_cache* c, const fox_batch* s, int row
 fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
                             void* workspace, size_t workspace_bytes, void* stream) {
+  return fox_cache_append_low(c, s, rows, k, k_stride, v, v_stride, z, z_stride, rot, nullptr, workspace, workspace_bytes,
+                              stream);
+}
+
+fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const float* z, int64_t z_stride,
+                                const fox_rotary* rot, float* g_low, void* workspace, size_t workspace_bytes,
+                                void* stream) {
   fox_status st = check_cache(c);
   if (st != FOX_OK) return st;
   CacheAppendArgs x = {};
@@ -145,6 +153,7 @@ fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, co
   st = check_pointers(c, s);
   if (st != FOX_OK) return st;
   if (!row_ok(k, k_stride, c->Hkv, c, rows) || !row_ok(v, v_stride, c->Hkv, c, rows)) return FOX_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(g_low) & 3u) return FOX_ERR_INVALID_ARG;
   if (!z || (reinterpret_cast<uintptr_t>(z) & 3u) || (rows > 1 && (z_stride < c->H || z_stride >= (1LL << 40))))
     return FOX_ERR_INVALID_ARG;
   if (rot) {
@@ -170,6 +179,7 @@ fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, co
   x.k_stride = k_stride;
   x.v_stride = v_stride;
   x.z_stride = z_stride;
+  x.g_low = g_low;
   return launch_cache_append(x, c->dtype == FOX_DTYPE_F32, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FOX_OK
              : FOX_ERR_CUDA;

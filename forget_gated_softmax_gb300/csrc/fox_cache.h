@@ -26,6 +26,7 @@ struct CacheAppendArgs {
   const float* cos;
   const float* sin;
   int max_pos, rot, pairs;
+  float* g_low;  // what the rounding of g leaves of the sums, laid out like g, or null
 };
 cudaError_t launch_cache_append(const CacheAppendArgs& x, bool f32, cudaStream_t s);
 struct DecodeArgs {

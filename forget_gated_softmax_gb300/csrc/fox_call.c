@@ -1,4 +1,4 @@
-/* The serving calls of libfox.so for Python: fox_cache_append and fox_decode with plain numbers (addresses,
+/* The serving calls of libfox.so for Python: fox_cache_append_low and fox_decode with plain numbers (addresses,
  * sizes, strides), which the binding has checked. A step of generation is some microseconds of GPU time; ctypes
  * takes two of them to convert a dozen arguments, these functions a tenth of that. */
 #define PY_SSIZE_T_CLEAN
@@ -7,7 +7,7 @@
 #include "../../include/fox.h"
 
 typedef fox_status (*append_fn)(const fox_cache*, const fox_batch*, int, const void*, int64_t, const void*, int64_t,
-                                const float*, int64_t, const fox_rotary*, void*, size_t, void*);
+                                const float*, int64_t, const fox_rotary*, float*, void*, size_t, void*);
 typedef fox_status (*decode_fn)(const fox_cache*, const fox_batch*, int, const void*, int64_t, float, int, void*, float*,
                                 void*, size_t, void*);
 static append_fn g_append;
@@ -34,10 +34,12 @@ static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* cache, batch, rows, k, k_stride, v, v_stride, z, z_stride, ws, ws_bytes, stream[, cos, sin, positions, dim, pairs, q,
- * q_stride, q_out] */
+ * q_stride, q_out][, g_low] */
 static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if ((n != 12 && n != 20) || !g_append) return PyErr_Format(PyExc_TypeError, "append takes 12 or 20 numbers, after bind");
+  const Py_ssize_t m = n == 13 || n == 21 ? n - 1 : n;  /* without g_low */
+  if ((m != 12 && m != 20) || !g_append)
+    return PyErr_Format(PyExc_TypeError, "append takes 12 or 20 numbers, and perhaps one more, after bind");
   const fox_cache* c = (const fox_cache*)ptr(a[0]);
   const fox_batch* b = (const fox_batch*)ptr(a[1]);
   const int rows = small(a[2]);
@@ -47,7 +49,8 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   void *ws = ptr(a[9]), *stream = ptr(a[11]);
   const size_t bytes = (size_t)PyLong_AsUnsignedLongLong(a[10]);
   fox_rotary r = {0};
-  if (n == 20) {
+  float* low = m < n ? (float*)ptr(a[m]) : NULL;
+  if (m == 20) {
     r.cos = (const float*)ptr(a[12]);
     r.sin = (const float*)ptr(a[13]);
     r.max_pos = small(a[14]);
@@ -60,7 +63,7 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) return NULL;
   fox_status st;
   Py_BEGIN_ALLOW_THREADS;
-  st = g_append(c, b, rows, k, ks, v, vs, z, zs, n == 20 ? &r : NULL, ws, bytes, stream);
+  st = g_append(c, b, rows, k, ks, v, vs, z, zs, m == 20 ? &r : NULL, low, ws, bytes, stream);
   Py_END_ALLOW_THREADS;
   return PyLong_FromLong((long)st);
 }
@@ -86,8 +89,8 @@ static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 static PyMethodDef methods[] = {
-    {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind(fox_cache_append, fox_decode): their addresses"},
-    {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "fox_cache_append; returns its status"},
+    {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind(fox_cache_append_low, fox_decode): their addresses"},
+    {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "fox_cache_append_low; returns its status"},
     {"decode", (PyCFunction)(void (*)(void))decode, METH_FASTCALL, "fox_decode; returns its status"},
     {NULL, NULL, 0, NULL},
 };

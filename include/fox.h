@@ -251,6 +251,12 @@ fox_status fox_tile_span(const fox_params* p, const void* q, const void* k, cons
  * H query heads share Hkv key heads: query head h reads key head h / (H / Hkv). The gate has one
  * logit a query head, as everywhere in this library.
  * Nothing has to be initialised: a page's slots are read only once tokens were appended to them.
+ * Precision of c_i - c_j: each of the two g is the nearest fp32 of its sum, so off by 2^-24 |g|, where the sum was
+ * formed by one call of at most 8 tokens a sequence, or with g_low (fox_cache_append_low); by 11 times that where one
+ * call brought more tokens. A call that goes on in a page that holds tokens adds to the rounded g: without g_low each
+ * such call adds one rounding, 2^-24 |g| for the largest |g| of the page, to the difference of all tokens before it and all
+ * after. That matters for tokens appended one at a time behind a strong gate in their page: over n of them c_i - c_j
+ * may be off by n 2^-24 |g|, 1e-3 for 127 tokens behind z = -132, 0.08 behind z = -1e4 (with g_low by 0.0012).
  */
 typedef struct fox_cache {
   int num_pages; /* >= 1 */
@@ -325,6 +331,17 @@ typedef struct fox_rotary {
 fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fox_cache_append with the gates' running sums in two parts: g_low [num_pages, H, page_size] fp32 holds what the
+ * rounding of g leaves of each sum, so that tokens appended one at a time add to the sum and not to its rounded value.
+ * Needs no initialisation, and every append to the cache should be given it: a slot whose g_low is not its g's (more
+ * than half a step of g) counts as 0 there. fox_decode does not read it. NULL: as fox_cache_append.
+ */
+fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const float* z, int64_t z_stride,
+                                const fox_rotary* rot, float* g_low, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /*
  * Attention of the new tokens over the cache (their own K, V and gates appended before): row i of
