@@ -148,7 +148,7 @@ cudaError_t launch_merge(const DecodeParams& p, cudaStream_t s) {
 }
 
 struct DecodeLayout {
-  int Rt, Gp, Rs, RTmax, workers;
+  int Rt, Gp, Rs, RTmax, workers, warps;  // warps: workers of a CTA
   size_t cum, ml, po, pml, ppo, end;
   PrefixPlan pre;
   long long po_rows;
@@ -170,7 +170,8 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   const int most = a.max_new * L.Gp;
   L.Rs = most < L.Rt ? most : L.Rt;
   L.RTmax = ceil_div(most, L.Rt);
-  L.workers = f32 ? f32_ctas(a.d) * kF32Warps : kSMs * decode_mma_warps(a.d);
+  L.warps = f32 ? kF32Warps : decode_mma_warps(a.d);
+  L.workers = (f32 ? f32_ctas(a.d) : kSMs) * L.warps;
   const size_t slots = (size_t)L.workers + (size_t)a.B * a.Hkv * L.RTmax;
   L.cum = kCacheHeaderBytes;
   L.po_rows = (long long)slots * L.Rs;
@@ -192,7 +193,7 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
 
 bool decode_fits(const PagedArgs& a, bool f32) {
   const DecodeLayout L = decode_layout(a, f32);
-  return most_units(a, L.Rt, L.Gp) < 0x7fffffffLL - L.workers &&
+  return line_fits(most_units(a, L.Rt, L.Gp), L.workers, L.warps) &&
          (unsigned long long)a.max_new * L.Gp * L.Gp < (1ull << 32) && L.po_rows < 0x7fffffffLL &&
          (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.line < 0x7fffffffLL - L.pre.each);
 }
@@ -216,7 +217,7 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.Gp = L.Gp;
   p.gp_inv = L.Gp > 1 ? static_cast<uint32_t>(((1ull << 32) + L.Gp - 1) / L.Gp) : 0u;
   p.workers = L.workers;
-  p.warps = f32 ? kF32Warps : decode_mma_warps(x.a.d);
+  p.warps = L.warps;
   p.cum = reinterpret_cast<int*>(ws + L.cum);
   p.count = reinterpret_cast<uint32_t*>(ws + kErrWordBytes);
   p.ml = reinterpret_cast<float2*>(ws + L.ml);

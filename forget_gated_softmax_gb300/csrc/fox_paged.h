@@ -119,12 +119,17 @@ FOX_HD int padded_group(int G, int Rt) { return G <= Rt ? G : ceil_div(G, Rt) * 
 FOX_HD int seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, int Gp, bool walk_prefix) {
   return walk_tiles(a, s.own, walk_prefix) * ceil_div(s.n * Gp, Rt);
 }
-// The most units that the batch's tables and row counts allow: has to stay below 2^31 - workers, so
-// that places on the line are ints.
+// The most units that the batch's tables and row counts allow.
 FOX_HD long long most_units(const PagedArgs& a, int Rt, int Gp) {
   const long long cap = (long long)a.prefix_len + (long long)a.table_stride * a.page_size;
   const long long rows = (long long)a.max_new * Gp;
   return (cap / kKeyTile + 2) * ((rows + Rt - 1) / Rt) * a.B * a.Hkv;
+}
+// Whether every place on a line of at most `most` units that the kernels form is an int: the ends of ranges before they
+// are cut off at the line's end, which lie up to a CTA's units (`warps` workers), or a worker's more, behind it.
+FOX_HD bool line_fits(long long most, int workers, int warps) {
+  const long long each = (most + workers - 1) / workers;
+  return most <= 0x7fffffffLL && most + workers + (warps + 1) * each <= 0x7fffffffLL;
 }
 FOX_HD int units_per_worker(int total, int workers) {
   const int q = (total + workers - 1) / workers;
