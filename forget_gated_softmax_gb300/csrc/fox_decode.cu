@@ -42,14 +42,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
   const int v0 = item * x.line / x.each, v1 = (item * x.line + x.key_tiles - 1) / x.each;
   const int n_pre = (v1 - v0 + 1) * (both ? 2 : 1), step = both ? kTile : 2 * kTile;
   const size_t pre0 = ((size_t)(v0 + item) * 2 + (both ? 0 : tile & 1)) * kTile + hl % x.hp * x.tpt + row % x.tpt;
+  const int item0 = first_item(p.num, b, s.row0);
   grid_dep_wait();
   const int tiles = ceil_div(s.own, kKeyTile), r = (row - s.row0) * p.Gp + hl, rt = r / p.Rt;
   const int per_head = __ldcg(p.cum + a.B), each = units_per_worker(per_head * a.Hkv, p.workers);
-  const int i0 = hkv * per_head + __ldcg(p.cum + b) + rt * tiles;
+  const int u0 = __ldcg(p.cum + b);
+  if (p.num.by_rows() && u0 == __ldcg(p.cum + b + 1)) return;  // left out there (scan_sequences): nothing was written for it
+  const int i0 = hkv * per_head + u0 + rt * tiles;
   // The own item's: one a block of workers, and its last worker's own where that is another (join_items).
   const int i1 = i0 + tiles - 1, w0 = i0 / each, w1 = i1 / each, c0 = w0 / p.warps, c1 = w1 / p.warps, nb = c1 - c0 + 1;
   const int n_own = nb + (w1 > w0 && w1 > c1 * p.warps && min(per_head * a.Hkv, (w1 + 1) * each) > i1 + 1);
-  const int n = n_own + n_pre, own0 = ((hkv * a.B + b) * p.RTmax + rt) * p.Rs + r - rt * p.Rt;
+  const int n = n_own + n_pre, own0 = (hkv * p.num.items + item0 + rt) * p.Rs + r - rt * p.Rt;
   float m = -INFINITY, l = 0.f, acc[E] = {};
 #pragma unroll 1
   for (int first = 0; first < n; first += 32 * deal) {
@@ -148,7 +151,9 @@ cudaError_t launch_merge(const DecodeParams& p, cudaStream_t s) {
 }
 
 struct DecodeLayout {
-  int Rt, Gp, Rs, RTmax, workers, warps;  // warps: workers of a CTA
+  int Rt, Gp, Rs, workers, warps;  // warps: workers of a CTA
+  Numbering num;
+  long long items;  // of a key head
   size_t cum, ml, po, pml, ppo, end;
   PrefixPlan pre;
   long long po_rows;
@@ -169,10 +174,11 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   L.Gp = padded_group(G, L.Rt);
   const int most = a.max_new * L.Gp;
   L.Rs = most < L.Rt ? most : L.Rt;
-  L.RTmax = ceil_div(most, L.Rt);
+  const int row_tiles = ceil_div(most, L.Rt);  // of a sequence
+  L.num = numbering(a, L.Gp, L.Rt == 1 ? 0 : L.Rt == 4 ? 2 : L.Rt == 8 ? 3 : 4, row_tiles, &L.items);
   L.warps = f32 ? kF32Warps : decode_mma_warps(a.d);
   L.workers = (f32 ? f32_ctas(a.d) : kSMs) * L.warps;
-  const size_t slots = (size_t)L.workers + (size_t)a.B * a.Hkv * L.RTmax;
+  const size_t slots = (size_t)L.workers + (size_t)a.Hkv * L.items;
   L.cum = kCacheHeaderBytes;
   L.po_rows = (long long)slots * L.Rs;
   L.ml = align_up(L.cum + sizeof(int) * ((size_t)a.B + 1), 256);
@@ -180,7 +186,7 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   L.pml = align_up(L.po + sizeof(float) * slots * L.Rs * a.d, 256);
   L.ppo = L.end = L.pml;
   L.pre = PrefixPlan{};
-  if (!f32 && a.prefix_len > 0 && share_prefix(a, L.RTmax)) {
+  if (!f32 && a.prefix_len > 0 && share_prefix(a, row_tiles)) {
     L.pre = prefix_plan(a);
     const size_t rows = ((size_t)L.pre.workers + (size_t)a.Hkv * L.pre.items) * 2 * kTile;
     L.ppo = align_up(L.pml + sizeof(float2) * rows, 256);
@@ -193,7 +199,7 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
 
 bool decode_fits(const PagedArgs& a, bool f32) {
   const DecodeLayout L = decode_layout(a, f32);
-  return line_fits(most_units(a, L.Rt, L.Gp), L.workers, L.warps) &&
+  return line_fits(most_units(a, L.items), L.workers, L.warps) &&
          (unsigned long long)a.max_new * L.Gp * L.Gp < (1ull << 32) && L.po_rows < 0x7fffffffLL &&
          (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.line < 0x7fffffffLL - L.pre.each);
 }
@@ -213,7 +219,7 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.lse = x.lse;
   p.Rt = L.Rt;
   p.Rs = L.Rs;
-  p.RTmax = L.RTmax;
+  p.num = L.num;
   p.Gp = L.Gp;
   p.gp_inv = L.Gp > 1 ? static_cast<uint32_t>(((1ull << 32) + L.Gp - 1) / L.Gp) : 0u;
   p.workers = L.workers;

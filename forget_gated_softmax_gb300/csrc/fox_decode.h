@@ -33,7 +33,8 @@ struct DecodeParams {
   void* o;
   float* lse;
   // Own items
-  int Rt, Rs, RTmax;   // rows of a row tile; rows kept of a slot; most row tiles of a sequence
+  int Rt, Rs;          // rows of a row tile; rows kept of a slot
+  Numbering num;       // of the items
   int Gp;              // rows of a token (padded_group)
   uint32_t gp_inv;     // ceil(2^32 / Gp), for token_of; 0: Gp is 1
   int workers, warps;  // workers, and of one CTA
@@ -61,17 +62,52 @@ struct Seq {
   int u0, row0, n, own;
 };
 
-// Fills seqs[0 .. B] by the whole block; `scratch` holds one value a warp. Ends with a block barrier.
+// The end of the rows of all sequences before b0, which are those that the threads before this one have. Apart from the
+// code that most calls run.
+static __device__ __noinline__ int rows_before(const DecodeParams& p, int b0, int b1, int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int end = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    bool bad;
+    const SeqInfo s = seq_info(p.a, b, &bad);  // without rows where bad
+    end = max(end, s.row0 + s.n);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end = max(end, y);
+  }
+  if (lane == 31) scratch[warp] = end;
+  end = __shfl_up_sync(0xffffffffu, end, 1);
+  if (lane == 0) end = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int w = 0; w < warp; ++w) end = max(end, scratch[w]);
+  __syncthreads();
+  return end;
+}
+
+// Fills seqs[0 .. B] by the whole block; `scratch` holds one value a warp. Ends with a block barrier. Where items are
+// numbered by rows, a sequence whose rows begin before the end of an earlier one's is left out.
 __device__ __forceinline__ void scan_sequences(const DecodeParams& p, SeqEntry* seqs, int* scratch) {
   const PagedArgs& a = p.a;
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = ceil_div(a.B, nt), b0 = tid * each, b1 = min(a.B, b0 + each);
-  int mine = 0;
+  int mine = 0, rows_end = 0;
   bool any_bad = false;
+  if (p.num.by_rows()) rows_end = rows_before(p, b0, b1, scratch);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     bool bad;
-    const SeqInfo s = seq_info(a, b, &bad);
+    SeqInfo s = seq_info(a, b, &bad);
+    if (p.num.by_rows() && !bad) {
+      if (s.row0 < rows_end) {
+        bad = true;
+        s = {0, 0, -1};
+      }
+      rows_end = max(rows_end, s.row0 + s.n);
+    }
     any_bad |= bad;
     seqs[b] = {mine, first_row(a, b), bad ? kBadSeq : s.own};
     mine += seq_units(a, s, p.Rt, p.Gp, p.walk_prefix);
@@ -242,7 +278,7 @@ __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16* dst, float4 v
 
 // Slot of a worker's partial result of an item, in rows of ml and po.
 __device__ __forceinline__ int slot_of(const DecodeParams& p, int worker, const Place& at) {
-  return (worker + (at.hkv * p.a.B + at.b) * p.RTmax + at.rt) * p.Rs;
+  return (worker + at.hkv * p.num.items + first_item(p.num, at.b, at.s.row0) + at.rt) * p.Rs;
 }
 // Rows that a row tile has.
 __device__ __forceinline__ int rows_of(const DecodeParams& p, const Place& at) {

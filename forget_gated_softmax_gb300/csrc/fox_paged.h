@@ -106,6 +106,11 @@ FOX_HD size_t gbase_offset(const PagedArgs& a, int page, int h) { return ((size_
 // An item that lies in one worker's range is finished there; of the others a worker can leave a partial
 // result, in slot worker + item: along the line each new (worker, item) pair raises one of the
 // two, so no two pairs meet, and there are fewer than workers + items slots.
+// Items of a key head are numbered so that the number follows from the sequence alone: by the most row tiles of any
+// sequence, or, where sequences bring very different counts, by the rows before it: with x = Gp / Rt
+// row tiles a row, sequence b has the numbers from floor(row0 x) + b on, ceil(n x) of them, which the next one's
+// floor((row0 + n) x) + b + 1 is not below. (64 sequences on 32 / 8 heads of 128 channels, one of them with 16384 new
+// tokens: 0.28 GB of partial results; by sequence 17.4 GB.) That takes row ranges that rise from sequence to sequence.
 constexpr int kKeyTile = 32;
 
 FOX_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -116,14 +121,27 @@ FOX_HD int walk_tiles(const PagedArgs& a, int own, bool walk_prefix) {
   return own < 0 ? 0 : (walk_prefix ? ceil_div(a.prefix_len, kKeyTile) : 0) + ceil_div(own, kKeyTile);
 }
 FOX_HD int padded_group(int G, int Rt) { return G <= Rt ? G : ceil_div(G, Rt) * Rt; }
+struct Numbering {
+  int items;                   // numbers of a key head
+  int per_seq, per_row, shift; // of a sequence's first item: b per_seq + (row0 per_row >> shift)
+  FOX_HD bool by_rows() const { return per_row > 0; }
+};
+FOX_HD int first_item(const Numbering& x, int b, int row0) { return b * x.per_seq + (row0 * x.per_row >> x.shift); }
+// The one of the two that takes fewer numbers; `rt_shift`: Rt = 1 << rt_shift, `row_tiles`: the most of a sequence.
+// `items` gets the count also where it is no int.
+inline Numbering numbering(const PagedArgs& a, int Gp, int rt_shift, int row_tiles, long long* items) {
+  const long long by_rows = ((long long)a.rows * Gp >> rt_shift) + a.B, by_seq = (long long)a.B * row_tiles;
+  *items = by_rows < by_seq ? by_rows : by_seq;
+  if (by_rows < by_seq) return {static_cast<int>(by_rows), 1, Gp, rt_shift};
+  return {static_cast<int>(by_seq), row_tiles, 0, 0};
+}
 FOX_HD int seq_units(const PagedArgs& a, const SeqInfo& s, int Rt, int Gp, bool walk_prefix) {
   return walk_tiles(a, s.own, walk_prefix) * ceil_div(s.n * Gp, Rt);
 }
-// The most units that the batch's tables and row counts allow.
-FOX_HD long long most_units(const PagedArgs& a, int Rt, int Gp) {
+// The most units that the batch's tables allow for so many items a key head.
+FOX_HD long long most_units(const PagedArgs& a, long long items) {
   const long long cap = (long long)a.prefix_len + (long long)a.table_stride * a.page_size;
-  const long long rows = (long long)a.max_new * Gp;
-  return (cap / kKeyTile + 2) * ((rows + Rt - 1) / Rt) * a.B * a.Hkv;
+  return (cap / kKeyTile + 2) * items * a.Hkv;
 }
 // Whether every place on a line of at most `most` units that the kernels form is an int: the ends of ranges before they
 // are cut off at the line's end, which lie up to a CTA's units (`warps` workers), or a worker's more, behind it.

@@ -297,12 +297,14 @@ typedef struct fox_batch {
 /*
  * Workspace of fox_cache_append and fox_decode for these arguments (0 if they are invalid): the
  * error word, and for fox_decode counters and the partial results of keys split among the SMs. It
- * depends on sizes only, never on the contents of lens. Its first FOX_CACHE_ZERO_BYTES must be zero
+ * depends on sizes only, never on the contents of lens: some rows * H * d * 4 bytes, more where sequences bring few.
+ * fox_cache_append uses its first 256 bytes alone, and takes no more. Its first FOX_CACHE_ZERO_BYTES must be zero
  * before its first call with these two functions (any other use in between, a call of fox_fwd for
  * instance, makes it a new one); they leave the counters zero, and only ever add bits to the error word, the
  * first 4 bytes, which fox_check_error reads and clears: a length, row range, page id or position
  * outside what the arguments allow sets one. The sequence, or the token, is then skipped, or an
- * unknown page read as page 0; its outputs are not meaningful, and no other sequence is touched.
+ * unknown page read as page 0; its outputs are not meaningful, and no other sequence is touched (rows that two
+ * sequences claim, by a cu_new that falls, are neither's).
  * Calls that may run at the same time (other streams, captured graphs) need workspaces of their own.
  * After a call whose device wait gave up (FOX_ERR_TIMEOUT) the header has to be made zero again.
  */
