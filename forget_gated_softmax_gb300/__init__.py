@@ -132,7 +132,7 @@ class fox_trace_record(ctypes.Structure):
 
 
 _lib = None
-_call = None  # fox_cache_append and fox_decode by way of _foxcall.so (csrc/fox_call.c)
+_call = None  # fox_cache_append_low and fox_decode by way of _foxcall.so (csrc/fox_call.c), or of ctypes without it
 
 
 def lib() -> ctypes.CDLL:
@@ -200,16 +200,32 @@ def lib() -> ctypes.CDLL:
         L.fox_decode.restype = i
         try:
             from . import _foxcall
-        except ImportError as e:
-            raise RuntimeError("_foxcall.so is not built; run `python -m forget_gated_softmax_gb300.build`") from e
-        _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append_low, L.fox_decode)))
-        _call = _foxcall
+        except ImportError:  # built without Python's headers: libfox.so is all that the calls need
+            _call = _CtypesCall
+        else:
+            _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append_low, L.fox_decode)))
+            _call = _foxcall
         L.fox_trace_begin.argtypes = []
         L.fox_trace_begin.restype = i
         L.fox_trace_end.argtypes = [ctypes.POINTER(fox_trace_record), i]
         L.fox_trace_end.restype = i
         _lib = L
     return _lib
+
+
+class _CtypesCall:
+    """_foxcall's functions by ctypes, the same numbers in the same order: some microseconds a call longer."""
+
+    @staticmethod
+    def append(c, b, rows, k, ks, v, vs, z, zs, ws, nbytes, stream, *more):
+        rot = ctypes.byref(fox_rotary(*more[:8])) if len(more) >= 8 else None
+        low = more[-1] if len(more) % 8 == 1 else None
+        return lib().fox_cache_append_low(ctypes.byref(fox_cache.from_address(c)), ctypes.byref(fox_batch.from_address(b)),
+                                          rows, k, ks, v, vs, z, zs, rot, low, ws, nbytes, stream)
+
+    @staticmethod
+    def decode(c, b, rows, *more):
+        return lib().fox_decode(ctypes.byref(fox_cache.from_address(c)), ctypes.byref(fox_batch.from_address(b)), rows, *more)
 
 
 def _load_call():
