@@ -104,13 +104,17 @@ bool row_ok(const void* p, int64_t stride, int heads, const fox_cache* c, int ro
   return rows <= 1 || (stride >= (int64_t)heads * c->d && stride < (1LL << 40) && stride * es % 16 == 0);
 }
 
-// Whether a call's output, rows of `heads` heads one after the other, lies within the span of the rows it reads.
-bool overlaps(const void* out, const void* in, int64_t in_stride, int heads, const fox_cache* c, int rows) {
-  const int es = c->dtype == FOX_DTYPE_BF16 ? 2 : 4;
-  const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
-  const __int128 row = (__int128)heads * c->d * es, last = rows > 1 ? (__int128)(rows - 1) * in_stride * es : 0;
-  return o < i + last + row && i < o + row * rows;
+// The bytes from the first to the last of `rows` rows, `stride` elements apart (one row has no next).
+struct Span {
+  uintptr_t at;
+  __int128 bytes;
+};
+Span span(const void* p, int rows, int64_t stride, int64_t elements, int element) {
+  return {reinterpret_cast<uintptr_t>(p), ((__int128)(rows - 1) * (rows > 1 ? stride : 0) + elements) * element};
 }
+// Whether a call's output lies over something else that the call reads or writes.
+bool overlap(const Span& a, const Span& b) { return a.at < b.at + b.bytes && b.at < a.at + a.bytes; }
+int element(const fox_cache* c) { return c->dtype == FOX_DTYPE_BF16 ? 2 : 4; }
 
 fox_status check_ws(void* ws, size_t bytes, size_t need) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || bytes < need) return FOX_ERR_WORKSPACE;
@@ -171,7 +175,16 @@ fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows
   }
   st = check_ws(workspace, workspace_bytes, kErrWordBytes);
   if (st != FOX_OK) return st;
-  if (rot && rot->q && overlaps(rot->q_out, rot->q, rot->q_stride, c->H, c, rows)) return FOX_ERR_INVALID_ARG;
+  if (rot && rot->q) {
+    const int es = element(c);
+    const int64_t row = (int64_t)c->H * c->d, kv = (int64_t)c->Hkv * c->d;
+    const Span out = span(rot->q_out, rows, row, row, es);
+    const int64_t angles = (int64_t)rot->max_pos * (rot->dim / 2);
+    if (overlap(out, span(rot->q, rows, rot->q_stride, row, es)) || overlap(out, span(k, rows, k_stride, kv, es)) ||
+        overlap(out, span(v, rows, v_stride, kv, es)) || overlap(out, span(z, rows, z_stride, c->H, 4)) ||
+        overlap(out, span(rot->cos, 1, 0, angles, 4)) || overlap(out, span(rot->sin, 1, 0, angles, 4)))
+      return FOX_ERR_INVALID_ARG;
+  }
   x.a.err = static_cast<uint32_t*>(workspace);
   x.k = k;
   x.v = v;
@@ -203,7 +216,10 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
   if (!decode_fits(x.a, f32)) return FOX_ERR_UNSUPPORTED;
   st = check_ws(workspace, workspace_bytes, decode_workspace_bytes(x.a, f32));
   if (st != FOX_OK) return st;
-  if (overlaps(o, q, q_stride, c->H, c, rows)) return FOX_ERR_INVALID_ARG;  // a row is read by several workers
+  const int64_t row = (int64_t)c->H * c->d;
+  const Span so = span(o, rows, row, row, element(c)), sl = span(lse, rows, c->H, c->H, 4);
+  const Span sq = span(q, rows, q_stride, row, element(c));  // a row of which several workers read
+  if (overlap(so, sq) || overlap(sl, sq) || overlap(so, sl)) return FOX_ERR_INVALID_ARG;
   x.a.err = static_cast<uint32_t*>(workspace);
   x.q = q;
   x.q_stride = q_stride;

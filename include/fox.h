@@ -320,7 +320,7 @@ typedef struct fox_rotary {
   int pairs;         /* 0: channel i with i + dim / 2;  1: channel 2i with 2i + 1 */
   const void* q;     /* [rows, H, d] to rotate with the same angles, or NULL */
   int64_t q_stride;  /* elements from one row of q to the next */
-  void* q_out;       /* [rows, H, d] contiguous, apart from q */
+  void* q_out;       /* [rows, H, d] contiguous, apart from q, k, v, z, cos and sin */
 } fox_rotary;
 
 /*
@@ -350,7 +350,7 @@ fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows
  * sequence b at position pos attends to the sequence's keys 0 .. pos with the scores of fox_fwd,
  *   x_ij = scale q_i . k_j + c_i - c_j   (c_{j-1} under bias_from_j = 1).
  * q: rows of [H, d], q_stride elements apart (multiples of 16 bytes; 16-byte aligned).
- * o: [rows, H, d] of the cache's type, apart from q; lse: [rows, H] fp32, natural log. Rows of idle
+ * o: [rows, H, d] of the cache's type; lse: [rows, H] fp32, natural log; q, o and lse apart from each other. Rows of idle
  * sequences get O = 0 and LSE = -inf. scale 0 selects d^-1/2.
  * A shared prefix of a bf16 cache is, where that saves more than it costs (B * prefix_len * Hkv * d * 4 bytes
  * above 72 MB, counted once for every 16 rows that a sequence brings a key head), multiplied once with the rows of
