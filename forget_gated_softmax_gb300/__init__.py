@@ -749,6 +749,8 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
         rot = (*rot, cache.g_low.data_ptr())
     if ws is None:
         ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
+    elif ws.get_device() != index:
+        raise ValueError(f"{where}: ws is not on the cache's device")
     st = (_call or _load_call()).append(
         cache.addr, batch.addr, rows, k.data_ptr(), ks, v.data_ptr(), vs, z.data_ptr(), zs, ws.data_ptr(), ws.numel(),
         _current_stream(index) if stream is None else stream.cuda_stream, *rot,
@@ -784,6 +786,8 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
         raise ValueError(f"{where}: lse must be contiguous [{rows}, {cache.H}] float32 on the cache's device")
     if ws is None:
         ws = _alloc_on(stream, lambda: cache_workspace(cache, batch, rows))
+    elif ws.get_device() != index:
+        raise ValueError(f"{where}: ws is not on the cache's device")
     st = (_call or _load_call()).decode(
         cache.addr, batch.addr, rows, q.data_ptr(), qs, scale, 1 if bias_from_j else 0, o.data_ptr(), lse.data_ptr(),
         ws.data_ptr(), ws.numel(), _current_stream(index) if stream is None else stream.cuda_stream,
