@@ -61,14 +61,15 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
   // This lane's key of a tile: its place in the pools, as elements and gate slot; page -1: no key.
   int page = -1, slot = 0;
   size_t kv = 0;
-  // The table's entry comes a tile ahead of its use: its key's page, -1 (reported) where it is none; -2: no key.
+  // The table's entry comes a tile ahead of its use: its key's page; -1: none of the pool, reported and read as page 0;
+  // -2: no key.
   auto look_up = [&](int tile) {
     const bool pre = tile < tp;
     const int j = (pre ? tile : tile - tp) * kKeyTile + lane;
     return j >= (pre ? P : at.s.own) ? -2 : pre ? prefix_page(a, j) : own_page(a, at.b, j);
   };
   auto find_key = [&](int tile, int id) {
-    page = max(id, -1);
+    page = id == -1 ? 0 : max(id, -1);
     if (id == -1 && a.err) atomicOr(a.err, DEV_ERR_BOUNDS);
     slot = ((tile < tp ? tile : tile - tp) * kKeyTile + lane) & (S - 1);
     kv = page < 0 ? 0 : kv_offset(a, page, at.hkv, slot);
