@@ -119,23 +119,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
   // Two channels a thread; with one warp a row, its lanes take them in turn.
 #pragma unroll 1
   for (int ch = (deal > 1 ? threadIdx.x : lane) * 2; ch < D; ch += 64 * deal) {
-  const int w0_ = deal > 1 ? 0 : warp, w1_ = deal > 1 ? kMergeWarps : warp + 1;
-  float top = -INFINITY;
+    const int w0_ = deal > 1 ? 0 : warp, w1_ = deal > 1 ? kMergeWarps : warp + 1;
+    float top = -INFINITY;
 #pragma unroll 1
-  for (int w = w0_; w < w1_; ++w) top = fmaxf(top, mls[w].x);
-  const float safe = top == -INFINITY ? 0.f : top;
-  float o0 = 0.f, o1 = 0.f, sum = 0.f;
+    for (int w = w0_; w < w1_; ++w) top = fmaxf(top, mls[w].x);
+    const float safe = top == -INFINITY ? 0.f : top;
+    float o0 = 0.f, o1 = 0.f, sum = 0.f;
 #pragma unroll 1
-  for (int w = w0_; w < w1_; ++w) {
-    const float t = ex2_approx(mls[w].x - safe);
-    o0 = fmaf(t, sums[w][ch], o0);
-    o1 = fmaf(t, sums[w][ch + 1], o1);
-    sum = fmaf(t, mls[w].y, sum);
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const size_t at = (size_t)row * a.H + h;
-  *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch) = pack_bf16x2(o0 * inv, o1 * inv);
-  if (ch == 0) p.lse[at] = sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+    for (int w = w0_; w < w1_; ++w) {
+      const float t = ex2_approx(mls[w].x - safe);
+      o0 = fmaf(t, sums[w][ch], o0);
+      o1 = fmaf(t, sums[w][ch + 1], o1);
+      sum = fmaf(t, mls[w].y, sum);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const size_t at = (size_t)row * a.H + h;
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch) = pack_bf16x2(o0 * inv, o1 * inv);
+    if (ch == 0) p.lse[at] = sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
   }
 }
 

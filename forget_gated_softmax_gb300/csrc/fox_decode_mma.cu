@@ -157,206 +157,206 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   for (int n = -stages; n < count; ++n) {
     if (n == 0 && warp == 0) find_ends<W>(p, seqs, total, each, ends);  // while the first copies are on their way
     if (n >= 0) {
-    if (!opened) {
-      // The item's rows: Q fragments, and places and cumulative gates of this thread's columns of S^T, rows
-      // 2 t4 and 2 t4 + 1; nothing summed yet.
-      opened = true;
-      if (n - since > 1)
-        cp_async_wait<1>();  // asked for before the last step
-      else
-        cp_async_wait<0>();
-      __syncwarp();
-      since = n;
-      fresh = true;
-      const uint32_t qa = smem_u32(q_of);
-      const int r0 = cur.rt * p.Rt;
+      if (!opened) {
+        // The item's rows: Q fragments, and places and cumulative gates of this thread's columns of S^T, rows
+        // 2 t4 and 2 t4 + 1; nothing summed yet.
+        opened = true;
+        if (n - since > 1)
+          cp_async_wait<1>();  // asked for before the last step
+        else
+          cp_async_wait<0>();
+        __syncwarp();
+        since = n;
+        fresh = true;
+        const uint32_t qa = smem_u32(q_of);
+        const int r0 = cur.rt * p.Rt;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-          uint32_t f[4];
-          const int row = nt * 8 + (lane & 7), chunk = ks * 2 + (lane >> 3);
-          ldsm4(qa + row * (D * 2) + ((chunk ^ (row & 7)) << 4), f);
-          qf[ks][nt][0] = f[0];
-          qf[ks][nt][1] = f[1];
-          qf[ks + 1][nt][0] = f[2];
-          qf[ks + 1][nt][1] = f[3];
+          for (int ks = 0; ks < D / 16; ks += 2) {
+            uint32_t f[4];
+            const int row = nt * 8 + (lane & 7), chunk = ks * 2 + (lane >> 3);
+            ldsm4(qa + row * (D * 2) + ((chunk ^ (row & 7)) << 4), f);
+            qf[ks][nt][0] = f[0];
+            qf[ks][nt][1] = f[1];
+            qf[ks + 1][nt][0] = f[2];
+            qf[ks + 1][nt][1] = f[3];
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int rl = nt * 8 + 2 * t4 + e, r = r0 + rl, t = token_of(p, r), g = r - t * Gp;
+            const bool here = t < cur.s.n && g < G;
+            pos[nt][e] = cur.s.own - cur.s.n + t;
+            gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : 0;
+            ci[nt][e] = {-INFINITY, 0.f};  // an empty row's scores are -inf
+            if (here) ci[nt][e] = gate_sum(it.base[rl], it.g[rl]);
+            m[nt][e] = -INFINITY;
+            l[nt][e] = 0.f;
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rl = nt * 8 + 2 * t4 + e, r = r0 + rl, t = token_of(p, r), g = r - t * Gp;
-          const bool here = t < cur.s.n && g < G;
-          pos[nt][e] = cur.s.own - cur.s.n + t;
-          gidx[nt][e] = here ? (G > L::kRows ? g - r0 % Gp : g) : 0;
-          ci[nt][e] = {-INFINITY, 0.f};  // an empty row's scores are -inf
-          if (here) ci[nt][e] = gate_sum(it.base[rl], it.g[rl]);
-          m[nt][e] = -INFINITY;
-          l[nt][e] = 0.f;
-        }
+        for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[dt][nt][e] = 0.f;
       }
-#pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[dt][nt][e] = 0.f;
-    }
-    uint8_t* st = ring + stage * (2 * L::kTileBytes);
-    ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][stage], phase, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA));
-    if (!ok) break;
-    cp_async_wait<L::kStages - 1>();  // the stage's bases: so many groups were committed after theirs
-    __syncwarp();
+      uint8_t* st = ring + stage * (2 * L::kTileBytes);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][stage], phase, abort_flag, a.err, DEV_ERR_TIMEOUT_TMA));
+      if (!ok) break;
+      cp_async_wait<L::kStages - 1>();  // the stage's bases: so many groups were committed after theirs
+      __syncwarp();
 
-    // The tile's keys are [j0, end) of the prefix, or of the sequence's own, which end for each row with its own.
-    const bool pre = cur.tile < tp;
-    const int j0 = (pre ? cur.tile : cur.tile - tp) * kKeyTile, end = pre ? P : cur.s.own;
-    const uint32_t sk = smem_u32(st), sv = sk + L::kTileBytes;
-    float s[2][NT][4];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t kf[4];
-        const int row = mt * 16 + krow, chunk = (ks & 3) * 2 + kchunk;
-        ldsm4(sk + (ks >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), kf);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], kf, qf[ks][nt][0], qf[ks][nt][1]);
-      }
-    }
-    // Scores of keys mt * 16 + g8 (+ 8) and rows 2 t4 (+ 1), in log2 units.
-    const uint8_t* sg = gates + stage * x.gstage;
-    const float2* bs = reinterpret_cast<const float2*>(sg + base_off);
-    const bool edge = j0 + kKeyTile > (pre ? P : cur.s.own - cur.s.n);  // some slot is no key of some row
-    bool grow = false;
-    float top[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        top[nt][e] = -INFINITY;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const int sub = S == 16 ? mt : 0;
-          const float2 base = bs[sub * heads + gidx[nt][e]];
-          const float beta = (ci[nt][e].hi - base.x) + (ci[nt][e].lo - base.y);
-          const float* gr = reinterpret_cast<const float*>(sg + sub * x.gsub) + gidx[nt][e] * gpitch + 4 -
-                            p.bias_from_j + (S == 16 ? 0 : mt * 16);
-#pragma unroll
-          for (int k8 = 0; k8 < 2; ++k8) {
-            const int key = g8 + k8 * 8;
-            float x = fmaf(beta - gr[key], kLog2e, s[mt][nt][k8 * 2 + e] * p.scale2);
-            if (edge && j0 + mt * 16 + key > (pre ? P - 1 : pos[nt][e])) x = -INFINITY;
-            s[mt][nt][k8 * 2 + e] = x;
-            top[nt][e] = fmaxf(top[nt][e], x);
-          }
-        }
-        grow |= top[nt][e] > m[nt][e] + kGrow;
-      }
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = top[nt][e];
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          const float mn = fmaxf(m[nt][e], x);
-          const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mn);
-          m[nt][e] = mn;
-          l[nt][e] *= alpha;
-#pragma unroll
-          for (int dt = 0; dt < D / 16; ++dt) {
-            acc[dt][nt][e] *= alpha;
-            acc[dt][nt][e + 2] *= alpha;
-          }
-        }
-    }
-    if (j0 + kKeyTile > end) {
-      // Slots behind the end may hold anything: V there becomes 0 (its weights are 0).
-      for (int e = lane; e < (j0 + kKeyTile - end) * (D / 8); e += 32) {
-        const int row = end - j0 + e / (D / 8), c = e % (D / 8);
-        sts_v4(sv + (c >> 3) * (kKeyTile * 128) + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
-      }
-      fence_proxy_async_smem();  // before the next copy into this stage
-      __syncwarp();
-    }
-    // P^T fragments, hi and lo.
-    uint32_t ph[2][NT][2], pl[2][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float o0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], o1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+      // The tile's keys are [j0, end) of the prefix, or of the sequence's own, which end for each row with its own.
+      const bool pre = cur.tile < tp;
+      const int j0 = (pre ? cur.tile : cur.tile - tp) * kKeyTile, end = pre ? P : cur.s.own;
+      const uint32_t sk = smem_u32(st), sv = sk + L::kTileBytes;
+      float s[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int k8 = 0; k8 < 2; ++k8) {
-          const float p0 = ex2_approx(s[mt][nt][k8 * 2] - o0), p1 = ex2_approx(s[mt][nt][k8 * 2 + 1] - o1);
-          l[nt][0] += p0;
-          l[nt][1] += p1;
-          const uint32_t hi = pack_bf16x2(p0, p1);
-          ph[mt][nt][k8] = turn8x8(hi);
-          pl[mt][nt][k8] = turn8x8(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
-        }
-    }
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
 #pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt) {
-        uint32_t vf[4];
-        const int row = mt * 16 + vrow, chunk = (dt & 3) * 2 + vchunk;
-        ldsm4_t(sv + (dt >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), vf);
+      for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(acc[dt][nt], vf, ph[mt][nt][0], ph[mt][nt][1]);
-          mma16816(acc[dt][nt], vf, pl[mt][nt][0], pl[mt][nt][1]);
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t kf[4];
+          const int row = mt * 16 + krow, chunk = (ks & 3) * 2 + kchunk;
+          ldsm4(sk + (ks >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), kf);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], kf, qf[ks][nt][0], qf[ks][nt][1]);
         }
       }
-    __syncwarp();  // every lane has read the stage
-
-    if (cur.tile + 1 == cur.tiles || n + 1 == count) {
-      // Results: O^T through shared memory to rows, finished or the worker's part of them: by the stage just
-      // read, or, for the block to join with its neighbours', kept at the ring's start (all copies were read).
-      const bool alone = cur.i0 >= u0 && cur.i0 + cur.tiles <= u0 + count, keep = !alone && n + 1 == count;
-      float* out = reinterpret_cast<float*>(keep ? ring : st);
+      // Scores of keys mt * 16 + g8 (+ 8) and rows 2 t4 (+ 1), in log2 units.
+      const uint8_t* sg = gates + stage * x.gstage;
+      const float2* bs = reinterpret_cast<const float2*>(sg + base_off);
+      const bool edge = j0 + kKeyTile > (pre ? P : cur.s.own - cur.s.n);  // some slot is no key of some row
+      bool grow = false;
+      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float y = l[nt][e];
+          top[nt][e] = -INFINITY;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-          const int rl = nt * 8 + 2 * t4 + e;
+          for (int mt = 0; mt < 2; ++mt) {
+            const int sub = S == 16 ? mt : 0;
+            const float2 base = bs[sub * heads + gidx[nt][e]];
+            const float beta = (ci[nt][e].hi - base.x) + (ci[nt][e].lo - base.y);
+            const float* gr = reinterpret_cast<const float*>(sg + sub * x.gsub) + gidx[nt][e] * gpitch + 4 -
+                              p.bias_from_j + (S == 16 ? 0 : mt * 16);
 #pragma unroll
-          for (int dt = 0; dt < D / 16; ++dt) {
-            out[rl * L::kOutStride + dt * 16 + g8] = acc[dt][nt][e];
-            out[rl * L::kOutStride + dt * 16 + g8 + 8] = acc[dt][nt][e + 2];
+            for (int k8 = 0; k8 < 2; ++k8) {
+              const int key = g8 + k8 * 8;
+              float x = fmaf(beta - gr[key], kLog2e, s[mt][nt][k8 * 2 + e] * p.scale2);
+              if (edge && j0 + mt * 16 + key > (pre ? P - 1 : pos[nt][e])) x = -INFINITY;
+              s[mt][nt][k8 * 2 + e] = x;
+              top[nt][e] = fmaxf(top[nt][e], x);
+            }
           }
-          if (g8 == 0) {
-            kept.m[warp][rl] = m[nt][e];
-            kept.l[warp][rl] = y;
+          grow |= top[nt][e] > m[nt][e] + kGrow;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = top[nt][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            const float mn = fmaxf(m[nt][e], x);
+            const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mn);
+            m[nt][e] = mn;
+            l[nt][e] *= alpha;
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              acc[dt][nt][e] *= alpha;
+              acc[dt][nt][e + 2] *= alpha;
+            }
+          }
+      }
+      if (j0 + kKeyTile > end) {
+        // Slots behind the end may hold anything: V there becomes 0 (its weights are 0).
+        for (int e = lane; e < (j0 + kKeyTile - end) * (D / 8); e += 32) {
+          const int row = end - j0 + e / (D / 8), c = e % (D / 8);
+          sts_v4(sv + (c >> 3) * (kKeyTile * 128) + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // before the next copy into this stage
+        __syncwarp();
+      }
+      // P^T fragments, hi and lo.
+      uint32_t ph[2][NT][2], pl[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float o0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], o1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int k8 = 0; k8 < 2; ++k8) {
+            const float p0 = ex2_approx(s[mt][nt][k8 * 2] - o0), p1 = ex2_approx(s[mt][nt][k8 * 2 + 1] - o1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            const uint32_t hi = pack_bf16x2(p0, p1);
+            ph[mt][nt][k8] = turn8x8(hi);
+            pl[mt][nt][k8] = turn8x8(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+          uint32_t vf[4];
+          const int row = mt * 16 + vrow, chunk = (dt & 3) * 2 + vchunk;
+          ldsm4_t(sv + (dt >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), vf);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(acc[dt][nt], vf, ph[mt][nt][0], ph[mt][nt][1]);
+            mma16816(acc[dt][nt], vf, pl[mt][nt][0], pl[mt][nt][1]);
           }
         }
-      if (keep && lane == 0) {
-        kept.i0[warp] = cur.i0;
-        kept.at[warp] = cur;
+      __syncwarp();  // every lane has read the stage
+
+      if (cur.tile + 1 == cur.tiles || n + 1 == count) {
+        // Results: O^T through shared memory to rows, finished or the worker's part of them: by the stage just
+        // read, or, for the block to join with its neighbours', kept at the ring's start (all copies were read).
+        const bool alone = cur.i0 >= u0 && cur.i0 + cur.tiles <= u0 + count, keep = !alone && n + 1 == count;
+        float* out = reinterpret_cast<float*>(keep ? ring : st);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = l[nt][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            const int rl = nt * 8 + 2 * t4 + e;
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              out[rl * L::kOutStride + dt * 16 + g8] = acc[dt][nt][e];
+              out[rl * L::kOutStride + dt * 16 + g8 + 8] = acc[dt][nt][e + 2];
+            }
+            if (g8 == 0) {
+              kept.m[warp][rl] = m[nt][e];
+              kept.l[warp][rl] = y;
+            }
+          }
+        if (keep && lane == 0) {
+          kept.i0[warp] = cur.i0;
+          kept.at[warp] = cur;
+        }
+        __syncwarp();
+        if (!keep)
+          leave_rows<__nv_bfloat16, D>(p, cur, w, alone && !shared, out, L::kOutStride, kept.m[warp], kept.l[warp]);
+        fence_proxy_async_smem();  // before the next copy into this stage
+        __syncwarp();
+        opened = false;
       }
-      __syncwarp();
-      if (!keep)
-        leave_rows<__nv_bfloat16, D>(p, cur, w, alone && !shared, out, L::kOutStride, kept.m[warp], kept.l[warp]);
-      fence_proxy_async_smem();  // before the next copy into this stage
-      __syncwarp();
-      opened = false;
-    }
-    if (++cur.tile == cur.tiles && n + 1 < count) next_item(p, seqs, cur);
-    if (++stage == stages) {
-      stage = 0;
-      phase ^= 1;
-    }
+      if (++cur.tile == cur.tiles && n + 1 < count) next_item(p, seqs, cur);
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
 
     if (fresh) {
