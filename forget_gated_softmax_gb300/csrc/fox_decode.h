@@ -229,15 +229,15 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// K and V pass through the L2 cache as what may go first where a step reads them once: what every call needs
-// again (its code, the tables, partial results) then stays. A prefix walked by every sequence is read again. (One sequence
-// of 65536 tokens: 57.6 -> 54.4 us; 32 behind 16384 shared ones, by the prefix kernel: 53.5 -> 52.6.)
-__device__ __forceinline__ uint64_t stream_policy(bool again) {
+// K and V pass through the L2 cache as what may go first, also where other row tiles, or other sequences behind the
+// same prefix, read them again: what every call needs again (its code, the tables, partial results) then stays. One
+// sequence of 65536 tokens: 57.6 -> 54.4 us; 32 behind 16384 shared ones, by the prefix kernel: 53.5 -> 52.6. Read again,
+// without the hint and with it: 16 sequences of 4096 with 28 rows a key head (two row tiles) 117.2 and 114.0, with 64 (four)
+// 215 and 208; one of 2048 with 2048 new tokens 776 and 777; 8 behind 2000 walked shared tokens 24.5 and 24.3; 256 behind 32768
+// (four items a key head) 183 and 184.
+__device__ __forceinline__ uint64_t stream_policy() {
   uint64_t x;
-  if (again)
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(x));
-  else
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(x));
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(x));
   return x;
 }
 __device__ __forceinline__ void tma_load_4d_by(uint64_t policy, void* dst, const CUtensorMap* map, uint64_t* bar, int c0,

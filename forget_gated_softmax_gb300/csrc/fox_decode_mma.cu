@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   Gate2 ci[NT][2];
   int pos[NT][2], gidx[NT][2];
   // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
-  const uint64_t policy = stream_policy(p.walk_prefix);
+  const uint64_t policy = stream_policy();
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
   const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
 

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     };
     if (warp == 8) {
       // -------------------------------------------------------- Q and K
-      const uint64_t policy = stream_policy(false);
+      const uint64_t policy = stream_policy();
       int id = ok ? page_of(t1 - 1) : -1, issued = 0;
       const bool began = ok;
       if (ok) {
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int head0 = hkv * G, mine = warp - 10;  // the stage of this warp
       const int s0 = (c0 & 1) == mine ? 0 : 1;
       const int last = P - 1, lpage = checked_page(a, a.prefix[last >> a.page_shift]);
-      const uint64_t policy = stream_policy(false);
+      const uint64_t policy = stream_policy();
       int id = ok ? page_of(t1 - 1 - s0) : -1, issued = 0;
 #pragma unroll 1
       for (int s = s0; s < nT && ok; s += 2) {
