@@ -705,8 +705,9 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
 
     cos, sin [positions, r / 2] fp32 rotate the first r channels of k by each token's position on the way
     (channel i with i + r / 2; `pairs`: 2i with 2i + 1), and those of q [rows, H, d] into q_out, which is
-    returned (None without q) and must overlap none of the other arguments. Rows may be strided views, as those of a joint projection's
-    output."""
+    returned (None without q) and must overlap none of the other arguments. Rows may be strided views, as those of
+    a joint projection's output. ws: 256 bytes, zero before the first call, or those of cache_workspace; without it what the
+    device reports (a page, length or position that does not fit, its token left out) is lost with the call's own."""
     torch = _torch()
     where = "fox_cache_append"
     index = _cache_call_device(where, cache, batch)
@@ -763,7 +764,8 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
 def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
                ws=None, stream=None) -> Tuple[object, object]:
     """Attention of the batch's newest tokens, appended before, over the cache: q [rows, H, d] -> (O [rows, H, d],
-    LSE [rows, H] fp32); q, o and lse apart from each other. A long shared prefix is read and multiplied once for all sequences (bf16).
+    LSE [rows, H] fp32); q, o and lse apart from each other. A long shared prefix is read and multiplied once for all
+    sequences (bf16; |v| >= 65536 in it is then reported). Without ws what the device reports is lost.
     Rows of idle sequences get O = 0 and LSE = -inf; rows behind the last sequence are not written."""
     torch = _torch()
     where = "fox_decode"
