@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
       const int rr = rt * p.Rt + lane, t = token_of(p, rr), h = hkv * G + min(rr - t * Gp, G - 1), i = s.own - s.n + t;
       ci[warp][lane] = gate_sum(a, own_page_or_0(a, at.b, i), i & (S - 1), h);
     }
+    // the first own key that not all of the item's rows see (the slots behind the last one hold zeros)
+    const int partly = s.n > 1 ? s.own - s.n + token_of(p, rt * p.Rt) + 1 : s.own + kKeyTile;
     if (first) find_ends<W>(p, seqs, total, each, ends);  // by the first warp's lanes, once
     first = false;
     __syncwarp();
@@ -178,17 +180,30 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid
       }
       cp_async_wait<1>();  // V
       __syncwarp();
+      if (NR == 1 || tile < tp || (tile - tp) * kKeyTile + kKeyTile <= partly) {
 #pragma unroll 4
-      for (int jj = 0; jj < kKeyTile; ++jj) {
-        float f[E];
+        for (int jj = 0; jj < kKeyTile; ++jj) {
+          float f[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = vs[jj * D + lane * E + e];
+          for (int e = 0; e < E; ++e) f[e] = vs[jj * D + lane * E + e];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float wt = __shfl_sync(0xffffffffu, sc[r], jj);
+          for (int r = 0; r < NR; ++r) {
+            const float wt = __shfl_sync(0xffffffffu, sc[r], jj);
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[r][e] = fmaf(wt, f[e], acc[r][e]);
+            for (int e = 0; e < E; ++e) acc[r][e] = fmaf(wt, f[e], acc[r][e]);
+          }
         }
+      } else {
+        // Keys that some of the rows do not see: a weight of 0 times an infinity or a NaN would be a NaN.
+#pragma unroll 1
+        for (int jj = 0; jj < kKeyTile; ++jj)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float wt = __shfl_sync(0xffffffffu, sc[r], jj);
+            if (wt == 0.f) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[r][e] = fmaf(wt, vs[jj * D + lane * E + e], acc[r][e]);
+          }
       }
       __syncwarp();
       if (tile + 1 < tile1)

@@ -54,6 +54,53 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Sets the values of keys [from, to) of a tile of V that are infinite or no number to 0; true if there were any.
+template <int D>
+static __device__ __noinline__ bool take_out(uint8_t* v, int from, int to) {
+  bool odd = false;
+#pragma unroll 1
+  for (int e = threadIdx.x & 31; e < (to - from) * (D / 8); e += 32) {
+    const int row = from + e / (D / 8), c = e % (D / 8);
+    uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * (kKeyTile * 128) + row * 128 + ((c ^ row) & 7) * 16);
+    uint32_t w[4] = {at->x, at->y, at->z, at->w};
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
+      any |= lo || hi;
+      w[i] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+    }
+    if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+    odd |= any;
+  }
+  fence_proxy_async_smem();  // before the next copy into the stage
+  __syncwarp();
+  return odd;
+}
+// What take_out took from keys that some of a segment's rows see, to the sums of those (rows + r * pitch), once more
+// from the cache. Key tiles from tile0 to tile1.
+template <int D>
+static __device__ __noinline__ void put_back(const DecodeParams& p, const Place& at, int tile0, int tile1, int tp,
+                                             float* rows, int pitch) {
+  const PagedArgs& a = p.a;
+  const int lane = threadIdx.x & 31, r0 = at.rt * p.Rt, R = rows_of(p, at), new0 = at.s.own - at.s.n;
+  const int lo = max((tile0 - tp) * kKeyTile, new0 + token_of(p, r0) + 1);
+  const int hi = min((tile1 - tp + 1) * kKeyTile, new0 + token_of(p, r0 + R - 1) + 1);
+#pragma unroll 1
+  for (int j = lo; j < hi; ++j) {
+    const int page = own_page_or_0(a, at.b, j);
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + kv_offset(a, page, at.hkv, j & (a.page_size - 1));
+#pragma unroll 1
+    for (int ch = lane; ch < D; ch += 32) {
+      const float f = __bfloat162float(v[ch]);
+      if (fabsf(f) < INFINITY) continue;
+#pragma unroll 1
+      for (int r = 0; r < R; ++r)
+        if (j <= new0 + token_of(p, r0 + r)) rows[r * pitch + ch] += f;
+    }
+  }
+  __syncwarp();
+}
 // Shared memory: K and V of every (warp, stage), then its gates, then the sequences' work offsets.
 // Gates of a stage: per sub-page (32 slots, or two of 16) [heads][slots + 4] sums, then [heads] bases.
 struct MmaShape {
@@ -79,7 +126,9 @@ struct ItemRows {
   float2 base[kRows];
 };
 
-template <int D, int NT>
+// kMany: sequences may bring more than one token, so that a tile may hold keys that some of an item's rows do not see
+// (a kernel of its own: one token a sequence took 0.5 to 4 % longer with that code in it, several tokens take up to 2 %).
+template <int D, int NT, bool kMany>
 __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
     decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ CUtensorMap tmap_g, const __grid_constant__ DecodeParams p,
@@ -135,6 +184,8 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   float m[NT][2], l[NT][2];
   Gate2 ci[NT][2];
   int pos[NT][2], gidx[NT][2];
+  int first = 0, last = 0;  // with kMany: own positions of the item's first and last row
+  bool odd = false;         // with kMany: an infinity or a NaN was taken out of the item's V
   // ldmatrix addresses of this lane: K rows (keys) x 16-byte channel chunks, V the same, transposed.
   const uint64_t policy = stream_policy();
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
@@ -170,6 +221,11 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
         fresh = true;
         const uint32_t qa = smem_u32(q_of);
         const int r0 = cur.rt * p.Rt;
+        if (kMany) {
+          first = cur.s.own - cur.s.n + token_of(p, r0);
+          last = cur.s.own - cur.s.n + min(token_of(p, r0 + p.Rt - 1), cur.s.n - 1);
+          odd = false;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -207,9 +263,11 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
       cp_async_wait<L::kStages - 1>();  // the stage's bases: so many groups were committed after theirs
       __syncwarp();
 
-      // The tile's keys are [j0, end) of the prefix, or of the sequence's own, which end for each row with its own.
+      // The tile's keys are those of the prefix, or of the sequence's own, which end for each row with its own: every
+      // row sees the keys before `seen`, no row those from `end` on.
       const bool pre = cur.tile < tp;
-      const int j0 = (pre ? cur.tile : cur.tile - tp) * kKeyTile, end = pre ? P : cur.s.own;
+      const int j0 = (pre ? cur.tile : cur.tile - tp) * kKeyTile, seen = pre ? P : kMany ? first + 1 : cur.s.own,
+                end = pre ? P : kMany ? last + 1 : cur.s.own;
       const uint32_t sk = smem_u32(st), sv = sk + L::kTileBytes;
       float s[2][NT][4];
 #pragma unroll
@@ -277,7 +335,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
             }
           }
       }
-      if (j0 + kKeyTile > end) {
+      if (j0 + kKeyTile > end && (!kMany || j0 < end)) {
         // Slots behind the end may hold anything: V there becomes 0 (its weights are 0).
         for (int e = lane; e < (j0 + kKeyTile - end) * (D / 8); e += 32) {
           const int row = end - j0 + e / (D / 8), c = e % (D / 8);
@@ -286,36 +344,42 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
         fence_proxy_async_smem();  // before the next copy into this stage
         __syncwarp();
       }
-      // P^T fragments, hi and lo.
-      uint32_t ph[2][NT][2], pl[2][NT][2];
+      // So does what is no number in the values of a key that only some of the rows see: times the others' weights of 0
+      // it would be a NaN.
+      if (kMany && j0 < end && j0 + kKeyTile > seen && seen < end)
+        odd |= take_out<D>(st + L::kTileBytes, max(seen - j0, 0), min(end - j0, kKeyTile));
+      if (!kMany || j0 < end) {  // not where no row sees a key of the tile
+        // P^T fragments, hi and lo.
+        uint32_t ph[2][NT][2], pl[2][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float o0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], o1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        for (int nt = 0; nt < NT; ++nt) {
+          const float o0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], o1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int k8 = 0; k8 < 2; ++k8) {
+              const float p0 = ex2_approx(s[mt][nt][k8 * 2] - o0), p1 = ex2_approx(s[mt][nt][k8 * 2 + 1] - o1);
+              l[nt][0] += p0;
+              l[nt][1] += p1;
+              const uint32_t hi = pack_bf16x2(p0, p1);
+              ph[mt][nt][k8] = turn8x8(hi);
+              pl[mt][nt][k8] = turn8x8(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
+            }
+        }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int k8 = 0; k8 < 2; ++k8) {
-            const float p0 = ex2_approx(s[mt][nt][k8 * 2] - o0), p1 = ex2_approx(s[mt][nt][k8 * 2 + 1] - o1);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            const uint32_t hi = pack_bf16x2(p0, p1);
-            ph[mt][nt][k8] = turn8x8(hi);
-            pl[mt][nt][k8] = turn8x8(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
+          for (int dt = 0; dt < D / 16; ++dt) {
+            uint32_t vf[4];
+            const int row = mt * 16 + vrow, chunk = (dt & 3) * 2 + vchunk;
+            ldsm4_t(sv + (dt >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), vf);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(acc[dt][nt], vf, ph[mt][nt][0], ph[mt][nt][1]);
+              mma16816(acc[dt][nt], vf, pl[mt][nt][0], pl[mt][nt][1]);
+            }
           }
       }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) {
-          uint32_t vf[4];
-          const int row = mt * 16 + vrow, chunk = (dt & 3) * 2 + vchunk;
-          ldsm4_t(sv + (dt >> 2) * (kKeyTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), vf);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816(acc[dt][nt], vf, ph[mt][nt][0], ph[mt][nt][1]);
-            mma16816(acc[dt][nt], vf, pl[mt][nt][0], pl[mt][nt][1]);
-          }
-        }
       __syncwarp();  // every lane has read the stage
 
       if (cur.tile + 1 == cur.tiles || n + 1 == count) {
@@ -341,6 +405,10 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
               kept.l[warp][rl] = y;
             }
           }
+        if (kMany && __any_sync(0xffffffffu, odd)) {
+          __syncwarp();
+          put_back<D>(p, cur, max(u0 - cur.i0, 0), cur.tile, tp, out, L::kOutStride);
+        }
         if (keep && lane == 0) {
           kept.i0[warp] = cur.i0;
           kept.at[warp] = cur;
@@ -489,10 +557,10 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   if (shared) grid_dep_wait();
 }
 
-template <int D, int NT>
-cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t s) {
+template <int D, int NT, bool kMany>
+cudaError_t launch_as(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t s) {
   using L = MmaLayout<D, NT>;
-  auto kernel = decode_mma_kernel<D, NT>;
+  auto kernel = decode_mma_kernel<D, NT, kMany>;
   const int G = p.a.H / p.a.Hkv, subs = p.a.page_size == 16 ? 2 : 1;
   MmaShape x;
   x.heads = G < L::kRows ? G : L::kRows;
@@ -516,6 +584,11 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t 
   const cudaError_t f =
       launch_dependent(kernel, dim3(kSMs), dim3(32 * L::kWarps), smem, s, maps[0], maps[1], maps[2], p, x);
   return f != cudaSuccess ? f : cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t s) {
+  return p.a.max_new > 1 ? launch_as<D, NT, true>(p, maps, s) : launch_as<D, NT, false>(p, maps, s);
 }
 
 }  // namespace

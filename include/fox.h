@@ -357,7 +357,8 @@ fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows
  * all sequences: its weights and V then pass through fp16 as in fox_fwd, so that |v| >= 65536 in its pages sets the
  * error word, and V below 2^-14 is held in steps of 2^-24. Otherwise, and in fp32, every sequence walks it, with V as
  * it is.
- * A K or V slot behind the sequence's end is never used, whatever it holds. The same arguments and
+ * Nothing behind a row's position is used for it, whatever K, V and the gates hold there (new tokens further on, slots
+ * behind the sequence's end). The same arguments and
  * contents give the same bits; how a row's sums are ordered follows from the lengths of the whole batch.
  */
 fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
