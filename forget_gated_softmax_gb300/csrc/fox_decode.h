@@ -231,7 +231,7 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // K and V pass through the L2 cache as what may go first, also where other row tiles, or other sequences behind the
 // same prefix, read them again: what every call needs again (its code, the tables, partial results) then stays. One
-// sequence of 65536 tokens: 57.6 -> 54.4 us; 32 behind 16384 shared ones, by the prefix kernel: 53.5 -> 52.6. Read again,
+// sequence of 65536 tokens: 56.1 -> 52.9 us; 32 behind 16384 shared ones, by the prefix kernel: 53.2 -> 52.3. Read again,
 // without the hint and with it: 16 sequences of 4096 with 28 rows a key head (two row tiles) 117.2 and 114.0, with 64 (four)
 // 215 and 208; one of 2048 with 2048 new tokens 776 and 777; 8 behind 2000 walked shared tokens 24.5 and 24.3; 256 behind 32768
 // (four items a key head) 183 and 184.
@@ -521,8 +521,9 @@ cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t s);
 // The fp32 kernel (fox_decode_f32.cu): row tile, workers of a CTA, CTAs of an SM, launch.
 int decode_f32_rows(int rows);
 constexpr int kF32Warps = 4;
-// CTAs: of 64 channels two fit an SM's shared memory (4 sequences of up to 2000 28 -> 21 us against one; eight warps in
-// one CTA were as fast there, but crowd short calls on few SMs: 14 -> 16.6 us).
+// CTAs: of 64 channels two fit an SM's shared memory (16 heads, 16 sequences of up to 1000: 49 -> 37.6 us against one, 4 of up
+// to 2000: 33 -> 27.5, with the tables' entries asked for ahead; eight warps in one CTA were as fast there, but crowd short
+// calls on few SMs).
 constexpr int f32_ctas(int d) { return d == 128 ? kSMs : 2 * kSMs; }
 cudaError_t launch_decode_f32(const DecodeParams& p, cudaStream_t s);
 PrefixPlan prefix_plan(const PagedArgs& a);

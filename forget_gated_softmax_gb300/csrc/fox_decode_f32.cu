@@ -10,9 +10,9 @@
 // whole, by asynchronous copies (a row of 512 bytes an instruction): K of the next tile while this one's
 // V is used, V of the next while its K is. Scores: a lane owns a key, whose row it reads with the rows
 // padded to different banks. Values: a lane owns d / 32 channels. The prefix's keys, where one is
-// shared, are walked like the sequence's own. Bound by latency where they are short (2 sequences of 257: 14 us), by
-// the few warps that shared memory leaves an SM where they are long (16 of up to 1000 with 16 heads of 64 channels,
-// 75 MB: 35 us).
+// shared, are walked like the sequence's own. Bound by latency where they are short (2 sequences of 257: 13 us), by
+// the few warps that shared memory leaves an SM where they are long, each with one K and one V tile at most on its way (16 of up
+// to 1000 with 16 heads of 64 channels, 75 MB: 34.5 us, 39 % of it what memory takes).
 #include "fox_decode.h"
 
 namespace fox {
@@ -25,8 +25,8 @@ struct F32Layout {
 };
 
 // NR: rows of a row tile. Loops over rows have no other bound: with one known only at run time every row was a
-// branch (8 sequences of up to 3000, 16 rows a key head: 69 -> 41 us; 4 of 2000 with 4 rows: 34 -> 23; 16 of 1000
-// with one, 64 channels: 38 -> 35).
+// branch (8 sequences of up to 3000 on 32 / 8 heads, 16 rows a key head: 347 -> 170 us; 4 of 2000 with 4 rows: 49.6 -> 33.5;
+// 16 of 1000 with one, 64 channels: 37.6 -> 34.2).
 template <int D, int NR>
 __global__ void __launch_bounds__(32 * kF32Warps) decode_f32_kernel(const __grid_constant__ DecodeParams p) {
   using L = F32Layout<D, NR>;

@@ -116,8 +116,8 @@ struct Window {
 
 // An item's rows are asked for by asynchronous copies while the item before is computed: Q and the gates when
 // that one begins, for which the table's entries for the rows' own tokens are there, asked for an item earlier.
-// Against loads when the item begins: 256 sequences of about 500 87 -> 81 us, one of 65536 61 -> 59, five guessed
-// tokens behind 8 long ones 70.6 -> 69.1; 128 of about 200 with 64 channels 37.9 -> 39.4.
+// Against loads when the item begins: 256 sequences of up to 500 86.5 -> 80.6 us, one of 65536 59.1 -> 57.3, 16 of up to 4096
+// with four tokens each 70.0 -> 68.7; 128 of up to 200 with 64 channels 29.7 -> 30.6.
 template <int kRows>
 struct ItemRows {
   Place at[2];         // by the item's number & 1, as the entries are

@@ -32,9 +32,10 @@
 // of 65536 or more in V (outside fp16) sets DEV_ERR_RANGE. A 32-column chunk of S, once read, holds its P.
 //
 // 32768 keys, 256 sequences x 4 heads a key head, 8 of these, d = 128: 133 us, 1030 TFLOP/s, 53 % of
-// cuBLAS's burst bf16 rate. What bounds it: the softmax warps' issue, two of them a scheduler at about four cycles an
-// instruction while both streams compute. Without the conversion of V it took 5 us less; 168 registers for
-// the softmax (88 for the others) took no less.
+// cuBLAS's burst bf16 rate. What bounds it is the chain of each stream, S -> softmax -> P V, and no unit: the tensor pipe is 48 %
+// active, issue slots 54 %. Of the time between two instructions of a warp a third goes on what it waits to be loaded (S from
+// tensor memory), then fixed latencies (15 %), the scheduler's other warps (13 %) and instruction fetch (8 %): two softmax
+// warps a scheduler cannot cover them. Without the conversion of V it took 5 us less; 168 registers for the softmax (88 for the others) took no less.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -125,8 +126,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   int u = blockIdx.x * pp.each;
 
   // V's stages: with one row tile three, the third in the place of a second row tile's Q, since a stream then has
-  // every other tile and would wait for its next V from the end of its last P V on (52.5 -> 50.5 us at 32 sequences behind 16384 tokens,
-  // 72 -> 66 at 30 behind 50000).
+  // every other tile and would wait for its next V from the end of its last P V on (52.3 -> 50.1 us at 32 sequences behind 16384 tokens,
+  // 75.0 -> 68.5 at 30 behind 50000).
   auto v_round = [](int c) { return kSplit ? c / 3 : c >> 1; };  // of key tile c, and its stage
   auto v_stage = [](int c) { return kSplit ? c % 3 : c & 1; };
   auto v_at = [](int st) { return kSplit && st == 2 ? L::kQ + L::kTileBytes : L::kV + st * L::kTileBytes; };
