@@ -470,16 +470,28 @@ __global__ void __launch_bounds__(kThreads) base_scan_kernel(const AppendParams 
   }
 }
 
+struct AppendBlocks {
+  int page_chunks, head_groups;
+  long long gates, copies;
+};
+AppendBlocks append_blocks(const PagedArgs& a, bool with_q, int vec) {
+  const CopyShape x = copy_shape((2 * a.Hkv + (with_q ? a.H : 0)) * (a.d / vec / 2));
+  AppendBlocks n;
+  n.page_chunks = ceil_div(a.max_new, a.page_size) + 1;
+  n.head_groups = ceil_div(a.H, kGateHeads);
+  n.gates = (long long)a.B * n.page_chunks * n.head_groups;
+  n.copies = (long long)ceil_div(a.rows, kRows * x.side) * x.chunks;
+  return n;
+}
+
 template <typename T>
 cudaError_t launch(AppendParams p, cudaStream_t s) {
   const PagedArgs& a = p.a;
-  const CopyShape x = copy_shape((2 * a.Hkv + (p.qn ? a.H : 0)) * (a.d / Vec<T>::kN / 2));
-  const long long copy = (long long)ceil_div(a.rows, kRows * x.side) * x.chunks;
-  p.page_chunks = ceil_div(a.max_new, a.page_size) + 1;
-  p.head_groups = ceil_div(a.H, kGateHeads);
+  const AppendBlocks n = append_blocks(a, p.qn != nullptr, Vec<T>::kN);
+  const long long gates = n.gates, copy = n.copies;
+  p.page_chunks = n.page_chunks;
+  p.head_groups = n.head_groups;
   p.scan_bases = a.max_new > a.page_size;
-  const long long gates = (long long)a.B * p.page_chunks * p.head_groups;
-  if (copy + gates > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.gate_blocks = static_cast<int>(gates);
   cudaError_t e;
   {
@@ -496,6 +508,11 @@ cudaError_t launch(AppendParams p, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool append_fits(const PagedArgs& a, bool with_q, bool f32) {
+  const AppendBlocks n = append_blocks(a, with_q, f32 ? Vec<float>::kN : Vec<__nv_bfloat16>::kN);
+  return n.gates + n.copies <= 0x7fffffffLL;
+}
 
 cudaError_t launch_cache_append(const CacheAppendArgs& x, bool f32, cudaStream_t s) {
   AppendParams p = {};

@@ -158,6 +158,7 @@ fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows
   if (st != FOX_OK) return st;
   if (!row_ok(k, k_stride, c->Hkv, c, rows) || !row_ok(v, v_stride, c->Hkv, c, rows)) return FOX_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(g_low) & 3u) return FOX_ERR_INVALID_ARG;
+  if (!append_fits(x.a, rot && rot->q, c->dtype == FOX_DTYPE_F32)) return FOX_ERR_UNSUPPORTED;
   if (!z || (reinterpret_cast<uintptr_t>(z) & 3u) || (rows > 1 && (z_stride < c->H || z_stride >= (1LL << 40))))
     return FOX_ERR_INVALID_ARG;
   if (rot) {

@@ -28,6 +28,7 @@ struct CacheAppendArgs {
   int max_pos, rot, pairs;
   float* g_low;  // what the rounding of g leaves of the sums, laid out like g, or null
 };
+bool append_fits(const PagedArgs& a, bool with_q, bool f32);  // its blocks are one grid's
 cudaError_t launch_cache_append(const CacheAppendArgs& x, bool f32, cudaStream_t s);
 struct DecodeArgs {
   PagedArgs a;

@@ -59,3 +59,12 @@ def test_the_rule_against_plain_numbers(tmp_path):
             top = max(most + warps * each, workers * each + each)
             assert not fits(most, workers, warps) or top <= INT_MAX
             assert fits(most, workers, warps) or top + workers + each > INT_MAX
+
+
+def test_appends_of_more_blocks_than_a_grid_has_are_refused(L):
+    """The gates' blocks: a sequence, a page of its most new tokens, 32 heads."""
+    c = fox.fox_cache(8, 16, 1024, 1, 64, 0, FAKE, FAKE, FAKE, FAKE)
+    for most, status in ((1 << 20, 2), (1 << 16, 3)):  # the second fits, and comes to its missing workspace
+        b = fox.fox_batch(2048, most, 1 << 20, 0, FAKE, FAKE, FAKE, None)
+        assert L.fox_cache_append(ctypes.byref(c), ctypes.byref(b), (1 << 20) - 1, FAKE, 64, FAKE, 64, FAKE, 1024, None, None,
+                                  256, None) == status
