@@ -8,7 +8,8 @@ library has not been built, every call fails with an error saying so.
 
 Names follow the C ABI: fox_fwd, fox_bwd, fox_fwd_workspace_bytes,
 fox_bwd_workspace_bytes, fox_check_error, fox_status_string; fox_cache_append
-and fox_decode work on handles made by make_cache and make_batch.
+and fox_decode work on handles made by make_cache and make_batch, the fox_cache4_*
+calls on make_cache4's, fox_pages_* on make_pages'.
 """
 from __future__ import annotations
 
@@ -62,6 +63,15 @@ EXPORTS = (
     "fox_cache_append",
     "fox_cache_append_low",
     "fox_decode",
+    "fox_cache4_workspace_bytes",
+    "fox_cache4_append",
+    "fox_cache4_decode",
+    "fox_cache4_read",
+    "fox_pages_workspace_bytes",
+    "fox_pages_step",
+    "fox_pages_compact",
+    "fox_cache_copy",
+    "fox_cache4_copy",
 )
 
 
@@ -101,6 +111,23 @@ class fox_cache(ctypes.Structure):
     ]
 
 
+class fox_cache4(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("Hkv", ctypes.c_int),
+        ("d", ctypes.c_int),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("ks", ctypes.c_void_p),
+        ("vs", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("gbase", ctypes.c_void_p),
+        ("g_low", ctypes.c_void_p),
+    ]
+
+
 class fox_batch(ctypes.Structure):
     _fields_ = [
         ("B", ctypes.c_int),
@@ -127,12 +154,26 @@ class fox_rotary(ctypes.Structure):
     ]
 
 
+class fox_pages(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("B", ctypes.c_int),
+        ("table_stride", ctypes.c_int),
+        ("prefix_len", ctypes.c_int),
+        ("refs", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("prefix_table", ctypes.c_void_p),
+    ]
+
+
 class fox_trace_record(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_char_p), ("ms", ctypes.c_float)]
 
 
 _lib = None
-_call = None  # fox_cache_append_low and fox_decode by way of _foxcall.so (csrc/fox_call.c), or of ctypes without it
+_call = None  # the serving calls (appends and decodes) by way of _foxcall.so (csrc/fox_call.c), or of ctypes without it
 
 
 def lib() -> ctypes.CDLL:
@@ -198,12 +239,31 @@ def lib() -> ctypes.CDLL:
         L.fox_cache_append_low.restype = i
         L.fox_decode.argtypes = [pc, pb, i, vp, i64, ctypes.c_float, i, vp, vp, vp, sz, vp]
         L.fox_decode.restype = i
+        p4, pg = ctypes.POINTER(fox_cache4), ctypes.POINTER(fox_pages)
+        L.fox_cache4_workspace_bytes.argtypes = [p4, pb, i]
+        L.fox_cache4_workspace_bytes.restype = sz
+        L.fox_cache4_append.argtypes = [p4, pb, i, vp, i64, vp, i64, vp, i64, ctypes.POINTER(fox_rotary), vp, sz, vp]
+        L.fox_cache4_append.restype = i
+        L.fox_cache4_decode.argtypes = [p4, pb, i, vp, i64, ctypes.c_float, i, vp, vp, vp, sz, vp]
+        L.fox_cache4_decode.restype = i
+        L.fox_cache4_read.argtypes = [p4, pb, i, vp, i64, vp, i64, vp, sz, vp]
+        L.fox_cache4_read.restype = i
+        L.fox_pages_workspace_bytes.argtypes = [pg, pg]
+        L.fox_pages_workspace_bytes.restype = sz
+        L.fox_pages_step.argtypes = [pg, pg, vp, vp, vp, vp, sz, vp]
+        L.fox_pages_step.restype = i
+        L.fox_pages_compact.argtypes = [pg, pg, vp, vp, i, vp, vp, sz, vp]
+        L.fox_pages_compact.restype = i
+        L.fox_cache_copy.argtypes = [pc, vp, vp, i, vp, sz, vp]
+        L.fox_cache_copy.restype = i
+        L.fox_cache4_copy.argtypes = [p4, vp, i, vp, sz, vp]
+        L.fox_cache4_copy.restype = i
         try:
             from . import _foxcall
         except ImportError:  # built without Python's headers: libfox.so is all that the calls need
             _call = _CtypesCall
         else:
-            _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append_low, L.fox_decode)))
+            _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append_low, L.fox_decode, L.fox_cache4_append, L.fox_cache4_decode)))
             _call = _foxcall
         L.fox_trace_begin.argtypes = []
         L.fox_trace_begin.restype = i
@@ -226,6 +286,16 @@ class _CtypesCall:
     @staticmethod
     def decode(c, b, rows, *more):
         return lib().fox_decode(ctypes.byref(fox_cache.from_address(c)), ctypes.byref(fox_batch.from_address(b)), rows, *more)
+
+    @staticmethod
+    def append4(c, b, rows, k, ks, v, vs, z, zs, ws, nbytes, stream, *more):
+        rot = ctypes.byref(fox_rotary(*more)) if more else None
+        return lib().fox_cache4_append(ctypes.byref(fox_cache4.from_address(c)), ctypes.byref(fox_batch.from_address(b)), rows, k,
+                                       ks, v, vs, z, zs, rot, ws, nbytes, stream)
+
+    @staticmethod
+    def decode4(c, b, rows, *more):
+        return lib().fox_cache4_decode(ctypes.byref(fox_cache4.from_address(c)), ctypes.byref(fox_batch.from_address(b)), rows, *more)
 
 
 def _load_call():
@@ -699,17 +769,8 @@ def _alloc_on(stream, make):
         return make()
 
 
-def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, sin=None, pairs: bool = False,
-                     q_out=None, ws=None, stream=None):
-    """Append the batch's new tokens: k, v [rows, Hkv, d] and gate logits z [rows, H] fp32 into the cache's pages.
-
-    cos, sin [positions, r / 2] fp32 rotate the first r channels of k by each token's position on the way
-    (channel i with i + r / 2; `pairs`: 2i with 2i + 1), and those of q [rows, H, d] into q_out, which is
-    returned (None without q) and must overlap none of the other arguments. Rows may be strided views, as those of
-    a joint projection's output. ws: 256 bytes, zero before the first call, or those of cache_workspace; without it what the
-    device reports (a page, length or position that does not fit, its token left out) is lost with the call's own."""
+def _append(where: str, call, low, cache, batch: Batch, k, v, z, q, cos, sin, pairs, q_out, ws, stream):
     torch = _torch()
-    where = "fox_cache_append"
     index = _cache_call_device(where, cache, batch)
     rows = k.shape[0]
     ks = _row_stride(where, "k", k, cache, cache.Hkv, rows, index)
@@ -746,13 +807,13 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
             raise ValueError(f"{where}: q_out without q")
         rot = (cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if pairs else 0,
                0 if q is None else q.data_ptr(), qs, 0 if q is None else q_out.data_ptr())
-    if cache.g_low is not None:
-        rot = (*rot, cache.g_low.data_ptr())
+    if low is not None:
+        rot = (*rot, low.data_ptr())
     if ws is None:
         ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
     elif ws.get_device() != index:
         raise ValueError(f"{where}: ws is not on the cache's device")
-    st = (_call or _load_call()).append(
+    st = call(
         cache.addr, batch.addr, rows, k.data_ptr(), ks, v.data_ptr(), vs, z.data_ptr(), zs, ws.data_ptr(), ws.numel(),
         _current_stream(index) if stream is None else stream.cuda_stream, *rot,
     )
@@ -761,14 +822,8 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
     return q_out
 
 
-def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
-               ws=None, stream=None) -> Tuple[object, object]:
-    """Attention of the batch's newest tokens, appended before, over the cache: q [rows, H, d] -> (O [rows, H, d],
-    LSE [rows, H] fp32); q, o and lse apart from each other. A long shared prefix is read and multiplied once for all
-    sequences (bf16; |v| >= 65536 in it is then reported). Without ws what the device reports is lost.
-    Rows of idle sequences get O = 0 and LSE = -inf; rows behind the last sequence are not written."""
+def _decode(where: str, call, make_ws, cache, batch: Batch, q, scale, bias_from_j, o, lse, ws, stream):
     torch = _torch()
-    where = "fox_decode"
     index = _cache_call_device(where, cache, batch)
     rows = q.shape[0]
     qs = _row_stride(where, "q", q, cache, cache.H, rows, index)
@@ -787,16 +842,276 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
     elif lse.shape != (rows, cache.H) or lse.dtype is not torch.float32 or lse.get_device() != index or not lse.is_contiguous():
         raise ValueError(f"{where}: lse must be contiguous [{rows}, {cache.H}] float32 on the cache's device")
     if ws is None:
-        ws = _alloc_on(stream, lambda: cache_workspace(cache, batch, rows))
+        ws = _alloc_on(stream, lambda: make_ws(cache, batch, rows))
     elif ws.get_device() != index:
         raise ValueError(f"{where}: ws is not on the cache's device")
-    st = (_call or _load_call()).decode(
+    st = call(
         cache.addr, batch.addr, rows, q.data_ptr(), qs, scale, 1 if bias_from_j else 0, o.data_ptr(), lse.data_ptr(),
         ws.data_ptr(), ws.numel(), _current_stream(index) if stream is None else stream.cuda_stream,
     )
     if st != 0:
         raise FoxError(st, where)
     return o, lse
+
+
+def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, sin=None, pairs: bool = False,
+                     q_out=None, ws=None, stream=None):
+    """Append the batch's new tokens: k, v [rows, Hkv, d] and gate logits z [rows, H] fp32 into the cache's pages.
+
+    cos, sin [positions, r / 2] fp32 rotate the first r channels of k by each token's position on the way
+    (channel i with i + r / 2; `pairs`: 2i with 2i + 1), and those of q [rows, H, d] into q_out, which is
+    returned (None without q) and must overlap none of the other arguments. Rows may be strided views, as those of
+    a joint projection's output. ws: 256 bytes, zero before the first call, or those of cache_workspace; without it what the
+    device reports (a page, length or position that does not fit, its token left out) is lost with the call's own."""
+    return _append("fox_cache_append", (_call or _load_call()).append, cache.g_low, cache, batch, k, v, z, q, cos, sin, pairs, q_out,
+                   ws, stream)
+
+
+def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
+               ws=None, stream=None) -> Tuple[object, object]:
+    """Attention of the batch's newest tokens, appended before, over the cache: q [rows, H, d] -> (O [rows, H, d],
+    LSE [rows, H] fp32); q, o and lse apart from each other. A long shared prefix is read and multiplied once for all
+    sequences (bf16; |v| >= 65536 in it is then reported). Without ws what the device reports is lost.
+    Rows of idle sequences get O = 0 and LSE = -inf; rows behind the last sequence are not written."""
+    return _decode("fox_decode", (_call or _load_call()).decode, cache_workspace, cache, batch, q, scale, bias_from_j, o, lse, ws,
+                   stream)
+
+
+# ------------------------------------------------------------------------------- the cache in 4 bits
+
+
+class Cache4:
+    """A paged cache in 4 bits over the caller's tensors (see fox_cache4 in include/fox.h). Made by make_cache4 or new_cache4."""
+
+    __slots__ = ("k", "v", "ks", "vs", "g", "gbase", "g_low", "params", "ref", "addr", "device", "index", "dtype", "H", "Hkv", "d", "page_size")
+
+
+def make_cache4(k, v, ks, vs, g, gbase, g_low=None) -> Cache4:
+    """A handle on a 4-bit cache: k, v [pages, Hkv, page_size, d / 2], ks [pages, Hkv, page_size, d / 32] and
+    vs [pages, Hkv, page_size / 16, 4, d / 32, 4] uint8; g [pages, H, page_size] and gbase [pages, H, 2] fp32, g_low like g
+    (as in make_cache); all contiguous on one CUDA device."""
+    torch = _torch()
+    pages, Hkv, S, half = k.shape
+    H, d = g.shape[1], 2 * half
+    if tuple(v.shape) != (pages, Hkv, S, half):
+        raise ValueError("make_cache4: v must have k's shape")
+    if tuple(ks.shape) != (pages, Hkv, S, d // 32) or tuple(vs.shape) != (pages, Hkv, S // 16, 4, d // 32, 4):
+        raise ValueError("make_cache4: ks must be [pages, Hkv, page_size, d / 32] and vs [pages, Hkv, page_size / 16, 4, d / 32, 4]")
+    if tuple(g.shape) != (pages, H, S) or tuple(gbase.shape) != (pages, H, 2):
+        raise ValueError("make_cache4: g must be [pages, H, page_size] and gbase [pages, H, 2]")
+    if g_low is not None and g_low.shape != g.shape:
+        raise ValueError("make_cache4: g_low must have g's shape")
+    if any(t.dtype != torch.uint8 for t in (k, v, ks, vs)):
+        raise TypeError("make_cache4: k, v, ks and vs must be uint8")
+    if any(t is not None and t.dtype != torch.float32 for t in (g, gbase, g_low)):
+        raise TypeError("make_cache4: g, gbase and g_low must be float32")
+    for t in (k, v, ks, vs, g, gbase, g_low):
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError("make_cache4 needs contiguous tensors")
+        if not t.is_cuda or t.device != k.device:
+            raise ValueError("make_cache4 needs tensors on one CUDA device")
+    c = Cache4()
+    c.k, c.v, c.ks, c.vs, c.g, c.gbase, c.g_low = k, v, ks, vs, g, gbase, g_low
+    c.device, c.index, c.dtype = k.device, k.device.index, torch.bfloat16  # of the rows that go in and come out
+    c.H, c.Hkv, c.d, c.page_size = H, Hkv, d, S
+    c.params = fox_cache4(pages, S, H, Hkv, d, _ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _ptr(g), _ptr(gbase), _ptr(g_low))
+    c.ref, c.addr = ctypes.byref(c.params), ctypes.addressof(c.params)
+    return c
+
+
+def new_cache4(pages: int, page_size: int, H: int, Hkv: int, d: int, *, device="cuda") -> Cache4:
+    """make_cache4 over newly allocated (uninitialised) tensors, g_low among them."""
+    torch = _torch()
+    byte = lambda *shape: torch.empty(shape, dtype=torch.uint8, device=device)  # noqa: E731
+    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)  # noqa: E731
+    return make_cache4(byte(pages, Hkv, page_size, d // 2), byte(pages, Hkv, page_size, d // 2),
+                       byte(pages, Hkv, page_size, d // 32), byte(pages, Hkv, page_size // 16, 4, d // 32, 4),
+                       f32(pages, H, page_size), f32(pages, H, 2), f32(pages, H, page_size))
+
+
+def fox_cache4_workspace_bytes(cache: Cache4, batch: Batch, rows: int) -> int:
+    return int(lib().fox_cache4_workspace_bytes(cache.ref, batch.ref, int(rows)))
+
+
+def cache4_workspace(cache: Cache4, batch: Batch, rows: int):
+    """A workspace for the calls on a 4-bit cache with `rows` rows of this batch, its header zero."""
+    n = fox_cache4_workspace_bytes(cache, batch, rows)
+    if n == 0:
+        raise FoxError(1, "cache4_workspace")
+    ws = workspace(n, cache.device)
+    ws[:FOX_CACHE_ZERO_BYTES].zero_()
+    return ws
+
+
+def fox_cache4_append(cache: Cache4, batch: Batch, k, v, z, *, q=None, cos=None, sin=None, pairs: bool = False,
+                      q_out=None, ws=None, stream=None):
+    """fox_cache_append into a 4-bit cache; k, v and q bf16. What the cache then holds of a token, fox_cache4_read returns.
+    A magnitude above 430080, an infinity or a NaN in k (rotated) or v is reported (fox_check_error)."""
+    return _append("fox_cache4_append", (_call or _load_call()).append4, None, cache, batch, k, v, z, q, cos, sin, pairs, q_out, ws,
+                   stream)
+
+
+def fox_cache4_decode(cache: Cache4, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
+                      ws=None, stream=None) -> Tuple[object, object]:
+    """fox_decode over a 4-bit cache: q [rows, H, d] bf16 -> (O [rows, H, d], LSE [rows, H] fp32)."""
+    return _decode("fox_cache4_decode", (_call or _load_call()).decode4, cache4_workspace, cache, batch, q, scale, bias_from_j, o, lse,
+                   ws, stream)
+
+
+def fox_cache4_read(cache: Cache4, batch: Batch, rows: Optional[int] = None, *, k=None, v=None, ws=None, stream=None):
+    """The values of the batch's newest tokens as the cache holds them: (K, V) [rows, Hkv, d] bf16. rows: of the batch (may be
+    left out with k or v, whose rows may be strided). Rows that no token of the cache has are left as they are (0 in a K or V
+    that the call makes). ws: as for fox_cache_append."""
+    torch = _torch()
+    where = "fox_cache4_read"
+    index = _cache_call_device(where, cache, batch)
+    if rows is None:
+        if k is None and v is None:
+            raise ValueError(f"{where}: rows, or a k or v that has them")
+        rows = (v if k is None else k).shape[0]
+    make = lambda: torch.zeros((rows, cache.Hkv, cache.d), dtype=torch.bfloat16, device=cache.device)  # noqa: E731
+    k = _alloc_on(stream, make) if k is None else k
+    v = _alloc_on(stream, make) if v is None else v
+    ks = _row_stride(where, "k", k, cache, cache.Hkv, rows, index)
+    vs = _row_stride(where, "v", v, cache, cache.Hkv, rows, index)
+    if ws is None:
+        ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
+    elif ws.get_device() != index:
+        raise ValueError(f"{where}: ws is not on the cache's device")
+    st = lib().fox_cache4_read(cache.ref, batch.ref, rows, k.data_ptr(), ks, v.data_ptr(), vs, ws.data_ptr(), ws.numel(),
+                               _current_stream(index) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise FoxError(st, where)
+    return k, v
+
+
+# ------------------------------------------------------------------------------- pages
+
+
+class Pages:
+    """A pool's pages and the tables that name them, over the caller's tensors (see fox_pages in include/fox.h). Made by
+    make_pages. The contents of its tensors may change between calls; their storage may not."""
+
+    __slots__ = ("refs", "lens", "table", "prefix_table", "params", "ref", "device", "index", "B")
+
+
+def make_pages(page_size: int, refs, lens, table, *, prefix_table=None, prefix_len: int = 0) -> Pages:
+    """A handle on a pool's pages: refs [pages], how many entries name each (0: free); lens [B], table [B, entries] and
+    prefix_table [ceil(prefix_len / page_size)] as in make_batch; contiguous int32 on one CUDA device."""
+    torch = _torch()
+    B = lens.shape[0]
+    if refs.dim() != 1 or lens.dim() != 1 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("make_pages: refs must be [pages], lens [B] and table [B, entries]")
+    if (prefix_table is None) != (int(prefix_len) == 0):
+        raise ValueError("make_pages: prefix_table and prefix_len come together")
+    if prefix_table is not None and (prefix_table.dim() != 1 or prefix_table.shape[0] * page_size < prefix_len):
+        raise ValueError("make_pages: prefix_table must be [ceil(prefix_len / page_size)]")
+    for t in (refs, lens, table, prefix_table):
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise TypeError("make_pages: refs, lens, table and prefix_table must be int32")
+        if not t.is_cuda or t.device != refs.device:
+            raise ValueError("make_pages needs tensors on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("make_pages needs contiguous tensors")
+    x = Pages()
+    x.refs, x.lens, x.table, x.prefix_table = refs, lens, table, prefix_table
+    x.device, x.index, x.B = refs.device, refs.device.index, B
+    x.params = fox_pages(refs.shape[0], int(page_size), B, table.shape[1], int(prefix_len), _ptr(refs), _ptr(lens), _ptr(table),
+                         _ptr(prefix_table))
+    x.ref = ctypes.byref(x.params)
+    return x
+
+
+def pages_workspace(pages: Pages, out: Optional[Pages] = None):
+    """A workspace for fox_pages_step and fox_pages_compact from `pages` to `out` (None: in place), its header zero."""
+    n = int(lib().fox_pages_workspace_bytes(pages.ref, (out or pages).ref))
+    if n == 0:
+        raise FoxError(1, "pages_workspace")
+    ws = workspace(n, pages.device)
+    ws[:FOX_CACHE_ZERO_BYTES].zero_()
+    return ws
+
+
+def _pages_call(where: str, pages: Pages, out: Pages, ws, stream, **ints) -> int:
+    """Checks int32 tensors ({name: (tensor, shape)}), devices and the workspace; returns the device's index."""
+    torch = _torch()
+    index = pages.index
+    if out.device != pages.device:
+        raise ValueError(f"{where}: pages and out are on different devices")
+    if index != _current_device():
+        raise ValueError(f"{where}: the pages are not on the current CUDA device")
+    for name, (t, shape) in ints.items():
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous {list(shape)} int32 on the pages' device")
+    if ws is not None and ws.get_device() != index:
+        raise ValueError(f"{where}: ws is not on the pages' device")
+    return index
+
+
+def fox_pages_step(pages: Pages, add, copies, *, parent=None, out: Optional[Pages] = None, ws=None, stream=None) -> Pages:
+    """One step's bookkeeping: sequence b of `out` goes on from sequence parent[b] of `pages` (-1: from nothing; without parent
+    each from itself) and gets pages for add[b] more tokens; sequences that nobody goes on from leave theirs. copies [B, 2] gets
+    the pages to copy (fox_cache_copy) before anything is appended. Without `out` (only without parent) in place. Returns out.
+    Where the free pages do not reach, a sequence gets none of its add, which its length and the workspace's error word tell.
+    ws: of pages_workspace; without it the report is lost with the call's own."""
+    where = "fox_pages_step"
+    out = pages if out is None else out
+    B = out.B
+    index = _pages_call(where, pages, out, ws, stream, add=(add, (B,)), copies=(copies, (B, 2)), parent=(parent, (B,)))
+    if ws is None:
+        ws = _alloc_on(stream, lambda: pages_workspace(pages, out))
+    st = lib().fox_pages_step(pages.ref, out.ref, _ptr(parent), add.data_ptr(), copies.data_ptr(), ws.data_ptr(), ws.numel(),
+                              _current_stream(index) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise FoxError(st, where)
+    return out
+
+
+def fox_pages_compact(pages: Pages, map, moves, used, *, out: Optional[Pages] = None, ws=None, stream=None) -> Pages:
+    """The pages in use moved to the front of the pool, at most moves.shape[0] of them: moves [n, 2] gets {from, to} (fox_cache_copy
+    takes it; {-1, -1} behind the last), map [pages] every page's new place, used [2] the pages in use and one more than the highest
+    then. refs, table and prefix_table of `out` (None: in place) get the new places. Returns out."""
+    where = "fox_pages_compact"
+    out = pages if out is None else out
+    n = moves.shape[0]
+    index = _pages_call(where, pages, out, ws, stream, map=(map, (pages.params.num_pages,)), moves=(moves, (n, 2)), used=(used, (2,)))
+    if ws is None:
+        ws = _alloc_on(stream, lambda: pages_workspace(pages, out))
+    st = lib().fox_pages_compact(pages.ref, out.ref, map.data_ptr(), moves.data_ptr(), n, used.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 _current_stream(index) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise FoxError(st, where)
+    return out
+
+
+def fox_cache_copy(cache, pairs, *, ws=None, stream=None) -> None:
+    """Copies pages inside a cache (a Cache or a Cache4): for each {from, to} of pairs [n, 2] int32 all that it holds of page `from`
+    to page `to`; {-1, -1} is no pair. No page may be `to` twice, or `to` of one pair and `from` of another. ws: 256 bytes as for
+    fox_cache_append; without it the report of a bad page is lost with the call's own."""
+    torch = _torch()
+    where = "fox_cache_copy"
+    index = cache.index
+    if index != _current_device():
+        raise ValueError(f"{where}: the cache is not on the current CUDA device")
+    if pairs.dim() != 2 or pairs.shape[1] != 2 or pairs.dtype is not torch.int32 or not pairs.is_contiguous() or pairs.get_device() != index:
+        raise ValueError(f"{where}: pairs must be contiguous [n, 2] int32 on the cache's device")
+    if ws is None:
+        ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
+    elif ws.get_device() != index:
+        raise ValueError(f"{where}: ws is not on the cache's device")
+    on = _current_stream(index) if stream is None else stream.cuda_stream
+    if isinstance(cache, Cache4):
+        st = lib().fox_cache4_copy(cache.ref, pairs.data_ptr(), pairs.shape[0], ws.data_ptr(), ws.numel(), on)
+    else:
+        st = lib().fox_cache_copy(cache.ref, _ptr(cache.g_low), pairs.data_ptr(), pairs.shape[0], ws.data_ptr(), ws.numel(), on)
+    if st != 0:
+        raise FoxError(st, where)
 
 
 def fox_check_error(ws, stream=None) -> int:

@@ -114,6 +114,12 @@ Span span(const void* p, int rows, int64_t stride, int64_t elements, int element
 }
 // Whether a call's output lies over something else that the call reads or writes.
 bool overlap(const Span& a, const Span& b) { return a.at < b.at + b.bytes && b.at < a.at + a.bytes; }
+// The same for rows of `row` bytes, `stride` from one to the next in both: they may lie between each other's.
+bool rows_overlap(const Span& a, const Span& b, int64_t stride, int64_t row) {
+  if (!overlap(a, b)) return false;
+  const int64_t r = static_cast<int64_t>((a.at > b.at ? a.at - b.at : b.at - a.at) % static_cast<uint64_t>(stride));
+  return r < row || stride - r < row;
+}
 int element(const fox_cache* c) { return c->dtype == FOX_DTYPE_BF16 ? 2 : 4; }
 
 fox_status check_ws(void* ws, size_t bytes, size_t need) {
@@ -121,29 +127,25 @@ fox_status check_ws(void* ws, size_t bytes, size_t need) {
   return FOX_OK;
 }
 
-}  // namespace
+Held held_by(const fox_cache* c) { return c->dtype == FOX_DTYPE_F32 ? Held::kF32 : Held::kBf16; }
 
-extern "C" {
-
-size_t fox_cache_workspace_bytes(const fox_cache* c, const fox_batch* s, int rows) {
-  PagedArgs a;
-  if (check_cache(c) != FOX_OK || check_batch(c, s, rows, &a) != FOX_OK) return 0;
-  if (a.B == 0 || rows == 0) return kCacheHeaderBytes;
-  if (!decode_fits(a, c->dtype == FOX_DTYPE_F32)) return 0;
-  return decode_workspace_bytes(a, c->dtype == FOX_DTYPE_F32);
+// A 4-bit cache as the bf16 one of its shape, whose rows k, v, q and o have, and its scales.
+fox_cache as_bf16(const fox_cache4* c) {
+  if (!c) return fox_cache{};  // refused, with no pages
+  return {c->num_pages, c->page_size, c->H, c->Hkv, c->d, FOX_DTYPE_BF16, c->k, c->v, c->g, c->gbase};
+}
+struct Four {
+  void* ks;
+  void* vs;
+};
+Four four_of(const fox_cache4* c) { return c ? Four{c->ks, c->vs} : Four{}; }
+fox_status check_four(const Four* f) {
+  return f->ks && f->vs && at16(f->ks) && at16(f->vs) ? FOX_OK : FOX_ERR_INVALID_ARG;
 }
 
-fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
-                            const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
-                            void* workspace, size_t workspace_bytes, void* stream) {
-  return fox_cache_append_low(c, s, rows, k, k_stride, v, v_stride, z, z_stride, rot, nullptr, workspace, workspace_bytes,
-                              stream);
-}
-
-fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
-                                const void* v, int64_t v_stride, const float* z, int64_t z_stride,
-                                const fox_rotary* rot, float* g_low, void* workspace, size_t workspace_bytes,
-                                void* stream) {
+fox_status append_to(const fox_cache* c, const Four* four, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                     const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot, float* g_low,
+                     void* workspace, size_t workspace_bytes, void* stream) {
   fox_status st = check_cache(c);
   if (st != FOX_OK) return st;
   CacheAppendArgs x = {};
@@ -155,10 +157,11 @@ fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows
   }
   if (s->B == 0 || rows == 0) return FOX_OK;
   st = check_pointers(c, s);
+  if (st == FOX_OK && four) st = check_four(four);
   if (st != FOX_OK) return st;
   if (!row_ok(k, k_stride, c->Hkv, c, rows) || !row_ok(v, v_stride, c->Hkv, c, rows)) return FOX_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(g_low) & 3u) return FOX_ERR_INVALID_ARG;
-  if (!append_fits(x.a, rot && rot->q, c->dtype == FOX_DTYPE_F32)) return FOX_ERR_UNSUPPORTED;
+  if (four ? !append4_fits(x.a, rot && rot->q) : !append_fits(x.a, rot && rot->q, c->dtype == FOX_DTYPE_F32)) return FOX_ERR_UNSUPPORTED;
   if (!z || (reinterpret_cast<uintptr_t>(z) & 3u) || (rows > 1 && (z_stride < c->H || z_stride >= (1LL << 40))))
     return FOX_ERR_INVALID_ARG;
   if (rot) {
@@ -194,13 +197,14 @@ fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows
   x.v_stride = v_stride;
   x.z_stride = z_stride;
   x.g_low = g_low;
-  return launch_cache_append(x, c->dtype == FOX_DTYPE_F32, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FOX_OK
-             : FOX_ERR_CUDA;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = four ? launch_cache_append4(x, four->ks, four->vs, on) : launch_cache_append(x, c->dtype == FOX_DTYPE_F32, on);
+  return e == cudaSuccess ? FOX_OK : FOX_ERR_CUDA;
 }
 
-fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
-                      int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+fox_status decode_over(const fox_cache* c, const Four* four, const fox_batch* s, int rows, const void* q, int64_t q_stride,
+                       float scale, int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream) {
   fox_status st = check_cache(c);
   if (st != FOX_OK) return st;
   DecodeArgs x = {};
@@ -210,12 +214,13 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
   if (bias_from_j != 0 && bias_from_j != 1) return FOX_ERR_INVALID_ARG;
   if (s->B == 0 || rows == 0) return FOX_OK;
   st = check_pointers(c, s);
+  if (st == FOX_OK && four) st = check_four(four);
   if (st != FOX_OK) return st;
   if (!row_ok(q, q_stride, c->H, c, rows) || !o || !at16(o) || !lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return FOX_ERR_INVALID_ARG;
-  const bool f32 = c->dtype == FOX_DTYPE_F32;
-  if (!decode_fits(x.a, f32)) return FOX_ERR_UNSUPPORTED;
-  st = check_ws(workspace, workspace_bytes, decode_workspace_bytes(x.a, f32));
+  const Held held = four ? Held::kFour : held_by(c);
+  if (!decode_fits(x.a, held)) return FOX_ERR_UNSUPPORTED;
+  st = check_ws(workspace, workspace_bytes, decode_workspace_bytes(x.a, held));
   if (st != FOX_OK) return st;
   const int64_t row = (int64_t)c->H * c->d;
   const Span so = span(o, rows, row, row, element(c)), sl = span(lse, rows, c->H, c->H, 4);
@@ -228,9 +233,136 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
   x.bias_from_j = bias_from_j;
   x.o = o;
   x.lse = lse;
-  return launch_decode(x, f32, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)) == cudaSuccess
+  x.ks = four ? four->ks : nullptr;
+  x.vs = four ? four->vs : nullptr;
+  return launch_decode(x, held, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FOX_OK
              : FOX_ERR_CUDA;
+}
+
+fox_status copy_in(const fox_cache* c, const Four* four, float* g_low, const int32_t* pairs, int n, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  fox_status st = check_cache(c);
+  if (st != FOX_OK) return st;
+  if (n < 0) return FOX_ERR_INVALID_ARG;
+  if (n == 0) return FOX_OK;
+  if (!c->k || !c->v || !c->g || !c->gbase || !at16(c->k) || !at16(c->v) || !at16(c->g) || !at16(c->gbase) || !at16(g_low))
+    return FOX_ERR_INVALID_ARG;
+  if (four && (st = check_four(four)) != FOX_OK) return st;
+  if (!pairs || (reinterpret_cast<uintptr_t>(pairs) & 7u)) return FOX_ERR_INVALID_ARG;
+  const long long tokens = (long long)c->Hkv * c->page_size, row = four ? c->d / 2 : (long long)c->d * element(c);
+  PageArrays x = {};
+  x.add(c->k, tokens * row);
+  x.add(c->v, tokens * row);
+  if (four) {
+    x.add(four->ks, tokens * (c->d / 32));
+    x.add(four->vs, tokens * (c->d / 32));
+  }
+  x.add(c->g, (long long)c->H * c->page_size * 4);
+  x.add(g_low, (long long)c->H * c->page_size * 4);
+  x.add(c->gbase, (long long)c->H * 8);
+  if (!pages_copy_fits(x, n)) return FOX_ERR_UNSUPPORTED;
+  st = check_ws(workspace, workspace_bytes, kErrWordBytes);
+  if (st != FOX_OK) return st;
+  return launch_pages_copy(x, c->num_pages, pairs, n, static_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? FOX_OK
+             : FOX_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fox_cache_workspace_bytes(const fox_cache* c, const fox_batch* s, int rows) {
+  PagedArgs a;
+  if (check_cache(c) != FOX_OK || check_batch(c, s, rows, &a) != FOX_OK) return 0;
+  if (a.B == 0 || rows == 0) return kCacheHeaderBytes;
+  if (!decode_fits(a, held_by(c))) return 0;
+  return decode_workspace_bytes(a, held_by(c));
+}
+
+fox_status fox_cache_append(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  return fox_cache_append_low(c, s, rows, k, k_stride, v, v_stride, z, z_stride, rot, nullptr, workspace, workspace_bytes,
+                              stream);
+}
+
+fox_status fox_cache_append_low(const fox_cache* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const float* z, int64_t z_stride,
+                                const fox_rotary* rot, float* g_low, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  return append_to(c, nullptr, s, rows, k, k_stride, v, v_stride, z, z_stride, rot, g_low, workspace, workspace_bytes, stream);
+}
+
+fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
+                      int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_over(c, nullptr, s, rows, q, q_stride, scale, bias_from_j, o, lse, workspace, workspace_bytes, stream);
+}
+
+size_t fox_cache4_workspace_bytes(const fox_cache4* c, const fox_batch* s, int rows) {
+  PagedArgs a;
+  const fox_cache as = as_bf16(c);
+  if (check_cache(&as) != FOX_OK || check_batch(&as, s, rows, &a) != FOX_OK) return 0;
+  if (a.B == 0 || rows == 0) return kCacheHeaderBytes;
+  return decode_fits(a, Held::kFour) ? decode_workspace_bytes(a, Held::kFour) : 0;
+}
+
+fox_status fox_cache4_append(const fox_cache4* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  const fox_cache as = as_bf16(c);
+  const Four four = four_of(c);
+  return append_to(&as, &four, s, rows, k, k_stride, v, v_stride, z, z_stride, rot, c ? c->g_low : nullptr, workspace,
+                   workspace_bytes, stream);
+}
+
+fox_status fox_cache4_decode(const fox_cache4* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
+                             int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const fox_cache as = as_bf16(c);
+  const Four four = four_of(c);
+  return decode_over(&as, &four, s, rows, q, q_stride, scale, bias_from_j, o, lse, workspace, workspace_bytes, stream);
+}
+
+fox_status fox_cache4_read(const fox_cache4* c, const fox_batch* s, int rows, void* k, int64_t k_stride, void* v,
+                           int64_t v_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  const fox_cache as = as_bf16(c);
+  const Four four = four_of(c);
+  fox_status st = check_cache(&as);
+  if (st != FOX_OK) return st;
+  CacheAppendArgs x = {};
+  st = check_batch(&as, s, rows, &x.a);
+  if (st != FOX_OK) return st;
+  if (s->B == 0 || rows == 0) return FOX_OK;
+  st = check_pointers(&as, s);
+  if (st == FOX_OK) st = check_four(&four);
+  if (st != FOX_OK) return st;
+  if (!row_ok(k, k_stride, c->Hkv, &as, rows) || !row_ok(v, v_stride, c->Hkv, &as, rows)) return FOX_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)c->Hkv * c->d;
+  const Span sk = span(k, rows, k_stride, row, 2), sv = span(v, rows, v_stride, row, 2);
+  if (rows > 1 && k_stride == v_stride ? rows_overlap(sk, sv, 2 * k_stride, 2 * row) : overlap(sk, sv)) return FOX_ERR_INVALID_ARG;
+  if (!append4_fits(x.a, false)) return FOX_ERR_UNSUPPORTED;
+  st = check_ws(workspace, workspace_bytes, kErrWordBytes);
+  if (st != FOX_OK) return st;
+  x.a.err = static_cast<uint32_t*>(workspace);
+  x.k = k;
+  x.v = v;
+  x.k_stride = k_stride;
+  x.v_stride = v_stride;
+  return launch_cache_read4(x, four.ks, four.vs, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FOX_OK : FOX_ERR_CUDA;
+}
+
+fox_status fox_cache_copy(const fox_cache* c, float* g_low, const int32_t* pairs, int n, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  return copy_in(c, nullptr, g_low, pairs, n, workspace, workspace_bytes, stream);
+}
+
+fox_status fox_cache4_copy(const fox_cache4* c, const int32_t* pairs, int n, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const fox_cache as = as_bf16(c);
+  const Four four = four_of(c);
+  return copy_in(&as, &four, c ? c->g_low : nullptr, pairs, n, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

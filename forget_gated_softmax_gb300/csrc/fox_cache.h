@@ -38,10 +38,32 @@ struct DecodeArgs {
   int bias_from_j;
   void* o;
   float* lse;
+  const void* ks;  // scales of a 4-bit cache
+  const void* vs;
 };
-bool decode_fits(const PagedArgs& a, bool f32);  // its work is counted in ints
-size_t decode_workspace_bytes(const PagedArgs& a, bool f32);
-cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t s);
+enum class Held { kBf16, kF32, kFour };  // what a cache holds K and V in
+bool decode_fits(const PagedArgs& a, Held held);  // its work is counted in ints
+size_t decode_workspace_bytes(const PagedArgs& a, Held held);
+cudaError_t launch_decode(const DecodeArgs& x, Held held, char* ws, cudaStream_t s);
+// The 4-bit cache: appending, and reading back (to x.k and x.v).
+bool append4_fits(const PagedArgs& a, bool with_q);
+cudaError_t launch_cache_append4(const CacheAppendArgs& x, void* ks, void* vs, cudaStream_t s);
+cudaError_t launch_cache_read4(const CacheAppendArgs& x, void* ks, void* vs, cudaStream_t s);
+
+// Arrays of a pool and the bytes of a page in each: multiples of 16 (of 8 where the base is no more aligned).
+struct PageArrays {
+  static constexpr int kMost = 7;
+  char* at[kMost];
+  long long bytes[kMost];
+  int n;
+  void add(void* p, long long page_bytes) {
+    if (!p) return;
+    at[n] = static_cast<char*>(p);
+    bytes[n++] = page_bytes;
+  }
+};
+bool pages_copy_fits(const PageArrays& x, int n);  // its blocks are one grid's
+cudaError_t launch_pages_copy(const PageArrays& x, int num_pages, const int32_t* pairs, int n, uint32_t* err, cudaStream_t s);
 
 // 4-D bf16 tensor map over a paged pool [pages, Hkv, page_size, d], box 64 channels x box_rows tokens, 128-byte swizzle.
 bool make_page_map(CUtensorMap* map, const void* base, int d, int page_size, int Hkv, int pages, int box_rows);

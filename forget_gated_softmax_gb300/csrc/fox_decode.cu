@@ -167,16 +167,17 @@ bool share_prefix(const PagedArgs& a, int row_tiles) {
   return (long long)a.B * row_tiles * a.prefix_len * a.Hkv * a.d * 4 > (72ll << 20);
 }
 
-DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
+DecodeLayout decode_layout(const PagedArgs& a, Held held) {
+  const bool f32 = held == Held::kF32, four = held == Held::kFour;
   DecodeLayout L;
   const int G = a.H / a.Hkv;
-  L.Rt = f32 ? decode_f32_rows(a.max_new * G) : decode_mma_rows(a.max_new * G);
+  L.Rt = f32 ? decode_f32_rows(a.max_new * G) : four ? decode4_rows(a.max_new * G) : decode_mma_rows(a.max_new * G);
   L.Gp = padded_group(G, L.Rt);
   const int most = a.max_new * L.Gp;
   L.Rs = most < L.Rt ? most : L.Rt;
   const int row_tiles = ceil_div(most, L.Rt);  // of a sequence
   L.num = numbering(a, L.Gp, L.Rt == 1 ? 0 : L.Rt == 4 ? 2 : L.Rt == 8 ? 3 : 4, row_tiles, &L.items);
-  L.warps = f32 ? kF32Warps : decode_mma_warps(a.d);
+  L.warps = f32 ? kF32Warps : four ? decode4_warps(a.d, L.Rt) : decode_mma_warps(a.d);
   L.workers = (f32 ? f32_ctas(a.d) : kSMs) * L.warps;
   const size_t slots = (size_t)L.workers + (size_t)a.Hkv * L.items;
   L.cum = kCacheHeaderBytes;
@@ -186,7 +187,7 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
   L.pml = align_up(L.po + sizeof(float) * slots * L.Rs * a.d, 256);
   L.ppo = L.end = L.pml;
   L.pre = PrefixPlan{};
-  if (!f32 && a.prefix_len > 0 && share_prefix(a, row_tiles)) {
+  if (held == Held::kBf16 && a.prefix_len > 0 && share_prefix(a, row_tiles)) {
     L.pre = prefix_plan(a);
     const size_t rows = ((size_t)L.pre.workers + (size_t)a.Hkv * L.pre.items) * 2 * kTile;
     L.ppo = align_up(L.pml + sizeof(float2) * rows, 256);
@@ -197,17 +198,17 @@ DecodeLayout decode_layout(const PagedArgs& a, bool f32) {
 
 }  // namespace
 
-bool decode_fits(const PagedArgs& a, bool f32) {
-  const DecodeLayout L = decode_layout(a, f32);
+bool decode_fits(const PagedArgs& a, Held held) {
+  const DecodeLayout L = decode_layout(a, held);
   return line_fits(most_units(a, L.items), L.workers, L.warps) &&
          (unsigned long long)a.max_new * L.Gp * L.Gp < (1ull << 32) && L.po_rows < 0x7fffffffLL &&
          (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.line < 0x7fffffffLL - L.pre.each);
 }
 
-size_t decode_workspace_bytes(const PagedArgs& a, bool f32) { return decode_layout(a, f32).end; }
+size_t decode_workspace_bytes(const PagedArgs& a, Held held) { return decode_layout(a, held).end; }
 
-cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t s) {
-  const DecodeLayout L = decode_layout(x.a, f32);
+cudaError_t launch_decode(const DecodeArgs& x, Held held, char* ws, cudaStream_t s) {
+  const DecodeLayout L = decode_layout(x.a, held);
   DecodeParams p = {};
   p.a = x.a;
   p.q = x.q;
@@ -217,6 +218,8 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   p.walk_prefix = x.a.prefix_len > 0 && L.pre.key_tiles == 0;
   p.o = x.o;
   p.lse = x.lse;
+  p.ks = static_cast<const uint8_t*>(x.ks);
+  p.vs = static_cast<const uint8_t*>(x.vs);
   p.Rt = L.Rt;
   p.Rs = L.Rs;
   p.num = L.num;
@@ -234,8 +237,8 @@ cudaError_t launch_decode(const DecodeArgs& x, bool f32, char* ws, cudaStream_t 
   static_assert(kErrWordBytes + 4 * 2 * kSMs <= kCacheHeaderBytes, "a counter a CTA");
   const cudaError_t e = p.pre.key_tiles > 0 ? launch_prefix(p, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  if (f32) return launch_decode_f32(p, s);
-  const cudaError_t f = launch_decode_mma(p, s);
+  if (held == Held::kF32) return launch_decode_f32(p, s);
+  const cudaError_t f = held == Held::kFour ? launch_decode4(p, s) : launch_decode_mma(p, s);
   if (f != cudaSuccess || p.pre.key_tiles == 0) return f;
   return x.a.d == 64 ? launch_merge<64>(p, s) : launch_merge<128>(p, s);
 }

@@ -32,6 +32,8 @@ struct DecodeParams {
   int walk_prefix;     // the items walk the prefix's keys themselves (nothing shares it out)
   void* o;
   float* lse;
+  const uint8_t* ks;   // scales of a 4-bit cache
+  const uint8_t* vs;
   // Own items
   int Rt, Rs;          // rows of a row tile; rows kept of a slot
   Numbering num;       // of the items
@@ -526,6 +528,10 @@ constexpr int kF32Warps = 4;
 // calls on few SMs).
 constexpr int f32_ctas(int d) { return d == 128 ? kSMs : 2 * kSMs; }
 cudaError_t launch_decode_f32(const DecodeParams& p, cudaStream_t s);
+// The kernel of the 4-bit cache (fox_decode4.cu), as the bf16 one's.
+int decode4_rows(int rows);
+int decode4_warps(int d, int Rt);
+cudaError_t launch_decode4(const DecodeParams& p, cudaStream_t s);
 PrefixPlan prefix_plan(const PagedArgs& a);
 cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s);
 

@@ -365,6 +365,129 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
                       int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---- The cache in 4 bits ----
+ *
+ * The same cache with K and V in blocks of 32 channels of one token and key head, 4.25 bits a value:
+ *   value = s u, u = -7 .. 7; s: the smallest number of 5 exponent bits (bias 15) and 3 mantissa bits, 0 .. 61440, with
+ *   7 s >= the block's largest magnitude; u: value / s rounded to the nearest, halves away from zero.
+ * A nibble holds u + 8, a scale is one byte (its bits are those of an fp16 from bit 14 on). s u has 7 significant bits, so
+ * bf16 and fp16 hold it as it is (fp16 up to 65504).
+ *   k   [num_pages, Hkv, page_size, d / 2]   32-bit words [4][d / 32] a token: word [t][b] has channels 32 b + 8 t + 0 .. 7,
+ *                                            their nibbles from the lowest in the order 7 2 0 4 6 3 1 5, the word then rotated right by 2
+ *   ks  [num_pages, Hkv, page_size, d / 32]  its scales
+ *   v   [num_pages, Hkv, page_size, d / 2]   16 bytes a block, two channels a byte, the even one low; block b of slot s at
+ *                                            place b ^ (s / 2 % 4), with d = 64 b ^ (s / 4 % 2)
+ *   vs  [num_pages, Hkv, page_size / 16, 4, d / 32, 4]  its scales, token j of 16 at [j % 8 / 2][b][2 (j % 2) + j / 8]
+ *   g, gbase as in fox_cache; g_low as in fox_cache_append_low, or NULL.
+ * Types of k, v and q, and of o: bf16. A magnitude above 430080, an infinity or a NaN sets the error word when it is
+ * appended and is held as the nearest the block has (a NaN as 0): what was appended is always finite. Nothing has to be initialised.
+ */
+typedef struct fox_cache4 {
+  int num_pages; /* as in fox_cache, with the same limits */
+  int page_size;
+  int H;
+  int Hkv;
+  int d;
+  void* k;       /* 16-byte aligned, as the others but g_low (4) */
+  void* v;
+  void* ks;
+  void* vs;
+  float* g;
+  float* gbase;
+  float* g_low;
+} fox_cache4;
+
+/*
+ * Workspace of the three calls below for these arguments, with fox_cache_workspace_bytes' rules; fox_cache4_append and
+ * fox_cache4_read use its first 256 bytes alone, and take no more.
+ */
+size_t fox_cache4_workspace_bytes(const fox_cache4* c, const fox_batch* s, int rows);
+
+/*
+ * fox_cache_append into a 4-bit cache. K is first rotated where rot is given, and then rounded to bf16: to the nearest of the
+ * exact a cos - b sin, so that what the cache holds follows from the inputs bit for bit (q_out the same).
+ */
+fox_status fox_cache4_append(const fox_cache4* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fox_decode over a 4-bit cache, with its arguments and results. The weights pass through fp16, at up to 2^11 times their
+ * value against the running maximum; a shared prefix is shared as there (above the same threshold), its pages spread out to bf16 in the
+ * workspace on the way.
+ */
+fox_status fox_cache4_decode(const fox_cache4* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
+                             int bias_from_j, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The values of the batch's newest tokens out of the cache, as bf16, exactly: rows of [Hkv, d] to k and v, strides as in
+ * fox_cache_append, neither over the other. With cu_new the running sum of lens (and no prefix) that is every sequence whole: for
+ * dense attention of many new tokens, or on the way to another cache. Rows of idle sequences, of tokens whose page is none of the
+ * pool (reported), and behind the last sequence are left as they are.
+ */
+fox_status fox_cache4_read(const fox_cache4* c, const fox_batch* s, int rows, void* k, int64_t k_stride, void* v,
+                           int64_t v_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Pages: handed out, shared, freed, moved ----
+ *
+ * Tables as in fox_batch, for every layer's cache at once, and how many entries name each page. All arrays are device memory and
+ * read when the work runs, so that these calls too can be captured and replayed; none waits for the device.
+ */
+typedef struct fox_pages {
+  int num_pages;         /* of the pool, 1 .. 2^24 */
+  int page_size;         /* 16, 32, 64 or 128 */
+  int B;                 /* sequences, 0 .. 2048 */
+  int table_stride;      /* entries of a sequence's row of `table`, >= 1 */
+  int prefix_len;        /* tokens of a prefix that all share, as in fox_batch; the entries of prefix_table count in refs */
+  int32_t* refs;         /* [num_pages] entries that name the page; 0 (or less): free */
+  int32_t* lens;         /* [B] tokens, the prefix among them; 0: idle, and without pages */
+  int32_t* table;        /* [B, table_stride] */
+  int32_t* prefix_table; /* [ceil(prefix_len / page_size)], or NULL with prefix_len 0 */
+} fox_pages;
+
+/* Workspace of fox_pages_step and fox_pages_compact from `in` to `out` (0 if they are invalid); rules as for the cache's. */
+size_t fox_pages_workspace_bytes(const fox_pages* in, const fox_pages* out);
+
+/*
+ * One step's bookkeeping. New sequence b (of out->B) goes on where old sequence parent[b] stands, or begins empty with -1, and
+ * gets room for add[b] >= 0 more tokens. So an old sequence that nobody names ends and leaves its pages, one that several name
+ * branches, and with add 0 and -1 a place is idle. Without parent (NULL) every sequence goes on by itself (out->B = in->B).
+ *   refs   of an old sequence's pages change by its children less one;
+ *   then, by rising b: pages that b still needs are the lowest free ones, and where its last page is partly filled and somebody
+ *   else still names it, it gets a page of its own first: copies[b] = {that page, the new one}, to be copied
+ *   (fox_cache_copy, for each layer) before the append; else {-1, -1}.
+ *   lens   becomes parent's + add (prefix_len + add for one that begins); entries of `table` up to there are written, no others.
+ * Where the free pages do not reach for b (or its row of the table does not), the error word is set and b gets none of its add:
+ * lens says so. b with enough of them is one that, with what all before it asked for, stays within the free pages.
+ * in and out: other arrays, or, without parent, the same ones (the step is then done in place). num_pages, page_size, table_stride
+ * and prefix_len have to agree. A parent or length outside its range is reported and counts as -1 or idle, a page outside the pool is
+ * reported and left out of refs. Integers all, in a fixed order: the same arguments give the same result.
+ */
+fox_status fox_pages_step(const fox_pages* in, const fox_pages* out, const int32_t* parent, const int32_t* add,
+                          int32_t* copies, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The U pages in use moved to the front: of those at U and behind, the highest goes to the lowest free page, the next highest to the
+ * next, and so on, at most max_moves of them. moves [max_moves, 2] gets {from, to} pairs in this order, {-1, -1} behind them, for
+ * fox_cache_copy (of each layer, before anything else is appended or read); map [num_pages] every page's new place (its own where
+ * it stays), for other tables than in's; used: {U, one more than the highest page then in use}. out->refs, out->table (the entries of
+ * in->lens' tokens, no others) and out->prefix_table get the new places; out->lens is not written. in and out: other arrays, or the same.
+ */
+fox_status fox_pages_compact(const fox_pages* in, const fox_pages* out, int32_t* map, int32_t* moves, int max_moves,
+                             int32_t* used, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Copies whole pages inside a cache: for each of n pairs {from, to} all that the cache holds of page `from` (K, V, gates, g_low
+ * where given) to page `to`. {-1, -1} is no pair; other ids outside the pool are reported, and skipped. No page may be `to` of two pairs,
+ * or `to` of one and `from` of another. pairs: device memory, 8-byte aligned; g_low 16-byte aligned. Workspace: 256 bytes (the error word).
+ */
+fox_status fox_cache_copy(const fox_cache* c, float* g_low, const int32_t* pairs, int n, void* workspace,
+                          size_t workspace_bytes, void* stream);
+fox_status fox_cache4_copy(const fox_cache4* c, const int32_t* pairs, int n, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
  * Forward without a caller-provided workspace, for callers that cannot
  * allocate device memory where they run this code (a plugin in a host
  * application that owns all device memory, a latency-bound loop that cannot
