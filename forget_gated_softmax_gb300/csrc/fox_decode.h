@@ -312,15 +312,15 @@ struct Kept {
   float m[kWarps][kRows], l[kWarps][kRows];  // of the warp's latest segment
 };
 
-// A finished segment's rows (rows + r * pitch, floats of shared memory) by one warp: to O where the worker
+// A finished segment's rows (rows + r * pitch, floats of shared memory), of these r0 to r1 - 1, by one warp: to O where the worker
 // had the whole item, else to its slot.
 template <typename T, int D>
 __device__ __forceinline__ void leave_rows(const DecodeParams& p, const Place& at, int worker, bool whole, const float* rows,
-                                           int pitch, const float* m, const float* l) {
+                                           int pitch, const float* m, const float* l, int r0 = 0, int r1 = 1 << 16) {
   constexpr int C4 = D / 4;
-  const int lane = threadIdx.x & 31, slot = slot_of(p, worker, at), F = rows_of(p, at) * C4;
+  const int lane = threadIdx.x & 31, slot = slot_of(p, worker, at), F = min(rows_of(p, at), r1) * C4;
 #pragma unroll 1
-  for (int f = lane; f < F; f += 32) {
+  for (int f = r0 * C4 + lane; f < F; f += 32) {
     const int r = f / C4, c4 = f % C4;
     const float4 v = *reinterpret_cast<const float4*>(rows + r * pitch + c4 * 4);
     if (whole) {
