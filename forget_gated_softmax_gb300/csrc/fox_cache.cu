@@ -137,9 +137,13 @@ fox_cache as_bf16(const fox_cache4* c) {
 struct Four {
   void* ks;
   void* vs;
+  bool counted;  // the kernels count a head's tokens through the pool in 32 bits
 };
-Four four_of(const fox_cache4* c) { return c ? Four{c->ks, c->vs} : Four{}; }
+Four four_of(const fox_cache4* c) {
+  return c ? Four{c->ks, c->vs, (long long)c->num_pages * c->page_size * c->Hkv < (1LL << 32)} : Four{};
+}
 fox_status check_four(const Four* f) {
+  if (!f->counted) return FOX_ERR_UNSUPPORTED;
   return f->ks && f->vs && at16(f->ks) && at16(f->vs) ? FOX_OK : FOX_ERR_INVALID_ARG;
 }
 

@@ -177,7 +177,7 @@ DecodeLayout decode_layout(const PagedArgs& a, Held held) {
   L.Rs = most < L.Rt ? most : L.Rt;
   const int row_tiles = ceil_div(most, L.Rt);  // of a sequence
   L.num = numbering(a, L.Gp, L.Rt == 1 ? 0 : L.Rt == 4 ? 2 : L.Rt == 8 ? 3 : 4, row_tiles, &L.items);
-  L.warps = f32 ? kF32Warps : four ? decode4_warps(a.d, L.Rt) : decode_mma_warps(a.d);
+  L.warps = f32 ? kF32Warps : four ? decode4_warps(a, L.Rt) : decode_mma_warps(a.d);
   L.workers = (f32 ? f32_ctas(a.d) : kSMs) * L.warps;
   const size_t slots = (size_t)L.workers + (size_t)a.Hkv * L.items;
   L.cum = kCacheHeaderBytes;

@@ -373,13 +373,14 @@ __device__ __forceinline__ void find_ends(const DecodeParams& p, const SeqEntry*
 }
 
 // By the whole block, at its end. Row r of warp w's kept segment lies at rows + w * warp_pitch + r * row_pitch
-// (floats). `offs`: [CTAs + 1] and `part`: [threads] of shared memory, clear of the kept rows.
+// (floats). `offs`: [CTAs + 1] and `part`: [threads] of shared memory, clear of the kept rows. kMoreWarps: of the block, that
+// are no workers.
 // With a shared prefix every item is left to the merge that follows, its partial results as above.
-template <typename T, int D, int kRows, int kWarps>
+template <typename T, int D, int kRows, int kWarps, int kMoreWarps = 0>
 __device__ __forceinline__ void join_items(const DecodeParams& p, const SeqEntry* seqs, int total, int each,
                                            const Kept<kRows, kWarps>& kept, const BlockEnds& ends, const float* rows, int warp_pitch,
                                            int row_pitch, int* offs, Column* part) {
-  constexpr int kThreads = 32 * kWarps, C4 = D / 4;
+  constexpr int kThreads = 32 * (kWarps + kMoreWarps), C4 = D / 4;
   __shared__ int results[2];
   const int tid = threadIdx.x, cta = blockIdx.x, w_cta = cta * kWarps;
   const bool shared = p.pre.key_tiles > 0;
@@ -530,7 +531,7 @@ constexpr int f32_ctas(int d) { return d == 128 ? kSMs : 2 * kSMs; }
 cudaError_t launch_decode_f32(const DecodeParams& p, cudaStream_t s);
 // The kernel of the 4-bit cache (fox_decode4.cu), as the bf16 one's.
 int decode4_rows(int rows);
-int decode4_warps(int d, int Rt);
+int decode4_warps(const PagedArgs& a, int Rt);
 cudaError_t launch_decode4(const DecodeParams& p, cudaStream_t s);
 PrefixPlan prefix_plan(const PagedArgs& a);
 cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s);

@@ -37,7 +37,7 @@ inline MmaShape mma_shape(const PagedArgs& a, int rows) {
   x.gstage = subs * x.gsub + (subs * x.heads * 8 + 127) / 128 * 128;
   return x;
 }
-constexpr int most_gates(int rows) { return 2 * ((rows * 20 * 4 + 127) / 128 * 128) + 256; }  // gstage at most
+constexpr int most_gates(int rows) { return 2 * ((rows * 20 * 4 + 127) / 128 * 128) + rows * 16; }  // gstage at most
 
 // Up to 32 successive key tiles of one item. The table's entries for them (with pages of 16 tokens two a
 // tile) come to shared memory by asynchronous copies, so that no instruction waits for them before their use.

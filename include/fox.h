@@ -383,7 +383,7 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
  * appended and is held as the nearest the block has (a NaN as 0): what was appended is always finite. Nothing has to be initialised.
  */
 typedef struct fox_cache4 {
-  int num_pages; /* as in fox_cache, with the same limits */
+  int num_pages; /* as in fox_cache, with the same limits; num_pages * page_size * Hkv below 2^32 */
   int page_size;
   int H;
   int Hkv;

@@ -59,6 +59,12 @@ def test_bad_caches_are_refused(L, kw, status):
         assert call(L, _cache(**kw)) == status
 
 
+def test_more_tokens_of_a_head_than_32_bits_count_are_refused(L):
+    for call in (_decode, _append, _read, _copy):
+        assert call(L, _cache(num_pages=1 << 26, page_size=64, Hkv=1)) == 2
+        assert call(L, _cache(num_pages=(1 << 26) - 1, page_size=64, Hkv=1), ws=None) == 3  # on to the next check
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(B=-1), 1), (dict(B=2049), 2), (dict(table_stride=0), 1), (dict(prefix_len=-1), 1), (dict(prefix_len=5), 1), (dict(lens=None), 1),
     (dict(lens=FAKE + 2), 1), (dict(table=None), 1), (dict(cu_new=FAKE, max_new=0), 1), (dict(cu_new=FAKE + 1), 1),
