@@ -6,16 +6,19 @@
 //
 // K. A lane's part of an MMA operand (a token's channels 8 t .. 8 t + 7 of every block) lies side by side. A nibble u + 8 = n at bits 9..6
 //   of an fp16 of exponent 0 is 1 + n / 16, at bits 5..2 it is 1 + n / 256: two masks on the word and two on the word rotated by 8 make
-//   the eight values of two MMA steps. With q' = 16 q and 256 q in their places the products sum to sum q u plus sums of q alone,
-//   which are taken off (one a block and row). So a block costs 5 instructions and no subtraction of its own, and fp32 sums keep
-//   2^-24 of 264 sum |q|. The block's scale multiplies its sum.
+//   the eight values of two MMA steps. With q' = 16 q and 256 q in their places the products sum to sum q u plus sums of q alone (one a
+//   block and row), whose products with the scales one more MMA takes off: scales as they are, the sums in three fp16. So a block costs 5
+//   instructions a word and no subtraction of its own, and fp32 sums keep 2^-24 of 264 sum |q|. The block's scale multiplies its sum.
 // V. ldmatrix.trans turns 16-bit units (four channels of a token) so that a register has the same four channels of two
 //   neighbouring tokens: what the V^T operand wants, nibble by nibble. The masks give 1 + n / 1024 and 1 + n / 64, an fma n - 8, exactly.
 //   The scales, which vary along the sum, go to P: P s in fp16 (P and s in fp16, so rounded twice by 2^-12), once a block of 32 channels.
 // Weights are P = 2^(x - r), with r = the running maximum less `lift`: as fp16 holds 2^15 down to 2^-24, weights down to
 //   2^-24 of the largest keep all bits at lift 10. lift falls where scales of 2 and above are met, so that P s stays below 2^15 too;
 //   r moves when a weight passes 2^(lift + 4), or a scale its bound, which one vote finds: the weights are then formed again.
-// q in fp16: each row times a power of two so that its largest |q| is in [32, 64); what a bf16 holds is then exact down to 2^-24 of that.
+// q in fp16: each row times a power of two so that its largest |q| is in [4, 8); what a bf16 holds is then exact down to 2^-21 of that,
+//   and off by 2^-32 of it at most.
+// Up to four rows a tile (kRows 4) stand twice among the eight columns, so that scores and weights of half the keys fall to each half of the
+//   lanes: columns 0..3 then sum the first 16 keys of a tile, columns 4..7 the others, and are added at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,10 +33,10 @@ constexpr int kRoom = 4;  // log2 units that a score may pass the running maximu
 // A weight of the running maximum is 2^lift; top_e: the largest exponent bits of a scale of V, 15 (scales below 2) at least.
 __device__ __forceinline__ int lift_of(int top_e) { return 25 - top_e; }
 
-template <int D, int NT>
+template <int D, int kRows_>  // rows of a row tile: 4, 8 or 16
 struct Layout4 {
   static constexpr int kStages = 2;
-  static constexpr int kRows = 8 * NT;
+  static constexpr int kRows = kRows_;
   static constexpr int kBlocks = D / kFourBlock;
   static constexpr int kTileBytes = kKeyTile * D / 2;          // codes of K or V of a stage
   static constexpr int kScaleBytes = kKeyTile * kBlocks;       // scales of K or V of a stage
@@ -43,7 +46,7 @@ struct Layout4 {
   static constexpr int kQPitch = D * 2 + 16;                     // bytes from one query row to the next
   static constexpr int kQBytes = kRows * kQPitch;
   static constexpr int kOutStride = D + 4;
-  static_assert(8 * kOutStride * 4 <= kStageBytes, "eight rows pass through a stage that was read");
+  static_assert((kRows < 8 ? kRows : 8) * kOutStride * 4 <= kStageBytes, "eight rows pass through a stage that was read");
   static_assert(kRows * kOutStride * 4 <= kStages * kStageBytes, "rows are kept in a ring that was read");
 };
 
@@ -90,17 +93,20 @@ struct RowGates {
   float g[kRows];
 };
 
-// 16 bytes on their way to shared memory: `size` of them (16 or 0) from src, zeros for the others.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int size, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(size), "l"(policy)
+// 16 bytes on their way to shared memory, or zeros where there are none to copy (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void copy16_or_0(uint32_t dst, const void* src, bool copy, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0), "l"(policy)
                : "memory");
 }
 
 // What a warp has on its way: the copies of its worker's key tiles, in the order of the line, `kStages` ahead of their use. Pages are
 // looked up for up to 32 tiles of an item at a time, a lane a tile, one such window ahead.
-template <int D, int NT>
+template <int D, int kRows>
 struct Loader {
-  using L = Layout4<D, NT>;
+  using L = Layout4<D, kRows>;
   static constexpr int NB = L::kBlocks, RowB = D / 2;
   Place pro;                 // behind the last window's last tile
   Window now, next;
@@ -148,46 +154,56 @@ struct Loader {
       look_ahead(p, seqs, tp);
     }
     const int t = now.tile + at, j = (t < tp ? t : t - tp) * kKeyTile, slot = j & (S - 1);
-    const bool two = S != 16 || j + 16 < (t < tp ? a.prefix_len : now.own);  // the second half's page may be none
-    const int page0 = __shfl_sync(0xffffffffu, id0, at), page1 = S == 16 ? __shfl_sync(0xffffffffu, id1, at) : page0;
-    const int slot1 = S == 16 ? 0 : slot + 16, size1 = two ? 16 : 0;
-    // Tokens of a head counted through the pool: 32 bits hold them (check_four). 16 of them lie side by side.
-    const uint32_t token0 = (static_cast<uint32_t>(page0) * a.Hkv + now.hkv) * S + slot;
-    const uint32_t token1 = (static_cast<uint32_t>(page1) * a.Hkv + now.hkv) * S + slot1;
+    const int G = a.H / a.Hkv, h0 = now.hkv * G + (G > kRows ? now.rt * p.Rt % p.Gp : 0), most = min(heads, a.H - h0);
+    const int page0 = __shfl_sync(0xffffffffu, id0, at);
+    // Tokens of a head counted through the pool: 32 bits hold them (check_four). Those of a page lie side by side, in halves of
+    // 16 that are two pages' with pages of 16: NB lanes a half of K's or V's scales, four lanes a half of a head's gates.
+    const uint32_t token0 = (static_cast<uint32_t>(page0) * a.Hkv + now.hkv << a.page_shift) + slot;
+    const int row0 = page0 * a.H + h0;
     const uint32_t mine = dst + lane * 16;
+    const int part = lane % NB, second = lane / NB & 1, h4 = lane >> 3, s4 = (lane & 3) * 4;
+    const uint8_t* scales = (lane < 2 * NB ? p.ks : p.vs) + part * 16;
+    if (S != 16) {
+      const uint8_t* k = static_cast<const uint8_t*>(a.k) + lane * 16 + (uint64_t)token0 * RowB;
+      const uint8_t* v = static_cast<const uint8_t*>(a.v) + lane * 16 + (uint64_t)token0 * RowB;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint8_t* pool = static_cast<const uint8_t*>(v ? a.v : a.k) + lane * 16;
-      const uint8_t* half0 = pool + (uint64_t)token0 * RowB;
-      const uint8_t* half1 = pool + (uint64_t)token1 * RowB;
+      for (int i = 0; i < D / 32; ++i) copy16(mine + i * 512, k + i * 512, policy);
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        copy16(mine + v * L::kTileBytes + i * 512, half0 + i * 512, 16, policy);
-        copy16(mine + v * L::kTileBytes + (D / 64 + i) * 512, half1 + i * 512, size1, policy);
+      for (int i = 0; i < D / 32; ++i) copy16(mine + L::kTileBytes + i * 512, v + i * 512, policy);
+      if (lane < 4 * NB) copy16(mine + 2 * L::kTileBytes, scales + second * 16 * NB + (uint64_t)token0 * NB, policy);
+      const float* g = a.g + (slot + (lane >> 2 & 1) * 16 + s4);
+      const uint32_t to = sg + (lane >> 2 & 1) * L::kGateSub + (4 + s4) * 4;
+      for (int h = h4; h < most; h += 4) copy16(to + h * 80, g + ((size_t)(row0 + h) << a.page_shift), policy);
+      if (lane < 2 * kRows && lane % kRows < most) {
+        const size_t row = row0 + lane % kRows;
+        cp_async8(sg + 2 * L::kGateSub + lane * 8, a.gbase + 2 * row);
+        if (p.bias_from_j) {  // the four slots before, 0 before a page's first
+          const int before = slot + lane / kRows * 16 - 4;
+          copy16_or_0(sg + lane / kRows * L::kGateSub + lane % kRows * 80, a.g + ((row << a.page_shift) + max(before, 0)), before >= 0, policy);
+        }
       }
-    }
-    // Scales: NB lanes a half of K or V.
-    if (lane < 4 * NB) {
-      const int part = lane % NB, half = lane / NB & 1, v = lane / (2 * NB);
-      copy16(mine + 2 * L::kTileBytes, (v ? p.vs : p.ks) + part * 16 + (uint64_t)(half ? token1 : token0) * NB, half ? size1 : 16,
-             policy);
-    }
-    // Gates of the row tile's heads, in halves of 16 slots: sums, with bias_from_j the four before them too (0 before a page's
-    // first), and bases. The heads lie side by side.
-    const int G = a.H / a.Hkv, h0 = now.hkv * G + (G > L::kRows ? now.rt * p.Rt % p.Gp : 0);
-    const int row0 = page0 * a.H + h0, row1 = page1 * a.H + h0, most = min(heads, a.H - h0);
-    for (int c = lane; c < most * 8; c += 32) {
-      const int h = c >> 3, half = c >> 2 & 1, s4 = (c & 3) * 4;
-      copy16(sg + half * L::kGateSub + (h * 20 + 4 + s4) * 4,
-             a.g + (((size_t)((half ? row1 : row0) + h) << a.page_shift) + (half ? slot1 : slot) + s4), half ? size1 : 16, policy);
-    }
-    if (lane < 2 * L::kRows && lane % L::kRows < most) {
-      const int half = lane / L::kRows, h = lane % L::kRows;
-      const size_t row = (half ? row1 : row0) + h;
-      cp_async8(sg + 2 * L::kGateSub + lane * 8, a.gbase + 2 * row);
-      if (p.bias_from_j) {
-        const int before = (half ? slot1 : slot) - 4;
-        copy16(sg + half * L::kGateSub + h * 80, a.g + ((row << a.page_shift) + max(before, 0)), before >= 0 ? 16 : 0, policy);
+    } else {
+      const bool two = j + 16 < (t < tp ? a.prefix_len : now.own);  // the second half's page may be none
+      const int page1 = __shfl_sync(0xffffffffu, id1, at), row1 = page1 * a.H + h0;
+      const uint32_t token1 = (static_cast<uint32_t>(page1) * a.Hkv + now.hkv) * 16;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint8_t* pool = static_cast<const uint8_t*>(x ? a.v : a.k) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          copy16(mine + x * L::kTileBytes + i * 512, pool + (uint64_t)token0 * RowB + i * 512, policy);
+          copy16_or_0(mine + x * L::kTileBytes + (D / 64 + i) * 512, pool + (uint64_t)token1 * RowB + i * 512, two, policy);
+        }
+      }
+      if (lane < 4 * NB)
+        copy16_or_0(mine + 2 * L::kTileBytes, scales + (uint64_t)(second ? token1 : token0) * NB, !second || two, policy);
+      const bool other = lane >> 2 & 1;
+      const uint32_t to = sg + (other ? L::kGateSub : 0) + (4 + s4) * 4;
+      for (int h = h4; h < most; h += 4)
+        copy16_or_0(to + h * 80, a.g + ((size_t)((other ? row1 : row0) + h) * 16 + s4), !other || two, policy);
+      if (lane < 2 * kRows && lane % kRows < most) {
+        cp_async8(sg + 2 * L::kGateSub + lane * 8, a.gbase + 2 * (size_t)((lane < kRows ? row0 : row1) + lane % kRows));
+        if (p.bias_from_j) copy16_or_0(sg + lane / kRows * L::kGateSub + lane % kRows * 80, a.g, false, policy);
       }
     }
     ++at;
@@ -195,10 +211,12 @@ struct Loader {
 };
 
 // kMany: sequences may bring more than one token, so that rows of a tile may end at different keys.
-template <int D, int NT, int W, bool kMany>
+template <int D, int kRows, int W, bool kMany>
 __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constant__ DecodeParams p, const int heads) {
-  using L = Layout4<D, NT>;
-  constexpr int NB = L::kBlocks, RowB = D / 2, stages = L::kStages;
+  using L = Layout4<D, kRows>;
+  constexpr int NB = L::kBlocks, RowB = D / 2, stages = L::kStages, NT = kRows == 16 ? 2 : 1;
+  constexpr bool kTwice = kRows == 4;        // rows stand twice among the columns
+  constexpr int MT = kTwice ? 1 : 2;         // of a tile's two halves of 16 keys, how many a lane forms weights of
   extern __shared__ uint8_t smem_raw[];
   __shared__ int scratch[W];
   __shared__ Kept<L::kRows, W> kept;
@@ -232,6 +250,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
   const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size;
   const int P = a.prefix_len, tp = p.walk_prefix ? ceil_div(P, kKeyTile) : 0;  // the prefix's tiles come first
   const int g8 = lane >> 2, t4 = lane & 3;
+  const int half = kTwice ? t4 >> 1 : 0;  // where rows stand twice, the half of a tile's keys that this lane weighs
   const uint32_t vplace = lane * RowB, vturn = NB == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1;
   const uint64_t policy = stream_policy();
 
@@ -278,7 +297,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
     }
   };
 
-  Loader<D, NT> load;
+  Loader<D, kRows> load;
   int asked = 0;  // tiles
   place_item();
   {
@@ -318,10 +337,10 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
     segment = done;
     __syncwarp();
     uint32_t qf[NB][NT][4];     // Q^T operand: of block b, its lane's channels 0 1, 2 3, 6 7, 4 5
-    float start[NB][NT][2];     // what a block's sum has too much, negated
+    uint32_t start[NT][2];      // what the blocks' sums have too much, negated, in three fp16 each: an operand beside the scales
     float unit[NT][2];          // log2 units of a row's S
     float acc[2 * NB][NT][4];   // O^T: of block b channels 4 g8 + 0, + 1 and + 2, + 3
-    float r[NT][2], l[NT][2];   // the reference that weights are taken against (-inf: none yet), their sum
+    float r[NT][2], l[NT][2];   // the reference that weights are taken against, their sum
     int top_e = 15;             // exponent bits of the largest scale of V so far, 15 at least
     uint32_t weight_room = 0, scale_room = 0;  // what is left to the bounds of weights and scales (`over` below)
     Gate2 ci[NT][2];
@@ -329,7 +348,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // Row nt * 8 + g8: this lane's channels of every block, in fp16 at a power of two.
-      const uint8_t* qr = q_of + (nt * 8 + g8) * L::kQPitch;
+      const uint8_t* qr = q_of + (nt * 8 + g8) % kRows * L::kQPitch;
       float f[NB][8], most = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -344,11 +363,12 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
       }
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-      // 2^-e brings `most` to [32, 64); in two factors, both of them normal numbers
-      const int e = most > 0.f ? min(static_cast<int>(__float_as_uint(most) >> 23), 254) - 127 - 5 : 0;
+      // 2^-e brings `most` to [4, 8); in two factors, both of them normal numbers
+      const int e = most > 0.f ? min(static_cast<int>(__float_as_uint(most) >> 23), 254) - 127 - 2 : 0;
       const float down0 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23),
                   down1 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
       const float row_unit = p.scale2 / down0 / down1;
+      uint32_t piece[3][NB / 2];  // the sums of two blocks, in three parts
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         float sum = 0.f;
@@ -359,25 +379,37 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
           const float up = low ? 256.f : 16.f;
           const uint32_t h = pack_f16x2(f[b][2 * i] * down0 * down1 * up, f[b][2 * i + 1] * down0 * down1 * up);
           const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          sum -= (back.x + back.y) * (low ? 264.f / 256.f : 24.f / 16.f);
+          sum -= (back.x + back.y) * (low ? 264.f / 256.f : 24.f / 16.f);  // 16 channels of at most 2048: below 2^16
           qf[b][nt][i == 0 ? 0 : i == 1 ? 1 : i == 3 ? 2 : 3] = h;
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        start[b][nt][0] = __shfl_sync(0xffffffffu, sum, t4 * 8);
-        start[b][nt][1] = __shfl_sync(0xffffffffu, sum, t4 * 8 + 4);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint32_t h = pack_f16x2(sum, 0.f) & 0xFFFFu;
+          sum -= __half2float(*reinterpret_cast<const __half*>(&h));
+          piece[i][b / 2] = b % 2 ? piece[i][b / 2] | h << 16 : h;
+        }
+      }
+      // The operand's rows 2 t4, 2 t4 + 1 and + 8, + 9 (blocks b, b + 1 of a part), beside which scales() puts the blocks' scales.
+      if (NB == 4) {
+        start[nt][0] = t4 == 0 ? piece[0][0] : t4 == 1 ? piece[0][NB / 2 - 1] : t4 == 2 ? piece[1][0] : piece[1][NB / 2 - 1];
+        start[nt][1] = t4 == 0 ? piece[2][0] : t4 == 1 ? piece[2][NB / 2 - 1] : 0u;
+      } else {
+        start[nt][0] = t4 == 0 ? piece[0][0] : t4 == 1 ? piece[1][0] : t4 == 2 ? piece[2][0] : 0u;
+        start[nt][1] = 0u;
       }
       unit[nt][0] = __shfl_sync(0xffffffffu, row_unit, t4 * 8);
       unit[nt][1] = __shfl_sync(0xffffffffu, row_unit, t4 * 8 + 4);
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
-        const int rl = nt * 8 + 2 * t4 + e2, rr = r0 + rl, t = token_of(p, rr), g = rr - t * Gp;
+        const int rl = (nt * 8 + 2 * t4 + e2) % kRows, rr = r0 + rl, t = token_of(p, rr), g = rr - t * Gp;
         const bool here = t < cur.s.n && g < G;
         pos[nt][e2] = new0 + t;
-        head[nt][e2] = here ? (G > L::kRows ? g - r0 % Gp : g) : 0;
+        head[nt][e2] = here ? (G > kRows ? g - r0 % Gp : g) : 0;
         ci[nt][e2] = {-INFINITY, 0.f};  // an empty row's scores are -inf
         if (here) ci[nt][e2] = gate_sum(rows->base[rl], rows->g[rl]);
-        r[nt][e2] = -INFINITY;
+        r[nt][e2] = 0.f;
         l[nt][e2] = 0.f;
       }
     }
@@ -418,12 +450,8 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
         float s[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
           // Keys mt * 16 + g8 and + 8: this lane's words of every block, and the blocks' scales.
-          uint32_t kw[2][NB];
+          uint32_t kw[2][NB], kh[2];
           float ks[2][NB];
 #pragma unroll
           for (int k8 = 0; k8 < 2; ++k8) {
@@ -449,7 +477,15 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
               ks[k8][b] = f.x;
               ks[k8][b + 1] = f.y;
+              kh[k8] = b && !(t4 & 1) ? kh[k8] : h;  // blocks 0, 1 or, in odd lanes, 2, 3
             }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+            const uint32_t both[4] = {kh[0], kh[1], kh[0], kh[1]};
+            mma_f16(s[mt][nt], both, start[nt][0], start[nt][1]);
           }
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
@@ -464,25 +500,28 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
               mma_f16(c, k0, qf[b][nt][0], qf[b][nt][1]);
               mma_f16(c, k1, qf[b][nt][2], qf[b][nt][3]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[mt][nt][e] = fmaf(c[e] + start[b][nt][e & 1], ks[e >> 1][b], s[mt][nt][e]);
+              for (int e = 0; e < 4; ++e) s[mt][nt][e] = fmaf(c[e], ks[e >> 1][b], s[mt][nt][e]);
             }
           }
         }
-        // Scores of keys mt * 16 + g8 (+ 8) and rows 2 t4 (+ 1), in log2 units.
+        // Scores less the reference, of keys m * 16 + g8 (+ 8) and rows 2 t4 (+ 1), in log2 units; m: mt, or this lane's half.
+        float y[MT][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float* gr = reinterpret_cast<const float*>(sg) + (head[nt][e] * 20 + 4 + g8 - p.bias_from_j);
-            const float2* bs = reinterpret_cast<const float2*>(sg + 2 * L::kGateSub) + head[nt][e];
+            const float* gr = reinterpret_cast<const float*>(sg) + (head[nt][e] * 20 + 4 + g8 - p.bias_from_j) + half * (L::kGateSub / 4);
+            const float2* bs = reinterpret_cast<const float2*>(sg + 2 * L::kGateSub) + head[nt][e] + half * kRows;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              const float2 base = bs[mt * L::kRows];
+            for (int mt = 0; mt < MT; ++mt) {
+              const float2 base = bs[mt * kRows];
               const float beta = (ci[nt][e].hi - base.x) + (ci[nt][e].lo - base.y);
 #pragma unroll
-              for (int k8 = 0; k8 < 2; ++k8)
-                s[mt][nt][k8 * 2 + e] =
-                    fmaf(beta - gr[mt * (L::kGateSub / 4) + k8 * 8], kLog2e, s[mt][nt][k8 * 2 + e] * unit[nt][e]);
+              for (int k8 = 0; k8 < 2; ++k8) {
+                const float x = kTwice && half ? s[1][nt][k8 * 2 + e] : s[mt][nt][k8 * 2 + e];
+                y[mt][nt][k8 * 2 + e] =
+                    fmaf(beta - gr[mt * (L::kGateSub / 4) + k8 * 8], kLog2e, fmaf(x, unit[nt][e], -r[nt][e]));
+              }
             }
           }
         if (edge) {
@@ -491,27 +530,25 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
-              for (int mt = 0; mt < 2; ++mt)
-                if (j0 + mt * 16 + (e >> 1) * 8 + g8 > (pre ? P - 1 : pos[nt][e & 1])) s[mt][nt][e] = -INFINITY;
+              for (int mt = 0; mt < MT; ++mt)
+                if (j0 + (mt + half) * 16 + (e >> 1) * 8 + g8 > (pre ? P - 1 : pos[nt][e & 1])) y[mt][nt][e] = -INFINITY;
         }
         // Weights, two rows to an fp16 pair.
-        uint32_t ph[2][NT][2];
-        float wt[2][NT][4];
+        uint32_t ph[MT][NT][2];
+        float wt[MT][NT][4];
         auto weigh = [&]() {
           uint32_t most = 0;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float o0 = r[nt][0] == -INFINITY ? 0.f : r[nt][0], o1 = r[nt][1] == -INFINITY ? 0.f : r[nt][1];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int k8 = 0; k8 < 2; ++k8) {
-                wt[mt][nt][k8 * 2] = ex2_approx(s[mt][nt][k8 * 2] - o0);
-                wt[mt][nt][k8 * 2 + 1] = ex2_approx(s[mt][nt][k8 * 2 + 1] - o1);
+                wt[mt][nt][k8 * 2] = ex2_approx(y[mt][nt][k8 * 2]);
+                wt[mt][nt][k8 * 2 + 1] = ex2_approx(y[mt][nt][k8 * 2 + 1]);
                 ph[mt][nt][k8] = pack_f16x2(wt[mt][nt][k8 * 2], wt[mt][nt][k8 * 2 + 1]);
                 most = hmax2(most, ph[mt][nt][k8]);
               }
-          }
           return most;
         };
         const uint32_t most = weigh();
@@ -532,17 +569,24 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float y = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+              // the largest score less the old reference; a row that weighed something had one of `was` there
+              float z = l[nt][e] > 0.f ? was : -INFINITY;
 #pragma unroll
-              for (int k = 4; k < 32; k <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, k));
-              const float rn = fmaxf(r[nt][e] + was, y) - lift;
-              const float alpha = rn == -INFINITY ? 1.f : ex2_approx(r[nt][e] - rn);
-              r[nt][e] = rn;
+              for (int mt = 0; mt < MT; ++mt) z = fmaxf(z, fmaxf(y[mt][nt][e], y[mt][nt][e + 2]));
+#pragma unroll
+              for (int k = kTwice ? 2 : 4; k < 32; k <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, k));
+              const float up = z == -INFINITY ? 0.f : z - lift, alpha = up > 0.f ? ex2_approx(-up) : 1.f;  // below 0 only where nothing is summed yet
+              r[nt][e] += up;
               l[nt][e] *= alpha;
 #pragma unroll
               for (int dt = 0; dt < 2 * NB; ++dt) {
                 acc[dt][nt][e] *= alpha;
                 acc[dt][nt][e + 2] *= alpha;
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                y[mt][nt][e] -= up;
+                y[mt][nt][e + 2] -= up;
               }
             }
           weigh();
@@ -550,42 +594,59 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int k8 = 0; k8 < 2; ++k8) {
               l[nt][0] += wt[mt][nt][k8 * 2];
               l[nt][1] += wt[mt][nt][k8 * 2 + 1];
               ph[mt][nt][k8] = turn8x8(ph[mt][nt][k8]);
             }
-        uint32_t vsw[2][NB];  // scales of tokens 2 t4, 2 t4 + 1 (+ 8) of each 16
+        // Scales of tokens 2 t4, 2 t4 + 1 (+ 8) of each 16, where rows stand twice of those whose weights this lane's column has.
+        uint32_t vsw[MT][NB];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint8_t* at16 = svs + (kTwice ? g8 >> 2 : mt) * 16 * NB + t4 * 4 * NB;
           if (NB == 4) {
-            const uint4 y = *reinterpret_cast<const uint4*>(svs + mt * 64 + t4 * 16);
-            vsw[mt][0] = y.x;
-            vsw[mt][1] = y.y;
-            vsw[mt][NB - 2] = y.z;
-            vsw[mt][NB - 1] = y.w;
+            const uint4 x = *reinterpret_cast<const uint4*>(at16);
+            vsw[mt][0] = x.x;
+            vsw[mt][1] = x.y;
+            vsw[mt][NB - 2] = x.z;
+            vsw[mt][NB - 1] = x.w;
           } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(svs + mt * 32 + t4 * 8);
-            vsw[mt][0] = y.x;
-            vsw[mt][1] = y.y;
+            const uint2 x = *reinterpret_cast<const uint2*>(at16);
+            vsw[mt][0] = x.x;
+            vsw[mt][1] = x.y;
           }
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t v[4];
           ldsm4_t(smem_u32(sv) + vplace + ((b ^ vturn) << 4), v);
+          uint32_t pa[2][NT], pb[2][NT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint32_t sa = (vsw[mt][b] & 0x00FF00FFu) * 128u, sb = (vsw[mt][b] >> 1) & 0x7F807F80u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              pa[mt][nt] = hmul2(ph[mt][nt][0], sa);
+              pb[mt][nt] = hmul2(ph[mt][nt][1], sb);
+            }
+          }
+          if (kTwice) {  // a column has no weights of the other half's keys
+            pa[1][0] = g8 < 4 ? 0u : pa[0][0];
+            pb[1][0] = g8 < 4 ? 0u : pb[0][0];
+            pa[0][0] = g8 < 4 ? pa[0][0] : 0u;
+            pb[0][0] = g8 < 4 ? pb[0][0] : 0u;
+          }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
             const uint32_t x0 = v[2 * mt], x1 = v[2 * mt + 1], y0 = x0 >> 8, y1 = x1 >> 8;
             const uint32_t v0[4] = {low_nibbles(x0), high_nibbles(x0), low_nibbles(x1), high_nibbles(x1)};
             const uint32_t v1[4] = {low_nibbles(y0), high_nibbles(y0), low_nibbles(y1), high_nibbles(y1)};
-            const uint32_t sa = (vsw[mt][b] & 0x00FF00FFu) * 128u, sb = (vsw[mt][b] >> 1) & 0x7F807F80u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t pa = hmul2(ph[mt][nt][0], sa), pb = hmul2(ph[mt][nt][1], sb);
-              mma_f16(acc[2 * b][nt], v0, pa, pb);
-              mma_f16(acc[2 * b + 1][nt], v1, pa, pb);
+              mma_f16(acc[2 * b][nt], v0, pa[mt][nt], pb[mt][nt]);
+              mma_f16(acc[2 * b + 1][nt], v1, pa[mt][nt], pb[mt][nt]);
             }
           }
         }
@@ -604,14 +665,21 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
           for (int e = 0; e < 2; ++e) {
             float y = l[nt][e];
 #pragma unroll
-            for (int k = 4; k < 32; k <<= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
+            for (int k = kTwice ? 2 : 4; k < 32; k <<= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
             const int rl = 2 * t4 + e;
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-              *reinterpret_cast<float4*>(out + rl * L::kOutStride + b * 32 + g8 * 4) =
-                  make_float4(acc[2 * b][nt][e], acc[2 * b][nt][e + 2], acc[2 * b + 1][nt][e], acc[2 * b + 1][nt][e + 2]);
-            if (g8 == 0) {
-              kept.m[warp][nt * 8 + rl] = r[nt][e];
+            for (int b = 0; b < NB; ++b) {
+              float4 x = make_float4(acc[2 * b][nt][e], acc[2 * b][nt][e + 2], acc[2 * b + 1][nt][e], acc[2 * b + 1][nt][e + 2]);
+              if (kTwice) {
+                x.x += __shfl_xor_sync(0xffffffffu, x.x, 2);
+                x.y += __shfl_xor_sync(0xffffffffu, x.y, 2);
+                x.z += __shfl_xor_sync(0xffffffffu, x.z, 2);
+                x.w += __shfl_xor_sync(0xffffffffu, x.w, 2);
+              }
+              if (rl < kRows) *reinterpret_cast<float4*>(out + rl * L::kOutStride + b * 32 + g8 * 4) = x;
+            }
+            if (g8 == 0 && rl < kRows) {
+              kept.m[warp][nt * 8 + rl] = y > 0.f ? r[nt][e] : -INFINITY;
               kept.l[warp][nt * 8 + rl] = y;
             }
           }
@@ -636,50 +704,51 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
     }
   }
   clear_idle_rows<__nv_bfloat16, D>(p, seqs);
-  // The threads' sums stand in the queries' place.
-  static_assert(32 * sizeof(Column) <= L::kQBytes, "they fit there");
+  // The threads' sums stand in the gates' place.
+  static_assert(32 * sizeof(Column) <= stages * L::kGateBytes, "they fit there");
   join_items<__nv_bfloat16, D, L::kRows, W>(p, seqs, total, each, kept, ends, reinterpret_cast<const float*>(sm),
-                                            stages * L::kStageBytes / 4, L::kOutStride, offs, reinterpret_cast<Column*>(all_q));
+                                            stages * L::kStageBytes / 4, L::kOutStride, offs, reinterpret_cast<Column*>(all_gates));
   if (shared) grid_dep_wait();  // as fox_decode_mma.cu's kernel
 }
 
-constexpr size_t smem_bytes(int D, int NT, int W, size_t B) {
-  const size_t stage = 2 * (kKeyTile * D / 2 + kKeyTile * D / kFourBlock), q = 8 * NT * (D * 2 + 16), gates = 8 * NT * 176;
+constexpr size_t smem_bytes(int D, int rows, int W, size_t B) {
+  const size_t stage = 2 * (kKeyTile * D / 2 + kKeyTile * D / kFourBlock), q = rows * (D * 2 + 16), gates = rows * 176;
   return 128 + sizeof(SeqEntry) * (B + 1) + W * (q + 2 * (stage + gates));
 }
 constexpr size_t kMost = 232448 - 8192;  // of an SM's shared memory, less the static part
 
-template <int D, int NT, int W, bool kMany>
+template <int D, int kRows, int W, bool kMany>
 cudaError_t launch_as(const DecodeParams& p, cudaStream_t s) {
-  using L = Layout4<D, NT>;
-  static_assert(smem_bytes(D, NT, W, 0) == 128 + sizeof(SeqEntry) + W * (L::kQBytes + L::kStages * (L::kStageBytes + L::kGateBytes)), "");
-  auto kernel = decode4_kernel<D, NT, W, kMany>;
+  using L = Layout4<D, kRows>;
+  static_assert(smem_bytes(D, kRows, W, 0) == 128 + sizeof(SeqEntry) + W * (L::kQBytes + L::kStages * (L::kStageBytes + L::kGateBytes)), "");
+  auto kernel = decode4_kernel<D, kRows, W, kMany>;
   const int G = p.a.H / p.a.Hkv;
   // One limit for every call (launch_as in fox_decode_mma.cu has the reason).
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode4", s);
-  const cudaError_t f = launch_dependent(kernel, dim3(kSMs), dim3(32 * W), smem_bytes(D, NT, W, p.a.B), s, p, G < L::kRows ? G : L::kRows);
+  const cudaError_t f = launch_dependent(kernel, dim3(kSMs), dim3(32 * W), smem_bytes(D, kRows, W, p.a.B), s, p, G < kRows ? G : kRows);
   return f != cudaSuccess ? f : cudaGetLastError();
 }
 
-template <int D, int NT, int W>
-cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
-  static_assert(smem_bytes(D, NT, W, kMaxSeqs) <= kMost, "shared memory");
-  return p.a.max_new > 1 ? launch_as<D, NT, W, true>(p, s) : launch_as<D, NT, W, false>(p, s);
-}
-
 // Workers of a CTA: three or two a scheduler, as registers allow.
-constexpr int warps_of(int D, int NT) { return NT == 1 || D == 64 ? 12 : 8; }
+constexpr int warps_of(int D, int rows) { return rows < 16 || D == 64 ? 12 : 8; }
+
+template <int D, int kRows>
+cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
+  constexpr int W = warps_of(D, kRows);
+  static_assert(smem_bytes(D, kRows, W, kMaxSeqs) <= kMost, "shared memory");
+  return p.a.max_new > 1 ? launch_as<D, kRows, W, true>(p, s) : launch_as<D, kRows, W, false>(p, s);
+}
 
 }  // namespace
 
-int decode4_rows(int rows) { return rows <= 8 ? 8 : 16; }
-int decode4_warps(const PagedArgs& a, int Rt) { return warps_of(a.d, Rt / 8); }
+int decode4_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+int decode4_warps(const PagedArgs& a, int Rt) { return warps_of(a.d, Rt); }
 
 cudaError_t launch_decode4(const DecodeParams& p, cudaStream_t s) {
-  if (p.a.d == 64) return p.Rt == 8 ? launch<64, 1, warps_of(64, 1)>(p, s) : launch<64, 2, warps_of(64, 2)>(p, s);
-  return p.Rt == 8 ? launch<128, 1, warps_of(128, 1)>(p, s) : launch<128, 2, warps_of(128, 2)>(p, s);
+  if (p.a.d == 64) return p.Rt == 4 ? launch<64, 4>(p, s) : p.Rt == 8 ? launch<64, 8>(p, s) : launch<64, 16>(p, s);
+  return p.Rt == 4 ? launch<128, 4>(p, s) : p.Rt == 8 ? launch<128, 8>(p, s) : launch<128, 16>(p, s);
 }
 
 }  // namespace fox
