@@ -155,6 +155,7 @@ struct DecodeLayout {
   Numbering num;
   long long items;  // of a key head
   size_t cum, ml, po, pml, ppo, end;
+  size_t pk, pv, pg, pbase, ptab;  // a 4-bit cache's shared prefix, spread out: a pool of its pages in order, and their table
   PrefixPlan pre;
   long long po_rows;
 };
@@ -165,6 +166,14 @@ struct DecodeLayout {
 // 24.8 and 28.7, at 78 MB 27.7 against 26.5, at 106 MB 31 against 25.5, at 150 MB 39 against 29.
 bool share_prefix(const PagedArgs& a, int row_tiles) {
   return (long long)a.B * row_tiles * a.prefix_len * a.Hkv * a.d * 4 > (72ll << 20);
+}
+// The same of a 4-bit cache, where a key tile walked costs instructions (1.2 ns of the whole GPU's time, half as much more in tiles of
+// 16 rows), and sharing spreads the prefix out first: some 16 us, and 8.6 ns a tile of the prefix at 128 channels. In tiles walked.
+// 32 heads on 8 of 128 channels, walked and shared: 8 sequences behind 16384 tokens 55 and 65 us, 16 behind 4096 37 and 40, 64 behind 1024
+// 40 and 39, 2 behind 65536 51 and 165, 256 behind 32768 2900 and 219; 16 heads of 64 channels, 16 sequences behind 4096 47 and 37.
+bool share_prefix4(const PagedArgs& a, int row_tiles, int Rt) {
+  const long long tiles = (long long)ceil_div(a.prefix_len, kKeyTile) * a.Hkv, walked = a.B * row_tiles * tiles;
+  return (Rt == 16 ? walked * 3 / 2 : walked) > 13000 + tiles * 7 * a.d / 128;
 }
 
 DecodeLayout decode_layout(const PagedArgs& a, Held held) {
@@ -187,11 +196,20 @@ DecodeLayout decode_layout(const PagedArgs& a, Held held) {
   L.pml = align_up(L.po + sizeof(float) * slots * L.Rs * a.d, 256);
   L.ppo = L.end = L.pml;
   L.pre = PrefixPlan{};
-  if (held == Held::kBf16 && a.prefix_len > 0 && share_prefix(a, row_tiles)) {
+  if (a.prefix_len > 0 && (held == Held::kBf16 ? share_prefix(a, row_tiles) : four && share_prefix4(a, row_tiles, L.Rt))) {
     L.pre = prefix_plan(a);
     const size_t rows = ((size_t)L.pre.workers + (size_t)a.Hkv * L.pre.items) * 2 * kTile;
     L.ppo = align_up(L.pml + sizeof(float2) * rows, 256);
     L.end = align_up(L.ppo + sizeof(float) * rows * a.d, 256);
+    if (four) {
+      const size_t pages = ceil_div(a.prefix_len, a.page_size), values = pages * a.Hkv * a.page_size * a.d;
+      L.pk = L.end;
+      L.pv = align_up(L.pk + 2 * values, 256);
+      L.pg = align_up(L.pv + 2 * values, 256);
+      L.pbase = align_up(L.pg + 4 * pages * a.H * a.page_size, 256);
+      L.ptab = align_up(L.pbase + 8 * pages * a.H, 256);
+      L.end = align_up(L.ptab + 4 * pages, 256);
+    }
   }
   return L;
 }
@@ -202,7 +220,8 @@ bool decode_fits(const PagedArgs& a, Held held) {
   const DecodeLayout L = decode_layout(a, held);
   return line_fits(most_units(a, L.items), L.workers, L.warps) &&
          (unsigned long long)a.max_new * L.Gp * L.Gp < (1ull << 32) && L.po_rows < 0x7fffffffLL &&
-         (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.line < 0x7fffffffLL - L.pre.each);
+         (L.pre.key_tiles == 0 || (long long)a.Hkv * L.pre.items * L.pre.line < 0x7fffffffLL - L.pre.each) &&
+         (L.pre.key_tiles == 0 || held != Held::kFour || ceil_div(a.prefix_len, a.page_size) * (2LL * a.Hkv + 1) <= 0x7fffffffLL);
 }
 
 size_t decode_workspace_bytes(const PagedArgs& a, Held held) { return decode_layout(a, held).end; }
@@ -235,7 +254,20 @@ cudaError_t launch_decode(const DecodeArgs& x, Held held, char* ws, cudaStream_t
   p.pre.ml = reinterpret_cast<float2*>(ws + L.pml);
   p.pre.po = reinterpret_cast<float*>(ws + L.ppo);
   static_assert(kErrWordBytes + 4 * 2 * kSMs <= kCacheHeaderBytes, "a counter a CTA");
-  const cudaError_t e = p.pre.key_tiles > 0 ? launch_prefix(p, s) : cudaSuccess;
+  cudaError_t e = cudaSuccess;
+  if (p.pre.key_tiles > 0 && held == Held::kFour) {
+    DecodeParams spread = p;
+    spread.a.num_pages = ceil_div(x.a.prefix_len, x.a.page_size);
+    spread.a.k = ws + L.pk;
+    spread.a.v = ws + L.pv;
+    spread.a.g = reinterpret_cast<float*>(ws + L.pg);
+    spread.a.gbase = reinterpret_cast<float*>(ws + L.pbase);
+    spread.a.prefix = reinterpret_cast<int32_t*>(ws + L.ptab);
+    e = launch_spread4(p, spread.a, s);
+    if (e == cudaSuccess) e = launch_prefix(spread, s);
+  } else if (p.pre.key_tiles > 0) {
+    e = launch_prefix(p, s);
+  }
   if (e != cudaSuccess) return e;
   if (held == Held::kF32) return launch_decode_f32(p, s);
   const cudaError_t f = held == Held::kFour ? launch_decode4(p, s) : launch_decode_mma(p, s);

@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
                 if (j0 + (mt + half) * 16 + (e >> 1) * 8 + g8 > (pre ? P - 1 : pos[nt][e & 1])) y[mt][nt][e] = -INFINITY;
         }
         // Weights, two rows to an fp16 pair.
-        uint32_t ph[MT][NT][2];
+        uint32_t ph[2][NT][2];
         float wt[MT][NT][4];
         auto weigh = [&]() {
           uint32_t most = 0;
@@ -600,6 +600,10 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
               l[nt][0] += wt[mt][nt][k8 * 2];
               l[nt][1] += wt[mt][nt][k8 * 2 + 1];
               ph[mt][nt][k8] = turn8x8(ph[mt][nt][k8]);
+              if (kTwice) {  // a column has no weights of the other half's keys
+                ph[1][nt][k8] = g8 < 4 ? 0u : ph[0][nt][k8];
+                ph[0][nt][k8] = g8 < 4 ? ph[0][nt][k8] : 0u;
+              }
             }
         // Scales of tokens 2 t4, 2 t4 + 1 (+ 8) of each 16, where rows stand twice of those whose weights this lane's column has.
         uint32_t vsw[MT][NB];
@@ -622,31 +626,17 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
         for (int b = 0; b < NB; ++b) {
           uint32_t v[4];
           ldsm4_t(smem_u32(sv) + vplace + ((b ^ vturn) << 4), v);
-          uint32_t pa[2][NT], pb[2][NT];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint32_t sa = (vsw[mt][b] & 0x00FF00FFu) * 128u, sb = (vsw[mt][b] >> 1) & 0x7F807F80u;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              pa[mt][nt] = hmul2(ph[mt][nt][0], sa);
-              pb[mt][nt] = hmul2(ph[mt][nt][1], sb);
-            }
-          }
-          if (kTwice) {  // a column has no weights of the other half's keys
-            pa[1][0] = g8 < 4 ? 0u : pa[0][0];
-            pb[1][0] = g8 < 4 ? 0u : pb[0][0];
-            pa[0][0] = g8 < 4 ? pa[0][0] : 0u;
-            pb[0][0] = g8 < 4 ? pb[0][0] : 0u;
-          }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
+            const uint32_t sw = vsw[kTwice ? 0 : mt][b], sa = (sw & 0x00FF00FFu) * 128u, sb = (sw >> 1) & 0x7F807F80u;
             const uint32_t x0 = v[2 * mt], x1 = v[2 * mt + 1], y0 = x0 >> 8, y1 = x1 >> 8;
             const uint32_t v0[4] = {low_nibbles(x0), high_nibbles(x0), low_nibbles(x1), high_nibbles(x1)};
             const uint32_t v1[4] = {low_nibbles(y0), high_nibbles(y0), low_nibbles(y1), high_nibbles(y1)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(acc[2 * b][nt], v0, pa[mt][nt], pb[mt][nt]);
-              mma_f16(acc[2 * b + 1][nt], v1, pa[mt][nt], pb[mt][nt]);
+              const uint32_t pa = hmul2(ph[mt][nt][0], sa), pb = hmul2(ph[mt][nt][1], sb);
+              mma_f16(acc[2 * b][nt], v0, pa, pb);
+              mma_f16(acc[2 * b + 1][nt], v1, pa, pb);
             }
           }
         }
@@ -711,6 +701,43 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
   if (shared) grid_dep_wait();  // as fox_decode_mma.cu's kernel
 }
 
+// One block a (page, key head, K or V), and one more a page for its gates and table entry. Bound by what is written.
+constexpr int kSpreadThreads = 256;
+__global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ PagedArgs to) {
+  const PagedArgs& a = p.a;
+  const int S = a.page_size, per = 2 * a.Hkv + 1, at = blockIdx.x / per, part = blockIdx.x - at * per, tid = threadIdx.x;
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int page = checked_page(a, a.prefix[at]), live = min(S, a.prefix_len - at * S);
+  if (part == 2 * a.Hkv) {
+    const size_t n = (size_t)a.H * S / 4;
+    const float4* g = reinterpret_cast<const float4*>(a.g) + (size_t)page * n;
+    float4* out = reinterpret_cast<float4*>(to.g) + (size_t)at * n;
+    for (size_t i = tid; i < n; i += kSpreadThreads) out[i] = g[i];
+    for (int h = tid; h < a.H; h += kSpreadThreads)
+      reinterpret_cast<float2*>(to.gbase)[(size_t)at * a.H + h] = reinterpret_cast<const float2*>(a.gbase)[(size_t)page * a.H + h];
+    if (tid == 0) const_cast<int32_t*>(to.prefix)[at] = at;
+    return;
+  }
+  const bool is_v = part >= a.Hkv;
+  const int hkv = is_v ? part - a.Hkv : part, words = a.d / 8, blocks = a.d / kFourBlock;
+  const uint8_t* from = static_cast<const uint8_t*>(is_v ? a.v : a.k) + four_row(a, page, hkv, 0);
+  const uint8_t* scales = (is_v ? p.vs : p.ks) + four_scale_row(a, page, hkv, 0);
+  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) + kv_offset(to, at, hkv, 0));
+#pragma unroll 4
+  for (int i = tid; i < S * words; i += kSpreadThreads) {
+    const int slot = i / words, w = i - slot * words, b = w >> 2, t = w & 3;
+    uint32_t code = *reinterpret_cast<const uint32_t*>(from + (size_t)slot * (a.d / 2) +
+                                                       (is_v ? four_v_word(b, t, slot, blocks) : four_k_word(b, t, blocks)));
+    if (!is_v) code = four_k_code(code);
+    const float s = four_scale(scales[is_v ? (slot & ~15) * blocks + four_v_scale(b, slot, blocks) : slot * blocks + b]);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = slot < live ? s * static_cast<float>(static_cast<int>(code >> (4 * e) & 15u) - 8) : 0.f;
+    out[i] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  }
+}
+
 constexpr size_t smem_bytes(int D, int rows, int W, size_t B) {
   const size_t stage = 2 * (kKeyTile * D / 2 + kKeyTile * D / kFourBlock), q = rows * (D * 2 + 16), gates = rows * 176;
   return 128 + sizeof(SeqEntry) * (B + 1) + W * (q + 2 * (stage + gates));
@@ -745,6 +772,13 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
 
 int decode4_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 int decode4_warps(const PagedArgs& a, int Rt) { return warps_of(a.d, Rt); }
+
+cudaError_t launch_spread4(const DecodeParams& p, const PagedArgs& to, cudaStream_t s) {
+  TraceScope trace("prefix_spread", s);
+  const cudaError_t e = launch_dependent(spread4_kernel, dim3(static_cast<unsigned>(to.num_pages) * (2 * p.a.Hkv + 1)), dim3(kSpreadThreads),
+                                         0, s, p, to);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 cudaError_t launch_decode4(const DecodeParams& p, cudaStream_t s) {
   if (p.a.d == 64) return p.Rt == 4 ? launch<64, 4>(p, s) : p.Rt == 8 ? launch<64, 8>(p, s) : launch<64, 16>(p, s);

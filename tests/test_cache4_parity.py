@@ -294,6 +294,59 @@ def test_decode(fox, n):
     check_decode(fox, c, f"decode4 {n}", bj, scale)
 
 
+# Behind prefixes long enough for the batch that they are shared out (spread to bf16, then one kernel for all sequences).
+SHARED = [
+    ([13 + i for i in range(48)], [1] * 48, 8, 8, 128, 64, 3001, dict(uniform=True, bias_from_j=True)),  # one row tile, keys split
+    ([3] * 150, [1] * 150, 4, 1, 128, 16, 5003, dict(uniform=True)),                       # row tiles of a small group
+    ([20 + i % 3 for i in range(170)], [2] * 170, 12, 4, 64, 64, 1537, dict(tail=3)),      # several, a tail of one key
+    ([None if i % 5 == 2 else 6 + 11 * (i % 4) for i in range(164)], [1 + i % 5 for i in range(164)], 14, 2, 128, 32, 1664,
+     dict(tail=1)),                                                                        # odd group, idle ones, no tail
+    ([9] * 29, [1] * 29, 20, 1, 128, 128, 22001, dict(uniform=True, scale=0.2)),           # a group of two head chunks
+    ([40, 5, 77, 300] * 4, [33, 5, 40, 1] * 4, 6, 2, 64, 16, 10002, dict(bias_from_j=True)),  # many new tokens
+]
+
+
+@pytest.mark.parametrize("n", range(len(SHARED)))
+def test_decode_behind_a_shared_prefix(fox, n):
+    own, new, H, Hkv, d, S, P, more = SHARED[n]
+    more = dict(more)
+    bj, scale = more.pop("bias_from_j", False), more.pop("scale", None)
+    c = Case4(own, new, H, Hkv, d, S, seed=150 + n, prefix=P, **more)
+    c.put()
+    check_decode(fox, c, f"decode4 shared {n}", bj, scale, want_prefix=True)
+
+
+def test_shared_values_outside_fp16_are_reported(fox):
+    """The shared prefix's P V runs in fp16: a V held as 65536 or more there sets the error word; among a sequence's own tokens,
+    or in a prefix that is walked, it is no error."""
+    for B, P, status in ((150, 5003, FOX_ERR_DEVICE), (3, 100, 0)):
+        for where in ("prefix", "own"):
+            c = Case4([9] * B, [1] * B, 4, 1, 128, 16, uniform=True, prefix=P, seed=6)
+            (c.pre if where == "prefix" else c.seq[1])[1][5, 0, 7] = 1.0e5
+            c.put()
+            cache, batch = c.cache4(fox), c.batch(fox)
+            ws = fox.cache4_workspace(cache, batch, c.rows)
+            fox.fox_cache4_decode(cache, batch, c.q, ws=ws)
+            assert fox.fox_check_error(ws) == (status if where == "prefix" else 0)
+
+
+@pytest.mark.parametrize("B,P", [(3, 100), (150, 5003)])
+def test_bad_pages_of_a_prefix_are_reported(fox, B, P):
+    """Page ids of the prefix outside the pool: reported, read as page 0 (finite here), nothing else."""
+    c = Case4([9] * B, [1] * B, 4, 1, 128, 16, uniform=True, prefix=P, seed=6)
+    for t in (c.k4, c.v4, c.ks, c.vs):
+        t.zero_()
+    c.put()
+    for t in (c.g, c.gbase):
+        t.nan_to_num_(0.0)
+    c.ptable[1], c.ptable[2] = c.k4.shape[0], -1
+    cache, batch = c.cache4(fox), c.batch(fox)
+    ws = fox.cache4_workspace(cache, batch, c.rows)
+    fox.fox_cache4_decode(cache, batch, c.q, ws=ws)
+    assert fox.fox_check_error(ws) == FOX_ERR_DEVICE
+    assert fox.fox_check_error(ws) == 0
+
+
 @pytest.mark.parametrize("H,d,S", [(16, 64, 16), (9, 128, 32), (8, 128, 64), (1, 64, 128)])
 def test_decode_of_the_most_sequences(fox, H, d, S):
     """2048 of them: the most shared memory that a call takes."""
