@@ -263,7 +263,8 @@ def lib() -> ctypes.CDLL:
         except ImportError:  # built without Python's headers: libfox.so is all that the calls need
             _call = _CtypesCall
         else:
-            _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append_low, L.fox_decode, L.fox_cache4_append, L.fox_cache4_decode)))
+            _foxcall.bind(*(ctypes.cast(f, vp).value for f in (L.fox_cache_append_low, L.fox_decode, L.fox_cache4_append, L.fox_cache4_decode,
+                                                                     L.fox_cache4_read)))
             _call = _foxcall
         L.fox_trace_begin.argtypes = []
         L.fox_trace_begin.restype = i
@@ -292,6 +293,10 @@ class _CtypesCall:
         rot = ctypes.byref(fox_rotary(*more)) if more else None
         return lib().fox_cache4_append(ctypes.byref(fox_cache4.from_address(c)), ctypes.byref(fox_batch.from_address(b)), rows, k,
                                        ks, v, vs, z, zs, rot, ws, nbytes, stream)
+
+    @staticmethod
+    def read4(c, b, rows, *more):
+        return lib().fox_cache4_read(ctypes.byref(fox_cache4.from_address(c)), ctypes.byref(fox_batch.from_address(b)), rows, *more)
 
     @staticmethod
     def decode4(c, b, rows, *more):
@@ -971,17 +976,18 @@ def fox_cache4_read(cache: Cache4, batch: Batch, rows: Optional[int] = None, *, 
         if k is None and v is None:
             raise ValueError(f"{where}: rows, or a k or v that has them")
         rows = (v if k is None else k).shape[0]
-    make = lambda: torch.zeros((rows, cache.Hkv, cache.d), dtype=torch.bfloat16, device=cache.device)  # noqa: E731
-    k = _alloc_on(stream, make) if k is None else k
-    v = _alloc_on(stream, make) if v is None else v
+    if k is None or v is None:
+        make = lambda: torch.zeros((rows, cache.Hkv, cache.d), dtype=torch.bfloat16, device=cache.device)  # noqa: E731
+        k = _alloc_on(stream, make) if k is None else k
+        v = _alloc_on(stream, make) if v is None else v
     ks = _row_stride(where, "k", k, cache, cache.Hkv, rows, index)
     vs = _row_stride(where, "v", v, cache, cache.Hkv, rows, index)
     if ws is None:
         ws = _alloc_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=cache.device))
     elif ws.get_device() != index:
         raise ValueError(f"{where}: ws is not on the cache's device")
-    st = lib().fox_cache4_read(cache.ref, batch.ref, rows, k.data_ptr(), ks, v.data_ptr(), vs, ws.data_ptr(), ws.numel(),
-                               _current_stream(index) if stream is None else stream.cuda_stream)
+    st = (_call or _load_call()).read4(cache.addr, batch.addr, rows, k.data_ptr(), ks, v.data_ptr(), vs, ws.data_ptr(), ws.numel(),
+                                       _current_stream(index) if stream is None else stream.cuda_stream)
     if st != 0:
         raise FoxError(st, where)
     return k, v

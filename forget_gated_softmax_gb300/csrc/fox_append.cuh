@@ -323,13 +323,13 @@ struct AppendBlocks {
   long long gates, copies;
   bool fit() const { return gates + copies <= 0x7fffffffLL; }  // a grid
 };
-inline AppendBlocks append_blocks(const PagedArgs& a, int row_units) {
+inline AppendBlocks append_blocks(const PagedArgs& a, int row_units, int thread_rows = kRows) {
   const CopyShape x = copy_shape(row_units);
   AppendBlocks n;
   n.page_chunks = ceil_div(a.max_new, a.page_size) + 1;
   n.head_groups = ceil_div(a.H, kGateHeads);
   n.gates = (long long)a.B * n.page_chunks * n.head_groups;
-  n.copies = (long long)ceil_div(a.rows, kRows * x.side) * x.chunks;
+  n.copies = (long long)ceil_div(a.rows, thread_rows * x.side) * x.chunks;
   return n;
 }
 
@@ -354,12 +354,12 @@ inline AppendParams append_params(const CacheAppendArgs& x) {
   return p;
 }
 
-// The launches of one append by `kernel`, whose blocks behind the gates' copy rows of `row_units` units each; Params is AppendParams
-// or has it as its base.
+// The launches of one append by `kernel`, whose blocks behind the gates' copy rows of `row_units` units each, `thread_rows` a
+// thread; Params is AppendParams or has it as its base.
 template <typename Params>
-cudaError_t launch_append(void (*kernel)(const Params), Params p, int row_units, cudaStream_t s) {
+cudaError_t launch_append(void (*kernel)(const Params), Params p, int row_units, cudaStream_t s, int thread_rows = kRows) {
   const PagedArgs& a = p.a;
-  const AppendBlocks n = append_blocks(a, row_units);
+  const AppendBlocks n = append_blocks(a, row_units, thread_rows);
   p.page_chunks = n.page_chunks;
   p.head_groups = n.head_groups;
   p.scan_bases = a.max_new > a.page_size;

@@ -1,12 +1,15 @@
 // Appending new tokens to the 4-bit cache, and reading tokens back.
 //
-// K is rotated as in fox_append.cu, but to the nearest bf16 of the exact a cos - b sin: the 4-bit form has borders everywhere, and a
+// Q is rotated as in fox_append.cu. K is too, but to the nearest bf16 of the exact a cos - b sin: the 4-bit form has borders everywhere, and a
 // value on the other side of one is a whole step away. Kahan's difference of products (one product's rounding error by a fused
 // multiply-add, taken off the fused difference) is within 1.5 units of the last place of fp32; where that leaves open on which side of
-// a border of bf16 the value lies (1 of 10000), 64 bits decide, in which the products are exact.
+// a border of bf16 a value lies (1 of 5000), 64 bits decide, in which the products are exact.
 //
-// A thread holds 8 channels, four neighbours a block: its largest magnitude by two shuffles, one scale byte by the first of them, a
-// word of codes by each (fox_four.h).
+// A thread has 16 channels of four rows, as in fox_append.cu: a chunk of 8 and its partner's in the rotation, or two neighbouring
+// chunks. A block of 32 channels is two threads' neighbouring chunks (K that was rotated with a partner passes through shared memory
+// for that): its largest magnitude by a shuffle, its scale by the first of them, two words of codes by each (fox_four.h).
+// The rows of a thread are taken in turn by the same code: unrolled, the warps waited for instructions more than for anything (6 prompts
+// of up to 16384 tokens, rotation in pairs: 427 us against 297). Few rows have a thread each, as the rows' angles then come one after the other.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,153 +32,206 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* f) {
     f[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
   }
 }
-
-// a c - b s in 64 bits, rounded to odd in fp32: what then rounds to bf16 is rounded once.
-__device__ __noinline__ float turned_exactly(float a, float c, float b, float s) {
-  const double x = static_cast<double>(a) * c - static_cast<double>(b) * s;
-  const float f = __double2float_rz(x);
-  return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
-}
-// a c - b s, to be rounded to bf16.
-__device__ __forceinline__ float turned(float a, float c, float b, float s) {
-  const float p = __fmul_rn(b, s), e = __fmaf_rn(b, s, -p);
-  const float r = __fsub_rn(__fmaf_rn(a, c, -p), e);
-  const uint32_t near = (__float_as_uint(r) & 0xFFFFu) - 0x7FFCu;
-  return near <= 8u ? turned_exactly(a, c, b, s) : r;
-}
-
-// Eight channels from c0 on of a head whose first `rot` are rotated; `mine` and `other` hold them and their partners'
-// (of `pairs` they are their own).
-__device__ __forceinline__ void turn8(float* x, const float* other, int c0, const float* cs, const float* sn, int rot,
-                                      int pairs) {
-  if (pairs) {
-    const float4 c = *reinterpret_cast<const float4*>(cs + c0 / 2), s = *reinterpret_cast<const float4*>(sn + c0 / 2);
-    const float co[4] = {c.x, c.y, c.z, c.w}, si[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = turned(a, co[i], b, si[i]);
-      x[2 * i + 1] = turned(b, co[i], -a, si[i]);
-    }
-    return;
-  }
-  const bool first = c0 < rot / 2;
-  const int at = first ? c0 : c0 - rot / 2;
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    const float4 c = *reinterpret_cast<const float4*>(cs + at + i), s = *reinterpret_cast<const float4*>(sn + at + i);
-    const float co[4] = {c.x, c.y, c.z, c.w}, si[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[i + j] = turned(x[i + j], co[j], first ? other[i + j] : -other[i + j], si[j]);
-  }
-}
-
 __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-__device__ __forceinline__ void copy_rows4(const Append4Params& p, RowPlace* places) {
+// a c - b s: rounded to fp32 twice, or within 1.5 units of the last place.
+template <bool kExact>
+__device__ __forceinline__ float turned(float a, float c, float b, float s) {
+  if (!kExact) return a * c - b * s;
+  const float p = __fmul_rn(b, s), e = __fmaf_rn(b, s, -p);
+  return __fsub_rn(__fmaf_rn(a, c, -p), e);
+}
+// The same in 64 bits, in which the products are exact, rounded to odd in fp32: what then rounds to bf16 is rounded once.
+__device__ __forceinline__ float turned_exactly(float a, float c, float b, float s) {
+  const double x = static_cast<double>(a) * c - static_cast<double>(b) * s;
+  const float f = __double2float_rz(x);
+  return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+// `least` so far and two values' lower halves less 0x7FFA, modulo 2^16, where a border of bf16 is 6 (a carry may add 1 to the upper):
+// up to 12 the side of the border is open.
+__device__ __forceinline__ uint32_t border(uint32_t least, float x, float y) {
+  return __vminu2(least, __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x5410) + 0x80068006u);
+}
+__device__ __forceinline__ bool at_border(uint32_t least) { return (least & 0xFFFFu) <= 12u || (least >> 16) <= 12u; }
+
+// Sixteen channels, x and y, turned by eight angles: channel i of x with i of y, or neighbours of either.
+struct Sixteen {
+  uint4 x, y;
+};
+template <bool kNeighbours, typename F>
+__device__ __forceinline__ Sixteen turn_with(const Sixteen& w, const float* cs, const float* sn, F turn) {
+  float x[8], y[8], co[8], si[8];
+  unpack8(w.x, x);
+  unpack8(w.y, y);
+#pragma unroll
+  for (int k = 0; k < 8; k += 4) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + k), s = *reinterpret_cast<const float4*>(sn + k);
+    co[k] = c.x, co[k + 1] = c.y, co[k + 2] = c.z, co[k + 3] = c.w;
+    si[k] = s.x, si[k + 1] = s.y, si[k + 2] = s.z, si[k + 3] = s.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& p = kNeighbours ? (i < 4 ? x[2 * i] : y[2 * i - 8]) : x[i];
+    float& q = kNeighbours ? (i < 4 ? x[2 * i + 1] : y[2 * i - 7]) : y[i];
+    const float a = p, b = q;
+    p = turn(a, co[i], b, si[i]);
+    q = turn(b, co[i], -a, si[i]);
+  }
+  return {pack8(x), pack8(y)};
+}
+template <bool kNeighbours>
+__device__ __noinline__ Sixteen turn16_exactly(Sixteen w, const float* cs, const float* sn) {
+  return turn_with<kNeighbours>(w, cs, sn, turned_exactly);
+}
+template <bool kNeighbours>
+__device__ __forceinline__ Sixteen turn16(const Sixteen& w, const float* cs, const float* sn, bool exact) {
+  if (!exact) return turn_with<kNeighbours>(w, cs, sn, turned<false>);
+  uint32_t least = 0xFFFFFFFFu;
+  float last = 0.f;
+  int n = 0;
+  const Sixteen z = turn_with<kNeighbours>(w, cs, sn, [&](float a, float c, float b, float s) {
+    const float x = turned<true>(a, c, b, s);
+    if (n++ & 1) least = border(least, last, x);
+    last = x;
+    return x;
+  });
+  return at_border(least) ? turn16_exactly<kNeighbours>(w, cs, sn) : z;
+}
+
+// Codes of eight of a block's values. Where the block has an infinity, a NaN or what is too large (its scale is then the largest) each is
+// held as the nearest there is.
+__device__ __forceinline__ uint32_t block_codes(const uint4& w, float inv, bool odd) {
+  float f[8];
+  unpack8(w, f);
+  if (odd) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = f[e] == f[e] ? fminf(fmaxf(f[e], -430080.f), 430080.f) : 0.f;
+  }
+  return four_codes(f, inv);
+}
+
+// Where a row's tokens stand: of head 0, counted through the pool (check_four); kNoRow: the row is not appended.
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+struct RowToken {
+  uint32_t token;
+  int slot, pos;
+};
+__device__ __forceinline__ RowToken row_token(const AppendParams& p, int row) {
+  const RowPlace x = row_place(p, row);
+  return {x.page < 0 ? kNoRow : static_cast<uint32_t>(x.page) * p.a.Hkv * p.a.page_size + x.slot, x.slot, x.pos};
+}
+
+enum Turn { kNone, kHalves, kPairs };  // channel i with i + rot / 2; 2 i with 2 i + 1
+
+template <Turn kTurn, int kR>  // kR: rows of a thread
+__device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* places, uint4* exchange) {
   const PagedArgs& a = p.a;
-  const int hs = a.d == 128 ? 4 : 3, hp = 1 << hs, blocks = a.d / kFourBlock;  // units of a head
+  const int hs = a.d == 128 ? 3 : 2, hp = 1 << hs, blocks = a.d / kFourBlock;  // units of a head
   const int nk = a.Hkv << hs;
   const CopyShape x = copy_shape(2 * nk + (p.qn ? a.H << hs : 0));
   const int tid = threadIdx.x, lane = tid & 31, block = blockIdx.x - p.gate_blocks;
-  const int chunk = block % x.chunks, row0 = block / x.chunks * (kRows * x.side);
+  const int chunk = block % x.chunks, row0 = block / x.chunks * (kR * x.side);
   const int sub = x.side > 1 ? tid / x.per_row : 0, at = x.side > 1 ? tid - sub * x.per_row : chunk * kThreads + tid;
-  // Units of a row are a multiple of 8 (16 with 128 channels) and so are a block's: a head's lie in neighbouring lanes.
+  // Units of a row are a multiple of 4 (8 with 128 channels) and so are a block's: a head's lie in neighbouring lanes.
   const bool live = at < x.per_row && sub < x.side, is_v = at >= nk && at < 2 * nk, is_q = at >= 2 * nk;
-  const int w = is_q ? at - 2 * nk : is_v ? at - nk : at, h = w >> hs, j = w & (hp - 1), c0 = j * 8;
+  const int w = is_q ? at - 2 * nk : is_v ? at - nk : at, h = w >> hs, j = w & (hp - 1);
+  const int half = p.rot / 2;
+  const bool apart = kTurn == kHalves && !is_v && j * 8 < half;
+  const int c0 = (apart ? j : 2 * j) * 8, c1 = apart ? c0 + half : c0 + 8;
+  const bool turns = kTurn != kNone && !is_v && c0 < p.rot;
   const long long stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_q ? p.qn : is_v ? p.vn : p.kn) +
-                             (size_t)(row0 + sub) * stride + h * a.d + c0;
-  uint4 u[kRows];
+                             (size_t)(row0 + sub) * stride + h * a.d;
+  Sixteen u[kR];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    u[i] = make_uint4(0, 0, 0, 0);
-    if (live && row0 + sub + i * x.side < a.rows) u[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+  for (int i = 0; i < kR; ++i) {
+    if (live && row0 + sub + i * x.side < a.rows) {
+      u[i].x = __ldcs(reinterpret_cast<const uint4*>(src + c0));
+      u[i].y = __ldcs(reinterpret_cast<const uint4*>(src + c1));
+    }
     src += x.side * stride;
   }
-  const int rows = min(kRows * x.side, a.rows - row0);
-  for (int r = tid; r < rows; r += kThreads) places[r] = row_place(p, row0 + r);
+  const int rows = min(kR * x.side, a.rows - row0);
+  for (int r = tid; r < rows; r += kThreads) places[r] = row_token(p, row0 + r);
   __syncthreads();
-  const int half = p.rot / 16;  // units of half the rotated channels
-  const int partner = (lane & ~(hp - 1)) | (j < half ? j + half : j - half);
-  bool odd = false;
+  if (!live) return;  // a head's lanes live or not together
+  const uint32_t head_lanes = (hp == 8 ? 0xFFu : 0xFu) << (lane & ~(hp - 1));
+  const int b = j >> 1, t = 2 * j & 3, head = h * a.page_size;  // of the two neighbouring chunks that are held
+  const float* cs = p.cos + (kTurn == kPairs ? c0 / 2 : c0);
+  const float* sn = p.sin + (kTurn == kPairs ? c0 / 2 : c0);
+  __nv_bfloat16* q_out = static_cast<__nv_bfloat16*>(p.qo) + ((size_t)(row0 + sub) * a.H + h) * a.d;
+  uint4* mine = exchange + (tid & ~(hp - 1)) * 2;  // a head's channels
+#pragma unroll 1
+  for (int r = sub; r < rows; r += x.side) {
+    Sixteen y = u[0];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = i * x.side + sub;
-    float f[8], o[8];
-    unpack8(u[i], f);
-    if (p.rot > 0 && !p.pairs) {
-      uint4 y;
-      y.x = __shfl_sync(0xffffffffu, u[i].x, partner);
-      y.y = __shfl_sync(0xffffffffu, u[i].y, partner);
-      y.z = __shfl_sync(0xffffffffu, u[i].z, partner);
-      y.w = __shfl_sync(0xffffffffu, u[i].w, partner);
-      unpack8(y, o);
-    }
-    const RowPlace g = live && r < rows ? places[r] : RowPlace{-1, 0, 0};
-    if (g.page >= 0 && !is_v && c0 < p.rot) {
-      turn8(f, o, c0, p.cos + (size_t)g.pos * (p.rot / 2), p.sin + (size_t)g.pos * (p.rot / 2), p.rot, p.pairs);
-      u[i] = pack8(f);
-      unpack8(u[i], f);
-    }
-    float most = 0.f;
-    bool nan = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      most = fmaxf(most, fabsf(f[e]));
-      nan |= f[e] != f[e];
-    }
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    if (g.page < 0) continue;
+    for (int i = 0; i + 1 < kR; ++i) u[i] = u[i + 1];
+    const RowToken g = places[r];  // of the row: the same for all of its lanes
+    if (g.token == kNoRow) continue;
+    if (turns) y = turn16<kTurn == kPairs>(y, cs + (size_t)g.pos * half, sn + (size_t)g.pos * half, !is_q);
     if (is_q) {
-      __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.qo) + ((size_t)(row0 + r) * a.H + h) * a.d + c0), u[i]);
+      __nv_bfloat16* dst = q_out + (size_t)(r - sub) * a.H * a.d;
+      __stcs(reinterpret_cast<uint4*>(dst + c0), y.x);
+      __stcs(reinterpret_cast<uint4*>(dst + c1), y.y);
       continue;
     }
-    odd |= nan || most > 430080.f;
-    const uint32_t byte = four_scale_byte(most);
+    if (kTurn == kHalves && !is_v) {
+      mine[c0 >> 3] = y.x;
+      mine[c1 >> 3] = y.y;
+      __syncwarp(head_lanes);
+      y = {mine[2 * j], mine[2 * j + 1]};
+      __syncwarp(head_lanes);
+    }
+    uint32_t most = __vmaxu2(four_most(y.x), four_most(y.y));
+    most = __vmaxu2(most, __shfl_xor_sync(0x3u << (lane & ~1), most, 1));
+    const float top = __uint_as_float(max(most & 0xFFFFu, most >> 16) << 16);
+    const uint32_t byte = four_scale_byte(top);
     const float inv = byte ? 1.f / four_scale(byte) : 0.f;
-    uint32_t code = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) code |= four_code(f[e], inv) << (4 * e);
-    const int b = j >> 2, t = j & 3;
-    uint8_t* row = static_cast<uint8_t*>(is_v ? a.v : a.k) + four_row(a, g.page, h, g.slot);
-    *reinterpret_cast<uint32_t*>(row + (is_v ? four_v_word(b, t, g.slot, blocks) : four_k_word(b, t, blocks))) =
-        is_v ? code : four_k_order(code);
-    if (t == 0) {
-      if (is_v)
-        p.vs[four_scale_row(a, g.page, h, g.slot & ~15) + four_v_scale(b, g.slot, blocks)] = static_cast<uint8_t>(byte);
-      else
-        p.ks[four_scale_row(a, g.page, h, g.slot) + b] = static_cast<uint8_t>(byte);
+    const bool odd = !(top <= 430080.f);
+    if (odd && a.err) atomicOr(a.err, DEV_ERR_RANGE);
+    const uint32_t w0 = block_codes(y.x, inv, odd), w1 = block_codes(y.y, inv, odd);
+    const uint32_t token = g.token + head;
+    uint8_t* row = static_cast<uint8_t*>(is_v ? a.v : a.k) + (uint64_t)token * (a.d / 2);
+    if (is_v) {
+      *reinterpret_cast<uint2*>(row + four_v_word(b, t, g.slot, blocks)) = make_uint2(w0, w1);
+      if (t == 0) p.vs[(uint64_t)(token - (g.slot & 15)) * blocks + four_v_scale(b, g.slot, blocks)] = static_cast<uint8_t>(byte);
+    } else {
+      *reinterpret_cast<uint32_t*>(row + four_k_word(b, t, blocks)) = four_k_order(w0);
+      *reinterpret_cast<uint32_t*>(row + four_k_word(b, t + 1, blocks)) = four_k_order(w1);
+      if (t == 0) p.ks[(uint64_t)token * blocks + b] = static_cast<uint8_t>(byte);
     }
   }
-  if (odd && a.err) atomicOr(a.err, DEV_ERR_RANGE);
 }
 
-__global__ void __launch_bounds__(kThreads, 8) cache_append4_kernel(const Append4Params p) {
-  __shared__ union {
+template <Turn kTurn, int kR>
+__global__ void __launch_bounds__(kThreads, 6) cache_append4_kernel(const Append4Params p) {
+  __shared__ __align__(16) union {
     float zs[128][kGateHeads + 1];
-    RowPlace places[kBlockRows];
+    struct {
+      uint4 exchange[kTurn == kHalves ? 2 * kThreads : 1];
+      RowToken places[kBlockRows];
+    } rows;
   } sh;
   grid_dep_wait();
   grid_dep_trigger();
   if (static_cast<int>(blockIdx.x) < p.gate_blocks)
     gate_block(p, sh.zs);
   else
-    copy_rows4(p, sh.places);
+    copy_rows4<kTurn, kR>(p, sh.rows.places, sh.rows.exchange);
 }
 
-// The values of rows, 8 channels a thread: s u has 7 significant bits, so bf16 has it exactly.
+// The values of rows, 8 channels a thread: s u has 7 significant bits, so bf16 has it exactly. Bound by the trips to memory of a row's
+// place and then its codes: a thread has four rows' on their way.
 struct Read4Params : AppendParams {
   const uint8_t* ks;
   const uint8_t* vs;
   __nv_bfloat16* ko;
   __nv_bfloat16* vo;
 };
-__global__ void __launch_bounds__(kThreads, 8) cache_read4_kernel(const Read4Params p) {
-  __shared__ RowPlace places[kBlockRows];
+__global__ void __launch_bounds__(kThreads, 12) cache_read4_kernel(const Read4Params p) {
+  __shared__ RowToken places[kBlockRows];
   grid_dep_wait();
   grid_dep_trigger();
   const PagedArgs& a = p.a;
@@ -186,42 +242,49 @@ __global__ void __launch_bounds__(kThreads, 8) cache_read4_kernel(const Read4Par
   const bool live = at < x.per_row && sub < x.side, is_v = at >= nk;
   const int w = is_v ? at - nk : at, h = w >> hs, j = w & ((1 << hs) - 1), b = j >> 2, t = j & 3;
   const int rows = min(kRows * x.side, a.rows - row0);
-  for (int r = tid; r < rows; r += kThreads) places[r] = row_place(p, row0 + r);
+  for (int r = tid; r < rows; r += kThreads) places[r] = row_token(p, row0 + r);
   __syncthreads();
   if (!live) return;
-  __nv_bfloat16* out = is_v ? p.vo : p.ko;
-  const long long stride = is_v ? p.v_stride : p.k_stride;
+  uint32_t words[kRows], bytes[kRows];
+  bool here[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = i * x.side + sub;
-    if (r >= rows) break;
-    const RowPlace g = places[r];
-    if (g.page < 0) continue;
-    const uint8_t* row = static_cast<const uint8_t*>(is_v ? a.v : a.k) + four_row(a, g.page, h, g.slot);
-    uint32_t code =
-        *reinterpret_cast<const uint32_t*>(row + (is_v ? four_v_word(b, t, g.slot, blocks) : four_k_word(b, t, blocks)));
-    if (!is_v) code = four_k_code(code);
-    const float s = four_scale(is_v ? p.vs[four_scale_row(a, g.page, h, g.slot & ~15) + four_v_scale(b, g.slot, blocks)]
-                                    : p.ks[four_scale_row(a, g.page, h, g.slot) + b]);
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = s * static_cast<float>(static_cast<int>(code >> (4 * e) & 15u) - 8);
-    __stcs(reinterpret_cast<uint4*>(out + (size_t)(row0 + r) * stride + h * a.d + j * 8), pack8(f));
+    const RowToken g = r < rows ? places[r] : RowToken{kNoRow, 0, 0};
+    here[i] = g.token != kNoRow;
+    if (!here[i]) continue;
+    const uint32_t token = g.token + h * a.page_size;
+    const uint8_t* row = static_cast<const uint8_t*>(is_v ? a.v : a.k) + (uint64_t)token * (a.d / 2);
+    words[i] = __ldcs(reinterpret_cast<const uint32_t*>(row + (is_v ? four_v_word(b, t, g.slot, blocks) : four_k_word(b, t, blocks))));
+    bytes[i] = is_v ? p.vs[(uint64_t)(token - (g.slot & 15)) * blocks + four_v_scale(b, g.slot, blocks)]
+                    : p.ks[(uint64_t)token * blocks + b];
   }
+  const long long stride = is_v ? p.v_stride : p.k_stride;
+  __nv_bfloat16* out = (is_v ? p.vo : p.ko) + (size_t)(row0 + sub) * stride + h * a.d + j * 8;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (here[i]) __stcs(reinterpret_cast<uint4*>(out + (size_t)i * x.side * stride), four_values(words[i], bytes[i], is_v));
 }
 
-int row_units4(const PagedArgs& a, bool with_q) { return (2 * a.Hkv + (with_q ? a.H : 0)) * (a.d / 8); }
+int row_units4(const PagedArgs& a, bool with_q, int channels) { return (2 * a.Hkv + (with_q ? a.H : 0)) * (a.d / channels); }
 
 }  // namespace
 
-bool append4_fits(const PagedArgs& a, bool with_q) { return append_blocks(a, row_units4(a, with_q)).fit(); }
+bool append4_fits(const PagedArgs& a, bool with_q) { return append_blocks(a, row_units4(a, with_q, 8)).fit(); }
 
 cudaError_t launch_cache_append4(const CacheAppendArgs& x, void* ks, void* vs, cudaStream_t s) {
   Append4Params p = {};
   static_cast<AppendParams&>(p) = append_params(x);
   p.ks = static_cast<uint8_t*>(ks);
   p.vs = static_cast<uint8_t*>(vs);
-  return launch_append(cache_append4_kernel, p, row_units4(p.a, p.qn != nullptr), s);
+  const int units = row_units4(p.a, p.qn != nullptr, 16);
+  if (append_blocks(p.a, units, 1).copies <= 6 * kSMs)  // one row a thread where those are on the SMs at once
+    return launch_append(p.rot == 0 ? cache_append4_kernel<kNone, 1>
+                                    : p.pairs ? cache_append4_kernel<kPairs, 1> : cache_append4_kernel<kHalves, 1>,
+                         p, units, s, 1);
+  return launch_append(p.rot == 0 ? cache_append4_kernel<kNone, kRows>
+                                  : p.pairs ? cache_append4_kernel<kPairs, kRows> : cache_append4_kernel<kHalves, kRows>,
+                       p, units, s);
 }
 
 cudaError_t launch_cache_read4(const CacheAppendArgs& x, void* ks, void* vs, cudaStream_t s) {
@@ -232,7 +295,7 @@ cudaError_t launch_cache_read4(const CacheAppendArgs& x, void* ks, void* vs, cud
   p.ko = static_cast<__nv_bfloat16*>(const_cast<void*>(x.k));
   p.vo = static_cast<__nv_bfloat16*>(const_cast<void*>(x.v));
   TraceScope trace("cache_read", s);
-  const cudaError_t e = launch_dependent(cache_read4_kernel, dim3(static_cast<unsigned>(append_blocks(p.a, row_units4(p.a, false)).copies)),
+  const cudaError_t e = launch_dependent(cache_read4_kernel, dim3(static_cast<unsigned>(append_blocks(p.a, row_units4(p.a, false, 8)).copies)),
                                          dim3(kThreads), 0, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -14,10 +14,12 @@ typedef fox_status (*append4_fn)(const fox_cache4*, const fox_batch*, int, const
                                  const float*, int64_t, const fox_rotary*, void*, size_t, void*);
 typedef fox_status (*decode4_fn)(const fox_cache4*, const fox_batch*, int, const void*, int64_t, float, int, void*, float*,
                                  void*, size_t, void*);
+typedef fox_status (*read4_fn)(const fox_cache4*, const fox_batch*, int, void*, int64_t, void*, int64_t, void*, size_t, void*);
 static append_fn g_append;
 static decode_fn g_decode;
 static append4_fn g_append4;
 static decode4_fn g_decode4;
+static read4_fn g_read4;
 
 static void* ptr(PyObject* x) { return (void*)(uintptr_t)PyLong_AsUnsignedLongLong(x); }
 static int64_t num(PyObject* x) { return (int64_t)PyLong_AsLongLong(x); }
@@ -30,16 +32,18 @@ static int small(PyObject* x) {
 
 static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (n != 4) return PyErr_Format(PyExc_TypeError, "bind takes 4 addresses");
+  if (n != 5) return PyErr_Format(PyExc_TypeError, "bind takes 5 addresses");
   append_fn f = (append_fn)ptr(a[0]);
   decode_fn g = (decode_fn)ptr(a[1]);
   append4_fn f4 = (append4_fn)ptr(a[2]);
   decode4_fn g4 = (decode4_fn)ptr(a[3]);
+  read4_fn r4 = (read4_fn)ptr(a[4]);
   if (PyErr_Occurred()) return NULL;
   g_append = f;
   g_decode = g;
   g_append4 = f4;
   g_decode4 = g4;
+  g_read4 = r4;
   Py_RETURN_NONE;
 }
 
@@ -115,12 +119,31 @@ static PyObject* decode4(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return decode_over(a, n, 1);
 }
 
+/* cache, batch, rows, k, k_stride, v, v_stride, ws, ws_bytes, stream */
+static PyObject* read4(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 10 || !g_read4) return PyErr_Format(PyExc_TypeError, "read4 takes 10 numbers, after bind");
+  const fox_cache4* c = (const fox_cache4*)ptr(a[0]);
+  const fox_batch* b = (const fox_batch*)ptr(a[1]);
+  const int rows = small(a[2]);
+  void *k = ptr(a[3]), *v = ptr(a[5]), *ws = ptr(a[7]), *stream = ptr(a[9]);
+  const int64_t ks = num(a[4]), vs = num(a[6]);
+  const size_t bytes = (size_t)PyLong_AsUnsignedLongLong(a[8]);
+  if (PyErr_Occurred()) return NULL;
+  fox_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_read4(c, b, rows, k, ks, v, vs, ws, bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong((long)st);
+}
+
 static PyMethodDef methods[] = {
-    {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind(fox_cache_append_low, fox_decode, fox_cache4_append, fox_cache4_decode): their addresses"},
+    {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind(fox_cache_append_low, fox_decode, fox_cache4_append, fox_cache4_decode, fox_cache4_read): their addresses"},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "fox_cache_append_low; returns its status"},
     {"decode", (PyCFunction)(void (*)(void))decode, METH_FASTCALL, "fox_decode; returns its status"},
     {"append4", (PyCFunction)(void (*)(void))append4, METH_FASTCALL, "fox_cache4_append; returns its status"},
     {"decode4", (PyCFunction)(void (*)(void))decode4, METH_FASTCALL, "fox_cache4_decode; returns its status"},
+    {"read4", (PyCFunction)(void (*)(void))read4, METH_FASTCALL, "fox_cache4_read; returns its status"},
     {NULL, NULL, 0, NULL},
 };
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_foxcall", NULL, -1, methods, NULL, NULL, NULL, NULL};

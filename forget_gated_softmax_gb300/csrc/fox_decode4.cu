@@ -727,14 +727,10 @@ __global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_co
 #pragma unroll 4
   for (int i = tid; i < S * words; i += kSpreadThreads) {
     const int slot = i / words, w = i - slot * words, b = w >> 2, t = w & 3;
-    uint32_t code = *reinterpret_cast<const uint32_t*>(from + (size_t)slot * (a.d / 2) +
-                                                       (is_v ? four_v_word(b, t, slot, blocks) : four_k_word(b, t, blocks)));
-    if (!is_v) code = four_k_code(code);
-    const float s = four_scale(scales[is_v ? (slot & ~15) * blocks + four_v_scale(b, slot, blocks) : slot * blocks + b]);
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = slot < live ? s * static_cast<float>(static_cast<int>(code >> (4 * e) & 15u) - 8) : 0.f;
-    out[i] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    const uint32_t code = *reinterpret_cast<const uint32_t*>(from + (size_t)slot * (a.d / 2) +
+                                                             (is_v ? four_v_word(b, t, slot, blocks) : four_k_word(b, t, blocks)));
+    const uint32_t byte = scales[is_v ? (slot & ~15) * blocks + four_v_scale(b, slot, blocks) : slot * blocks + b];
+    out[i] = slot < live ? four_values(code, byte, is_v) : make_uint4(0, 0, 0, 0);
   }
 }
 

@@ -38,11 +38,6 @@ FOX_HD uint32_t four_k_order(uint32_t code) {
                      (code >> 24 & 15u) << 16 | (code >> 12 & 15u) << 20 | (code >> 4 & 15u) << 24 | (code >> 20 & 15u) << 28;
   return w >> 2 | w << 30;
 }
-FOX_HD uint32_t four_k_code(uint32_t w) {
-  w = w << 2 | w >> 30;
-  return (w >> 8 & 15u) | (w >> 24 & 15u) << 4 | (w >> 4 & 15u) << 8 | (w >> 20 & 15u) << 12 | (w >> 12 & 15u) << 16 |
-         (w >> 28 & 15u) << 20 | (w >> 16 & 15u) << 24 | (w & 15u) << 28;
-}
 
 // ---- scales: 5 exponent bits (bias 15), 3 mantissa bits ----
 FOX_HD float bits_float(uint32_t x) {
@@ -74,12 +69,47 @@ FOX_HD uint32_t four_scale_byte(float amax) {
   if (t < 0x1p-14f) return static_cast<uint32_t>(ceilf(t * 0x1p17f));
   return (float_bits(t) + 0xFFFFFu >> 20) - (112u << 3);
 }
-// u + 8 of x, inv = 1 / s (0 where s is): |x| / s rounded, halves up. A bf16 value over s is a half or 2^-11 away from it,
-// which the 2^-12 makes up for the rounding of inv and of the product.
+// u + 8 of a finite x of at most 7 s, inv = 1 / s (0 where s is): floor(x / s + 8.5), with 2^-12 away from zero for the halves: a bf16
+// value over s is a half or 2^-11 away from it, so that this makes up for the roundings of inv and of the product. On the device left in
+// the low bits by an addition of 2^23 that rounds down.
 FOX_HD uint32_t four_code(float x, float inv) {
-  const float y = fabsf(x) * inv + (0.5f + 0x1p-12f);
-  const int u = y >= kFourTop ? kFourTop : y >= 1.f ? static_cast<int>(y) : 0;  // NaN: 0
-  return static_cast<uint32_t>(8 + (x < 0.f ? -u : u));
+  const float half = 8.5f + copysignf(0x1p-12f, x);
+#ifdef __CUDA_ARCH__
+  return __float_as_uint(__fadd_rz(fmaf(x, inv, half), 8388608.f)) - 0x4B000000u;
+#else
+  return static_cast<uint32_t>(std::fma(x, inv, half));
+#endif
 }
+
+#ifdef __CUDACC__
+// ---- eight channels at once, on the device ----
+__device__ __forceinline__ uint32_t four_bf16(uint32_t n, uint32_t s2) {  // nibbles at bits 3..0 of both halves: s u, exactly
+  uint32_t x, y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(n), "r"(0x000F000Fu), "r"(0x43004300u));  // 128 + n
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xC308C308u));                          // - 136
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(y), "r"(s2));
+  return x;
+}
+// The bf16 values of a word of K or of V.
+__device__ __forceinline__ uint4 four_values(uint32_t w, uint32_t byte, bool is_v) {
+  const uint32_t s = float_bits(four_scale(byte)) >> 16, s2 = s << 16 | s;
+  if (is_v) {  // a byte's nibbles 16 bits apart: times 0x1001
+    const uint32_t b[4] = {(w & 255u) * 0x1001u, (w >> 8 & 255u) * 0x1001u, (w >> 16 & 255u) * 0x1001u, (w >> 24) * 0x1001u};
+    return make_uint4(four_bf16(b[0], s2), four_bf16(b[1], s2), four_bf16(b[2], s2), four_bf16(b[3], s2));
+  }
+  return make_uint4(four_bf16(w >> 6, s2), four_bf16(w >> 2, s2), four_bf16(w >> 10, s2), four_bf16(w >> 14 | w << 18, s2));
+}
+// Largest magnitude of eight bf16 as bits of two; of a NaN larger than an infinity's.
+__device__ __forceinline__ uint32_t four_most(const uint4& w) {
+  return __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+}
+// Codes of eight values: nibble c is channel c's.
+__device__ __forceinline__ uint32_t four_codes(const float* f, float inv) {
+  uint32_t code = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) code += four_code(f[e], inv) << (4 * e);
+  return code;
+}
+#endif
 
 }  // namespace fox

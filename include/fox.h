@@ -380,7 +380,8 @@ fox_status fox_decode(const fox_cache* c, const fox_batch* s, int rows, const vo
  *   vs  [num_pages, Hkv, page_size / 16, 4, d / 32, 4]  its scales, token j of 16 at [j % 8 / 2][b][2 (j % 2) + j / 8]
  *   g, gbase as in fox_cache; g_low as in fox_cache_append_low, or NULL.
  * Types of k, v and q, and of o: bf16. A magnitude above 430080, an infinity or a NaN sets the error word when it is
- * appended and is held as the nearest the block has (a NaN as 0): what was appended is always finite. Nothing has to be initialised.
+ * appended and is held as the nearest there is (a NaN as 0), its block with the largest scale: what was appended is always finite.
+ * Nothing has to be initialised.
  */
 typedef struct fox_cache4 {
   int num_pages; /* as in fox_cache, with the same limits; num_pages * page_size * Hkv below 2^32 */
@@ -405,7 +406,7 @@ size_t fox_cache4_workspace_bytes(const fox_cache4* c, const fox_batch* s, int r
 
 /*
  * fox_cache_append into a 4-bit cache. K is first rotated where rot is given, and then rounded to bf16: to the nearest of the
- * exact a cos - b sin, so that what the cache holds follows from the inputs bit for bit (q_out the same).
+ * exact a cos - b sin, so that what the cache holds follows from the inputs bit for bit. q_out is as fox_cache_append's.
  */
 fox_status fox_cache4_append(const fox_cache4* c, const fox_batch* s, int rows, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, const float* z, int64_t z_stride, const fox_rotary* rot,
