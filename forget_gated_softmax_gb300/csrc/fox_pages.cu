@@ -1,8 +1,10 @@
 // Pages of the pool: one step's bookkeeping, packing, and copies of pages. C ABI, validation and kernels; the contract is in
 // include/fox.h.
 //
-// step and compact are integers all: what bounds them is latency. One CTA does each: references, places by prefix sums over the sequences
-// and over the pages, table entries.
+// step and compact are integers all: what bounds them is latency, a dependent trip to memory or a barrier after the other, so that they take
+// few of both. step: one CTA for what hangs together, behind a kernel that copies references and table rows where the new state is
+// apart from the old. compact: a count of the pages in use by blocks of them, then every block knows its pages' ranks, then tables; a small
+// pool by one CTA.
 // copy is bound by memory: each page read once and written once, 16 KB a block.
 #include <cstdint>
 
@@ -15,7 +17,7 @@
 namespace fox {
 namespace {
 
-constexpr int kPageThreads = 1024;
+constexpr int kPageThreads = 1024, kCopyThreads = 256;
 
 struct Pool {
   int num_pages, shift, B, stride, prefix_len;  // page_size = 1 << shift
@@ -67,133 +69,169 @@ struct StepParams {
   const int32_t* parent;
   const int32_t* add;
   int32_t* copies;
+  int32_t* list;  // [num_pages] of the workspace: free pages, the lowest first
   uint32_t* err;
 };
 
-// What a new sequence begins with and asks for.
-struct Want {
-  int src, len, n0, n1, last;  // parent (-1: none), its tokens, pages held and needed; page of its last token
-};
+__device__ __forceinline__ int parent_of(const StepParams& p, int b) {
+  const int src = p.parent ? p.parent[b] : b;
+  if (src >= -1 && src < p.in.B) return src;
+  atomicOr(p.err, DEV_ERR_BOUNDS);
+  return -1;
+}
 
-__global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepParams p) {
-  constexpr int kEach = kMaxSeqs / kPageThreads;
-  __shared__ int kids[kMaxSeqs];   // children of the old sequences; then the pages that stand to be copied
-  __shared__ int upto[kMaxSeqs];   // pages wanted by the new sequences up to each
-  __shared__ int scratch[32];
+// What of the old state the new one begins with: references, and a row of the table a block.
+__global__ void __launch_bounds__(kCopyThreads) pages_begin_kernel(const StepParams p) {
+  const Pool &in = p.in, &out = p.out;
   grid_dep_wait();
   grid_dep_trigger();
-  const Pool &in = p.in, &out = p.out;
-  const int tid = threadIdx.x;
-  for (int b = tid; b < in.B; b += kPageThreads) kids[b] = 0;
+  const int b = blockIdx.x, tid = threadIdx.x;
   if (out.refs != in.refs)
-    for (int i = tid; i < in.num_pages; i += kPageThreads) out.refs[i] = in.refs[i];
+    for (int i = b * kCopyThreads + tid; i < in.num_pages; i += gridDim.x * kCopyThreads) out.refs[i] = in.refs[i];
+  if (b >= out.B || out.table == in.table) return;
+  const int src = parent_of(p, b);
+  if (src < 0) return;
+  const int n = pages_of(in, own_tokens(in, in.lens[src], p.err));
+  for (int c = tid; c < n; c += kCopyThreads) out.table[(size_t)b * out.stride + c] = in.table[(size_t)src * in.stride + c];
+}
+
+__global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepParams p) {
+  constexpr int kEach = kMaxSeqs / kPageThreads, kLoad = 16, kNoPages = 0x7FFFFFFF;
+  __shared__ int kids[kMaxSeqs];       // children of the old sequences; then the shared pages that may have to be copied, -1: none
+  __shared__ int upto[kMaxSeqs];       // pages wanted by the new sequences up to each
+  __shared__ int first_new[kMaxSeqs];  // a new sequence's entry for its first wanted page; kNoPages: it gets none. Before, old
+                                       // sequences whose references change
+  __shared__ int scratch[32], changed;
+  const Pool &in = p.in, &out = p.out;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int b = tid; b < in.B; b += kPageThreads) kids[b] = 0;
+  if (tid == 0) changed = 0;
+  grid_dep_wait();
+  grid_dep_trigger();
   __syncthreads();
-  Want w[kEach];
+  // Sequence b is thread b's, and b + 1024 too.
+  int len[kEach], n0[kEach], n1[kEach], add[kEach], last[kEach];
   bool grows[kEach], part[kEach];
+#pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int b = tid * kEach + i;
-    w[i] = {-1, 0, 0, 0, -1};
+    const int b = tid + i * kPageThreads;
+    last[i] = -1;
+    len[i] = n0[i] = n1[i] = add[i] = 0;
     grows[i] = part[i] = false;
     if (b >= out.B) continue;
-    int src = p.parent ? p.parent[b] : b;
-    if (src < -1 || src >= in.B) {
-      atomicOr(p.err, DEV_ERR_BOUNDS);
-      src = -1;
-    }
-    int len = src >= 0 ? in.lens[src] : 0, own = own_tokens(in, len, p.err);
+    const int src = parent_of(p, b);
+    len[i] = src >= 0 ? in.lens[src] : 0;
+    add[i] = p.add[b];
     if (src >= 0) atomicAdd(&kids[src], 1);
-    if (own < 0) len = own = 0;
-    int add = p.add[b];
-    if (add < 0) {
+    int own = own_tokens(in, len[i], p.err);
+    if (own < 0) len[i] = own = 0;
+    if (add[i] < 0) {
       atomicOr(p.err, DEV_ERR_BOUNDS);
-      add = 0;
+      add[i] = 0;
     }
-    const int n0 = pages_of(in, own);
+    n0[i] = pages_of(in, own);
     const long long cap = (long long)in.stride << in.shift;
-    grows[i] = add > 0 && own + (long long)add <= cap;
-    if (add > 0 && !grows[i]) atomicOr(p.err, DEV_ERR_BOUNDS);
-    w[i] = {src, len, n0, grows[i] ? pages_of(in, own + add) : n0, n0 > 0 ? in.table[(size_t)src * in.stride + n0 - 1] : -1};
-    part[i] = grows[i] && (own & ((1 << in.shift) - 1)) != 0 && w[i].last >= 0 && w[i].last < in.num_pages;
-    upto[b] = add;  // for now
+    grows[i] = add[i] > 0 && own + (long long)add[i] <= cap;
+    if (add[i] > 0 && !grows[i]) atomicOr(p.err, DEV_ERR_BOUNDS);
+    n1[i] = grows[i] ? pages_of(in, own + add[i]) : n0[i];
+    if (grows[i] && (own & ((1 << in.shift) - 1)) != 0) {
+      last[i] = in.table[(size_t)src * in.stride + n0[i] - 1];
+      part[i] = last[i] >= 0 && last[i] < in.num_pages;
+    }
   }
   __syncthreads();
   // References: every entry of an old sequence by its children less one.
-  for (int b = tid >> 5; b < in.B; b += kPageThreads / 32) {
-    const int d = kids[b] - 1, own = d ? own_tokens(in, in.lens[b], p.err) : 0, n = own > 0 ? pages_of(in, own) : 0;
-    for (int c = tid & 31; c < n; c += 32) {
-      const int id = in.table[(size_t)b * in.stride + c];
-      if (id >= 0 && id < in.num_pages)
-        atomicAdd(out.refs + id, d);
-      else
-        atomicOr(p.err, DEV_ERR_BOUNDS);
+  if (p.parent) {
+    for (int b = tid; b < in.B; b += kPageThreads) {
+      const int n = kids[b] == 1 ? 0 : pages_of(in, own_tokens(in, in.lens[b], p.err));
+      upto[b] = n;
+      if (n > 0) first_new[atomicAdd(&changed, 1)] = b;
+    }
+    __syncthreads();
+    for (int x = warp; x < changed; x += kPageThreads / 32) {
+      const int b = first_new[x], d = kids[b] - 1, n = upto[b];
+#pragma unroll 4
+      for (int c = lane; c < n; c += 32) {
+        const int id = in.table[(size_t)b * in.stride + c];
+        if (id >= 0 && id < in.num_pages)
+          atomicAdd(out.refs + id, d);
+        else
+          atomicOr(p.err, DEV_ERR_BOUNDS);
+      }
+    }
+    __threadfence();
+    __syncthreads();
+  }
+  // A partly filled last page is copied unless its other holders were copied before: who shares one looks for those.
+  int refs[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    refs[i] = part[i] ? __ldcg(out.refs + last[i]) : 0;
+    kids[tid + i * kPageThreads] = part[i] && refs[i] > 1 ? last[i] : -1;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    unsigned looks = __ballot_sync(0xffffffffu, part[i] && refs[i] > 1);
+#pragma unroll 1
+    while (looks) {  // the warp for one lane after the other
+      const int who = __ffs(looks) - 1, b = warp * 32 + who + i * kPageThreads, page = __shfl_sync(0xffffffffu, last[i], who);
+      looks &= looks - 1;
+      int before = 0;
+      for (int o = lane; o < b; o += 32) before += kids[o] == page;
+      before = __reduce_add_sync(0xffffffffu, before);
+      if (lane == who) refs[i] -= before;
     }
   }
-  __threadfence();
-  __syncthreads();
-  for (int i = 0; i < kEach; ++i)
-    if (tid * kEach + i < out.B) kids[tid * kEach + i] = part[i] ? w[i].last : -1;
-  __syncthreads();
-  // A partly filled last page is copied unless its other holders were copied before.
-  int need[kEach], add[kEach], mine = 0;
   bool copied[kEach];
+  int need[kEach], start[kEach], total = 0;
+#pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int b = tid * kEach + i;
-    need[i] = 0;
-    copied[i] = false;
-    if (b >= out.B) continue;
-    add[i] = upto[b];
-    if (part[i]) {
-      int left = __ldcg(out.refs + w[i].last);
-      for (int o = 0; o < b; ++o) left -= kids[o] == w[i].last;
-      copied[i] = left > 1;
-    }
-    need[i] = grows[i] ? w[i].n1 - w[i].n0 + copied[i] : 0;
-    mine += need[i];
+    copied[i] = part[i] && refs[i] > 1;
+    need[i] = grows[i] ? n1[i] - n0[i] + copied[i] : 0;
+    int all;
+    start[i] = total + block_before(need[i], scratch, &all);
+    total += all;
+    upto[tid + i * kPageThreads] = start[i] + need[i];
   }
-  __syncthreads();
-  int total, at = block_before(mine, scratch, &total);
-  int first[kEach];
-  for (int i = 0; i < kEach; ++i) {
-    first[i] = at;
-    at += need[i];
-    if (tid * kEach + i < out.B) upto[tid * kEach + i] = at;
-  }
-  __syncthreads();
-  // Free pages, up to as many as are wanted.
+  // Free pages, as many as are wanted, into the list.
   int found = 0;
-  for (int i0 = 0; i0 < in.num_pages && found < total; i0 += kPageThreads) {
-    const int i = i0 + tid;
-    found += __syncthreads_count(i < in.num_pages && __ldcg(out.refs + i) <= 0);
-  }
-  // Lengths, copies, and the entries that the sequences begin with.
-  bool short_of = false;
-  for (int i = 0; i < kEach; ++i) {
-    const int b = tid * kEach + i;
-    if (b >= out.B) continue;
-    const bool served = grows[i] && (need[i] == 0 || first[i] + need[i] <= found);
-    short_of |= grows[i] && !served;
-    out.lens[b] = served ? (w[i].len > 0 ? w[i].len : in.prefix_len) + add[i] : w[i].len;
-    if (!(served && copied[i])) {
-      p.copies[2 * b] = p.copies[2 * b + 1] = -1;
+#pragma unroll 1
+  for (int i0 = 0; i0 < in.num_pages && found < total; i0 += kPageThreads * kLoad) {
+    const int i = i0 + tid * kLoad;
+    uint32_t mask = 0;
+    if (i + kLoad <= in.num_pages && (reinterpret_cast<uintptr_t>(out.refs) & 15) == 0) {
+#pragma unroll
+      for (int k = 0; k < kLoad; k += 4) {
+        const int4 r = __ldcg(reinterpret_cast<const int4*>(out.refs + i + k));
+        mask |= (uint32_t(r.x <= 0) | uint32_t(r.y <= 0) << 1 | uint32_t(r.z <= 0) << 2 | uint32_t(r.w <= 0) << 3) << k;
+      }
     } else {
-      p.copies[2 * b] = w[i].last;
-      atomicSub(out.refs + w[i].last, 1);
+      for (int k = 0; k < kLoad; ++k)
+        if (i + k < in.num_pages) mask |= uint32_t(__ldcg(out.refs + i + k) <= 0) << k;
     }
-    for (int c = 0; c < w[i].n0; ++c)
-      if (out.table != in.table) out.table[(size_t)b * out.stride + c] = in.table[(size_t)w[i].src * in.stride + c];
-    kids[b] = served ? (copied[i] ? -w[i].n0 - 1 : w[i].n0) : 0x7fffffff;  // where the new pages go
+    int all, at = found + block_before(__popc(mask), scratch, &all);
+    for (; mask && at < total; mask &= mask - 1) p.list[at++] = i + __ffs(mask) - 1;
+    found += all;
+  }
+  // Lengths, and who gets what.
+  bool short_of = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = tid + i * kPageThreads;
+    if (b >= out.B) continue;
+    const bool served = grows[i] && (need[i] == 0 || start[i] + need[i] <= found), copies = served && copied[i];
+    short_of |= grows[i] && !served;
+    out.lens[b] = served ? (len[i] > 0 ? len[i] : in.prefix_len) + add[i] : len[i];
+    p.copies[2 * b] = copies ? last[i] : -1;
+    if (!copies) p.copies[2 * b + 1] = -1;
+    if (copies) atomicSub(out.refs + last[i], 1);
+    kids[b] = copies;
+    first_new[b] = served ? n0[i] - copies : kNoPages;
   }
   if (short_of) atomicOr(p.err, DEV_ERR_BOUNDS);
-  __threadfence();
   __syncthreads();
-  int rank0 = 0;
-  for (int i0 = 0; i0 < in.num_pages && rank0 < min(found, total); i0 += kPageThreads) {
-    const int i = i0 + tid;
-    const bool free = i < in.num_pages && __ldcg(out.refs + i) <= 0;
-    int all;
-    const int rank = rank0 + block_before(free, scratch, &all);
-    rank0 += all;
-    if (!free || rank >= total) continue;
+  for (int rank = tid; rank < min(found, total); rank += kPageThreads) {
     int lo = -1, hi = out.B - 1;  // upto[lo] <= rank < upto[hi]
     while (hi - lo > 1) {
       const int mid = lo + hi >> 1;
@@ -202,12 +240,12 @@ __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepPara
       else
         hi = mid;
     }
-    const int k = rank - (hi > 0 ? upto[hi - 1] : 0), to = kids[hi];
-    if (to == 0x7fffffff) continue;
-    out.refs[i] = 1;
-    const int n0 = to < 0 ? -to - 1 : to, c = to < 0 ? n0 + k - 1 : n0 + k;
-    out.table[(size_t)hi * out.stride + c] = i;
-    if (to < 0 && k == 0) p.copies[2 * hi + 1] = i;
+    const int k = rank - (hi > 0 ? upto[hi - 1] : 0), to = first_new[hi];
+    if (to == kNoPages) continue;
+    const int page = p.list[rank];
+    out.refs[page] = 1;
+    out.table[(size_t)hi * out.stride + to + k] = page;
+    if (k == 0 && kids[hi]) p.copies[2 * hi + 1] = page;
   }
 }
 
@@ -217,69 +255,156 @@ struct CompactParams {
   int2* moves;
   int max_moves;
   int32_t* used;
+  int32_t* counts;  // of the workspace: pages in use of each block of kCountPages
   uint32_t* err;
 };
 
+// Renames a table's entries; a page's place in map may stand there as -1 - its move.
+__device__ __forceinline__ int renamed(const CompactParams& p, int id) {
+  if (id < 0 || id >= p.in.num_pages) {
+    atomicOr(p.err, DEV_ERR_BOUNDS);
+    return id;
+  }
+  const int to = __ldcg(p.map + id);
+  return to >= 0 ? to : __ldcg(&p.moves[-1 - to].y);
+}
+__device__ __forceinline__ void rename_row(const CompactParams& p, int b, int first, int step) {
+  const Pool& in = p.in;
+  const int n = pages_of(in, own_tokens(in, in.lens[b], p.err));
+  for (int c = first; c < n; c += step) p.out.table[(size_t)b * in.stride + c] = renamed(p, in.table[(size_t)b * in.stride + c]);
+}
+__device__ __forceinline__ void move_refs(const CompactParams& p, int r) {
+  const int2 x = p.moves[r];
+  p.map[x.x] = x.y;
+  p.out.refs[x.y] = p.in.refs[x.x];  // in place: nobody else has either
+  p.out.refs[x.x] = 0;
+}
+
+constexpr int kCountPages = 4096, kCountEach = kCountPages / kPageThreads;
+
+// Pages in use among four of a thread's, as bits.
+__device__ __forceinline__ uint32_t in_use(const Pool& x, int i) {
+  uint32_t mask = 0;
+#pragma unroll
+  for (int k = 0; k < kCountEach; ++k)
+    if (i + k < x.num_pages) mask |= uint32_t(x.refs[i + k] > 0) << k;
+  return mask;
+}
+
+// The moves of a thread's pages i .. i + 3, `mask` of them in use, `rank` pages in use before them: of U in all, n that stand behind U,
+// m of which move. map gets a moving page's move as -1 - r where the moves are another block's too (`later`).
+__device__ __forceinline__ void place_pages(const CompactParams& p, int i, uint32_t mask, int rank, int U, int m, bool later) {
+#pragma unroll
+  for (int k = 0; k < kCountEach; ++k) {
+    const int page = i + k;
+    if (page >= p.in.num_pages) break;
+    const bool used = mask >> k & 1;
+    int to = page;
+    if (used && page >= U) {
+      const int r = U - 1 - rank;  // pages in use behind this one
+      if (r < m) {
+        p.moves[r].x = page;
+        if (later) to = -1 - r;
+      }
+      if (r == m) p.used[1] = page + 1;
+    } else if (!used && page < U && page - rank < m) {
+      p.moves[page - rank].y = page;
+    }
+    p.map[page] = to;
+    if (p.out.refs != p.in.refs) p.out.refs[page] = p.in.refs[page];
+    rank += used;
+  }
+}
+
+__global__ void __launch_bounds__(kPageThreads) pages_count_kernel(const CompactParams p) {
+  __shared__ int scratch[32];
+  grid_dep_wait();
+  grid_dep_trigger();
+  int all;
+  block_before(__popc(in_use(p.in, (blockIdx.x * kPageThreads + threadIdx.x) * kCountEach)), scratch, &all);
+  if (threadIdx.x == 0) p.counts[blockIdx.x] = all;
+}
+
+// Each block finds the moves of its pages: U and the counts before it from all counts, and how many pages move from those before U.
+__global__ void __launch_bounds__(kPageThreads) pages_place_kernel(const CompactParams p) {
+  __shared__ int scratch[32];
+  const Pool& in = p.in;
+  const int tid = threadIdx.x, blocks = gridDim.x, mine = blockIdx.x;
+  const int i = (mine * kPageThreads + tid) * kCountEach;
+  grid_dep_wait();
+  grid_dep_trigger();
+  const uint32_t mask = in_use(in, i);
+  int sum = 0, before = 0;
+  for (int b = tid; b < blocks; b += kPageThreads) {
+    const int n = __ldcg(p.counts + b);
+    sum += n;
+    before += b < mine ? n : 0;
+  }
+  int U, here, all;
+  block_before(sum, scratch, &U);
+  block_before(before, scratch, &before);
+  const int rank = before + block_before(__popc(mask), scratch, &here);  // pages in use before this thread's
+  const int edge = U / kCountPages;                                      // the block that page U is in
+  int front = 0;
+  for (int b = tid; b < min(edge, blocks); b += kPageThreads) front += __ldcg(p.counts + b);
+  const int at = edge * kCountPages + tid * kCountEach;
+  const uint32_t those = in_use(in, at);
+#pragma unroll
+  for (int k = 0; k < kCountEach; ++k) front += at + k < U && (those >> k & 1);
+  block_before(front, scratch, &all);
+  const int n = U - all, m = min(n, p.max_moves);  // free places in front, and pages behind that move there
+  place_pages(p, i, mask, rank, U, m, true);
+  for (int r = m + mine * kPageThreads + tid; r < p.max_moves; r += blocks * kPageThreads) p.moves[r] = make_int2(-1, -1);
+  if (mine == 0 && tid == 0) {
+    p.used[0] = U;
+    if (m == n) p.used[1] = U;
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) pages_rename_kernel(const CompactParams p) {
+  const Pool& in = p.in;
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int tid = threadIdx.x, b = blockIdx.x;
+  if (b < in.B) {
+    rename_row(p, b, tid, kCopyThreads);
+  } else {
+    const int first = (b - in.B) * kCopyThreads + tid, step = (gridDim.x - in.B) * kCopyThreads;
+    for (int c = first; c < pages_of(in, in.prefix_len); c += step) p.out.prefix[c] = renamed(p, in.prefix[c]);
+    for (int r = first; r < p.max_moves; r += step)
+      if (p.moves[r].x >= 0) move_refs(p, r);
+  }
+}
+
+// A small pool by one CTA: the same in one launch.
 __global__ void __launch_bounds__(kPageThreads) pages_compact_kernel(const CompactParams p) {
   __shared__ int scratch[32];
   grid_dep_wait();
   grid_dep_trigger();
-  const Pool &in = p.in, &out = p.out;
-  const int tid = threadIdx.x, N = in.num_pages;
-  int U = 0, front = 0;
-  for (int i0 = 0; i0 < N; i0 += kPageThreads) U += __syncthreads_count(i0 + tid < N && in.refs[i0 + tid] > 0);
-  for (int i0 = 0; i0 < U; i0 += kPageThreads) front += __syncthreads_count(i0 + tid < U && in.refs[i0 + tid] > 0);
-  const int n = U - front, m = min(n, p.max_moves);
-  for (int i = tid; i < p.max_moves; i += kPageThreads) p.moves[i] = make_int2(-1, -1);
-  for (int i = tid; i < N; i += kPageThreads) p.map[i] = i;
+  const Pool& in = p.in;
+  const int tid = threadIdx.x, i = tid * kCountEach;
+  const uint32_t mask = in_use(in, i);
+  int U, all, front = 0;
+  const int rank = block_before(__popc(mask), scratch, &U);
+#pragma unroll
+  for (int k = 0; k < kCountEach; ++k) front += i + k < U && (mask >> k & 1);
+  block_before(front, scratch, &all);
+  const int n = U - all, m = min(n, p.max_moves);
+  place_pages(p, i, mask, rank, U, m, false);
+  for (int r = m + tid; r < p.max_moves; r += kPageThreads) p.moves[r] = make_int2(-1, -1);
   if (tid == 0) {
     p.used[0] = U;
-    p.used[1] = U;
+    if (m == n) p.used[1] = U;
   }
   __syncthreads();
-  int done = 0;
-  for (int i0 = 0; i0 < U; i0 += kPageThreads) {  // free places in front, the lowest first
-    const bool free = i0 + tid < U && in.refs[i0 + tid] <= 0;
-    int all;
-    const int r = done + block_before(free, scratch, &all);
-    done += all;
-    if (free && r < m) p.moves[r].y = i0 + tid;
-  }
-  done = 0;
-  for (int i0 = U; i0 < N; i0 += kPageThreads) {  // pages in use behind, the highest first
-    const bool used = i0 + tid < N && in.refs[i0 + tid] > 0;
-    int all;
-    const int r = n - 1 - done - block_before(used, scratch, &all);
-    done += all;
-    if (used && r < m) p.moves[r].x = i0 + tid;
-    if (used && r == m) p.used[1] = i0 + tid + 1;
-  }
-  if (out.refs != in.refs)
-    for (int i = tid; i < N; i += kPageThreads) out.refs[i] = in.refs[i];
+  for (int r = tid; r < m; r += kPageThreads) move_refs(p, r);
   __syncthreads();
-  for (int r = tid; r < m; r += kPageThreads) {
-    const int2 x = p.moves[r];
-    p.map[x.x] = x.y;
-    const int refs = in.refs[x.x];
-    out.refs[x.y] = refs;
-    out.refs[x.x] = 0;
-  }
-  __syncthreads();
-  auto renamed = [&](int id) {
-    if (id >= 0 && id < N) return p.map[id];
-    atomicOr(p.err, DEV_ERR_BOUNDS);
-    return id;
-  };
-  for (int b = tid >> 5; b < in.B; b += kPageThreads / 32) {
-    const int own = own_tokens(in, in.lens[b], p.err), n_pages = own > 0 ? pages_of(in, own) : 0;
-    for (int c = tid & 31; c < n_pages; c += 32)
-      out.table[(size_t)b * in.stride + c] = renamed(in.table[(size_t)b * in.stride + c]);
-  }
-  for (int c = tid; c < pages_of(in, in.prefix_len); c += kPageThreads) out.prefix[c] = renamed(in.prefix[c]);
+  for (int b = tid >> 5; b < in.B; b += kPageThreads / 32) rename_row(p, b, tid & 31, 32);
+  for (int c = tid; c < pages_of(in, in.prefix_len); c += kPageThreads) p.out.prefix[c] = renamed(p, in.prefix[c]);
 }
 
 // ---- copies ----
-constexpr int kCopyThreads = 256, kCopyLoads = 4, kArrays = PageArrays::kMost;
+constexpr int kCopyLoads = 4, kArrays = PageArrays::kMost;
 constexpr int kCopyBytes = kCopyThreads * kCopyLoads * 16;  // of a block
 
 struct CopyParams {
@@ -375,7 +500,11 @@ bool apart(const Range (&out)[kOut], const Range (&in)[kIn]) {
 fox_status check_header(void* ws, size_t bytes, size_t need) {
   return ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && bytes >= need ? FOX_OK : FOX_ERR_WORKSPACE;
 }
-size_t pages_workspace(const fox_pages*) { return kCacheHeaderBytes; }
+// The header, and an int a page (step's list; compact's counts are fewer).
+size_t pages_workspace(const fox_pages* x) { return kCacheHeaderBytes + align_up(sizeof(int32_t) * (size_t)x->num_pages, 256); }
+int32_t* behind_header(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kCacheHeaderBytes); }
+// One CTA has a pool of 4096 pages in its registers.
+bool compacts_alone(const fox_pages* x) { return x->num_pages <= kCountPages && (long long)x->B * x->table_stride <= 65536; }
 
 CopyParams copy_params(const PageArrays& x) {
   CopyParams p = {};
@@ -432,10 +561,18 @@ fox_status fox_pages_step(const fox_pages* in, const fox_pages* out, const int32
     return FOX_ERR_INVALID_ARG;
   st = check_header(workspace, workspace_bytes, pages_workspace(in));
   if (st != FOX_OK) return st;
-  const StepParams p = {pool_of(in), pool_of(out), parent, add, copies, static_cast<uint32_t*>(workspace)};
+  const StepParams p = {pool_of(in), pool_of(out), parent, add, copies, behind_header(workspace), static_cast<uint32_t*>(workspace)};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  TraceScope trace("pages_step", s);
-  const cudaError_t e = launch_dependent(pages_step_kernel, dim3(1), dim3(kPageThreads), 0, s, p);
+  cudaError_t e = cudaSuccess;
+  if (in->refs != out->refs || in->table != out->table) {
+    TraceScope trace("pages_begin", s);
+    const int blocks = ceil_div(in->num_pages, kCopyThreads), wide = blocks < kSMs ? blocks : kSMs;
+    e = launch_dependent(pages_begin_kernel, dim3(out->B > wide ? out->B : wide), dim3(kCopyThreads), 0, s, p);
+  }
+  if (e == cudaSuccess) {
+    TraceScope trace("pages_step", s);
+    e = launch_dependent(pages_step_kernel, dim3(1), dim3(kPageThreads), 0, s, p);
+  }
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FOX_OK : FOX_ERR_CUDA;
 }
 
@@ -456,11 +593,29 @@ fox_status fox_pages_compact(const fox_pages* in, const fox_pages* out, int32_t*
   if (!apart(outs, ins)) return FOX_ERR_INVALID_ARG;
   st = check_header(workspace, workspace_bytes, pages_workspace(in));
   if (st != FOX_OK) return st;
-  const CompactParams p = {pool_of(in), pool_of(out), map,  reinterpret_cast<int2*>(moves),
-                           max_moves,   used,         static_cast<uint32_t*>(workspace)};
+  const CompactParams p = {pool_of(in), pool_of(out), map, reinterpret_cast<int2*>(moves), max_moves, used, behind_header(workspace),
+                           static_cast<uint32_t*>(workspace)};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  TraceScope trace("pages_compact", s);
-  const cudaError_t e = launch_dependent(pages_compact_kernel, dim3(1), dim3(kPageThreads), 0, s, p);
+  cudaError_t e = cudaSuccess;
+  if (compacts_alone(in)) {
+    TraceScope trace("pages_compact", s);
+    e = launch_dependent(pages_compact_kernel, dim3(1), dim3(kPageThreads), 0, s, p);
+  } else {
+    const int blocks = ceil_div(in->num_pages, kCountPages);
+    {
+      TraceScope trace("pages_count", s);
+      e = launch_dependent(pages_count_kernel, dim3(blocks), dim3(kPageThreads), 0, s, p);
+    }
+    if (e == cudaSuccess) {
+      TraceScope trace("pages_place", s);
+      e = launch_dependent(pages_place_kernel, dim3(blocks), dim3(kPageThreads), 0, s, p);
+    }
+    if (e == cudaSuccess) {
+      TraceScope trace("pages_rename", s);
+      const int work = max_moves > 0 ? ceil_div(max_moves, 4 * kCopyThreads) : 1;
+      e = launch_dependent(pages_rename_kernel, dim3(in->B + (work < kSMs ? work : kSMs)), dim3(kCopyThreads), 0, s, p);
+    }
+  }
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FOX_OK : FOX_ERR_CUDA;
 }
 
