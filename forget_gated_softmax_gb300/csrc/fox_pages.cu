@@ -69,7 +69,8 @@ struct StepParams {
   const int32_t* parent;
   const int32_t* add;
   int32_t* copies;
-  int32_t* list;  // [num_pages] of the workspace: free pages, the lowest first
+  int32_t* list;  // [num_pages] of the workspace: of a shared last page the last sequence that goes on in it; then free pages, the lowest first
+  bool begun;     // pages_begin_kernel was launched
   uint32_t* err;
 };
 
@@ -97,8 +98,8 @@ __global__ void __launch_bounds__(kCopyThreads) pages_begin_kernel(const StepPar
 
 __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepParams p) {
   constexpr int kEach = kMaxSeqs / kPageThreads, kLoad = 16, kNoPages = 0x7FFFFFFF;
-  __shared__ int kids[kMaxSeqs];       // children of the old sequences; then the shared pages that may have to be copied, -1: none
-  __shared__ int upto[kMaxSeqs];       // pages wanted by the new sequences up to each
+  __shared__ int kids[kMaxSeqs];       // children of the old sequences; then whether a new one's last page is copied
+  __shared__ int upto[kMaxSeqs];       // pages wanted by the new sequences up to each; before, pages of the old ones
   __shared__ int first_new[kMaxSeqs];  // a new sequence's entry for its first wanted page; kNoPages: it gets none. Before, old
                                        // sequences whose references change
   __shared__ int scratch[32], changed;
@@ -106,22 +107,24 @@ __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepPara
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int b = tid; b < in.B; b += kPageThreads) kids[b] = 0;
   if (tid == 0) changed = 0;
-  grid_dep_wait();
+  // Behind pages_begin_kernel, which let this one start once all before it were through, what the call was given may be read at once.
+  if (!p.begun) grid_dep_wait();
   grid_dep_trigger();
   __syncthreads();
   // Sequence b is thread b's, and b + 1024 too.
-  int len[kEach], n0[kEach], n1[kEach], add[kEach], last[kEach];
+  int len[kEach], n0[kEach], n1[kEach], add[kEach], last[kEach], old_len[kEach];
   bool grows[kEach], part[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int b = tid + i * kPageThreads;
+    old_len[i] = p.parent && b < in.B ? in.lens[b] : 0;
     last[i] = -1;
     len[i] = n0[i] = n1[i] = add[i] = 0;
     grows[i] = part[i] = false;
     if (b >= out.B) continue;
     const int src = parent_of(p, b);
-    len[i] = src >= 0 ? in.lens[src] : 0;
     add[i] = p.add[b];
+    len[i] = src >= 0 ? in.lens[src] : 0;
     if (src >= 0) atomicAdd(&kids[src], 1);
     int own = own_tokens(in, len[i], p.err);
     if (own < 0) len[i] = own = 0;
@@ -137,62 +140,59 @@ __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepPara
     if (grows[i] && (own & ((1 << in.shift) - 1)) != 0) {
       last[i] = in.table[(size_t)src * in.stride + n0[i] - 1];
       part[i] = last[i] >= 0 && last[i] < in.num_pages;
+      if (part[i]) p.list[last[i]] = -1;
     }
   }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = tid + i * kPageThreads;
+    if (old_len[i] == 0 || kids[b] == 1) continue;
+    upto[b] = pages_of(in, own_tokens(in, old_len[i], p.err));
+    if (upto[b] > 0) first_new[atomicAdd(&changed, 1)] = b;
+  }
+  if (p.begun) grid_dep_wait();
+  __threadfence();
   __syncthreads();
   // References: every entry of an old sequence by its children less one.
-  if (p.parent) {
-    for (int b = tid; b < in.B; b += kPageThreads) {
-      const int n = kids[b] == 1 ? 0 : pages_of(in, own_tokens(in, in.lens[b], p.err));
-      upto[b] = n;
-      if (n > 0) first_new[atomicAdd(&changed, 1)] = b;
-    }
-    __syncthreads();
-    for (int x = warp; x < changed; x += kPageThreads / 32) {
-      const int b = first_new[x], d = kids[b] - 1, n = upto[b];
+  for (int x = warp; x < changed; x += kPageThreads / 32) {
+    const int b = first_new[x], d = kids[b] - 1, n = upto[b];
 #pragma unroll 4
-      for (int c = lane; c < n; c += 32) {
-        const int id = in.table[(size_t)b * in.stride + c];
-        if (id >= 0 && id < in.num_pages)
-          atomicAdd(out.refs + id, d);
-        else
-          atomicOr(p.err, DEV_ERR_BOUNDS);
-      }
+    for (int c = lane; c < n; c += 32) {
+      const int id = in.table[(size_t)b * in.stride + c];
+      if (id >= 0 && id < in.num_pages)
+        atomicAdd(out.refs + id, d);
+      else
+        atomicOr(p.err, DEV_ERR_BOUNDS);
     }
-    __threadfence();
-    __syncthreads();
   }
-  // A partly filled last page is copied unless its other holders were copied before: who shares one looks for those.
-  int refs[kEach];
+  // A partly filled last page is copied by all that go on in it, unless they are all that hold it: the last of them then keeps it.
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    refs[i] = part[i] ? __ldcg(out.refs + last[i]) : 0;
-    kids[tid + i * kPageThreads] = part[i] && refs[i] > 1 ? last[i] : -1;
-  }
+  for (int i = 0; i < kEach; ++i)
+    if (part[i]) {
+      atomicSub(out.refs + last[i], 1);
+      atomicMax(p.list + last[i], tid + i * kPageThreads);
+    }
+  __threadfence();
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    unsigned looks = __ballot_sync(0xffffffffu, part[i] && refs[i] > 1);
-#pragma unroll 1
-    while (looks) {  // the warp for one lane after the other
-      const int who = __ffs(looks) - 1, b = warp * 32 + who + i * kPageThreads, page = __shfl_sync(0xffffffffu, last[i], who);
-      looks &= looks - 1;
-      int before = 0;
-      for (int o = lane; o < b; o += 32) before += kids[o] == page;
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (lane == who) refs[i] -= before;
-    }
-  }
   bool copied[kEach];
   int need[kEach], start[kEach], total = 0;
 #pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    copied[i] = part[i] && (__ldcg(out.refs + last[i]) > 0 || __ldcg(p.list + last[i]) != tid + i * kPageThreads);
+  __syncthreads();
+#pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    copied[i] = part[i] && refs[i] > 1;
+    if (part[i] && !copied[i]) atomicAdd(out.refs + last[i], 1);
     need[i] = grows[i] ? n1[i] - n0[i] + copied[i] : 0;
     int all;
     start[i] = total + block_before(need[i], scratch, &all);
     total += all;
     upto[tid + i * kPageThreads] = start[i] + need[i];
+  }
+  if (total > 0) {
+    __threadfence();
+    __syncthreads();
   }
   // Free pages, as many as are wanted, into the list.
   int found = 0;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepPara
     out.lens[b] = served ? (len[i] > 0 ? len[i] : in.prefix_len) + add[i] : len[i];
     p.copies[2 * b] = copies ? last[i] : -1;
     if (!copies) p.copies[2 * b + 1] = -1;
-    if (copies) atomicSub(out.refs + last[i], 1);
+    if (copied[i] && !served) atomicAdd(out.refs + last[i], 1);  // it still holds it
     kids[b] = copies;
     first_new[b] = served ? n0[i] - copies : kNoPages;
   }
@@ -561,10 +561,11 @@ fox_status fox_pages_step(const fox_pages* in, const fox_pages* out, const int32
     return FOX_ERR_INVALID_ARG;
   st = check_header(workspace, workspace_bytes, pages_workspace(in));
   if (st != FOX_OK) return st;
-  const StepParams p = {pool_of(in), pool_of(out), parent, add, copies, behind_header(workspace), static_cast<uint32_t*>(workspace)};
+  const StepParams p = {pool_of(in), pool_of(out), parent, add, copies, behind_header(workspace),
+                        in->refs != out->refs || in->table != out->table, static_cast<uint32_t*>(workspace)};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (in->refs != out->refs || in->table != out->table) {
+  if (p.begun) {
     TraceScope trace("pages_begin", s);
     const int blocks = ceil_div(in->num_pages, kCopyThreads), wide = blocks < kSMs ? blocks : kSMs;
     e = launch_dependent(pages_begin_kernel, dim3(out->B > wide ? out->B : wide), dim3(kCopyThreads), 0, s, p);
