@@ -22,7 +22,10 @@ namespace {
 struct Append4Params : AppendParams {
   uint8_t* ks;
   uint8_t* vs;
+  int thread_rows;
 };
+constexpr int kMostRows = 16;                        // rows of a thread
+constexpr int kMostPlaces = kMostRows * kThreads / 8;  // of a block
 
 __device__ __forceinline__ void unpack8(const uint4& w, float* f) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
@@ -125,14 +128,14 @@ __device__ __forceinline__ RowToken row_token(const AppendParams& p, int row) {
 
 enum Turn { kNone, kHalves, kPairs };  // channel i with i + rot / 2; 2 i with 2 i + 1
 
-template <Turn kTurn, int kR>  // kR: rows of a thread
+template <Turn kTurn, int kR>  // kR: rows of a thread whose loads are in flight together
 __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* places, uint4* exchange) {
   const PagedArgs& a = p.a;
   const int hs = a.d == 128 ? 3 : 2, hp = 1 << hs, blocks = a.d / kFourBlock;  // units of a head
   const int nk = a.Hkv << hs;
   const CopyShape x = copy_shape(2 * nk + (p.qn ? a.H << hs : 0));
   const int tid = threadIdx.x, lane = tid & 31, block = blockIdx.x - p.gate_blocks;
-  const int chunk = block % x.chunks, row0 = block / x.chunks * (kR * x.side);
+  const int chunk = block % x.chunks, row0 = block / x.chunks * (p.thread_rows * x.side);
   const int sub = x.side > 1 ? tid / x.per_row : 0, at = x.side > 1 ? tid - sub * x.per_row : chunk * kThreads + tid;
   // Units of a row are a multiple of 4 (8 with 128 channels) and so are a block's: a head's lie in neighbouring lanes.
   const bool live = at < x.per_row && sub < x.side, is_v = at >= nk && at < 2 * nk, is_q = at >= 2 * nk;
@@ -144,16 +147,14 @@ __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* pla
   const long long stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_q ? p.qn : is_v ? p.vn : p.kn) +
                              (size_t)(row0 + sub) * stride + h * a.d;
+  const int rows = min(p.thread_rows * x.side, a.rows - row0);
+  auto fetch = [&](Sixteen* u, bool there) {
+    if (there) *u = {__ldcs(reinterpret_cast<const uint4*>(src + c0)), __ldcs(reinterpret_cast<const uint4*>(src + c1))};
+    src += x.side * stride;
+  };
   Sixteen u[kR];
 #pragma unroll
-  for (int i = 0; i < kR; ++i) {
-    if (live && row0 + sub + i * x.side < a.rows) {
-      u[i].x = __ldcs(reinterpret_cast<const uint4*>(src + c0));
-      u[i].y = __ldcs(reinterpret_cast<const uint4*>(src + c1));
-    }
-    src += x.side * stride;
-  }
-  const int rows = min(kR * x.side, a.rows - row0);
+  for (int i = 0; i < kR; ++i) fetch(&u[i], live && sub + i * x.side < rows);
   for (int r = tid; r < rows; r += kThreads) places[r] = row_token(p, row0 + r);
   __syncthreads();
   if (!live) return;  // a head's lanes live or not together
@@ -168,6 +169,7 @@ __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* pla
     Sixteen y = u[0];
 #pragma unroll
     for (int i = 0; i + 1 < kR; ++i) u[i] = u[i + 1];
+    if (kR > 1) fetch(&u[kR - 1], r + kR * x.side < rows);
     const RowToken g = places[r];  // of the row: the same for all of its lanes
     if (g.token == kNoRow) continue;
     if (turns) y = turn16<kTurn == kPairs>(y, cs + (size_t)g.pos * half, sn + (size_t)g.pos * half, !is_q);
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 6) cache_append4_kernel(const Append
     float zs[128][kGateHeads + 1];
     struct {
       uint4 exchange[kTurn == kHalves ? 2 * kThreads : 1];
-      RowToken places[kBlockRows];
+      RowToken places[kMostPlaces];
     } rows;
   } sh;
   grid_dep_wait();
@@ -222,53 +224,76 @@ __global__ void __launch_bounds__(kThreads, 6) cache_append4_kernel(const Append
     copy_rows4<kTurn, kR>(p, sh.rows.places, sh.rows.exchange);
 }
 
-// The values of rows, 8 channels a thread: s u has 7 significant bits, so bf16 has it exactly. Bound by the trips to memory of a row's
-// place and then its codes: a thread has four rows' on their way.
+// The values of rows, 16 channels a thread: a chunk of each half of a head, so that stores are contiguous over lanes. s u has 7
+// significant bits, so bf16 has it exactly.
 struct Read4Params : AppendParams {
   const uint8_t* ks;
   const uint8_t* vs;
   __nv_bfloat16* ko;
   __nv_bfloat16* vo;
+  int thread_rows;
 };
-__global__ void __launch_bounds__(kThreads, 12) cache_read4_kernel(const Read4Params p) {
-  __shared__ RowToken places[kBlockRows];
+__global__ void __launch_bounds__(kThreads, 10) cache_read4_kernel(const Read4Params p) {
+  __shared__ RowToken places[kMostPlaces];
   grid_dep_wait();
   grid_dep_trigger();
   const PagedArgs& a = p.a;
-  const int hs = a.d == 128 ? 4 : 3, blocks = a.d / kFourBlock, nk = a.Hkv << hs;
+  const int hs = a.d == 128 ? 3 : 2, blocks = a.d / kFourBlock, half = blocks / 2, nk = a.Hkv << hs;
   const CopyShape x = copy_shape(2 * nk);
-  const int tid = threadIdx.x, chunk = blockIdx.x % x.chunks, row0 = blockIdx.x / x.chunks * (kRows * x.side);
+  const int tid = threadIdx.x, chunk = blockIdx.x % x.chunks, row0 = blockIdx.x / x.chunks * (p.thread_rows * x.side);
   const int sub = x.side > 1 ? tid / x.per_row : 0, at = x.side > 1 ? tid - sub * x.per_row : chunk * kThreads + tid;
   const bool live = at < x.per_row && sub < x.side, is_v = at >= nk;
-  const int w = is_v ? at - nk : at, h = w >> hs, j = w & ((1 << hs) - 1), b = j >> 2, t = j & 3;
-  const int rows = min(kRows * x.side, a.rows - row0);
+  const int w = is_v ? at - nk : at, h = w >> hs, j = w & ((1 << hs) - 1), b = j >> 2, t = j & 3, head = h * a.page_size;
+  const int rows = min(p.thread_rows * x.side, a.rows - row0);
   for (int r = tid; r < rows; r += kThreads) places[r] = row_token(p, row0 + r);
   __syncthreads();
   if (!live) return;
-  uint32_t words[kRows], bytes[kRows];
-  bool here[kRows];
+  const long long stride = (is_v ? p.v_stride : p.k_stride) * x.side;
+  __nv_bfloat16* out = (is_v ? p.vo : p.ko) + (size_t)(row0 + sub) * (is_v ? p.v_stride : p.k_stride) + h * a.d + j * 8;
+  const uint8_t* held = static_cast<const uint8_t*>(is_v ? a.v : a.k);
+  const uint8_t* scales = is_v ? p.vs : p.ks;
+  const int apart = is_v ? 4 * half : half;  // the two blocks' scales
+#pragma unroll 1
+  for (int first = sub; first < rows; first += kRows * x.side) {
+    uint32_t w0[kRows], w1[kRows], s0[kRows], s1[kRows];
+    bool here[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = i * x.side + sub;
-    const RowToken g = r < rows ? places[r] : RowToken{kNoRow, 0, 0};
-    here[i] = g.token != kNoRow;
-    if (!here[i]) continue;
-    const uint32_t token = g.token + h * a.page_size;
-    const uint8_t* row = static_cast<const uint8_t*>(is_v ? a.v : a.k) + (uint64_t)token * (a.d / 2);
-    words[i] = __ldcs(reinterpret_cast<const uint32_t*>(row + (is_v ? four_v_word(b, t, g.slot, blocks) : four_k_word(b, t, blocks))));
-    bytes[i] = is_v ? p.vs[(uint64_t)(token - (g.slot & 15)) * blocks + four_v_scale(b, g.slot, blocks)]
-                    : p.ks[(uint64_t)token * blocks + b];
+    for (int i = 0; i < kRows; ++i) {
+      const int r = i * x.side + first;
+      const RowToken g = r < rows ? places[r] : RowToken{kNoRow, 0, 0};
+      here[i] = g.token != kNoRow;
+      if (!here[i]) continue;
+      const uint32_t token = g.token + head;
+      const uint8_t* row = held + (uint64_t)token * (a.d / 2);
+      const int word = is_v ? four_v_word(b, t, g.slot, blocks) : four_k_word(b, t, blocks);
+      const uint8_t* scale = scales + (is_v ? (uint64_t)(token - (g.slot & 15)) * blocks + four_v_scale(b, g.slot, blocks)
+                                            : (uint64_t)token * blocks + b);
+      w0[i] = __ldcs(reinterpret_cast<const uint32_t*>(row + word));
+      w1[i] = __ldcs(reinterpret_cast<const uint32_t*>(row + (is_v ? word ^ half * 16 : word + half * 4)));
+      s0[i] = scale[0];
+      s1[i] = scale[apart];
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (here[i]) {
+        __stcs(reinterpret_cast<uint4*>(out), four_values(w0[i], s0[i], is_v));
+        __stcs(reinterpret_cast<uint4*>(out + a.d / 2), four_values(w1[i], s1[i], is_v));
+      }
+      out += stride;
+    }
   }
-  const long long stride = is_v ? p.v_stride : p.k_stride;
-  __nv_bfloat16* out = (is_v ? p.vo : p.ko) + (size_t)(row0 + sub) * stride + h * a.d + j * 8;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    if (here[i]) __stcs(reinterpret_cast<uint4*>(out + (size_t)i * x.side * stride), four_values(words[i], bytes[i], is_v));
 }
 
 int row_units4(const PagedArgs& a, bool with_q, int channels) { return (2 * a.Hkv + (with_q ? a.H : 0)) * (a.d / channels); }
 
 }  // namespace
+
+// Rows of a thread: one where those are on the SMs at once, else four, or as many as keep the SMs busy for some rounds of blocks (a block
+// looks its rows' places up before anything else).
+int thread_rows4(const PagedArgs& a, int units) {
+  if (append_blocks(a, units, 1).copies <= 6 * kSMs) return 1;
+  return append_blocks(a, units, kMostRows).copies >= 24 * kSMs ? kMostRows : kRows;
+}
 
 bool append4_fits(const PagedArgs& a, bool with_q) { return append_blocks(a, row_units4(a, with_q, 8)).fit(); }
 
@@ -278,13 +303,14 @@ cudaError_t launch_cache_append4(const CacheAppendArgs& x, void* ks, void* vs, c
   p.ks = static_cast<uint8_t*>(ks);
   p.vs = static_cast<uint8_t*>(vs);
   const int units = row_units4(p.a, p.qn != nullptr, 16);
-  if (append_blocks(p.a, units, 1).copies <= 6 * kSMs)  // one row a thread where those are on the SMs at once
+  p.thread_rows = thread_rows4(p.a, units);
+  if (p.thread_rows == 1)
     return launch_append(p.rot == 0 ? cache_append4_kernel<kNone, 1>
                                     : p.pairs ? cache_append4_kernel<kPairs, 1> : cache_append4_kernel<kHalves, 1>,
                          p, units, s, 1);
   return launch_append(p.rot == 0 ? cache_append4_kernel<kNone, kRows>
                                   : p.pairs ? cache_append4_kernel<kPairs, kRows> : cache_append4_kernel<kHalves, kRows>,
-                       p, units, s);
+                       p, units, s, p.thread_rows);
 }
 
 cudaError_t launch_cache_read4(const CacheAppendArgs& x, void* ks, void* vs, cudaStream_t s) {
@@ -294,8 +320,10 @@ cudaError_t launch_cache_read4(const CacheAppendArgs& x, void* ks, void* vs, cud
   p.vs = static_cast<const uint8_t*>(vs);
   p.ko = static_cast<__nv_bfloat16*>(const_cast<void*>(x.k));
   p.vo = static_cast<__nv_bfloat16*>(const_cast<void*>(x.v));
+  const int units = row_units4(p.a, false, 16);
+  p.thread_rows = thread_rows4(p.a, units);
   TraceScope trace("cache_read", s);
-  const cudaError_t e = launch_dependent(cache_read4_kernel, dim3(static_cast<unsigned>(append_blocks(p.a, row_units4(p.a, false, 8)).copies)),
+  const cudaError_t e = launch_dependent(cache_read4_kernel, dim3(static_cast<unsigned>(append_blocks(p.a, units, p.thread_rows).copies)),
                                          dim3(kThreads), 0, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

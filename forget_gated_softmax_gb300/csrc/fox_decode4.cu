@@ -701,15 +701,20 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
   if (shared) grid_dep_wait();  // as fox_decode_mma.cu's kernel
 }
 
-// One block a (page, key head, K or V), and one more a page for its gates and table entry. Bound by what is written.
-constexpr int kSpreadThreads = 256;
-__global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ PagedArgs to) {
+// Blocks of kSpreadUnits units of a page's K, then of its V, and one more a page for its gates and table entry. A unit is 16 channels of one
+// token and head, a chunk of each half of the head: stores are contiguous over lanes. Bound by what is written.
+constexpr int kSpreadThreads = 256, kSpreadUnits = 8 * kSpreadThreads;
+inline int spread_blocks(const PagedArgs& a) { return ceil_div(a.Hkv * a.page_size * (a.d / 16), kSpreadUnits); }
+template <int D>
+__global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ PagedArgs to,
+                                                                 int blocks) {
+  constexpr int kBlocks = D / kFourBlock, kHalf = kBlocks / 2, kUnits = D / 16;
   const PagedArgs& a = p.a;
-  const int S = a.page_size, per = 2 * a.Hkv + 1, at = blockIdx.x / per, part = blockIdx.x - at * per, tid = threadIdx.x;
+  const int S = a.page_size, per = 2 * blocks + 1, at = blockIdx.x / per, part = blockIdx.x - at * per, tid = threadIdx.x;
   grid_dep_wait();
   grid_dep_trigger();
   const int page = checked_page(a, a.prefix[at]), live = min(S, a.prefix_len - at * S);
-  if (part == 2 * a.Hkv) {
+  if (part == 2 * blocks) {
     const size_t n = (size_t)a.H * S / 4;
     const float4* g = reinterpret_cast<const float4*>(a.g) + (size_t)page * n;
     float4* out = reinterpret_cast<float4*>(to.g) + (size_t)at * n;
@@ -719,18 +724,24 @@ __global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_co
     if (tid == 0) const_cast<int32_t*>(to.prefix)[at] = at;
     return;
   }
-  const bool is_v = part >= a.Hkv;
-  const int hkv = is_v ? part - a.Hkv : part, words = a.d / 8, blocks = a.d / kFourBlock;
-  const uint8_t* from = static_cast<const uint8_t*>(is_v ? a.v : a.k) + four_row(a, page, hkv, 0);
-  const uint8_t* scales = (is_v ? p.vs : p.ks) + four_scale_row(a, page, hkv, 0);
-  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) + kv_offset(to, at, hkv, 0));
+  const bool is_v = part >= blocks;
+  const int begin = (is_v ? part - blocks : part) * kSpreadUnits, end = min(begin + kSpreadUnits, a.Hkv * S * kUnits);
+  const int j = tid % kUnits, b = j >> 2, t = j & 3;
+  const uint8_t* from = static_cast<const uint8_t*>(is_v ? a.v : a.k) + four_row(a, page, 0, 0);
+  const uint8_t* scales = (is_v ? p.vs : p.ks) + four_scale_row(a, page, 0, 0);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) + kv_offset(to, at, 0, 0) + j * 8;
 #pragma unroll 4
-  for (int i = tid; i < S * words; i += kSpreadThreads) {
-    const int slot = i / words, w = i - slot * words, b = w >> 2, t = w & 3;
-    const uint32_t code = *reinterpret_cast<const uint32_t*>(from + (size_t)slot * (a.d / 2) +
-                                                             (is_v ? four_v_word(b, t, slot, blocks) : four_k_word(b, t, blocks)));
-    const uint32_t byte = scales[is_v ? (slot & ~15) * blocks + four_v_scale(b, slot, blocks) : slot * blocks + b];
-    out[i] = slot < live ? four_values(code, byte, is_v) : make_uint4(0, 0, 0, 0);
+  for (int i = begin + tid; i < end; i += kSpreadThreads) {
+    const int row = i / kUnits, slot = row & (S - 1);
+    const int word = is_v ? four_v_word(b, t, slot, kBlocks) : four_k_word(b, t, kBlocks);
+    const uint8_t* codes = from + (size_t)row * (D / 2);
+    const uint8_t* scale = scales + (is_v ? (row & ~15) * kBlocks + four_v_scale(b, slot, kBlocks) : row * kBlocks + b);
+    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(codes + word);
+    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + (is_v ? word ^ kHalf * 16 : word + kHalf * 4));
+    const uint32_t s0 = scale[0], s1 = scale[is_v ? 4 * kHalf : kHalf];
+    uint4* to_row = reinterpret_cast<uint4*>(out + (size_t)row * D);
+    to_row[0] = slot < live ? four_values(w0, s0, is_v) : make_uint4(0, 0, 0, 0);
+    to_row[D / 16] = slot < live ? four_values(w1, s1, is_v) : make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -771,8 +782,9 @@ int decode4_warps(const PagedArgs& a, int Rt) { return warps_of(a.d, Rt); }
 
 cudaError_t launch_spread4(const DecodeParams& p, const PagedArgs& to, cudaStream_t s) {
   TraceScope trace("prefix_spread", s);
-  const cudaError_t e = launch_dependent(spread4_kernel, dim3(static_cast<unsigned>(to.num_pages) * (2 * p.a.Hkv + 1)), dim3(kSpreadThreads),
-                                         0, s, p, to);
+  const int blocks = spread_blocks(p.a);
+  const cudaError_t e = launch_dependent(p.a.d == 64 ? spread4_kernel<64> : spread4_kernel<128>,
+                                         dim3(static_cast<unsigned>(to.num_pages) * (2 * blocks + 1)), dim3(kSpreadThreads), 0, s, p, to, blocks);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
