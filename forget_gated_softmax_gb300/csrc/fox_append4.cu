@@ -5,11 +5,16 @@
 // multiply-add, taken off the fused difference) is within 1.5 units of the last place of fp32; where that leaves open on which side of
 // a border of bf16 a value lies (1 of 5000), 64 bits decide, in which the products are exact.
 //
-// A thread has 16 channels of four rows, as in fox_append.cu: a chunk of 8 and its partner's in the rotation, or two neighbouring
-// chunks. A block of 32 channels is two threads' neighbouring chunks (K that was rotated with a partner passes through shared memory
-// for that): its largest magnitude by a shuffle, its scale by the first of them, two words of codes by each (fox_four.h).
-// The rows of a thread are taken in turn by the same code: unrolled, the warps waited for instructions more than for anything (6 prompts
-// of up to 16384 tokens, rotation in pairs: 427 us against 297). Few rows have a thread each, as the rows' angles then come one after the other.
+// A thread has 16 channels of up to eight rows: a chunk of 8 and its partner's in the rotation, or two neighbouring chunks. A block of 32
+// channels is two threads' neighbouring chunks (K that was rotated with a partner passes through shared memory for that): its largest
+// magnitude by a shuffle, its scale by the first of them, two words of codes by each (fox_four.h).
+//
+// Bound by instructions, then by memory (6 prompts of up to 16384 tokens, 32 + 2 * 8 heads of 128, rotation in pairs: 1.25 GB in 252 us,
+// 5.0 TB/s; the exact rotation is 25 us of them). What that took: the rows of a thread in turn by the same code (unrolled, the warps
+// waited for instructions: 427 us, in turn 297), a row's loads one row ahead of its use and 64 registers, so that 8 blocks are on an SM
+// (four rows ahead and 6 blocks 289, two and 8 blocks 258, one and 10 blocks with spills 311), and eight rows a thread, before which a block looks up
+// where its rows stand (four 266, sixteen 250 but 62 for 57 where they are read back).
+// One token of each of 128 sequences: 12 us by itself, most of it the launch and dependent trips to memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,7 +29,8 @@ struct Append4Params : AppendParams {
   uint8_t* vs;
   int thread_rows;
 };
-constexpr int kMostRows = 16;                        // rows of a thread
+constexpr int kResident = 8;                           // blocks of an SM
+constexpr int kMostRows = 8;                           // rows of a thread
 constexpr int kMostPlaces = kMostRows * kThreads / 8;  // of a block
 
 __device__ __forceinline__ void unpack8(const uint4& w, float* f) {
@@ -128,7 +134,7 @@ __device__ __forceinline__ RowToken row_token(const AppendParams& p, int row) {
 
 enum Turn { kNone, kHalves, kPairs };  // channel i with i + rot / 2; 2 i with 2 i + 1
 
-template <Turn kTurn, int kR>  // kR: rows of a thread whose loads are in flight together
+template <Turn kTurn>
 __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* places, uint4* exchange) {
   const PagedArgs& a = p.a;
   const int hs = a.d == 128 ? 3 : 2, hp = 1 << hs, blocks = a.d / kFourBlock;  // units of a head
@@ -148,13 +154,12 @@ __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* pla
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_q ? p.qn : is_v ? p.vn : p.kn) +
                              (size_t)(row0 + sub) * stride + h * a.d;
   const int rows = min(p.thread_rows * x.side, a.rows - row0);
-  auto fetch = [&](Sixteen* u, bool there) {
-    if (there) *u = {__ldcs(reinterpret_cast<const uint4*>(src + c0)), __ldcs(reinterpret_cast<const uint4*>(src + c1))};
+  Sixteen next;
+  auto fetch = [&](int r) {
+    if (r < rows) next = {__ldcs(reinterpret_cast<const uint4*>(src + c0)), __ldcs(reinterpret_cast<const uint4*>(src + c1))};
     src += x.side * stride;
   };
-  Sixteen u[kR];
-#pragma unroll
-  for (int i = 0; i < kR; ++i) fetch(&u[i], live && sub + i * x.side < rows);
+  if (live) fetch(sub);
   for (int r = tid; r < rows; r += kThreads) places[r] = row_token(p, row0 + r);
   __syncthreads();
   if (!live) return;  // a head's lanes live or not together
@@ -166,10 +171,8 @@ __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* pla
   uint4* mine = exchange + (tid & ~(hp - 1)) * 2;  // a head's channels
 #pragma unroll 1
   for (int r = sub; r < rows; r += x.side) {
-    Sixteen y = u[0];
-#pragma unroll
-    for (int i = 0; i + 1 < kR; ++i) u[i] = u[i + 1];
-    if (kR > 1) fetch(&u[kR - 1], r + kR * x.side < rows);
+    Sixteen y = next;
+    fetch(r + x.side);
     const RowToken g = places[r];  // of the row: the same for all of its lanes
     if (g.token == kNoRow) continue;
     if (turns) y = turn16<kTurn == kPairs>(y, cs + (size_t)g.pos * half, sn + (size_t)g.pos * half, !is_q);
@@ -207,8 +210,8 @@ __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* pla
   }
 }
 
-template <Turn kTurn, int kR>
-__global__ void __launch_bounds__(kThreads, 6) cache_append4_kernel(const Append4Params p) {
+template <Turn kTurn>
+__global__ void __launch_bounds__(kThreads, kResident) cache_append4_kernel(const Append4Params p) {
   __shared__ __align__(16) union {
     float zs[128][kGateHeads + 1];
     struct {
@@ -221,11 +224,12 @@ __global__ void __launch_bounds__(kThreads, 6) cache_append4_kernel(const Append
   if (static_cast<int>(blockIdx.x) < p.gate_blocks)
     gate_block(p, sh.zs);
   else
-    copy_rows4<kTurn, kR>(p, sh.rows.places, sh.rows.exchange);
+    copy_rows4<kTurn>(p, sh.rows.places, sh.rows.exchange);
 }
 
 // The values of rows, 16 channels a thread: a chunk of each half of a head, so that stores are contiguous over lanes. s u has 7
-// significant bits, so bf16 has it exactly.
+// significant bits, so bf16 has it exactly. Bound by memory, what is written above all (the tokens of 6 prompts: 0.3 GB in 57 us, 5.2 TB/s; a chunk
+// and four rows a thread, so that blocks are short and look-ups many: 86).
 struct Read4Params : AppendParams {
   const uint8_t* ks;
   const uint8_t* vs;
@@ -288,11 +292,12 @@ int row_units4(const PagedArgs& a, bool with_q, int channels) { return (2 * a.Hk
 
 }  // namespace
 
-// Rows of a thread: one where those are on the SMs at once, else four, or as many as keep the SMs busy for some rounds of blocks (a block
-// looks its rows' places up before anything else).
+// Rows of a thread: one where those blocks are on the SMs at once, else twice as many until they are, up to kMostRows (rows that few threads
+// take one after the other wait for each other's angles: one token of each of 128 sequences 12.2 us with one row, 16.5 with four).
 int thread_rows4(const PagedArgs& a, int units) {
-  if (append_blocks(a, units, 1).copies <= 6 * kSMs) return 1;
-  return append_blocks(a, units, kMostRows).copies >= 24 * kSMs ? kMostRows : kRows;
+  int n = 1;
+  while (n < kMostRows && append_blocks(a, units, n).copies > kResident * kSMs) n *= 2;
+  return n;
 }
 
 bool append4_fits(const PagedArgs& a, bool with_q) { return append_blocks(a, row_units4(a, with_q, 8)).fit(); }
@@ -304,12 +309,7 @@ cudaError_t launch_cache_append4(const CacheAppendArgs& x, void* ks, void* vs, c
   p.vs = static_cast<uint8_t*>(vs);
   const int units = row_units4(p.a, p.qn != nullptr, 16);
   p.thread_rows = thread_rows4(p.a, units);
-  if (p.thread_rows == 1)
-    return launch_append(p.rot == 0 ? cache_append4_kernel<kNone, 1>
-                                    : p.pairs ? cache_append4_kernel<kPairs, 1> : cache_append4_kernel<kHalves, 1>,
-                         p, units, s, 1);
-  return launch_append(p.rot == 0 ? cache_append4_kernel<kNone, kRows>
-                                  : p.pairs ? cache_append4_kernel<kPairs, kRows> : cache_append4_kernel<kHalves, kRows>,
+  return launch_append(p.rot == 0 ? cache_append4_kernel<kNone> : p.pairs ? cache_append4_kernel<kPairs> : cache_append4_kernel<kHalves>,
                        p, units, s, p.thread_rows);
 }
 
