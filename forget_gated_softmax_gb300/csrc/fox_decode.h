@@ -373,14 +373,13 @@ __device__ __forceinline__ void find_ends(const DecodeParams& p, const SeqEntry*
 }
 
 // By the whole block, at its end. Row r of warp w's kept segment lies at rows + w * warp_pitch + r * row_pitch
-// (floats). `offs`: [CTAs + 1] and `part`: [threads] of shared memory, clear of the kept rows. kMoreWarps: of the block, that
-// are no workers.
+// (floats). `offs`: [CTAs + 1] and `part`: [threads] of shared memory, clear of the kept rows.
 // With a shared prefix every item is left to the merge that follows, its partial results as above.
-template <typename T, int D, int kRows, int kWarps, int kMoreWarps = 0>
+template <typename T, int D, int kRows, int kWarps>
 __device__ __forceinline__ void join_items(const DecodeParams& p, const SeqEntry* seqs, int total, int each,
                                            const Kept<kRows, kWarps>& kept, const BlockEnds& ends, const float* rows, int warp_pitch,
                                            int row_pitch, int* offs, Column* part) {
-  constexpr int kThreads = 32 * (kWarps + kMoreWarps), C4 = D / 4;
+  constexpr int kThreads = 32 * kWarps, C4 = D / 4;
   __shared__ int results[2];
   const int tid = threadIdx.x, cta = blockIdx.x, w_cta = cta * kWarps;
   const bool shared = p.pre.key_tiles > 0;
@@ -490,7 +489,7 @@ __device__ __forceinline__ void join_items(const DecodeParams& p, const SeqEntry
     if (deal > 1 && tid < F) {
       Column c = part[tid];
 #pragma unroll 1
-      for (int k = 1; k < deal; ++k) {
+      for (int k = 1; k < min(deal, n); ++k) {  // the others had none
         const Column& o = part[k * F + tid];
         add_column(c, o.v, o.m, o.l);
       }
