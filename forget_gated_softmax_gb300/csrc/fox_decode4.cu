@@ -111,6 +111,8 @@ struct Loader {
   Place pro;                 // behind the last window's last tile
   Window now, next;
   int at, left;              // the next tile of `now`; units that no window holds yet
+  uint32_t gates_to;         // this lane's place in a stage's gates
+  int h0, most;              // first head of `now`'s rows, and how many
   int id0, id1, nid0, nid1;  // this lane's tile of `now` and `next`: its page, and with pages of 16 tokens the second one
 
   __device__ __forceinline__ void look_ahead(const DecodeParams& p, const SeqEntry* seqs, int tp) {
@@ -134,6 +136,8 @@ struct Loader {
     if (pro.tile == pro.tiles && left > 0) next_item(p, seqs, pro);
   }
   __device__ __forceinline__ void begin(const DecodeParams& p, const SeqEntry* seqs, int tp, const Place& first, int count) {
+    const int lane = threadIdx.x & 31;
+    gates_to = (lane >> 2 & 1) * L::kGateSub + (4 + (lane & 3) * 4) * 4 + (lane >> 3) * 80;
     pro = first;
     left = count;
     at = now.n = 0;
@@ -142,7 +146,7 @@ struct Loader {
     if (count > 0) look_ahead(p, seqs, tp);
   }
   // Asks for the next tile of the line; there is one. `dst`, `sg`: where its codes and scales, and its gates, go in shared memory.
-  __device__ __forceinline__ void ask(const DecodeParams& p, int heads, const SeqEntry* seqs, int tp, uint32_t dst, uint32_t sg,
+  __device__ __forceinline__ void ask(const DecodeParams& p, int G, const SeqEntry* seqs, int tp, uint32_t dst, uint32_t sg,
                                       uint64_t policy) {
     const PagedArgs& a = p.a;
     const int lane = threadIdx.x & 31, S = 1 << a.page_shift;
@@ -152,28 +156,32 @@ struct Loader {
       id0 = lane < now.n ? checked_page(a, nid0) : 0;
       id1 = lane < now.n ? checked_page(a, nid1) : 0;
       look_ahead(p, seqs, tp);
+      h0 = now.hkv * G + (G > kRows ? now.rt * p.Rt % p.Gp : 0);
+      most = min(min(G, kRows), a.H - h0);
     }
     const int t = now.tile + at, j = (t < tp ? t : t - tp) * kKeyTile, slot = j & (S - 1);
-    const int G = a.H / a.Hkv, h0 = now.hkv * G + (G > kRows ? now.rt * p.Rt % p.Gp : 0), most = min(heads, a.H - h0);
     const int page0 = __shfl_sync(0xffffffffu, id0, at);
     // Tokens of a head counted through the pool: 32 bits hold them (check_four). Those of a page lie side by side, in halves of
     // 16 that are two pages' with pages of 16: NB lanes a half of K's or V's scales, four lanes a half of a head's gates.
     const uint32_t token0 = (static_cast<uint32_t>(page0) * a.Hkv + now.hkv << a.page_shift) + slot;
     const int row0 = page0 * a.H + h0;
-    const uint32_t mine = dst + lane * 16;
-    const int part = lane % NB, second = lane / NB & 1, h4 = lane >> 3, s4 = (lane & 3) * 4;
-    const uint8_t* scales = (lane < 2 * NB ? p.ks : p.vs) + part * 16;
+    const uint32_t l16 = lane * 16, mine = dst + l16;
+    const uint8_t* scales = (lane < 2 * NB ? p.ks : p.vs - 32 * NB) + l16;
+    const int h4 = lane >> 3;
     if (S != 16) {
-      const uint8_t* k = static_cast<const uint8_t*>(a.k) + lane * 16 + (uint64_t)token0 * RowB;
-      const uint8_t* v = static_cast<const uint8_t*>(a.v) + lane * 16 + (uint64_t)token0 * RowB;
+      const uint64_t codes = (uint64_t)token0 * RowB + l16;
+      const uint8_t* k = static_cast<const uint8_t*>(a.k) + codes;
+      const uint8_t* v = static_cast<const uint8_t*>(a.v) + codes;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) copy16(mine + i * 512, k + i * 512, policy);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) copy16(mine + L::kTileBytes + i * 512, v + i * 512, policy);
-      if (lane < 4 * NB) copy16(mine + 2 * L::kTileBytes, scales + second * 16 * NB + (uint64_t)token0 * NB, policy);
-      const float* g = a.g + (slot + (lane >> 2 & 1) * 16 + s4);
-      const uint32_t to = sg + (lane >> 2 & 1) * L::kGateSub + (4 + s4) * 4;
-      for (int h = h4; h < most; h += 4) copy16(to + h * 80, g + ((size_t)(row0 + h) << a.page_shift), policy);
+      if (lane < 4 * NB) copy16(mine + 2 * L::kTileBytes, scales + (uint64_t)token0 * NB, policy);
+      const float* g = a.g + ((size_t)(row0 + h4) * S + (slot + (lane & 7) * 4));
+      const uint32_t to = sg + gates_to;
+#pragma unroll
+      for (int h = 0; h < kRows; h += 4)
+        if (h + h4 < most) copy16(to + h * 80, g + (size_t)h * S, policy);
       if (lane < 2 * kRows && lane % kRows < most) {
         const size_t row = row0 + lane % kRows;
         cp_async8(sg + 2 * L::kGateSub + lane * 8, a.gbase + 2 * row);
@@ -195,12 +203,15 @@ struct Loader {
           copy16_or_0(mine + x * L::kTileBytes + (D / 64 + i) * 512, pool + (uint64_t)token1 * RowB + i * 512, two, policy);
         }
       }
-      if (lane < 4 * NB)
-        copy16_or_0(mine + 2 * L::kTileBytes, scales + (uint64_t)(second ? token1 : token0) * NB, !second || two, policy);
+      if (lane < 4 * NB) {
+        const bool second = lane / NB & 1;
+        copy16_or_0(mine + 2 * L::kTileBytes, scales - (second ? 16 * NB : 0) + (uint64_t)(second ? token1 : token0) * NB, !second || two,
+                    policy);
+      }
       const bool other = lane >> 2 & 1;
-      const uint32_t to = sg + (other ? L::kGateSub : 0) + (4 + s4) * 4;
+      const uint32_t to = sg + gates_to;
       for (int h = h4; h < most; h += 4)
-        copy16_or_0(to + h * 80, a.g + ((size_t)((other ? row1 : row0) + h) * 16 + s4), !other || two, policy);
+        copy16_or_0(to + (h - h4) * 80, a.g + ((size_t)((other ? row1 : row0) + h) * 16 + (lane & 3) * 4), !other || two, policy);
       if (lane < 2 * kRows && lane % kRows < most) {
         cp_async8(sg + 2 * L::kGateSub + lane * 8, a.gbase + 2 * (size_t)((lane < kRows ? row0 : row1) + lane % kRows));
         if (p.bias_from_j) copy16_or_0(sg + lane / kRows * L::kGateSub + lane % kRows * 80, a.g, false, policy);
@@ -212,7 +223,7 @@ struct Loader {
 
 // kMany: sequences may bring more than one token, so that rows of a tile may end at different keys.
 template <int D, int kRows, int W, bool kMany>
-__global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constant__ DecodeParams p, const int heads) {
+__global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constant__ DecodeParams p, const int G) {
   using L = Layout4<D, kRows>;
   constexpr int NB = L::kBlocks, RowB = D / 2, stages = L::kStages, NT = kRows == 16 ? 2 : 1;
   constexpr bool kTwice = kRows == 4;        // rows stand twice among the columns
@@ -247,7 +258,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
   const int total = seqs[a.B].u0 * a.Hkv, each = units_per_worker(total, p.workers);
   const int w = blockIdx.x * W + warp;
   const int u0 = min(total, w * each), count = min(total, u0 + each) - u0;
-  const int G = a.H / a.Hkv, Gp = p.Gp, S = a.page_size;
+  const int Gp = p.Gp, S = a.page_size;
   const int P = a.prefix_len, tp = p.walk_prefix ? ceil_div(P, kKeyTile) : 0;  // the prefix's tiles come first
   const int g8 = lane >> 2, t4 = lane & 3;
   const int half = kTwice ? t4 >> 1 : 0;  // where rows stand twice, the half of a tile's keys that this lane weighs
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
 #pragma unroll 1
   for (; asked < stages; ++asked) {
     if (asked < count)
-      load.ask(p, heads, seqs, tp, smem_u32(ring + asked * L::kStageBytes), smem_u32(gates + asked * L::kGateBytes), policy);
+      load.ask(p, G, seqs, tp, smem_u32(ring + asked * L::kStageBytes), smem_u32(gates + asked * L::kGateBytes), policy);
     cp_async_commit();
   }
   place_item();
@@ -686,7 +697,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
         }
       }
       if (asked < count) {
-        load.ask(p, heads, seqs, tp, smem_u32(st), smem_u32(sg), policy);
+        load.ask(p, G, seqs, tp, smem_u32(st), smem_u32(sg), policy);
         ++asked;
       }
       cp_async_commit();
@@ -756,12 +767,11 @@ cudaError_t launch_as(const DecodeParams& p, cudaStream_t s) {
   using L = Layout4<D, kRows>;
   static_assert(smem_bytes(D, kRows, W, 0) == 128 + sizeof(SeqEntry) + W * (L::kQBytes + L::kStages * (L::kStageBytes + L::kGateBytes)), "");
   auto kernel = decode4_kernel<D, kRows, W, kMany>;
-  const int G = p.a.H / p.a.Hkv;
   // One limit for every call (launch_as in fox_decode_mma.cu has the reason).
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
   if (e != cudaSuccess) return e;
   TraceScope trace("decode4", s);
-  const cudaError_t f = launch_dependent(kernel, dim3(kSMs), dim3(32 * W), smem_bytes(D, kRows, W, p.a.B), s, p, G < kRows ? G : kRows);
+  const cudaError_t f = launch_dependent(kernel, dim3(kSMs), dim3(32 * W), smem_bytes(D, kRows, W, p.a.B), s, p, p.a.H / p.a.Hkv);
   return f != cudaSuccess ? f : cudaGetLastError();
 }
 
