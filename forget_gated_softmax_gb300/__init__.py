@@ -724,7 +724,9 @@ def cache_workspace(cache: Cache, batch: Batch, rows: int):
     return ws
 
 
-def _cache_call_device(where: str, cache: Cache, batch: Batch) -> int:
+def _cache_call_device(where: str, kind: type, cache, batch: Batch) -> int:
+    if not isinstance(cache, kind):  # the calls read the handle's C struct
+        raise TypeError(f"{where} takes a {kind.__name__}, got {type(cache).__name__}")
     index = cache.index
     if batch.device != cache.device:
         raise ValueError(f"{where}: cache and batch are on different devices")
@@ -774,9 +776,9 @@ def _alloc_on(stream, make):
         return make()
 
 
-def _append(where: str, call, low, cache, batch: Batch, k, v, z, q, cos, sin, pairs, q_out, ws, stream):
+def _append(where: str, kind: type, call, low, cache, batch: Batch, k, v, z, q, cos, sin, pairs, q_out, ws, stream):
     torch = _torch()
-    index = _cache_call_device(where, cache, batch)
+    index = _cache_call_device(where, kind, cache, batch)
     rows = k.shape[0]
     ks = _row_stride(where, "k", k, cache, cache.Hkv, rows, index)
     vs = _row_stride(where, "v", v, cache, cache.Hkv, rows, index)
@@ -827,9 +829,9 @@ def _append(where: str, call, low, cache, batch: Batch, k, v, z, q, cos, sin, pa
     return q_out
 
 
-def _decode(where: str, call, make_ws, cache, batch: Batch, q, scale, bias_from_j, o, lse, ws, stream):
+def _decode(where: str, kind: type, call, make_ws, cache, batch: Batch, q, scale, bias_from_j, o, lse, ws, stream):
     torch = _torch()
-    index = _cache_call_device(where, cache, batch)
+    index = _cache_call_device(where, kind, cache, batch)
     rows = q.shape[0]
     qs = _row_stride(where, "q", q, cache, cache.H, rows, index)
     if o is None:
@@ -868,8 +870,8 @@ def fox_cache_append(cache: Cache, batch: Batch, k, v, z, *, q=None, cos=None, s
     returned (None without q) and must overlap none of the other arguments. Rows may be strided views, as those of
     a joint projection's output. ws: 256 bytes, zero before the first call, or those of cache_workspace; without it what the
     device reports (a page, length or position that does not fit, its token left out) is lost with the call's own."""
-    return _append("fox_cache_append", (_call or _load_call()).append, cache.g_low, cache, batch, k, v, z, q, cos, sin, pairs, q_out,
-                   ws, stream)
+    return _append("fox_cache_append", Cache, (_call or _load_call()).append, cache.g_low, cache, batch, k, v, z, q, cos, sin, pairs,
+                   q_out, ws, stream)
 
 
 def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
@@ -878,8 +880,8 @@ def fox_decode(cache: Cache, batch: Batch, q, *, scale: float = 0.0, bias_from_j
     LSE [rows, H] fp32); q, o and lse apart from each other. A long shared prefix is read and multiplied once for all
     sequences (bf16; |v| >= 65536 in it is then reported). Without ws what the device reports is lost.
     Rows of idle sequences get O = 0 and LSE = -inf; rows behind the last sequence are not written."""
-    return _decode("fox_decode", (_call or _load_call()).decode, cache_workspace, cache, batch, q, scale, bias_from_j, o, lse, ws,
-                   stream)
+    return _decode("fox_decode", Cache, (_call or _load_call()).decode, cache_workspace, cache, batch, q, scale, bias_from_j, o, lse,
+                   ws, stream)
 
 
 # ------------------------------------------------------------------------------- the cache in 4 bits
@@ -954,15 +956,15 @@ def fox_cache4_append(cache: Cache4, batch: Batch, k, v, z, *, q=None, cos=None,
                       q_out=None, ws=None, stream=None):
     """fox_cache_append into a 4-bit cache; k, v and q bf16. What the cache then holds of a token, fox_cache4_read returns.
     A magnitude above 430080, an infinity or a NaN in k (rotated) or v is reported (fox_check_error)."""
-    return _append("fox_cache4_append", (_call or _load_call()).append4, None, cache, batch, k, v, z, q, cos, sin, pairs, q_out, ws,
-                   stream)
+    return _append("fox_cache4_append", Cache4, (_call or _load_call()).append4, None, cache, batch, k, v, z, q, cos, sin, pairs, q_out,
+                   ws, stream)
 
 
 def fox_cache4_decode(cache: Cache4, batch: Batch, q, *, scale: float = 0.0, bias_from_j: bool = False, o=None, lse=None,
                       ws=None, stream=None) -> Tuple[object, object]:
     """fox_decode over a 4-bit cache: q [rows, H, d] bf16 -> (O [rows, H, d], LSE [rows, H] fp32)."""
-    return _decode("fox_cache4_decode", (_call or _load_call()).decode4, cache4_workspace, cache, batch, q, scale, bias_from_j, o, lse,
-                   ws, stream)
+    return _decode("fox_cache4_decode", Cache4, (_call or _load_call()).decode4, cache4_workspace, cache, batch, q, scale, bias_from_j,
+                   o, lse, ws, stream)
 
 
 def fox_cache4_read(cache: Cache4, batch: Batch, rows: Optional[int] = None, *, k=None, v=None, ws=None, stream=None):
@@ -971,7 +973,7 @@ def fox_cache4_read(cache: Cache4, batch: Batch, rows: Optional[int] = None, *, 
     that the call makes). ws: as for fox_cache_append."""
     torch = _torch()
     where = "fox_cache4_read"
-    index = _cache_call_device(where, cache, batch)
+    index = _cache_call_device(where, Cache4, cache, batch)
     if rows is None:
         if k is None and v is None:
             raise ValueError(f"{where}: rows, or a k or v that has them")
