@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 10) cache_read4_kernel(const Read4Pa
   }
 }
 
-int row_units4(const PagedArgs& a, bool with_q, int channels) { return (2 * a.Hkv + (with_q ? a.H : 0)) * (a.d / channels); }
+int row_units4(const PagedArgs& a, bool with_q) { return (2 * a.Hkv + (with_q ? a.H : 0)) * (a.d / 16); }
 
 }  // namespace
 
@@ -300,14 +300,17 @@ int thread_rows4(const PagedArgs& a, int units) {
   return n;
 }
 
-bool append4_fits(const PagedArgs& a, bool with_q) { return append_blocks(a, row_units4(a, with_q, 8)).fit(); }
+bool append4_fits(const PagedArgs& a, bool with_q) {
+  const int units = row_units4(a, with_q);
+  return append_blocks(a, units, thread_rows4(a, units)).fit();
+}
 
 cudaError_t launch_cache_append4(const CacheAppendArgs& x, void* ks, void* vs, cudaStream_t s) {
   Append4Params p = {};
   static_cast<AppendParams&>(p) = append_params(x);
   p.ks = static_cast<uint8_t*>(ks);
   p.vs = static_cast<uint8_t*>(vs);
-  const int units = row_units4(p.a, p.qn != nullptr, 16);
+  const int units = row_units4(p.a, p.qn != nullptr);
   p.thread_rows = thread_rows4(p.a, units);
   return launch_append(p.rot == 0 ? cache_append4_kernel<kNone> : p.pairs ? cache_append4_kernel<kPairs> : cache_append4_kernel<kHalves>,
                        p, units, s, p.thread_rows);
@@ -320,7 +323,7 @@ cudaError_t launch_cache_read4(const CacheAppendArgs& x, void* ks, void* vs, cud
   p.vs = static_cast<const uint8_t*>(vs);
   p.ko = static_cast<__nv_bfloat16*>(const_cast<void*>(x.k));
   p.vo = static_cast<__nv_bfloat16*>(const_cast<void*>(x.v));
-  const int units = row_units4(p.a, false, 16);
+  const int units = row_units4(p.a, false);
   p.thread_rows = thread_rows4(p.a, units);
   TraceScope trace("cache_read", s);
   const cudaError_t e = launch_dependent(cache_read4_kernel, dim3(static_cast<unsigned>(append_blocks(p.a, units, p.thread_rows).copies)),

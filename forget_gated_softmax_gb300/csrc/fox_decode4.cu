@@ -164,7 +164,7 @@ struct Loader {
     // Tokens of a head counted through the pool: 32 bits hold them (check_four). Those of a page lie side by side, in halves of
     // 16 that are two pages' with pages of 16: NB lanes a half of K's or V's scales, four lanes a half of a head's gates.
     const uint32_t token0 = (static_cast<uint32_t>(page0) * a.Hkv + now.hkv << a.page_shift) + slot;
-    const int row0 = page0 * a.H + h0;
+    const uint32_t row0 = static_cast<uint32_t>(page0) * a.H + h0;
     const uint32_t l16 = lane * 16, mine = dst + l16;
     const uint8_t* scales = (lane < 2 * NB ? p.ks : p.vs - 32 * NB) + l16;
     const int h4 = lane >> 3;
@@ -192,7 +192,8 @@ struct Loader {
       }
     } else {
       const bool two = j + 16 < (t < tp ? a.prefix_len : now.own);  // the second half's page may be none
-      const int page1 = __shfl_sync(0xffffffffu, id1, at), row1 = page1 * a.H + h0;
+      const int page1 = __shfl_sync(0xffffffffu, id1, at);
+      const uint32_t row1 = static_cast<uint32_t>(page1) * a.H + h0;
       const uint32_t token1 = (static_cast<uint32_t>(page1) * a.Hkv + now.hkv) * 16;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {

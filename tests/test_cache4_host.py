@@ -122,6 +122,28 @@ def test_more_work_than_ints_count_is_refused(L):
     assert _decode(L, s=big, rows=2048) == 2
 
 
+def test_the_extension_passes_what_ctypes_passes(L):
+    """_foxcall's calls of the 4-bit cache: the statuses of the same calls by ctypes, whatever argument is bad."""
+    from forget_gated_softmax_gb300 import _foxcall
+
+    c, b = _cache(), _batch()
+    at = ctypes.addressof(c), ctypes.addressof(b)
+    far = 1 << 33
+    decode = [*at, 2, FAKE, 1024, 0.0, 0, 1 << 32, far, FAKE, 16, 0]
+    append = [*at, 2, FAKE, 256, FAKE, 256, FAKE, 8, FAKE, 16, 0]
+    read = [*at, 2, FAKE, 256, 1 << 32, 256, FAKE, 16, 0]
+    bad = {2: -1, 3: FAKE + 1, 4: 3, 5: FAKE + 1}
+    for name, good in (("decode4", decode), ("append4", append), ("read4", read)):
+        for i, x in [(None, None), *bad.items()]:
+            if name == "decode4" and i == 5:
+                x = float("nan")
+            a = list(good) if i is None else [x if j == i else y for j, y in enumerate(good)]
+            got = getattr(_foxcall, name)(*a)
+            assert got == getattr(fox._CtypesCall, name)(*a) != 0, (name, i)  # at the least the workspace is too small
+        with pytest.raises(TypeError):
+            getattr(_foxcall, name)(*good[:-1])
+
+
 # ---- pages ----
 
 

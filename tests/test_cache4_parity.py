@@ -79,6 +79,11 @@ APPENDS = [
     ([31, 100], [31, 31], 4, 1, 64, 16, dict(prefix=32, uniform=True, rot=48)),         # partners across blocks
     ([2500], [2500], 2, 1, 64, 16, dict(rot=64)),                                       # 157 pages
     ([9, 30], [9, 2], 5, 1, 128, 32, dict(rot=96, pairs=True)),
+    # Rows that threads take one after the other: two, four and eight, also where rows lie side by side in a block.
+    ([700, 3], [600, 3], 32, 8, 128, 64, dict(rot=128)),
+    ([1000, None, 301], [1000, 2, 301], 32, 8, 128, 16, dict(rot=64, pairs=True, tail=5)),
+    ([2600, 17], [2600, 5], 16, 16, 128, 64, dict(rot=128)),
+    ([9000, None, 1003], [9000, 1, 1003], 2, 1, 64, 128, dict(rot=64, pairs=True)),
 ]
 
 
@@ -633,6 +638,108 @@ def test_two_batches_at_once_on_their_own_streams_and_workspaces(fox):
         for o, lse in out[i]:
             assert torch.equal(bits(o), bits(out[i][0][0])) and torch.equal(bits(lse), bits(out[i][0][1]))
         assert_o(tensor_f64(out[i][0][0]), tensor_f64(ro), "bf16", "decode4 streams")
+
+
+def test_a_captured_decode_behind_a_shared_prefix_is_replayed(fox):
+    """The prefix is spread out in the workspace by the graph itself: what another call left there, and other tokens in the pool,
+    make no difference to a replay but the tokens' own."""
+    B, P = 150, 5003
+    c = Case4([3] * B, [1] * B, 4, 1, 128, 16, uniform=True, seed=90, prefix=P)
+    c.put()
+    cache, batch = c.cache4(fox), c.batch(fox)
+    ws = fox.cache4_workspace(cache, batch, B)
+    o, lse = torch.empty_like(c.q), torch.empty(B, 4, device="cuda")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        fox.fox_cache4_decode(cache, batch, c.q, o=o, lse=lse, ws=ws, stream=side)
+    for i in range(2):
+        if i:  # other tokens in the same pages
+            other = Case4([3] * B, [1] * B, 4, 1, 128, 16, uniform=True, seed=91, prefix=P)
+            c.pre, c.seq = other.pre, other.seq
+            c.put()
+            ws[fox.FOX_CACHE_ZERO_BYTES:].fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fox.fox_check_error(ws) == 0
+        direct, dl = fox.fox_cache4_decode(cache, batch, c.q)
+        assert torch.equal(bits(o), bits(direct)) and torch.equal(bits(lse), bits(dl))
+        ro, rl = c.attend()
+        assert_o(tensor_f64(o), tensor_f64(ro), "bf16", "decode4 shared graph")
+        assert (lse.double() - rl).abs().max().item() <= foxtest.TOL_LSE_BF16
+
+
+def test_threads_of_the_host_call_at_once(fox):
+    """Appends, decodes and reads of four threads, each with its own cache, stream and workspace."""
+    import threading
+
+    cases = [Case4([200 + 30 * i, 50], [2, 1], 8, 2, 128, 32, seed=100 + i) for i in range(4)]
+    for c in cases:
+        c.put()
+    torch.cuda.synchronize()
+    results, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            c, s = cases[i], torch.cuda.Stream()
+            cache, batch = c.cache4(fox), c.batch(fox)
+            with torch.cuda.stream(s):
+                ws = fox.cache4_workspace(cache, batch, c.rows)
+                k, v, z = c.new_rows()
+                for _ in range(30):
+                    fox.fox_cache4_append(cache, batch, k, v, z, ws=ws, stream=s)
+                    out = fox.fox_cache4_decode(cache, batch, c.q, ws=ws, stream=s)
+                    read = fox.fox_cache4_read(cache, batch, c.rows, ws=ws, stream=s)
+            s.synchronize()
+            results[i] = (out, read, fox.fox_check_error(ws, s))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for c, ((o, lse), (rk, rv), status) in zip(cases, results):
+        assert status == 0
+        ro, rl = c.attend()
+        assert_o(tensor_f64(o), tensor_f64(ro), "bf16", "decode4 threads")
+        for b in range(c.B):
+            r, n = slice(c.row0[b], c.row0[b] + c.new[b]), c.own[b] - c.new[b]
+            assert torch.equal(rk[r].double(), c.held[b][0][n:]) and torch.equal(rv[r].double(), c.held[b][1][n:])
+
+
+def test_without_the_extension(fox, monkeypatch):
+    """The same calls by way of ctypes."""
+    c = Case4([40, 20], [1, 3], 4, 2, 64, 16, seed=3, low=True)
+    c.put()
+    cache, batch = c.cache4(fox), c.batch(fox)
+    cos, sin = angles(64, 32)
+
+    def calls():
+        k, v, z = c.new_rows()
+        q = fox.fox_cache4_append(cache, batch, k, v, z, q=c.q, cos=cos, sin=sin)
+        fox.fox_cache4_append(cache, batch, k, v, z)
+        return [q, *fox.fox_cache4_decode(cache, batch, c.q, scale=0.3), *fox.fox_cache4_read(cache, batch, c.rows)]
+
+    first = calls()
+    monkeypatch.setattr(fox, "_call", fox._CtypesCall)
+    for x, y in zip(first, calls()):
+        assert torch.equal(bits(x), bits(y))
+
+
+def test_handles_of_the_other_kind_are_refused(fox):
+    """The calls read the handle's C struct, and the two kinds' differ."""
+    c = Case4([40, 20], [1, 1], 4, 2, 64, 16, uniform=True, seed=3)
+    four, batch, rows = c.cache4(fox), c.batch(fox), c.new_rows()
+    bf16 = fox.make_cache(c.k, c.v, c.g, c.gbase)
+    for call, cache in ((fox.fox_cache4_append, bf16), (fox.fox_cache_append, four)):
+        with pytest.raises(TypeError):
+            call(cache, batch, *rows)
+    for call, cache in ((fox.fox_cache4_decode, bf16), (fox.fox_decode, four)):
+        with pytest.raises(TypeError):
+            call(cache, batch, c.q)
+    with pytest.raises(TypeError):
+        fox.fox_cache4_read(bf16, batch, 2)
 
 
 def test_binding_refusals(fox):
