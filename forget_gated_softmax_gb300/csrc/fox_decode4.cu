@@ -19,6 +19,12 @@
 //   and off by 2^-32 of it at most.
 // Up to four rows a tile (kRows 4) stand twice among the eight columns, so that scores and weights of half the keys fall to each half of the
 //   lanes: columns 0..3 then sum the first 16 keys of a tile, columns 4..7 the others, and are added at the end.
+//
+// Bound by instructions: 785 a key tile of 128 channels and 4 rows, 180 of them to spread K out, 200 V, 95 the copies (all lanes' own: by
+// bulk copies of a loading warp, which has a lane a worker, 301 us against 235 then). 64 sequences of up to 16384 tokens, 32 heads on 8, 725 MB:
+// 169 us, 4.3 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 132. V as subnormals, unchanged by a subtraction
+// of 8 that two more products make: 4 % fewer instructions, 177 for 172 us. One sequence of 65536, 80 MB: 34 us, of which launch and first
+// look-ups are 13 and the join of the workers' parts 6; one of 1000, 16 heads of 64 channels: 14.5, all but 3 of them launch, look-ups and join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -714,7 +720,8 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
 }
 
 // Blocks of kSpreadUnits units of a page's K, then of its V, and one more a page for its gates and table entry. A unit is 16 channels of one
-// token and head, a chunk of each half of the head: stores are contiguous over lanes. Bound by what is written.
+// token and head, a chunk of each half of the head: stores are contiguous over lanes. Bound by memory: 32768 tokens of 8 heads of 128 channels, 34 MB
+// to 134, 30 us, 5.5 TB/s (a chunk a thread, blocks of one head 45).
 constexpr int kSpreadThreads = 256, kSpreadUnits = 8 * kSpreadThreads;
 inline int spread_blocks(const PagedArgs& a) { return ceil_div(a.Hkv * a.page_size * (a.d / 16), kSpreadUnits); }
 template <int D>
@@ -776,7 +783,9 @@ cudaError_t launch_as(const DecodeParams& p, cudaStream_t s) {
   return f != cudaSuccess ? f : cudaGetLastError();
 }
 
-// Workers of a CTA: three or two a scheduler, as registers allow.
+// Workers of a CTA: three a scheduler, as registers allow, or two where a worker's rings and rows leave no room for three in shared memory.
+// 64 sequences of up to 16384 tokens, 4 rows: 12 workers 169 us, 14 and 16 (128 registers, some of them spilled) 194 and 182; a third stage
+// of the ring 171. 16 rows of 128 channels, up to 8192: 8 workers 160, 10 262.
 constexpr int warps_of(int D, int rows) { return rows < 16 || D == 64 ? 12 : 8; }
 
 template <int D, int kRows>
@@ -788,6 +797,8 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// The smallest tile that holds them: 4 rows a key head, 64 sequences of up to 16384 tokens, 169 us in tiles of 4 and 182 of 8; 8 rows, up
+// to 8192, 107 of 8 and 151 of 16 (64 channels: 4 rows 127 and 134, 8 rows 137 and 189).
 int decode4_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 int decode4_warps(const PagedArgs& a, int Rt) { return warps_of(a.d, Rt); }
 

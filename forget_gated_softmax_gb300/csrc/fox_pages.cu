@@ -3,9 +3,10 @@
 //
 // step and compact are integers all: what bounds them is latency, a dependent trip to memory or a barrier after the other, so that they take
 // few of both. step: one CTA for what hangs together, behind a kernel that copies references and table rows where the new state is
-// apart from the old. compact: a count of the pages in use by blocks of them, then every block knows its pages' ranks, then tables; a small
-// pool by one CTA.
-// copy is bound by memory: each page read once and written once, 16 KB a block.
+// apart from the old (512 sequences on 65536 pages 16 us, in one kernel 61; 8 of a search on 2048 pages 8.5). compact: a count of the
+// pages in use by blocks of them, then every block knows its pages' ranks, then tables (262144 pages, 1024 sequences 13 us; by one CTA
+// 407); a small pool by one CTA (6.4 us).
+// copy is bound by memory: each page read once and written once, 16 KB a block (1.28 GB read and written 188 us, 6.8 TB/s; 26 MB 5.2 us).
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -503,8 +504,12 @@ fox_status check_header(void* ws, size_t bytes, size_t need) {
 // The header, and an int a page (step's list; compact's counts are fewer).
 size_t pages_workspace(const fox_pages* x) { return kCacheHeaderBytes + align_up(sizeof(int32_t) * (size_t)x->num_pages, 256); }
 int32_t* behind_header(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kCacheHeaderBytes); }
-// One CTA has a pool of 4096 pages in its registers.
-bool compacts_alone(const fox_pages* x) { return x->num_pages <= kCountPages && (long long)x->B * x->table_stride <= 65536; }
+// One CTA has a pool of 4096 pages in its registers, and renames 32 pieces of 32 entries at a time, half a microsecond or more each. By one
+// CTA and by three kernels: 16 sequences of 32 entries (512 pages) 3.9 and 6.4 us, 64 of 64 (4096 pages: 4 rounds) 9.4 and 10.5, 128 of 512
+// (64 rounds) 42 and 11, 2048 of 32 63 and 12.
+bool compacts_alone(const fox_pages* x) {
+  return x->num_pages <= kCountPages && x->B * (long long)ceil_div(x->table_stride, 32) <= 4 * kPageThreads / 32;
+}
 
 CopyParams copy_params(const PageArrays& x) {
   CopyParams p = {};
