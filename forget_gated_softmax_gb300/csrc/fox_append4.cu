@@ -3,7 +3,7 @@
 // Q is rotated as in fox_append.cu. K is too, but to the nearest bf16 of the exact a cos - b sin: the 4-bit form has borders everywhere, and a
 // value on the other side of one is a whole step away. Kahan's difference of products (one product's rounding error by a fused
 // multiply-add, taken off the fused difference) is within 1.5 units of the last place of fp32; where that leaves open on which side of
-// a border of bf16 a value lies (1 of 5000), 64 bits decide, in which the products are exact.
+// a border of bf16 a value lies (1 of 8000), 64 bits decide, in which the products are exact.
 //
 // A thread has 16 channels of up to eight rows: a chunk of 8 and its partner's in the rotation, or two neighbouring chunks. A block of 32
 // channels is two threads' neighbouring chunks (K that was rotated with a partner passes through shared memory for that): its largest
@@ -58,12 +58,12 @@ __device__ __forceinline__ float turned_exactly(float a, float c, float b, float
   const float f = __double2float_rz(x);
   return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
-// `least` so far and two values' lower halves less 0x7FFA, modulo 2^16, where a border of bf16 is 6 (a carry may add 1 to the upper):
-// up to 12 the side of the border is open.
+// `least` so far and two values' lower halves less 0x7FFD, modulo 2^16, where a border of bf16 is 3 (a carry may add 1 to the upper):
+// up to 7 the side of the border is open (1.5 units, 2.5 where products are subnormal).
 __device__ __forceinline__ uint32_t border(uint32_t least, float x, float y) {
-  return __vminu2(least, __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x5410) + 0x80068006u);
+  return __vminu2(least, __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x5410) + 0x80038003u);
 }
-__device__ __forceinline__ bool at_border(uint32_t least) { return (least & 0xFFFFu) <= 12u || (least >> 16) <= 12u; }
+__device__ __forceinline__ bool at_border(uint32_t least) { return (least & 0xFFFFu) <= 7u || (least >> 16) <= 7u; }
 
 // Sixteen channels, x and y, turned by eight angles: channel i of x with i of y, or neighbours of either.
 struct Sixteen {
@@ -189,11 +189,11 @@ __device__ __forceinline__ void copy_rows4(const Append4Params& p, RowToken* pla
       y = {mine[2 * j], mine[2 * j + 1]};
       __syncwarp(head_lanes);
     }
-    uint32_t most = __vmaxu2(four_most(y.x), four_most(y.y));
-    most = __vmaxu2(most, __shfl_xor_sync(0x3u << (lane & ~1), most, 1));
-    const float top = __uint_as_float(max(most & 0xFFFFu, most >> 16) << 16);
+    uint32_t most = four_larger(four_larger(y.x), four_larger(y.y));
+    most = four_larger(most, __shfl_xor_sync(0x3u << (lane & ~1), most, 1));
+    const float top = fabsf(__uint_as_float(four_larger(most, most << 16) & 0xFFFF0000u));
     const uint32_t byte = four_scale_byte(top);
-    const float inv = byte ? 1.f / four_scale(byte) : 0.f;
+    const float inv = byte ? __fdividef(1.f, four_scale(byte)) : 0.f;  // 2 units of the last place are enough (four_code_bits)
     const bool odd = !(top <= 430080.f);
     if (odd && a.err) atomicOr(a.err, DEV_ERR_RANGE);
     const uint32_t w0 = block_codes(y.x, inv, odd), w1 = block_codes(y.y, inv, odd);

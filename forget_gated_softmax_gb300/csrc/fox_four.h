@@ -69,17 +69,12 @@ FOX_HD uint32_t four_scale_byte(float amax) {
   if (t < 0x1p-14f) return static_cast<uint32_t>(ceilf(t * 0x1p17f));
   return (float_bits(t) + 0xFFFFFu >> 20) - (112u << 3);
 }
-// u + 8 of a finite x of at most 7 s, inv = 1 / s (0 where s is): floor(x / s + 8.5), with 2^-12 away from zero for the halves: a bf16
-// value over s is a half or 2^-11 away from it, so that this makes up for the roundings of inv and of the product. On the device left in
-// the low bits by an addition of 2^23 that rounds down.
-FOX_HD uint32_t four_code(float x, float inv) {
-  const float half = 8.5f + copysignf(0x1p-12f, x);
-#ifdef __CUDA_ARCH__
-  return __float_as_uint(__fadd_rz(fmaf(x, inv, half), 8388608.f)) - 0x4B000000u;
-#else
-  return static_cast<uint32_t>(std::fma(x, inv, half));
-#endif
-}
+// u + 8 of a finite x of at most 7 s, in bits above kFourNone's; inv = 1 / s within 2^-22 of it (0 where s is): x / s is a half or 2^-11
+// away from one, so a factor of 1 + 2^-15 brings halves (0.5 at least) 2^-16 away from zero, and nothing else over a half. The nearest
+// integer is then what an fma with 1.5 * 2^23 leaves in the low bits.
+constexpr uint32_t kFourNone = 0x4B400000u;
+FOX_HD uint32_t four_code_bits(float x, float inv) { return float_bits(fmaf(x, inv * (1.f + 0x1p-15f), 12582912.f + 8.f)); }
+FOX_HD uint32_t four_code(float x, float inv) { return four_code_bits(x, inv) - kFourNone; }
 
 #ifdef __CUDACC__
 // ---- eight channels at once, on the device ----
@@ -99,16 +94,22 @@ __device__ __forceinline__ uint4 four_values(uint32_t w, uint32_t byte, bool is_
   }
   return make_uint4(four_bf16(w >> 6, s2), four_bf16(w >> 2, s2), four_bf16(w >> 10, s2), four_bf16(w >> 14 | w << 18, s2));
 }
-// Largest magnitude of eight bf16 as bits of two; of a NaN larger than an infinity's.
-__device__ __forceinline__ uint32_t four_most(const uint4& w) {
-  return __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+// The larger magnitude in both halves of two bf16 pairs, a NaN where there is one; the signs are no numbers'.
+__device__ __forceinline__ uint32_t four_larger(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
+__device__ __forceinline__ uint32_t four_larger(const uint4& w) { return four_larger(four_larger(w.x, w.y), four_larger(w.z, w.w)); }
 // Codes of eight values: nibble c is channel c's.
 __device__ __forceinline__ uint32_t four_codes(const float* f, float inv) {
-  uint32_t code = 0;
+  uint32_t code = four_code_bits(f[7], inv), none = kFourNone;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) code += four_code(f[e], inv) << (4 * e);
-  return code;
+  for (int e = 6; e >= 0; --e) {
+    code = code * 16 + four_code_bits(f[e], inv);
+    none = none * 16 + kFourNone;
+  }
+  return code - none;
 }
 #endif
 
