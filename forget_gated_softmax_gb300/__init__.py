@@ -1074,7 +1074,9 @@ def fox_pages_step(pages: Pages, add, copies, *, parent=None, out: Optional[Page
     index = _pages_call(where, pages, out, ws, stream, add=(add, (B,)), copies=(copies, (B, 2)), parent=(parent, (B,)))
     if ws is None:
         ws = _alloc_on(stream, lambda: pages_workspace(pages, out))
-    st = lib().fox_pages_step(pages.ref, out.ref, _ptr(parent), add.data_ptr(), copies.data_ptr(), ws.data_ptr(), ws.numel(),
+    # the parents of no sequences are not read, but are parents
+    parents = None if parent is None else parent.data_ptr() or ws.data_ptr()
+    st = lib().fox_pages_step(pages.ref, out.ref, parents, add.data_ptr(), copies.data_ptr(), ws.data_ptr(), ws.numel(),
                               _current_stream(index) if stream is None else stream.cuda_stream)
     if st != 0:
         raise FoxError(st, where)

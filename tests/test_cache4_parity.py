@@ -727,6 +727,22 @@ def test_without_the_extension(fox, monkeypatch):
         assert torch.equal(bits(x), bits(y))
 
 
+@pytest.mark.parametrize("H,Hkv,d,new,bad", [(8, 2, 128, 1, float("nan")), (32, 2, 64, 1, float("inf")), (4, 1, 128, 3, float("-inf"))])
+def test_a_bad_query_row_stays_alone(fox, H, Hkv, d, new, bad):
+    """A NaN or an infinity in one row of q: the rows that share its tiles are as without it."""
+    c = Case4([900, 40], [new] * 2, H, Hkv, d, 32, seed=130, uniform=True)
+    c.put()
+    ro, rl = c.attend()
+    q = c.q.clone()
+    q[0, 1, 5] = bad
+    o, lse = fox.fox_cache4_decode(c.cache4(fox), c.batch(fox), q)
+    sound = torch.ones(c.rows, H, dtype=torch.bool, device="cuda")
+    sound[0, 1] = False
+    assert_o(tensor_f64(o[sound]), tensor_f64(ro[sound]), "bf16", "decode4 beside a bad row")
+    assert (lse.double() - rl)[sound].abs().max().item() <= foxtest.TOL_LSE_BF16
+    assert not torch.isfinite(lse[0, 1]) or not torch.isfinite(o[0, 1]).all()
+
+
 def test_handles_of_the_other_kind_are_refused(fox):
     """The calls read the handle's C struct, and the two kinds' differ."""
     c = Case4([40, 20], [1, 1], 4, 2, 64, 16, uniform=True, seed=3)

@@ -350,6 +350,25 @@ def test_step_and_copy_in_a_graph(fox):
         assert [tuple(c) for c in copies.tolist()] == want
 
 
+def test_nothing_to_do(fox):
+    """No sequences, no moves, no pairs; a batch that begins from none."""
+    refs = ints([0] * 20)
+    none = fox.make_pages(16, refs, ints([]), ints([], 0, 5))
+    ws = fox.pages_workspace(none)
+    fox.fox_pages_step(none, ints([]), ints([], 0, 2), ws=ws)
+    mp, used = ints([7] * 20), ints([7, 7])
+    fox.fox_pages_compact(none, mp, ints([], 0, 2), used, ws=ws)
+    fox.fox_cache_copy(fox.new_cache4(4, 16, 4, 2, 64), ints([], 0, 2))
+    assert fox.fox_check_error(ws) == 0 and mp.tolist() == list(range(20)) and used.tolist() == [0, 0]
+    two = fox.make_pages(16, ints([-1] * 20), ints([-1, -1]), ints([-1] * 10, 2, 5))
+    copies = ints([7] * 4, 2, 2)
+    fox.fox_pages_step(none, ints([17, 1]), copies, parent=ints([-1, -1]), out=two)
+    assert two.refs.tolist() == [1] * 3 + [0] * 17 and two.lens.tolist() == [17, 1] and copies.tolist() == [[-1, -1]] * 2
+    assert two.table.tolist() == [[0, 1, -1, -1, -1], [2, -1, -1, -1, -1]]
+    fox.fox_pages_step(two, ints([]), ints([], 0, 2), parent=ints([]), out=none, ws=ws)  # all end
+    assert fox.fox_check_error(ws) == 0 and refs.tolist() == [0] * 20
+
+
 def test_binding_refusals(fox):
     x = Pool(random.Random(1), 4, 16, 4, 60, 0)
     now, out = x.pages(fox), x.blank(fox, 4)
