@@ -9,8 +9,8 @@
 // channels is two threads' neighbouring chunks (K that was rotated with a partner passes through shared memory for that): its largest
 // magnitude by a shuffle, its scale by the first of them, two words of codes by each (fox_four.h).
 //
-// Bound by instructions, then by memory (6 prompts of up to 16384 tokens, 32 + 2 * 8 heads of 128, rotation in pairs: 1.25 GB in 252 us,
-// 5.0 TB/s; the exact rotation is 25 us of them). What that took: the rows of a thread in turn by the same code (unrolled, the warps
+// Bound by memory, as far as rows are on their way (6 prompts of up to 16384 tokens, 32 + 2 * 8 heads of 128, rotation in pairs: 1.27 GB in
+// 242 us, 5.2 TB/s; 18 % fewer instructions, with q in a loop of its own, took as long). What that took: the rows of a thread in turn by the same code (unrolled, the warps
 // waited for instructions: 427 us, in turn 297), a row's loads one row ahead of its use and 64 registers, so that 8 blocks are on an SM
 // (four rows ahead and 6 blocks 289, two and 8 blocks 258, one and 10 blocks with spills 311), and eight rows a thread, before which a block looks up
 // where its rows stand (four 266, sixteen 250 but 62 for 57 where they are read back).
