@@ -6,7 +6,8 @@
 // apart from the old (512 sequences on 65536 pages 16 us, in one kernel 61; 8 of a search on 2048 pages 8.5). compact: a count of the
 // pages in use by blocks of them, then every block knows its pages' ranks, then tables (262144 pages, 1024 sequences 13 us; by one CTA
 // 407); a small pool by one CTA (6.4 us).
-// copy is bound by memory: each page read once and written once, 16 KB a block (1.28 GB read and written 188 us, 6.8 TB/s; 26 MB 5.2 us).
+// copy is bound by memory: each page read once and written once, 16 KB a block (1.28 GB read and written 188 us, 6.8 TB/s; 26 MB 5.2 us),
+// or of many small pages 1024 units of 16 bytes, whatever their array (40000 of 2.1 KB: 174 MB in 35 us, 5.0 TB/s).
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -453,6 +454,70 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyPara
   }
 }
 
+// Small pages: the pairs' units of 8 or 16 bytes of all arrays in one row, 1024 a block, so that no block has a few of one array alone.
+struct UnitParams {
+  char* at[kArrays];
+  uint32_t bytes[kArrays];      // of a page
+  uint32_t first[kArrays + 1];  // units of a page before the array
+  uint32_t wide;                // bit k: array k in units of 16 bytes, else 8
+  int arrays, num_pages, n;
+  const int2* pairs;
+  uint32_t* err;
+};
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_units_kernel(const UnitParams p) {
+  grid_dep_wait();
+  grid_dep_trigger();
+  const uint32_t per = p.first[p.arrays];
+  const uint64_t begin = static_cast<uint64_t>(blockIdx.x) * (kCopyThreads * kCopyLoads);
+  const int pair0 = static_cast<int>(begin / per);
+  const uint32_t rest = static_cast<uint32_t>(begin - static_cast<uint64_t>(pair0) * per);
+  uint4 x[kCopyLoads];
+  char* to[kCopyLoads];
+  bool wide[kCopyLoads];
+#pragma unroll
+  for (int i = 0; i < kCopyLoads; ++i) {
+    const uint32_t at = rest + i * kCopyThreads + threadIdx.x;
+    const int pair = pair0 + static_cast<int>(at / per);
+    const uint32_t unit = at % per;
+    to[i] = nullptr;
+    if (pair >= p.n) continue;
+    const int2 y = p.pairs[pair];
+    if (y.x < 0 || y.x >= p.num_pages || y.y < 0 || y.y >= p.num_pages) {
+      if ((y.x != -1 || y.y != -1) && unit == 0) atomicOr(p.err, DEV_ERR_BOUNDS);
+      continue;
+    }
+    char* base = p.at[0];
+    uint32_t bytes = p.bytes[0], first = 0;
+    int k = 0;
+#pragma unroll
+    for (int j = 1; j < kArrays; ++j)
+      if (j < p.arrays && unit >= p.first[j]) {
+        base = p.at[j];
+        bytes = p.bytes[j];
+        first = p.first[j];
+        k = j;
+      }
+    wide[i] = p.wide >> k & 1;
+    const uint32_t offset = (unit - first) * (wide[i] ? 16 : 8);
+    const char* from = base + static_cast<uint64_t>(y.x) * bytes + offset;
+    to[i] = base + static_cast<uint64_t>(y.y) * bytes + offset;
+    if (wide[i]) {
+      x[i] = __ldcs(reinterpret_cast<const uint4*>(from));
+    } else {
+      const uint2 z = __ldcs(reinterpret_cast<const uint2*>(from));
+      x[i] = make_uint4(z.x, z.y, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyLoads; ++i) {
+    if (!to[i]) continue;
+    if (wide[i])
+      __stcs(reinterpret_cast<uint4*>(to[i]), x[i]);
+    else
+      __stcs(reinterpret_cast<uint2*>(to[i]), make_uint2(x[i].x, x[i].y));
+  }
+}
+
 // ---- host ----
 bool ints(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -523,18 +588,54 @@ CopyParams copy_params(const PageArrays& x) {
   return p;
 }
 
+// Pages below 24 KB by units, where there are more blocks of chunks than the SMs hold at once. By units and by chunks: 40000 pages of 2.1 KB
+// 35 and 283 us, 30000 of 5.1 KB 58 and 153, 20000 of 12.6 KB 92 and 143, 10000 of 21 KB 78.1 and 79.4, 6000 of 42 KB 93 and 78,
+// 8000 of 84 KB 240 and 202; 48 of 2.1 KB 3.3 and 2.2.
+bool copies_units(const PageArrays& x, int n) {
+  long long bytes = 0;
+  for (int k = 0; k < x.n; ++k) bytes += x.bytes[k];
+  return bytes < 24576 && (long long)n * copy_params(x).chunks[x.n] > 2048 / kCopyThreads * kSMs;
+}
+UnitParams unit_params(const PageArrays& x) {
+  UnitParams p = {};
+  p.arrays = x.n;
+  for (int k = 0; k < x.n; ++k) {
+    const bool wide = x.bytes[k] % 16 == 0;
+    p.at[k] = x.at[k];
+    p.bytes[k] = static_cast<uint32_t>(x.bytes[k]);
+    p.wide |= static_cast<uint32_t>(wide) << k;
+    p.first[k + 1] = p.first[k] + p.bytes[k] / (wide ? 16 : 8);
+  }
+  return p;
+}
+long long copy_blocks(const PageArrays& x, int n) {
+  constexpr int kUnits = kCopyThreads * kCopyLoads;
+  if (copies_units(x, n)) return ((long long)n * unit_params(x).first[x.n] + kUnits - 1) / kUnits;
+  return (long long)n * copy_params(x).chunks[x.n];
+}
+
 }  // namespace
 
-bool pages_copy_fits(const PageArrays& x, int n) { return (long long)n * copy_params(x).chunks[x.n] <= 0x7fffffffLL; }
+bool pages_copy_fits(const PageArrays& x, int n) { return copy_blocks(x, n) <= 0x7fffffffLL; }
 
 cudaError_t launch_pages_copy(const PageArrays& x, int num_pages, const int32_t* pairs, int n, uint32_t* err, cudaStream_t s) {
-  CopyParams p = copy_params(x);
-  p.num_pages = num_pages;
-  p.pairs = reinterpret_cast<const int2*>(pairs);
-  p.err = err;
+  const dim3 blocks(static_cast<unsigned>(copy_blocks(x, n)));
   TraceScope trace("pages_copy", s);
-  const cudaError_t e = launch_dependent(pages_copy_kernel, dim3(static_cast<unsigned>(n) * p.chunks[p.arrays]),
-                                         dim3(kCopyThreads), 0, s, p);
+  cudaError_t e;
+  if (copies_units(x, n)) {
+    UnitParams p = unit_params(x);
+    p.num_pages = num_pages;
+    p.n = n;
+    p.pairs = reinterpret_cast<const int2*>(pairs);
+    p.err = err;
+    e = launch_dependent(pages_copy_units_kernel, blocks, dim3(kCopyThreads), 0, s, p);
+  } else {
+    CopyParams p = copy_params(x);
+    p.num_pages = num_pages;
+    p.pairs = reinterpret_cast<const int2*>(pairs);
+    p.err = err;
+    e = launch_dependent(pages_copy_kernel, blocks, dim3(kCopyThreads), 0, s, p);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -227,7 +227,8 @@ def arrays(c):
 
 @pytest.mark.parametrize("kind", ["4bit", "bf16", "f32"])
 @pytest.mark.parametrize("H,Hkv,d,S,pages,n,low", [(1, 1, 64, 16, 7, 3, True), (14, 2, 128, 64, 60, 25, False), (9, 3, 64, 32, 300, 140, True),
-                                                   (32, 8, 128, 128, 12, 6, True)])
+                                                   (32, 8, 128, 128, 12, 6, True),
+                                                   (9, 1, 64, 16, 1500, 700, True), (8, 2, 64, 16, 900, 400, False)])  # many small pages
 def test_copy(fox, kind, H, Hkv, d, S, pages, n, low):
     gen = torch.Generator("cuda").manual_seed(1)
     c = (fox.new_cache4(pages, S, H, Hkv, d) if kind == "4bit" else
@@ -249,7 +250,7 @@ def test_copy(fox, kind, H, Hkv, d, S, pages, n, low):
     for x, y in zip(arrays(c), want):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     # ids outside the pool: reported, nothing is copied for them
-    bad = ints([[pages, int(order[0])], [int(order[0]), -1], [-5, -5], [int(order[0]), pages + 7]])
+    bad = ints([[pages, int(order[0])], [int(order[0]), -1], [-5, -5], [int(order[0]), pages + 7]] * (300 if n >= 400 else 1))
     fox.fox_cache_copy(c, bad, ws=ws)
     assert fox.fox_check_error(ws) == FOX_ERR_DEVICE
     for x, y in zip(arrays(c), want):
