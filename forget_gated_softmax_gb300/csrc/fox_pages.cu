@@ -3,7 +3,8 @@
 //
 // step and compact are integers all: what bounds them is latency, a dependent trip to memory or a barrier after the other, so that they take
 // few of both. step: one CTA for what hangs together, behind a kernel that copies references and table rows where the new state is
-// apart from the old (512 sequences on 65536 pages 16 us, in one kernel 61; 8 of a search on 2048 pages 8.5). compact: a count of the
+// apart from the old, and one that counts references where there are many (512 sequences on 65536 pages 12 us, in one kernel 61; 8 of a
+// search on 2048 pages 8.2). compact: a count of the
 // pages in use by blocks of them, then every block knows its pages' ranks, then tables (262144 pages, 1024 sequences 13 us; by one CTA
 // 407); a small pool by one CTA (6.4 us).
 // copy is bound by memory: each page read once and written once, 16 KB a block (1.28 GB read and written 188 us, 6.8 TB/s; 26 MB 5.2 us),
@@ -73,6 +74,7 @@ struct StepParams {
   int32_t* copies;
   int32_t* list;  // [num_pages] of the workspace: of a shared last page the last sequence that goes on in it; then free pages, the lowest first
   bool begun;     // pages_begin_kernel was launched
+  bool counted;   // and pages_refs_kernel
   uint32_t* err;
 };
 
@@ -98,6 +100,28 @@ __global__ void __launch_bounds__(kCopyThreads) pages_begin_kernel(const StepPar
   for (int c = tid; c < n; c += kCopyThreads) out.table[(size_t)b * out.stride + c] = in.table[(size_t)src * in.stride + c];
 }
 
+// References of an old sequence's pages, a block a sequence: by its children less one.
+__global__ void __launch_bounds__(kCopyThreads) pages_refs_kernel(const StepParams p) {
+  const Pool& in = p.in;
+  grid_dep_trigger();
+  const int b = blockIdx.x, tid = threadIdx.x;
+  int mine = 0;
+  for (int i = tid; i < p.out.B; i += kCopyThreads) mine += p.parent[i] == b;
+  const int kids = __syncthreads_count(mine & 1) + 2 * __syncthreads_count(mine >> 1 & 1) + 4 * __syncthreads_count(mine >> 2 & 1) +
+                   8 * __syncthreads_count(mine >> 3);  // at most 8 of a thread
+  static_assert(kMaxSeqs <= 8 * kCopyThreads, "");
+  const int n = kids == 1 ? 0 : pages_of(in, own_tokens(in, in.lens[b], p.err));
+  grid_dep_wait();
+#pragma unroll 4
+  for (int c = tid; c < n; c += kCopyThreads) {
+    const int id = in.table[(size_t)b * in.stride + c];
+    if (id >= 0 && id < in.num_pages)
+      atomicAdd(p.out.refs + id, kids - 1);
+    else
+      atomicOr(p.err, DEV_ERR_BOUNDS);
+  }
+}
+
 __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepParams p) {
   constexpr int kEach = kMaxSeqs / kPageThreads, kLoad = 16, kNoPages = 0x7FFFFFFF;
   __shared__ int kids[kMaxSeqs];       // children of the old sequences; then whether a new one's last page is copied
@@ -119,7 +143,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepPara
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int b = tid + i * kPageThreads;
-    old_len[i] = p.parent && b < in.B ? in.lens[b] : 0;
+    old_len[i] = p.parent && !p.counted && b < in.B ? in.lens[b] : 0;
     last[i] = -1;
     len[i] = n0[i] = n1[i] = add[i] = 0;
     grows[i] = part[i] = false;
@@ -569,6 +593,9 @@ fox_status check_header(void* ws, size_t bytes, size_t need) {
 // The header, and an int a page (step's list; compact's counts are fewer).
 size_t pages_workspace(const fox_pages* x) { return kCacheHeaderBytes + align_up(sizeof(int32_t) * (size_t)x->num_pages, 256); }
 int32_t* behind_header(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kCacheHeaderBytes); }
+// References of large tables by a kernel of their own: one SM's atomics take a nanosecond each. By it and by the step's CTA: 8 sequences of 64
+// entries 9.9 and 8.2 us, 64 of a search of 64 10.5 and 10.8, 256 10.7 and 15.7, 1024 of 94 14.8 and 46; 512 of 129, most of which go on, 12.0 and 15.8.
+bool counts_apart(const fox_pages* in, const int32_t* parent) { return parent && (long long)in->B * in->table_stride > 2048; }
 // One CTA has a pool of 4096 pages in its registers, and renames 32 pieces of 32 entries at a time, half a microsecond or more each. By one
 // CTA and by three kernels: 16 sequences of 32 entries (512 pages) 3.9 and 6.4 us, 64 of 64 (4096 pages: 4 rounds) 9.4 and 10.5, 128 of 512
 // (64 rounds) 42 and 11, 2048 of 32 63 and 12.
@@ -668,13 +695,17 @@ fox_status fox_pages_step(const fox_pages* in, const fox_pages* out, const int32
   st = check_header(workspace, workspace_bytes, pages_workspace(in));
   if (st != FOX_OK) return st;
   const StepParams p = {pool_of(in), pool_of(out), parent, add, copies, behind_header(workspace),
-                        in->refs != out->refs || in->table != out->table, static_cast<uint32_t*>(workspace)};
+                        in->refs != out->refs || in->table != out->table, counts_apart(in, parent), static_cast<uint32_t*>(workspace)};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (p.begun) {
     TraceScope trace("pages_begin", s);
     const int blocks = ceil_div(in->num_pages, kCopyThreads), wide = blocks < kSMs ? blocks : kSMs;
     e = launch_dependent(pages_begin_kernel, dim3(out->B > wide ? out->B : wide), dim3(kCopyThreads), 0, s, p);
+  }
+  if (e == cudaSuccess && p.counted) {
+    TraceScope trace("pages_refs", s);
+    e = launch_dependent(pages_refs_kernel, dim3(in->B), dim3(kCopyThreads), 0, s, p);
   }
   if (e == cudaSuccess) {
     TraceScope trace("pages_step", s);

@@ -135,6 +135,21 @@ def test_step(fox, n, how):
     assert not any(refs)
 
 
+@pytest.mark.parametrize("stride", [500, 1000])  # references counted by the step itself, and by a kernel of their own
+def test_most_sequences_go_on_from_one(fox, stride):
+    import pagestest
+
+    x = Pool(random.Random(9), 3, 16, stride, 8000, 0, full=0.5, idle=0)
+    parent, add = [1] * 2047 + [2], [1] * 2048
+    refs, lens, rows, copies, short = pagestest.step(x.refs, x.lens, x.table, parent, add, 16, 0, 2048)
+    now, out = x.pages(fox), x.blank(fox, 2048)
+    got, ws = ints([0] * 4096, 2048, 2), fox.pages_workspace(now, out)
+    fox.fox_pages_step(now, ints(add), got, parent=ints(parent), out=out, ws=ws)
+    assert not short and fox.fox_check_error(ws) == 0
+    assert out.refs.tolist() == refs and out.lens.tolist() == lens
+    assert out.table.tolist() == table_of(rows, 2048, stride) and [tuple(c) for c in got.tolist()] == copies
+
+
 def test_step_of_what_does_not_fit_is_reported(fox):
     """Parents, lengths, adds and pages outside their ranges: reported, the other sequences as if it were not there."""
     import pagestest
