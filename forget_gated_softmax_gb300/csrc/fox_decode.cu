@@ -170,7 +170,7 @@ bool share_prefix(const PagedArgs& a, int row_tiles) {
 // The same of a 4-bit cache, where a key tile walked costs instructions (1 ns of the whole GPU's time, half as much more in tiles of
 // 16 rows), and sharing spreads the prefix out first: some 16 us, and 5.5 ns a tile of the prefix at 128 channels. In tiles walked.
 // 32 heads on 8 of 128 channels, walked and shared: 8 sequences behind 16384 tokens 52 and 55 us, 16 behind 4096 36 and 42, 64 behind 1024
-// 39 and 40, 2 behind 65536 46 and 125, 256 behind 32768 2053 and 199; 16 heads of 64 channels, 16 sequences behind 4096 40.5 and 38.6,
+// 39 and 40, 2 behind 65536 46 and 125, 256 behind 32768 2053 and 192; 16 heads of 64 channels, 16 sequences behind 4096 40.5 and 38.6,
 // 32 behind 4096 65 and 42; 4 with 16 new tokens each behind 4096 49 and 51.
 bool share_prefix4(const PagedArgs& a, int row_tiles, int Rt) {
   const long long tiles = (long long)ceil_div(a.prefix_len, kKeyTile) * a.Hkv, walked = a.B * row_tiles * tiles;
@@ -265,9 +265,9 @@ cudaError_t launch_decode(const DecodeArgs& x, Held held, char* ws, cudaStream_t
     spread.a.gbase = reinterpret_cast<float*>(ws + L.pbase);
     spread.a.prefix = reinterpret_cast<int32_t*>(ws + L.ptab);
     e = launch_spread4(p, spread.a, s);
-    if (e == cudaSuccess) e = launch_prefix(spread, s);
+    if (e == cudaSuccess) e = launch_prefix(spread, true, s);
   } else if (p.pre.key_tiles > 0) {
-    e = launch_prefix(p, s);
+    e = launch_prefix(p, false, s);
   }
   if (e != cudaSuccess) return e;
   if (held == Held::kF32) return launch_decode_f32(p, s);

@@ -532,10 +532,10 @@ cudaError_t launch_decode_f32(const DecodeParams& p, cudaStream_t s);
 int decode4_rows(int rows);
 int decode4_warps(const PagedArgs& a, int Rt);
 cudaError_t launch_decode4(const DecodeParams& p, cudaStream_t s);
-// A 4-bit cache's shared prefix, K and V spread out to bf16 (exactly) in the pool `to` of its pages in their order, with their gates and
+// A 4-bit cache's shared prefix, K spread out to bf16 and V to fp16 (exactly) in the pool `to` of its pages in their order, with their gates and
 // their table, for the prefix kernel.
 cudaError_t launch_spread4(const DecodeParams& p, const PagedArgs& to, cudaStream_t s);
 PrefixPlan prefix_plan(const PagedArgs& a);
-cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_prefix(const DecodeParams& p, bool v16, cudaStream_t s);  // v16: V in fp16
 
 }  // namespace fox

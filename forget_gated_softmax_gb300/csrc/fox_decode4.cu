@@ -719,11 +719,15 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
   if (shared) grid_dep_wait();  // as fox_decode_mma.cu's kernel
 }
 
+// The prefix's K in bf16 and V in fp16, as the prefix kernel multiplies them; V of 65536 and above is reported.
 // Blocks of kSpreadUnits units of a page's K, then of its V, and one more a page for its gates and table entry. A unit is 16 channels of one
 // token and head, a chunk of each half of the head: stores are contiguous over lanes. Bound by memory: 32768 tokens of 8 heads of 128 channels, 34 MB
 // to 134, 30 us, 5.5 TB/s (a chunk a thread, blocks of one head 45).
 constexpr int kSpreadThreads = 256, kSpreadUnits = 8 * kSpreadThreads;
 inline int spread_blocks(const PagedArgs& a) { return ceil_div(a.Hkv * a.page_size * (a.d / 16), kSpreadUnits); }
+__device__ __forceinline__ uint32_t four_largest(const uint4& w) {
+  return __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+}
 template <int D>
 __global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ PagedArgs to,
                                                                  int blocks) {
@@ -746,6 +750,7 @@ __global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_co
   const bool is_v = part >= blocks;
   const int begin = (is_v ? part - blocks : part) * kSpreadUnits, end = min(begin + kSpreadUnits, a.Hkv * S * kUnits);
   const int j = tid % kUnits, b = j >> 2, t = j & 3;
+  uint32_t most = 0;  // magnitudes of V, as bits
   const uint8_t* from = static_cast<const uint8_t*>(is_v ? a.v : a.k) + four_row(a, page, 0, 0);
   const uint8_t* scales = (is_v ? p.vs : p.ks) + four_scale_row(a, page, 0, 0);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) + kv_offset(to, at, 0, 0) + j * 8;
@@ -759,9 +764,16 @@ __global__ void __launch_bounds__(kSpreadThreads) spread4_kernel(const __grid_co
     const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + (is_v ? word ^ kHalf * 16 : word + kHalf * 4));
     const uint32_t s0 = scale[0], s1 = scale[is_v ? 4 * kHalf : kHalf];
     uint4* to_row = reinterpret_cast<uint4*>(out + (size_t)row * D);
-    to_row[0] = slot < live ? four_values(w0, s0, is_v) : make_uint4(0, 0, 0, 0);
-    to_row[D / 16] = slot < live ? four_values(w1, s1, is_v) : make_uint4(0, 0, 0, 0);
+    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+    if (slot < live) {
+      x0 = is_v ? four_v16(w0, s0) : four_values(w0, s0, false);
+      x1 = is_v ? four_v16(w1, s1) : four_values(w1, s1, false);
+      if (is_v) most = __vmaxu2(most, __vmaxu2(four_largest(x0), four_largest(x1)));
+    }
+    to_row[0] = x0;
+    to_row[D / 16] = x1;
   }
+  if (((most & 0xFFFFu) >= 0x7C00u || most >= 0x7C000000u) && a.err) atomicOr(a.err, DEV_ERR_RANGE);
 }
 
 constexpr size_t smem_bytes(int D, int rows, int W, size_t B) {

@@ -85,6 +85,19 @@ __device__ __forceinline__ uint32_t four_bf16(uint32_t n, uint32_t s2) {  // nib
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(y), "r"(s2));
   return x;
 }
+// The fp16 values of a word of V, an infinity for 65536 and above. Pairs of 1024 + n, less 1032, times s: exact.
+__device__ __forceinline__ uint32_t four_f16(uint32_t n, uint32_t s2) {  // nibbles at bits 3..0 of both halves
+  uint32_t x, y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(n), "r"(0x000F000Fu), "r"(0x64006400u));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xE408E408u));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(y), "r"(s2));
+  return x;
+}
+__device__ __forceinline__ uint4 four_v16(uint32_t w, uint32_t byte) {
+  const uint32_t s2 = byte * 0x00800080u;  // a byte's nibbles 16 bits apart: times 0x1001
+  return make_uint4(four_f16((w & 255u) * 0x1001u, s2), four_f16((w >> 8 & 255u) * 0x1001u, s2), four_f16((w >> 16 & 255u) * 0x1001u, s2),
+                    four_f16((w >> 24) * 0x1001u, s2));
+}
 // The bf16 values of a word of K or of V.
 __device__ __forceinline__ uint4 four_values(uint32_t w, uint32_t byte, bool is_v) {
   const uint32_t s = float_bits(four_scale(byte)) >> 16, s2 = s << 16 | s;

@@ -24,7 +24,7 @@
 // loads Q and K, warps 9 and 14 issue the streams' MMAs (one warp for both spent 1.7 us a key tile on
 // waits, fences and commits that two have side by side), warps 10-11 load V and make the gate terms
 // log2 e (c_j - c_last) of a key tile's keys and the row tile's heads, a stage each, and warps 12, 13 and 15
-// turn each V tile from bf16 to fp16 in place.
+// turn each V tile from bf16 to fp16 in place (kV16: only clear what is behind the prefix's end).
 //
 // P V runs in fp16, as in fox_attn_fwd_kernel and for its reason: with bf16 P its 8 significant bits add an
 // error as large as O's own rounding. Two bf16 terms a weight (as in fox_decode_mma.cu, where products
@@ -82,7 +82,7 @@ enum PBar {
 
 __host__ __device__ constexpr int e_bar(int stream, int half) { return 2 * stream + half; }
 
-template <int D, bool kSplit>
+template <int D, bool kSplit, bool kV16>  // kV16: V comes in fp16
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ DecodeParams p) {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // No further unrolled: in bursts the softmax waits for its loads of shared memory (by 2 137 us, by 4 153,
         // by 8 171 at 32768 keys and 1024 rows a key head).
 #pragma unroll 2
-        for (int e = first; e < L::kTileBytes / 16; e += 32 * kConverters) {
+        for (int e = first; !kV16 && e < L::kTileBytes / 16; e += 32 * kConverters) {
           const uint4 w = tile[e];
           const uint32_t in[4] = {w.x, w.y, w.z, w.w};
           uint32_t out[4];
@@ -531,10 +531,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   }
 }
 
-template <int D, bool kSplit>
+template <int D, bool kSplit, bool kV16>
 cudaError_t launch(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t s) {
   using L = PrefixLayout<D>;
-  auto kernel = prefix_kernel<D, kSplit>;
+  auto kernel = prefix_kernel<D, kSplit, kV16>;
   // At least 116 KB, so that one CTA, which takes all of tensor memory, is ever resident on an SM.
   constexpr size_t kLeast = 118784;
   size_t smem = 1024 + L::kKap + sizeof(float) * 2 * p.pre.kap_tiles * p.pre.hp * kKapPitch;
@@ -584,15 +584,22 @@ PrefixPlan prefix_plan(const PagedArgs& a) {
   return x;
 }
 
-cudaError_t launch_prefix(const DecodeParams& p, cudaStream_t s) {
+namespace {
+template <bool kV16>
+cudaError_t launch_as(const DecodeParams& p, const CUtensorMap* maps, cudaStream_t s) {
+  if (p.pre.row_tiles == 1) return p.a.d == 64 ? launch<64, true, kV16>(p, maps, s) : launch<128, true, kV16>(p, maps, s);
+  return p.a.d == 64 ? launch<64, false, kV16>(p, maps, s) : launch<128, false, kV16>(p, maps, s);
+}
+}  // namespace
+
+cudaError_t launch_prefix(const DecodeParams& p, bool v16, cudaStream_t s) {
   const PagedArgs& a = p.a;
   CUtensorMap maps[3];
   if (!make_q_rows_map(&maps[0], p.q, a.d, a.H, a.rows, p.q_stride, 1, p.pre.tpt) ||
       !make_page_map(&maps[1], a.k, a.d, a.page_size, a.Hkv, a.num_pages, a.page_size) ||
       !make_page_map(&maps[2], a.v, a.d, a.page_size, a.Hkv, a.num_pages, a.page_size))
     return cudaErrorInvalidValue;
-  if (p.pre.row_tiles == 1) return a.d == 64 ? launch<64, true>(p, maps, s) : launch<128, true>(p, maps, s);
-  return a.d == 64 ? launch<64, false>(p, maps, s) : launch<128, false>(p, maps, s);
+  return v16 ? launch_as<true>(p, maps, s) : launch_as<false>(p, maps, s);
 }
 
 }  // namespace fox

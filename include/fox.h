@@ -414,7 +414,7 @@ fox_status fox_cache4_append(const fox_cache4* c, const fox_batch* s, int rows, 
 
 /*
  * fox_decode over a 4-bit cache, with its arguments and results. The weights pass through fp16, at up to 2^10 times their
- * value against the running maximum; a shared prefix is, where that saves time, spread out to bf16 in the workspace and shared as
+ * value against the running maximum; a shared prefix is, where that saves time, spread out to bf16 and fp16 in the workspace and shared as
  * there (a V held as 65536 or more in it then sets the error word).
  */
 fox_status fox_cache4_decode(const fox_cache4* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,

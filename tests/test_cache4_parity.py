@@ -309,7 +309,7 @@ def test_decode(fox, n):
     check_decode(fox, c, f"decode4 {n}", bj, scale)
 
 
-# Behind prefixes long enough for the batch that they are shared out (spread to bf16, then one kernel for all sequences).
+# Behind prefixes long enough for the batch that they are shared out (spread out, then one kernel for all sequences).
 SHARED = [
     ([13 + i for i in range(48)], [1] * 48, 8, 8, 128, 64, 3001, dict(uniform=True, bias_from_j=True)),  # one row tile, keys split
     ([3] * 150, [1] * 150, 4, 1, 128, 16, 5003, dict(uniform=True)),                       # row tiles of a small group
