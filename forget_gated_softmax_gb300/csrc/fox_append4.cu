@@ -10,8 +10,9 @@
 // magnitude by a shuffle, its scale by the first of them, two words of codes by each (fox_four.h).
 //
 // Bound by memory, as far as rows are on their way (6 prompts of up to 16384 tokens, 32 + 2 * 8 heads of 128, rotation in pairs: 1.27 GB in
-// 242 us, 5.2 TB/s; 18 % fewer instructions, with q in a loop of its own, took as long). What that took: the rows of a thread in turn by the same code (unrolled, the warps
-// waited for instructions: 427 us, in turn 297), a row's loads one row ahead of its use and 64 registers, so that 8 blocks are on an SM
+// 242 us, 5.2 TB/s; 18 % fewer instructions, with q in a loop of its own, took as long). What that took: the rows of a thread in turn by
+// the same code (unrolled, the warps waited for instructions: 427 us, in turn 297), a row's loads one row ahead of its use and 64
+// registers, so that 8 blocks are on an SM
 // (four rows ahead and 6 blocks 289, two and 8 blocks 258, one and 10 blocks with spills 311), and eight rows a thread, before which a block looks up
 // where its rows stand (four 266, sixteen 250 but 62 for 57 where they are read back).
 // One token of each of 128 sequences: 12 us by itself, most of it the launch and dependent trips to memory.

@@ -11,7 +11,7 @@
 //   instructions a word and no subtraction of its own, and fp32 sums keep 2^-24 of 264 sum |q|. The block's scale multiplies its sum.
 // V. ldmatrix.trans turns 16-bit units (four channels of a token) so that a register has the same four channels of two
 //   neighbouring tokens: what the V^T operand wants, nibble by nibble. The masks give 1 + n / 1024 and 1 + n / 64, an fma n - 8, exactly.
-//   The scales, which vary along the sum, go to P: P s in fp16 (P and s in fp16, so rounded twice by 2^-12), once a block of 32 channels.
+//   The scales, which vary along the sum, go to P: P s in fp16 (P is, and the product; s exactly: rounded twice, by 2^-11 at most), once a block of 32 channels.
 // Weights are P = 2^(x - r), with r = the running maximum less `lift`: as fp16 holds 2^15 down to 2^-24, weights down to
 //   2^-24 of the largest keep all bits at lift 10. lift falls where scales of 2 and above are met, so that P s stays below 2^15 too;
 //   r moves when a weight passes 2^(lift + 4), or a scale its bound, which one vote finds: the weights are then formed again.
@@ -22,7 +22,8 @@
 //
 // Bound by instructions: 785 a key tile of 128 channels and 4 rows, 180 of them to spread K out, 200 V, 95 the copies (all lanes' own: by
 // bulk copies of a loading warp, which has a lane a worker, 301 us against 235 then). 64 sequences of up to 16384 tokens, 32 heads on 8, 725 MB:
-// 169 us, 4.3 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 132. V as subnormals, unchanged by a subtraction
+// 169 us, 4.3 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 130, the
+// rest without them 135 (15 of either are launch, look-ups and join). V as subnormals, unchanged by a subtraction
 // of 8 that two more products make: 4 % fewer instructions, 177 for 172 us. One sequence of 65536, 80 MB: 34 us, of which launch and first
 // look-ups are 13 and the join of the workers' parts 6; one of 1000, 16 heads of 64 channels: 14.5, all but 3 of them launch, look-ups and join.
 #include <cuda_bf16.h>

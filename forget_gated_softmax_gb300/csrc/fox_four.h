@@ -74,7 +74,6 @@ FOX_HD uint32_t four_scale_byte(float amax) {
 // integer is then what an fma with 1.5 * 2^23 leaves in the low bits.
 constexpr uint32_t kFourNone = 0x4B400000u;
 FOX_HD uint32_t four_code_bits(float x, float inv) { return float_bits(fmaf(x, inv * (1.f + 0x1p-15f), 12582912.f + 8.f)); }
-FOX_HD uint32_t four_code(float x, float inv) { return four_code_bits(x, inv) - kFourNone; }
 
 #ifdef __CUDACC__
 // ---- eight channels at once, on the device ----

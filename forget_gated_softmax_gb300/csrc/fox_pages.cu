@@ -594,7 +594,8 @@ fox_status check_header(void* ws, size_t bytes, size_t need) {
 size_t pages_workspace(const fox_pages* x) { return kCacheHeaderBytes + align_up(sizeof(int32_t) * (size_t)x->num_pages, 256); }
 int32_t* behind_header(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kCacheHeaderBytes); }
 // References of large tables by a kernel of their own: one SM's atomics take a nanosecond each. By it and by the step's CTA: 8 sequences of 64
-// entries 9.9 and 8.2 us, 64 of a search of 64 10.5 and 10.8, 256 10.7 and 15.7, 1024 of 94 14.8 and 46; 512 of 129, most of which go on, 12.0 and 15.8.
+// entries 9.9 and 8.2 us, 64 of a search of 64 10.5 and 10.8, 256 10.7 and 15.7, 1024 of 94 14.8 and 46; 512 of 129, most of which go on,
+// 12.0 and 15.8.
 bool counts_apart(const fox_pages* in, const int32_t* parent) { return parent && (long long)in->B * in->table_stride > 2048; }
 // One CTA has a pool of 4096 pages in its registers, and renames 32 pieces of 32 entries at a time, half a microsecond or more each. By one
 // CTA and by three kernels: 16 sequences of 32 entries (512 pages) 3.9 and 6.4 us, 64 of 64 (4096 pages: 4 rounds) 9.4 and 10.5, 128 of 512

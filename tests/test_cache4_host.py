@@ -214,7 +214,7 @@ using namespace fox;
 extern "C" {
 int scale_byte(float x) { return (int)four_scale_byte(x); }
 float scale(int b) { return four_scale((uint32_t)b); }
-int code(float x, int b) { return (int)four_code(x, b ? 1.f / four_scale((uint32_t)b) : 0.f); }
+int code(float x, int b) { return (int)(four_code_bits(x, b ? 1.f / four_scale((uint32_t)b) : 0.f) - kFourNone); }
 unsigned order(unsigned w) { return four_k_order(w); }
 long long place(int what, int Hkv, int S, int d, int page, int h, int slot, int b, int t) {
   PagedArgs a = {};
