@@ -22,9 +22,8 @@
 //
 // Bound by instructions: 785 a key tile of 128 channels and 4 rows, 180 of them to spread K out, 200 V, 95 the copies (all lanes' own: by
 // bulk copies of a loading warp, which has a lane a worker, 301 us against 235 then). 64 sequences of up to 16384 tokens, 32 heads on 8, 725 MB:
-// 169 us, 4.3 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 130, the
-// rest without them 135 (15 of either are launch, look-ups and join). V as subnormals, unchanged by a subtraction
-// of 8 that two more products make: 4 % fewer instructions, 177 for 172 us. One sequence of 65536, 80 MB: 34 us, of which launch and first
+// 169 us, 4.3 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 130, the rest without them 135 (15 of either are
+// launch, look-ups and join). V as subnormals, their offset of 8 taken off by two more products: 4 % fewer instructions, 177 for 172 us. One sequence of 65536, 80 MB: 34 us, of which launch and first
 // look-ups are 13 and the join of the workers' parts 6; one of 1000, 16 heads of 64 channels: 14.5, all but 3 of them launch, look-ups and join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
