@@ -11,10 +11,13 @@
 //   instructions a word and no subtraction of its own, and fp32 sums keep 2^-24 of 264 sum |q|. The block's scale multiplies its sum.
 // V. ldmatrix.trans turns 16-bit units (four channels of a token) so that a register has the same four channels of two
 //   neighbouring tokens: what the V^T operand wants, nibble by nibble. The masks give 1 + n / 1024 and 1 + n / 64, an fma n - 8, exactly.
-//   The scales, which vary along the sum, go to P: P s in fp16 (P is, and the product; s exactly: rounded twice, by 2^-11 at most), once a block of 32 channels.
-// Weights are P = 2^(x - r), with r = the running maximum less `lift`: as fp16 holds 2^15 down to 2^-24, weights down to
-//   2^-24 of the largest keep all bits at lift 10. lift falls where scales of 2 and above are met, so that P s stays below 2^15 too;
-//   r moves when a weight passes 2^(lift + 4), or a scale its bound, which one vote finds: the weights are then formed again.
+//   The scales, which vary along the sum, go to P, once a block of 32 channels: P s f in fp16, with f the power of two that brings the largest
+//   scale met so far in the block's channels to [1, 2), so that neither small nor large values leave fp16's range. P is rounded to fp16,
+//   and the product again, by 2^-11 of itself at most each while the product is 2^-14 or more; f is taken off when the sums leave. A lane
+//   spreads s f out for the warp, a word of four, over the stage's scales (by every lane for itself, 8 more instructions a tile: 176 us below).
+// Weights are P = 2^(x - r), with r = the running maximum less kLift: as fp16 holds 2^-24 and above, in full from 2^-14 on, weights down to
+//   2^-25 of the largest keep all bits, and so do their products with scales of the largest's size (of 2^-k of it, from 2^(k - 25) on);
+//   r moves when a weight passes 2^(kLift + kRoom), f when a scale passes its bound, which one vote finds: the weights are then formed again.
 // q in fp16: each row times a power of two so that its largest |q| is in [4, 8); what a bf16 holds is then exact down to 2^-21 of that,
 //   and off by 2^-32 of it at most.
 // Up to four rows a tile (kRows 4) stand twice among the eight columns, so that scores and weights of half the keys fall to each half of the
@@ -22,7 +25,7 @@
 //
 // Bound by instructions: 785 a key tile of 128 channels and 4 rows, 180 of them to spread K out, 200 V, 95 the copies (all lanes' own: by
 // bulk copies of a loading warp, which has a lane a worker, 301 us against 235 then). 64 sequences of up to 16384 tokens, 32 heads on 8, 725 MB:
-// 169 us, 4.3 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 130, the rest without them 135 (15 of either are
+// 171 us, 4.2 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 130, the rest without them 135 (15 of either are
 // launch, look-ups and join). V as subnormals, their offset of 8 taken off by two more products: 4 % fewer instructions, 177 for 172 us. One sequence of 65536, 80 MB: 34 us, of which launch and first
 // look-ups are 13 and the join of the workers' parts 6; one of 1000, 16 heads of 64 channels: 14.5, all but 3 of them launch, look-ups and join.
 #include <cuda_bf16.h>
@@ -35,9 +38,11 @@
 namespace fox {
 namespace {
 
-constexpr int kRoom = 4;  // log2 units that a score may pass the running maximum by
-// A weight of the running maximum is 2^lift; top_e: the largest exponent bits of a scale of V, 15 (scales below 2) at least.
-__device__ __forceinline__ int lift_of(int top_e) { return 25 - top_e; }
+// A weight of the running maximum is 2^kLift at least, and 2^(kLift + kRoom) before the reference moves: 2^15 times 1.875, the largest scale
+// times f, is below fp16's end.
+constexpr int kLift = 11, kRoom = 4;
+constexpr uint32_t kWeightRoom = (0x7FFFu - (kLift + kRoom + 15 << 10)) * 0x00010001u;  // added to a weight above 2^(kLift + kRoom): a sign bit
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 template <int D, int kRows_>  // rows of a row tile: 4, 8 or 16
 struct Layout4 {
@@ -76,6 +81,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t majority(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xe8;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
 // (w & mask) | 1.0 in both halves, one instruction.
@@ -359,8 +369,10 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
     float unit[NT][2];          // log2 units of a row's S
     float acc[2 * NB][NT][4];   // O^T: of block b channels 4 g8 + 0, + 1 and + 2, + 3
     float r[NT][2], l[NT][2];   // the reference that weights are taken against, their sum
-    int top_e = 15;             // exponent bits of the largest scale of V so far, 15 at least
-    uint32_t weight_room = 0, scale_room = 0;  // what is left to the bounds of weights and scales (`over` below)
+    // Of the block of channels whose scales this lane spreads out, lane % NB: exponent bits of the largest scale of V so far, its bound
+    // (`over` below), and f, 2^(15 - exponent bits), twice.
+    int top_e = 0;
+    uint32_t scale_room = 0, scale_low = 0, f2 = 0;
     Gate2 ci[NT][2];
     int pos[NT][2], head[NT][2];  // a row's own place, its head of the row tile's
 #pragma unroll
@@ -452,7 +464,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
       uint8_t* st = ring + stage * L::kStageBytes;
       const uint8_t* sk = st;
       const uint8_t* sv = st + L::kTileBytes;
-      const uint8_t* sks = sv + L::kTileBytes;
+      uint8_t* sks = st + 2 * L::kTileBytes;
       uint8_t* svs = st + 2 * L::kTileBytes + L::kScaleBytes;
       const uint8_t* sg = gates + stage * L::kGateBytes;
       // The tile's keys are those of the prefix, or of the sequence's own, which end for each row with its own.
@@ -570,36 +582,41 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
           return most;
         };
         const uint32_t most = weigh();
-        // A weight above 2^(lift + 4), or a scale byte above top_e's (a lane's four, or two, of the tile's): sums that reach the next
-        // sign bit. And where nothing was weighed before.
-        const uint32_t wide = NB == 4 ? *reinterpret_cast<const uint32_t*>(svs + lane * 4)
-                                      : *reinterpret_cast<const uint16_t*>(svs + lane * 2);
-        const uint32_t over = ((most + weight_room) & 0x80008000u) | (((wide & 0x7F7F7F7Fu) + scale_room) & wide & 0x80808080u);
+        // A weight above 2^(kLift + kRoom), or a scale byte above top_e's (a lane's four of the tile's, all of one block): sums of
+        // the lower bits that reach a sign bit, for bytes with or without the sign bits. And where nothing was weighed before.
+        const uint32_t wide = *reinterpret_cast<const uint32_t*>(svs + lane % (8 * NB) * 4);
+        const uint32_t over = ((most + kWeightRoom) & 0x80008000u) | (majority(wide, (wide & 0x7F7F7F7Fu) + scale_room, scale_low) & 0x80808080u);
         if (__any_sync(0xffffffffu, over != 0 || tile == tile0)) {
-          const float was = static_cast<float>(lift_of(top_e));
           uint32_t top_s = max(max(wide & 255u, wide >> 8 & 255u), max(wide >> 16 & 255u, wide >> 24));
-          top_s = __reduce_max_sync(0xffffffffu, top_s);
+#pragma unroll
+          for (int k = NB; k < 8 * NB; k <<= 1) top_s = max(top_s, __shfl_xor_sync(0xffffffffu, top_s, k));
+          const int was_e = top_e;
           top_e = max(top_e, static_cast<int>(top_s >> 3));
-          const float lift = static_cast<float>(lift_of(top_e));
-          weight_room = (0x7FFFu - (static_cast<uint32_t>(lift_of(top_e) + kRoom + 15) << 10)) * 0x00010001u;
-          scale_room = (0xFFu - static_cast<uint32_t>(top_e << 3 | 7)) * 0x01010101u;
+          const uint32_t bound = static_cast<uint32_t>(top_e << 3 | 7);
+          scale_room = (0x7Fu - (bound & 0x7Fu)) * 0x01010101u;
+          scale_low = bound < 0x80u ? 0xFFFFFFFFu : 0u;
+          const float f = power_of_2(15 - top_e), fell = power_of_2(was_e - top_e);
+          f2 = pack_f16x2(f, f);
+          float down[NB];  // of the sums so far
+#pragma unroll
+          for (int b = 0; b < NB; ++b) down[b] = __shfl_sync(0xffffffffu, fell, b);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              // the largest score less the old reference; a row that weighed something had one of `was` there
-              float z = l[nt][e] > 0.f ? was : -INFINITY;
+              // the largest score less the reference; a row that weighed something had one of kLift there
+              float z = l[nt][e] > 0.f ? static_cast<float>(kLift) : -INFINITY;
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) z = fmaxf(z, fmaxf(y[mt][nt][e], y[mt][nt][e + 2]));
 #pragma unroll
               for (int k = kTwice ? 2 : 4; k < 32; k <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, k));
-              const float up = z == -INFINITY ? 0.f : z - lift, alpha = up > 0.f ? ex2_approx(-up) : 1.f;  // below 0 only where nothing is summed yet
+              const float up = z == -INFINITY ? 0.f : z - kLift, alpha = up > 0.f ? ex2_approx(-up) : 1.f;  // below 0 only where nothing is summed yet
               r[nt][e] += up;
               l[nt][e] *= alpha;
 #pragma unroll
               for (int dt = 0; dt < 2 * NB; ++dt) {
-                acc[dt][nt][e] *= alpha;
-                acc[dt][nt][e + 2] *= alpha;
+                acc[dt][nt][e] *= alpha * down[dt / 2];
+                acc[dt][nt][e + 2] *= alpha * down[dt / 2];
               }
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
@@ -609,6 +626,11 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
             }
           weigh();
         }
+        // Scales of V times f, in fp16, in the place of the stage's scales, all of which were read: of each word of four those of tokens 2 t, 2 t + 1
+        // and of + 8, + 9, as the weights' operands have them.
+        *reinterpret_cast<uint2*>(sks + lane % (8 * NB) * 8) =
+            make_uint2(hmul2((wide & 0x00FF00FFu) * 128u, f2), hmul2((wide >> 1) & 0x7F807F80u, f2));
+        __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -624,35 +646,28 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
               }
             }
         // Scales of tokens 2 t4, 2 t4 + 1 (+ 8) of each 16, where rows stand twice of those whose weights this lane's column has.
-        uint32_t vsw[MT][NB];
+        uint2 vsw[MT][NB];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint8_t* at16 = svs + (kTwice ? g8 >> 2 : mt) * 16 * NB + t4 * 4 * NB;
-          if (NB == 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(at16);
-            vsw[mt][0] = x.x;
-            vsw[mt][1] = x.y;
-            vsw[mt][NB - 2] = x.z;
-            vsw[mt][NB - 1] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(at16);
-            vsw[mt][0] = x.x;
-            vsw[mt][1] = x.y;
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int b = 0; b < NB; b += 2) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sks + (((kTwice ? g8 >> 2 : mt) * 4 + t4) * NB + b) * 8);
+            vsw[mt][b] = make_uint2(x.x, x.y);
+            vsw[mt][b + 1] = make_uint2(x.z, x.w);
           }
-        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t v[4];
           ldsm4_t(smem_u32(sv) + vplace + ((b ^ vturn) << 4), v);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            const uint32_t sw = vsw[kTwice ? 0 : mt][b], sa = (sw & 0x00FF00FFu) * 128u, sb = (sw >> 1) & 0x7F807F80u;
+            const uint2 sw = vsw[kTwice ? 0 : mt][b];
             const uint32_t x0 = v[2 * mt], x1 = v[2 * mt + 1], y0 = x0 >> 8, y1 = x1 >> 8;
             const uint32_t v0[4] = {low_nibbles(x0), high_nibbles(x0), low_nibbles(x1), high_nibbles(x1)};
             const uint32_t v1[4] = {low_nibbles(y0), high_nibbles(y0), low_nibbles(y1), high_nibbles(y1)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t pa = hmul2(ph[mt][nt][0], sa), pb = hmul2(ph[mt][nt][1], sb);
+              const uint32_t pa = hmul2(ph[mt][nt][0], sw.x), pb = hmul2(ph[mt][nt][1], sw.y);
               mma_f16(acc[2 * b][nt], v0, pa, pb);
               mma_f16(acc[2 * b + 1][nt], v1, pa, pb);
             }
@@ -666,6 +681,9 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
         // ring's start (all copies were read).
         const bool alone = cur.i0 >= u0 && cur.i0 + cur.tiles <= u0 + count, keep = !alone && done == count;
         cur.tile = tile1;
+        float up[NB];  // takes f off
+#pragma unroll
+        for (int b = 0; b < NB; ++b) up[b] = power_of_2(__shfl_sync(0xffffffffu, top_e, b) - 15);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float* out = reinterpret_cast<float*>(keep ? ring : st) + (keep ? nt * 8 * L::kOutStride : 0);
@@ -677,7 +695,8 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
             const int rl = 2 * t4 + e;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-              float4 x = make_float4(acc[2 * b][nt][e], acc[2 * b][nt][e + 2], acc[2 * b + 1][nt][e], acc[2 * b + 1][nt][e + 2]);
+              float4 x = make_float4(acc[2 * b][nt][e] * up[b], acc[2 * b][nt][e + 2] * up[b], acc[2 * b + 1][nt][e] * up[b],
+                                     acc[2 * b + 1][nt][e + 2] * up[b]);
               if (kTwice) {
                 x.x += __shfl_xor_sync(0xffffffffu, x.x, 2);
                 x.y += __shfl_xor_sync(0xffffffffu, x.y, 2);

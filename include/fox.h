@@ -413,8 +413,10 @@ fox_status fox_cache4_append(const fox_cache4* c, const fox_batch* s, int rows, 
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * fox_decode over a 4-bit cache, with its arguments and results. The weights pass through fp16, at up to 2^10 times their
- * value against the running maximum; a shared prefix is, where that saves time, spread out to bf16 and fp16 in the workspace and shared as
+ * fox_decode over a 4-bit cache, with its arguments and results. Weights and their products with V's scales pass through fp16,
+ * brought to its range by powers of two: with w the weight against the row's largest, and V's scales against the largest scale S
+ * that the same 32 channels have in the sequence, w and w s / S of 2^-25 and more are rounded by 2^-11 of themselves at most, each,
+ * smaller ones by 2^-36, and scales below 2^-21 S by 2^-25 S. A shared prefix is, where that saves time, spread out to bf16 and fp16 in the workspace and shared as
  * there (a V held as 65536 or more in it then sets the error word).
  */
 fox_status fox_cache4_decode(const fox_cache4* c, const fox_batch* s, int rows, const void* q, int64_t q_stride, float scale,
