@@ -5,10 +5,12 @@
 // are a quarter; what a key costs in instructions is more, so the codes' layout (fox_four.h) is made for this kernel:
 //
 // K. A lane's part of an MMA operand (a token's channels 8 t .. 8 t + 7 of every block) lies side by side. A nibble u + 8 = n at bits 9..6
-//   of an fp16 of exponent 0 is 1 + n / 16, at bits 5..2 it is 1 + n / 256: two masks on the word and two on the word rotated by 8 make
-//   the eight values of two MMA steps. With q' = 16 q and 256 q in their places the products sum to sum q u plus sums of q alone (one a
-//   block and row), whose products with the scales one more MMA takes off: scales as they are, the sums in three fp16. So a block costs 5
-//   instructions a word and no subtraction of its own, and fp32 sums keep 2^-24 of 264 sum |q|. The block's scale multiplies its sum.
+//   of an fp16 whose other bits are 0 is n 2^-18, at bits 5..2 it is n 2^-22, both exactly: two masks on the word and two on the word rotated
+//   by 8 make the eight values of two MMA steps. With 2^8 q and 2^12 q in their places the products sum to 2^-10 sum q u plus sums of q alone
+//   (one a block and row), whose products with the scales one more MMA takes off: scales as they are, the sums in three fp16. So a block costs 5
+//   instructions a word and no subtraction of its own. An MMA aligns its terms by their operands' exponents, here as 256 |q|, cuts each
+//   at 2^-25 of the largest, and the sum to fp32 (measured); with 1 + n / 16 and 1 + n / 256 for values, whose sums stand 264 sum |q| high,
+//   LSE came out four to six times further off at the same time. The block's scale multiplies its sum.
 // V. ldmatrix.trans turns 16-bit units (four channels of a token) so that a register has the same four channels of two
 //   neighbouring tokens: what the V^T operand wants, nibble by nibble. The masks give 1 + n / 1024 and 1 + n / 64, an fma n - 8, exactly.
 //   The scales, which vary along the sum, go to P, once a block of 32 channels: P s f in fp16, with f the power of two that brings the largest
@@ -18,8 +20,8 @@
 // Weights are P = 2^(x - r), with r = the running maximum less kLift: as fp16 holds 2^-24 and above, in full from 2^-14 on, weights down to
 //   2^-25 of the largest keep all bits, and so do their products with scales of the largest's size (of 2^-k of it, from 2^(k - 25) on);
 //   r moves when a weight passes 2^(kLift + kRoom), f when a scale passes its bound, which one vote finds: the weights are then formed again.
-// q in fp16: each row times a power of two so that its largest |q| is in [4, 8); what a bf16 holds is then exact down to 2^-21 of that,
-//   and off by 2^-32 of it at most.
+// q in fp16: each row times a power of two so that its largest |q| is in [4, 8); what a bf16 holds is then exact down to 2^-27 of that,
+//   and off by 2^-35 of it at most.
 // Up to four rows a tile (kRows 4) stand twice among the eight columns, so that scores and weights of half the keys fall to each half of the
 //   lanes: columns 0..3 then sum the first 16 keys of a tile, columns 4..7 the others, and are added at the end.
 //
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
       const int e = most > 0.f ? min(static_cast<int>(__float_as_uint(most) >> 23), 254) - 127 - 2 : 0;
       const float down0 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23),
                   down1 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
-      const float row_unit = p.scale2 / down0 / down1;
+      const float row_unit = p.scale2 / down0 * 0x1p10f / down1;
       uint32_t piece[3][NB / 2];  // the sums of two blocks, in three parts
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -406,10 +408,10 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
         for (int i = 0; i < 4; ++i) {
           // pairs 0 and 3 stand at bits 9..6, pairs 1 and 2 at bits 5..2
           const bool low = i == 1 || i == 2;
-          const float up = low ? 256.f : 16.f;
+          const float up = low ? 4096.f : 256.f;
           const uint32_t h = pack_f16x2(f[b][2 * i] * down0 * down1 * up, f[b][2 * i + 1] * down0 * down1 * up);
           const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          sum -= (back.x + back.y) * (low ? 264.f / 256.f : 24.f / 16.f);  // 16 channels of at most 2048: below 2^16
+          sum -= (back.x + back.y) * (8.f / 1024.f / up);  // 32 channels of 8 times less than 8, 2^-10: at most 2
           qf[b][nt][i == 0 ? 0 : i == 1 ? 1 : i == 3 ? 2 : 3] = h;
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -520,10 +522,8 @@ __global__ void __launch_bounds__(32 * W, 1) decode4_kernel(const __grid_constan
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint32_t x0 = kw[0][b], x1 = kw[1][b], y0 = __funnelshift_r(x0, x0, 8), y1 = __funnelshift_r(x1, x1, 8);
-            const uint32_t k0[4] = {over_one(x0, 0x03C003C0u), over_one(x1, 0x03C003C0u), over_one(x0, 0x003C003Cu),
-                                    over_one(x1, 0x003C003Cu)};
-            const uint32_t k1[4] = {over_one(y0, 0x03C003C0u), over_one(y1, 0x03C003C0u), over_one(y0, 0x003C003Cu),
-                                    over_one(y1, 0x003C003Cu)};
+            const uint32_t k0[4] = {x0 & 0x03C003C0u, x1 & 0x03C003C0u, x0 & 0x003C003Cu, x1 & 0x003C003Cu};
+            const uint32_t k1[4] = {y0 & 0x03C003C0u, y1 & 0x03C003C0u, y0 & 0x003C003Cu, y1 & 0x003C003Cu};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float c[4] = {0.f, 0.f, 0.f, 0.f};
