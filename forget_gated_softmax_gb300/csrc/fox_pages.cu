@@ -97,7 +97,11 @@ __global__ void __launch_bounds__(kCopyThreads) pages_begin_kernel(const StepPar
   const int src = parent_of(p, b);
   if (src < 0) return;
   const int n = pages_of(in, own_tokens(in, in.lens[src], p.err));
-  for (int c = tid; c < n; c += kCopyThreads) out.table[(size_t)b * out.stride + c] = in.table[(size_t)src * in.stride + c];
+  for (int c = tid; c < n; c += kCopyThreads) {
+    const int id = in.table[(size_t)src * in.stride + c];
+    if (id < 0 || id >= in.num_pages) atomicOr(p.err, DEV_ERR_BOUNDS);
+    out.table[(size_t)b * out.stride + c] = id;
+  }
 }
 
 // References of an old sequence's pages, a block a sequence: by its children less one.
@@ -166,7 +170,10 @@ __global__ void __launch_bounds__(kPageThreads) pages_step_kernel(const StepPara
     if (grows[i] && (own & ((1 << in.shift) - 1)) != 0) {
       last[i] = in.table[(size_t)src * in.stride + n0[i] - 1];
       part[i] = last[i] >= 0 && last[i] < in.num_pages;
-      if (part[i]) p.list[last[i]] = -1;
+      if (part[i])
+        p.list[last[i]] = -1;
+      else
+        atomicOr(p.err, DEV_ERR_BOUNDS);
     }
   }
   __syncthreads();

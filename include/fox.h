@@ -464,8 +464,9 @@ size_t fox_pages_workspace_bytes(const fox_pages* in, const fox_pages* out);
  * Where the free pages do not reach for b (or its row of the table does not), the error word is set and b gets none of its add:
  * lens says so. b with enough of them is one that, with what all before it asked for, stays within the free pages.
  * in and out: other arrays, or, without parent, the same ones (the step is then done in place). num_pages, page_size, table_stride
- * and prefix_len have to agree. A parent or length outside its range is reported and counts as -1 or idle, a page outside the pool is
- * reported and left out of refs. Integers all, in a fixed order: the same arguments give the same result.
+ * and prefix_len have to agree. A parent or length outside its range is reported and counts as -1 or idle. A page outside the pool is
+ * reported, left out of refs and copies, and stays in the table; a step into the same table sees the partly filled last pages of sequences
+ * that grow, no others. prefix_table is neither read nor written. Integers all, in a fixed order: the same arguments give the same result.
  */
 fox_status fox_pages_step(const fox_pages* in, const fox_pages* out, const int32_t* parent, const int32_t* add,
                           int32_t* copies, void* workspace, size_t workspace_bytes, void* stream);
