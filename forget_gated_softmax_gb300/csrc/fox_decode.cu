@@ -173,7 +173,7 @@ bool share_prefix(const PagedArgs& a, int row_tiles) {
 // 39 and 40, 2 behind 65536 46 and 125, 256 behind 32768 2053 and 192; 16 heads of 64 channels, 16 sequences behind 4096 40.5 and 38.6,
 // 32 behind 4096 65 and 42; 4 with 16 new tokens each behind 4096 49 and 51.
 bool share_prefix4(const PagedArgs& a, int row_tiles, int Rt) {
-  const long long tiles = (long long)ceil_div(a.prefix_len, kKeyTile) * a.Hkv, walked = a.B * row_tiles * tiles;
+  const long long tiles = (long long)ceil_div(a.prefix_len, kKeyTile) * a.Hkv, walked = (long long)a.B * row_tiles * tiles;
   return (Rt == 16 ? walked * 3 / 2 : walked) > 16000 + tiles * 11 * a.d / 256;
 }
 
