@@ -53,11 +53,12 @@ __device__ __forceinline__ float turned(float a, float c, float b, float s) {
   const float p = __fmul_rn(b, s), e = __fmaf_rn(b, s, -p);
   return __fsub_rn(__fmaf_rn(a, c, -p), e);
 }
-// The same in 64 bits, in which the products are exact, rounded to odd in fp32: what then rounds to bf16 is rounded once.
+// The same through 64 bits, in which the products are exact, but not the difference of two that lie far apart: rounded down and up, to 64 bits
+// and then to fp32, which leaves the fp32 value itself, or its two neighbours. Of these the odd one then rounds to bf16 as the exact one does.
 __device__ __forceinline__ float turned_exactly(float a, float c, float b, float s) {
-  const double x = static_cast<double>(a) * c - static_cast<double>(b) * s;
-  const float f = __double2float_rz(x);
-  return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+  const double q = -(static_cast<double>(b) * s);
+  const float below = __double2float_rd(__fma_rd(a, c, q)), above = __double2float_ru(__fma_ru(a, c, q));
+  return __float_as_uint(below) & 1u ? below : above;
 }
 // `least` so far and two values' lower halves less 0x7FFD, modulo 2^16, where a border of bf16 is 3 (a carry may add 1 to the upper):
 // up to 7 the side of the border is open (1.5 units, 2.5 where products are subnormal).
