@@ -33,18 +33,7 @@ struct Append4Params : AppendParams {
 constexpr int kResident = 8;                           // blocks of an SM
 constexpr int kMostRows = 8;                           // rows of a thread
 constexpr int kMostPlaces = kMostRows * kThreads / 8;  // of a block
-
-__device__ __forceinline__ void unpack8(const uint4& w, float* f) {
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(r[i] << 16);
-    f[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
+using Bf16 = Vec<__nv_bfloat16>;
 
 // a c - b s: rounded to fp32 twice, or within 1.5 units of the last place.
 template <bool kExact>
@@ -74,8 +63,8 @@ struct Sixteen {
 template <bool kNeighbours, typename F>
 __device__ __forceinline__ Sixteen turn_with(const Sixteen& w, const float* cs, const float* sn, F turn) {
   float x[8], y[8], co[8], si[8];
-  unpack8(w.x, x);
-  unpack8(w.y, y);
+  Bf16::unpack(w.x, x);
+  Bf16::unpack(w.y, y);
 #pragma unroll
   for (int k = 0; k < 8; k += 4) {
     const float4 c = *reinterpret_cast<const float4*>(cs + k), s = *reinterpret_cast<const float4*>(sn + k);
@@ -90,7 +79,7 @@ __device__ __forceinline__ Sixteen turn_with(const Sixteen& w, const float* cs, 
     p = turn(a, co[i], b, si[i]);
     q = turn(b, co[i], -a, si[i]);
   }
-  return {pack8(x), pack8(y)};
+  return {Bf16::pack(x), Bf16::pack(y)};
 }
 template <bool kNeighbours>
 __device__ __noinline__ Sixteen turn16_exactly(Sixteen w, const float* cs, const float* sn) {
@@ -115,7 +104,7 @@ __device__ __forceinline__ Sixteen turn16(const Sixteen& w, const float* cs, con
 // held as the nearest there is.
 __device__ __forceinline__ uint32_t block_codes(const uint4& w, float inv, bool odd) {
   float f[8];
-  unpack8(w, f);
+  Bf16::unpack(w, f);
   if (odd) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = f[e] == f[e] ? fminf(fmaxf(f[e], -430080.f), 430080.f) : 0.f;

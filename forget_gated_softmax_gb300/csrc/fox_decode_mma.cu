@@ -30,6 +30,12 @@ namespace {
 
 constexpr float kGrow = 8.0f;  // log2 units that a score may pass the running maximum by
 
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -85,6 +91,33 @@ static __device__ __noinline__ void put_back(const DecodeParams& p, const Place&
   __syncwarp();
 }
 // Shared memory: K and V of every (warp, stage), then its gates, then the sequences' work offsets.
+// Gates of a stage: per sub-page (32 slots, or two of 16) [heads][slots + 4] sums, then [heads] bases.
+struct MmaShape {
+  int heads, gpitch;          // heads of a row tile; floats from one head's sums to the next's
+  int gsub, gstage;           // bytes of a sub-page's sums (a TMA destination: 128-byte steps); of a stage's gates
+};
+inline MmaShape mma_shape(const PagedArgs& a, int rows) {
+  const int G = a.H / a.Hkv, subs = a.page_size == 16 ? 2 : 1;
+  MmaShape x;
+  x.heads = G < rows ? G : rows;
+  x.gpitch = (subs == 2 ? 16 : kKeyTile) + 4;
+  x.gsub = (x.heads * x.gpitch * 4 + 127) / 128 * 128;
+  x.gstage = subs * x.gsub + (subs * x.heads * 8 + 127) / 128 * 128;
+  return x;
+}
+constexpr int most_gates(int rows) { return 2 * ((rows * 20 * 4 + 127) / 128 * 128) + rows * 16; }  // gstage at most
+
+// An item's rows are asked for by asynchronous copies while the item before is computed: Q and the gates when
+// that one begins, for which the table's entries for the rows' own tokens are there, asked for an item earlier.
+// Against loads when the item begins: 256 sequences of up to 500 86.5 -> 80.6 us, one of 65536 59.1 -> 57.3, 16 of up to 4096
+// with four tokens each 70.0 -> 68.7; 128 of up to 200 with 64 channels 29.7 -> 30.6.
+template <int kRows>
+struct ItemRows {
+  Place at[2];         // by the item's number & 1, as the entries are
+  int page[2][kRows];
+  float g[kRows];
+  float2 base[kRows];
+};
 
 // kMany: sequences may bring more than one token, so that a tile may hold keys that some of an item's rows do not see
 // (a kernel of its own: one token a sequence took 0.5 to 4 % longer with that code in it, several tokens take up to 2 %).
@@ -100,7 +133,7 @@ __global__ void __launch_bounds__(32 * MmaLayout<D, NT>::kWarps, 1)
   __shared__ __align__(8) uint64_t bars[W][L::kStages];
   __shared__ int abort_word;
   __shared__ Kept<L::kRows, W> kept;
-  __shared__ int ids[W][2][64];
+  __shared__ int ids[W][2][64];  // two windows' table entries, by asynchronous copies: no instruction waits for them before their use
   __shared__ BlockEnds ends;
   __shared__ ItemRows<L::kRows> rows_of[W];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

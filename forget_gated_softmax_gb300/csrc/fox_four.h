@@ -9,7 +9,6 @@
 namespace fox {
 
 constexpr int kFourBlock = 32;        // channels that share a scale
-constexpr int kFourTop = 7;           // codes are u + 8, u = -7 .. 7
 constexpr int kFourMaxScale = 0xF7;   // 61440; larger bytes are no scales (in fp16 an infinity and NaNs)
 
 // ---- layout, in bytes from the pool's start ----
