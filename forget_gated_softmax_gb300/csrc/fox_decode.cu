@@ -169,9 +169,9 @@ bool share_prefix(const PagedArgs& a, int row_tiles) {
 }
 // The same of a 4-bit cache, where a key tile walked costs instructions (1 ns of the whole GPU's time, half as much more in tiles of
 // 16 rows), and sharing spreads the prefix out first: some 16 us, and 5.5 ns a tile of the prefix at 128 channels. In tiles walked.
-// 32 heads on 8 of 128 channels, walked and shared: 8 sequences behind 16384 tokens 52 and 55 us, 16 behind 4096 36 and 42, 64 behind 1024
-// 39 and 40, 2 behind 65536 46 and 125, 256 behind 32768 2053 and 192; 16 heads of 64 channels, 16 sequences behind 4096 40.5 and 38.6,
-// 32 behind 4096 65 and 42; 4 with 16 new tokens each behind 4096 49 and 51.
+// 32 heads on 8 of 128 channels, walked and shared: 8 sequences behind 16384 tokens 52 and 54 us, 16 behind 4096 36 and 43, 64 behind 1024
+// 39 and 42, 2 behind 65536 47 and 120, 256 behind 32768 2099 and 192; 16 heads of 64 channels, 16 sequences behind 4096 41.4 and 37.8,
+// 32 behind 4096 66 and 40; 4 with 16 new tokens each behind 4096 50 and 51.
 bool share_prefix4(const PagedArgs& a, int row_tiles, int Rt) {
   const long long tiles = (long long)ceil_div(a.prefix_len, kKeyTile) * a.Hkv, walked = (long long)a.B * row_tiles * tiles;
   return (Rt == 16 ? walked * 3 / 2 : walked) > 16000 + tiles * 11 * a.d / 256;

@@ -25,10 +25,10 @@
 // Up to four rows a tile (kRows 4) stand twice among the eight columns, so that scores and weights of half the keys fall to each half of the
 //   lanes: columns 0..3 then sum the first 16 keys of a tile, columns 4..7 the others, and are added at the end.
 //
-// Bound by instructions: 785 a key tile of 128 channels and 4 rows, 180 of them to spread K out, 200 V, 95 the copies (all lanes' own: by
+// Bound by instructions: 798 a key tile of 128 channels and 4 rows, some 180 of them to spread K out, 200 V, 95 the copies (all lanes' own: by
 // bulk copies of a loading warp, which has a lane a worker, 301 us against 235 then). 64 sequences of up to 16384 tokens, 32 heads on 8, 725 MB:
-// 171 us, 4.2 TB/s, issue slots 58 % used and the ALU's pipe 54 %; the copies alone take 130, the rest without them 135 (15 of either are
-// launch, look-ups and join). V as subnormals, their offset of 8 taken off by two more products: 4 % fewer instructions, 177 for 172 us. One sequence of 65536, 80 MB: 34 us, of which launch and first
+// 171 us, 4.2 TB/s, issue slots 58 % used and the ALU's pipe 52 %; the copies alone took 130, the rest without them 135 when both took 169 (15 of
+// either are launch, look-ups and join). V as subnormals, their offset of 8 taken off by two more products: 4 % fewer instructions, 177 for 172 us. One sequence of 65536, 80 MB: 34 us, of which launch and first
 // look-ups are 13 and the join of the workers' parts 6; one of 1000, 16 heads of 64 channels: 14.5, all but 3 of them launch, look-ups and join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -815,8 +815,8 @@ cudaError_t launch_as(const DecodeParams& p, cudaStream_t s) {
 }
 
 // Workers of a CTA: three a scheduler, as registers allow, or two where a worker's rings and rows leave no room for three in shared memory.
-// 64 sequences of up to 16384 tokens, 4 rows: 12 workers 169 us, 14 and 16 (128 registers, some of them spilled) 194 and 182; a third stage
-// of the ring 171. 16 rows of 128 channels, up to 8192: 8 workers 160, 10 262.
+// 64 sequences of up to 16384 tokens, 4 rows: 12 workers 172 us, 10 199, 14 and 16 (128 registers, some of them spilled) 190 and 178 (64 channels,
+// up to 8192: 130, 151, 138 and 126); a third stage of the ring 171 where two took 169. 16 rows of 128 channels, up to 8192: 8 workers 163, 10 279.
 constexpr int warps_of(int D, int rows) { return rows < 16 || D == 64 ? 12 : 8; }
 
 template <int D, int kRows>
@@ -828,8 +828,8 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// The smallest tile that holds them: 4 rows a key head, 64 sequences of up to 16384 tokens, 169 us in tiles of 4 and 182 of 8; 8 rows, up
-// to 8192, 107 of 8 and 151 of 16 (64 channels: 4 rows 127 and 134, 8 rows 137 and 189).
+// The smallest tile that holds them: 4 rows a key head, 64 sequences of up to 16384 tokens, 172 us in tiles of 4 and 179 of 8; 8 rows, up
+// to 8192, 105 of 8 and 153 of 16 (64 channels: 4 rows 130 and 137, 8 rows 140 and 190).
 int decode4_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 int decode4_warps(const PagedArgs& a, int Rt) { return warps_of(a.d, Rt); }
 
