@@ -123,3 +123,32 @@ def test_small_values_behind_a_prefix(fox, walked):
     c, scale = sink(B, 1, 8, 64, n, e, v, prefix=P)
     o, _ = decode(fox, c, scale)
     check(o, c, n + P - 1, e)
+
+
+@pytest.mark.parametrize("G,d,new", [(1, 128, 3), (4, 64, 2), (4, 128, 3), (8, 64, 5)])  # tiles of 4, 8, 16 and of 16 rows, three a sequence
+@pytest.mark.parametrize("size,e", [(1.0e-3, 24), (0.05, 21), (30000.0, 24)])
+def test_several_new_tokens(fox, G, d, new, size, e):
+    """Row t of a sequence sees new - 1 - t keys fewer than its last one."""
+    n = 1500
+    c, scale = sink(64, G, 32, d, n, e, torch.full((d,), size, device="cuda"), new=new)
+    o, _ = decode(fox, c, scale)
+    for t in range(new):
+        seen = n - (new - 1 - t)
+        want = held(c) * (seen * 2.0**-e / (1 + seen * 2.0**-e))
+        row = o[t::new].double()
+        want = want[None, :, None].expand(64, -1, G, -1).reshape(row.shape)
+        off = (row - want).abs() / want.abs()
+        assert (off <= TOL).all(), (t, off.max().item())
+
+
+@pytest.mark.parametrize("G,d", [(1, 128), (4, 64), (12, 64)])
+@pytest.mark.parametrize("at", [3, 800])
+def test_a_large_value_without_weight_in_the_same_channels(fox, G, d, at):
+    """V of 30000 at a key that weighs nothing (2^-160): its scale is 2^19 times the others', whose weights of 2^-5 times that
+    are 2^-24, within what 11 bits hold."""
+    n, e = 1500, 5
+    c, scale = sink(64, G, 32, d, n, e, torch.full((d,), 0.05, device="cuda"))
+    for k, v, z in c.seq:
+        k[at, :, 0], v[at] = -56.0, 30000.0  # 30000 * 2^-160 adds nothing
+    o, _ = decode(fox, c, scale)
+    check(o, c, n - 1, e)
